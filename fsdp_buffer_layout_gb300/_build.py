@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libvsf.so")
 BUILD = os.path.join(PKG, "_build")
 VARIANTS = {None: ("libvsf.so", []), "bounds": ("libvsf_bounds.so", ["-DVSF_DEBUG_BOUNDS"])}
 
-SOURCES = ["plan.cpp", "vsf_kernels.cu", "muon.cu"]
+SOURCES = ["plan.cpp", "vsf_kernels.cu", "muon.cu", "objective.cu", "route.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

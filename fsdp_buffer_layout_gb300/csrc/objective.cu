@@ -1,0 +1,546 @@
+// objective.cu — losses over a model's logits and their gradients: token log
+// probabilities, the clipped policy loss with a KL term, and the preference
+// loss of pairs.
+//
+// All three rest on one row operation. For a row x of logits with maximum m,
+//   s = sum_v exp((x_v - m) / temperature),
+//   ln p(y) = (x_y - m) / temperature - ln s,
+//   d loss / d x_v = a (1[v = y] - exp((x_v - m) / temperature) / s),
+// where a = d loss / d ln p(y) / temperature depends on the token alone
+// (policy) or on its pair of sequences (preference).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "objective.cuh"
+
+namespace vsf {
+namespace {
+
+using namespace obj;
+
+constexpr int kRowThreads = 512;
+constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kTokenThreads = 512;
+
+// Workspace: the head, then per token {m, s} and the gradient's coefficient,
+// then per pair the loss and the margin.
+struct ObjectiveWs {
+  WsHead* head;
+  float2* row;    // [tokens] maximum and sum of a live row
+  float* coef;    // [tokens] a of a token; 0: no gradient
+  double* pair;   // [2 * pairs] loss and beta h of a pair
+  static size_t bytes(int64_t tokens, int64_t pairs) {
+    return sizeof(WsHead) + (size_t)((tokens * 12 + 15) / 16 * 16) + (size_t)pairs * 16;
+  }
+  ObjectiveWs(void* ws, int64_t tokens) {
+    unsigned char* p = static_cast<unsigned char*>(ws);
+    head = reinterpret_cast<WsHead*>(p);
+    row = reinterpret_cast<float2*>(p + sizeof(WsHead));
+    coef = reinterpret_cast<float*>(row + tokens);
+    pair = reinterpret_cast<double*>(p + sizeof(WsHead) + (tokens * 12 + 15) / 16 * 16);
+  }
+};
+
+// Rows of logits and their targets.
+template <typename T>
+struct Rows {
+  const T* x;
+  int64_t ld;
+  int64_t T_;
+  int32_t V;
+  const int64_t* target;
+  const float* weight;  // NULL: 1
+  Log2Scale c;
+  float inv_tf;
+  double inv_t;
+};
+
+// The target of a live token, or -1.
+template <typename T>
+__device__ __forceinline__ int32_t live_target(const Rows<T>& r, int64_t t, uint32_t* err) {
+  const int64_t y = r.target[t];
+  if (y < 0) return -1;
+  if (r.weight != nullptr && r.weight[t] == 0.f) return -1;
+  if (y >= r.V) {
+    if (err != nullptr) atomicOr(err, kErrTarget);
+    return -1;
+  }
+  return (int32_t)y;
+}
+
+// ln p(y) from x_y - m and s, in fp64 with few fp64 operations: ln s = k ln 2
+// + ln f with f in [0.75, 1.5), where logf's absolute error is at most 3e-8
+// (logf(s) itself would round at 5e-7 for s in the thousands). All terms of s
+// but the maximum's 1 carry the mean error of ex2, which would add up over a
+// sequence, and is taken off here.
+__device__ __forceinline__ double log_prob(float d, float s, double inv_t) {
+  int k = 0;
+  float f = s;
+  if (s >= 1.1754944e-38f && s < INFINITY) {
+    const uint32_t b = __float_as_uint(s);
+    k = (int)((b + 0x00400000u) >> 23) - 127;
+    f = __uint_as_float(b - ((uint32_t)k << 23));
+  }
+  const float bias = (float)kEx2Bias * (1.f - 1.f / s);
+  return (double)d * inv_t - ((double)k * 0.69314718055994530942 + (double)(logf(f) - bias));
+}
+
+struct MaxSum {
+  float m, s;
+};
+
+// Joins by expf, whose mean error is a tenth of ex2's: a term passes several
+// joins on its way to the row's sum.
+__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float inv_t) {
+  const float m = fmaxf(a.m, b.m), z = finite_max(m);
+  return {m, a.s * expf((a.m - z) * inv_t) + b.s * expf((b.m - z) * inv_t)};
+}
+
+__device__ __forceinline__ MaxSum join_warp(MaxSum v, float inv_t) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const MaxSum w = {__shfl_xor_sync(~0u, v.m, o), __shfl_xor_sync(~0u, v.s, o)};
+    v = join(v, w, inv_t);
+  }
+  return v;
+}
+
+// Every live row's maximum and sum, and its log probability.
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads)
+    row_stats_kernel(Rows<T> r, float2* row, float* logp, WsHead* head) {
+  __shared__ MaxSum part[kRowWarps];
+  for (int64_t t = blockIdx.x; t < r.T_; t += gridDim.x) {
+    const int32_t y = live_target(r, t, threadIdx.x == 0 ? &head->err : nullptr);
+    if (y < 0) {
+      if (threadIdx.x == 0 && logp != nullptr) logp[t] = 0.f;
+      continue;
+    }
+    const T* x = r.x + t * r.ld;
+    MaxSum v = {-INFINITY, 0.f};
+    for (int i = threadIdx.x; i < r.V; i += kRowThreads) {
+      const float e = to_f(x[i]);
+      if (e > v.m) v = join(v, {e, 0.f}, r.inv_tf);
+      v.s += exp_scaled(e - finite_max(v.m), r.c);
+    }
+    v = join_warp(v, r.inv_tf);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      v = threadIdx.x < kRowWarps ? part[threadIdx.x] : MaxSum{-INFINITY, 0.f};
+      v = join_warp(v, r.inv_tf);
+      if (threadIdx.x == 0) {
+        if (row != nullptr) row[t] = make_float2(v.m, v.s);
+        if (logp != nullptr) logp[t] = (float)log_prob(to_f(x[y]) - v.m, v.s, r.inv_t);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+struct PolicyIn {
+  const float *old_logp, *ref_logp, *adv;
+  float lo, hi, beta, scale;  // the ratio's clip bounds; loss factors
+  int mean;
+};
+
+// One token's policy and KL terms and d(policy + beta kl)/d logp.
+struct PolicyTerm {
+  float policy, kl, slope;
+};
+
+__device__ __forceinline__ PolicyTerm policy_term(const PolicyIn& p, int64_t t, double lp) {
+  PolicyTerm o;
+  const float a = p.adv[t];
+  const float ratio = expf((float)(lp - (double)p.old_logp[t]));
+  const float freed = ratio * a;
+  const float held = fminf(fmaxf(ratio, p.lo), p.hi) * a;
+  const bool clipped = freed > held;  // a NaN ratio is not clipped away
+  o.policy = -(clipped ? held : freed);
+  o.slope = clipped ? 0.f : -freed;
+  o.kl = 0.f;
+  if (p.beta != 0.f) {
+    const float u = (float)((double)p.ref_logp[t] - lp);
+    const float e = expm1f(u);
+    // exp(u) - 1 - u; near 0 by its series, whose first terms do not cancel
+    o.kl = fabsf(u) < 0.25f
+               ? u * u * (0.5f + u * (1.f / 6 + u * (1.f / 24 + u * (1.f / 120 + u * (1.f / 720 + u * (1.f / 5040))))))
+               : e - u;
+    o.slope -= p.beta * e;
+  }
+  return o;
+}
+
+__device__ __forceinline__ double block_sum(double v, double* part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0;
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) v += part[w];
+  return v;
+}
+
+// Policy loss of every token in one CTA, and the gradient's coefficients.
+template <typename T>
+__global__ void __launch_bounds__(kTokenThreads)
+    policy_tokens_kernel(Rows<T> r, PolicyIn p, const float2* row, float* coef, float* stats) {
+  __shared__ double part[kTokenThreads / 32];
+  double n = 0.0;
+  for (int64_t t = threadIdx.x; t < r.T_; t += kTokenThreads)
+    if (live_target(r, t, nullptr) >= 0) n += r.weight != nullptr ? (double)r.weight[t] : 1.0;
+  n = block_sum(n, part);
+  const double f = (double)p.scale / (p.mean && n != 0.0 ? n : 1.0);
+  double pol = 0.0, kl = 0.0;
+  for (int64_t t = threadIdx.x; t < r.T_; t += kTokenThreads) {
+    const int32_t y = live_target(r, t, nullptr);
+    if (y < 0) {
+      coef[t] = 0.f;
+      continue;
+    }
+    const double w = r.weight != nullptr ? (double)r.weight[t] : 1.0;
+    const float2 ms = row[t];
+    const PolicyTerm o = policy_term(p, t, log_prob(to_f(r.x[t * r.ld + y]) - ms.x, ms.y, r.inv_t));
+    pol += w * (double)o.policy;
+    kl += w * (double)o.kl;
+    coef[t] = (float)(f * w * r.inv_t * (double)o.slope);
+  }
+  pol = block_sum(pol, part) * f;
+  kl = block_sum(kl, part) * f;
+  if (threadIdx.x == 0) {
+    stats[0] = (float)(pol + (p.beta != 0.f ? (double)p.beta * kl : 0.0));
+    stats[1] = (float)pol;
+    stats[2] = (float)kl;
+    stats[3] = (float)n;
+  }
+}
+
+struct PairIn {
+  const float* ref_logp;
+  const int64_t* starts;
+  float* rewards;
+  int64_t pairs;
+  float beta, smoothing, margin, scale;
+  int kind, average;
+};
+
+__device__ __forceinline__ int64_t clamp_start(int64_t v, int64_t T_) {
+  return v < 0 ? 0 : v > T_ ? T_ : v;
+}
+
+// One pair a CTA: both log ratios, the loss, and its tokens' coefficients.
+template <typename T>
+__global__ void __launch_bounds__(kTokenThreads)
+    pair_kernel(Rows<T> r, PairIn p, const float2* row, float* coef, double* pair) {
+  __shared__ double part[kTokenThreads / 32];
+  const int64_t q = blockIdx.x;
+  double ratio[2], length[2];
+  for (int side = 0; side < 2; ++side) {
+    const int64_t b = clamp_start(p.starts[side * p.pairs + q], r.T_);
+    const int64_t e = clamp_start(p.starts[side * p.pairs + q + 1], r.T_);
+    double d = 0.0, n = 0.0;
+    for (int64_t t = b + threadIdx.x; t < e; t += kTokenThreads) {
+      const int32_t y = live_target(r, t, nullptr);
+      if (y < 0) continue;
+      const double w = r.weight != nullptr ? (double)r.weight[t] : 1.0;
+      const float2 ms = row[t];
+      const double lp = log_prob(to_f(r.x[t * r.ld + y]) - ms.x, ms.y, r.inv_t);
+      d += w * (p.ref_logp != nullptr ? lp - (double)p.ref_logp[t] : lp);
+      n += w;
+    }
+    d = block_sum(d, part);
+    n = block_sum(n, part);
+    length[side] = p.average && n != 0.0 ? n : 1.0;
+    ratio[side] = d / length[side];
+    if (threadIdx.x == 0 && p.rewards != nullptr)
+      p.rewards[side * p.pairs + q] = (float)((double)p.beta * ratio[side]);
+  }
+  const double h = ratio[0] - ratio[1];
+  double loss, slope;
+  if (p.kind == VSF_PREF_SIGMOID) {
+    const double z = (double)p.beta * h - (double)p.margin;
+    const double tail = log1p(exp(-fabs(z)));
+    const double up = 1.0 / (1.0 + exp(-z));
+    loss = (1.0 - (double)p.smoothing) * (tail - (z > 0.0 ? 0.0 : z)) +
+           (double)p.smoothing * (tail + (z < 0.0 ? 0.0 : z));
+    slope = (double)p.beta * (up - (1.0 - (double)p.smoothing));
+  } else {
+    const double gap = h - 0.5 / (double)p.beta;
+    loss = gap * gap;
+    slope = 2.0 * gap;
+  }
+  if (threadIdx.x == 0) {
+    pair[2 * q] = loss;
+    pair[2 * q + 1] = (double)p.beta * h;
+  }
+  for (int side = 0; side < 2; ++side) {
+    const int64_t b = clamp_start(p.starts[side * p.pairs + q], r.T_);
+    const int64_t e = clamp_start(p.starts[side * p.pairs + q + 1], r.T_);
+    const double a = (side ? -1.0 : 1.0) * (double)p.scale / (double)p.pairs * slope /
+                     length[side] * r.inv_t;
+    for (int64_t t = b + threadIdx.x; t < e; t += kTokenThreads)
+      coef[t] = live_target(r, t, nullptr) < 0
+                    ? 0.f
+                    : (float)(a * (r.weight != nullptr ? (double)r.weight[t] : 1.0));
+  }
+}
+
+__global__ void __launch_bounds__(kTokenThreads)
+    pair_sum_kernel(const double* pair, int64_t pairs, float scale, float* stats) {
+  __shared__ double part[kTokenThreads / 32];
+  double l = 0.0, h = 0.0;
+  for (int64_t q = threadIdx.x; q < pairs; q += kTokenThreads) {
+    l += pair[2 * q];
+    h += pair[2 * q + 1];
+  }
+  l = block_sum(l, part);
+  h = block_sum(h, part);
+  if (threadIdx.x == 0) {
+    stats[0] = (float)((double)scale * l / (double)pairs);
+    stats[1] = (float)(h / (double)pairs);
+  }
+}
+
+// The gradient's rows from each row's maximum, sum and coefficient.
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads)
+    row_grad_kernel(Rows<T> r, const float2* row, const float* coef, T* grad, int64_t grad_ld) {
+  for (int64_t t = blockIdx.x; t < r.T_; t += gridDim.x) {
+    const float a = coef[t];
+    T* g = grad + t * grad_ld;
+    if (a == 0.f) {
+      for (int i = threadIdx.x; i < r.V; i += kRowThreads) g[i] = from_f<T>(0.f);
+      continue;
+    }
+    const T* x = r.x + t * r.ld;
+    const int32_t y = (int32_t)r.target[t];
+    const float2 ms = row[t];
+    const float z = finite_max(ms.x), inv_s = 1.f / ms.y;
+    for (int i = threadIdx.x; i < r.V; i += kRowThreads) {
+      const float p = exp_scaled(to_f(x[i]) - z, r.c) * inv_s;
+      g[i] = from_f<T>(i == y ? a * (1.f - p) : -a * p);
+    }
+  }
+}
+
+// ------------------------------------------------------------- host side
+struct RowsArg {
+  const void* logits;
+  int32_t dtype;
+  int64_t T_, V, ld;
+  const int64_t* target;
+  const float* weight;
+  float inv_t;
+};
+
+vsf_status check_rows(const char* who, const RowsArg& a, void* ws, size_t ws_bytes,
+                      int64_t pairs) {
+  const std::string w(who);
+  if (a.dtype != VSF_BF16 && a.dtype != VSF_FP32) return fail(VSF_ERR_ARG, w + ": bad dtype");
+  if (a.T_ < 0 || a.T_ > INT32_MAX || a.V < 1 || a.V > INT32_MAX || a.ld < a.V ||
+      a.ld > (int64_t(1) << 40))
+    return fail(VSF_ERR_ARG, w + ": sizes out of range");
+  if (!(a.inv_t > 0.f) || !std::isfinite(a.inv_t))
+    return fail(VSF_ERR_ARG, w + ": inv_temperature must be positive and finite");
+  if (ws == nullptr || (a.T_ > 0 && (a.logits == nullptr || a.target == nullptr)))
+    return fail(VSF_ERR_ARG, w + ": NULL pointer");
+  if (ws_bytes < ObjectiveWs::bytes(a.T_, pairs))
+    return fail(VSF_ERR_ARG, w + ": workspace too small");
+  if (!aligned(ws, 16) || !aligned(a.logits, a.dtype == VSF_BF16 ? 2 : 4) ||
+      !aligned(a.target, 8) || !aligned(a.weight, 4))
+    return fail(VSF_ERR_ALIGN, w + ": pointer alignment");
+  return VSF_OK;
+}
+
+vsf_status check_grad(const char* who, const RowsArg& a, const void* grad, int64_t grad_ld) {
+  if (grad == nullptr) return VSF_OK;
+  const int64_t size = a.dtype == VSF_BF16 ? 2 : 4;
+  if (grad_ld < a.V || grad_ld > (int64_t(1) << 40))
+    return fail(VSF_ERR_ARG, std::string(who) + ": grad_ld out of range");
+  if (!aligned(grad, size)) return fail(VSF_ERR_ALIGN, std::string(who) + ": pointer alignment");
+  if (a.T_ == 0) return VSF_OK;
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(a.logits);
+  const uintptr_t g0 = reinterpret_cast<uintptr_t>(grad);
+  const uintptr_t x1 = x0 + ((a.T_ - 1) * a.ld + a.V) * size;
+  const uintptr_t g1 = g0 + ((a.T_ - 1) * grad_ld + a.V) * size;
+  if (x0 < g1 && g0 < x1 && !(x0 == g0 && a.ld == grad_ld))
+    return fail(VSF_ERR_ARG, std::string(who) + ": grad overlaps the logits in part");
+  return VSF_OK;
+}
+
+template <typename T>
+Rows<T> rows_of(const RowsArg& a) {
+  Rows<T> r;
+  r.x = static_cast<const T*>(a.logits);
+  r.ld = a.ld;
+  r.T_ = a.T_;
+  r.V = (int32_t)a.V;
+  r.target = a.target;
+  r.weight = a.weight;
+  r.c = log2_scale(a.inv_t);
+  r.inv_tf = a.inv_t;
+  r.inv_t = (double)a.inv_t;
+  return r;
+}
+
+unsigned row_grid(int64_t T_) { return (unsigned)std::min<int64_t>(T_, 152 * 4); }
+
+template <typename T>
+cudaError_t launch_stats(const Rows<T>& r, float2* row, float* logp, WsHead* head,
+                         cudaStream_t st) {
+  if (r.T_ == 0) return cudaSuccess;
+  row_stats_kernel<T><<<row_grid(r.T_), kRowThreads, 0, st>>>(r, row, logp, head);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_grad(const Rows<T>& r, const ObjectiveWs& w, void* grad, int64_t grad_ld,
+                        cudaStream_t st) {
+  if (r.T_ == 0 || grad == nullptr) return cudaSuccess;
+  row_grad_kernel<T><<<row_grid(r.T_), kRowThreads, 0, st>>>(r, w.row, w.coef,
+                                                             static_cast<T*>(grad), grad_ld);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t policy(const RowsArg& a, const PolicyIn& p, float* stats, float* logp, void* grad,
+                   int64_t grad_ld, const ObjectiveWs& w, cudaStream_t st) {
+  const Rows<T> r = rows_of<T>(a);
+  cudaError_t e = launch_stats(r, w.row, logp, w.head, st);
+  if (e != cudaSuccess) return e;
+  policy_tokens_kernel<T><<<1, kTokenThreads, 0, st>>>(r, p, w.row, w.coef, stats);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_grad(r, w, grad, grad_ld, st);
+}
+
+template <typename T>
+cudaError_t preference(const RowsArg& a, const PairIn& p, float* stats, float* logp, void* grad,
+                       int64_t grad_ld, const ObjectiveWs& w, cudaStream_t st) {
+  const Rows<T> r = rows_of<T>(a);
+  cudaError_t e = launch_stats(r, w.row, logp, w.head, st);
+  if (e == cudaSuccess && a.T_ > 0) e = cudaMemsetAsync(w.coef, 0, a.T_ * 4, st);
+  if (e != cudaSuccess) return e;
+  pair_kernel<T><<<(unsigned)p.pairs, kTokenThreads, 0, st>>>(r, p, w.row, w.coef, w.pair);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  pair_sum_kernel<<<1, kTokenThreads, 0, st>>>(w.pair, p.pairs, p.scale, stats);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_grad(r, w, grad, grad_ld, st);
+}
+
+}  // namespace
+}  // namespace vsf
+
+using namespace vsf;
+
+extern "C" {
+
+size_t vsf_objective_workspace_bytes(int64_t tokens, int64_t pairs) {
+  if (tokens < 0 || tokens > INT32_MAX || pairs < 0 || pairs > INT32_MAX) return 0;
+  return ObjectiveWs::bytes(tokens, pairs);
+}
+
+vsf_status vsf_objective_workspace_init(void* d_workspace, size_t bytes, void* stream) {
+  vsf::Range nvtx_range("vsf_objective_workspace_init");
+  if (d_workspace == nullptr || bytes < sizeof(WsHead))
+    return fail(VSF_ERR_ARG, "vsf_objective_workspace_init: NULL or too small");
+  if (!aligned(d_workspace, 16))
+    return fail(VSF_ERR_ALIGN, "vsf_objective_workspace_init: workspace alignment");
+  const cudaError_t e = cudaMemsetAsync(d_workspace, 0, bytes, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VSF_OK : cuda_error(e, "vsf_objective_workspace_init");
+}
+
+vsf_status vsf_token_logprobs(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                              const int64_t* targets, float inv_temperature, float* logp,
+                              void* d_workspace, size_t ws_bytes, void* stream) {
+  vsf::Range nvtx_range("vsf_token_logprobs");
+  const RowsArg a = {logits, dtype, T, V, ld, targets, nullptr, inv_temperature};
+  const vsf_status s = check_rows("vsf_token_logprobs", a, d_workspace, ws_bytes, 0);
+  if (s != VSF_OK) return s;
+  if (T > 0 && logp == nullptr) return fail(VSF_ERR_ARG, "vsf_token_logprobs: NULL pointer");
+  if (!aligned(logp, 4)) return fail(VSF_ERR_ALIGN, "vsf_token_logprobs: pointer alignment");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const ObjectiveWs w(d_workspace, T);
+  const cudaError_t e =
+      dtype == VSF_BF16 ? launch_stats(rows_of<uint16_t>(a), nullptr, logp, w.head, st)
+                        : launch_stats(rows_of<float>(a), nullptr, logp, w.head, st);
+  return e == cudaSuccess ? VSF_OK : cuda_error(e, "vsf_token_logprobs");
+}
+
+vsf_status vsf_policy_loss(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                           const int64_t* targets, const float* old_logp, const float* ref_logp,
+                           const float* advantages, const float* weights,
+                           const vsf_policy_hparams* hp, float* stats, float* logp, void* grad,
+                           int64_t grad_ld, void* d_workspace, size_t ws_bytes, void* stream) {
+  vsf::Range nvtx_range("vsf_policy_loss");
+  const char* who = "vsf_policy_loss";
+  if (hp == nullptr || stats == nullptr) return fail(VSF_ERR_ARG, "vsf_policy_loss: NULL pointer");
+  const RowsArg a = {logits, dtype, T, V, ld, targets, weights, hp->inv_temperature};
+  vsf_status s = check_rows(who, a, d_workspace, ws_bytes, 0);
+  if (s == VSF_OK) s = check_grad(who, a, grad, grad_ld);
+  if (s != VSF_OK) return s;
+  if (T > 0 && (old_logp == nullptr || advantages == nullptr ||
+                (hp->kl_beta != 0.f && ref_logp == nullptr)))
+    return fail(VSF_ERR_ARG, "vsf_policy_loss: NULL pointer");
+  if (!(hp->clip_low >= 0.f && hp->clip_low <= 1.f && hp->clip_high >= 0.f) ||
+      !std::isfinite(hp->kl_beta) || !std::isfinite(hp->scale))
+    return fail(VSF_ERR_ARG, "vsf_policy_loss: hyper-parameters out of range");
+  if (!aligned(old_logp, 4) || !aligned(ref_logp, 4) || !aligned(advantages, 4) ||
+      !aligned(stats, 4) || !aligned(logp, 4))
+    return fail(VSF_ERR_ALIGN, "vsf_policy_loss: pointer alignment");
+  const PolicyIn p = {old_logp,
+                      ref_logp,
+                      advantages,
+                      1.f - hp->clip_low,
+                      1.f + hp->clip_high,
+                      hp->kl_beta,
+                      hp->scale,
+                      hp->mean != 0};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const ObjectiveWs w(d_workspace, T);
+  const cudaError_t e = dtype == VSF_BF16
+                            ? policy<uint16_t>(a, p, stats, logp, grad, grad_ld, w, st)
+                            : policy<float>(a, p, stats, logp, grad, grad_ld, w, st);
+  return e == cudaSuccess ? VSF_OK : cuda_error(e, who);
+}
+
+vsf_status vsf_preference_loss(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                               const int64_t* targets, const float* ref_logp,
+                               const float* weights, const int64_t* seq_starts, int64_t pairs,
+                               const vsf_preference_hparams* hp, float* stats, float* rewards,
+                               float* logp, void* grad, int64_t grad_ld, void* d_workspace,
+                               size_t ws_bytes, void* stream) {
+  vsf::Range nvtx_range("vsf_preference_loss");
+  const char* who = "vsf_preference_loss";
+  if (hp == nullptr || stats == nullptr || seq_starts == nullptr)
+    return fail(VSF_ERR_ARG, "vsf_preference_loss: NULL pointer");
+  if (pairs < 1 || pairs > (1 << 24))
+    return fail(VSF_ERR_ARG, "vsf_preference_loss: pairs out of range");
+  const RowsArg a = {logits, dtype, T, V, ld, targets, weights, hp->inv_temperature};
+  vsf_status s = check_rows(who, a, d_workspace, ws_bytes, pairs);
+  if (s == VSF_OK) s = check_grad(who, a, grad, grad_ld);
+  if (s != VSF_OK) return s;
+  if ((hp->kind != VSF_PREF_SIGMOID && hp->kind != VSF_PREF_SQUARED) || !(hp->beta > 0.f) ||
+      !std::isfinite(hp->beta) || !(hp->smoothing >= 0.f && hp->smoothing <= 0.5f) ||
+      !std::isfinite(hp->margin) || !std::isfinite(hp->scale))
+    return fail(VSF_ERR_ARG, "vsf_preference_loss: hyper-parameters out of range");
+  if (!aligned(ref_logp, 4) || !aligned(seq_starts, 8) || !aligned(stats, 4) ||
+      !aligned(rewards, 4) || !aligned(logp, 4))
+    return fail(VSF_ERR_ALIGN, "vsf_preference_loss: pointer alignment");
+  const PairIn p = {ref_logp,   seq_starts,    rewards,   pairs,    hp->beta,
+                    hp->smoothing, hp->margin, hp->scale, hp->kind, hp->average != 0};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const ObjectiveWs w(d_workspace, T);
+  const cudaError_t e = dtype == VSF_BF16
+                            ? preference<uint16_t>(a, p, stats, logp, grad, grad_ld, w, st)
+                            : preference<float>(a, p, stats, logp, grad, grad_ld, w, st);
+  return e == cudaSuccess ? VSF_OK : cuda_error(e, who);
+}
+
+}  // extern "C"

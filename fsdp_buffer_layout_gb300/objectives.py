@@ -1,0 +1,249 @@
+"""Training objectives: device buffers (allocated with torch) around libvsf's
+loss and router calls, as ``step.ShardStep`` is around the shard step.
+
+TokenLogprobs   log probability of each token under its row of logits
+PolicyLoss      clipped policy loss with a KL term, and the logits' gradient
+PreferenceLoss  loss of (chosen, rejected) pairs, and the logits' gradient
+Router          top-k choice, gates, per-expert counts, balance loss; gradient
+
+An object owns its workspace and its outputs, sized for the largest call
+(`tokens` rows); a call returns views of the outputs, which the next call of
+the same object overwrites, on the object's stream. As everywhere in the
+library nothing is synchronised: a caller that works on another stream orders
+the two itself. The formulas stand at the C functions in include/vsf.h.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import vsf as V
+
+_DTYPES = {torch.bfloat16: V.VSF_BF16, torch.float32: V.VSF_FP32}
+
+
+class _Objective:
+    """The device, the stream and the checks of arguments."""
+
+    def __init__(self, tokens: int, width: int, dtype, device, stream):
+        if dtype not in _DTYPES:
+            raise ValueError(f"logits are bfloat16 or float32, not {dtype}")
+        if tokens < 0 or width < 1:
+            raise ValueError(f"sizes out of range: {tokens} tokens, rows of {width}")
+        self.tokens, self.width, self.dtype = int(tokens), int(width), dtype
+        self._vdt = _DTYPES[dtype]
+        device = torch.device("cuda" if device is None else device)
+        self.device = device if device.index is not None \
+            else torch.device(device.type, torch.cuda.current_device())
+        self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
+        self._st = self.stream.cuda_stream
+
+    def _new(self, *shape, dtype=torch.float32):
+        return torch.empty(*shape, dtype=dtype, device=self.device)
+
+    def _workspace(self, nbytes: int):
+        if not nbytes:
+            raise ValueError("sizes out of range")
+        self.workspace = self._new(nbytes, dtype=torch.uint8)
+        self._ws, self._ws_bytes = self.workspace.data_ptr(), nbytes
+        V.vsf_objective_workspace_init(self._ws, nbytes, self._st)
+
+    def _rows(self, x, what: str) -> int:
+        """Checks rows of logits (or their gradient); the row stride."""
+        if x.dtype is not self.dtype or x.dim() != 2 or x.shape[1] != self.width \
+                or x.device != self.device:
+            raise ValueError(f"{what}: expected {self.dtype} [<= {self.tokens}, {self.width}] on "
+                             f"{self.device}, got {x.dtype} {tuple(x.shape)} on {x.device}")
+        rows, cols = x.shape
+        if rows > self.tokens:
+            raise ValueError(f"{what}: {rows} rows, the object was made for {self.tokens}")
+        ld, unit = x.stride()
+        if cols > 1 and unit != 1:
+            raise ValueError(f"{what}: the elements of a row must be adjacent (stride {unit})")
+        if rows <= 1:
+            return max(ld, cols)
+        if ld < cols:
+            raise ValueError(f"{what}: rows overlap (stride {ld}, {cols} elements)")
+        return ld
+
+    def _vec(self, x, n: int, dtype, what: str):
+        """Checks a contiguous vector of n elements; its address (None: none)."""
+        if x is None:
+            return None
+        if x.dtype is not dtype or x.numel() != n or not x.is_contiguous() \
+                or x.device != self.device:
+            raise ValueError(f"{what}: expected {n} contiguous {dtype} on {self.device}, got "
+                             f"{x.dtype} {tuple(x.shape)} on {x.device}")
+        return x.data_ptr()
+
+    def device_error(self) -> int:
+        """The device error word (0: no wait ran out, every target in range)."""
+        return int(self.workspace[:4].view(torch.int32).item())
+
+
+class TokenLogprobs(_Objective):
+    """logp[t] = ln softmax(inv_temperature * logits[t])[targets[t]]; 0 where
+    the target is negative. targets: int64."""
+
+    def __init__(self, tokens: int, vocab: int, *, dtype=torch.bfloat16,
+                 inv_temperature: float = 1.0, device=None, stream=None):
+        super().__init__(tokens, vocab, dtype, device, stream)
+        self.inv_temperature = inv_temperature
+        self._workspace(V.vsf_objective_workspace_bytes(self.tokens))
+        self.logp = self._new(self.tokens)
+
+    def __call__(self, logits, targets):
+        ld, n = self._rows(logits, "logits"), logits.shape[0]
+        logp = self.logp[:n]
+        V.vsf_token_logprobs(logits.data_ptr(), self._vdt, n, self.width, ld,
+                             self._vec(targets, n, torch.int64, "targets"), self.inv_temperature,
+                             logp.data_ptr(), self._ws, self._ws_bytes, self._st)
+        return logp
+
+
+class _LogitsLoss(_Objective):
+    def _outputs(self, pairs: int, stats: int, with_grad: bool):
+        self._workspace(V.vsf_objective_workspace_bytes(self.tokens, pairs))
+        self.stats = self._new(stats)
+        self.logp = self._new(self.tokens)
+        self.grad = self._new(self.tokens, self.width, dtype=self.dtype) if with_grad else None
+
+    def _grad(self, n: int, grad):
+        """The gradient's tensor, address and row stride of a call."""
+        if grad is None:
+            if self.grad is None:
+                return None, None, self.width
+            grad = self.grad[:n]
+            return grad, grad.data_ptr(), self.width
+        ld = self._rows(grad, "grad")
+        if grad.shape[0] != n:
+            raise ValueError(f"grad: {grad.shape[0]} rows, logits have {n}")
+        return grad, grad.data_ptr(), ld
+
+
+class PolicyLoss(_LogitsLoss):
+    """Clipped policy loss with a KL term. A call returns (stats, logp, grad):
+    stats = [loss, policy term, KL term, sum of the live weights]. grad is the
+    object's own buffer, or the tensor given (the logits themselves to write
+    in place); with_grad=False and no tensor given: loss only, grad None."""
+
+    def __init__(self, tokens: int, vocab: int, *, dtype=torch.bfloat16, clip_low: float = 0.2,
+                 clip_high: float = 0.2, kl_beta: float = 0.0, inv_temperature: float = 1.0,
+                 scale: float = 1.0, mean: bool = True, with_grad: bool = True, device=None,
+                 stream=None):
+        super().__init__(tokens, vocab, dtype, device, stream)
+        self.hp = V.make_policy_hparams(clip_low, clip_high, kl_beta, inv_temperature, scale, mean)
+        self._outputs(0, 4, with_grad)
+
+    def __call__(self, logits, targets, old_logp, advantages, ref_logp=None, weights=None,
+                 grad=None):
+        ld, n = self._rows(logits, "logits"), logits.shape[0]
+        grad, g, grad_ld = self._grad(n, grad)
+        logp, f32 = self.logp[:n], torch.float32
+        V.vsf_policy_loss(logits.data_ptr(), self._vdt, n, self.width, ld,
+                          self._vec(targets, n, torch.int64, "targets"),
+                          self._vec(old_logp, n, f32, "old_logp"),
+                          self._vec(ref_logp, n, f32, "ref_logp"),
+                          self._vec(advantages, n, f32, "advantages"),
+                          self._vec(weights, n, f32, "weights"), self.hp, self.stats.data_ptr(),
+                          logp.data_ptr(), g, grad_ld, self._ws, self._ws_bytes, self._st)
+        return self.stats, logp, grad
+
+
+class PreferenceLoss(_LogitsLoss):
+    """Preference loss of `pairs` pairs: sequences 0..pairs-1 are the chosen
+    ones, pairs..2*pairs-1 the rejected ones, sequence s at rows
+    [seq_starts[s], seq_starts[s+1]) (int64). A call returns (stats, rewards,
+    logp, grad): stats = [loss, mean of beta h], rewards = beta D_s."""
+
+    KINDS = {"sigmoid": V.VSF_PREF_SIGMOID, "squared": V.VSF_PREF_SQUARED}
+
+    def __init__(self, pairs: int, tokens: int, vocab: int, *, dtype=torch.bfloat16,
+                 kind: str = "sigmoid", beta: float = 0.1, smoothing: float = 0.0,
+                 margin: float = 0.0, average: bool = False, inv_temperature: float = 1.0,
+                 scale: float = 1.0, with_grad: bool = True, device=None, stream=None):
+        super().__init__(tokens, vocab, dtype, device, stream)
+        if kind not in self.KINDS:
+            raise ValueError(f"kind: one of {sorted(self.KINDS)}, not {kind!r}")
+        if pairs < 1:
+            raise ValueError(f"pairs: at least 1, not {pairs}")
+        self.pairs = int(pairs)
+        self.hp = V.make_preference_hparams(beta, smoothing, margin, inv_temperature, scale,
+                                            self.KINDS[kind], average)
+        self._outputs(self.pairs, 2, with_grad)
+        self.rewards = self._new(2 * self.pairs)
+
+    def __call__(self, logits, targets, seq_starts, ref_logp=None, weights=None, grad=None):
+        ld, n = self._rows(logits, "logits"), logits.shape[0]
+        grad, g, grad_ld = self._grad(n, grad)
+        logp, f32 = self.logp[:n], torch.float32
+        V.vsf_preference_loss(logits.data_ptr(), self._vdt, n, self.width, ld,
+                              self._vec(targets, n, torch.int64, "targets"),
+                              self._vec(ref_logp, n, f32, "ref_logp"),
+                              self._vec(weights, n, f32, "weights"),
+                              self._vec(seq_starts, 2 * self.pairs + 1, torch.int64,
+                                        "seq_starts"),
+                              self.pairs, self.hp, self.stats.data_ptr(),
+                              self.rewards.data_ptr(), logp.data_ptr(), g, grad_ld, self._ws,
+                              self._ws_bytes, self._st)
+        return self.stats, self.rewards, logp, grad
+
+
+class Router(_Objective):
+    """A mixture-of-experts router. forward returns (idx [T, top_k] int32,
+    gates [T, top_k] fp32, counts [E] int32, balance loss fp32 scalar);
+    backward the logits' gradient from the gates' gradient (None: none) and
+    loss_scale times the balance loss, for the last forward call."""
+
+    SCORES = {"softmax": V.VSF_SCORE_SOFTMAX, "sigmoid": V.VSF_SCORE_SIGMOID}
+
+    def __init__(self, tokens: int, experts: int, top_k: int, *, dtype=torch.bfloat16,
+                 score: str = "softmax", renorm: bool = True, route_scale: float = 1.0,
+                 balance: float = 0.0, sequences: int = 1, device=None, stream=None):
+        super().__init__(tokens, experts, dtype, device, stream)
+        if score not in self.SCORES:
+            raise ValueError(f"score: one of {sorted(self.SCORES)}, not {score!r}")
+        self.top_k, self.sequences = int(top_k), int(sequences)
+        self.hp = V.make_route_hparams(top_k, self.SCORES[score], renorm, route_scale, balance)
+        self._workspace(V.vsf_route_workspace_bytes(self.width, self.sequences))
+        i32 = torch.int32
+        self.idx = self._new(self.tokens, self.top_k, dtype=i32)
+        self.gates = self._new(self.tokens, self.top_k)
+        self.counts = self._new(self.width, dtype=i32)
+        self.loss = self._new(())
+        self.seq_counts = self._new(self.sequences, self.width, dtype=i32)
+        self.seq_coef = self._new(self.sequences)
+        self.grad = None  # made by the first backward
+
+    def _args(self, logits, live, seq_starts):
+        ld, n = self._rows(logits, "logits"), logits.shape[0]
+        if seq_starts is None and self.sequences != 1:
+            raise ValueError(f"seq_starts: needed for {self.sequences} sequences")
+        return (n, ld, self._vec(live, n, torch.uint8, "live"),
+                self._vec(seq_starts, self.sequences + 1, torch.int64, "seq_starts"))
+
+    def forward(self, logits, bias=None, live=None, seq_starts=None):
+        n, ld, lv, starts = self._args(logits, live, seq_starts)
+        V.vsf_route(logits.data_ptr(), self._vdt, n, self.width, ld,
+                    self._vec(bias, self.width, torch.float32, "bias"), lv, starts,
+                    self.sequences, self.hp, self.idx.data_ptr(), self.gates.data_ptr(),
+                    self.counts.data_ptr(), self.loss.data_ptr(), self.seq_counts.data_ptr(),
+                    self.seq_coef.data_ptr(), self._ws, self._ws_bytes, self._st)
+        return self.idx[:n], self.gates[:n], self.counts, self.loss
+
+    def backward(self, logits, d_gates=None, live=None, seq_starts=None, loss_scale: float = 1.0,
+                 grad=None):
+        n, ld, lv, starts = self._args(logits, live, seq_starts)
+        if grad is None:
+            if self.grad is None:
+                self.grad = self._new(self.tokens, self.width, dtype=self.dtype)
+            grad, grad_ld = self.grad[:n], self.width
+        else:
+            grad_ld = self._rows(grad, "grad")
+            if grad.shape[0] != n:
+                raise ValueError(f"grad: {grad.shape[0]} rows, logits have {n}")
+        V.vsf_route_grad(logits.data_ptr(), self._vdt, n, self.width, ld, lv, starts,
+                         self.sequences, self.hp, self.idx.data_ptr(),
+                         self._vec(d_gates, n * self.top_k, torch.float32, "d_gates"),
+                         self.seq_counts.data_ptr(), self.seq_coef.data_ptr(), loss_scale,
+                         grad.data_ptr(), grad_ld, self._st)
+        return grad

@@ -16,6 +16,8 @@ VSF_ERR_ALIGN, VSF_ERR_CUDA, VSF_ERR_STATE = -4, -5, -6
 VSF_GRAN_ELEM, VSF_GRAN_ROWS, VSF_GRAN_TILE = 0, 1, 2
 VSF_ORDER_DEFAULT, VSF_ORDER_BLOCK, VSF_ORDER_SHAPE, VSF_ORDER_BEST3 = 0, 1, 2, 3
 VSF_BF16, VSF_FP32 = 0, 1
+VSF_PREF_SIGMOID, VSF_PREF_SQUARED = 0, 1
+VSF_SCORE_SOFTMAX, VSF_SCORE_SIGMOID = 0, 1
 
 
 class VsfError(RuntimeError):
@@ -54,6 +56,23 @@ class vsf_muon_hparams(ctypes.Structure):
                 ("weight_decay", ctypes.c_double), ("eps", ctypes.c_double),
                 ("ns_a", ctypes.c_double), ("ns_b", ctypes.c_double), ("ns_c", ctypes.c_double),
                 ("ns_steps", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class vsf_policy_hparams(ctypes.Structure):
+    _fields_ = [("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float),
+                ("kl_beta", ctypes.c_float), ("inv_temperature", ctypes.c_float),
+                ("scale", ctypes.c_float), ("mean", ctypes.c_int32)]
+
+
+class vsf_preference_hparams(ctypes.Structure):
+    _fields_ = [("beta", ctypes.c_float), ("smoothing", ctypes.c_float),
+                ("margin", ctypes.c_float), ("inv_temperature", ctypes.c_float),
+                ("scale", ctypes.c_float), ("kind", ctypes.c_int32), ("average", ctypes.c_int32)]
+
+
+class vsf_route_hparams(ctypes.Structure):
+    _fields_ = [("top_k", ctypes.c_int32), ("score", ctypes.c_int32), ("renorm", ctypes.c_int32),
+                ("route_scale", ctypes.c_float), ("balance", ctypes.c_float)]
 
 
 _lock = threading.Lock()
@@ -147,6 +166,28 @@ def lib():
             L.vsf_muon_step.restype = st
             L.vsf_muon_step.argtypes = [vp, vp, vp, vp, vp, P(vsf_muon_hparams), vp,
                                         ctypes.c_size_t, vp]
+            sz, f32 = ctypes.c_size_t, ctypes.c_float
+            L.vsf_objective_workspace_bytes.restype = sz
+            L.vsf_objective_workspace_bytes.argtypes = [i64, i64]
+            L.vsf_route_workspace_bytes.restype = sz
+            L.vsf_route_workspace_bytes.argtypes = [i64, i64]
+            L.vsf_objective_workspace_init.restype = st
+            L.vsf_objective_workspace_init.argtypes = [vp, sz, vp]
+            L.vsf_token_logprobs.restype = st
+            L.vsf_token_logprobs.argtypes = [vp, i32, i64, i64, i64, vp, f32, vp, vp, sz, vp]
+            L.vsf_policy_loss.restype = st
+            L.vsf_policy_loss.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp,
+                                          P(vsf_policy_hparams), vp, vp, vp, i64, vp, sz, vp]
+            L.vsf_preference_loss.restype = st
+            L.vsf_preference_loss.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, i64,
+                                              P(vsf_preference_hparams), vp, vp, vp, vp, i64, vp,
+                                              sz, vp]
+            L.vsf_route.restype = st
+            L.vsf_route.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, i64,
+                                    P(vsf_route_hparams), vp, vp, vp, vp, vp, vp, vp, sz, vp]
+            L.vsf_route_grad.restype = st
+            L.vsf_route_grad.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64,
+                                         P(vsf_route_hparams), vp, vp, vp, vp, f32, vp, i64, vp]
             L.vsf_status_string.restype = ctypes.c_char_p
             L.vsf_status_string.argtypes = [st]
             L.vsf_last_error.restype = ctypes.c_char_p
@@ -361,6 +402,73 @@ def vsf_muon_step(plan: int, packed_grad: int, momentum: int, master: int, packe
                   hp: vsf_muon_hparams, d_workspace: int, ws_bytes: int, stream: int) -> None:
     _check(lib().vsf_muon_step(plan, packed_grad, momentum, master, packed_bf16, ctypes.byref(hp),
                                d_workspace, ws_bytes, stream))
+
+
+def vsf_objective_workspace_bytes(tokens: int, pairs: int = 0) -> int:
+    return int(lib().vsf_objective_workspace_bytes(tokens, pairs))
+
+
+def vsf_route_workspace_bytes(experts: int, sequences: int = 1) -> int:
+    return int(lib().vsf_route_workspace_bytes(experts, sequences))
+
+
+def vsf_objective_workspace_init(d_workspace: int, nbytes: int, stream: int) -> None:
+    _check(lib().vsf_objective_workspace_init(d_workspace, nbytes, stream))
+
+
+def vsf_token_logprobs(logits, dtype: int, T: int, V: int, ld: int, targets,
+                       inv_temperature: float, logp, d_workspace, ws_bytes: int,
+                       stream: int) -> None:
+    _check(lib().vsf_token_logprobs(logits, dtype, T, V, ld, targets, inv_temperature, logp,
+                                    d_workspace, ws_bytes, stream))
+
+
+def make_policy_hparams(clip_low=0.2, clip_high=0.2, kl_beta=0.0, inv_temperature=1.0, scale=1.0,
+                        mean=True) -> vsf_policy_hparams:
+    return vsf_policy_hparams(clip_low, clip_high, kl_beta, inv_temperature, scale, int(mean))
+
+
+def vsf_policy_loss(logits, dtype: int, T: int, V: int, ld: int, targets, old_logp, ref_logp,
+                    advantages, weights, hp: vsf_policy_hparams, stats, logp, grad, grad_ld: int,
+                    d_workspace, ws_bytes: int, stream: int) -> None:
+    _check(lib().vsf_policy_loss(logits, dtype, T, V, ld, targets, old_logp, ref_logp, advantages,
+                                 weights, ctypes.byref(hp), stats, logp, grad, grad_ld,
+                                 d_workspace, ws_bytes, stream))
+
+
+def make_preference_hparams(beta=0.1, smoothing=0.0, margin=0.0, inv_temperature=1.0, scale=1.0,
+                            kind=VSF_PREF_SIGMOID, average=False) -> vsf_preference_hparams:
+    return vsf_preference_hparams(beta, smoothing, margin, inv_temperature, scale, kind,
+                                  int(average))
+
+
+def vsf_preference_loss(logits, dtype: int, T: int, V: int, ld: int, targets, ref_logp, weights,
+                        seq_starts, pairs: int, hp: vsf_preference_hparams, stats, rewards, logp,
+                        grad, grad_ld: int, d_workspace, ws_bytes: int, stream: int) -> None:
+    _check(lib().vsf_preference_loss(logits, dtype, T, V, ld, targets, ref_logp, weights,
+                                     seq_starts, pairs, ctypes.byref(hp), stats, rewards, logp,
+                                     grad, grad_ld, d_workspace, ws_bytes, stream))
+
+
+def make_route_hparams(top_k, score=VSF_SCORE_SOFTMAX, renorm=True, route_scale=1.0,
+                       balance=0.0) -> vsf_route_hparams:
+    return vsf_route_hparams(top_k, score, int(renorm), route_scale, balance)
+
+
+def vsf_route(logits, dtype: int, T: int, E: int, ld: int, bias, live, seq_starts, sequences: int,
+              hp: vsf_route_hparams, idx, gates, counts, loss, seq_counts, seq_coef, d_workspace,
+              ws_bytes: int, stream: int) -> None:
+    _check(lib().vsf_route(logits, dtype, T, E, ld, bias, live, seq_starts, sequences,
+                           ctypes.byref(hp), idx, gates, counts, loss, seq_counts, seq_coef,
+                           d_workspace, ws_bytes, stream))
+
+
+def vsf_route_grad(logits, dtype: int, T: int, E: int, ld: int, live, seq_starts, sequences: int,
+                   hp: vsf_route_hparams, idx, d_gates, seq_counts, seq_coef, loss_scale: float,
+                   grad, grad_ld: int, stream: int) -> None:
+    _check(lib().vsf_route_grad(logits, dtype, T, E, ld, live, seq_starts, sequences,
+                                ctypes.byref(hp), idx, d_gates, seq_counts, seq_coef, loss_scale,
+                                grad, grad_ld, stream))
 
 
 def vsf_status_string(status: int) -> str:

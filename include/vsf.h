@@ -452,6 +452,145 @@ vsf_status vsf_group_norm_scale_static(const void* const* grads, const int64_t* 
                                        int32_t dtype, const vsf_adam_hparams* hp, float* d_factor,
                                        double* d_norm, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Training objectives: what stands between a model's outputs and the
+ * gradients that vsf_pack takes. The loss calls read rows of logits and write
+ * the logits' gradient in the same call; the router calls turn a gate's
+ * logits into the experts' choice and back.
+ *
+ * Common to the calls below:
+ *   - logits: T rows of V (or E) elements of `dtype` (VSF_BF16 or VSF_FP32),
+ *     row t starting at element t*ld (ld >= V). Pointers need the alignment
+ *     of their element type only, the workspace 16 bytes (VSF_ERR_ALIGN);
+ *     rows that start on a 16-byte boundary are read with wide copies. T may
+ *     be 0 (scalars are still written); T, V < 2^31; offsets are 64-bit.
+ *   - sums, maxima and per-token values are fp32 or wider; results do not
+ *     depend on scheduling: equal inputs give equal bits.
+ *   - d_workspace: caller memory of at least the size that
+ *     vsf_objective_workspace_bytes (losses) or vsf_route_workspace_bytes
+ *     gives, prepared once by vsf_objective_workspace_init and then left to
+ *     the library. Calls that share a workspace must be ordered on the
+ *     device. Its first 32-bit word is a device error word: bit 1 (value 2)
+ *     a bounded wait ran out (results not to be trusted), bit 4 (value 16) a
+ *     target was >= V; such a token is left out like a masked one.
+ *   - a live token has 0 <= target < V and a weight that is not 0. The logits
+ *     of other tokens are not read (they may be NaN); their log probability
+ *     is 0 and their gradient row is zeros. -inf logits have probability 0;
+ *     a live row with a NaN, a +inf or only -inf gives NaN.
+ *   - probabilities are softmax(inv_temperature * logits).
+ *   Errors: VSF_ERR_ARG (NULL, sizes or hyper-parameters out of range, a
+ *   workspace too small), VSF_ERR_ALIGN, VSF_ERR_CUDA; all but the last are
+ *   found before the first launch. */
+size_t vsf_objective_workspace_bytes(int64_t tokens, int64_t pairs);
+size_t vsf_route_workspace_bytes(int64_t experts, int64_t sequences);
+vsf_status vsf_objective_workspace_init(void* d_workspace, size_t bytes, void* stream);
+
+/* Log probability of each token: logp[t] = ln p_t(targets[t]), 0 for a token
+ * whose target is negative. targets: int64[T]; logp: fp32[T]. The old and the
+ * reference policy's terms of the two losses below. */
+vsf_status vsf_token_logprobs(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                              const int64_t* targets, float inv_temperature, float* logp,
+                              void* d_workspace, size_t ws_bytes, void* stream);
+
+/* Clipped policy loss with a KL term, loss and gradient:
+ *   r = exp(logp - old), u = ref - logp, with N = sum of the live weights
+ *   (mean = 1; 1 where that sum is 0) or 1 (mean = 0):
+ *   policy = scale/N sum_t w_t -min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A)
+ *   kl     = scale/N sum_t w_t (exp(u) - u - 1)
+ *   loss   = policy + kl_beta kl
+ *   grad[t][v] = d loss / d logits[t][v].
+ * old_logp, ref_logp (read only when kl_beta != 0, else may be NULL),
+ * advantages: fp32[T]; weights: fp32[T] or NULL (all 1). stats: fp32[4] =
+ * loss, policy, kl, sum of the live weights. logp: fp32[T] or NULL. grad: the
+ * logits' type, T rows at stride grad_ld, or NULL (loss only); it may be the
+ * logits themselves (same ld), otherwise it must not overlap them. */
+typedef struct {
+  float clip_low, clip_high; /* >= 0; clip_low <= 1 */
+  float kl_beta;
+  float inv_temperature;     /* > 0 */
+  float scale;
+  int32_t mean;
+} vsf_policy_hparams;
+
+vsf_status vsf_policy_loss(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                           const int64_t* targets, const float* old_logp, const float* ref_logp,
+                           const float* advantages, const float* weights,
+                           const vsf_policy_hparams* hp, float* stats, float* logp, void* grad,
+                           int64_t grad_ld, void* d_workspace, size_t ws_bytes, void* stream);
+
+/* Preference loss of `pairs` (chosen, rejected) pairs, loss and gradient.
+ * Sequence s owns tokens [seq_starts[s], seq_starts[s+1]); sequences
+ * 0..pairs-1 are the chosen ones, pairs..2*pairs-1 the rejected ones of the
+ * same pairs. seq_starts: device int64[2*pairs + 1], not decreasing; a
+ * sequence may be empty, tokens in none get a zero gradient. With
+ *   D_s = sum_t w_t (logp_t - ref_t)  [/ sum_t w_t when average = 1 and that
+ *   sum is not 0], h = D_chosen - D_rejected:
+ *   VSF_PREF_SIGMOID: z = beta h - margin,
+ *                     L = -(1 - smoothing) ln s(z) - smoothing ln s(-z)
+ *   VSF_PREF_SQUARED: L = (h - 1/(2 beta))^2
+ *   loss = scale/pairs sum L;  grad = d loss / d logits.
+ * ref_logp: fp32[T] or NULL (0: no reference). stats: fp32[2] = loss, mean of
+ * beta h. rewards: fp32[2*pairs] = beta D_s, or NULL. weights, logp, grad as
+ * above. */
+enum { VSF_PREF_SIGMOID = 0, VSF_PREF_SQUARED = 1 };
+typedef struct {
+  float beta;      /* > 0 */
+  float smoothing; /* in [0, 0.5] */
+  float margin;
+  float inv_temperature;
+  float scale;
+  int32_t kind;    /* VSF_PREF_* */
+  int32_t average;
+} vsf_preference_hparams;
+
+vsf_status vsf_preference_loss(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                               const int64_t* targets, const float* ref_logp,
+                               const float* weights, const int64_t* seq_starts, int64_t pairs,
+                               const vsf_preference_hparams* hp, float* stats, float* rewards,
+                               float* logp, void* grad, int64_t grad_ld, void* d_workspace,
+                               size_t ws_bytes, void* stream);
+
+/* A mixture-of-experts router. Scores s = softmax(logits) or sigmoid(logits)
+ * over E experts; each live token (live: uint8[T], or NULL for all) takes the
+ * top_k experts of largest logits (bias NULL) or of largest s + bias (bias:
+ * fp32[E], for the choice only), best first, ties to the lowest index, NaN
+ * last. gates = route_scale * s / (sum of the chosen s + 1e-20) (renorm = 1)
+ * or route_scale * s. Masked tokens get idx -1 and gates 0.
+ * Counts and balance loss over sequences (seq_starts: device int64[sequences
+ * + 1], not decreasing; NULL: one sequence of T tokens): with n_se the live
+ * tokens of sequence s that chose e, T_s its live tokens, q = s / (sum_e s +
+ * 1e-20) and S' the number of sequences with T_s > 0,
+ *   coef_s = balance * E / (top_k T_s^2 S'),  loss = sum_s coef_s sum_e n_se
+ *   sum_{t in s} q_te.
+ * Tokens outside every sequence are routed but neither counted nor balanced.
+ * Outputs: idx int32[T*top_k], gates fp32[T*top_k], counts int32[E] (over all
+ * sequences), loss fp32[1]; seq_counts int32[sequences*E] (n_se) and seq_coef
+ * fp32[sequences], which vsf_route_grad reads.
+ * 1 <= E <= 512, 1 <= top_k <= min(E, 32), 1 <= sequences <= 2^20. */
+enum { VSF_SCORE_SOFTMAX = 0, VSF_SCORE_SIGMOID = 1 };
+typedef struct {
+  int32_t top_k, score, renorm;
+  float route_scale, balance;
+} vsf_route_hparams;
+
+vsf_status vsf_route(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ld,
+                     const float* bias, const uint8_t* live, const int64_t* seq_starts,
+                     int64_t sequences, const vsf_route_hparams* hp, int32_t* idx, float* gates,
+                     int32_t* counts, float* loss, int32_t* seq_counts, float* seq_coef,
+                     void* d_workspace, size_t ws_bytes, void* stream);
+
+/* Gradient of the router's logits: through the gates (d_gates: fp32[T*top_k]
+ * or NULL for none) and through loss_scale * the balance loss, whose counts
+ * are constants. The forward call's logits, live, seq_starts, hp, idx,
+ * seq_counts and seq_coef are passed again; grad has the logits' type, T rows
+ * at stride grad_ld, must not overlap them unless it is them (same ld).
+ * Needs no workspace. An idx outside [0, E) takes no gradient. */
+vsf_status vsf_route_grad(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ld,
+                          const uint8_t* live, const int64_t* seq_starts, int64_t sequences,
+                          const vsf_route_hparams* hp, const int32_t* idx, const float* d_gates,
+                          const int32_t* seq_counts, const float* seq_coef, float loss_scale,
+                          void* grad, int64_t grad_ld, void* stream);
+
 const char* vsf_status_string(vsf_status s);
 const char* vsf_last_error(void);
 
