@@ -13,6 +13,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include "objective.cuh"
 
@@ -22,25 +23,29 @@ namespace {
 using namespace obj;
 
 constexpr int kRowThreads = 512;
-constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kTokenThreads = 512;
 
-// Workspace: the head, then per token {m, s} and the gradient's coefficient,
-// then per pair the loss and the margin.
+constexpr int kMaxPipeClusters = 1024;  // clusters whose sums the workspace holds
+
+// Workspace: the head, the pipelined kernel's sums per cluster, then per token
+// {m, s} and the gradient's coefficient, then per pair the loss and the margin.
 struct ObjectiveWs {
+  static constexpr size_t kFront = sizeof(WsHead) + 3 * 8 * (size_t)kMaxPipeClusters;
   WsHead* head;
+  double* partial;  // [3 * kMaxPipeClusters]
   float2* row;    // [tokens] maximum and sum of a live row
   float* coef;    // [tokens] a of a token; 0: no gradient
   double* pair;   // [2 * pairs] loss and beta h of a pair
   static size_t bytes(int64_t tokens, int64_t pairs) {
-    return sizeof(WsHead) + (size_t)((tokens * 12 + 15) / 16 * 16) + (size_t)pairs * 16;
+    return kFront + (size_t)((tokens * 12 + 15) / 16 * 16) + (size_t)pairs * 16;
   }
   ObjectiveWs(void* ws, int64_t tokens) {
     unsigned char* p = static_cast<unsigned char*>(ws);
     head = reinterpret_cast<WsHead*>(p);
-    row = reinterpret_cast<float2*>(p + sizeof(WsHead));
+    partial = reinterpret_cast<double*>(p + sizeof(WsHead));
+    row = reinterpret_cast<float2*>(p + kFront);
     coef = reinterpret_cast<float*>(row + tokens);
-    pair = reinterpret_cast<double*>(p + sizeof(WsHead) + (tokens * 12 + 15) / 16 * 16);
+    pair = reinterpret_cast<double*>(p + kFront + (tokens * 12 + 15) / 16 * 16);
   }
 };
 
@@ -58,17 +63,29 @@ struct Rows {
   double inv_t;
 };
 
+struct Token {
+  int64_t y;
+  float w;
+};
+template <typename T>
+__device__ __forceinline__ Token token_at(const Rows<T>& r, int64_t t) {
+  if (t >= r.T_) return {-1, 0.f};
+  return {r.target[t], r.weight != nullptr ? r.weight[t] : 1.f};
+}
+
 // The target of a live token, or -1.
 template <typename T>
-__device__ __forceinline__ int32_t live_target(const Rows<T>& r, int64_t t, uint32_t* err) {
-  const int64_t y = r.target[t];
-  if (y < 0) return -1;
-  if (r.weight != nullptr && r.weight[t] == 0.f) return -1;
-  if (y >= r.V) {
+__device__ __forceinline__ int32_t live_target(const Rows<T>& r, Token k, uint32_t* err) {
+  if (k.y < 0 || k.w == 0.f) return -1;
+  if (k.y >= r.V) {
     if (err != nullptr) atomicOr(err, kErrTarget);
     return -1;
   }
-  return (int32_t)y;
+  return (int32_t)k.y;
+}
+template <typename T>
+__device__ __forceinline__ int32_t live_target(const Rows<T>& r, int64_t t, uint32_t* err) {
+  return live_target(r, token_at(r, t), err);
 }
 
 // ln p(y) from x_y - m and s, in fp64 with few fp64 operations: ln s = k ln 2
@@ -99,48 +116,6 @@ __device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float inv_t) {
   return {m, a.s * expf((a.m - z) * inv_t) + b.s * expf((b.m - z) * inv_t)};
 }
 
-__device__ __forceinline__ MaxSum join_warp(MaxSum v, float inv_t) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const MaxSum w = {__shfl_xor_sync(~0u, v.m, o), __shfl_xor_sync(~0u, v.s, o)};
-    v = join(v, w, inv_t);
-  }
-  return v;
-}
-
-// Every live row's maximum and sum, and its log probability.
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads)
-    row_stats_kernel(Rows<T> r, float2* row, float* logp, WsHead* head) {
-  __shared__ MaxSum part[kRowWarps];
-  for (int64_t t = blockIdx.x; t < r.T_; t += gridDim.x) {
-    const int32_t y = live_target(r, t, threadIdx.x == 0 ? &head->err : nullptr);
-    if (y < 0) {
-      if (threadIdx.x == 0 && logp != nullptr) logp[t] = 0.f;
-      continue;
-    }
-    const T* x = r.x + t * r.ld;
-    MaxSum v = {-INFINITY, 0.f};
-    for (int i = threadIdx.x; i < r.V; i += kRowThreads) {
-      const float e = to_f(x[i]);
-      if (e > v.m) v = join(v, {e, 0.f}, r.inv_tf);
-      v.s += exp_scaled(e - finite_max(v.m), r.c);
-    }
-    v = join_warp(v, r.inv_tf);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    if (threadIdx.x < 32) {
-      v = threadIdx.x < kRowWarps ? part[threadIdx.x] : MaxSum{-INFINITY, 0.f};
-      v = join_warp(v, r.inv_tf);
-      if (threadIdx.x == 0) {
-        if (row != nullptr) row[t] = make_float2(v.m, v.s);
-        if (logp != nullptr) logp[t] = (float)log_prob(to_f(x[y]) - v.m, v.s, r.inv_t);
-      }
-    }
-    __syncthreads();
-  }
-}
-
 struct PolicyIn {
   const float *old_logp, *ref_logp, *adv;
   float lo, hi, beta, scale;  // the ratio's clip bounds; loss factors
@@ -152,10 +127,10 @@ struct PolicyTerm {
   float policy, kl, slope;
 };
 
-__device__ __forceinline__ PolicyTerm policy_term(const PolicyIn& p, int64_t t, double lp) {
+__device__ __forceinline__ PolicyTerm policy_term(const PolicyIn& p, double lp, float old, float ref,
+                                                  float a) {
   PolicyTerm o;
-  const float a = p.adv[t];
-  const float ratio = expf((float)(lp - (double)p.old_logp[t]));
+  const float ratio = expf((float)(lp - (double)old));
   const float freed = ratio * a;
   const float held = fminf(fmaxf(ratio, p.lo), p.hi) * a;
   const bool clipped = freed > held;  // a NaN ratio is not clipped away
@@ -163,7 +138,7 @@ __device__ __forceinline__ PolicyTerm policy_term(const PolicyIn& p, int64_t t, 
   o.slope = clipped ? 0.f : -freed;
   o.kl = 0.f;
   if (p.beta != 0.f) {
-    const float u = (float)((double)p.ref_logp[t] - lp);
+    const float u = (float)((double)ref - lp);
     const float e = expm1f(u);
     // exp(u) - 1 - u; near 0 by its series, whose first terms do not cancel
     o.kl = fabsf(u) < 0.25f
@@ -204,7 +179,9 @@ __global__ void __launch_bounds__(kTokenThreads)
     }
     const double w = r.weight != nullptr ? (double)r.weight[t] : 1.0;
     const float2 ms = row[t];
-    const PolicyTerm o = policy_term(p, t, log_prob(to_f(r.x[t * r.ld + y]) - ms.x, ms.y, r.inv_t));
+    const PolicyTerm o =
+        policy_term(p, log_prob(to_f(r.x[t * r.ld + y]) - ms.x, ms.y, r.inv_t), p.old_logp[t],
+                    p.beta != 0.f ? p.ref_logp[t] : 0.f, p.adv[t]);
     pol += w * (double)o.policy;
     kl += w * (double)o.kl;
     coef[t] = (float)(f * w * r.inv_t * (double)o.slope);
@@ -327,6 +304,9 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
+#include "mbarrier.cuh"
+#include "row_pipe.cuh"
+
 // ------------------------------------------------------------- host side
 struct RowsArg {
   const void* logits;
@@ -389,12 +369,105 @@ Rows<T> rows_of(const RowsArg& a) {
 
 unsigned row_grid(int64_t T_) { return (unsigned)std::min<int64_t>(T_, 152 * 4); }
 
+#ifndef VSF_PIPE_W
+#define VSF_PIPE_W 8
+#endif
+#ifndef VSF_PIPE_SLOTS
+#define VSF_PIPE_SLOTS 12
+#endif
+constexpr int kPipeWarps = VSF_PIPE_W;
+constexpr uint32_t kPipeSlots = VSF_PIPE_SLOTS;
+
+// Clusters of C CTAs of a kernel that fit on the current device at a time,
+// looked up once per device and size; 0 with *e set where that fails.
+template <typename T, bool POLICY>
+int pipe_clusters(int C, cudaError_t* e) {
+  using Shape = PipeShape<kPipeWarps>;
+  static std::mutex mu;
+  static int cached[64][5] = {};
+  int dev = 0;
+  if ((*e = cudaGetDevice(&dev)) != cudaSuccess) return 0;
+  if (dev < 0 || dev >= 64) {
+    *e = cudaErrorInvalidDevice;
+    return 0;
+  }
+  int slot = 0;
+  while ((1 << slot) < C) ++slot;
+  std::lock_guard<std::mutex> lock(mu);
+  int& n = cached[dev][slot];
+  if (n == 0) {
+    auto fn = row_pipe_kernel<T, kPipeWarps, POLICY>;
+    constexpr uint32_t smem = pipe_smem<kPipeWarps>(kPipeSlots);
+    *e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (*e != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C * 64);
+    cfg.blockDim = dim3(Shape::threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int got = 0;
+    *e = cudaOccupancyMaxActiveClusters(&got, fn, &cfg);
+    if (*e != cudaSuccess) return 0;
+    n = std::max(1, std::min(got, kMaxPipeClusters));
+  }
+  return n;
+}
+
+// CTAs that share a row. `hold`: the share stays in the ring until its
+// gradient is written, so it may fill at most two thirds of it (the rest reads
+// ahead); 0 if no cluster size does that. With few rows, more CTAs a row as
+// long as they all run at a time and each has a chunk's half to read.
+template <typename T>
+int pipe_cluster_size(int64_t T_, int64_t V, bool hold) {
+  constexpr int64_t CV = PipeShape<kPipeWarps>::chunk_vecs;
+  const int64_t nvec = V / Vec<T>::n;
+  int C = 1;
+  while (hold && (nvec / C + 1 + CV - 1) / CV > kPipeSlots * 2 / 3) {
+    C *= 2;
+    if (C > 8) return 0;
+  }
+  while (C < 8 && T_ * C * 2 <= 152 * (16 / kPipeWarps) && nvec / (2 * C) >= CV / 2) C *= 2;
+  return C;
+}
+
+template <typename T, bool POLICY>
+cudaError_t launch_pipe(PipeArgs<T>& a, int C, cudaStream_t st) {
+  using Shape = PipeShape<kPipeWarps>;
+  cudaError_t e = cudaSuccess;
+  const int most = pipe_clusters<T, POLICY>(C, &e);
+  if (most == 0) return e;
+  a.slots = kPipeSlots;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(C * std::max<int64_t>(1, std::min<int64_t>(most, a.r.T_))));
+  cfg.blockDim = dim3(Shape::threads);
+  cfg.dynamicSmemBytes = pipe_smem<kPipeWarps>(kPipeSlots);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, row_pipe_kernel<T, kPipeWarps, POLICY>, a);
+}
+
 template <typename T>
 cudaError_t launch_stats(const Rows<T>& r, float2* row, float* logp, WsHead* head,
                          cudaStream_t st) {
   if (r.T_ == 0) return cudaSuccess;
-  row_stats_kernel<T><<<row_grid(r.T_), kRowThreads, 0, st>>>(r, row, logp, head);
-  return cudaGetLastError();
+  PipeArgs<T> a = {};
+  a.r = r;
+  a.row = row;
+  a.logp = logp;
+  a.head = head;
+  return launch_pipe<T, false>(a, pipe_cluster_size<T>(r.T_, r.V, false), st);
 }
 
 template <typename T>
@@ -410,6 +483,20 @@ template <typename T>
 cudaError_t policy(const RowsArg& a, const PolicyIn& p, float* stats, float* logp, void* grad,
                    int64_t grad_ld, const ObjectiveWs& w, cudaStream_t st) {
   const Rows<T> r = rows_of<T>(a);
+  const int C = pipe_cluster_size<T>(r.T_, r.V, true);
+  if (C > 0) {
+    PipeArgs<T> k = {};
+    k.r = r;
+    k.p = p;
+    k.grad = static_cast<T*>(grad);
+    k.grad_ld = grad_ld;
+    k.logp = logp;
+    k.stats = stats;
+    k.head = w.head;
+    k.partial = w.partial;
+    return launch_pipe<T, true>(k, C, st);
+  }
+  // a row too long for a cluster's shared memory: statistics, then gradient
   cudaError_t e = launch_stats(r, w.row, logp, w.head, st);
   if (e != cudaSuccess) return e;
   policy_tokens_kernel<T><<<1, kTokenThreads, 0, st>>>(r, p, w.row, w.coef, stats);

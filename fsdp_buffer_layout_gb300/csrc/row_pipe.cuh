@@ -1,0 +1,548 @@
+// row_pipe.cuh — the pipelined kernel over rows of logits: each live row's
+// maximum and sum (and with them its log probability), or, for the policy
+// loss, the row's gradient in the same pass over device memory. Included by
+// objective.cu.
+//
+// A cluster of C CTAs takes a row, each CTA an equal share of its 16-byte
+// vectors. In a CTA the last warp streams the share into a ring of
+// shared-memory chunks with bulk copies; W consumer warps add up the terms
+// exp(x - m) of each chunk with a running maximum a thread. The threads' sums
+// are joined in the warp, in the CTA and, with 16-byte asynchronous stores
+// into every CTA of the cluster, over the row. The policy loss then reads the
+// share once more from shared memory, where the chunks have stayed, and writes
+// the gradient; only then do they go back to the producer. So logits cross the
+// memory bus once and gradients once.
+//
+// Elements in front of a row's first 16-byte boundary and behind its last one
+// are read by single threads. A gradient row whose address differs from the
+// logits' modulo 16 bytes is written element by element.
+//
+// Every wait is bounded (mbarrier.cuh): after a timeout the CTA still passes
+// its barriers and sends its messages, but skips the arithmetic.
+
+// 16 bytes of a row as floats in pairs.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<uint16_t> {
+  static constexpr int n = 8;
+  static constexpr uint32_t lowest = 0xff80ff80u;  // -inf, -inf
+};
+template <>
+struct Vec<float> {
+  static constexpr int n = 4;
+  static constexpr uint32_t lowest = 0xff800000u;
+};
+
+// Pairs of floats in the packed fp32 instructions of sm_100 and later: one
+// issue slot for two elements.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_get(F2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v.v));
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// The pairs of one vector.
+template <typename T>
+struct Pairs {
+  F2 p[Vec<T>::n / 2];
+};
+__device__ __forceinline__ void unpack(const uint4& v, Pairs<uint16_t>& o) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o.p[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void unpack(const uint4& v, Pairs<float>& o) {
+  o.p[0] = f2(__uint_as_float(v.x), __uint_as_float(v.y));
+  o.p[1] = f2(__uint_as_float(v.z), __uint_as_float(v.w));
+}
+
+// Largest element of two vectors; NaN is passed over.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ float largest(const uint4& a, const uint4& b);
+template <>
+__device__ __forceinline__ float largest<uint16_t>(const uint4& a, const uint4& b) {
+  const uint32_t m = max_bf16x2(max_bf16x2(max_bf16x2(a.x, a.y), max_bf16x2(a.z, a.w)),
+                                max_bf16x2(max_bf16x2(b.x, b.y), max_bf16x2(b.z, b.w)));
+  return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float largest<float>(const uint4& a, const uint4& b) {
+  return fmaxf(fmaxf(fmaxf(__uint_as_float(a.x), __uint_as_float(a.y)),
+                     fmaxf(__uint_as_float(a.z), __uint_as_float(a.w))),
+               fmaxf(fmaxf(__uint_as_float(b.x), __uint_as_float(b.y)),
+                     fmaxf(__uint_as_float(b.z), __uint_as_float(b.w))));
+}
+
+// exp((x - m) / temperature) of a pair, with nm = (-m, -m).
+struct PairScale {
+  F2 hi, lo;
+};
+__device__ __forceinline__ F2 exp_pair(F2 x, F2 nm, const PairScale& c) {
+  const F2 d = f2_add(x, nm);
+  float a, b;
+  f2_get(f2_fma(d, c.hi, f2_mul(d, c.lo)), a, b);
+  return f2(ex2(a), ex2(b));
+}
+
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cta_count() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// 16 bytes into the shared memory of the cluster's CTA `rank`, completing
+// transaction bytes on its barrier.
+__device__ __forceinline__ void put_async(uint32_t slot, uint32_t bar, uint32_t rank, float a,
+                                          float b, float c) {
+  uint32_t rs, rb;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rs) : "r"(slot), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rb) : "r"(bar), "r"(rank));
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+          rs),
+      "f"(a), "f"(b), "f"(c), "f"(0.f), "r"(rb)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack_vec(const float (&o)[Vec<T>::n]);
+template <>
+__device__ __forceinline__ uint4 pack_vec<uint16_t>(const float (&o)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(o[2 * i + 1]), "f"(o[2 * i]));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <>
+__device__ __forceinline__ uint4 pack_vec<float>(const float (&o)[4]) {
+  return make_uint4(__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]),
+                    __float_as_uint(o[3]));
+}
+
+constexpr int kMaxPipeCluster = 16;
+
+// One shape of the kernel: W consumer warps, each thread two vectors of a
+// chunk.
+template <int W>
+struct PipeShape {
+  static constexpr int consumers = W * 32;
+  static constexpr int threads = consumers + 32;
+  static constexpr int chunk_vecs = 2 * consumers;
+  static constexpr uint32_t chunk_bytes = chunk_vecs * 16;
+};
+
+struct PipeTail {  // shared memory behind the ring and its barriers
+  float4 message[2][kMaxPipeCluster];
+  MaxSum part[2][16];
+  double sum[16];
+  float4 result;  // m, b = -a / s, a
+  uint32_t stop, xstop;
+};
+
+template <int W>
+constexpr uint32_t pipe_smem(uint32_t slots) {
+  return slots * PipeShape<W>::chunk_bytes + 16 * slots + 16 + (uint32_t)sizeof(PipeTail) + 128;
+}
+
+template <typename T>
+struct PipeArgs {
+  Rows<T> r;
+  PolicyIn p;
+  T* grad;
+  int64_t grad_ld;
+  float2* row;   // statistics: {m, s} of a live row, or NULL
+  float* logp;
+  float* stats;  // policy: fp32[4]
+  WsHead* head;
+  double* partial;  // policy: {policy, kl, weight} sums of each cluster
+  uint32_t slots;
+};
+
+// Where a row's vectors lie: `head` elements, then nvec vectors, then a tail.
+struct Span {
+  int32_t head, nvec;
+};
+template <typename T>
+__device__ __forceinline__ Span span_of(const T* p, int32_t V) {
+  const int32_t skew = (int32_t)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (int32_t)sizeof(T);
+  const int32_t head = min(skew, V);
+  return {head, (V - head) / Vec<T>::n};
+}
+__device__ __forceinline__ int32_t share(int32_t nvec, uint32_t rank, uint32_t count) {
+  return (int32_t)((int64_t)nvec * rank / count);
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  return v;
+}
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  return v;
+}
+// The join of a warp's maxima and sums.
+__device__ __forceinline__ MaxSum warp_join(MaxSum v, float inv_t) {
+  const float m = warp_max(v.m);
+  return {m, warp_sum(v.s * expf((v.m - finite_max(m)) * inv_t))};
+}
+
+// Zeroes the gradient row's share of this CTA.
+template <typename T>
+__device__ __forceinline__ void zero_share(T* g, int32_t V, uint32_t rank, uint32_t count, int tid,
+                                           int threads) {
+  const Span s = span_of(g, V);
+  uint4* v = reinterpret_cast<uint4*>(g + s.head);
+  const int32_t end = share(s.nvec, rank + 1, count);
+  for (int32_t i = share(s.nvec, rank, count) + tid; i < end; i += threads)
+    __stcs(v + i, make_uint4(0, 0, 0, 0));
+  const int32_t tail = s.head + s.nvec * Vec<T>::n;
+  if (rank == 0 && tid < s.head) g[tid] = from_f<T>(0.f);
+  if (rank + 1 == count && tail + tid < V) g[tail + tid] = from_f<T>(0.f);
+}
+
+template <typename T, int W, bool POLICY>
+__global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
+    row_pipe_kernel(const __grid_constant__ PipeArgs<T> a) {
+  using Shape = PipeShape<W>;
+  constexpr int VE = Vec<T>::n;
+  extern __shared__ unsigned char raw[];
+  unsigned char* ring =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~(uintptr_t)127);
+  const uint32_t slots = a.slots;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + slots * Shape::chunk_bytes);
+  PipeTail* sh = reinterpret_cast<PipeTail*>(bars + 2 * slots + 2);
+  const uint32_t full = smem_u32(bars), empty = smem_u32(bars + slots);
+  const uint32_t xbar = smem_u32(bars + 2 * slots);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t C = cta_count(), rank = C > 1 ? cta_rank() : 0;
+  const int64_t cluster = blockIdx.x / C, clusters = gridDim.x / C;
+  const Rows<T>& r = a.r;
+  unsigned* err = &a.head->err;
+
+  if (tid == 0) {
+    for (uint32_t s = 0; s < slots; ++s) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, W);
+    }
+    mbar_init(xbar, 1);
+    mbar_init(xbar + 8, 1);
+    sh->stop = sh->xstop = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  __syncthreads();
+  if (C > 1) cluster_sync();
+
+  if (warp == W) {  // ------------------------------------------- producer
+    if (lane == 0) {
+      uint32_t k = 0;  // chunks issued
+      bool ok = true;
+      Token next = token_at(r, cluster);
+      for (int64_t t = cluster; t < r.T_ && ok; t += clusters) {
+        const int32_t y = live_target(r, next, nullptr);
+        next = token_at(r, t + clusters);
+        if (y < 0) continue;
+        const T* x = r.x + t * r.ld;
+        const Span s = span_of(x, r.V);
+        const char* base = reinterpret_cast<const char*>(x + s.head);
+        const int32_t end = share(s.nvec, rank + 1, C);
+        for (int32_t v = share(s.nvec, rank, C); v < end; v += Shape::chunk_vecs, ++k) {
+          const uint32_t slot = k % slots;
+          if (k >= slots && !mbar_wait(empty + 8 * slot, ((k / slots) - 1) & 1, err, &sh->stop)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bytes = (uint32_t)min(end - v, (int32_t)Shape::chunk_vecs) * 16;
+          mbar_expect_tx(full + 8 * slot, bytes);
+          bulk_load(smem_u32(ring + slot * Shape::chunk_bytes), base + (int64_t)v * 16, bytes,
+                    full + 8 * slot);
+        }
+      }
+      // every copy issued has to land before the CTA may end
+      const uint64_t deadline = global_ns() + kWaitNs;
+      for (uint32_t j = k > slots ? k - slots : 0; j < k; ++j)
+        if (!mbar_drain(full + 8 * (j % slots), (j / slots) & 1, deadline, err)) break;
+    }
+  } else {  // ---------------------------------------------------- consumers
+    auto sync_consumers = [] {
+      asm volatile("bar.sync 1, %0;" ::"r"(Shape::consumers) : "memory");
+    };
+    const PairScale c2 = {f2(r.c.hi, r.c.hi), f2(r.c.lo, r.c.lo)};
+    double factor = 0.0, weight_sum = 0.0, pol = 0.0, kls = 0.0;
+    if (POLICY) {
+      // The sum of the live weights scales every gradient: each CTA adds it up
+      // for itself, in the same order, while its first row is on its way.
+      factor = (double)a.p.scale;
+      if (a.p.mean) {
+        float w4[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int64_t t = tid; t < r.T_; t += 4 * Shape::consumers)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int64_t u = t + j * Shape::consumers;
+            if (u < r.T_) {
+              const int64_t y = r.target[u];
+              if (y >= 0 && y < r.V) w4[j] += r.weight != nullptr ? r.weight[u] : 1.f;
+            }
+          }
+        const double n = warp_sum(((double)w4[0] + w4[1]) + ((double)w4[2] + w4[3]));
+        if (lane == 0) sh->sum[warp] = n;
+        sync_consumers();
+        double all = 0.0;
+        for (int w = 0; w < W; ++w) all += sh->sum[w];
+        if (all != 0.0) factor /= all;
+      }
+    }
+    uint32_t k = 0, done = 0;  // chunks taken; live rows done
+    bool ok = true;
+    Token next = token_at(r, cluster);
+    for (int64_t t = cluster; t < r.T_; t += clusters) {
+      const int32_t y = live_target(r, next, tid == 0 ? err : nullptr);
+      const float weight = next.w;
+      next = token_at(r, t + clusters);
+      if (y < 0) {
+        if (POLICY && a.grad != nullptr)
+          zero_share(a.grad + t * a.grad_ld, r.V, rank, C, tid, Shape::consumers);
+        if (tid == 0 && rank == 0 && a.logp != nullptr) a.logp[t] = 0.f;
+        continue;
+      }
+      const T* x = r.x + t * r.ld;
+      // the scalars of the token, on their way while the row is added up
+      float xy = 0.f, old = 0.f, ref = 0.f, adv = 0.f;
+      if (warp == 0) {
+        xy = to_f(x[y]);
+        if (POLICY) {
+          old = a.p.old_logp[t];
+          adv = a.p.adv[t];
+          if (a.p.beta != 0.f) ref = a.p.ref_logp[t];
+        }
+      }
+      const Span s = span_of(x, r.V);
+      const int32_t begin = share(s.nvec, rank, C), end = share(s.nvec, rank + 1, C);
+      // the loose element of this thread, if any
+      int32_t loose = -1;
+      if (rank == 0 && tid < s.head) loose = tid;
+      if (rank + 1 == C && tid >= 16 && s.head + s.nvec * VE + tid - 16 < r.V)
+        loose = s.head + s.nvec * VE + tid - 16;
+      float xl = -INFINITY;
+      if (loose >= 0) xl = to_f(x[loose]);
+
+      // ---- maximum and sum
+      float m = -INFINITY, sl = 0.f;
+      F2 sum0 = f2(0.f, 0.f), sum1 = sum0;
+      const uint32_t k0 = k;
+      for (int32_t v = begin; v < end; v += Shape::chunk_vecs, ++k) {
+        const uint32_t slot = k % slots;
+        ok = mbar_wait(full + 8 * slot, (k / slots) & 1, err, &sh->stop) && ok;
+        if (!ok) continue;
+        const uint4* q = reinterpret_cast<const uint4*>(ring + slot * Shape::chunk_bytes);
+        const int32_t n = end - v;
+        if (tid < n) {
+          const uint4 v0 = q[tid];
+          uint4 v1 = make_uint4(Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest);
+          if (tid + Shape::consumers < n) v1 = q[tid + Shape::consumers];
+          const float bm = largest<T>(v0, v1);
+          if (bm > m) {
+            const float f = expf((m - bm) * r.inv_tf);
+            sum0 = f2_mul(sum0, f2(f, f));
+            sum1 = f2_mul(sum1, f2(f, f));
+            m = bm;
+          }
+          const float z = -finite_max(m);
+          const F2 nm = f2(z, z);
+          Pairs<T> p0, p1;
+          unpack(v0, p0);
+          unpack(v1, p1);
+#pragma unroll
+          for (int i = 0; i < VE / 2; ++i) {
+            sum0 = f2_add(sum0, exp_pair(p0.p[i], nm, c2));
+            sum1 = f2_add(sum1, exp_pair(p1.p[i], nm, c2));
+          }
+        }
+        if (!POLICY) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty + 8 * slot);
+        }
+      }
+      {
+        float s0, s1, s2, s3;
+        f2_get(sum0, s0, s1);
+        f2_get(sum1, s2, s3);
+        sl = (s0 + s1) + (s2 + s3);
+      }
+      MaxSum ms = {m, sl};
+      if (loose >= 0) ms = join(ms, {xl, xl == -INFINITY ? 0.f : 1.f}, r.inv_tf);
+      if (xl != xl) ms.s = xl;
+      // ---- joined over the warp, the CTA and the cluster
+      const uint32_t par = done & 1;
+      ms = warp_join(ms, r.inv_tf);
+      if (lane == 0) sh->part[par][warp] = ms;
+      sync_consumers();
+      if (warp == 0) {
+        ms = lane < W ? sh->part[par][lane] : MaxSum{-INFINITY, 0.f};
+        ms = warp_join(ms, r.inv_tf);
+        if (C > 1) {
+          const uint32_t bar = xbar + 8 * par;
+          if (lane == 0) mbar_expect_tx(bar, C * 16);
+          __syncwarp();
+          // xy goes with the message, so that it has been read before any
+          // CTA of the cluster may write the gradient over the logits
+          if (lane < C) put_async(smem_u32(&sh->message[par][rank]), bar, lane, ms.m, ms.s, xy);
+          mbar_wait_cluster(bar, (done >> 1) & 1, err, &sh->xstop);
+          const float4 got = sh->message[par][lane < C ? lane : 0];
+          ms = warp_join(lane < C ? MaxSum{got.x, got.y} : MaxSum{-INFINITY, 0.f}, r.inv_tf);
+        }
+        const double lp = log_prob(xy - ms.m, ms.s, r.inv_t);
+        if (lane == 0 && rank == 0) {
+          if (a.row != nullptr) a.row[t] = make_float2(ms.m, ms.s);
+          if (a.logp != nullptr) a.logp[t] = (float)lp;
+        }
+        if (POLICY) {
+          const PolicyTerm o = policy_term(a.p, lp, old, ref, adv);
+          const float coef = (float)(factor * (double)weight * r.inv_t * (double)o.slope);
+          pol += (double)weight * (double)o.policy;
+          kls += (double)weight * (double)o.kl;
+          weight_sum += (double)weight;
+          if (lane == 0) sh->result = make_float4(ms.m, -coef / ms.s, coef, 0.f);
+        }
+      }
+      ++done;
+      if (!POLICY) continue;
+      sync_consumers();
+      // ---- the gradient from the chunks still in shared memory
+      const float4 res = sh->result;
+      if (a.grad != nullptr) {
+        T* g = a.grad + t * a.grad_ld;
+        const float z = finite_max(res.x), b = res.y, coef = res.z;
+        if (coef == 0.f) {
+          zero_share(g, r.V, rank, C, tid, Shape::consumers);
+        } else {
+          const bool same = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
+          const F2 nm = f2(-z, -z), b2 = f2(b, b);
+          uint4* gv = reinterpret_cast<uint4*>(g + s.head);
+          const int32_t yv = y >= s.head ? (y - s.head) / VE : -1;  // the target's vector
+          uint32_t kk = k0;
+          for (int32_t v = begin; v < end && ok; v += Shape::chunk_vecs, ++kk) {
+            const unsigned char* chunk = ring + (kk % slots) * Shape::chunk_bytes;
+            const int32_t n = min(end - v, (int32_t)Shape::chunk_vecs);
+            if (same) {
+              const uint4* q = reinterpret_cast<const uint4*>(chunk);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int32_t i = tid + j * Shape::consumers;
+                if (i >= n) break;
+                Pairs<T> p;
+                unpack(q[i], p);
+                float o[VE];
+#pragma unroll
+                for (int e = 0; e < VE / 2; ++e)
+                  f2_get(f2_mul(exp_pair(p.p[e], nm, c2), b2), o[2 * e], o[2 * e + 1]);
+                if (v + i == yv) {
+#pragma unroll
+                  for (int e = 0; e < VE; ++e)
+                    if (s.head + yv * VE + e == y) o[e] += coef;
+                }
+                __stcs(gv + v + i, pack_vec<T>(o));
+              }
+            } else {
+              const T* q = reinterpret_cast<const T*>(chunk);
+              const int32_t first = s.head + v * VE;
+              for (int32_t i = tid; i < n * VE; i += Shape::consumers) {
+                const float e = b * exp_scaled(to_f(q[i]) - z, r.c);
+                g[first + i] = from_f<T>(first + i == y ? e + coef : e);
+              }
+            }
+          }
+          if (loose >= 0) {
+            const float e = b * exp_scaled(xl - z, r.c);
+            g[loose] = from_f<T>(loose == y ? e + coef : e);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0 && ok)
+        for (uint32_t j = k0; j < k; ++j) mbar_arrive(empty + 8 * (j % slots));
+    }
+    if (POLICY && warp == 0 && rank == 0) {
+      // the last cluster to finish adds up all of them in their order
+      uint32_t last = 0;
+      if (lane == 0) {
+        double* p = a.partial + 3 * cluster;
+        p[0] = pol;
+        p[1] = kls;
+        p[2] = weight_sum;
+        __threadfence();
+        last = atomicAdd(&a.head->ticket, 1u) + 1 == (uint32_t)clusters;
+        __threadfence();
+      }
+      if (__shfl_sync(~0u, last, 0)) {
+        double v[3] = {0.0, 0.0, 0.0};
+        for (int64_t q = lane; q < clusters; q += 32)
+          for (int j = 0; j < 3; ++j) v[j] += __ldcg(a.partial + 3 * q + j);
+        for (int j = 0; j < 3; ++j) v[j] = warp_sum(v[j]);
+        if (lane == 0) {
+          const double f = (double)a.p.scale / (a.p.mean && v[2] != 0.0 ? v[2] : 1.0);
+          a.stats[0] = (float)(f * (v[0] + (a.p.beta != 0.f ? (double)a.p.beta * v[1] : 0.0)));
+          a.stats[1] = (float)(f * v[0]);
+          a.stats[2] = (float)(f * v[1]);
+          a.stats[3] = (float)v[2];
+          a.head->ticket = 0;
+        }
+      }
+    }
+  }
+  __syncwarp();
+  // no CTA leaves while another of its cluster may still write to it
+  if (C > 1) cluster_sync();
+}

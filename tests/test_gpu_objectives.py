@@ -258,12 +258,14 @@ def test_no_tokens():
 
 
 def test_offsets_past_32_bits():
-    """Rows at element offsets above 2^32, in the logits and in the gradient."""
+    """Rows at element offsets above 2^32, in the logits and in the gradient,
+    against the same rows close together (at the same places modulo 16 bytes,
+    which set the order of a row's sum)."""
     from fsdp_buffer_layout_gb300.objectives import PolicyLoss
     ld, vocab = (1 << 30) + 8, 1003
     x = torch.empty(4 * ld + vocab, dtype=BF16, device="cuda").as_strided((5, vocab), (ld, 1))
     g = torch.empty(4 * ld + vocab, dtype=BF16, device="cuda").as_strided((5, vocab), (ld, 1))
-    small, y, w, old, ref, adv = policy_case(5, vocab, BF16, masked=False)
+    small, y, w, old, ref, adv = policy_case(5, vocab, BF16, pad=5, masked=False)
     x.copy_(small)
     op = PolicyLoss(5, vocab, kl_beta=0.1)
     args = (dev(y, torch.int64), dev(old), dev(adv), dev(ref), dev(w))
