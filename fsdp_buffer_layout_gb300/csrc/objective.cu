@@ -372,11 +372,7 @@ unsigned row_grid(int64_t T_) { return (unsigned)std::min<int64_t>(T_, 152 * 4);
 #ifndef VSF_PIPE_W
 #define VSF_PIPE_W 8
 #endif
-#ifndef VSF_PIPE_SLOTS
-#define VSF_PIPE_SLOTS 12
-#endif
 constexpr int kPipeWarps = VSF_PIPE_W;
-constexpr uint32_t kPipeSlots = VSF_PIPE_SLOTS;
 
 // Clusters of C CTAs of a kernel that fit on the current device at a time,
 // looked up once per device and size; 0 with *e set where that fails.
@@ -397,7 +393,7 @@ int pipe_clusters(int C, cudaError_t* e) {
   int& n = cached[dev][slot];
   if (n == 0) {
     auto fn = row_pipe_kernel<T, kPipeWarps, POLICY>;
-    constexpr uint32_t smem = pipe_smem<kPipeWarps>(kPipeSlots);
+    constexpr uint32_t smem = pipe_smem<kPipeWarps>();
     *e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (*e != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
@@ -428,11 +424,11 @@ int pipe_cluster_size(int64_t T_, int64_t V, bool hold) {
   constexpr int64_t CV = PipeShape<kPipeWarps>::chunk_vecs;
   const int64_t nvec = V / Vec<T>::n;
   int C = 1;
-  while (hold && (nvec / C + 1 + CV - 1) / CV > kPipeSlots * 2 / 3) {
+  while (hold && (nvec / C + 1 + CV - 1) / CV > (int)PipeShape<kPipeWarps>::slots * 2 / 3) {
     C *= 2;
     if (C > 8) return 0;
   }
-  while (C < 8 && T_ * C * 2 <= 152 * (16 / kPipeWarps) && nvec / (2 * C) >= CV / 2) C *= 2;
+  while (C < 8 && T_ * C * 2 <= 152 * (16 / kPipeWarps) && nvec / (2 * C) >= 256) C *= 2;
   return C;
 }
 
@@ -442,11 +438,10 @@ cudaError_t launch_pipe(PipeArgs<T>& a, int C, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   const int most = pipe_clusters<T, POLICY>(C, &e);
   if (most == 0) return e;
-  a.slots = kPipeSlots;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(C * std::max<int64_t>(1, std::min<int64_t>(most, a.r.T_))));
   cfg.blockDim = dim3(Shape::threads);
-  cfg.dynamicSmemBytes = pipe_smem<kPipeWarps>(kPipeSlots);
+  cfg.dynamicSmemBytes = pipe_smem<kPipeWarps>();
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -47,6 +47,20 @@ __device__ __forceinline__ F2 f2(float a, float b) {
 __device__ __forceinline__ void f2_get(F2 v, float& a, float& b) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v.v));
 }
+#ifdef VSF_SCALAR
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  float a0, a1, b0, b1;
+  f2_get(a, a0, a1);
+  f2_get(b, b0, b1);
+  return f2(__fadd_rn(a0, b0), __fadd_rn(a1, b1));
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  float a0, a1, b0, b1;
+  f2_get(a, a0, a1);
+  f2_get(b, b0, b1);
+  return f2(__fmul_rn(a0, b0), __fmul_rn(a1, b1));
+}
+#else
 __device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
   F2 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
@@ -57,6 +71,7 @@ __device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
+#endif
 __device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
   F2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
@@ -79,38 +94,53 @@ __device__ __forceinline__ void unpack(const uint4& v, Pairs<float>& o) {
   o.p[1] = f2(__uint_as_float(v.z), __uint_as_float(v.w));
 }
 
-// Largest element of two vectors; NaN is passed over.
+// Largest element of a thread's vectors; NaN is passed over.
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-template <typename T>
-__device__ __forceinline__ float largest(const uint4& a, const uint4& b);
-template <>
-__device__ __forceinline__ float largest<uint16_t>(const uint4& a, const uint4& b) {
-  const uint32_t m = max_bf16x2(max_bf16x2(max_bf16x2(a.x, a.y), max_bf16x2(a.z, a.w)),
-                                max_bf16x2(max_bf16x2(b.x, b.y), max_bf16x2(b.z, b.w)));
+template <int N>
+__device__ __forceinline__ float largest(const uint4 (&v)[N], uint16_t) {
+  uint32_t m = Vec<uint16_t>::lowest;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    m = max_bf16x2(m, max_bf16x2(max_bf16x2(v[i].x, v[i].y), max_bf16x2(v[i].z, v[i].w)));
   return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
 }
-template <>
-__device__ __forceinline__ float largest<float>(const uint4& a, const uint4& b) {
-  return fmaxf(fmaxf(fmaxf(__uint_as_float(a.x), __uint_as_float(a.y)),
-                     fmaxf(__uint_as_float(a.z), __uint_as_float(a.w))),
-               fmaxf(fmaxf(__uint_as_float(b.x), __uint_as_float(b.y)),
-                     fmaxf(__uint_as_float(b.z), __uint_as_float(b.w))));
+template <int N>
+__device__ __forceinline__ float largest(const uint4 (&v)[N], float) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(v[i].x), __uint_as_float(v[i].y)),
+                       fmaxf(__uint_as_float(v[i].z), __uint_as_float(v[i].w))));
+  return m;
 }
 
 // exp((x - m) / temperature) of a pair, with nm = (-m, -m).
 struct PairScale {
   F2 hi, lo;
 };
+#ifdef VSF_SCALAR
+__device__ __forceinline__ F2 exp_pair(F2 x, F2 nm, const PairScale& c) {
+  float x0, x1, m0, m1, h0, h1, l0, l1;
+  f2_get(x, x0, x1);
+  f2_get(nm, m0, m1);
+  f2_get(c.hi, h0, h1);
+  f2_get(c.lo, l0, l1);
+  x0 = __fadd_rn(x0, m0);
+  x1 = __fadd_rn(x1, m0);
+  return f2(ex2(__fmaf_rn(x0, h0, __fmul_rn(x0, l0))), ex2(__fmaf_rn(x1, h0, __fmul_rn(x1, l0))));
+}
+#else
 __device__ __forceinline__ F2 exp_pair(F2 x, F2 nm, const PairScale& c) {
   const F2 d = f2_add(x, nm);
   float a, b;
   f2_get(f2_fma(d, c.hi, f2_mul(d, c.lo)), a, b);
   return f2(ex2(a), ex2(b));
 }
+#endif
 
 __device__ __forceinline__ uint32_t cta_rank() {
   uint32_t r;
@@ -166,27 +196,40 @@ __device__ __forceinline__ uint4 pack_vec<float>(const float (&o)[4]) {
 
 constexpr int kMaxPipeCluster = 16;
 
-// One shape of the kernel: W consumer warps, each thread two vectors of a
-// chunk.
+// One shape of the kernel: W consumer warps, each thread `per` vectors of a
+// chunk, and a ring of 96 KB a CTA at W = 8, two CTAs an SM.
 template <int W>
 struct PipeShape {
+  static constexpr int per = 4;
   static constexpr int consumers = W * 32;
   static constexpr int threads = consumers + 32;
-  static constexpr int chunk_vecs = 2 * consumers;
+  static constexpr int chunk_vecs = per * consumers;
   static constexpr uint32_t chunk_bytes = chunk_vecs * 16;
+  static constexpr uint32_t slots = (W * 12u * 1024u) / chunk_bytes;
+};
+// A place in the ring: slot and how often the ring has gone round, modulo 2.
+template <uint32_t SLOTS>
+struct Place {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == SLOTS) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
 };
 
 struct PipeTail {  // shared memory behind the ring and its barriers
   float4 message[2][kMaxPipeCluster];
   MaxSum part[2][16];
   double sum[16];
-  float4 result;  // m, b = -a / s, a
+  float4 result;  // m, b = -a / s, a, x_y
   uint32_t stop, xstop;
 };
 
 template <int W>
-constexpr uint32_t pipe_smem(uint32_t slots) {
-  return slots * PipeShape<W>::chunk_bytes + 16 * slots + 16 + (uint32_t)sizeof(PipeTail) + 128;
+constexpr uint32_t pipe_smem() {
+  return PipeShape<W>::slots * (PipeShape<W>::chunk_bytes + 16) + 16 + (uint32_t)sizeof(PipeTail) + 128;
 }
 
 template <typename T>
@@ -200,7 +243,6 @@ struct PipeArgs {
   float* stats;  // policy: fp32[4]
   WsHead* head;
   double* partial;  // policy: {policy, kl, weight} sums of each cluster
-  uint32_t slots;
 };
 
 // Where a row's vectors lie: `head` elements, then nvec vectors, then a tail.
@@ -260,7 +302,7 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
   extern __shared__ unsigned char raw[];
   unsigned char* ring =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~(uintptr_t)127);
-  const uint32_t slots = a.slots;
+  constexpr uint32_t slots = Shape::slots;
   uint64_t* bars = reinterpret_cast<uint64_t*>(ring + slots * Shape::chunk_bytes);
   PipeTail* sh = reinterpret_cast<PipeTail*>(bars + 2 * slots + 2);
   const uint32_t full = smem_u32(bars), empty = smem_u32(bars + slots);
@@ -287,7 +329,8 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
 
   if (warp == W) {  // ------------------------------------------- producer
     if (lane == 0) {
-      uint32_t k = 0;  // chunks issued
+      uint32_t issued = 0;  // chunks, counted up to the ring's length
+      Place<slots> at;
       bool ok = true;
       Token next = token_at(r, cluster);
       for (int64_t t = cluster; t < r.T_ && ok; t += clusters) {
@@ -298,9 +341,9 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
         const Span s = span_of(x, r.V);
         const char* base = reinterpret_cast<const char*>(x + s.head);
         const int32_t end = share(s.nvec, rank + 1, C);
-        for (int32_t v = share(s.nvec, rank, C); v < end; v += Shape::chunk_vecs, ++k) {
-          const uint32_t slot = k % slots;
-          if (k >= slots && !mbar_wait(empty + 8 * slot, ((k / slots) - 1) & 1, err, &sh->stop)) {
+        for (int32_t v = share(s.nvec, rank, C); v < end; v += Shape::chunk_vecs) {
+          const uint32_t slot = at.slot;
+          if (issued == slots && !mbar_wait(empty + 8 * slot, at.phase ^ 1, err, &sh->stop)) {
             ok = false;
             break;
           }
@@ -308,12 +351,16 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
           mbar_expect_tx(full + 8 * slot, bytes);
           bulk_load(smem_u32(ring + slot * Shape::chunk_bytes), base + (int64_t)v * 16, bytes,
                     full + 8 * slot);
+          at.next();
+          if (issued < slots) ++issued;
         }
       }
       // every copy issued has to land before the CTA may end
       const uint64_t deadline = global_ns() + kWaitNs;
-      for (uint32_t j = k > slots ? k - slots : 0; j < k; ++j)
-        if (!mbar_drain(full + 8 * (j % slots), (j / slots) & 1, deadline, err)) break;
+      if (issued < slots) at = Place<slots>();
+      else at.phase ^= 1;  // the oldest of the last `slots` chunks
+      for (; issued > 0; --issued, at.next())
+        if (!mbar_drain(full + 8 * at.slot, at.phase, deadline, err)) break;
     }
   } else {  // ---------------------------------------------------- consumers
     auto sync_consumers = [] {
@@ -344,7 +391,8 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
         if (all != 0.0) factor /= all;
       }
     }
-    uint32_t k = 0, done = 0;  // chunks taken; live rows done
+    Place<slots> at;
+    uint32_t done = 0;  // live rows
     bool ok = true;
     Token next = token_at(r, cluster);
     for (int64_t t = cluster; t < r.T_; t += clusters) {
@@ -381,18 +429,20 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
       // ---- maximum and sum
       float m = -INFINITY, sl = 0.f;
       F2 sum0 = f2(0.f, 0.f), sum1 = sum0;
-      const uint32_t k0 = k;
-      for (int32_t v = begin; v < end; v += Shape::chunk_vecs, ++k) {
-        const uint32_t slot = k % slots;
-        ok = mbar_wait(full + 8 * slot, (k / slots) & 1, err, &sh->stop) && ok;
+      const Place<slots> first = at;
+      for (int32_t v = begin; v < end; v += Shape::chunk_vecs, at.next()) {
+        ok = mbar_wait(full + 8 * at.slot, at.phase, err, &sh->stop) && ok;
         if (!ok) continue;
-        const uint4* q = reinterpret_cast<const uint4*>(ring + slot * Shape::chunk_bytes);
-        const int32_t n = end - v;
-        if (tid < n) {
-          const uint4 v0 = q[tid];
-          uint4 v1 = make_uint4(Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest);
-          if (tid + Shape::consumers < n) v1 = q[tid + Shape::consumers];
-          const float bm = largest<T>(v0, v1);
+        const uint4* q = reinterpret_cast<const uint4*>(ring + at.slot * Shape::chunk_bytes) + tid;
+        const int32_t n = end - v - tid;
+        if (n > 0) {
+          uint4 x4[Shape::per];
+#pragma unroll
+          for (int j = 0; j < Shape::per; ++j) {
+            x4[j] = make_uint4(Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest);
+            if (j == 0 || j * Shape::consumers < n) x4[j] = q[j * Shape::consumers];
+          }
+          const float bm = largest(x4, T());
           if (bm > m) {
             const float f = expf((m - bm) * r.inv_tf);
             sum0 = f2_mul(sum0, f2(f, f));
@@ -401,18 +451,20 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
           }
           const float z = -finite_max(m);
           const F2 nm = f2(z, z);
-          Pairs<T> p0, p1;
-          unpack(v0, p0);
-          unpack(v1, p1);
 #pragma unroll
-          for (int i = 0; i < VE / 2; ++i) {
-            sum0 = f2_add(sum0, exp_pair(p0.p[i], nm, c2));
-            sum1 = f2_add(sum1, exp_pair(p1.p[i], nm, c2));
+          for (int j = 0; j < Shape::per; ++j) {
+            Pairs<T> p;
+            unpack(x4[j], p);
+#pragma unroll
+            for (int i = 0; i < VE / 2; i += 2) {
+              sum0 = f2_add(sum0, exp_pair(p.p[i], nm, c2));
+              sum1 = f2_add(sum1, exp_pair(p.p[i + 1], nm, c2));
+            }
           }
         }
         if (!POLICY) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(empty + 8 * slot);
+          if (lane == 0) mbar_arrive(empty + 8 * at.slot);
         }
       }
       {
@@ -454,13 +506,14 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
           pol += (double)weight * (double)o.policy;
           kls += (double)weight * (double)o.kl;
           weight_sum += (double)weight;
-          if (lane == 0) sh->result = make_float4(ms.m, -coef / ms.s, coef, 0.f);
+          if (lane == 0) sh->result = make_float4(ms.m, -coef / ms.s, coef, xy);
         }
       }
       ++done;
       if (!POLICY) continue;
       sync_consumers();
       // ---- the gradient from the chunks still in shared memory
+      bool held = ok;
       const float4 res = sh->result;
       if (a.grad != nullptr) {
         T* g = a.grad + t * a.grad_ld;
@@ -471,39 +524,40 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
           const bool same = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
           const F2 nm = f2(-z, -z), b2 = f2(b, b);
           uint4* gv = reinterpret_cast<uint4*>(g + s.head);
-          const int32_t yv = y >= s.head ? (y - s.head) / VE : -1;  // the target's vector
-          uint32_t kk = k0;
-          for (int32_t v = begin; v < end && ok; v += Shape::chunk_vecs, ++kk) {
-            const unsigned char* chunk = ring + (kk % slots) * Shape::chunk_bytes;
-            const int32_t n = min(end - v, (int32_t)Shape::chunk_vecs);
+          Place<slots> from = first;
+          for (int32_t v = begin; v < end && ok; v += Shape::chunk_vecs, from.next()) {
+            const unsigned char* chunk = ring + from.slot * Shape::chunk_bytes;
             if (same) {
-              const uint4* q = reinterpret_cast<const uint4*>(chunk);
+              const uint4* q = reinterpret_cast<const uint4*>(chunk) + tid;
+              uint4* out = gv + v + tid;
+              const int32_t n = end - v - tid;
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int32_t i = tid + j * Shape::consumers;
-                if (i >= n) break;
+              for (int j = 0; j < Shape::per; ++j) {
+                if (j * Shape::consumers >= n) break;
                 Pairs<T> p;
-                unpack(q[i], p);
+                unpack(q[j * Shape::consumers], p);
                 float o[VE];
 #pragma unroll
                 for (int e = 0; e < VE / 2; ++e)
                   f2_get(f2_mul(exp_pair(p.p[e], nm, c2), b2), o[2 * e], o[2 * e + 1]);
-                if (v + i == yv) {
-#pragma unroll
-                  for (int e = 0; e < VE; ++e)
-                    if (s.head + yv * VE + e == y) o[e] += coef;
-                }
-                __stcs(gv + v + i, pack_vec<T>(o));
+                __stcs(out + j * Shape::consumers, pack_vec<T>(o));
               }
             } else {
               const T* q = reinterpret_cast<const T*>(chunk);
-              const int32_t first = s.head + v * VE;
-              for (int32_t i = tid; i < n * VE; i += Shape::consumers) {
-                const float e = b * exp_scaled(to_f(q[i]) - z, r.c);
-                g[first + i] = from_f<T>(first + i == y ? e + coef : e);
-              }
+              const int32_t n = min(end - v, (int32_t)Shape::chunk_vecs) * VE;
+              T* out = g + s.head + (int64_t)v * VE;
+              for (int32_t i = tid; i < n; i += Shape::consumers)
+                out[i] = from_f<T>(b * exp_scaled(to_f(q[i]) - z, r.c));
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + 8 * from.slot);
           }
+          held = false;
+          // the target's element again, by the thread that wrote it
+          const int32_t ye = y - s.head, yv = ye / VE;
+          if (ye >= 0 && yv >= begin && yv < end &&
+              tid == (same ? yv - begin : ye - begin * VE) % Shape::consumers)
+            g[y] = from_f<T>(b * exp_scaled(res.w - z, r.c) + coef);
           if (loose >= 0) {
             const float e = b * exp_scaled(xl - z, r.c);
             g[loose] = from_f<T>(loose == y ? e + coef : e);
@@ -511,8 +565,11 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
         }
       }
       __syncwarp();
-      if (lane == 0 && ok)
-        for (uint32_t j = k0; j < k; ++j) mbar_arrive(empty + 8 * (j % slots));
+      if (lane == 0 && held) {
+        Place<slots> from = first;
+        for (int32_t v = begin; v < end; v += Shape::chunk_vecs, from.next())
+          mbar_arrive(empty + 8 * from.slot);
+      }
     }
     if (POLICY && warp == 0 && rank == 0) {
       // the last cluster to finish adds up all of them in their order
