@@ -305,6 +305,12 @@ __global__ void __launch_bounds__(kRowThreads)
 }
 
 #include "mbarrier.cuh"
+#ifndef VSF_PIPE_W
+#define VSF_PIPE_W 16
+#endif
+#ifndef VSF_PIPE_PER
+#define VSF_PIPE_PER 4
+#endif
 #include "row_pipe.cuh"
 
 // ------------------------------------------------------------- host side
@@ -369,9 +375,6 @@ Rows<T> rows_of(const RowsArg& a) {
 
 unsigned row_grid(int64_t T_) { return (unsigned)std::min<int64_t>(T_, 152 * 4); }
 
-#ifndef VSF_PIPE_W
-#define VSF_PIPE_W 8
-#endif
 constexpr int kPipeWarps = VSF_PIPE_W;
 
 // Clusters of C CTAs of a kernel that fit on the current device at a time,
@@ -415,21 +418,27 @@ int pipe_clusters(int C, cudaError_t* e) {
   return n;
 }
 
-// CTAs that share a row. `hold`: the share stays in the ring until its
-// gradient is written, so it may fill at most two thirds of it (the rest reads
-// ahead); 0 if no cluster size does that. With few rows, more CTAs a row as
-// long as they all run at a time and each has a chunk's half to read.
+// CTAs that share a row (0: none that holds it), and whether two rows' shares
+// fit the ring. `hold`: a share stays in the ring until its gradient is
+// written. With few rows, more CTAs a row as long as they all run at a time and
+// each has 256 vectors to read.
+struct PipeSplit {
+  int C;
+  bool ahead;
+};
 template <typename T>
-int pipe_cluster_size(int64_t T_, int64_t V, bool hold) {
-  constexpr int64_t CV = PipeShape<kPipeWarps>::chunk_vecs;
+PipeSplit pipe_split(int64_t T_, int64_t V, bool hold) {
+  using Shape = PipeShape<kPipeWarps>;
   const int64_t nvec = V / Vec<T>::n;
-  int C = 1;
-  while (hold && (nvec / C + 1 + CV - 1) / CV > (int)PipeShape<kPipeWarps>::slots * 2 / 3) {
-    C *= 2;
-    if (C > 8) return 0;
+  auto chunks = [&](int C) { return (nvec / C + 1 + Shape::chunk_vecs - 1) / Shape::chunk_vecs; };
+  PipeSplit s = {1, true};
+  if (hold) {
+    while (s.C <= 8 && 2 * chunks(s.C) > Shape::slots) s.C *= 2;
+    if (s.C > 8) s = {chunks(8) <= Shape::slots ? 8 : 0, false};
+    if (s.C == 0) return s;
   }
-  while (C < 8 && T_ * C * 2 <= 152 * (16 / kPipeWarps) && nvec / (2 * C) >= 256) C *= 2;
-  return C;
+  while (s.C < 8 && T_ * s.C * 2 <= 152 * (16 / kPipeWarps) && nvec / (2 * s.C) >= 256) s.C *= 2;
+  return s;
 }
 
 template <typename T, bool POLICY>
@@ -462,7 +471,7 @@ cudaError_t launch_stats(const Rows<T>& r, float2* row, float* logp, WsHead* hea
   a.row = row;
   a.logp = logp;
   a.head = head;
-  return launch_pipe<T, false>(a, pipe_cluster_size<T>(r.T_, r.V, false), st);
+  return launch_pipe<T, false>(a, pipe_split<T>(r.T_, r.V, false).C, st);
 }
 
 template <typename T>
@@ -478,8 +487,8 @@ template <typename T>
 cudaError_t policy(const RowsArg& a, const PolicyIn& p, float* stats, float* logp, void* grad,
                    int64_t grad_ld, const ObjectiveWs& w, cudaStream_t st) {
   const Rows<T> r = rows_of<T>(a);
-  const int C = pipe_cluster_size<T>(r.T_, r.V, true);
-  if (C > 0) {
+  const PipeSplit split = pipe_split<T>(r.T_, r.V, true);
+  if (split.C > 0) {
     PipeArgs<T> k = {};
     k.r = r;
     k.p = p;
@@ -489,7 +498,8 @@ cudaError_t policy(const RowsArg& a, const PolicyIn& p, float* stats, float* log
     k.stats = stats;
     k.head = w.head;
     k.partial = w.partial;
-    return launch_pipe<T, true>(k, C, st);
+    k.ahead = split.ahead;
+    return launch_pipe<T, true>(k, split.C, st);
   }
   // a row too long for a cluster's shared memory: statistics, then gradient
   cudaError_t e = launch_stats(r, w.row, logp, w.head, st);

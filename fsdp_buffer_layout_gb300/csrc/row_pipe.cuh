@@ -4,21 +4,30 @@
 // objective.cu.
 //
 // A cluster of C CTAs takes a row, each CTA an equal share of its 16-byte
-// vectors. In a CTA the last warp streams the share into a ring of
-// shared-memory chunks with bulk copies; W consumer warps add up the terms
-// exp(x - m) of each chunk with a running maximum a thread. The threads' sums
-// are joined in the warp, in the CTA and, with 16-byte asynchronous stores
-// into every CTA of the cluster, over the row. The policy loss then reads the
-// share once more from shared memory, where the chunks have stayed, and writes
-// the gradient; only then do they go back to the producer. So logits cross the
-// memory bus once and gradients once.
+// vectors. A CTA has three kinds of warps:
+//   producer  finds the cluster's rows (live ones and masked ones are dealt
+//             out apart, so that every cluster gets as many), puts each into a
+//             queue, and streams its share into a ring of shared-memory chunks
+//             with bulk copies;
+//   consumers (W warps) add up the terms exp(x - m) of each chunk with a
+//             running maximum a thread and leave the warp's join to
+//   the joiner, which joins the warps and, with 16-byte asynchronous stores
+//             into every CTA of the cluster, the row, and computes what hangs
+//             on it: the log probability, the policy's terms, the gradient's
+//             coefficient.
+// For the gradient the consumers read a row's share once more from shared
+// memory, where the chunks have stayed, so logits cross the memory bus once and
+// gradients once. They do so after the NEXT row's sums (`ahead`), so that
+// nobody waits for the joiner: the ring then holds two rows' shares. No barrier
+// spans the consumers; they meet the other warps at mbarriers alone.
 //
 // Elements in front of a row's first 16-byte boundary and behind its last one
 // are read by single threads. A gradient row whose address differs from the
 // logits' modulo 16 bytes is written element by element.
 //
-// Every wait is bounded (mbarrier.cuh): after a timeout the CTA still passes
-// its barriers and sends its messages, but skips the arithmetic.
+// Every wait is bounded (mbarrier.cuh). After a timeout all waits of the CTA
+// return at once and its warps leave their loops; the cluster then meets at
+// its end as always, and waits a moment for messages still on their way.
 
 // 16 bytes of a row as floats in pairs.
 template <typename T>
@@ -195,41 +204,53 @@ __device__ __forceinline__ uint4 pack_vec<float>(const float (&o)[4]) {
 }
 
 constexpr int kMaxPipeCluster = 16;
+constexpr uint32_t kQueue = 8;  // rows handed on and not yet added up
 
 // One shape of the kernel: W consumer warps, each thread `per` vectors of a
-// chunk, and a ring of 96 KB a CTA at W = 8, two CTAs an SM.
+// chunk, and a ring of 208 KB for the CTAs of an SM together.
 template <int W>
 struct PipeShape {
-  static constexpr int per = 4;
+  static constexpr int per = VSF_PIPE_PER;
   static constexpr int consumers = W * 32;
-  static constexpr int threads = consumers + 32;
+  static constexpr int threads = consumers + 64;
   static constexpr int chunk_vecs = per * consumers;
   static constexpr uint32_t chunk_bytes = chunk_vecs * 16;
-  static constexpr uint32_t slots = (W * 12u * 1024u) / chunk_bytes;
+  static constexpr uint32_t slots = (W * 13u * 1024u) / chunk_bytes;
+  // full and empty of each slot; full, empty and parts ready of each queue
+  // place; result ready, two; messages, two
+  static constexpr uint32_t barriers = 2 * slots + 3 * kQueue + 4;
 };
 // A place in the ring: slot and how often the ring has gone round, modulo 2.
-template <uint32_t SLOTS>
+template <uint32_t N>
 struct Place {
   uint32_t slot = 0, phase = 0;
   __device__ __forceinline__ void next() {
-    if (++slot == SLOTS) {
+    if (++slot == N) {
       slot = 0;
       phase ^= 1;
     }
   }
 };
 
+// A row as the producer hands it on.
+struct RowItem {
+  int64_t t;  // -1: no more rows
+  int32_t y;  // -1: masked
+  float w;
+};
 struct PipeTail {  // shared memory behind the ring and its barriers
   float4 message[2][kMaxPipeCluster];
-  MaxSum part[2][16];
+  float4 result[2];  // m, b = -a / s, a, x_y
+  RowItem item[kQueue];
+  MaxSum part[kQueue][16];
   double sum[16];
-  float4 result;  // m, b = -a / s, a, x_y
-  uint32_t stop, xstop;
+  uint32_t stop;
 };
 
 template <int W>
 constexpr uint32_t pipe_smem() {
-  return PipeShape<W>::slots * (PipeShape<W>::chunk_bytes + 16) + 16 + (uint32_t)sizeof(PipeTail) + 128;
+  return PipeShape<W>::slots * PipeShape<W>::chunk_bytes + 8 * PipeShape<W>::barriers +
+         (uint32_t)sizeof(PipeTail) + 128;
 }
 
 template <typename T>
@@ -243,6 +264,7 @@ struct PipeArgs {
   float* stats;  // policy: fp32[4]
   WsHead* head;
   double* partial;  // policy: {policy, kl, weight} sums of each cluster
+  int32_t ahead;    // the ring holds two rows' shares
 };
 
 // Where a row's vectors lie: `head` elements, then nvec vectors, then a tail.
@@ -294,67 +316,133 @@ __device__ __forceinline__ void zero_share(T* g, int32_t V, uint32_t rank, uint3
   if (rank + 1 == count && tail + tid < V) g[tail + tid] = from_f<T>(0.f);
 }
 
+// The waits of a whole warp: all of its lanes go on, or none does.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned* err,
+                                          volatile uint32_t* stop) {
+  return __all_sync(~0u, mbar_wait(bar, parity, err, stop));
+}
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, unsigned* err,
+                                                  volatile uint32_t* stop) {
+  return __all_sync(~0u, mbar_wait_cluster(bar, parity, err, stop));
+}
+
+// A row whose gradient is still to be written.
+template <uint32_t SLOTS>
+struct Pending {
+  int64_t t;
+  int32_t y, loose;
+  float xl;  // the loose element
+  Place<SLOTS> first;
+};
+
 template <typename T, int W, bool POLICY>
 __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
     row_pipe_kernel(const __grid_constant__ PipeArgs<T> a) {
   using Shape = PipeShape<W>;
   constexpr int VE = Vec<T>::n;
+  constexpr uint32_t slots = Shape::slots;
   extern __shared__ unsigned char raw[];
   unsigned char* ring =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~(uintptr_t)127);
-  constexpr uint32_t slots = Shape::slots;
   uint64_t* bars = reinterpret_cast<uint64_t*>(ring + slots * Shape::chunk_bytes);
-  PipeTail* sh = reinterpret_cast<PipeTail*>(bars + 2 * slots + 2);
-  const uint32_t full = smem_u32(bars), empty = smem_u32(bars + slots);
-  const uint32_t xbar = smem_u32(bars + 2 * slots);
+  PipeTail* sh = reinterpret_cast<PipeTail*>(bars + Shape::barriers);
+  const uint32_t full = smem_u32(bars), empty = full + 8 * slots;
+  const uint32_t qfull = empty + 8 * slots, qempty = qfull + 8 * kQueue;
+  const uint32_t pbar = qempty + 8 * kQueue, rbar = pbar + 8 * kQueue, xbar = rbar + 16;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t C = cta_count(), rank = C > 1 ? cta_rank() : 0;
   const int64_t cluster = blockIdx.x / C, clusters = gridDim.x / C;
   const Rows<T>& r = a.r;
   unsigned* err = &a.head->err;
+  volatile uint32_t* stop = &sh->stop;
 
   if (tid == 0) {
     for (uint32_t s = 0; s < slots; ++s) {
       mbar_init(full + 8 * s, 1);
       mbar_init(empty + 8 * s, W);
     }
-    mbar_init(xbar, 1);
-    mbar_init(xbar + 8, 1);
-    sh->stop = sh->xstop = 0;
+    for (uint32_t s = 0; s < kQueue; ++s) {
+      mbar_init(qfull + 8 * s, 1);
+      mbar_init(qempty + 8 * s, W + 1);
+      mbar_init(pbar + 8 * s, W);
+    }
+    for (uint32_t s = 0; s < 2; ++s) {
+      mbar_init(rbar + 8 * s, 1);
+      mbar_init(xbar + 8 * s, 1);
+    }
+    sh->stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   __syncthreads();
   if (C > 1) cluster_sync();
 
-  if (warp == W) {  // ------------------------------------------- producer
-    if (lane == 0) {
-      uint32_t issued = 0;  // chunks, counted up to the ring's length
-      Place<slots> at;
-      bool ok = true;
-      Token next = token_at(r, cluster);
-      for (int64_t t = cluster; t < r.T_ && ok; t += clusters) {
-        const int32_t y = live_target(r, next, nullptr);
-        next = token_at(r, t + clusters);
-        if (y < 0) continue;
-        const T* x = r.x + t * r.ld;
-        const Span s = span_of(x, r.V);
-        const char* base = reinterpret_cast<const char*>(x + s.head);
-        const int32_t end = share(s.nvec, rank + 1, C);
-        for (int32_t v = share(s.nvec, rank, C); v < end; v += Shape::chunk_vecs) {
-          const uint32_t slot = at.slot;
-          if (issued == slots && !mbar_wait(empty + 8 * slot, at.phase ^ 1, err, &sh->stop)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bytes = (uint32_t)min(end - v, (int32_t)Shape::chunk_vecs) * 16;
-          mbar_expect_tx(full + 8 * slot, bytes);
-          bulk_load(smem_u32(ring + slot * Shape::chunk_bytes), base + (int64_t)v * 16, bytes,
-                    full + 8 * slot);
-          at.next();
-          if (issued < slots) ++issued;
-        }
+  if (warp == W) {  // -------------------------------------------- producer
+    Place<slots> at;
+    Place<kQueue> q;
+    uint32_t issued = 0, queued = 0;  // counted up to the ring's and the queue's length
+    // hands a row on; lane 0 alone
+    auto push = [&](int64_t t, int32_t y, float w) -> bool {
+      if (queued == kQueue && !mbar_wait(qempty + 8 * q.slot, q.phase ^ 1, err, stop)) return false;
+      sh->item[q.slot] = {t, y, w};
+      mbar_arrive(qfull + 8 * q.slot);
+      q.next();
+      if (queued < kQueue) ++queued;
+      return true;
+    };
+    auto stream = [&](int64_t t) -> bool {
+      const T* x = r.x + t * r.ld;
+      const Span s = span_of(x, r.V);
+      const char* base = reinterpret_cast<const char*>(x + s.head);
+      const int32_t end = share(s.nvec, rank + 1, C);
+      for (int32_t v = share(s.nvec, rank, C); v < end; v += Shape::chunk_vecs) {
+        if (issued == slots && !mbar_wait(empty + 8 * at.slot, at.phase ^ 1, err, stop)) return false;
+        const uint32_t bytes = (uint32_t)min(end - v, (int32_t)Shape::chunk_vecs) * 16;
+        mbar_expect_tx(full + 8 * at.slot, bytes);
+        bulk_load(smem_u32(ring + at.slot * Shape::chunk_bytes), base + (int64_t)v * 16, bytes,
+                  full + 8 * at.slot);
+        at.next();
+        if (issued < slots) ++issued;
       }
+      return true;
+    };
+    int64_t lives = 0, deads = 0;  // tokens seen of each kind
+    int64_t my_live = cluster, my_dead = cluster;
+    bool ok = true;
+    Token next = token_at(r, (int64_t)lane);
+    for (int64_t t0 = 0; t0 < r.T_ && ok; t0 += 32) {
+      const Token k = next;
+      next = token_at(r, t0 + 32 + lane);
+      const bool owner = rank == 0 && (uint32_t)(t0 >> 5) % (uint32_t)clusters == (uint32_t)cluster;
+      const int32_t y = live_target(r, k, owner ? err : nullptr);
+      const uint32_t live = __ballot_sync(~0u, y >= 0);
+      const uint32_t dead = __ballot_sync(~0u, y < 0 && t0 + lane < r.T_);
+      const uint32_t below = (1u << lane) - 1;
+      if (owner && y < 0 && t0 + lane < r.T_ && a.logp != nullptr) a.logp[t0 + lane] = 0.f;
+      while (ok && my_live < lives + __popc(live)) {
+        const uint32_t hit =
+            __ballot_sync(~0u, y >= 0 && lives + __popc(live & below) == my_live);
+        const int who = __ffs(hit) - 1;
+        const int32_t yy = __shfl_sync(~0u, y, who);
+        const float ww = __shfl_sync(~0u, k.w, who);
+        if (lane == 0) ok = push(t0 + who, yy, ww) && stream(t0 + who);
+        ok = __shfl_sync(~0u, (int)ok, 0) != 0;
+        my_live += clusters;
+      }
+      lives += __popc(live);
+      if (POLICY) {
+        while (ok && my_dead < deads + __popc(dead)) {
+          const uint32_t hit = __ballot_sync(~0u, (dead >> lane & 1) &&
+                                                      deads + __popc(dead & below) == my_dead);
+          if (lane == 0) ok = push(t0 + __ffs(hit) - 1, -1, 0.f);
+          ok = __shfl_sync(~0u, (int)ok, 0) != 0;
+          my_dead += clusters;
+        }
+        deads += __popc(dead);
+      }
+    }
+    if (lane == 0) {
+      if (ok) push(-1, -1, 0.f);
       // every copy issued has to land before the CTA may end
       const uint64_t deadline = global_ns() + kWaitNs;
       if (issued < slots) at = Place<slots>();
@@ -362,127 +450,61 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
       for (; issued > 0; --issued, at.next())
         if (!mbar_drain(full + 8 * at.slot, at.phase, deadline, err)) break;
     }
-  } else {  // ---------------------------------------------------- consumers
-    auto sync_consumers = [] {
-      asm volatile("bar.sync 1, %0;" ::"r"(Shape::consumers) : "memory");
-    };
-    const PairScale c2 = {f2(r.c.hi, r.c.hi), f2(r.c.lo, r.c.lo)};
-    double factor = 0.0, weight_sum = 0.0, pol = 0.0, kls = 0.0;
-    if (POLICY) {
-      // The sum of the live weights scales every gradient: each CTA adds it up
-      // for itself, in the same order, while its first row is on its way.
-      factor = (double)a.p.scale;
-      if (a.p.mean) {
+  } else {
+    // The sum of the live weights scales every gradient: each CTA adds it up
+    // for itself, in the same order, while its first rows are on their way.
+    if (POLICY && a.p.mean) {
+      if (warp < W) {
         float w4[4] = {0.f, 0.f, 0.f, 0.f};
         for (int64_t t = tid; t < r.T_; t += 4 * Shape::consumers)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int64_t u = t + j * Shape::consumers;
             if (u < r.T_) {
-              const int64_t y = r.target[u];
-              if (y >= 0 && y < r.V) w4[j] += r.weight != nullptr ? r.weight[u] : 1.f;
+              const Token k = token_at(r, u);
+              if (k.y >= 0 && k.y < r.V) w4[j] += k.w;
             }
           }
         const double n = warp_sum(((double)w4[0] + w4[1]) + ((double)w4[2] + w4[3]));
         if (lane == 0) sh->sum[warp] = n;
-        sync_consumers();
-        double all = 0.0;
-        for (int w = 0; w < W; ++w) all += sh->sum[w];
-        if (all != 0.0) factor /= all;
+        asm volatile("bar.arrive 1, %0;" ::"r"(Shape::consumers + 32) : "memory");
+      } else {
+        asm volatile("bar.sync 1, %0;" ::"r"(Shape::consumers + 32) : "memory");
       }
     }
-    Place<slots> at;
-    uint32_t done = 0;  // live rows
-    bool ok = true;
-    Token next = token_at(r, cluster);
-    for (int64_t t = cluster; t < r.T_; t += clusters) {
-      const int32_t y = live_target(r, next, tid == 0 ? err : nullptr);
-      const float weight = next.w;
-      next = token_at(r, t + clusters);
-      if (y < 0) {
-        if (POLICY && a.grad != nullptr)
-          zero_share(a.grad + t * a.grad_ld, r.V, rank, C, tid, Shape::consumers);
-        if (tid == 0 && rank == 0 && a.logp != nullptr) a.logp[t] = 0.f;
-        continue;
+    Place<kQueue> q;
+    if (warp == W + 1) {  // ------------------------------------------ joiner
+      double factor = 0.0, weight_sum = 0.0, pol = 0.0, kls = 0.0;
+      if (POLICY) {
+        factor = (double)a.p.scale;
+        if (a.p.mean) {
+          double all = 0.0;
+          for (int w = 0; w < W; ++w) all += sh->sum[w];
+          if (all != 0.0) factor /= all;
+        }
       }
-      const T* x = r.x + t * r.ld;
-      // the scalars of the token, on their way while the row is added up
-      float xy = 0.f, old = 0.f, ref = 0.f, adv = 0.f;
-      if (warp == 0) {
-        xy = to_f(x[y]);
+      for (uint32_t done = 0;; q.next()) {
+        if (!warp_wait(qfull + 8 * q.slot, q.phase, err, stop)) break;
+        const RowItem it = sh->item[q.slot];
+        if (it.t < 0) break;
+        if (it.y < 0) {
+          if (!warp_wait(pbar + 8 * q.slot, q.phase, err, stop)) break;
+          if (lane == 0) mbar_arrive(qempty + 8 * q.slot);
+          continue;
+        }
+        const float xy = to_f(r.x[it.t * r.ld + it.y]);
+        float old = 0.f, ref = 0.f, adv = 0.f;
         if (POLICY) {
-          old = a.p.old_logp[t];
-          adv = a.p.adv[t];
-          if (a.p.beta != 0.f) ref = a.p.ref_logp[t];
+          old = a.p.old_logp[it.t];
+          adv = a.p.adv[it.t];
+          if (a.p.beta != 0.f) ref = a.p.ref_logp[it.t];
         }
-      }
-      const Span s = span_of(x, r.V);
-      const int32_t begin = share(s.nvec, rank, C), end = share(s.nvec, rank + 1, C);
-      // the loose element of this thread, if any
-      int32_t loose = -1;
-      if (rank == 0 && tid < s.head) loose = tid;
-      if (rank + 1 == C && tid >= 16 && s.head + s.nvec * VE + tid - 16 < r.V)
-        loose = s.head + s.nvec * VE + tid - 16;
-      float xl = -INFINITY;
-      if (loose >= 0) xl = to_f(x[loose]);
-
-      // ---- maximum and sum
-      float m = -INFINITY, sl = 0.f;
-      F2 sum0 = f2(0.f, 0.f), sum1 = sum0;
-      const Place<slots> first = at;
-      for (int32_t v = begin; v < end; v += Shape::chunk_vecs, at.next()) {
-        ok = mbar_wait(full + 8 * at.slot, at.phase, err, &sh->stop) && ok;
-        if (!ok) continue;
-        const uint4* q = reinterpret_cast<const uint4*>(ring + at.slot * Shape::chunk_bytes) + tid;
-        const int32_t n = end - v - tid;
-        if (n > 0) {
-          uint4 x4[Shape::per];
-#pragma unroll
-          for (int j = 0; j < Shape::per; ++j) {
-            x4[j] = make_uint4(Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest);
-            if (j == 0 || j * Shape::consumers < n) x4[j] = q[j * Shape::consumers];
-          }
-          const float bm = largest(x4, T());
-          if (bm > m) {
-            const float f = expf((m - bm) * r.inv_tf);
-            sum0 = f2_mul(sum0, f2(f, f));
-            sum1 = f2_mul(sum1, f2(f, f));
-            m = bm;
-          }
-          const float z = -finite_max(m);
-          const F2 nm = f2(z, z);
-#pragma unroll
-          for (int j = 0; j < Shape::per; ++j) {
-            Pairs<T> p;
-            unpack(x4[j], p);
-#pragma unroll
-            for (int i = 0; i < VE / 2; i += 2) {
-              sum0 = f2_add(sum0, exp_pair(p.p[i], nm, c2));
-              sum1 = f2_add(sum1, exp_pair(p.p[i + 1], nm, c2));
-            }
-          }
-        }
-        if (!POLICY) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(empty + 8 * at.slot);
-        }
-      }
-      {
-        float s0, s1, s2, s3;
-        f2_get(sum0, s0, s1);
-        f2_get(sum1, s2, s3);
-        sl = (s0 + s1) + (s2 + s3);
-      }
-      MaxSum ms = {m, sl};
-      if (loose >= 0) ms = join(ms, {xl, xl == -INFINITY ? 0.f : 1.f}, r.inv_tf);
-      if (xl != xl) ms.s = xl;
-      // ---- joined over the warp, the CTA and the cluster
-      const uint32_t par = done & 1;
-      ms = warp_join(ms, r.inv_tf);
-      if (lane == 0) sh->part[par][warp] = ms;
-      sync_consumers();
-      if (warp == 0) {
-        ms = lane < W ? sh->part[par][lane] : MaxSum{-INFINITY, 0.f};
+        const uint32_t par = done & 1, phase = (done >> 1) & 1;
+        ++done;
+        if (!warp_wait(pbar + 8 * q.slot, q.phase, err, stop)) break;
+        MaxSum ms = lane < W ? sh->part[q.slot][lane] : MaxSum{-INFINITY, 0.f};
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qempty + 8 * q.slot);
         ms = warp_join(ms, r.inv_tf);
         if (C > 1) {
           const uint32_t bar = xbar + 8 * par;
@@ -491,115 +513,222 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
           // xy goes with the message, so that it has been read before any
           // CTA of the cluster may write the gradient over the logits
           if (lane < C) put_async(smem_u32(&sh->message[par][rank]), bar, lane, ms.m, ms.s, xy);
-          mbar_wait_cluster(bar, (done >> 1) & 1, err, &sh->xstop);
+          if (!warp_wait_cluster(bar, phase, err, stop)) break;
           const float4 got = sh->message[par][lane < C ? lane : 0];
           ms = warp_join(lane < C ? MaxSum{got.x, got.y} : MaxSum{-INFINITY, 0.f}, r.inv_tf);
         }
         const double lp = log_prob(xy - ms.m, ms.s, r.inv_t);
-        if (lane == 0 && rank == 0) {
-          if (a.row != nullptr) a.row[t] = make_float2(ms.m, ms.s);
-          if (a.logp != nullptr) a.logp[t] = (float)lp;
-        }
         if (POLICY) {
           const PolicyTerm o = policy_term(a.p, lp, old, ref, adv);
-          const float coef = (float)(factor * (double)weight * r.inv_t * (double)o.slope);
-          pol += (double)weight * (double)o.policy;
-          kls += (double)weight * (double)o.kl;
-          weight_sum += (double)weight;
-          if (lane == 0) sh->result = make_float4(ms.m, -coef / ms.s, coef, xy);
+          const float coef = (float)(factor * (double)it.w * r.inv_t * (double)o.slope);
+          if (lane == 0) {
+            sh->result[par] = make_float4(ms.m, -coef / ms.s, coef, xy);
+            mbar_arrive(rbar + 8 * par);
+          }
+          pol += (double)it.w * (double)o.policy;
+          kls += (double)it.w * (double)o.kl;
+          weight_sum += (double)it.w;
+        }
+        if (lane == 0 && rank == 0) {
+          if (a.row != nullptr) a.row[it.t] = make_float2(ms.m, ms.s);
+          if (a.logp != nullptr) a.logp[it.t] = (float)lp;
         }
       }
-      ++done;
-      if (!POLICY) continue;
-      sync_consumers();
-      // ---- the gradient from the chunks still in shared memory
-      bool held = ok;
-      const float4 res = sh->result;
-      if (a.grad != nullptr) {
-        T* g = a.grad + t * a.grad_ld;
+      if (POLICY && rank == 0) {
+        // the last cluster to finish adds up all of them in their order
+        uint32_t last = 0;
+        if (lane == 0) {
+          double* p = a.partial + 3 * cluster;
+          p[0] = pol;
+          p[1] = kls;
+          p[2] = weight_sum;
+          __threadfence();
+          last = atomicAdd(&a.head->ticket, 1u) + 1 == (uint32_t)clusters;
+          __threadfence();
+        }
+        if (__shfl_sync(~0u, last, 0)) {
+          double v[3] = {0.0, 0.0, 0.0};
+          for (int64_t c = lane; c < clusters; c += 32)
+            for (int j = 0; j < 3; ++j) v[j] += __ldcg(a.partial + 3 * c + j);
+          for (int j = 0; j < 3; ++j) v[j] = warp_sum(v[j]);
+          if (lane == 0) {
+            const double f = (double)a.p.scale / (a.p.mean && v[2] != 0.0 ? v[2] : 1.0);
+            a.stats[0] = (float)(f * (v[0] + (a.p.beta != 0.f ? (double)a.p.beta * v[1] : 0.0)));
+            a.stats[1] = (float)(f * v[0]);
+            a.stats[2] = (float)(f * v[1]);
+            a.stats[3] = (float)v[2];
+            a.head->ticket = 0;
+          }
+        }
+      }
+    } else {  // ---------------------------------------------------- consumers
+      const PairScale c2 = {f2(r.c.hi, r.c.hi), f2(r.c.lo, r.c.lo)};
+      Place<slots> at;
+      uint32_t written = 0;  // live rows whose gradient has been written
+      // The gradient of a row from the chunks still in shared memory.
+      auto write_grad = [&](const Pending<slots>& p) -> bool {
+        const uint32_t par = written & 1, phase = (written >> 1) & 1;
+        ++written;
+        if (!warp_wait(rbar + 8 * par, phase, err, stop)) return false;
+        const float4 res = sh->result[par];
+        const T* x = r.x + p.t * r.ld;
+        const Span s = span_of(x, r.V);
+        const int32_t begin = share(s.nvec, rank, C), end = share(s.nvec, rank + 1, C);
         const float z = finite_max(res.x), b = res.y, coef = res.z;
+        T* g = a.grad + p.t * a.grad_ld;
+        const bool same = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
+        const F2 nm = f2(-z, -z), b2 = f2(b, b);
+        uint4* gv = reinterpret_cast<uint4*>(g + s.head);
+        Place<slots> from = p.first;
+        for (int32_t v = begin; v < end; v += Shape::chunk_vecs, from.next()) {
+          const unsigned char* chunk = ring + from.slot * Shape::chunk_bytes;
+          if (a.grad == nullptr || coef == 0.f) {
+          } else if (same) {
+            const uint4* c = reinterpret_cast<const uint4*>(chunk) + tid;
+            uint4* out = gv + v + tid;
+            const int32_t n = end - v - tid;
+#pragma unroll
+            for (int j = 0; j < Shape::per; ++j) {
+              if (j * Shape::consumers >= n) break;
+              Pairs<T> e;
+              unpack(c[j * Shape::consumers], e);
+              float o[VE];
+#pragma unroll
+              for (int i = 0; i < VE / 2; ++i)
+                f2_get(f2_mul(exp_pair(e.p[i], nm, c2), b2), o[2 * i], o[2 * i + 1]);
+              __stcs(out + j * Shape::consumers, pack_vec<T>(o));
+            }
+          } else {
+            const T* c = reinterpret_cast<const T*>(chunk);
+            const int32_t n = min(end - v, (int32_t)Shape::chunk_vecs) * VE;
+            T* out = g + s.head + (int64_t)v * VE;
+            for (int32_t i = tid; i < n; i += Shape::consumers)
+              out[i] = from_f<T>(b * exp_scaled(to_f(c[i]) - z, r.c));
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty + 8 * from.slot);
+        }
+        if (a.grad == nullptr) return true;
         if (coef == 0.f) {
           zero_share(g, r.V, rank, C, tid, Shape::consumers);
-        } else {
-          const bool same = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
-          const F2 nm = f2(-z, -z), b2 = f2(b, b);
-          uint4* gv = reinterpret_cast<uint4*>(g + s.head);
-          Place<slots> from = first;
-          for (int32_t v = begin; v < end && ok; v += Shape::chunk_vecs, from.next()) {
-            const unsigned char* chunk = ring + from.slot * Shape::chunk_bytes;
-            if (same) {
-              const uint4* q = reinterpret_cast<const uint4*>(chunk) + tid;
-              uint4* out = gv + v + tid;
-              const int32_t n = end - v - tid;
+          return true;
+        }
+        if (p.loose >= 0) {
+          const float e = b * exp_scaled(p.xl - z, r.c);
+          g[p.loose] = from_f<T>(p.loose == p.y ? e + coef : e);
+        }
+        // the target's element again, by the thread that wrote it
+        const int32_t ye = p.y - s.head, yv = ye / VE;
+        if (ye >= 0 && yv >= begin && yv < end &&
+            tid == (same ? yv - begin : ye - begin * VE) % Shape::consumers)
+          g[p.y] = from_f<T>(b * exp_scaled(res.w - z, r.c) + coef);
+        return true;
+      };
+      Pending<slots> prev = {};
+      prev.t = -1;
+      bool ok = true;
+      for (; ok; q.next()) {
+        if (!warp_wait(qfull + 8 * q.slot, q.phase, err, stop)) {
+          ok = false;
+          break;
+        }
+        const RowItem it = sh->item[q.slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qempty + 8 * q.slot);
+        if (it.t < 0) break;
+        if (it.y < 0) {
+          if (lane == 0) mbar_arrive(pbar + 8 * q.slot);
+          if (a.grad != nullptr)
+            zero_share(a.grad + it.t * a.grad_ld, r.V, rank, C, tid, Shape::consumers);
+          continue;
+        }
+        Pending<slots> row;
+        row.t = it.t;
+        row.y = it.y;
+        row.first = at;
+        const T* x = r.x + it.t * r.ld;
+        const Span s = span_of(x, r.V);
+        const int32_t begin = share(s.nvec, rank, C), end = share(s.nvec, rank + 1, C);
+        row.loose = -1;
+        if (rank == 0 && tid < s.head) row.loose = tid;
+        if (rank + 1 == C && tid >= 16 && s.head + s.nvec * VE + tid - 16 < r.V)
+          row.loose = s.head + s.nvec * VE + tid - 16;
+        row.xl = -INFINITY;
+        if (row.loose >= 0) row.xl = to_f(x[row.loose]);
+
+        // ---- maximum and sum
+        float m = -INFINITY;
+        F2 sum0 = f2(0.f, 0.f), sum1 = sum0;
+        for (int32_t v = begin; v < end; v += Shape::chunk_vecs, at.next()) {
+          if (!warp_wait(full + 8 * at.slot, at.phase, err, stop)) {
+            ok = false;
+            break;
+          }
+          const uint4* c = reinterpret_cast<const uint4*>(ring + at.slot * Shape::chunk_bytes) + tid;
+          const int32_t n = end - v - tid;
+          if (n > 0) {
+            uint4 x4[Shape::per];
 #pragma unroll
-              for (int j = 0; j < Shape::per; ++j) {
-                if (j * Shape::consumers >= n) break;
-                Pairs<T> p;
-                unpack(q[j * Shape::consumers], p);
-                float o[VE];
-#pragma unroll
-                for (int e = 0; e < VE / 2; ++e)
-                  f2_get(f2_mul(exp_pair(p.p[e], nm, c2), b2), o[2 * e], o[2 * e + 1]);
-                __stcs(out + j * Shape::consumers, pack_vec<T>(o));
-              }
-            } else {
-              const T* q = reinterpret_cast<const T*>(chunk);
-              const int32_t n = min(end - v, (int32_t)Shape::chunk_vecs) * VE;
-              T* out = g + s.head + (int64_t)v * VE;
-              for (int32_t i = tid; i < n; i += Shape::consumers)
-                out[i] = from_f<T>(b * exp_scaled(to_f(q[i]) - z, r.c));
+            for (int j = 0; j < Shape::per; ++j) {
+              x4[j] = make_uint4(Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest);
+              if (j == 0 || j * Shape::consumers < n) x4[j] = c[j * Shape::consumers];
             }
+            const float bm = largest(x4, T());
+            if (bm > m) {
+              const float f = expf((m - bm) * r.inv_tf);
+              sum0 = f2_mul(sum0, f2(f, f));
+              sum1 = f2_mul(sum1, f2(f, f));
+              m = bm;
+            }
+            const float z = -finite_max(m);
+            const F2 nm = f2(z, z);
+#pragma unroll
+            for (int j = 0; j < Shape::per; ++j) {
+              Pairs<T> p;
+              unpack(x4[j], p);
+#pragma unroll
+              for (int i = 0; i < VE / 2; i += 2) {
+                sum0 = f2_add(sum0, exp_pair(p.p[i], nm, c2));
+                sum1 = f2_add(sum1, exp_pair(p.p[i + 1], nm, c2));
+              }
+            }
+          }
+          if (!POLICY) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(empty + 8 * from.slot);
-          }
-          held = false;
-          // the target's element again, by the thread that wrote it
-          const int32_t ye = y - s.head, yv = ye / VE;
-          if (ye >= 0 && yv >= begin && yv < end &&
-              tid == (same ? yv - begin : ye - begin * VE) % Shape::consumers)
-            g[y] = from_f<T>(b * exp_scaled(res.w - z, r.c) + coef);
-          if (loose >= 0) {
-            const float e = b * exp_scaled(xl - z, r.c);
-            g[loose] = from_f<T>(loose == y ? e + coef : e);
+            if (lane == 0) mbar_arrive(empty + 8 * at.slot);
           }
         }
-      }
-      __syncwarp();
-      if (lane == 0 && held) {
-        Place<slots> from = first;
-        for (int32_t v = begin; v < end; v += Shape::chunk_vecs, from.next())
-          mbar_arrive(empty + 8 * from.slot);
-      }
-    }
-    if (POLICY && warp == 0 && rank == 0) {
-      // the last cluster to finish adds up all of them in their order
-      uint32_t last = 0;
-      if (lane == 0) {
-        double* p = a.partial + 3 * cluster;
-        p[0] = pol;
-        p[1] = kls;
-        p[2] = weight_sum;
-        __threadfence();
-        last = atomicAdd(&a.head->ticket, 1u) + 1 == (uint32_t)clusters;
-        __threadfence();
-      }
-      if (__shfl_sync(~0u, last, 0)) {
-        double v[3] = {0.0, 0.0, 0.0};
-        for (int64_t q = lane; q < clusters; q += 32)
-          for (int j = 0; j < 3; ++j) v[j] += __ldcg(a.partial + 3 * q + j);
-        for (int j = 0; j < 3; ++j) v[j] = warp_sum(v[j]);
+        if (!ok) break;
+        float s0, s1, s2, s3;
+        f2_get(sum0, s0, s1);
+        f2_get(sum1, s2, s3);
+        MaxSum ms = {m, (s0 + s1) + (s2 + s3)};
+        if (row.loose >= 0) ms = join(ms, {row.xl, row.xl == -INFINITY ? 0.f : 1.f}, r.inv_tf);
+        ms = warp_join(ms, r.inv_tf);
         if (lane == 0) {
-          const double f = (double)a.p.scale / (a.p.mean && v[2] != 0.0 ? v[2] : 1.0);
-          a.stats[0] = (float)(f * (v[0] + (a.p.beta != 0.f ? (double)a.p.beta * v[1] : 0.0)));
-          a.stats[1] = (float)(f * v[0]);
-          a.stats[2] = (float)(f * v[1]);
-          a.stats[3] = (float)v[2];
-          a.head->ticket = 0;
+          sh->part[q.slot][warp] = ms;
+          mbar_arrive(pbar + 8 * q.slot);
+        }
+        if (POLICY) {
+          if (!a.ahead) {
+            ok = write_grad(row);
+          } else {
+            if (prev.t >= 0) ok = write_grad(prev);
+            prev = row;
+          }
         }
       }
+      if (POLICY && a.ahead && ok && prev.t >= 0) write_grad(prev);
     }
   }
   __syncwarp();
   // no CTA leaves while another of its cluster may still write to it
-  if (C > 1) cluster_sync();
+  if (C > 1) {
+    cluster_sync();
+    if (*stop != 0u) {
+      const uint64_t t0 = global_ns();
+      while (global_ns() - t0 < 100000ull) {
+      }
+    }
+  }
 }
