@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <string>
@@ -51,18 +52,23 @@ __device__ __forceinline__ float ex2(float t) {
   return r;
 }
 
-// The factor log2(e) / temperature as a sum of two positive floats. One
-// float's rounding error would act like a slightly different temperature, the
-// same way for every token, and add up over a sequence's log ratios. Both are
-// positive, so that -inf times either is -inf.
+// The factor c = log2(e) / temperature. One float's rounding error would act
+// like a slightly different temperature, the same way for every token, and add
+// up over a sequence's log ratios. So either as a sum of two floats, hi + lo
+// (both positive: -inf times either is -inf), or, where one product an element
+// has to do, rounded down (hi) in some threads and up in the others, in such a
+// share (ups / 2^32) that the mean is c.
 struct Log2Scale {
-  float hi, lo;
+  float hi, lo, up;
+  uint32_t ups;
 };
 inline Log2Scale log2_scale(float inv_t) {
   const double c = (double)inv_t * 1.4426950408889634074;
   float hi = (float)c;
   if ((double)hi >= c) hi = std::nextafter(hi, 0.f);
-  return {hi, (float)(c - (double)hi)};
+  const float up = std::nextafter(hi, INFINITY);
+  const double part = (c - (double)hi) / ((double)up - (double)hi);
+  return {hi, (float)(c - (double)hi), up, (uint32_t)std::min(part * 4294967296.0, 4294967295.0)};
 }
 
 // exp(d / temperature) for d = x - max <= 0.

@@ -81,11 +81,21 @@ __device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
   return r;
 }
 #endif
+#ifdef VSF_SCALAR
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  float a0, a1, b0, b1, c0, c1;
+  f2_get(a, a0, a1);
+  f2_get(b, b0, b1);
+  f2_get(c, c0, c1);
+  return f2(__fmaf_rn(a0, b0, c0), __fmaf_rn(a1, b1, c1));
+}
+#else
 __device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
   F2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
   return r;
 }
+#endif
 
 // The pairs of one vector.
 template <typename T>
@@ -125,6 +135,12 @@ __device__ __forceinline__ float largest(const uint4 (&v)[N], float) {
     m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(v[i].x), __uint_as_float(v[i].y)),
                        fmaxf(__uint_as_float(v[i].z), __uint_as_float(v[i].w))));
   return m;
+}
+
+__device__ __forceinline__ F2 exp2_pair(F2 t) {
+  float a, b;
+  f2_get(t, a, b);
+  return f2(ex2(a), ex2(b));
 }
 
 // exp((x - m) / temperature) of a pair, with nm = (-m, -m).
@@ -277,8 +293,9 @@ __device__ __forceinline__ Span span_of(const T* p, int32_t V) {
   const int32_t head = min(skew, V);
   return {head, (V - head) / Vec<T>::n};
 }
-__device__ __forceinline__ int32_t share(int32_t nvec, uint32_t rank, uint32_t count) {
-  return (int32_t)((int64_t)nvec * rank / count);
+// First vector of a CTA's share, in a cluster of 2^log CTAs.
+__device__ __forceinline__ int32_t share(int32_t nvec, uint32_t rank, uint32_t log) {
+  return (int32_t)(((int64_t)nvec * rank) >> log);
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -304,16 +321,16 @@ __device__ __forceinline__ MaxSum warp_join(MaxSum v, float inv_t) {
 
 // Zeroes the gradient row's share of this CTA.
 template <typename T>
-__device__ __forceinline__ void zero_share(T* g, int32_t V, uint32_t rank, uint32_t count, int tid,
+__device__ __forceinline__ void zero_share(T* g, int32_t V, uint32_t rank, uint32_t log, int tid,
                                            int threads) {
   const Span s = span_of(g, V);
   uint4* v = reinterpret_cast<uint4*>(g + s.head);
-  const int32_t end = share(s.nvec, rank + 1, count);
-  for (int32_t i = share(s.nvec, rank, count) + tid; i < end; i += threads)
+  const int32_t end = share(s.nvec, rank + 1, log);
+  for (int32_t i = share(s.nvec, rank, log) + tid; i < end; i += threads)
     __stcs(v + i, make_uint4(0, 0, 0, 0));
   const int32_t tail = s.head + s.nvec * Vec<T>::n;
   if (rank == 0 && tid < s.head) g[tid] = from_f<T>(0.f);
-  if (rank + 1 == count && tail + tid < V) g[tail + tid] = from_f<T>(0.f);
+  if (rank + 1 == 1u << log && tail + tid < V) g[tail + tid] = from_f<T>(0.f);
 }
 
 // The waits of a whole warp: all of its lanes go on, or none does.
@@ -351,6 +368,7 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
   const uint32_t pbar = qempty + 8 * kQueue, rbar = pbar + 8 * kQueue, xbar = rbar + 16;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t C = cta_count(), rank = C > 1 ? cta_rank() : 0;
+  const uint32_t logC = 31 - __clz(C);
   const int64_t cluster = blockIdx.x / C, clusters = gridDim.x / C;
   const Rows<T>& r = a.r;
   unsigned* err = &a.head->err;
@@ -394,8 +412,8 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
       const T* x = r.x + t * r.ld;
       const Span s = span_of(x, r.V);
       const char* base = reinterpret_cast<const char*>(x + s.head);
-      const int32_t end = share(s.nvec, rank + 1, C);
-      for (int32_t v = share(s.nvec, rank, C); v < end; v += Shape::chunk_vecs) {
+      const int32_t end = share(s.nvec, rank + 1, logC);
+      for (int32_t v = share(s.nvec, rank, logC); v < end; v += Shape::chunk_vecs) {
         if (issued == slots && !mbar_wait(empty + 8 * at.slot, at.phase ^ 1, err, stop)) return false;
         const uint32_t bytes = (uint32_t)min(end - v, (int32_t)Shape::chunk_vecs) * 16;
         mbar_expect_tx(full + 8 * at.slot, bytes);
@@ -563,6 +581,9 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
       }
     } else {  // ---------------------------------------------------- consumers
       const PairScale c2 = {f2(r.c.hi, r.c.hi), f2(r.c.lo, r.c.lo)};
+      // this thread's factor: log2(e) / temperature rounded down or up
+      const float c1 = (uint32_t)tid * 2654435769u < r.c.ups ? r.c.up : r.c.hi;
+      const F2 cc = f2(c1, c1);
       Place<slots> at;
       uint32_t written = 0;  // live rows whose gradient has been written
       // The gradient of a row from the chunks still in shared memory.
@@ -573,11 +594,15 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
         const float4 res = sh->result[par];
         const T* x = r.x + p.t * r.ld;
         const Span s = span_of(x, r.V);
-        const int32_t begin = share(s.nvec, rank, C), end = share(s.nvec, rank + 1, C);
+        const int32_t begin = share(s.nvec, rank, logC), end = share(s.nvec, rank + 1, logC);
         const float z = finite_max(res.x), b = res.y, coef = res.z;
         T* g = a.grad + p.t * a.grad_ld;
         const bool same = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
-        const F2 nm = f2(-z, -z), b2 = f2(b, b);
+        // bf16 keeps 8 bits: there 2^(x c - m c) with rounded c and m c serves,
+        // where m c does not overflow
+        const bool near = sizeof(T) == 2 && fabsf(z) < 1e30f;
+        const F2 nm = f2(-z, -z), b2 = f2(b, b), c0 = f2(r.c.hi, r.c.hi);
+        const F2 kk = f2(-z * r.c.hi, -z * r.c.hi);
         uint4* gv = reinterpret_cast<uint4*>(g + s.head);
         Place<slots> from = p.first;
         for (int32_t v = begin; v < end; v += Shape::chunk_vecs, from.next()) {
@@ -593,9 +618,15 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
               Pairs<T> e;
               unpack(c[j * Shape::consumers], e);
               float o[VE];
+              if (near) {
 #pragma unroll
-              for (int i = 0; i < VE / 2; ++i)
-                f2_get(f2_mul(exp_pair(e.p[i], nm, c2), b2), o[2 * i], o[2 * i + 1]);
+                for (int i = 0; i < VE / 2; ++i)
+                  f2_get(f2_mul(exp2_pair(f2_fma(e.p[i], c0, kk)), b2), o[2 * i], o[2 * i + 1]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < VE / 2; ++i)
+                  f2_get(f2_mul(exp_pair(e.p[i], nm, c2), b2), o[2 * i], o[2 * i + 1]);
+              }
               __stcs(out + j * Shape::consumers, pack_vec<T>(o));
             }
           } else {
@@ -610,7 +641,7 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
         }
         if (a.grad == nullptr) return true;
         if (coef == 0.f) {
-          zero_share(g, r.V, rank, C, tid, Shape::consumers);
+          zero_share(g, r.V, rank, logC, tid, Shape::consumers);
           return true;
         }
         if (p.loose >= 0) {
@@ -620,7 +651,7 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
         // the target's element again, by the thread that wrote it
         const int32_t ye = p.y - s.head, yv = ye / VE;
         if (ye >= 0 && yv >= begin && yv < end &&
-            tid == (same ? yv - begin : ye - begin * VE) % Shape::consumers)
+            tid == ((same ? yv - begin : ye - begin * VE) & (Shape::consumers - 1)))
           g[p.y] = from_f<T>(b * exp_scaled(res.w - z, r.c) + coef);
         return true;
       };
@@ -639,7 +670,7 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
         if (it.y < 0) {
           if (lane == 0) mbar_arrive(pbar + 8 * q.slot);
           if (a.grad != nullptr)
-            zero_share(a.grad + it.t * a.grad_ld, r.V, rank, C, tid, Shape::consumers);
+            zero_share(a.grad + it.t * a.grad_ld, r.V, rank, logC, tid, Shape::consumers);
           continue;
         }
         Pending<slots> row;
@@ -648,7 +679,7 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
         row.first = at;
         const T* x = r.x + it.t * r.ld;
         const Span s = span_of(x, r.V);
-        const int32_t begin = share(s.nvec, rank, C), end = share(s.nvec, rank + 1, C);
+        const int32_t begin = share(s.nvec, rank, logC), end = share(s.nvec, rank + 1, logC);
         row.loose = -1;
         if (rank == 0 && tid < s.head) row.loose = tid;
         if (rank + 1 == C && tid >= 16 && s.head + s.nvec * VE + tid - 16 < r.V)
@@ -659,6 +690,27 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
         // ---- maximum and sum
         float m = -INFINITY;
         F2 sum0 = f2(0.f, 0.f), sum1 = sum0;
+        auto add_up = [&](const uint4 (&x4)[Shape::per]) {
+          const float bm = largest(x4, T());
+          if (bm > m) {
+            const float f = expf((m - bm) * r.inv_tf);
+            sum0 = f2_mul(sum0, f2(f, f));
+            sum1 = f2_mul(sum1, f2(f, f));
+            m = bm;
+          }
+          const float z = -finite_max(m);
+          const F2 nm = f2(z, z);
+#pragma unroll
+          for (int j = 0; j < Shape::per; ++j) {
+            Pairs<T> p;
+            unpack(x4[j], p);
+#pragma unroll
+            for (int i = 0; i < VE / 2; i += 2) {
+              sum0 = f2_add(sum0, exp2_pair(f2_mul(f2_add(p.p[i], nm), cc)));
+              sum1 = f2_add(sum1, exp2_pair(f2_mul(f2_add(p.p[i + 1], nm), cc)));
+            }
+          }
+        };
         for (int32_t v = begin; v < end; v += Shape::chunk_vecs, at.next()) {
           if (!warp_wait(full + 8 * at.slot, at.phase, err, stop)) {
             ok = false;
@@ -666,32 +718,18 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
           }
           const uint4* c = reinterpret_cast<const uint4*>(ring + at.slot * Shape::chunk_bytes) + tid;
           const int32_t n = end - v - tid;
-          if (n > 0) {
-            uint4 x4[Shape::per];
+          uint4 x4[Shape::per];
+          if (n > (Shape::per - 1) * Shape::consumers) {
+#pragma unroll
+            for (int j = 0; j < Shape::per; ++j) x4[j] = c[j * Shape::consumers];
+            add_up(x4);
+          } else if (n > 0) {
 #pragma unroll
             for (int j = 0; j < Shape::per; ++j) {
               x4[j] = make_uint4(Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest);
               if (j == 0 || j * Shape::consumers < n) x4[j] = c[j * Shape::consumers];
             }
-            const float bm = largest(x4, T());
-            if (bm > m) {
-              const float f = expf((m - bm) * r.inv_tf);
-              sum0 = f2_mul(sum0, f2(f, f));
-              sum1 = f2_mul(sum1, f2(f, f));
-              m = bm;
-            }
-            const float z = -finite_max(m);
-            const F2 nm = f2(z, z);
-#pragma unroll
-            for (int j = 0; j < Shape::per; ++j) {
-              Pairs<T> p;
-              unpack(x4[j], p);
-#pragma unroll
-              for (int i = 0; i < VE / 2; i += 2) {
-                sum0 = f2_add(sum0, exp_pair(p.p[i], nm, c2));
-                sum1 = f2_add(sum1, exp_pair(p.p[i + 1], nm, c2));
-              }
-            }
+            add_up(x4);
           }
           if (!POLICY) {
             __syncwarp();
