@@ -88,21 +88,36 @@ __device__ __forceinline__ int32_t live_target(const Rows<T>& r, int64_t t, uint
   return live_target(r, token_at(r, t), err);
 }
 
-// ln p(y) from x_y - m and s, in fp64 with few fp64 operations: ln s = k ln 2
-// + ln f with f in [0.75, 1.5), where logf's absolute error is at most 3e-8
-// (logf(s) itself would round at 5e-7 for s in the thousands). All terms of s
-// but the maximum's 1 carry the mean error of ex2, which would add up over a
-// sequence, and is taken off here.
-__device__ __forceinline__ double log_prob(float d, float s, double inv_t) {
-  int k = 0;
-  float f = s;
+// ln s = k ln 2 + f, with |f| at most 0.41, where logf's absolute error is
+// below 3e-8 (logf(s) itself would round at 5e-7 for s in the thousands). All
+// terms of s but the maximum's 1 carry the mean error of ex2, which would add
+// up over a sequence, and is taken off here.
+struct LogSum {
+  float k, f;
+};
+__device__ __forceinline__ LogSum log_sum(float s) {
+  float k = 0.f, f = s;
   if (s >= 1.1754944e-38f && s < INFINITY) {
     const uint32_t b = __float_as_uint(s);
-    k = (int)((b + 0x00400000u) >> 23) - 127;
-    f = __uint_as_float(b - ((uint32_t)k << 23));
+    const uint32_t e = (b + 0x00400000u) >> 23;  // f in [0.75, 1.5)
+    k = (float)((int)e - 127);
+    f = __uint_as_float(b - ((e - 127u) << 23));
   }
   const float bias = (float)kEx2Bias * (1.f - 1.f / s);
-  return (double)d * inv_t - ((double)k * 0.69314718055994530942 + (double)(logf(f) - bias));
+  return {k, logf(f) - bias};
+}
+
+// ln p(y) - ref in fp32, with d = x_y - m: the large parts cancel first. ln 2 =
+// 355/512 - 2.12194440e-4 (the split of Cody and Waite): k times the first is
+// exact.
+__device__ __forceinline__ float log_ratio(float d, float inv_t, float ref, LogSum s) {
+  const float a = __fmaf_rn(d, inv_t, -ref);
+  return __fmaf_rn(-s.k, 0.693359375f, a) - __fmaf_rn(s.k, -2.12194440e-4f, s.f);
+}
+// ln p(y) in fp64.
+__device__ __forceinline__ double log_prob(float d, float s, double inv_t) {
+  const LogSum l = log_sum(s);
+  return (double)d * inv_t - ((double)l.k * 0.69314718055994530942 + (double)l.f);
 }
 
 struct MaxSum {
@@ -122,15 +137,15 @@ struct PolicyIn {
   int mean;
 };
 
-// One token's policy and KL terms and d(policy + beta kl)/d logp.
+// One token's policy and KL terms and d(policy + beta kl)/d logp, from
+// logp - old, u = ref - logp and its advantage.
 struct PolicyTerm {
   float policy, kl, slope;
 };
 
-__device__ __forceinline__ PolicyTerm policy_term(const PolicyIn& p, double lp, float old, float ref,
-                                                  float a) {
+__device__ __forceinline__ PolicyTerm policy_term(const PolicyIn& p, float ahead, float u, float a) {
   PolicyTerm o;
-  const float ratio = expf((float)(lp - (double)old));
+  const float ratio = expf(ahead);
   const float freed = ratio * a;
   const float held = fminf(fmaxf(ratio, p.lo), p.hi) * a;
   const bool clipped = freed > held;  // a NaN ratio is not clipped away
@@ -138,7 +153,6 @@ __device__ __forceinline__ PolicyTerm policy_term(const PolicyIn& p, double lp, 
   o.slope = clipped ? 0.f : -freed;
   o.kl = 0.f;
   if (p.beta != 0.f) {
-    const float u = (float)((double)ref - lp);
     const float e = expm1f(u);
     // exp(u) - 1 - u; near 0 by its series, whose first terms do not cancel
     o.kl = fabsf(u) < 0.25f
@@ -179,9 +193,10 @@ __global__ void __launch_bounds__(kTokenThreads)
     }
     const double w = r.weight != nullptr ? (double)r.weight[t] : 1.0;
     const float2 ms = row[t];
+    const double lp = log_prob(to_f(r.x[t * r.ld + y]) - ms.x, ms.y, r.inv_t);
     const PolicyTerm o =
-        policy_term(p, log_prob(to_f(r.x[t * r.ld + y]) - ms.x, ms.y, r.inv_t), p.old_logp[t],
-                    p.beta != 0.f ? p.ref_logp[t] : 0.f, p.adv[t]);
+        policy_term(p, (float)(lp - (double)p.old_logp[t]),
+                    p.beta != 0.f ? (float)((double)p.ref_logp[t] - lp) : 0.f, p.adv[t]);
     pol += w * (double)o.policy;
     kl += w * (double)o.kl;
     coef[t] = (float)(f * w * r.inv_t * (double)o.slope);

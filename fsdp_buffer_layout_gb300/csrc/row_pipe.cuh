@@ -221,6 +221,7 @@ __device__ __forceinline__ uint4 pack_vec<float>(const float (&o)[4]) {
 
 constexpr int kMaxPipeCluster = 16;
 constexpr uint32_t kQueue = 8;  // rows handed on and not yet added up
+constexpr int kList = 2048;     // rows of a cluster that its list holds
 
 // One shape of the kernel: W consumer warps, each thread `per` vectors of a
 // chunk, and a ring of 208 KB for the CTAs of an SM together.
@@ -248,11 +249,12 @@ struct Place {
   }
 };
 
-// A row as the producer hands it on.
+// A row as the producer hands it on. Its x_y has been read by then, so the
+// gradient may be written over the logits.
 struct RowItem {
-  int64_t t;  // -1: no more rows
+  int32_t t;  // -1: no more rows
   int32_t y;  // -1: masked
-  float w;
+  float w, xy, old, ref, adv;
 };
 struct PipeTail {  // shared memory behind the ring and its barriers
   float4 message[2][kMaxPipeCluster];
@@ -260,6 +262,9 @@ struct PipeTail {  // shared memory behind the ring and its barriers
   RowItem item[kQueue];
   MaxSum part[kQueue][16];
   double sum[16];
+  uint32_t count[2][16];  // live tokens of each warp's, masked ones << 16
+  int32_t rows[kList];    // the cluster's live rows from the front, masked ones from the back
+  int32_t n_live, n_dead;
   uint32_t stop;
 };
 
@@ -298,14 +303,17 @@ __device__ __forceinline__ int32_t share(int32_t nvec, uint32_t rank, uint32_t l
   return (int32_t)(((int64_t)nvec * rank) >> log);
 }
 
+// Largest of a warp's values; NaN is passed over.
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
-  return v;
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
+// Sum over the first N lanes (a power of two), in each of them.
+template <int N = 32>
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  for (int o = N / 2; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
 __device__ __forceinline__ double warp_sum(double v) {
@@ -313,10 +321,12 @@ __device__ __forceinline__ double warp_sum(double v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
-// The join of a warp's maxima and sums.
+// The join of the maxima and sums of a warp's first N lanes, in those lanes;
+// the others hold {-inf, 0}.
+template <int N = 32>
 __device__ __forceinline__ MaxSum warp_join(MaxSum v, float inv_t) {
   const float m = warp_max(v.m);
-  return {m, warp_sum(v.s * expf((v.m - finite_max(m)) * inv_t))};
+  return {m, warp_sum<N>(v.s * expf((v.m - finite_max(m)) * inv_t))};
 }
 
 // Zeroes the gradient row's share of this CTA.
@@ -371,6 +381,9 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
   const uint32_t logC = 31 - __clz(C);
   const int64_t cluster = blockIdx.x / C, clusters = gridDim.x / C;
   const Rows<T>& r = a.r;
+  // whether live and masked rows are dealt out apart, by a list; beyond its
+  // length the clusters take rows in turn as they come
+  const bool listed = 2 * (r.T_ / clusters + 1) <= kList;
   unsigned* err = &a.head->err;
   volatile uint32_t* stop = &sh->stop;
 
@@ -399,13 +412,20 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
     Place<slots> at;
     Place<kQueue> q;
     uint32_t issued = 0, queued = 0;  // counted up to the ring's and the queue's length
-    // hands a row on; lane 0 alone
-    auto push = [&](int64_t t, int32_t y, float w) -> bool {
-      if (queued == kQueue && !mbar_wait(qempty + 8 * q.slot, q.phase ^ 1, err, stop)) return false;
-      sh->item[q.slot] = {t, y, w};
-      mbar_arrive(qfull + 8 * q.slot);
+    // hands a row on, which lane `from` holds
+    auto push = [&](const RowItem& item, int from) -> bool {
+      bool ok = true;
+      if (queued == kQueue) {
+        if (lane == 0) ok = mbar_wait(qempty + 8 * q.slot, q.phase ^ 1, err, stop);
+        if (!__shfl_sync(~0u, (int)ok, 0)) return false;
+      } else {
+        ++queued;
+      }
+      if (lane == from) {
+        sh->item[q.slot] = item;
+        mbar_arrive(qfull + 8 * q.slot);
+      }
       q.next();
-      if (queued < kQueue) ++queued;
       return true;
     };
     auto stream = [&](int64_t t) -> bool {
@@ -424,43 +444,55 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
       }
       return true;
     };
-    int64_t lives = 0, deads = 0;  // tokens seen of each kind
-    int64_t my_live = cluster, my_dead = cluster;
-    bool ok = true;
-    Token next = token_at(r, (int64_t)lane);
-    for (int64_t t0 = 0; t0 < r.T_ && ok; t0 += 32) {
-      const Token k = next;
-      next = token_at(r, t0 + 32 + lane);
-      const bool owner = rank == 0 && (uint32_t)(t0 >> 5) % (uint32_t)clusters == (uint32_t)cluster;
-      const int32_t y = live_target(r, k, owner ? err : nullptr);
-      const uint32_t live = __ballot_sync(~0u, y >= 0);
-      const uint32_t dead = __ballot_sync(~0u, y < 0 && t0 + lane < r.T_);
-      const uint32_t below = (1u << lane) - 1;
-      if (owner && y < 0 && t0 + lane < r.T_ && a.logp != nullptr) a.logp[t0 + lane] = 0.f;
-      while (ok && my_live < lives + __popc(live)) {
-        const uint32_t hit =
-            __ballot_sync(~0u, y >= 0 && lives + __popc(live & below) == my_live);
-        const int who = __ffs(hit) - 1;
-        const int32_t yy = __shfl_sync(~0u, y, who);
-        const float ww = __shfl_sync(~0u, k.w, who);
-        if (lane == 0) ok = push(t0 + who, yy, ww) && stream(t0 + who);
-        ok = __shfl_sync(~0u, (int)ok, 0) != 0;
-        my_live += clusters;
+    asm volatile("bar.sync 1, %0;" ::"r"(Shape::threads) : "memory");  // the list is there
+    // Rows in turn, masked ones spread among the live ones; a lane fetches what
+    // the joiner needs of a row, 32 rows at a time and as many ahead.
+    const int n_live = sh->n_live, n_rows = n_live + sh->n_dead;
+    auto row_at = [&](int i) -> int {
+      if (!listed) {
+        const int64_t t = cluster + i * clusters;
+        return t < r.T_ ? (int)t : -1;
       }
-      lives += __popc(live);
+      if (i >= n_rows) return -1;
+      // of the first i rows, i n_live / n_rows rounded up are live
+      const int before = (i * n_live + n_rows - 1) / n_rows;
+      const int after = ((i + 1) * n_live + n_rows - 1) / n_rows;
+      return after > before ? sh->rows[before] : sh->rows[kList - 1 - (i - before)];
+    };
+    auto fetch = [&](int i) -> RowItem {
+      RowItem it = {row_at(i), -1, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (it.t < 0) return it;
+      const Token k = token_at(r, it.t);
+      it.y = live_target(r, k, nullptr);
+      it.w = k.w;
+      if (it.y < 0) return it;
+      it.xy = to_f(r.x[(int64_t)it.t * r.ld + it.y]);
       if (POLICY) {
-        while (ok && my_dead < deads + __popc(dead)) {
-          const uint32_t hit = __ballot_sync(~0u, (dead >> lane & 1) &&
-                                                      deads + __popc(dead & below) == my_dead);
-          if (lane == 0) ok = push(t0 + __ffs(hit) - 1, -1, 0.f);
-          ok = __shfl_sync(~0u, (int)ok, 0) != 0;
-          my_dead += clusters;
-        }
-        deads += __popc(dead);
+        it.old = a.p.old_logp[it.t];
+        it.adv = a.p.adv[it.t];
+        if (a.p.beta != 0.f) it.ref = a.p.ref_logp[it.t];
       }
+      return it;
+    };
+    bool ok = true;
+    RowItem next = fetch(lane);
+    for (int i0 = 32; ok; i0 += 32) {
+      const RowItem now = next;
+      const int n = __popc(__ballot_sync(~0u, now.t >= 0));
+      if (n == 32) next = fetch(i0 + lane);
+      for (int j = 0; j < n && ok; ++j) {
+        const int tj = __shfl_sync(~0u, now.t, j), yj = __shfl_sync(~0u, now.y, j);
+        if (!POLICY && yj < 0) continue;
+        ok = push(now, j);
+        if (ok && yj >= 0) {
+          if (lane == 0) ok = stream(tj);
+          ok = __shfl_sync(~0u, (int)ok, 0) != 0;
+        }
+      }
+      if (n < 32) break;
     }
+    if (ok) push({-1, -1, 0.f, 0.f, 0.f, 0.f, 0.f}, 0);
     if (lane == 0) {
-      if (ok) push(-1, -1, 0.f);
       // every copy issued has to land before the CTA may end
       const uint64_t deadline = global_ns() + kWaitNs;
       if (issued < slots) at = Place<slots>();
@@ -469,30 +501,81 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
         if (!mbar_drain(full + 8 * at.slot, at.phase, deadline, err)) break;
     }
   } else {
-    // The sum of the live weights scales every gradient: each CTA adds it up
-    // for itself, in the same order, while its first rows are on their way.
-    if (POLICY && a.p.mean) {
-      if (warp < W) {
-        float w4[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int64_t t = tid; t < r.T_; t += 4 * Shape::consumers)
+    if (warp < W) {
+      // Once through the tokens, 8 times 32 a warp at a time: the sum of the
+      // live weights, which scales every gradient (each CTA adds it up for
+      // itself, in the same order), and the cluster's rows.
+      constexpr int kBlocks = 8;
+      const bool first = cluster == 0 && rank == 0;
+      const int step = (int)clusters, own = (int)cluster;
+      float w2[2] = {0.f, 0.f};
+      int lives = 0, deads = 0, buf = 0;
+      for (int64_t t0 = 0; t0 < r.T_; t0 += W * kBlocks * 32, buf ^= 1) {
+        const int64_t tw = t0 + warp * kBlocks * 32;
+        uint32_t lb = 0, db = 0;  // lane j: live and masked tokens of block j
+        Token k[kBlocks];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int64_t u = t + j * Shape::consumers;
-            if (u < r.T_) {
-              const Token k = token_at(r, u);
-              if (k.y >= 0 && k.y < r.V) w4[j] += k.w;
-            }
+        for (int j = 0; j < kBlocks; ++j) k[j] = token_at(r, tw + 32 * j + lane);
+#pragma unroll
+        for (int j = 0; j < kBlocks; ++j) {
+          const int64_t t = tw + 32 * j + lane;
+          const int32_t y = live_target(r, k[j], first ? err : nullptr);
+          if (y >= 0) w2[j & 1] += k[j].w;
+          else if (first && t < r.T_ && a.logp != nullptr) a.logp[t] = 0.f;
+          const uint32_t l = __ballot_sync(~0u, y >= 0), d = __ballot_sync(~0u, y < 0 && t < r.T_);
+          if (lane == j) {
+            lb = l;
+            db = d;
           }
-        const double n = warp_sum(((double)w4[0] + w4[1]) + ((double)w4[2] + w4[3]));
-        if (lane == 0) sh->sum[warp] = n;
-        asm volatile("bar.arrive 1, %0;" ::"r"(Shape::consumers + 32) : "memory");
-      } else {
-        asm volatile("bar.sync 1, %0;" ::"r"(Shape::consumers + 32) : "memory");
+        }
+        if (!listed) continue;
+        // live and masked tokens (at most 256 a warp) up to each block's end
+        const uint32_t mine = __popc(lb) | __popc(db) << 16;
+        uint32_t sum = mine;
+#pragma unroll
+        for (int o = 1; o < kBlocks; o <<= 1) {
+          const uint32_t u = __shfl_up_sync(~0u, sum, o);
+          if (lane >= o) sum += u;
+        }
+        if (lane == kBlocks - 1) sh->count[buf][warp] = sum;
+        asm volatile("bar.sync 2, %0;" ::"r"(Shape::consumers) : "memory");
+        uint32_t before = 0, all = 0;  // of the warps before this one; of all
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const uint32_t c = sh->count[buf][w];
+          all += c;
+          if (w < warp) before += c;
+        }
+        before += sum - mine;
+        // numbers own, own + step, ... of all live (masked) tokens
+        auto list = [&](uint32_t bits, int start, bool front) {
+          int i = start <= own ? 0 : (int)((uint32_t)(start - own + step - 1) / (uint32_t)step);
+          for (int at = own + i * step - start; at < __popc(bits); at += step, ++i) {
+            uint32_t rest = bits;
+            for (int d = 0; d < at; ++d) rest &= rest - 1;
+            sh->rows[front ? i : kList - 1 - i] = (int)tw + 32 * lane + __ffs(rest) - 1;
+          }
+        };
+        if (lane < kBlocks) {
+          list(lb, lives + (int)(before & 0xffffu), true);
+          if (POLICY) list(db, deads + (int)(before >> 16), false);
+        }
+        lives += (int)(all & 0xffffu);
+        deads += (int)(all >> 16);
       }
+      const double n = warp_sum((double)w2[0] + (double)w2[1]);
+      if (lane == 0) sh->sum[warp] = n;
+      if (tid == 0) {
+        sh->n_live = lives > own ? (lives - own + step - 1) / step : 0;
+        sh->n_dead = POLICY && deads > own ? (deads - own + step - 1) / step : 0;
+      }
+      asm volatile("bar.arrive 1, %0;" ::"r"(Shape::threads) : "memory");
+    } else {
+      asm volatile("bar.sync 1, %0;" ::"r"(Shape::threads) : "memory");
     }
     Place<kQueue> q;
     if (warp == W + 1) {  // ------------------------------------------ joiner
-      double factor = 0.0, weight_sum = 0.0, pol = 0.0, kls = 0.0;
+      double factor = 0.0;
       if (POLICY) {
         factor = (double)a.p.scale;
         if (a.p.mean) {
@@ -501,21 +584,16 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
           if (all != 0.0) factor /= all;
         }
       }
+      const float scale = (float)(factor * r.inv_t);
+      double sum = 0.0;  // lane 0: policy, lane 1: KL, lane 2: weight
       for (uint32_t done = 0;; q.next()) {
         if (!warp_wait(qfull + 8 * q.slot, q.phase, err, stop)) break;
-        const RowItem it = sh->item[q.slot];
-        if (it.t < 0) break;
-        if (it.y < 0) {
+        const RowItem now = sh->item[q.slot];
+        if (now.t < 0) break;
+        if (now.y < 0) {
           if (!warp_wait(pbar + 8 * q.slot, q.phase, err, stop)) break;
           if (lane == 0) mbar_arrive(qempty + 8 * q.slot);
           continue;
-        }
-        const float xy = to_f(r.x[it.t * r.ld + it.y]);
-        float old = 0.f, ref = 0.f, adv = 0.f;
-        if (POLICY) {
-          old = a.p.old_logp[it.t];
-          adv = a.p.adv[it.t];
-          if (a.p.beta != 0.f) ref = a.p.ref_logp[it.t];
         }
         const uint32_t par = done & 1, phase = (done >> 1) & 1;
         ++done;
@@ -523,44 +601,44 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
         MaxSum ms = lane < W ? sh->part[q.slot][lane] : MaxSum{-INFINITY, 0.f};
         __syncwarp();
         if (lane == 0) mbar_arrive(qempty + 8 * q.slot);
-        ms = warp_join(ms, r.inv_tf);
+        ms = warp_join<W>(ms, r.inv_tf);
         if (C > 1) {
           const uint32_t bar = xbar + 8 * par;
           if (lane == 0) mbar_expect_tx(bar, C * 16);
           __syncwarp();
-          // xy goes with the message, so that it has been read before any
-          // CTA of the cluster may write the gradient over the logits
-          if (lane < C) put_async(smem_u32(&sh->message[par][rank]), bar, lane, ms.m, ms.s, xy);
+          if (lane < C) put_async(smem_u32(&sh->message[par][rank]), bar, lane, ms.m, ms.s, now.xy);
           if (!warp_wait_cluster(bar, phase, err, stop)) break;
           const float4 got = sh->message[par][lane < C ? lane : 0];
-          ms = warp_join(lane < C ? MaxSum{got.x, got.y} : MaxSum{-INFINITY, 0.f}, r.inv_tf);
+          ms = warp_join<kMaxPipeCluster>(lane < C ? MaxSum{got.x, got.y} : MaxSum{-INFINITY, 0.f},
+                                          r.inv_tf);
         }
-        const double lp = log_prob(xy - ms.m, ms.s, r.inv_t);
+        // lane 0 (of the cluster's first lanes) holds the row's maximum and sum
+        const LogSum ls = log_sum(ms.s);
+        const float d = now.xy - ms.m;
         if (POLICY) {
-          const PolicyTerm o = policy_term(a.p, lp, old, ref, adv);
-          const float coef = (float)(factor * (double)it.w * r.inv_t * (double)o.slope);
+          const PolicyTerm o = policy_term(a.p, log_ratio(d, r.inv_tf, now.old, ls),
+                                           -log_ratio(d, r.inv_tf, now.ref, ls), now.adv);
+          const float coef = scale * now.w * o.slope;
           if (lane == 0) {
-            sh->result[par] = make_float4(ms.m, -coef / ms.s, coef, xy);
+            sh->result[par] = make_float4(ms.m, -coef / ms.s, coef, now.xy);
             mbar_arrive(rbar + 8 * par);
           }
-          pol += (double)it.w * (double)o.policy;
-          kls += (double)it.w * (double)o.kl;
-          weight_sum += (double)it.w;
+          sum += (double)(lane == 0 ? now.w * o.policy : lane == 1 ? now.w * o.kl : now.w);
         }
         if (lane == 0 && rank == 0) {
-          if (a.row != nullptr) a.row[it.t] = make_float2(ms.m, ms.s);
-          if (a.logp != nullptr) a.logp[it.t] = (float)lp;
+          if (a.row != nullptr) a.row[now.t] = make_float2(ms.m, ms.s);
+          if (a.logp != nullptr) a.logp[now.t] = log_ratio(d, r.inv_tf, 0.f, ls);
         }
       }
       if (POLICY && rank == 0) {
         // the last cluster to finish adds up all of them in their order
         uint32_t last = 0;
-        if (lane == 0) {
-          double* p = a.partial + 3 * cluster;
-          p[0] = pol;
-          p[1] = kls;
-          p[2] = weight_sum;
+        if (lane < 3) {
+          a.partial[3 * cluster + lane] = sum;
           __threadfence();
+        }
+        __syncwarp();
+        if (lane == 0) {
           last = atomicAdd(&a.head->ticket, 1u) + 1 == (uint32_t)clusters;
           __threadfence();
         }
@@ -670,14 +748,14 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
         if (it.y < 0) {
           if (lane == 0) mbar_arrive(pbar + 8 * q.slot);
           if (a.grad != nullptr)
-            zero_share(a.grad + it.t * a.grad_ld, r.V, rank, logC, tid, Shape::consumers);
+            zero_share(a.grad + (int64_t)it.t * a.grad_ld, r.V, rank, logC, tid, Shape::consumers);
           continue;
         }
         Pending<slots> row;
         row.t = it.t;
         row.y = it.y;
         row.first = at;
-        const T* x = r.x + it.t * r.ld;
+        const T* x = r.x + (int64_t)it.t * r.ld;
         const Span s = span_of(x, r.V);
         const int32_t begin = share(s.nvec, rank, logC), end = share(s.nvec, rank + 1, logC);
         row.loose = -1;
