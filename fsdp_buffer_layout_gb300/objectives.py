@@ -34,6 +34,7 @@ class _Objective:
         device = torch.device("cuda" if device is None else device)
         self.device = device if device.index is not None \
             else torch.device(device.type, torch.cuda.current_device())
+        self._index = self.device.index
         self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
         self._st = self.stream.cuda_stream
 
@@ -47,33 +48,36 @@ class _Objective:
         self._ws, self._ws_bytes = self.workspace.data_ptr(), nbytes
         V.vsf_objective_workspace_init(self._ws, nbytes, self._st)
 
-    def _rows(self, x, what: str) -> int:
-        """Checks rows of logits (or their gradient); the row stride."""
-        if x.dtype is not self.dtype or x.dim() != 2 or x.shape[1] != self.width \
-                or x.device != self.device:
+    def _rows(self, x, what: str):
+        """Checks rows of logits (or their gradient); their number and stride."""
+        shape = x.shape
+        if x.dtype is not self.dtype or len(shape) != 2 or shape[1] != self.width \
+                or shape[0] > self.tokens or x.get_device() != self._index:
             raise ValueError(f"{what}: expected {self.dtype} [<= {self.tokens}, {self.width}] on "
-                             f"{self.device}, got {x.dtype} {tuple(x.shape)} on {x.device}")
-        rows, cols = x.shape
-        if rows > self.tokens:
-            raise ValueError(f"{what}: {rows} rows, the object was made for {self.tokens}")
+                             f"{self.device}, got {x.dtype} {tuple(shape)} on {x.device}")
+        rows, cols = shape
         ld, unit = x.stride()
-        if cols > 1 and unit != 1:
+        if unit != 1 and cols > 1:
             raise ValueError(f"{what}: the elements of a row must be adjacent (stride {unit})")
-        if rows <= 1:
-            return max(ld, cols)
         if ld < cols:
-            raise ValueError(f"{what}: rows overlap (stride {ld}, {cols} elements)")
-        return ld
+            if rows > 1:
+                raise ValueError(f"{what}: rows overlap (stride {ld}, {cols} elements)")
+            ld = cols
+        return rows, ld
 
     def _vec(self, x, n: int, dtype, what: str):
         """Checks a contiguous vector of n elements; its address (None: none)."""
         if x is None:
             return None
-        if x.dtype is not dtype or x.numel() != n or not x.is_contiguous() \
-                or x.device != self.device:
+        if x.dtype is not dtype or x.numel() != n or x.get_device() != self._index \
+                or not x.is_contiguous():
             raise ValueError(f"{what}: expected {n} contiguous {dtype} on {self.device}, got "
                              f"{x.dtype} {tuple(x.shape)} on {x.device}")
         return x.data_ptr()
+
+    def _first(self, buf, n: int):
+        """The first n rows of an output of the object's own."""
+        return buf if n == self.tokens else buf[:n]
 
     def device_error(self) -> int:
         """The device error word (0: no wait ran out, every target in range)."""
@@ -90,14 +94,14 @@ class TokenLogprobs(_Objective):
         self.inv_temperature = inv_temperature
         self._workspace(V.vsf_objective_workspace_bytes(self.tokens))
         self.logp = self._new(self.tokens)
+        self._logp = self.logp.data_ptr()
 
     def __call__(self, logits, targets):
-        ld, n = self._rows(logits, "logits"), logits.shape[0]
-        logp = self.logp[:n]
+        n, ld = self._rows(logits, "logits")
         V.vsf_token_logprobs(logits.data_ptr(), self._vdt, n, self.width, ld,
                              self._vec(targets, n, torch.int64, "targets"), self.inv_temperature,
-                             logp.data_ptr(), self._ws, self._ws_bytes, self._st)
-        return logp
+                             self._logp, self._ws, self._ws_bytes, self._st)
+        return self._first(self.logp, n)
 
 
 class _LogitsLoss(_Objective):
@@ -105,19 +109,28 @@ class _LogitsLoss(_Objective):
         self._workspace(V.vsf_objective_workspace_bytes(self.tokens, pairs))
         self.stats = self._new(stats)
         self.logp = self._new(self.tokens)
-        self.grad = self._new(self.tokens, self.width, dtype=self.dtype) if with_grad else None
+        self._out = self.stats.data_ptr(), self.logp.data_ptr()
+        self.grad = None
+        # The gradient's rows start at the same places modulo 16 bytes as those
+        # of logits with aligned or adjacent rows, so both go in wide pieces.
+        self._pad = -self.width % (16 // self.dtype.itemsize)
+        if with_grad:
+            self._buffer = self._new(self.tokens * (self.width + self._pad), dtype=self.dtype)
+            self._views = {p: self._buffer.as_strided((self.tokens, self.width),
+                                                      (self.width + p, 1)) for p in (0, self._pad)}
+            self.grad = self._views[self._pad]
 
-    def _grad(self, n: int, grad):
+    def _grad(self, n: int, ld: int, grad):
         """The gradient's tensor, address and row stride of a call."""
-        if grad is None:
-            if self.grad is None:
-                return None, None, self.width
-            grad = self.grad[:n]
-            return grad, grad.data_ptr(), self.width
-        ld = self._rows(grad, "grad")
-        if grad.shape[0] != n:
-            raise ValueError(f"grad: {grad.shape[0]} rows, logits have {n}")
-        return grad, grad.data_ptr(), ld
+        if grad is not None:
+            rows, grad_ld = self._rows(grad, "grad")
+            if rows != n:
+                raise ValueError(f"grad: {rows} rows, logits have {n}")
+            return grad, grad.data_ptr(), grad_ld
+        if self.grad is None:
+            return None, None, self.width
+        pad = 0 if ld == self.width else self._pad
+        return self._first(self._views[pad], n), self._buffer.data_ptr(), self.width + pad
 
 
 class PolicyLoss(_LogitsLoss):
@@ -136,17 +149,18 @@ class PolicyLoss(_LogitsLoss):
 
     def __call__(self, logits, targets, old_logp, advantages, ref_logp=None, weights=None,
                  grad=None):
-        ld, n = self._rows(logits, "logits"), logits.shape[0]
-        grad, g, grad_ld = self._grad(n, grad)
-        logp, f32 = self.logp[:n], torch.float32
+        n, ld = self._rows(logits, "logits")
+        grad, g, grad_ld = self._grad(n, ld, grad)
+        f32 = torch.float32
+        stats, logp = self._out
         V.vsf_policy_loss(logits.data_ptr(), self._vdt, n, self.width, ld,
                           self._vec(targets, n, torch.int64, "targets"),
                           self._vec(old_logp, n, f32, "old_logp"),
                           self._vec(ref_logp, n, f32, "ref_logp"),
                           self._vec(advantages, n, f32, "advantages"),
-                          self._vec(weights, n, f32, "weights"), self.hp, self.stats.data_ptr(),
-                          logp.data_ptr(), g, grad_ld, self._ws, self._ws_bytes, self._st)
-        return self.stats, logp, grad
+                          self._vec(weights, n, f32, "weights"), self.hp, stats, logp, g,
+                          grad_ld, self._ws, self._ws_bytes, self._st)
+        return self.stats, self._first(self.logp, n), grad
 
 
 class PreferenceLoss(_LogitsLoss):
@@ -171,21 +185,22 @@ class PreferenceLoss(_LogitsLoss):
                                             self.KINDS[kind], average)
         self._outputs(self.pairs, 2, with_grad)
         self.rewards = self._new(2 * self.pairs)
+        self._rewards = self.rewards.data_ptr()
 
     def __call__(self, logits, targets, seq_starts, ref_logp=None, weights=None, grad=None):
-        ld, n = self._rows(logits, "logits"), logits.shape[0]
-        grad, g, grad_ld = self._grad(n, grad)
-        logp, f32 = self.logp[:n], torch.float32
+        n, ld = self._rows(logits, "logits")
+        grad, g, grad_ld = self._grad(n, ld, grad)
+        f32 = torch.float32
+        stats, logp = self._out
         V.vsf_preference_loss(logits.data_ptr(), self._vdt, n, self.width, ld,
                               self._vec(targets, n, torch.int64, "targets"),
                               self._vec(ref_logp, n, f32, "ref_logp"),
                               self._vec(weights, n, f32, "weights"),
                               self._vec(seq_starts, 2 * self.pairs + 1, torch.int64,
                                         "seq_starts"),
-                              self.pairs, self.hp, self.stats.data_ptr(),
-                              self.rewards.data_ptr(), logp.data_ptr(), g, grad_ld, self._ws,
-                              self._ws_bytes, self._st)
-        return self.stats, self.rewards, logp, grad
+                              self.pairs, self.hp, stats, self._rewards, logp, g, grad_ld,
+                              self._ws, self._ws_bytes, self._st)
+        return self.stats, self.rewards, self._first(self.logp, n), grad
 
 
 class Router(_Objective):
@@ -212,10 +227,12 @@ class Router(_Objective):
         self.loss = self._new(())
         self.seq_counts = self._new(self.sequences, self.width, dtype=i32)
         self.seq_coef = self._new(self.sequences)
+        self._out = [t.data_ptr() for t in (self.idx, self.gates, self.counts, self.loss,
+                                            self.seq_counts, self.seq_coef)]
         self.grad = None  # made by the first backward
 
     def _args(self, logits, live, seq_starts):
-        ld, n = self._rows(logits, "logits"), logits.shape[0]
+        n, ld = self._rows(logits, "logits")
         if seq_starts is None and self.sequences != 1:
             raise ValueError(f"seq_starts: needed for {self.sequences} sequences")
         return (n, ld, self._vec(live, n, torch.uint8, "live"),
@@ -225,10 +242,8 @@ class Router(_Objective):
         n, ld, lv, starts = self._args(logits, live, seq_starts)
         V.vsf_route(logits.data_ptr(), self._vdt, n, self.width, ld,
                     self._vec(bias, self.width, torch.float32, "bias"), lv, starts,
-                    self.sequences, self.hp, self.idx.data_ptr(), self.gates.data_ptr(),
-                    self.counts.data_ptr(), self.loss.data_ptr(), self.seq_counts.data_ptr(),
-                    self.seq_coef.data_ptr(), self._ws, self._ws_bytes, self._st)
-        return self.idx[:n], self.gates[:n], self.counts, self.loss
+                    self.sequences, self.hp, *self._out, self._ws, self._ws_bytes, self._st)
+        return self._first(self.idx, n), self._first(self.gates, n), self.counts, self.loss
 
     def backward(self, logits, d_gates=None, live=None, seq_starts=None, loss_scale: float = 1.0,
                  grad=None):
@@ -236,14 +251,14 @@ class Router(_Objective):
         if grad is None:
             if self.grad is None:
                 self.grad = self._new(self.tokens, self.width, dtype=self.dtype)
-            grad, grad_ld = self.grad[:n], self.width
+            grad, grad_ld = self._first(self.grad, n), self.width
         else:
-            grad_ld = self._rows(grad, "grad")
-            if grad.shape[0] != n:
-                raise ValueError(f"grad: {grad.shape[0]} rows, logits have {n}")
+            rows, grad_ld = self._rows(grad, "grad")
+            if rows != n:
+                raise ValueError(f"grad: {rows} rows, logits have {n}")
         V.vsf_route_grad(logits.data_ptr(), self._vdt, n, self.width, ld, lv, starts,
-                         self.sequences, self.hp, self.idx.data_ptr(),
+                         self.sequences, self.hp, self._out[0],
                          self._vec(d_gates, n * self.top_k, torch.float32, "d_gates"),
-                         self.seq_counts.data_ptr(), self.seq_coef.data_ptr(), loss_scale,
+                         *self._out[4:], loss_scale,
                          grad.data_ptr(), grad_ld, self._st)
         return grad

@@ -88,6 +88,8 @@ def library_path() -> str:
 def lib():
     """Loads libvsf.so. Raises if it has not been built: there is no fallback."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
