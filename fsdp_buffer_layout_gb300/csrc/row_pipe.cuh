@@ -343,6 +343,18 @@ __device__ __forceinline__ void zero_share(T* g, int32_t V, uint32_t rank, uint3
   if (rank + 1 == 1u << log && tail + tid < V) g[tail + tid] = from_f<T>(0.f);
 }
 
+// Whether the phase of the given parity is over; does not wait.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // The waits of a whole warp: all of its lanes go on, or none does.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned* err,
                                           volatile uint32_t* stop) {
@@ -381,9 +393,9 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
   const uint32_t logC = 31 - __clz(C);
   const int64_t cluster = blockIdx.x / C, clusters = gridDim.x / C;
   const Rows<T>& r = a.r;
-  // whether live and masked rows are dealt out apart, by a list; beyond its
-  // length the clusters take rows in turn as they come
-  const bool listed = 2 * (r.T_ / clusters + 1) <= kList;
+  // whether live and masked rows are dealt out apart, by a list; with a row a
+  // cluster at most, or more than it holds, clusters take rows as they come
+  const bool listed = r.T_ > clusters && 2 * (r.T_ / clusters + 1) <= kList;
   unsigned* err = &a.head->err;
   volatile uint32_t* stop = &sh->stop;
 
@@ -412,8 +424,12 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
     Place<slots> at;
     Place<kQueue> q;
     uint32_t issued = 0, queued = 0;  // counted up to the ring's and the queue's length
-    // hands a row on, which lane `from` holds
-    auto push = [&](const RowItem& item, int from) -> bool {
+    // Hands a row on, which lane `from` holds, and streams its share. As many
+    // chunks as the ring has room for are asked for before the row's scalars
+    // are waited for, the others after the row is in the queue (the consumers
+    // make room only for a row they know).
+    auto hand_on = [&](const RowItem& item, int from) -> bool {
+      const int32_t t = __shfl_sync(~0u, item.t, from), y = __shfl_sync(~0u, item.y, from);
       bool ok = true;
       if (queued == kQueue) {
         if (lane == 0) ok = mbar_wait(qempty + 8 * q.slot, q.phase ^ 1, err, stop);
@@ -421,33 +437,45 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
       } else {
         ++queued;
       }
+      const bool reads = t >= 0 && y >= 0;
+      const T* x = r.x + (reads ? t * r.ld : 0);
+      const Span s = span_of(x, r.V);
+      const char* base = reinterpret_cast<const char*>(x + s.head);
+      int32_t v = share(s.nvec, rank, logC);
+      const int32_t end = reads ? share(s.nvec, rank + 1, logC) : v;
+      auto stream = [&](bool wait) -> bool {
+        for (; v < end; v += Shape::chunk_vecs) {
+          if (issued == slots) {
+            const uint32_t bar = empty + 8 * at.slot;
+            if (wait ? !mbar_wait(bar, at.phase ^ 1, err, stop) : !mbar_test(bar, at.phase ^ 1))
+              return false;
+          } else {
+            ++issued;
+          }
+          const uint32_t bytes = (uint32_t)min(end - v, (int32_t)Shape::chunk_vecs) * 16;
+          mbar_expect_tx(full + 8 * at.slot, bytes);
+          bulk_load(smem_u32(ring + at.slot * Shape::chunk_bytes), base + (int64_t)v * 16, bytes,
+                    full + 8 * at.slot);
+          at.next();
+        }
+        return true;
+      };
+      if (lane == 0) stream(false);
+      __syncwarp();
       if (lane == from) {
         sh->item[q.slot] = item;
         mbar_arrive(qfull + 8 * q.slot);
       }
       q.next();
-      return true;
+      __syncwarp();
+      if (lane == 0) ok = stream(true);
+      return __shfl_sync(~0u, (int)ok, 0) != 0;
     };
-    auto stream = [&](int64_t t) -> bool {
-      const T* x = r.x + t * r.ld;
-      const Span s = span_of(x, r.V);
-      const char* base = reinterpret_cast<const char*>(x + s.head);
-      const int32_t end = share(s.nvec, rank + 1, logC);
-      for (int32_t v = share(s.nvec, rank, logC); v < end; v += Shape::chunk_vecs) {
-        if (issued == slots && !mbar_wait(empty + 8 * at.slot, at.phase ^ 1, err, stop)) return false;
-        const uint32_t bytes = (uint32_t)min(end - v, (int32_t)Shape::chunk_vecs) * 16;
-        mbar_expect_tx(full + 8 * at.slot, bytes);
-        bulk_load(smem_u32(ring + at.slot * Shape::chunk_bytes), base + (int64_t)v * 16, bytes,
-                  full + 8 * at.slot);
-        at.next();
-        if (issued < slots) ++issued;
-      }
-      return true;
-    };
-    asm volatile("bar.sync 1, %0;" ::"r"(Shape::threads) : "memory");  // the list is there
+    if (listed)  // the list is there
+      asm volatile("bar.sync 1, %0;" ::"r"(Shape::threads) : "memory");
     // Rows in turn, masked ones spread among the live ones; a lane fetches what
     // the joiner needs of a row, 32 rows at a time and as many ahead.
-    const int n_live = sh->n_live, n_rows = n_live + sh->n_dead;
+    const int n_live = listed ? sh->n_live : 0, n_rows = listed ? n_live + sh->n_dead : 0;
     auto row_at = [&](int i) -> int {
       if (!listed) {
         const int64_t t = cluster + i * clusters;
@@ -480,18 +508,11 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
       const RowItem now = next;
       const int n = __popc(__ballot_sync(~0u, now.t >= 0));
       if (n == 32) next = fetch(i0 + lane);
-      for (int j = 0; j < n && ok; ++j) {
-        const int tj = __shfl_sync(~0u, now.t, j), yj = __shfl_sync(~0u, now.y, j);
-        if (!POLICY && yj < 0) continue;
-        ok = push(now, j);
-        if (ok && yj >= 0) {
-          if (lane == 0) ok = stream(tj);
-          ok = __shfl_sync(~0u, (int)ok, 0) != 0;
-        }
-      }
+      for (int j = 0; j < n && ok; ++j)
+        if (POLICY || __shfl_sync(~0u, now.y, j) >= 0) ok = hand_on(now, j);
       if (n < 32) break;
     }
-    if (ok) push({-1, -1, 0.f, 0.f, 0.f, 0.f, 0.f}, 0);
+    if (ok) hand_on({-1, -1, 0.f, 0.f, 0.f, 0.f, 0.f}, 0);
     if (lane == 0) {
       // every copy issued has to land before the CTA may end
       const uint64_t deadline = global_ns() + kWaitNs;
@@ -569,9 +590,11 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
         sh->n_live = lives > own ? (lives - own + step - 1) / step : 0;
         sh->n_dead = POLICY && deads > own ? (deads - own + step - 1) / step : 0;
       }
-      asm volatile("bar.arrive 1, %0;" ::"r"(Shape::threads) : "memory");
+      if (listed) asm volatile("bar.arrive 1, %0;" ::"r"(Shape::threads) : "memory");
+      else asm volatile("bar.arrive 1, %0;" ::"r"(Shape::threads - 32) : "memory");
     } else {
-      asm volatile("bar.sync 1, %0;" ::"r"(Shape::threads) : "memory");
+      if (listed) asm volatile("bar.sync 1, %0;" ::"r"(Shape::threads) : "memory");
+      else asm volatile("bar.sync 1, %0;" ::"r"(Shape::threads - 32) : "memory");
     }
     Place<kQueue> q;
     if (warp == W + 1) {  // ------------------------------------------ joiner
