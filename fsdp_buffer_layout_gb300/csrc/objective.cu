@@ -14,6 +14,7 @@
 #include <algorithm>
 #include <cmath>
 #include <mutex>
+#include <utility>
 
 #include "objective.cuh"
 
@@ -22,30 +23,29 @@ namespace {
 
 using namespace obj;
 
-constexpr int kRowThreads = 512;
 constexpr int kTokenThreads = 512;
 
 constexpr int kMaxPipeClusters = 1024;  // clusters whose sums the workspace holds
 
 // Workspace: the head, the pipelined kernel's sums per cluster, then per token
-// {m, s} and the gradient's coefficient, then per pair the loss and the margin.
+// {m, s, x_y} and the gradient's coefficient, then per pair the loss and the margin.
 struct ObjectiveWs {
   static constexpr size_t kFront = sizeof(WsHead) + 3 * 8 * (size_t)kMaxPipeClusters;
   WsHead* head;
   double* partial;  // [3 * kMaxPipeClusters]
-  float2* row;    // [tokens] maximum and sum of a live row
+  float4* row;    // [tokens] maximum, sum and target's logit of a live row
   float* coef;    // [tokens] a of a token; 0: no gradient
-  double* pair;   // [2 * pairs] loss and beta h of a pair
+  float2* pair;   // [pairs] loss and beta h
   static size_t bytes(int64_t tokens, int64_t pairs) {
-    return kFront + (size_t)((tokens * 12 + 15) / 16 * 16) + (size_t)pairs * 16;
+    return kFront + (size_t)((tokens * 20 + 15) / 16 * 16) + (size_t)pairs * 8;
   }
   ObjectiveWs(void* ws, int64_t tokens) {
     unsigned char* p = static_cast<unsigned char*>(ws);
     head = reinterpret_cast<WsHead*>(p);
     partial = reinterpret_cast<double*>(p + sizeof(WsHead));
-    row = reinterpret_cast<float2*>(p + kFront);
+    row = reinterpret_cast<float4*>(p + kFront);
     coef = reinterpret_cast<float*>(row + tokens);
-    pair = reinterpret_cast<double*>(p + kFront + (tokens * 12 + 15) / 16 * 16);
+    pair = reinterpret_cast<float2*>(p + kFront + (tokens * 20 + 15) / 16 * 16);
   }
 };
 
@@ -114,6 +114,23 @@ __device__ __forceinline__ float log_ratio(float d, float inv_t, float ref, LogS
   const float a = __fmaf_rn(d, inv_t, -ref);
   return __fmaf_rn(-s.k, 0.693359375f, a) - __fmaf_rn(s.k, -2.12194440e-4f, s.f);
 }
+// The same to about fp32's last bit of the difference itself, for sums over a
+// sequence: the rounding errors of the product and the two large differences
+// are kept and added (Dekker's and Knuth's exact transformations).
+__device__ __forceinline__ float exact_log_ratio(float d, float inv_t, float ref, LogSum s) {
+  const float p = __fmul_rn(d, inv_t), ep = __fmaf_rn(d, inv_t, -p);
+  auto minus = [](float a, float b, float& err) {  // a - b, and what rounding took off
+    const float v = __fsub_rn(a, b), t = __fsub_rn(v, a);
+    err = __fsub_rn(__fsub_rn(a, __fsub_rn(v, t)), __fadd_rn(b, t));
+    return v;
+  };
+  float e1, e2;
+  const float a = minus(p, ref, e1);
+  const float c = minus(a, __fmul_rn(s.k, 0.693359375f), e2);
+  const float low = __fadd_rn(__fadd_rn(ep, e1), e2);
+  // an infinite or NaN difference has no error worth keeping
+  return __fsub_rn(c, __fmaf_rn(s.k, -2.12194440e-4f, s.f)) + (low - low == 0.f ? low : 0.f);
+}
 // ln p(y) in fp64.
 __device__ __forceinline__ double log_prob(float d, float s, double inv_t) {
   const LogSum l = log_sum(s);
@@ -177,7 +194,7 @@ __device__ __forceinline__ double block_sum(double v, double* part) {
 // Policy loss of every token in one CTA, and the gradient's coefficients.
 template <typename T>
 __global__ void __launch_bounds__(kTokenThreads)
-    policy_tokens_kernel(Rows<T> r, PolicyIn p, const float2* row, float* coef, float* stats) {
+    policy_tokens_kernel(Rows<T> r, PolicyIn p, const float4* row, float* coef, float* stats) {
   __shared__ double part[kTokenThreads / 32];
   double n = 0.0;
   for (int64_t t = threadIdx.x; t < r.T_; t += kTokenThreads)
@@ -186,14 +203,13 @@ __global__ void __launch_bounds__(kTokenThreads)
   const double f = (double)p.scale / (p.mean && n != 0.0 ? n : 1.0);
   double pol = 0.0, kl = 0.0;
   for (int64_t t = threadIdx.x; t < r.T_; t += kTokenThreads) {
-    const int32_t y = live_target(r, t, nullptr);
-    if (y < 0) {
+    if (live_target(r, t, nullptr) < 0) {
       coef[t] = 0.f;
       continue;
     }
     const double w = r.weight != nullptr ? (double)r.weight[t] : 1.0;
-    const float2 ms = row[t];
-    const double lp = log_prob(to_f(r.x[t * r.ld + y]) - ms.x, ms.y, r.inv_t);
+    const float4 ms = row[t];
+    const double lp = log_prob(ms.z - ms.x, ms.y, r.inv_t);
     const PolicyTerm o =
         policy_term(p, (float)(lp - (double)p.old_logp[t]),
                     p.beta != 0.f ? (float)((double)p.ref_logp[t] - lp) : 0.f, p.adv[t]);
@@ -224,98 +240,111 @@ __device__ __forceinline__ int64_t clamp_start(int64_t v, int64_t T_) {
   return v < 0 ? 0 : v > T_ ? T_ : v;
 }
 
-// One pair a CTA: both log ratios, the loss, and its tokens' coefficients.
+// One pair a CTA: both log ratios, the loss, and its tokens' coefficients; the
+// last CTA to finish adds up the pairs, in their order. Tokens in front of the
+// first sequence and behind the last one get the coefficient 0. All in fp32 but
+// the sum over pairs: fp64 runs at a 64th of the rate here, and a version in
+// fp64 took 40 us for two pairs.
+constexpr int kPairThreads = 256;
+
+// Sums of two values over the CTA, the same in every thread.
+__device__ __forceinline__ float2 block_sum2(float a, float b, float2* part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(~0u, a, o);
+    b += __shfl_xor_sync(~0u, b, o);
+  }
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(a, b);
+  __syncthreads();
+  a = b = 0.f;
+#pragma unroll
+  for (int w = 0; w < kPairThreads / 32; ++w) {
+    a += part[w].x;
+    b += part[w].y;
+  }
+  return make_float2(a, b);
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kTokenThreads)
-    pair_kernel(Rows<T> r, PairIn p, const float2* row, float* coef, double* pair) {
-  __shared__ double part[kTokenThreads / 32];
+__global__ void __launch_bounds__(kPairThreads)
+    pair_kernel(Rows<T> r, PairIn p, const float4* row, float* coef, float2* pair, float* stats,
+                WsHead* head) {
+  __shared__ float2 part[kPairThreads / 32];
+  __shared__ bool last;
+  cudaGridDependencySynchronize();
   const int64_t q = blockIdx.x;
-  double ratio[2], length[2];
+  float ratio[2], length[2];
+  int64_t first[2], end[2];
   for (int side = 0; side < 2; ++side) {
-    const int64_t b = clamp_start(p.starts[side * p.pairs + q], r.T_);
-    const int64_t e = clamp_start(p.starts[side * p.pairs + q + 1], r.T_);
-    double d = 0.0, n = 0.0;
-    for (int64_t t = b + threadIdx.x; t < e; t += kTokenThreads) {
-      const int32_t y = live_target(r, t, nullptr);
-      if (y < 0) continue;
-      const double w = r.weight != nullptr ? (double)r.weight[t] : 1.0;
-      const float2 ms = row[t];
-      const double lp = log_prob(to_f(r.x[t * r.ld + y]) - ms.x, ms.y, r.inv_t);
-      d += w * (p.ref_logp != nullptr ? lp - (double)p.ref_logp[t] : lp);
-      n += w;
+    first[side] = clamp_start(p.starts[side * p.pairs + q], r.T_);
+    end[side] = clamp_start(p.starts[side * p.pairs + q + 1], r.T_);
+    float d = 0.f, n = 0.f;
+    for (int64_t t = first[side] + threadIdx.x; t < end[side]; t += kPairThreads) {
+      const Token k = token_at(r, t);
+      if (live_target(r, k, nullptr) < 0) continue;
+      const float4 ms = row[t];
+      d += k.w * exact_log_ratio(ms.z - ms.x, r.inv_tf, p.ref_logp != nullptr ? p.ref_logp[t] : 0.f,
+                                 log_sum(ms.y));
+      n += k.w;
     }
-    d = block_sum(d, part);
-    n = block_sum(n, part);
-    length[side] = p.average && n != 0.0 ? n : 1.0;
-    ratio[side] = d / length[side];
-    if (threadIdx.x == 0 && p.rewards != nullptr)
-      p.rewards[side * p.pairs + q] = (float)((double)p.beta * ratio[side]);
+    const float2 sum = block_sum2(d, n, part);
+    length[side] = p.average && sum.y != 0.f ? sum.y : 1.f;
+    ratio[side] = sum.x / length[side];
+    if (threadIdx.x == 0 && p.rewards != nullptr) p.rewards[side * p.pairs + q] = p.beta * ratio[side];
   }
-  const double h = ratio[0] - ratio[1];
-  double loss, slope;
+  const float h = ratio[0] - ratio[1];
+  float loss, slope;
   if (p.kind == VSF_PREF_SIGMOID) {
-    const double z = (double)p.beta * h - (double)p.margin;
-    const double tail = log1p(exp(-fabs(z)));
-    const double up = 1.0 / (1.0 + exp(-z));
-    loss = (1.0 - (double)p.smoothing) * (tail - (z > 0.0 ? 0.0 : z)) +
-           (double)p.smoothing * (tail + (z < 0.0 ? 0.0 : z));
-    slope = (double)p.beta * (up - (1.0 - (double)p.smoothing));
+    const float z = p.beta * h - p.margin;
+    const float away = expf(-fabsf(z)), tail = log1pf(away);
+    const float up = (z < 0.f ? away : 1.f) / (1.f + away);  // s(z)
+    const float down = (z < 0.f ? 1.f : away) / (1.f + away);  // 1 - s(z)
+    loss = (1.f - p.smoothing) * (tail - (z > 0.f ? 0.f : z)) +
+           p.smoothing * (tail + (z < 0.f ? 0.f : z));
+    slope = p.beta * (p.smoothing * up - (1.f - p.smoothing) * down);
   } else {
-    const double gap = h - 0.5 / (double)p.beta;
+    const float gap = h - 0.5f / p.beta;
     loss = gap * gap;
-    slope = 2.0 * gap;
+    slope = 2.f * gap;
   }
   if (threadIdx.x == 0) {
-    pair[2 * q] = loss;
-    pair[2 * q + 1] = (double)p.beta * h;
+    pair[q] = make_float2(loss, p.beta * h);
+    __threadfence();
+    last = atomicAdd(&head->ticket, 1u) + 1 == gridDim.x;
+    __threadfence();
   }
   for (int side = 0; side < 2; ++side) {
-    const int64_t b = clamp_start(p.starts[side * p.pairs + q], r.T_);
-    const int64_t e = clamp_start(p.starts[side * p.pairs + q + 1], r.T_);
-    const double a = (side ? -1.0 : 1.0) * (double)p.scale / (double)p.pairs * slope /
-                     length[side] * r.inv_t;
-    for (int64_t t = b + threadIdx.x; t < e; t += kTokenThreads)
-      coef[t] = live_target(r, t, nullptr) < 0
-                    ? 0.f
-                    : (float)(a * (r.weight != nullptr ? (double)r.weight[t] : 1.0));
+    const float a = (side ? -1.f : 1.f) * p.scale / (float)p.pairs * slope / length[side] * r.inv_tf;
+    for (int64_t t = first[side] + threadIdx.x; t < end[side]; t += kPairThreads) {
+      const Token k = token_at(r, t);
+      coef[t] = live_target(r, k, nullptr) < 0 ? 0.f : a * k.w;
+    }
   }
-}
-
-__global__ void __launch_bounds__(kTokenThreads)
-    pair_sum_kernel(const double* pair, int64_t pairs, float scale, float* stats) {
-  __shared__ double part[kTokenThreads / 32];
-  double l = 0.0, h = 0.0;
-  for (int64_t q = threadIdx.x; q < pairs; q += kTokenThreads) {
-    l += pair[2 * q];
-    h += pair[2 * q + 1];
+  if (q == 0) {
+    const int64_t b = clamp_start(p.starts[0], r.T_);
+    for (int64_t t = threadIdx.x; t < b; t += kPairThreads) coef[t] = 0.f;
+    for (int64_t t = clamp_start(p.starts[2 * p.pairs], r.T_) + threadIdx.x; t < r.T_;
+         t += kPairThreads)
+      coef[t] = 0.f;
   }
-  l = block_sum(l, part);
-  h = block_sum(h, part);
+  __syncthreads();
+  if (!last || threadIdx.x >= 32) return;
+  double l = 0.0, m = 0.0;
+  for (int64_t i = threadIdx.x; i < p.pairs; i += 32) {
+    const float2 v = __ldcg(pair + i);
+    l += (double)v.x;
+    m += (double)v.y;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    l += __shfl_xor_sync(~0u, l, o);
+    m += __shfl_xor_sync(~0u, m, o);
+  }
   if (threadIdx.x == 0) {
-    stats[0] = (float)((double)scale * l / (double)pairs);
-    stats[1] = (float)(h / (double)pairs);
-  }
-}
-
-// The gradient's rows from each row's maximum, sum and coefficient.
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads)
-    row_grad_kernel(Rows<T> r, const float2* row, const float* coef, T* grad, int64_t grad_ld) {
-  for (int64_t t = blockIdx.x; t < r.T_; t += gridDim.x) {
-    const float a = coef[t];
-    T* g = grad + t * grad_ld;
-    if (a == 0.f) {
-      for (int i = threadIdx.x; i < r.V; i += kRowThreads) g[i] = from_f<T>(0.f);
-      continue;
-    }
-    const T* x = r.x + t * r.ld;
-    const int32_t y = (int32_t)r.target[t];
-    const float2 ms = row[t];
-    const float z = finite_max(ms.x), inv_s = 1.f / ms.y;
-    for (int i = threadIdx.x; i < r.V; i += kRowThreads) {
-      const float p = exp_scaled(to_f(x[i]) - z, r.c) * inv_s;
-      g[i] = from_f<T>(i == y ? a * (1.f - p) : -a * p);
-    }
+    stats[0] = (float)((double)p.scale * l / (double)p.pairs);
+    stats[1] = (float)(m / (double)p.pairs);
+    head->ticket = 0;
   }
 }
 
@@ -387,8 +416,6 @@ Rows<T> rows_of(const RowsArg& a) {
   r.inv_t = (double)a.inv_t;
   return r;
 }
-
-unsigned row_grid(int64_t T_) { return (unsigned)std::min<int64_t>(T_, 152 * 4); }
 
 constexpr int kPipeWarps = VSF_PIPE_W;
 
@@ -478,7 +505,7 @@ cudaError_t launch_pipe(PipeArgs<T>& a, int C, cudaStream_t st) {
 }
 
 template <typename T>
-cudaError_t launch_stats(const Rows<T>& r, float2* row, float* logp, WsHead* head,
+cudaError_t launch_stats(const Rows<T>& r, float4* row, float* logp, WsHead* head,
                          cudaStream_t st) {
   if (r.T_ == 0) return cudaSuccess;
   PipeArgs<T> a = {};
@@ -489,13 +516,31 @@ cudaError_t launch_stats(const Rows<T>& r, float2* row, float* logp, WsHead* hea
   return launch_pipe<T, false>(a, pipe_split<T>(r.T_, r.V, false).C, st);
 }
 
+// A launch that may be set up while the kernel before it on the stream ends.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*fn)(P...), unsigned grid, unsigned threads, cudaStream_t st,
+                          A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, std::forward<A>(args)...);
+}
+
 template <typename T>
 cudaError_t launch_grad(const Rows<T>& r, const ObjectiveWs& w, void* grad, int64_t grad_ld,
                         cudaStream_t st) {
   if (r.T_ == 0 || grad == nullptr) return cudaSuccess;
-  row_grad_kernel<T><<<row_grid(r.T_), kRowThreads, 0, st>>>(r, w.row, w.coef,
-                                                             static_cast<T*>(grad), grad_ld);
-  return cudaGetLastError();
+  const int32_t pieces =
+      (int32_t)std::max<int64_t>(1, (r.V / Vec<T>::n + kGradPiece - 1) / kGradPiece);
+  return launch_behind(row_grad_kernel<T>, (unsigned)std::min<int64_t>(r.T_ * pieces, 152 * 4),
+                       kGradThreads, st, r, (const float4*)w.row, (const float*)w.coef,
+                       static_cast<T*>(grad), grad_ld, pieces);
 }
 
 template <typename T>
@@ -530,13 +575,9 @@ cudaError_t preference(const RowsArg& a, const PairIn& p, float* stats, float* l
                        int64_t grad_ld, const ObjectiveWs& w, cudaStream_t st) {
   const Rows<T> r = rows_of<T>(a);
   cudaError_t e = launch_stats(r, w.row, logp, w.head, st);
-  if (e == cudaSuccess && a.T_ > 0) e = cudaMemsetAsync(w.coef, 0, a.T_ * 4, st);
   if (e != cudaSuccess) return e;
-  pair_kernel<T><<<(unsigned)p.pairs, kTokenThreads, 0, st>>>(r, p, w.row, w.coef, w.pair);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  pair_sum_kernel<<<1, kTokenThreads, 0, st>>>(w.pair, p.pairs, p.scale, stats);
-  e = cudaGetLastError();
+  e = launch_behind(pair_kernel<T>, (unsigned)p.pairs, kPairThreads, st, r, p,
+                    (const float4*)w.row, w.coef, w.pair, stats, w.head);
   if (e != cudaSuccess) return e;
   return launch_grad(r, w, grad, grad_ld, st);
 }

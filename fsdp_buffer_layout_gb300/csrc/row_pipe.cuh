@@ -280,7 +280,7 @@ struct PipeArgs {
   PolicyIn p;
   T* grad;
   int64_t grad_ld;
-  float2* row;   // statistics: {m, s} of a live row, or NULL
+  float4* row;   // statistics: {m, s, x_y} of a live row, or NULL
   float* logp;
   float* stats;  // policy: fp32[4]
   WsHead* head;
@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
           sum += (double)(lane == 0 ? now.w * o.policy : lane == 1 ? now.w * o.kl : now.w);
         }
         if (lane == 0 && rank == 0) {
-          if (a.row != nullptr) a.row[now.t] = make_float2(ms.m, ms.s);
+          if (a.row != nullptr) a.row[now.t] = make_float4(ms.m, ms.s, now.xy, 0.f);
           if (a.logp != nullptr) a.logp[now.t] = log_ratio(d, r.inv_tf, 0.f, ls);
         }
       }
@@ -867,6 +867,90 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
     if (*stop != 0u) {
       const uint64_t t0 = global_ns();
       while (global_ns() - t0 < 100000ull) {
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------ gradient alone
+// The gradient's rows where a row's coefficient is known only after the sums of
+// all rows (preference loss), or its share of a cluster's shared memory is too
+// long. A thread takes eight vectors of a row at a time. Rows are taken last
+// first: the pass before read them first to last, so that the end of the logits
+// is still in L2.
+constexpr int kGradThreads = 256;
+constexpr int kGradVecs = 8;
+constexpr int kGradPiece = kGradThreads * kGradVecs;  // vectors of a row at a time
+
+template <typename T>
+__global__ void __launch_bounds__(kGradThreads, 4)
+    row_grad_kernel(const __grid_constant__ Rows<T> r, const float4* row, const float* coef,
+                    T* grad, int64_t grad_ld, int32_t pieces) {
+  constexpr int VE = Vec<T>::n;
+  cudaGridDependencySynchronize();
+  const int tid = threadIdx.x;
+  const PairScale c2 = {f2(r.c.hi, r.c.hi), f2(r.c.lo, r.c.lo)};
+  const int64_t items = r.T_ * pieces;
+  for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+    const int64_t t = r.T_ - 1 - i / pieces;
+    const int32_t piece = (int32_t)(i % pieces);
+    const int32_t y = live_target(r, t, nullptr);
+    const float a = coef[t];
+    const float4 st = row[t];
+    T* g = grad + t * grad_ld;
+    const T* x = r.x + t * r.ld;
+    const Span s = span_of(g, r.V);
+    const int32_t begin = piece * kGradPiece;
+    const int32_t end = piece + 1 == pieces ? s.nvec : min(s.nvec, begin + kGradPiece);
+    const int32_t tail = s.head + s.nvec * VE;
+    // the loose element of this thread, if any
+    int32_t loose = -1;
+    if (piece == 0 && tid < s.head) loose = tid;
+    if (piece + 1 == pieces && tid >= 16 && tail + tid - 16 < r.V) loose = tail + tid - 16;
+    uint4* out = reinterpret_cast<uint4*>(g + s.head) + tid;
+    if (y < 0 || a == 0.f) {
+      for (int32_t v = begin; v + tid < end; v += kGradThreads)
+        __stcs(out + v, make_uint4(0, 0, 0, 0));
+      if (loose >= 0) g[loose] = from_f<T>(0.f);
+      continue;
+    }
+    const float z = finite_max(st.x), b = -a / st.y;
+    if (loose >= 0) {
+      const float e = b * exp_scaled(to_f(x[loose]) - z, r.c);
+      g[loose] = from_f<T>(loose == y ? e + a : e);
+    }
+    const int32_t ye = y - s.head, yv = ye / VE;
+    const bool mine = ye >= 0 && yv >= begin && yv < end;  // the target is in this piece
+    if (((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0) {
+      const bool near = sizeof(T) == 2 && fabsf(z) < 1e30f;
+      const F2 nm = f2(-z, -z), b2 = f2(b, b), c0 = f2(r.c.hi, r.c.hi);
+      const F2 kk = f2(-z * r.c.hi, -z * r.c.hi);
+      const uint4* in = reinterpret_cast<const uint4*>(x + s.head) + tid;
+      for (int32_t v = begin; v < end; v += kGradPiece) {
+        uint4 q[kGradVecs];
+#pragma unroll
+        for (int j = 0; j < kGradVecs; ++j)
+          if (v + j * kGradThreads + tid < end) q[j] = __ldcs(in + v + j * kGradThreads);
+#pragma unroll
+        for (int j = 0; j < kGradVecs; ++j) {
+          if (v + j * kGradThreads + tid >= end) break;
+          Pairs<T> e;
+          unpack(q[j], e);
+          float o[VE];
+#pragma unroll
+          for (int k = 0; k < VE / 2; ++k)
+            f2_get(f2_mul(near ? exp2_pair(f2_fma(e.p[k], c0, kk)) : exp_pair(e.p[k], nm, c2), b2),
+                   o[2 * k], o[2 * k + 1]);
+          __stcs(out + v + j * kGradThreads, pack_vec<T>(o));
+        }
+      }
+      if (mine && tid == ((yv - begin) & (kGradThreads - 1)))
+        g[y] = from_f<T>(b * exp_scaled(st.z - z, r.c) + a);
+    } else {
+      const int32_t first = s.head + begin * VE, n = (end - begin) * VE;
+      for (int32_t k = tid; k < n; k += kGradThreads) {
+        const float e = b * exp_scaled(to_f(x[first + k]) - z, r.c);
+        g[first + k] = from_f<T>(first + k == y ? e + a : e);
       }
     }
   }

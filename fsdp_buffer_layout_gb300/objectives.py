@@ -111,14 +111,20 @@ class _LogitsLoss(_Objective):
         self.logp = self._new(self.tokens)
         self._out = self.stats.data_ptr(), self.logp.data_ptr()
         self.grad = None
-        # The gradient's rows start at the same places modulo 16 bytes as those
-        # of logits with aligned or adjacent rows, so both go in wide pieces.
-        self._pad = -self.width % (16 // self.dtype.itemsize)
+        # The gradient's rows lie as far apart, modulo 16 bytes, as the logits',
+        # so that both go in wide pieces.
+        self._step = 16 // self.dtype.itemsize
+        self._views = {}
         if with_grad:
-            self._buffer = self._new(self.tokens * (self.width + self._pad), dtype=self.dtype)
-            self._views = {p: self._buffer.as_strided((self.tokens, self.width),
-                                                      (self.width + p, 1)) for p in (0, self._pad)}
-            self.grad = self._views[self._pad]
+            self._buffer = self._new(self.tokens * (self.width + self._step - 1), dtype=self.dtype)
+            self._grad_at = self._buffer.data_ptr()
+            self.grad = self._view(-self.width % self._step)
+
+    def _view(self, pad: int):
+        if pad not in self._views:
+            self._views[pad] = self._buffer.as_strided((self.tokens, self.width),
+                                                       (self.width + pad, 1))
+        return self._views[pad]
 
     def _grad(self, n: int, ld: int, grad):
         """The gradient's tensor, address and row stride of a call."""
@@ -129,8 +135,8 @@ class _LogitsLoss(_Objective):
             return grad, grad.data_ptr(), grad_ld
         if self.grad is None:
             return None, None, self.width
-        pad = 0 if ld == self.width else self._pad
-        return self._first(self._views[pad], n), self._buffer.data_ptr(), self.width + pad
+        pad = (ld - self.width) % self._step
+        return self._first(self._view(pad), n), self._grad_at, self.width + pad
 
 
 class PolicyLoss(_LogitsLoss):
