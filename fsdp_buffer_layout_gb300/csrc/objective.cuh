@@ -23,7 +23,7 @@ struct WsHead {
   uint32_t ticket;  // CTAs of the running launch that have finished
   uint32_t nan;     // a NaN score was seen (router)
   uint32_t pad;
-  double acc[6];
+  float part[12];   // parts of a loss
 };
 static_assert(sizeof(WsHead) == 64, "the head is four 16-byte words");
 

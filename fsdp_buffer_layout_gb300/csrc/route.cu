@@ -11,7 +11,9 @@
 //   logits:  d x_e  = s_e (d s_e - sum_j s_j d s_j)              softmax
 //                   = s_e (1 - s_e) d s_e                        sigmoid
 //
-// A warp takes a token; lane l holds experts l, l + 32, ... in registers.
+// A group of L lanes (8, 16 or a warp) takes a token; lane l of it holds the
+// experts l, l + L, ... in registers. A CTA takes a run of tokens, one sequence
+// of it after the other, so that the sequence's sums stay in registers.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -31,7 +33,7 @@ constexpr int kMaxTopK = 32;
 constexpr int64_t kMaxExperts = 512;
 // Sums of shares are kept in fixed point, 2^-40 a unit: integer additions
 // give the same sum in any order. A share is at most 1, so 2^23 tokens fit.
-constexpr double kShareUnit = 1099511627776.0;
+constexpr float kShareUnit = 1099511627776.f;
 
 struct RouteIn {
   int64_t T_, ld, sequences;
@@ -40,20 +42,43 @@ struct RouteIn {
   const float* bias;
   const uint8_t* live;
   const int64_t* starts;  // NULL: one sequence of T_ tokens
+  Log2Scale c;
 };
 
-// The sequence that holds token t, or -1: the last one that starts at or
-// before t. Always below `sequences`, whatever the starts hold.
-__device__ __forceinline__ int64_t sequence_of(const RouteIn& p, int64_t t) {
-  if (p.starts == nullptr) return 0;
-  int64_t lo = 0, hi = p.sequences;  // starts[lo] <= t < starts[hi], if any
-  if (t < p.starts[0] || t >= p.starts[p.sequences]) return -1;
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) / 2;
-    if (p.starts[mid] <= t) lo = mid; else hi = mid;
+// The sequences of a run of tokens [pos, end), in turn. Tokens in front of the
+// first start have sequence -1, those behind the last one `sequences`. Whatever
+// the starts hold, every token comes once and the walk ends.
+struct Walk {
+  int64_t pos, end, seq, stop;  // tokens [pos, stop) belong to seq
+  __device__ __forceinline__ void bound(const RouteIn& p) {
+    const int64_t v = p.starts == nullptr || seq >= p.sequences ? end : p.starts[seq + 1];
+    stop = v < pos ? pos : v > end ? end : v;
   }
-  return lo;
-}
+  __device__ __forceinline__ void settle(const RouteIn& p) {  // on to one with tokens
+    for (bound(p); stop == pos && pos < end; bound(p)) ++seq;
+  }
+  __device__ __forceinline__ Walk(const RouteIn& p, int64_t first, int64_t last)
+      : pos(first), end(last), seq(0) {
+    if (p.starts != nullptr) {
+      int64_t lo = -1, hi = p.sequences + 1;  // starts[lo] <= pos < starts[hi]
+      while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) / 2;
+        if (p.starts[mid] <= pos) lo = mid; else hi = mid;
+      }
+      seq = lo;
+    }
+    settle(p);
+  }
+  __device__ __forceinline__ bool done() const { return pos >= end; }
+  __device__ __forceinline__ bool inside(const RouteIn& p) const {
+    return seq >= 0 && seq < p.sequences;
+  }
+  __device__ __forceinline__ void next(const RouteIn& p) {
+    pos = stop;
+    ++seq;
+    settle(p);
+  }
+};
 
 // Order-preserving 32-bit key of a float: larger is better, -0 equals +0,
 // NaN comes after every number. 0 is below every key.
@@ -63,274 +88,462 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+template <int L>
+__device__ __forceinline__ float group_max(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
+  for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
   return v;
 }
 
-// Scores of a token's experts from its logits, in place; returns Z.
-template <int N>
-__device__ __forceinline__ float scores(float (&x)[N], int32_t E, int32_t score, int lane) {
-  if (score == VSF_SCORE_SOFTMAX) {
-    float m = -INFINITY;
+// 1 / (1 + exp(-x)): ex2.approx and rcp.approx, within 4 ulp together.
+__device__ __forceinline__ float sigmoid(float x, Log2Scale c) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp_scaled(-x, c)));
+  return r;
+}
+
+// A token's scores: max and 1 / sum of the softmax, or nothing, and from them
+// the score of one logit.
+struct Norm {
+  float m, inv;
+};
+template <int L, int N>
+__device__ __forceinline__ Norm scores(float (&x)[N], const RouteIn& p, int lane, float& z) {
+  Norm n = {0.f, 1.f};
+  if (p.score == VSF_SCORE_SOFTMAX) {
+    float m = x[0];
 #pragma unroll
-    for (int j = 0; j < N; ++j) m = fmaxf(m, x[j]);
-    m = warp_max(m);
-    float z = 0.f;
+    for (int j = 1; j < N; ++j) m = fmaxf(m, x[j]);
+    n.m = group_max<L>(m);
+    float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      x[j] = lane + 32 * j < E ? expf(x[j] - m) : 0.f;
-      z += x[j];
+      x[j] = exp_scaled(x[j] - n.m, p.c);
+      if (lane + L * j >= p.E) x[j] = 0.f;
+      sum += x[j];
     }
-    z = warp_sum(z);
+    n.inv = 1.f / group_sum<L>(sum);
 #pragma unroll
-    for (int j = 0; j < N; ++j) x[j] = x[j] / z;
-    return 1.f;
+    for (int j = 0; j < N; ++j) x[j] *= n.inv;
+    z = 1.f;
+    return n;
   }
-  float z = 0.f;
+  float sum = 0.f;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    x[j] = lane + 32 * j < E ? 1.f / (1.f + expf(-x[j])) : 0.f;
-    z += x[j];
+    x[j] = lane + L * j < p.E ? sigmoid(x[j], p.c) : 0.f;
+    sum += x[j];
   }
-  return warp_sum(z) + 1e-20f;
+  z = group_sum<L>(sum) + 1e-20f;
+  return n;
+}
+__device__ __forceinline__ float score_of(float x, Norm n, const RouteIn& p) {
+  return p.score == VSF_SCORE_SOFTMAX ? exp_scaled(x - n.m, p.c) * n.inv : sigmoid(x, p.c);
 }
 
-template <typename T, int N>
+template <typename T, int L, int N>
 __device__ __forceinline__ void load_token(float (&x)[N], const T* row, int32_t E, int lane) {
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    const int e = lane + 32 * j;
+    const int e = lane + L * j;
     x[j] = e < E ? to_f(row[e]) : -INFINITY;
   }
 }
 
-template <typename T, int N>
-__global__ void __launch_bounds__(kRouteThreads)
-    route_kernel(const T* logits, RouteIn p, int32_t* idx, float* gates, int32_t* seq_counts,
-                 unsigned long long* seq_share, int32_t* seq_tokens, WsHead* head) {
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * kRouteWarps;
-  for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5); t < p.T_; t += warps) {
-    if (p.live != nullptr && p.live[t] == 0) {
-      for (int k = lane; k < p.K; k += 32) {
-        idx[t * p.K + k] = -1;
-        gates[t * p.K + k] = 0.f;
+// The K experts of largest key, best first, ties to the lowest; lane k of the
+// group gets the k-th. Keys are lost. Round by round, the group's largest key
+// is found and taken out.
+template <int L, int N>
+__device__ __forceinline__ int choose_rounds(uint32_t (&key)[N], int K, int lane, uint32_t mask) {
+  int mine = -1;
+  for (int k = 0; k < K; ++k) {
+    uint32_t best = key[0];
+    int be = lane;
+#pragma unroll
+    for (int j = 1; j < N; ++j)
+      if (key[j] > best) {
+        best = key[j];
+        be = lane + L * j;
       }
-      continue;
-    }
-    float x[N];
-    uint32_t key[N];
-    load_token(x, logits + t * p.ld, p.E, lane);
-    if (p.bias == nullptr) {
-#pragma unroll
-      for (int j = 0; j < N; ++j) key[j] = order_key(x[j]);
-    }
-    const float z = scores(x, p.E, p.score, lane);
-    if (p.bias != nullptr) {
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (lane + 32 * j < p.E) key[j] = order_key(x[j] + p.bias[lane + 32 * j]);
-    }
+    const uint32_t top = __reduce_max_sync(mask, best);
+    const int e = (int)__reduce_min_sync(mask, best == top ? (uint32_t)be : 0xffffffffu);
 #pragma unroll
     for (int j = 0; j < N; ++j)
-      if (lane + 32 * j >= p.E) key[j] = 0u;
-    const int64_t seq = sequence_of(p, t);
-    float mine = 0.f, sum = 0.f;  // lane k keeps choice k's score
-    int chosen = -1;
-    for (int k = 0; k < p.K; ++k) {
-      uint32_t best = 0;
-      int be = INT32_MAX;
-      float bs = 0.f;
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (key[j] > best) {
-          best = key[j];
-          be = lane + 32 * j;
-          bs = x[j];
-        }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const uint32_t ok = __shfl_xor_sync(~0u, best, o);
-        const int oe = __shfl_xor_sync(~0u, be, o);
-        const float os = __shfl_xor_sync(~0u, bs, o);
-        if (ok > best || (ok == best && oe < be)) {
-          best = ok;
-          be = oe;
-          bs = os;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (lane + 32 * j == be) key[j] = 0u;
-      if (lane == k) {
-        chosen = be;
-        mine = bs;
-      }
-      sum += bs;
-    }
-    if (lane < p.K) {
-      idx[t * p.K + lane] = chosen;
-      gates[t * p.K + lane] = p.renorm ? p.scale * mine / (sum + 1e-20f) : p.scale * mine;
-      if (seq >= 0) atomicAdd(&seq_counts[seq * p.E + chosen], 1);
-    }
-    if (seq >= 0) {
-      bool bad = false;
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int e = lane + 32 * j;
-        if (e >= p.E) continue;
-        const float q = x[j] / z;
-        bad |= q != q;
-        if (q > 0.f)
-          atomicAdd(&seq_share[seq * p.E + e], (unsigned long long)((double)q * kShareUnit + 0.5));
-      }
-      if (bad) head->nan = 1u;
-      if (lane == 0) atomicAdd(&seq_tokens[seq], 1);
-    }
+      if (lane + L * j == e) key[j] = 0u;
+    if (lane == k) mine = e;
   }
+  return mine;
 }
 
-// Counts over all sequences, the sequences' coefficients and the balance loss.
-__global__ void __launch_bounds__(512)
-    route_finish_kernel(RouteIn p, const int32_t* seq_counts, const unsigned long long* seq_share,
-                        const int32_t* seq_tokens, int32_t* counts, float* seq_coef, float* loss,
-                        WsHead* head) {
-  __shared__ double part[16];
-  __shared__ int full;  // sequences with a live token
-  if (threadIdx.x == 0) full = 0;
-  __syncthreads();
+// The same with fewer instructions where a lane holds several keys: the K-th
+// largest of the lanes' largest keys bounds the choice from below; the few
+// candidates from it on go to a lane each, and the rounds look at one key a
+// lane. More than 32 candidates (many equal keys) take the rounds above.
+template <int N>
+__device__ __forceinline__ int choose(uint32_t (&key)[N], int K, int lane, uint2* cand) {
+  if (N == 1) return choose_rounds<32, N>(key, K, lane, ~0u);
+  uint32_t lane_max = key[0];
+#pragma unroll
+  for (int j = 1; j < N; ++j) lane_max = max(lane_max, key[j]);
+  uint32_t bound = 0;
+  for (int n = 0; n < K;) {
+    bound = __reduce_max_sync(~0u, lane_max);
+    const bool hit = lane_max == bound;
+    n += __popc(__ballot_sync(~0u, hit));
+    if (hit) lane_max = 0u;
+  }
+  // a bound of 0 means fewer lanes with experts than choices
+  int n = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const bool in = key[j] >= bound && key[j] != 0u;
+    const uint32_t all = __ballot_sync(~0u, in);
+    const int at = n + __popc(all & ((1u << lane) - 1));
+    if (in && at < 32) cand[at] = make_uint2(key[j], (uint32_t)(lane + 32 * j));
+    n += __popc(all);
+  }
+  if (n > 32) return choose_rounds<32, N>(key, K, lane, ~0u);
+  __syncwarp();
+  uint2 c = lane < n ? cand[lane] : make_uint2(0u, 0u);  // in the order of the experts
+  __syncwarp();
+  int mine = -1;
+  for (int k = 0; k < K; ++k) {
+    const uint32_t top = __reduce_max_sync(~0u, c.x);
+    const int who = __ffs(__ballot_sync(~0u, c.x == top)) - 1;
+    const int e = (int)__shfl_sync(~0u, c.y, who);
+    if (lane == who) c.x = 0u;
+    if (lane == k) mine = e;
+  }
+  return mine;
+}
+
+// Sums of the calls' workspace, zero between calls.
+struct RouteSums {
+  int32_t* tokens;            // [sequences] live tokens
+  int32_t* count;             // [sequences * E] choices
+  unsigned long long* share;  // [sequences * E] sums of shares
+};
+
+struct RouteOut {
+  int32_t* idx;
+  float* gates;
+  int32_t* counts;
+  float* loss;
+  int32_t* seq_counts;
+  float* seq_coef;
+};
+
+// Experts [e0, e0 + en) of all sequences: copies the counts out, adds up their
+// totals, the balance loss and (first part) the sequences' coefficients, and
+// zeroes the sums. A thread keeps to one expert and every G-th sequence. The
+// loss of this part goes to thread 0.
+__device__ float route_finish(const RouteIn& p, const RouteSums& w, const RouteOut& o, int e0,
+                              int en, bool first) {
+  __shared__ int total[kMaxExperts];
+  __shared__ float part[kRouteWarps];
+  const int tid = threadIdx.x;
+  for (int e = tid; e < en; e += kRouteThreads) total[e] = 0;
   int mine = 0;
-  for (int64_t s = threadIdx.x; s < p.sequences; s += 512) mine += seq_tokens[s] > 0;
-  if (mine) atomicAdd(&full, mine);
-  __syncthreads();
-  for (int64_t s = threadIdx.x; s < p.sequences; s += 512) {
-    const double n = seq_tokens[s];
-    seq_coef[s] = n > 0 ? (float)((double)p.balance * p.E / (p.K * n * n * full)) : 0.f;
+  for (int64_t s = tid; s < p.sequences; s += kRouteThreads) mine += __ldcg(w.tokens + s) > 0;
+  // (sequences with a live token; also orders total[] before its use)
+  int full = 0;
+  {
+    __shared__ int sum;
+    if (tid == 0) sum = 0;
+    __syncthreads();
+    if (mine) atomicAdd(&sum, mine);
+    __syncthreads();
+    full = sum;
   }
-  double l = 0.0;
-  for (int e = threadIdx.x; e < p.E; e += 512) {
+  const float f = full > 0 ? p.balance * (float)p.E / ((float)p.K * (float)full) : 0.f;
+  int width = 1;  // threads side by side on the experts
+  while (width < en && width < kRouteThreads) width *= 2;
+  const int G = kRouteThreads / width;
+  float l = 0.f;
+  for (int e = tid & (width - 1); e < en; e += width) {
     int c = 0;
-    for (int64_t s = 0; s < p.sequences; ++s) {
-      const int n_se = seq_counts[s * p.E + e];
-      c += n_se;
-      if (n_se) {
-        const double n = seq_tokens[s];
-        l += (double)p.balance * p.E / (p.K * n * n * full) * n_se *
-             ((double)seq_share[s * p.E + e] / kShareUnit);
+#pragma unroll 4
+    for (int64_t s = tid / width; s < p.sequences; s += G) {
+      const int64_t at = s * p.E + e0 + e;
+      const int n = __ldcg(w.count + at);
+      const unsigned long long share = __ldcg(w.share + at);
+      const float t = (float)__ldcg(w.tokens + s);
+      o.seq_counts[at] = n;
+      w.count[at] = 0;
+      w.share[at] = 0ull;
+      c += n;
+      if (n) l += f / (t * t) * ((float)n * ((float)share / kShareUnit));
+    }
+    if (G == 1) total[e] = c;
+    else if (c) atomicAdd(&total[e], c);
+  }
+  if (first)
+    for (int64_t s = tid; s < p.sequences; s += kRouteThreads) {
+      const float t = (float)__ldcg(w.tokens + s);
+      o.seq_coef[s] = t > 0.f ? f / (t * t) : 0.f;
+    }
+  l = group_sum<32>(l);
+  if ((tid & 31) == 0) part[tid >> 5] = l;
+  __syncthreads();
+  for (int e = tid; e < en; e += kRouteThreads) o.counts[e0 + e] = total[e];
+  l = 0.f;
+  for (int i = 0; i < kRouteWarps; ++i) l += part[i];
+  return l;
+}
+
+template <typename T, int L, int N>
+__global__ void __launch_bounds__(kRouteThreads, N <= 8 ? 4 : 2)
+    route_kernel(const T* logits, const __grid_constant__ RouteIn p,
+                 const __grid_constant__ RouteSums w, const __grid_constant__ RouteOut o,
+                 WsHead* head, int32_t finish) {
+  constexpr int kGroups = kRouteThreads / L;
+  __shared__ float share[kGroups][N * L];  // sums of shares of each group
+  __shared__ int32_t count[N * L];         // choices of the CTA
+  __shared__ uint2 cand[kRouteWarps][32];  // candidates of a token's choice
+  __shared__ int tokens, last;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & (L - 1), group = tid / L;
+  const uint32_t mask = L == 32 ? ~0u : ((1u << (L & 31)) - 1) << ((tid & 31) & ~(L - 1));
+  for (int e = tid; e < N * L; e += kRouteThreads) count[e] = 0;
+  if (tid == 0) tokens = 0;
+  __syncthreads();
+  const int64_t per = (p.T_ + gridDim.x - 1) / gridDim.x;
+  const int64_t from = min((int64_t)blockIdx.x * per, p.T_);
+  for (Walk run(p, from, min(from + per, p.T_)); !run.done(); run.next(p)) {
+    const bool counted = run.inside(p);
+    float acc[N];
+    int seen = 0;
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[j] = 0.f;
+    // the groups of a warp go round together: shuffles span them
+    for (int64_t t0 = run.pos + warp * (32 / L); t0 < run.stop; t0 += kGroups) {
+      const int64_t t = t0 + (tid & 31) / L;
+      const bool in = t < run.stop;
+      const bool on = in && (p.live == nullptr || p.live[t] != 0);
+      const T* row = logits + (on ? t : run.pos) * p.ld;
+      float x[N];
+      uint32_t key[N];
+      load_token<T, L>(x, row, on ? p.E : 0, lane);
+      if (p.bias == nullptr) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) key[j] = order_key(x[j]);
+      }
+      float z;
+      const Norm norm = scores<L>(x, p, lane, z);
+      if (p.bias != nullptr) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          key[j] = lane + L * j < p.E ? order_key(x[j] + p.bias[lane + L * j]) : 0u;
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (lane + L * j >= p.E) key[j] = 0u;
+      const int chosen = L == 32 && N > 1 ? choose<N>(key, p.K, lane, cand[warp])
+                                          : choose_rounds<L, N>(key, p.K, lane, mask);
+      float score = 0.f;
+      if (on && lane < p.K) score = score_of(to_f(row[chosen]), norm, p);
+      const float sum = group_sum<L>(score) + 1e-20f;
+      if (in && lane < p.K) {
+        o.idx[t * p.K + lane] = on ? chosen : -1;
+        o.gates[t * p.K + lane] = on ? (p.renorm ? p.scale * score / sum : p.scale * score) : 0.f;
+        if (on && counted) atomicAdd(&count[chosen], 1);
+      }
+      if (on && counted) {
+        const float inv = 1.f / z;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const float q = x[j] * inv;
+          bad |= q != q;
+          acc[j] += q;
+        }
+        ++seen;
       }
     }
-    counts[e] = c;
-  }
+    if (!counted) continue;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = l;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    l = 0.0;
-    for (int w = 0; w < 16; ++w) l += part[w];
-    *loss = head->nan ? NAN : (float)l;
+    for (int j = 0; j < N; ++j) share[group][lane + L * j] = acc[j];
+    if (lane == 0 && seen > 0) atomicAdd(&tokens, seen);
+    if (bad) head->nan = 1u;
+    __syncthreads();
+    for (int e = tid; e < p.E; e += kRouteThreads) {
+      float q = 0.f;
+      for (int g = 0; g < kGroups; ++g) q += share[g][e];
+      const int64_t at = run.seq * p.E + e;
+      if (q > 0.f) atomicAdd(w.share + at, (unsigned long long)__float2ull_rn(q * kShareUnit));
+      if (count[e] > 0) atomicAdd(w.count + at, count[e]);
+      count[e] = 0;
+    }
+    if (tid == 0) {
+      if (tokens > 0) atomicAdd(w.tokens + run.seq, tokens);
+      tokens = 0;
+    }
+    __syncthreads();
+  }
+  if (!finish) return;
+  if (gridDim.x > 1) {  // the last CTA finishes
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+      last = atomicAdd(&head->ticket, 1u) + 1 == gridDim.x;
+      __threadfence();
+    }
+    __syncthreads();
+    if (!last) return;
+  }
+  const float l = route_finish(p, w, o, 0, p.E, true);
+  for (int64_t s = tid; s < p.sequences; s += kRouteThreads) w.tokens[s] = 0;
+  if (tid == 0) {
+    *o.loss = __ldcg(&head->nan) ? NAN : l;
     head->nan = 0u;
+    head->ticket = 0u;
   }
 }
 
-template <typename T, int N>
+// The finish as a launch of its own, for many sequences: 64 experts a CTA.
+constexpr int kFinishExperts = 64;
 __global__ void __launch_bounds__(kRouteThreads)
-    route_grad_kernel(const T* logits, RouteIn p, const int32_t* idx, const float* d_gates,
-                      const int32_t* seq_counts, const float* seq_coef, float loss_scale, T* grad,
-                      int64_t grad_ld) {
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * kRouteWarps;
-  for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5); t < p.T_; t += warps) {
-    T* g = grad + t * grad_ld;
-    if (p.live != nullptr && p.live[t] == 0) {
-      for (int e = lane; e < p.E; e += 32) g[e] = from_f<T>(0.f);
-      continue;
-    }
-    float x[N], ds[N];
-    load_token(x, logits + t * p.ld, p.E, lane);
-    const float z = scores(x, p.E, p.score, lane);
+    route_finish_kernel(const __grid_constant__ RouteIn p, const __grid_constant__ RouteSums w,
+                        const __grid_constant__ RouteOut o, WsHead* head) {
+  __shared__ int last;
+  const int e0 = blockIdx.x * kFinishExperts, tid = threadIdx.x;
+  const float l = route_finish(p, w, o, e0, min(kFinishExperts, p.E - e0), blockIdx.x == 0);
+  if (tid == 0) {
+    head->part[blockIdx.x] = l;
+    __threadfence();
+    last = atomicAdd(&head->ticket, 1u) + 1 == gridDim.x;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!last) return;
+  for (int64_t s = tid; s < p.sequences; s += kRouteThreads) w.tokens[s] = 0;
+  if (tid == 0) {
+    float sum = 0.f;
+    for (uint32_t i = 0; i < gridDim.x; ++i) sum += __ldcg(&head->part[i]);
+    *o.loss = __ldcg(&head->nan) ? NAN : sum;
+    head->nan = 0u;
+    head->ticket = 0u;
+  }
+}
+
+template <typename T, int L, int N>
+__global__ void __launch_bounds__(kRouteThreads, N <= 8 ? 4 : 2)
+    route_grad_kernel(const T* logits, const __grid_constant__ RouteIn p, const int32_t* idx,
+                      const float* d_gates, const int32_t* seq_counts, const float* seq_coef,
+                      float loss_scale, T* grad, int64_t grad_ld) {
+  constexpr int kGroups = kRouteThreads / L;
+  __shared__ float pulled[kGroups][N * L];  // the gates' pull on each score; zero between tokens
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & (L - 1);
+  float* pull = pulled[tid / L];
 #pragma unroll
-    for (int j = 0; j < N; ++j) ds[j] = 0.f;
-    if (d_gates != nullptr) {
-      const int mine = lane < p.K ? idx[t * p.K + lane] : -1;
-      const float dg = lane < p.K ? d_gates[t * p.K + lane] : 0.f;
-      float picked = 0.f;  // lane k: the score of choice k
-      for (int k = 0; k < p.K; ++k) {
-        const int e = __shfl_sync(~0u, mine, k);
-        float v = 0.f;
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-          if (e >= 0 && (e >> 5) == j) v = x[j];
-        v = __shfl_sync(~0u, v, e & 31);
-        if (lane == k && e >= 0 && e < p.E) picked = v;
-      }
-      float pull = dg;
-      if (p.renorm) {
-        const float down = warp_sum(picked) + 1e-20f;
-        const float dot = warp_sum(dg * picked) / down;
-        pull = (dg - dot) / down;
-      }
-      pull *= p.scale;
-      for (int k = 0; k < p.K; ++k) {
-        const int e = __shfl_sync(~0u, mine, k);
-        const float v = __shfl_sync(~0u, pull, k);
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-          if (lane + 32 * j == e) ds[j] = v;
-      }
-    }
-    const int64_t seq = sequence_of(p, t);
-    if (seq >= 0 && loss_scale != 0.f) {
-      const float f = loss_scale * seq_coef[seq];
-      float b[N], dot = 0.f;
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int e = lane + 32 * j;
-        b[j] = e < p.E ? f * (float)seq_counts[seq * p.E + e] : 0.f;
-        dot += b[j] * x[j];
-      }
-      if (p.score == VSF_SCORE_SIGMOID) dot = warp_sum(dot) / z;
-      else dot = 0.f;
-#pragma unroll
-      for (int j = 0; j < N; ++j) ds[j] += (b[j] - dot) / z;
-    }
-    float dot = 0.f;
-    if (p.score == VSF_SCORE_SOFTMAX) {
-#pragma unroll
-      for (int j = 0; j < N; ++j) dot += x[j] * ds[j];
-      dot = warp_sum(dot);
-    }
+  for (int j = 0; j < N; ++j) pull[lane + L * j] = 0.f;
+  __syncwarp();
+  const int64_t per = (p.T_ + gridDim.x - 1) / gridDim.x;
+  const int64_t from = min((int64_t)blockIdx.x * per, p.T_);
+  for (Walk run(p, from, min(from + per, p.T_)); !run.done(); run.next(p)) {
+    float b[N];  // the balance loss's pull on each share
+    const bool balanced = run.inside(p) && loss_scale != 0.f;
+    const float f = balanced ? loss_scale * seq_coef[run.seq] : 0.f;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int e = lane + 32 * j;
-      if (e < p.E)
-        g[e] = from_f<T>(p.score == VSF_SCORE_SOFTMAX ? x[j] * (ds[j] - dot)
-                                                      : x[j] * (1.f - x[j]) * ds[j]);
+      const int e = lane + L * j;
+      b[j] = balanced && e < p.E ? f * (float)seq_counts[run.seq * p.E + e] : 0.f;
+    }
+    for (int64_t t0 = run.pos + warp * (32 / L); t0 < run.stop; t0 += kGroups) {
+      const int64_t t = t0 + (tid & 31) / L;
+      const bool in = t < run.stop;
+      const bool on = in && (p.live == nullptr || p.live[t] != 0);
+      const T* row = logits + (on ? t : run.pos) * p.ld;
+      float x[N];
+      load_token<T, L>(x, row, on ? p.E : 0, lane);
+      int e = -1;
+      float dg = 0.f, xe = 0.f;
+      if (on && d_gates != nullptr && lane < p.K) {
+        e = idx[t * p.K + lane];
+        if (e < 0 || e >= p.E) e = -1;
+        if (e >= 0) {
+          dg = d_gates[t * p.K + lane];
+          xe = to_f(row[e]);
+        }
+      }
+      float z;
+      const Norm norm = scores<L>(x, p, lane, z);
+      float ds[N];
+      if (d_gates != nullptr) {
+        float v = dg;
+        if (p.renorm) {
+          const float s = e >= 0 ? score_of(xe, norm, p) : 0.f;
+          const float inv = 1.f / (group_sum<L>(s) + 1e-20f);
+          v = (dg - group_sum<L>(dg * s) * inv) * inv;
+        }
+        if (e >= 0) pull[e] = p.scale * v;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < N; ++j) ds[j] = pull[lane + L * j];
+        __syncwarp();
+        if (e >= 0) pull[e] = 0.f;
+        __syncwarp();
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) ds[j] = 0.f;
+      }
+      const float inv = 1.f / z;
+      float dot = 0.f;
+      if (p.score == VSF_SCORE_SOFTMAX) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          ds[j] += b[j];
+          dot += x[j] * ds[j];
+        }
+        dot = group_sum<L>(dot);
+      } else if (balanced) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) dot += b[j] * x[j];
+        dot = group_sum<L>(dot) * inv;
+#pragma unroll
+        for (int j = 0; j < N; ++j) ds[j] += (b[j] - dot) * inv;
+      }
+      if (!in) continue;
+      T* g = grad + t * grad_ld;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int at = lane + L * j;
+        if (at < p.E) {
+          const float v = p.score == VSF_SCORE_SOFTMAX ? x[j] * (ds[j] - dot)
+                                                       : x[j] * (1.f - x[j]) * ds[j];
+          g[at] = from_f<T>(on ? v : 0.f);
+        }
+      }
     }
   }
 }
 
 // ------------------------------------------------------------- host side
 struct RouteWs {
-  WsHead* head;
-  int32_t* tokens;             // [sequences] live tokens
-  unsigned long long* share;   // [sequences * E] sums of shares
   static size_t tokens_bytes(int64_t sequences) { return (size_t)((sequences * 4 + 15) / 16 * 16); }
-  static size_t bytes(int64_t E, int64_t sequences) {
-    return sizeof(WsHead) + tokens_bytes(sequences) + (size_t)(E * sequences) * 8;
+  static size_t count_bytes(int64_t E, int64_t sequences) {
+    return (size_t)((E * sequences * 4 + 15) / 16 * 16);
   }
-  RouteWs(void* ws, int64_t sequences) {
+  static size_t bytes(int64_t E, int64_t sequences) {
+    return sizeof(WsHead) + tokens_bytes(sequences) + count_bytes(E, sequences) +
+           (size_t)(E * sequences) * 8;
+  }
+  WsHead* head;
+  RouteSums sums;
+  RouteWs(void* ws, int64_t E, int64_t sequences) {
     unsigned char* b = static_cast<unsigned char*>(ws);
     head = reinterpret_cast<WsHead*>(b);
-    tokens = reinterpret_cast<int32_t*>(b + sizeof(WsHead));
-    share = reinterpret_cast<unsigned long long*>(b + sizeof(WsHead) + tokens_bytes(sequences));
+    b += sizeof(WsHead);
+    sums.tokens = reinterpret_cast<int32_t*>(b);
+    b += tokens_bytes(sequences);
+    sums.count = reinterpret_cast<int32_t*>(b);
+    b += count_bytes(E, sequences);
+    sums.share = reinterpret_cast<unsigned long long*>(b);
   }
 };
 
@@ -355,49 +568,66 @@ vsf_status check_route(const char* who, const void* logits, int32_t dtype, int64
 RouteIn route_in(int64_t T_, int64_t E, int64_t ld, const float* bias, const uint8_t* live,
                  const int64_t* starts, int64_t sequences, const vsf_route_hparams* hp) {
   return {T_, ld, sequences, (int32_t)E, hp->top_k, hp->score, hp->renorm != 0,
-          hp->route_scale, hp->balance, bias, live, starts};
+          hp->route_scale, hp->balance, bias, live, starts, log2_scale(1.f)};
 }
 
+// CTAs: two tokens a group at least, 4 CTAs an SM at most (2 with more than
+// 256 experts: registers).
+template <int L, int N>
 unsigned route_grid(int64_t T_) {
-  return (unsigned)std::min<int64_t>((T_ + kRouteWarps - 1) / kRouteWarps, 152 * 8);
+  const int64_t least = 2 * kRouteThreads / L;
+  return (unsigned)std::max<int64_t>(
+      1, std::min<int64_t>((T_ + least - 1) / least, 152 * (N <= 8 ? 4 : 2)));
 }
 
-template <typename T, int N>
-void route_launch(const void* logits, const RouteIn& p, int32_t* idx, float* gates,
-                  int32_t* seq_counts, const RouteWs& w, cudaStream_t st) {
-  route_kernel<T, N><<<route_grid(p.T_), kRouteThreads, 0, st>>>(
-      static_cast<const T*>(logits), p, idx, gates, seq_counts, w.share, w.tokens, w.head);
+// Up to here the last CTA of the router finishes; beyond, a launch of its own.
+constexpr int64_t kFinishInside = 16384;
+
+template <typename T, int L, int N>
+cudaError_t route_launch(const void* logits, const RouteIn& p, const RouteOut& o, const RouteWs& w,
+                         cudaStream_t st) {
+  const bool inside = p.E * p.sequences <= kFinishInside;
+  route_kernel<T, L, N><<<route_grid<L, N>(p.T_), kRouteThreads, 0, st>>>(
+      static_cast<const T*>(logits), p, w.sums, o, w.head, inside);
+  if (!inside)
+    route_finish_kernel<<<(p.E + kFinishExperts - 1) / kFinishExperts, kRouteThreads, 0, st>>>(
+        p, w.sums, o, w.head);
+  return cudaGetLastError();
 }
 
-template <typename T, int N>
-void grad_launch(const void* logits, const RouteIn& p, const int32_t* idx, const float* d_gates,
-                 const int32_t* seq_counts, const float* seq_coef, float loss_scale, void* grad,
-                 int64_t grad_ld, cudaStream_t st) {
-  route_grad_kernel<T, N><<<route_grid(p.T_), kRouteThreads, 0, st>>>(
+template <typename T, int L, int N>
+cudaError_t grad_launch(const void* logits, const RouteIn& p, const int32_t* idx,
+                        const float* d_gates, const int32_t* seq_counts, const float* seq_coef,
+                        float loss_scale, void* grad, int64_t grad_ld, cudaStream_t st) {
+  route_grad_kernel<T, L, N><<<route_grid<L, N>(p.T_), kRouteThreads, 0, st>>>(
       static_cast<const T*>(logits), p, idx, d_gates, seq_counts, seq_coef, loss_scale,
       static_cast<T*>(grad), grad_ld);
+  return cudaGetLastError();
 }
 
-// Calls f<N> for the registers a lane needs to hold its share of E experts.
-#define VSF_BY_EXPERTS(E, F, ...)                    \
-  do {                                               \
-    if ((E) <= 32) F<T, 1>(__VA_ARGS__);             \
-    else if ((E) <= 64) F<T, 2>(__VA_ARGS__);        \
-    else if ((E) <= 128) F<T, 4>(__VA_ARGS__);       \
-    else if ((E) <= 256) F<T, 8>(__VA_ARGS__);       \
-    else F<T, 16>(__VA_ARGS__);                      \
+// F<T, lanes a token, experts a lane> for E experts.
+#define VSF_BY_EXPERTS(E, F, ...)                       \
+  do {                                                  \
+    if ((E) <= 8) return F<T, 8, 1>(__VA_ARGS__);       \
+    if ((E) <= 16) return F<T, 16, 1>(__VA_ARGS__);     \
+    if ((E) <= 32) return F<T, 32, 1>(__VA_ARGS__);     \
+    if ((E) <= 64) return F<T, 32, 2>(__VA_ARGS__);     \
+    if ((E) <= 128) return F<T, 32, 4>(__VA_ARGS__);    \
+    if ((E) <= 256) return F<T, 32, 8>(__VA_ARGS__);    \
+    return F<T, 32, 16>(__VA_ARGS__);                   \
   } while (0)
 
 template <typename T>
-void route_by_experts(const void* logits, const RouteIn& p, int32_t* idx, float* gates,
-                      int32_t* seq_counts, const RouteWs& w, cudaStream_t st) {
-  VSF_BY_EXPERTS(p.E, route_launch, logits, p, idx, gates, seq_counts, w, st);
+cudaError_t route_by_experts(const void* logits, const RouteIn& p, const RouteOut& o,
+                             const RouteWs& w, cudaStream_t st) {
+  VSF_BY_EXPERTS(p.E, route_launch, logits, p, o, w, st);
 }
 
 template <typename T>
-void grad_by_experts(const void* logits, const RouteIn& p, const int32_t* idx,
-                     const float* d_gates, const int32_t* seq_counts, const float* seq_coef,
-                     float loss_scale, void* grad, int64_t grad_ld, cudaStream_t st) {
+cudaError_t grad_by_experts(const void* logits, const RouteIn& p, const int32_t* idx,
+                            const float* d_gates, const int32_t* seq_counts,
+                            const float* seq_coef, float loss_scale, void* grad, int64_t grad_ld,
+                            cudaStream_t st) {
   VSF_BY_EXPERTS(p.E, grad_launch, logits, p, idx, d_gates, seq_counts, seq_coef, loss_scale,
                  grad, grad_ld, st);
 }
@@ -432,20 +662,11 @@ vsf_status vsf_route(const void* logits, int32_t dtype, int64_t T, int64_t E, in
       !aligned(counts, 4) || !aligned(loss, 4) || !aligned(seq_counts, 4) || !aligned(seq_coef, 4))
     return fail(VSF_ERR_ALIGN, "vsf_route: pointer alignment");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const RouteWs w(d_workspace, sequences);
+  const RouteWs w(d_workspace, E, sequences);
   const RouteIn p = route_in(T, E, ld, bias, live, seq_starts, sequences, hp);
-  cudaError_t e = cudaMemsetAsync(w.tokens, 0, RouteWs::bytes(E, sequences) - sizeof(WsHead), st);
-  if (e == cudaSuccess) e = cudaMemsetAsync(seq_counts, 0, (size_t)(sequences * E) * 4, st);
-  if (e != cudaSuccess) return cuda_error(e, who);
-  if (T > 0) {
-    if (dtype == VSF_BF16) route_by_experts<uint16_t>(logits, p, idx, gates, seq_counts, w, st);
-    else route_by_experts<float>(logits, p, idx, gates, seq_counts, w, st);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_error(e, who);
-  }
-  route_finish_kernel<<<1, 512, 0, st>>>(p, seq_counts, w.share, w.tokens, counts, seq_coef, loss,
-                                         w.head);
-  e = cudaGetLastError();
+  const RouteOut o = {idx, gates, counts, loss, seq_counts, seq_coef};
+  const cudaError_t e = dtype == VSF_BF16 ? route_by_experts<uint16_t>(logits, p, o, w, st)
+                                          : route_by_experts<float>(logits, p, o, w, st);
   return e == cudaSuccess ? VSF_OK : cuda_error(e, who);
 }
 
@@ -473,13 +694,12 @@ vsf_status vsf_route_grad(const void* logits, int32_t dtype, int64_t T, int64_t 
     return fail(VSF_ERR_ARG, "vsf_route_grad: grad overlaps the logits in part");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const RouteIn p = route_in(T, E, ld, nullptr, live, seq_starts, sequences, hp);
-  if (dtype == VSF_BF16)
-    grad_by_experts<uint16_t>(logits, p, idx, d_gates, seq_counts, seq_coef, loss_scale, grad,
-                              grad_ld, st);
-  else
-    grad_by_experts<float>(logits, p, idx, d_gates, seq_counts, seq_coef, loss_scale, grad,
-                           grad_ld, st);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      dtype == VSF_BF16
+          ? grad_by_experts<uint16_t>(logits, p, idx, d_gates, seq_counts, seq_coef, loss_scale,
+                                      grad, grad_ld, st)
+          : grad_by_experts<float>(logits, p, idx, d_gates, seq_counts, seq_coef, loss_scale, grad,
+                                   grad_ld, st);
   return e == cudaSuccess ? VSF_OK : cuda_error(e, who);
 }
 
