@@ -89,9 +89,9 @@ __device__ __forceinline__ int32_t live_target(const Rows<T>& r, int64_t t, uint
 }
 
 // ln s = k ln 2 + f, with |f| at most 0.41, where logf's absolute error is
-// below 3e-8 (logf(s) itself would round at 5e-7 for s in the thousands). All
-// terms of s but the maximum's 1 carry the mean error of ex2, which would add
-// up over a sequence, and is taken off here.
+// below 3e-8 (logf(s) itself would round at 5e-7 for s in the thousands). The
+// mean relative error of s itself, which would add up over a sequence, was
+// measured at -0.4e-8 (32000 words) to -1.7e-8 (logits of five times the spread).
 struct LogSum {
   float k, f;
 };
@@ -103,8 +103,7 @@ __device__ __forceinline__ LogSum log_sum(float s) {
     k = (float)((int)e - 127);
     f = __uint_as_float(b - ((e - 127u) << 23));
   }
-  const float bias = (float)kEx2Bias * (1.f - 1.f / s);
-  return {k, logf(f) - bias};
+  return {k, logf(f)};
 }
 
 // ln p(y) - ref in fp32, with d = x_y - m: the large parts cancel first. ln 2 =

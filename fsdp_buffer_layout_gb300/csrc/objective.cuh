@@ -42,10 +42,7 @@ __device__ __forceinline__ uint16_t from_f<uint16_t>(float v) {
   return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// 2^t by the special-function unit (ex2.approx: 2 ulp; 2^-inf = 0). Measured
-// on GB300 over t in [-26, -1]: its relative error has a mean of -5.06e-8 in
-// every octave, rms 5.9e-8, and none at t = 0.
-constexpr double kEx2Bias = -5.06e-8;
+// 2^t by the special-function unit (ex2.approx: 2 ulp; 2^-inf = 0).
 __device__ __forceinline__ float ex2(float t) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
