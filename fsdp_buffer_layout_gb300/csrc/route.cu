@@ -11,9 +11,13 @@
 //   logits:  d x_e  = s_e (d s_e - sum_j s_j d s_j)              softmax
 //                   = s_e (1 - s_e) d s_e                        sigmoid
 //
-// A group of L lanes (8, 16 or a warp) takes a token; lane l of it holds the
-// experts l, l + L, ... in registers. A CTA takes a run of tokens, one sequence
-// of it after the other, so that the sequence's sums stay in registers.
+// A group of L lanes (8, 16 or a warp) takes a token and holds its experts in
+// registers, N a lane. A CTA takes a run of tokens, one sequence of it after the
+// other, so that the sequence's sums stay in registers. Instructions bound the
+// large sizes (256 experts: 1 KB of logits a token against some hundred
+// instructions a warp), so the common form, 32 N experts in aligned rows, is
+// compiled apart: no checks of the expert's number, the score's kind known,
+// 16-byte loads and stores.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -42,7 +46,7 @@ struct RouteIn {
   const float* bias;
   const uint8_t* live;
   const int64_t* starts;  // NULL: one sequence of T_ tokens
-  Log2Scale c;
+  float c;                // log2(e)
 };
 
 // The sequences of a run of tokens [pos, end), in turn. Tokens in front of the
@@ -80,13 +84,36 @@ struct Walk {
   }
 };
 
-// Order-preserving 32-bit key of a float: larger is better, -0 equals +0,
-// NaN comes after every number. 0 is below every key.
+// Order-preserving 32-bit key of a number: larger is better, -0 equals +0.
+// Numbers lie above 1, the key of NaN; 0 is below every key. The caller tells
+// whether a NaN may be there.
 __device__ __forceinline__ uint32_t order_key(float v) {
-  if (v != v) return 1u;
-  const uint32_t b = __float_as_uint(v + 0.f);
-  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+  const int b = __float_as_int(v + 0.f);
+  return (uint32_t)(b ^ (b >> 31 | (int)0x80000000));
 }
+
+// How a lane holds experts. Full: E = L N, each lane V adjacent experts at a
+// time, which are one load; else expert `lane + L j` in register j.
+template <typename T, int L, int N, bool FULL>
+struct Hold {
+  static constexpr int V = FULL ? (N * (int)sizeof(T) < 16 ? N : 16 / (int)sizeof(T)) : 1;
+  static __device__ __forceinline__ int expert(int lane, int j) {
+    return FULL ? j / V * (L * V) + lane * V + j % V : lane + L * j;
+  }
+  static __device__ __forceinline__ bool has(int lane, int j, int E) {
+    return FULL || lane + L * j < E;
+  }
+};
+template <int B>
+struct Bytes;
+template <>
+struct Bytes<2> { using type = uint16_t; };
+template <>
+struct Bytes<4> { using type = uint32_t; };
+template <>
+struct Bytes<8> { using type = uint2; };
+template <>
+struct Bytes<16> { using type = uint4; };
 
 template <int L>
 __device__ __forceinline__ float group_sum(float v) {
@@ -96,86 +123,99 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 template <int L>
 __device__ __forceinline__ float group_max(float v) {
+  if (L == 32) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+  }
 #pragma unroll
   for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
   return v;
 }
 
-// 1 / (1 + exp(-x)): ex2.approx and rcp.approx, within 4 ulp together.
-__device__ __forceinline__ float sigmoid(float x, Log2Scale c) {
+// 1 / (1 + exp(-x)): ex2.approx and rcp.approx and the rounding of x log2(e).
+__device__ __forceinline__ float sigmoid(float x, float c) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp_scaled(-x, c)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(-x * c)));
   return r;
 }
 
-// A token's scores: max and 1 / sum of the softmax, or nothing, and from them
-// the score of one logit.
+// A token's scores from its logits, in place: the largest logit and 1 / sum of
+// the softmax (0 and 1 for sigmoids), with which score_of gives one logit's
+// score again, and Z.
 struct Norm {
-  float m, inv;
+  float m, inv, z;
 };
-template <int L, int N>
-__device__ __forceinline__ Norm scores(float (&x)[N], const RouteIn& p, int lane, float& z) {
-  Norm n = {0.f, 1.f};
-  if (p.score == VSF_SCORE_SOFTMAX) {
+template <typename H, int L, int N>
+__device__ __forceinline__ Norm scores(float (&x)[N], bool softmax, int E, float c, int lane) {
+  float sum = 0.f;
+  if (softmax) {
     float m = x[0];
 #pragma unroll
     for (int j = 1; j < N; ++j) m = fmaxf(m, x[j]);
-    n.m = group_max<L>(m);
-    float sum = 0.f;
+    m = group_max<L>(m);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      x[j] = exp_scaled(x[j] - n.m, p.c);
-      if (lane + L * j >= p.E) x[j] = 0.f;
+      x[j] = H::has(lane, j, E) ? ex2((x[j] - m) * c) : 0.f;
       sum += x[j];
     }
-    n.inv = 1.f / group_sum<L>(sum);
+    const float inv = 1.f / group_sum<L>(sum);
 #pragma unroll
-    for (int j = 0; j < N; ++j) x[j] *= n.inv;
-    z = 1.f;
-    return n;
+    for (int j = 0; j < N; ++j) x[j] *= inv;
+    return {m, inv, 1.f};
   }
-  float sum = 0.f;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    x[j] = lane + L * j < p.E ? sigmoid(x[j], p.c) : 0.f;
+    x[j] = H::has(lane, j, E) ? sigmoid(x[j], c) : 0.f;
     sum += x[j];
   }
-  z = group_sum<L>(sum) + 1e-20f;
-  return n;
+  return {0.f, 1.f, group_sum<L>(sum) + 1e-20f};
 }
-__device__ __forceinline__ float score_of(float x, Norm n, const RouteIn& p) {
-  return p.score == VSF_SCORE_SOFTMAX ? exp_scaled(x - n.m, p.c) * n.inv : sigmoid(x, p.c);
+__device__ __forceinline__ float score_of(float x, Norm n, bool softmax, float c) {
+  return softmax ? ex2((x - n.m) * c) * n.inv : sigmoid(x, c);
 }
 
-template <typename T, int L, int N>
-__device__ __forceinline__ void load_token(float (&x)[N], const T* row, int32_t E, int lane) {
+template <typename H, typename T, int L, int N>
+__device__ __forceinline__ void load_token(float (&x)[N], const T* row, int E, int lane, bool on) {
+  constexpr int V = H::V;
+  using Piece = typename Bytes<V * (int)sizeof(T)>::type;
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int e = lane + L * j;
-    x[j] = e < E ? to_f(row[e]) : -INFINITY;
+  for (int j = 0; j < N; j += V) {
+    union {
+      Piece p;
+      T t[V];
+    } u;
+    if (on && H::has(lane, j, E)) {
+      u.p = *reinterpret_cast<const Piece*>(row + H::expert(lane, j));
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[j + v] = to_f(u.t[v]);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[j + v] = -INFINITY;
+    }
   }
 }
 
 // The K experts of largest key, best first, ties to the lowest; lane k of the
 // group gets the k-th. Keys are lost. Round by round, the group's largest key
 // is found and taken out.
-template <int L, int N>
+template <typename H, int N>
 __device__ __forceinline__ int choose_rounds(uint32_t (&key)[N], int K, int lane, uint32_t mask) {
   int mine = -1;
   for (int k = 0; k < K; ++k) {
     uint32_t best = key[0];
-    int be = lane;
+    int be = H::expert(lane, 0);
 #pragma unroll
     for (int j = 1; j < N; ++j)
       if (key[j] > best) {
         best = key[j];
-        be = lane + L * j;
+        be = H::expert(lane, j);
       }
     const uint32_t top = __reduce_max_sync(mask, best);
     const int e = (int)__reduce_min_sync(mask, best == top ? (uint32_t)be : 0xffffffffu);
 #pragma unroll
     for (int j = 0; j < N; ++j)
-      if (lane + L * j == e) key[j] = 0u;
+      if (H::expert(lane, j) == e) key[j] = 0u;
     if (lane == k) mine = e;
   }
   return mine;
@@ -185,9 +225,9 @@ __device__ __forceinline__ int choose_rounds(uint32_t (&key)[N], int K, int lane
 // largest of the lanes' largest keys bounds the choice from below; the few
 // candidates from it on go to a lane each, and the rounds look at one key a
 // lane. More than 32 candidates (many equal keys) take the rounds above.
-template <int N>
+template <typename H, int N>
 __device__ __forceinline__ int choose(uint32_t (&key)[N], int K, int lane, uint2* cand) {
-  if (N == 1) return choose_rounds<32, N>(key, K, lane, ~0u);
+  if (N == 1) return choose_rounds<H, N>(key, K, lane, ~0u);
   uint32_t lane_max = key[0];
 #pragma unroll
   for (int j = 1; j < N; ++j) lane_max = max(lane_max, key[j]);
@@ -198,27 +238,27 @@ __device__ __forceinline__ int choose(uint32_t (&key)[N], int K, int lane, uint2
     n += __popc(__ballot_sync(~0u, hit));
     if (hit) lane_max = 0u;
   }
-  // a bound of 0 means fewer lanes with experts than choices
+  bound = max(bound, 1u);
   int n = 0;
+  const uint32_t below = (1u << lane) - 1;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    const bool in = key[j] >= bound && key[j] != 0u;
+    const bool in = key[j] >= bound;
     const uint32_t all = __ballot_sync(~0u, in);
-    const int at = n + __popc(all & ((1u << lane) - 1));
-    if (in && at < 32) cand[at] = make_uint2(key[j], (uint32_t)(lane + 32 * j));
+    const int at = n + __popc(all & below);
+    if (in && at < 32) cand[at] = make_uint2(key[j], (uint32_t)H::expert(lane, j));
     n += __popc(all);
   }
-  if (n > 32) return choose_rounds<32, N>(key, K, lane, ~0u);
   __syncwarp();
-  uint2 c = lane < n ? cand[lane] : make_uint2(0u, 0u);  // in the order of the experts
+  if (n > 32) return choose_rounds<H, N>(key, K, lane, ~0u);
+  uint2 c = lane < n ? cand[lane] : make_uint2(0u, 0xffffffffu);
   __syncwarp();
   int mine = -1;
   for (int k = 0; k < K; ++k) {
     const uint32_t top = __reduce_max_sync(~0u, c.x);
-    const int who = __ffs(__ballot_sync(~0u, c.x == top)) - 1;
-    const int e = (int)__shfl_sync(~0u, c.y, who);
-    if (lane == who) c.x = 0u;
-    if (lane == k) mine = e;
+    const uint32_t e = __reduce_min_sync(~0u, c.x == top ? c.y : 0xffffffffu);
+    if (c.y == e) c.x = 0u;
+    if (lane == k) mine = (int)e;
   }
   return mine;
 }
@@ -297,11 +337,13 @@ __device__ float route_finish(const RouteIn& p, const RouteSums& w, const RouteO
   return l;
 }
 
-template <typename T, int L, int N>
+// SCORE: the score's kind, or -1 where it is known at run time only.
+template <typename T, int L, int N, bool FULL, int SCORE>
 __global__ void __launch_bounds__(kRouteThreads, N <= 8 ? 4 : 2)
     route_kernel(const T* logits, const __grid_constant__ RouteIn p,
                  const __grid_constant__ RouteSums w, const __grid_constant__ RouteOut o,
                  WsHead* head, int32_t finish) {
+  using H = Hold<T, L, N, FULL>;
   constexpr int kGroups = kRouteThreads / L;
   __shared__ float share[kGroups][N * L];  // sums of shares of each group
   __shared__ int32_t count[N * L];         // choices of the CTA
@@ -312,6 +354,12 @@ __global__ void __launch_bounds__(kRouteThreads, N <= 8 ? 4 : 2)
   for (int e = tid; e < N * L; e += kRouteThreads) count[e] = 0;
   if (tid == 0) tokens = 0;
   __syncthreads();
+  const bool softmax = SCORE < 0 ? p.score == VSF_SCORE_SOFTMAX : SCORE == VSF_SCORE_SOFTMAX;
+  const float c = p.c;
+  float bias[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    bias[j] = p.bias != nullptr && H::has(lane, j, p.E) ? p.bias[H::expert(lane, j)] : 0.f;
   const int64_t per = (p.T_ + gridDim.x - 1) / gridDim.x;
   const int64_t from = min((int64_t)blockIdx.x * per, p.T_);
   for (Walk run(p, from, min(from + per, p.T_)); !run.done(); run.next(p)) {
@@ -329,45 +377,57 @@ __global__ void __launch_bounds__(kRouteThreads, N <= 8 ? 4 : 2)
       const T* row = logits + (on ? t : run.pos) * p.ld;
       float x[N];
       uint32_t key[N];
-      load_token<T, L>(x, row, on ? p.E : 0, lane);
+      load_token<H, T, L, N>(x, row, p.E, lane, on);
       if (p.bias == nullptr) {
 #pragma unroll
         for (int j = 0; j < N; ++j) key[j] = order_key(x[j]);
       }
-      float z;
-      const Norm norm = scores<L>(x, p, lane, z);
+      bool odd = false;  // a NaN among the logits
+#pragma unroll
+      for (int j = 0; j < N; ++j) odd |= x[j] != x[j];
+      const Norm norm = scores<H, L, N>(x, softmax, p.E, c, lane);
       if (p.bias != nullptr) {
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-          key[j] = lane + L * j < p.E ? order_key(x[j] + p.bias[lane + L * j]) : 0u;
+        for (int j = 0; j < N; ++j) {
+          const float s = x[j] + bias[j];
+          key[j] = order_key(s);
+          odd |= s != s;
+        }
+      }
+      if (__any_sync(~0u, odd)) {
+        // NaN after every number: of a logit, or, with a bias, of a sum
+        float y[N];
+        load_token<H, T, L, N>(y, row, p.E, lane, on);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          if (p.bias != nullptr) y[j] = x[j] + bias[j];
+          if (y[j] != y[j]) key[j] = 1u;
+        }
       }
 #pragma unroll
       for (int j = 0; j < N; ++j)
-        if (lane + L * j >= p.E) key[j] = 0u;
-      const int chosen = L == 32 && N > 1 ? choose<N>(key, p.K, lane, cand[warp])
-                                          : choose_rounds<L, N>(key, p.K, lane, mask);
+        if (!H::has(lane, j, p.E)) key[j] = 0u;
+      const int chosen = L == 32 && N > 1 ? choose<H, N>(key, p.K, lane, cand[warp])
+                                          : choose_rounds<H, N>(key, p.K, lane, mask);
       float score = 0.f;
-      if (on && lane < p.K) score = score_of(to_f(row[chosen]), norm, p);
+      if (on && lane < p.K) score = score_of(to_f(row[chosen]), norm, softmax, c);
       const float sum = group_sum<L>(score) + 1e-20f;
       if (in && lane < p.K) {
         o.idx[t * p.K + lane] = on ? chosen : -1;
-        o.gates[t * p.K + lane] = on ? (p.renorm ? p.scale * score / sum : p.scale * score) : 0.f;
+        o.gates[t * p.K + lane] = on ? p.scale * (p.renorm ? __fdividef(score, sum) : score) : 0.f;
         if (on && counted) atomicAdd(&count[chosen], 1);
       }
-      if (on && counted) {
-        const float inv = 1.f / z;
+      if (on) {
+        const float inv = softmax ? 1.f : 1.f / norm.z;
+        bad |= norm.z != norm.z || norm.inv != norm.inv;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const float q = x[j] * inv;
-          bad |= q != q;
-          acc[j] += q;
-        }
+        for (int j = 0; j < N; ++j) acc[j] = __fmaf_rn(x[j], inv, acc[j]);
         ++seen;
       }
     }
     if (!counted) continue;
 #pragma unroll
-    for (int j = 0; j < N; ++j) share[group][lane + L * j] = acc[j];
+    for (int j = 0; j < N; ++j) share[group][H::expert(lane, j)] = acc[j];
     if (lane == 0 && seen > 0) atomicAdd(&tokens, seen);
     if (bad) head->nan = 1u;
     __syncthreads();
@@ -431,18 +491,21 @@ __global__ void __launch_bounds__(kRouteThreads)
   }
 }
 
-template <typename T, int L, int N>
+template <typename T, int L, int N, bool FULL, int SCORE>
 __global__ void __launch_bounds__(kRouteThreads, N <= 8 ? 4 : 2)
     route_grad_kernel(const T* logits, const __grid_constant__ RouteIn p, const int32_t* idx,
                       const float* d_gates, const int32_t* seq_counts, const float* seq_coef,
                       float loss_scale, T* grad, int64_t grad_ld) {
-  constexpr int kGroups = kRouteThreads / L;
-  __shared__ float pulled[kGroups][N * L];  // the gates' pull on each score; zero between tokens
+  using H = Hold<T, L, N, FULL>;
+  constexpr int kGroups = kRouteThreads / L, V = H::V;
+  __shared__ __align__(16) float pulled[kGroups][N * L];  // the gates' pull; zero between tokens
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & (L - 1);
   float* pull = pulled[tid / L];
 #pragma unroll
   for (int j = 0; j < N; ++j) pull[lane + L * j] = 0.f;
   __syncwarp();
+  const bool softmax = SCORE < 0 ? p.score == VSF_SCORE_SOFTMAX : SCORE == VSF_SCORE_SOFTMAX;
+  const float c = p.c;
   const int64_t per = (p.T_ + gridDim.x - 1) / gridDim.x;
   const int64_t from = min((int64_t)blockIdx.x * per, p.T_);
   for (Walk run(p, from, min(from + per, p.T_)); !run.done(); run.next(p)) {
@@ -450,17 +513,17 @@ __global__ void __launch_bounds__(kRouteThreads, N <= 8 ? 4 : 2)
     const bool balanced = run.inside(p) && loss_scale != 0.f;
     const float f = balanced ? loss_scale * seq_coef[run.seq] : 0.f;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int e = lane + L * j;
-      b[j] = balanced && e < p.E ? f * (float)seq_counts[run.seq * p.E + e] : 0.f;
-    }
+    for (int j = 0; j < N; ++j)
+      b[j] = balanced && H::has(lane, j, p.E)
+                 ? f * (float)seq_counts[run.seq * p.E + H::expert(lane, j)]
+                 : 0.f;
     for (int64_t t0 = run.pos + warp * (32 / L); t0 < run.stop; t0 += kGroups) {
       const int64_t t = t0 + (tid & 31) / L;
       const bool in = t < run.stop;
       const bool on = in && (p.live == nullptr || p.live[t] != 0);
       const T* row = logits + (on ? t : run.pos) * p.ld;
       float x[N];
-      load_token<T, L>(x, row, on ? p.E : 0, lane);
+      load_token<H, T, L, N>(x, row, p.E, lane, on);
       int e = -1;
       float dg = 0.f, xe = 0.f;
       if (on && d_gates != nullptr && lane < p.K) {
@@ -471,20 +534,19 @@ __global__ void __launch_bounds__(kRouteThreads, N <= 8 ? 4 : 2)
           xe = to_f(row[e]);
         }
       }
-      float z;
-      const Norm norm = scores<L>(x, p, lane, z);
+      const Norm norm = scores<H, L, N>(x, softmax, p.E, c, lane);
       float ds[N];
       if (d_gates != nullptr) {
         float v = dg;
         if (p.renorm) {
-          const float s = e >= 0 ? score_of(xe, norm, p) : 0.f;
+          const float s = e >= 0 ? score_of(xe, norm, softmax, c) : 0.f;
           const float inv = 1.f / (group_sum<L>(s) + 1e-20f);
           v = (dg - group_sum<L>(dg * s) * inv) * inv;
         }
         if (e >= 0) pull[e] = p.scale * v;
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < N; ++j) ds[j] = pull[lane + L * j];
+        for (int j = 0; j < N; ++j) ds[j] = pull[H::expert(lane, j)];
         __syncwarp();
         if (e >= 0) pull[e] = 0.f;
         __syncwarp();
@@ -492,33 +554,45 @@ __global__ void __launch_bounds__(kRouteThreads, N <= 8 ? 4 : 2)
 #pragma unroll
         for (int j = 0; j < N; ++j) ds[j] = 0.f;
       }
-      const float inv = 1.f / z;
       float dot = 0.f;
-      if (p.score == VSF_SCORE_SOFTMAX) {
+      if (softmax) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           ds[j] += b[j];
-          dot += x[j] * ds[j];
+          dot = __fmaf_rn(x[j], ds[j], dot);
         }
         dot = group_sum<L>(dot);
-      } else if (balanced) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) dot += b[j] * x[j];
-        dot = group_sum<L>(dot) * inv;
+        for (int j = 0; j < N; ++j) x[j] *= ds[j] - dot;
+      } else {
+        const float inv = 1.f / norm.z;
+        if (balanced) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) ds[j] += (b[j] - dot) * inv;
-      }
-      if (!in) continue;
-      T* g = grad + t * grad_ld;
+          for (int j = 0; j < N; ++j) dot = __fmaf_rn(b[j], x[j], dot);
+          dot = group_sum<L>(dot) * inv;
+        }
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int at = lane + L * j;
-        if (at < p.E) {
-          const float v = p.score == VSF_SCORE_SOFTMAX ? x[j] * (ds[j] - dot)
-                                                       : x[j] * (1.f - x[j]) * ds[j];
-          g[at] = from_f<T>(on ? v : 0.f);
+        for (int j = 0; j < N; ++j) {
+          if (balanced) ds[j] = __fmaf_rn(b[j] - dot, inv, ds[j]);
+          x[j] = x[j] * (1.f - x[j]) * ds[j];
         }
       }
+      if (in) {
+        T* g = grad + t * grad_ld;
+        using Piece = typename Bytes<V * (int)sizeof(T)>::type;
+#pragma unroll
+        for (int j = 0; j < N; j += V) {
+          if (!H::has(lane, j, p.E)) continue;
+          union {
+            Piece p;
+            T t[V];
+          } u;
+#pragma unroll
+          for (int v = 0; v < V; ++v) u.t[v] = from_f<T>(on ? x[j + v] : 0.f);
+          *reinterpret_cast<Piece*>(g + H::expert(lane, j)) = u.p;
+        }
+      }
+      __syncwarp();
     }
   }
 }
@@ -568,7 +642,7 @@ vsf_status check_route(const char* who, const void* logits, int32_t dtype, int64
 RouteIn route_in(int64_t T_, int64_t E, int64_t ld, const float* bias, const uint8_t* live,
                  const int64_t* starts, int64_t sequences, const vsf_route_hparams* hp) {
   return {T_, ld, sequences, (int32_t)E, hp->top_k, hp->score, hp->renorm != 0,
-          hp->route_scale, hp->balance, bias, live, starts, log2_scale(1.f)};
+          hp->route_scale, hp->balance, bias, live, starts, 1.44269504f};
 }
 
 // CTAs: two tokens a group at least, 4 CTAs an SM at most (2 with more than
@@ -583,11 +657,11 @@ unsigned route_grid(int64_t T_) {
 // Up to here the last CTA of the router finishes; beyond, a launch of its own.
 constexpr int64_t kFinishInside = 16384;
 
-template <typename T, int L, int N>
+template <typename T, int L, int N, bool FULL, int SCORE>
 cudaError_t route_launch(const void* logits, const RouteIn& p, const RouteOut& o, const RouteWs& w,
                          cudaStream_t st) {
   const bool inside = p.E * p.sequences <= kFinishInside;
-  route_kernel<T, L, N><<<route_grid<L, N>(p.T_), kRouteThreads, 0, st>>>(
+  route_kernel<T, L, N, FULL, SCORE><<<route_grid<L, N>(p.T_), kRouteThreads, 0, st>>>(
       static_cast<const T*>(logits), p, w.sums, o, w.head, inside);
   if (!inside)
     route_finish_kernel<<<(p.E + kFinishExperts - 1) / kFinishExperts, kRouteThreads, 0, st>>>(
@@ -595,32 +669,45 @@ cudaError_t route_launch(const void* logits, const RouteIn& p, const RouteOut& o
   return cudaGetLastError();
 }
 
-template <typename T, int L, int N>
+template <typename T, int L, int N, bool FULL, int SCORE>
 cudaError_t grad_launch(const void* logits, const RouteIn& p, const int32_t* idx,
                         const float* d_gates, const int32_t* seq_counts, const float* seq_coef,
                         float loss_scale, void* grad, int64_t grad_ld, cudaStream_t st) {
-  route_grad_kernel<T, L, N><<<route_grid<L, N>(p.T_), kRouteThreads, 0, st>>>(
+  route_grad_kernel<T, L, N, FULL, SCORE><<<route_grid<L, N>(p.T_), kRouteThreads, 0, st>>>(
       static_cast<const T*>(logits), p, idx, d_gates, seq_counts, seq_coef, loss_scale,
       static_cast<T*>(grad), grad_ld);
   return cudaGetLastError();
 }
 
-// F<T, lanes a token, experts a lane> for E experts.
-#define VSF_BY_EXPERTS(E, F, ...)                       \
-  do {                                                  \
-    if ((E) <= 8) return F<T, 8, 1>(__VA_ARGS__);       \
-    if ((E) <= 16) return F<T, 16, 1>(__VA_ARGS__);     \
-    if ((E) <= 32) return F<T, 32, 1>(__VA_ARGS__);     \
-    if ((E) <= 64) return F<T, 32, 2>(__VA_ARGS__);     \
-    if ((E) <= 128) return F<T, 32, 4>(__VA_ARGS__);    \
-    if ((E) <= 256) return F<T, 32, 8>(__VA_ARGS__);    \
-    return F<T, 32, 16>(__VA_ARGS__);                   \
+// F<T, lanes a token, experts a lane, full, score> for the experts of p; wide:
+// every row of the arrays starts on a 16-byte boundary.
+#define VSF_FULL(F, N, ...)                                                              \
+  (p.score == VSF_SCORE_SOFTMAX ? F<T, 32, N, true, VSF_SCORE_SOFTMAX>(__VA_ARGS__)      \
+                                : F<T, 32, N, true, VSF_SCORE_SIGMOID>(__VA_ARGS__))
+#define VSF_BY_EXPERTS(F, wide, ...)                                  \
+  do {                                                                \
+    if ((wide) && p.E == 64) return VSF_FULL(F, 2, __VA_ARGS__);      \
+    if ((wide) && p.E == 128) return VSF_FULL(F, 4, __VA_ARGS__);     \
+    if ((wide) && p.E == 256) return VSF_FULL(F, 8, __VA_ARGS__);     \
+    if (p.E <= 8) return F<T, 8, 1, false, -1>(__VA_ARGS__);          \
+    if (p.E <= 16) return F<T, 16, 1, false, -1>(__VA_ARGS__);        \
+    if (p.E <= 32) return F<T, 32, 1, false, -1>(__VA_ARGS__);        \
+    if (p.E <= 64) return F<T, 32, 2, false, -1>(__VA_ARGS__);        \
+    if (p.E <= 128) return F<T, 32, 4, false, -1>(__VA_ARGS__);       \
+    if (p.E <= 256) return F<T, 32, 8, false, -1>(__VA_ARGS__);       \
+    return F<T, 32, 16, false, -1>(__VA_ARGS__);                      \
   } while (0)
+
+// Whether rows of T at this stride start on 16-byte boundaries.
+template <typename T>
+bool wide_rows(const void* p, int64_t ld) {
+  return aligned(p, 16) && ld * (int64_t)sizeof(T) % 16 == 0;
+}
 
 template <typename T>
 cudaError_t route_by_experts(const void* logits, const RouteIn& p, const RouteOut& o,
                              const RouteWs& w, cudaStream_t st) {
-  VSF_BY_EXPERTS(p.E, route_launch, logits, p, o, w, st);
+  VSF_BY_EXPERTS(route_launch, wide_rows<T>(logits, p.ld), logits, p, o, w, st);
 }
 
 template <typename T>
@@ -628,8 +715,8 @@ cudaError_t grad_by_experts(const void* logits, const RouteIn& p, const int32_t*
                             const float* d_gates, const int32_t* seq_counts,
                             const float* seq_coef, float loss_scale, void* grad, int64_t grad_ld,
                             cudaStream_t st) {
-  VSF_BY_EXPERTS(p.E, grad_launch, logits, p, idx, d_gates, seq_counts, seq_coef, loss_scale,
-                 grad, grad_ld, st);
+  VSF_BY_EXPERTS(grad_launch, wide_rows<T>(logits, p.ld) && wide_rows<T>(grad, grad_ld), logits, p,
+                 idx, d_gates, seq_counts, seq_coef, loss_scale, grad, grad_ld, st);
 }
 
 }  // namespace
