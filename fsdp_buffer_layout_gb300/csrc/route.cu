@@ -61,13 +61,19 @@ struct Walk {
   __device__ __forceinline__ void settle(const RouteIn& p) {  // on to one with tokens
     for (bound(p); stop == pos && pos < end; bound(p)) ++seq;
   }
+  // All lanes of a warp together: a step of the search looks at 32 starts.
   __device__ __forceinline__ Walk(const RouteIn& p, int64_t first, int64_t last)
       : pos(first), end(last), seq(0) {
     if (p.starts != nullptr) {
-      int64_t lo = -1, hi = p.sequences + 1;  // starts[lo] <= pos < starts[hi]
+      const int64_t n = p.sequences + 1;
+      int64_t lo = -1, hi = n;  // starts[lo] <= pos < starts[hi]
       while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) / 2;
-        if (p.starts[mid] <= pos) lo = mid; else hi = mid;
+        const int64_t step = (hi - lo + 31) / 32;
+        const int64_t at = lo + ((threadIdx.x & 31) + 1) * step;
+        const bool in = at < hi && p.starts[at < n ? at : n - 1] <= pos;
+        const int k = __ffs(~__ballot_sync(~0u, in)) - 1;  // steps taken; -1: all 32
+        lo += (k < 0 ? 32 : k) * step;
+        if (lo + step < hi) hi = lo + step;
       }
       seq = lo;
     }
@@ -97,6 +103,7 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 template <typename T, int L, int N, bool FULL>
 struct Hold {
   static constexpr int V = FULL ? (N * (int)sizeof(T) < 16 ? N : 16 / (int)sizeof(T)) : 1;
+  static constexpr bool kWarp = L == 32;
   static __device__ __forceinline__ int expert(int lane, int j) {
     return FULL ? j / V * (L * V) + lane * V + j % V : lane + L * j;
   }
@@ -123,22 +130,24 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 template <int L>
 __device__ __forceinline__ float group_max(float v) {
-  if (L == 32) {
+  if constexpr (L == 32) {
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
-  }
+  } else {
 #pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
-  return v;
+    for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
+    return v;
+  }
 }
 
 // 1 / (1 + exp(-x)): ex2.approx and rcp.approx and the rounding of x log2(e).
-__device__ __forceinline__ float sigmoid(float x, float c) {
+__device__ __forceinline__ float rcp(float v) {  // 1 ulp
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(-x * c)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
+__device__ __forceinline__ float sigmoid(float x, float c) { return rcp(1.f + ex2(-x * c)); }
 
 // A token's scores from its logits, in place: the largest logit and 1 / sum of
 // the softmax (0 and 1 for sigmoids), with which score_of gives one logit's
@@ -159,7 +168,7 @@ __device__ __forceinline__ Norm scores(float (&x)[N], bool softmax, int E, float
       x[j] = H::has(lane, j, E) ? ex2((x[j] - m) * c) : 0.f;
       sum += x[j];
     }
-    const float inv = 1.f / group_sum<L>(sum);
+    const float inv = rcp(group_sum<L>(sum));
 #pragma unroll
     for (int j = 0; j < N; ++j) x[j] *= inv;
     return {m, inv, 1.f};
@@ -175,26 +184,30 @@ __device__ __forceinline__ float score_of(float x, Norm n, bool softmax, float c
   return softmax ? ex2((x - n.m) * c) * n.inv : sigmoid(x, c);
 }
 
-template <typename H, typename T, int L, int N>
-__device__ __forceinline__ void load_token(float (&x)[N], const T* row, int E, int lane, bool on) {
-  constexpr int V = H::V;
+// A token's logits as they lie in memory, on their way while the token before
+// it is worked on.
+template <typename H, typename T, int N>
+struct Raw {
+  static constexpr int V = H::V;
   using Piece = typename Bytes<V * (int)sizeof(T)>::type;
+  union {
+    Piece p[N / V];
+    T t[N];
+  };
+  bool on;
+  __device__ __forceinline__ void fetch(const T* row, int E, int lane, bool live) {
+    on = live;
 #pragma unroll
-  for (int j = 0; j < N; j += V) {
-    union {
-      Piece p;
-      T t[V];
-    } u;
-    if (on && H::has(lane, j, E)) {
-      u.p = *reinterpret_cast<const Piece*>(row + H::expert(lane, j));
-#pragma unroll
-      for (int v = 0; v < V; ++v) x[j + v] = to_f(u.t[v]);
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) x[j + v] = -INFINITY;
-    }
+    for (int j = 0; j < N; j += V)
+      if (on && H::has(lane, j, E)) p[j / V] = *reinterpret_cast<const Piece*>(row + H::expert(lane, j));
   }
-}
+  // (of a whole warp's token: only where it is live)
+  __device__ __forceinline__ void get(float (&x)[N], int E, int lane) const {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      x[j] = (H::kWarp || on) && H::has(lane, j, E) ? to_f(t[j]) : -INFINITY;
+  }
+};
 
 // The K experts of largest key, best first, ties to the lowest; lane k of the
 // group gets the k-th. Keys are lost. Round by round, the group's largest key
@@ -221,24 +234,20 @@ __device__ __forceinline__ int choose_rounds(uint32_t (&key)[N], int K, int lane
   return mine;
 }
 
-// The same with fewer instructions where a lane holds several keys: the K-th
-// largest of the lanes' largest keys bounds the choice from below; the few
-// candidates from it on go to a lane each, and the rounds look at one key a
-// lane. More than 32 candidates (many equal keys) take the rounds above.
+// The same with fewer instructions where a lane holds several keys. A bound
+// from below leaves few candidates, which go to a lane each, and the rounds
+// look at one key a lane. Up to 8 choices, the smallest of the largest keys of
+// 8 groups of 4 lanes bounds them (at least 8 keys reach it; 22 on average, as
+// many as it takes to draw each of 8 kinds); with more choices, or more than 32
+// candidates, the K-th largest of the lanes' largest keys. Where that leaves
+// more than 32 as well (equal keys), the rounds above.
+struct Candidates {
+  uint32_t key[32];
+  int32_t expert[32];
+};
 template <typename H, int N>
-__device__ __forceinline__ int choose(uint32_t (&key)[N], int K, int lane, uint2* cand) {
-  if (N == 1) return choose_rounds<H, N>(key, K, lane, ~0u);
-  uint32_t lane_max = key[0];
-#pragma unroll
-  for (int j = 1; j < N; ++j) lane_max = max(lane_max, key[j]);
-  uint32_t bound = 0;
-  for (int n = 0; n < K;) {
-    bound = __reduce_max_sync(~0u, lane_max);
-    const bool hit = lane_max == bound;
-    n += __popc(__ballot_sync(~0u, hit));
-    if (hit) lane_max = 0u;
-  }
-  bound = max(bound, 1u);
+__device__ __forceinline__ int gather(const uint32_t (&key)[N], uint32_t bound, int lane,
+                                      Candidates& c) {
   int n = 0;
   const uint32_t below = (1u << lane) - 1;
 #pragma unroll
@@ -246,18 +255,47 @@ __device__ __forceinline__ int choose(uint32_t (&key)[N], int K, int lane, uint2
     const bool in = key[j] >= bound;
     const uint32_t all = __ballot_sync(~0u, in);
     const int at = n + __popc(all & below);
-    if (in && at < 32) cand[at] = make_uint2(key[j], (uint32_t)H::expert(lane, j));
+    if (in && at < 32) {
+      c.key[at] = key[j];
+      c.expert[at] = H::expert(lane, j);
+    }
     n += __popc(all);
   }
+  return n;
+}
+template <typename H, int N>
+__device__ __forceinline__ int choose(uint32_t (&key)[N], int K, int lane, Candidates& cand) {
+  if (N == 1) return choose_rounds<H, N>(key, K, lane, ~0u);
+  uint32_t lane_max = key[0];
+#pragma unroll
+  for (int j = 1; j < N; ++j) lane_max = max(lane_max, key[j]);
+  int n = 33;
+  if (K <= 8) {
+    uint32_t four = max(lane_max, __shfl_xor_sync(~0u, lane_max, 1));
+    four = max(four, __shfl_xor_sync(~0u, four, 2));
+    n = gather<H, N>(key, max(__reduce_min_sync(~0u, four), 1u), lane, cand);
+  }
+  if (n > 32) {
+    uint32_t bound = 0;
+    for (int k = 0; k < K;) {
+      bound = __reduce_max_sync(~0u, lane_max);
+      const bool hit = lane_max == bound;
+      k += __popc(__ballot_sync(~0u, hit));
+      if (hit) lane_max = 0u;
+    }
+    __syncwarp();
+    n = gather<H, N>(key, max(bound, 1u), lane, cand);
+    if (n > 32) return choose_rounds<H, N>(key, K, lane, ~0u);
+  }
   __syncwarp();
-  if (n > 32) return choose_rounds<H, N>(key, K, lane, ~0u);
-  uint2 c = lane < n ? cand[lane] : make_uint2(0u, 0xffffffffu);
+  uint32_t mine_key = lane < n ? cand.key[lane] : 0u;
+  const uint32_t mine_e = lane < n ? (uint32_t)cand.expert[lane] : 0xffffffffu;
   __syncwarp();
   int mine = -1;
   for (int k = 0; k < K; ++k) {
-    const uint32_t top = __reduce_max_sync(~0u, c.x);
-    const uint32_t e = __reduce_min_sync(~0u, c.x == top ? c.y : 0xffffffffu);
-    if (c.y == e) c.x = 0u;
+    const uint32_t top = __reduce_max_sync(~0u, mine_key);
+    const uint32_t e = __reduce_min_sync(~0u, mine_key == top ? mine_e : 0xffffffffu);
+    if (mine_e == e) mine_key = 0u;
     if (lane == k) mine = (int)e;
   }
   return mine;
@@ -337,9 +375,13 @@ __device__ float route_finish(const RouteIn& p, const RouteSums& w, const RouteO
   return l;
 }
 
+// CTAs an SM: registers for the token ahead as well. At 256 experts 3 run in 93 us
+// (65536 tokens, both ways) where 4, which spill, take 105 and 2 take 106.
+constexpr int route_ctas(int n) { return n <= 4 ? 4 : n <= 8 ? 3 : 2; }
+
 // SCORE: the score's kind, or -1 where it is known at run time only.
 template <typename T, int L, int N, bool FULL, int SCORE>
-__global__ void __launch_bounds__(kRouteThreads, N <= 8 ? 4 : 2)
+__global__ void __launch_bounds__(kRouteThreads, route_ctas(N))
     route_kernel(const T* logits, const __grid_constant__ RouteIn p,
                  const __grid_constant__ RouteSums w, const __grid_constant__ RouteOut o,
                  WsHead* head, int32_t finish) {
@@ -347,7 +389,7 @@ __global__ void __launch_bounds__(kRouteThreads, N <= 8 ? 4 : 2)
   constexpr int kGroups = kRouteThreads / L;
   __shared__ float share[kGroups][N * L];  // sums of shares of each group
   __shared__ int32_t count[N * L];         // choices of the CTA
-  __shared__ uint2 cand[kRouteWarps][32];  // candidates of a token's choice
+  __shared__ Candidates cand[kRouteWarps];
   __shared__ int tokens, last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & (L - 1), group = tid / L;
   const uint32_t mask = L == 32 ? ~0u : ((1u << (L & 31)) - 1) << ((tid & 31) & ~(L - 1));
@@ -357,9 +399,13 @@ __global__ void __launch_bounds__(kRouteThreads, N <= 8 ? 4 : 2)
   const bool softmax = SCORE < 0 ? p.score == VSF_SCORE_SOFTMAX : SCORE == VSF_SCORE_SOFTMAX;
   const float c = p.c;
   float bias[N];
+  bool strange = false;  // a NaN in the bias
 #pragma unroll
-  for (int j = 0; j < N; ++j)
+  for (int j = 0; j < N; ++j) {
     bias[j] = p.bias != nullptr && H::has(lane, j, p.E) ? p.bias[H::expert(lane, j)] : 0.f;
+    strange |= bias[j] != bias[j];
+  }
+  strange = __any_sync(~0u, strange);
   const int64_t per = (p.T_ + gridDim.x - 1) / gridDim.x;
   const int64_t from = min((int64_t)blockIdx.x * per, p.T_);
   for (Walk run(p, from, min(from + per, p.T_)); !run.done(); run.next(p)) {
@@ -370,34 +416,44 @@ __global__ void __launch_bounds__(kRouteThreads, N <= 8 ? 4 : 2)
 #pragma unroll
     for (int j = 0; j < N; ++j) acc[j] = 0.f;
     // the groups of a warp go round together: shuffles span them
-    for (int64_t t0 = run.pos + warp * (32 / L); t0 < run.stop; t0 += kGroups) {
-      const int64_t t = t0 + (tid & 31) / L;
-      const bool in = t < run.stop;
-      const bool on = in && (p.live == nullptr || p.live[t] != 0);
+    Raw<H, T, N> next;
+    auto fetch = [&](int64_t t) {
+      const bool live = t < run.stop && (p.live == nullptr || p.live[t] != 0);
+      next.fetch(logits + (live ? t : run.pos) * p.ld, p.E, lane, live);
+    };
+    int64_t t = run.pos + warp * (32 / L) + (tid & 31) / L;
+    fetch(t);
+    for (int64_t t0 = run.pos + warp * (32 / L); t0 < run.stop; t0 += kGroups, t += kGroups) {
+      const bool in = t < run.stop, on = next.on;
       const T* row = logits + (on ? t : run.pos) * p.ld;
+      if (L == 32 && !on) {
+        if (lane < p.K) {
+          o.idx[t * p.K + lane] = -1;
+          o.gates[t * p.K + lane] = 0.f;
+        }
+        fetch(t + kGroups);
+        continue;
+      }
       float x[N];
       uint32_t key[N];
-      load_token<H, T, L, N>(x, row, p.E, lane, on);
+      next.get(x, p.E, lane);
+      fetch(t + kGroups);
       if (p.bias == nullptr) {
 #pragma unroll
         for (int j = 0; j < N; ++j) key[j] = order_key(x[j]);
       }
-      bool odd = false;  // a NaN among the logits
-#pragma unroll
-      for (int j = 0; j < N; ++j) odd |= x[j] != x[j];
       const Norm norm = scores<H, L, N>(x, softmax, p.E, c, lane);
       if (p.bias != nullptr) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const float s = x[j] + bias[j];
-          key[j] = order_key(s);
-          odd |= s != s;
-        }
+        for (int j = 0; j < N; ++j) key[j] = order_key(x[j] + bias[j]);
       }
-      if (__any_sync(~0u, odd)) {
+      const bool odd = norm.z != norm.z || norm.inv != norm.inv;  // a NaN somewhere
+      if (__any_sync(~0u, odd) || strange) {
         // NaN after every number: of a logit, or, with a bias, of a sum
+        Raw<H, T, N> again;
         float y[N];
-        load_token<H, T, L, N>(y, row, p.E, lane, on);
+        again.fetch(row, p.E, lane, on);
+        again.get(y, p.E, lane);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           if (p.bias != nullptr) y[j] = x[j] + bias[j];
@@ -418,8 +474,8 @@ __global__ void __launch_bounds__(kRouteThreads, N <= 8 ? 4 : 2)
         if (on && counted) atomicAdd(&count[chosen], 1);
       }
       if (on) {
-        const float inv = softmax ? 1.f : 1.f / norm.z;
-        bad |= norm.z != norm.z || norm.inv != norm.inv;
+        const float inv = softmax ? 1.f : rcp(norm.z);
+        bad |= odd;
 #pragma unroll
         for (int j = 0; j < N; ++j) acc[j] = __fmaf_rn(x[j], inv, acc[j]);
         ++seen;
@@ -492,7 +548,7 @@ __global__ void __launch_bounds__(kRouteThreads)
 }
 
 template <typename T, int L, int N, bool FULL, int SCORE>
-__global__ void __launch_bounds__(kRouteThreads, N <= 8 ? 4 : 2)
+__global__ void __launch_bounds__(kRouteThreads, route_ctas(N))
     route_grad_kernel(const T* logits, const __grid_constant__ RouteIn p, const int32_t* idx,
                       const float* d_gates, const int32_t* seq_counts, const float* seq_coef,
                       float loss_scale, T* grad, int64_t grad_ld) {
@@ -517,30 +573,47 @@ __global__ void __launch_bounds__(kRouteThreads, N <= 8 ? 4 : 2)
       b[j] = balanced && H::has(lane, j, p.E)
                  ? f * (float)seq_counts[run.seq * p.E + H::expert(lane, j)]
                  : 0.f;
-    for (int64_t t0 = run.pos + warp * (32 / L); t0 < run.stop; t0 += kGroups) {
-      const int64_t t = t0 + (tid & 31) / L;
-      const bool in = t < run.stop;
-      const bool on = in && (p.live == nullptr || p.live[t] != 0);
-      const T* row = logits + (on ? t : run.pos) * p.ld;
-      float x[N];
-      load_token<H, T, L, N>(x, row, p.E, lane, on);
-      int e = -1;
-      float dg = 0.f, xe = 0.f;
-      if (on && d_gates != nullptr && lane < p.K) {
-        e = idx[t * p.K + lane];
-        if (e < 0 || e >= p.E) e = -1;
-        if (e >= 0) {
-          dg = d_gates[t * p.K + lane];
-          xe = to_f(row[e]);
-        }
+    Raw<H, T, N> next;
+    int next_e = -1;  // lane k: choice k and its gate's gradient
+    float next_dg = 0.f;
+    auto fetch = [&](int64_t t) {
+      const bool live = t < run.stop && (p.live == nullptr || p.live[t] != 0);
+      next.fetch(logits + (live ? t : run.pos) * p.ld, p.E, lane, live);
+      next_e = -1;
+      if (live && d_gates != nullptr && lane < p.K) {
+        next_e = idx[t * p.K + lane];
+        next_dg = d_gates[t * p.K + lane];
       }
+    };
+    int64_t t = run.pos + warp * (32 / L) + (tid & 31) / L;
+    fetch(t);
+    for (int64_t t0 = run.pos + warp * (32 / L); t0 < run.stop; t0 += kGroups, t += kGroups) {
+      const bool in = t < run.stop, on = next.on;
+      float x[N];
+      if (L == 32 && !on) {
+        fetch(t + kGroups);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (H::has(lane, j, p.E)) grad[t * grad_ld + H::expert(lane, j)] = from_f<T>(0.f);
+        continue;
+      }
+      next.get(x, p.E, lane);
+      int e = next_e;
+      float dg = next_dg, xe = 0.f;
+      if (e >= 0 && e < p.E) {
+        xe = to_f(logits[t * p.ld + e]);
+      } else {
+        e = -1;
+        dg = 0.f;
+      }
+      fetch(t + kGroups);
       const Norm norm = scores<H, L, N>(x, softmax, p.E, c, lane);
       float ds[N];
       if (d_gates != nullptr) {
         float v = dg;
         if (p.renorm) {
           const float s = e >= 0 ? score_of(xe, norm, softmax, c) : 0.f;
-          const float inv = 1.f / (group_sum<L>(s) + 1e-20f);
+          const float inv = rcp(group_sum<L>(s) + 1e-20f);
           v = (dg - group_sum<L>(dg * s) * inv) * inv;
         }
         if (e >= 0) pull[e] = p.scale * v;
@@ -565,7 +638,7 @@ __global__ void __launch_bounds__(kRouteThreads, N <= 8 ? 4 : 2)
 #pragma unroll
         for (int j = 0; j < N; ++j) x[j] *= ds[j] - dot;
       } else {
-        const float inv = 1.f / norm.z;
+        const float inv = rcp(norm.z);
         if (balanced) {
 #pragma unroll
           for (int j = 0; j < N; ++j) dot = __fmaf_rn(b[j], x[j], dot);
@@ -645,13 +718,12 @@ RouteIn route_in(int64_t T_, int64_t E, int64_t ld, const float* bias, const uin
           hp->route_scale, hp->balance, bias, live, starts, 1.44269504f};
 }
 
-// CTAs: two tokens a group at least, 4 CTAs an SM at most (2 with more than
-// 256 experts: registers).
+// CTAs: two tokens a group at least, no more than run at a time.
 template <int L, int N>
 unsigned route_grid(int64_t T_) {
   const int64_t least = 2 * kRouteThreads / L;
   return (unsigned)std::max<int64_t>(
-      1, std::min<int64_t>((T_ + least - 1) / least, 152 * (N <= 8 ? 4 : 2)));
+      1, std::min<int64_t>((T_ + least - 1) / least, 152 * route_ctas(N)));
 }
 
 // Up to here the last CTA of the router finishes; beyond, a launch of its own.
