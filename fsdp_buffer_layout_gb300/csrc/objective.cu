@@ -30,9 +30,10 @@ constexpr int kMaxPipeClusters = 1024;  // clusters whose sums the workspace hol
 // Workspace: the head, the pipelined kernel's sums per cluster, then per token
 // {m, s, x_y} and the gradient's coefficient, then per pair the loss and the margin.
 struct ObjectiveWs {
-  static constexpr size_t kFront = sizeof(WsHead) + 3 * 8 * (size_t)kMaxPipeClusters;
+  static constexpr size_t kFront = sizeof(WsHead) + (3 * (size_t)kMaxPipeClusters + 2) * 8;
   WsHead* head;
-  double* partial;  // [3 * kMaxPipeClusters]
+  double* partial;  // [3 * kMaxPipeClusters] sums of clusters or CTAs
+  double* total;    // sum of the live weights, where a launch of its own adds it up
   float4* row;    // [tokens] maximum, sum and target's logit of a live row
   float* coef;    // [tokens] a of a token; 0: no gradient
   float2* pair;   // [pairs] loss and beta h
@@ -43,6 +44,7 @@ struct ObjectiveWs {
     unsigned char* p = static_cast<unsigned char*>(ws);
     head = reinterpret_cast<WsHead*>(p);
     partial = reinterpret_cast<double*>(p + sizeof(WsHead));
+    total = partial + 3 * kMaxPipeClusters;
     row = reinterpret_cast<float4*>(p + kFront);
     coef = reinterpret_cast<float*>(row + tokens);
     pair = reinterpret_cast<float2*>(p + kFront + (tokens * 20 + 15) / 16 * 16);
@@ -355,6 +357,7 @@ __global__ void __launch_bounds__(kPairThreads)
 #define VSF_PIPE_PER 4
 #endif
 #include "row_pipe.cuh"
+#include "row_regs.cuh"
 
 // ------------------------------------------------------------- host side
 struct RowsArg {
@@ -503,18 +506,6 @@ cudaError_t launch_pipe(PipeArgs<T>& a, int C, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, row_pipe_kernel<T, kPipeWarps, POLICY>, a);
 }
 
-template <typename T>
-cudaError_t launch_stats(const Rows<T>& r, float4* row, float* logp, WsHead* head,
-                         cudaStream_t st) {
-  if (r.T_ == 0) return cudaSuccess;
-  PipeArgs<T> a = {};
-  a.r = r;
-  a.row = row;
-  a.logp = logp;
-  a.head = head;
-  return launch_pipe<T, false>(a, pipe_split<T>(r.T_, r.V, false).C, st);
-}
-
 // A launch that may be set up while the kernel before it on the stream ends.
 template <typename... P, typename... A>
 cudaError_t launch_behind(void (*fn)(P...), unsigned grid, unsigned threads, cudaStream_t st,
@@ -529,6 +520,58 @@ cudaError_t launch_behind(void (*fn)(P...), unsigned grid, unsigned threads, cud
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, fn, std::forward<A>(args)...);
+}
+
+// Rows short enough for the registers of 8 warps at 8 vectors a thread.
+template <typename T>
+bool short_rows(int64_t V) {
+#ifndef VSF_SHORT
+#define VSF_SHORT (8 * kRegsThreads)
+#endif
+  return V / Vec<T>::n <= VSF_SHORT;
+}
+
+template <typename T, bool POLICY, int G, int NV>
+cudaError_t launch_regs_as(const PipeArgs<T>& a, const ObjectiveWs& w, cudaStream_t st) {
+  const int64_t rows = 8 / G, most = 152 * (NV <= 4 ? 4 : 3);
+  const unsigned grid =
+      (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, (a.r.T_ + rows - 1) / rows));
+  static_assert(152 * 4 <= kMaxPipeClusters, "the workspace holds a sum of every CTA");
+  const double* total = nullptr;
+  if (POLICY && a.p.mean && a.r.T_ > 2048) {
+    total = w.total;
+    const unsigned n = (unsigned)std::min<int64_t>(64, (a.r.T_ + 2047) / 2048);
+    weight_sum_kernel<<<n, 512, 0, st>>>(a.r.target, a.r.weight, a.r.T_, a.r.V, w.partial, w.total,
+                                         w.head);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_behind(row_regs_kernel<T, G, NV, POLICY>, grid, kRegsThreads, st, a, total);
+  }
+  row_regs_kernel<T, G, NV, POLICY><<<grid, kRegsThreads, 0, st>>>(a, total);
+  return cudaGetLastError();
+}
+
+template <typename T, bool POLICY>
+cudaError_t launch_regs(const PipeArgs<T>& a, const ObjectiveWs& w, cudaStream_t st) {
+  const int64_t nvec = a.r.V / Vec<T>::n;
+  if (nvec <= 4 * 32) return launch_regs_as<T, POLICY, 1, 4>(a, w, st);
+  if (nvec <= 4 * 64) return launch_regs_as<T, POLICY, 2, 4>(a, w, st);
+  if (nvec <= 4 * 128) return launch_regs_as<T, POLICY, 4, 4>(a, w, st);
+  if (nvec <= 4 * 256) return launch_regs_as<T, POLICY, 8, 4>(a, w, st);
+  return launch_regs_as<T, POLICY, 8, 8>(a, w, st);
+}
+
+template <typename T>
+cudaError_t launch_stats(const Rows<T>& r, float4* row, float* logp, const ObjectiveWs& w,
+                         cudaStream_t st) {
+  if (r.T_ == 0) return cudaSuccess;
+  PipeArgs<T> a = {};
+  a.r = r;
+  a.row = row;
+  a.logp = logp;
+  a.head = w.head;
+  if (short_rows<T>(r.V)) return launch_regs<T, false>(a, w, st);
+  return launch_pipe<T, false>(a, pipe_split<T>(r.T_, r.V, false).C, st);
 }
 
 template <typename T>
@@ -546,22 +589,23 @@ template <typename T>
 cudaError_t policy(const RowsArg& a, const PolicyIn& p, float* stats, float* logp, void* grad,
                    int64_t grad_ld, const ObjectiveWs& w, cudaStream_t st) {
   const Rows<T> r = rows_of<T>(a);
+  PipeArgs<T> k = {};
+  k.r = r;
+  k.p = p;
+  k.grad = static_cast<T*>(grad);
+  k.grad_ld = grad_ld;
+  k.logp = logp;
+  k.stats = stats;
+  k.head = w.head;
+  k.partial = w.partial;
+  if (short_rows<T>(r.V)) return launch_regs<T, true>(k, w, st);
   const PipeSplit split = pipe_split<T>(r.T_, r.V, true);
   if (split.C > 0) {
-    PipeArgs<T> k = {};
-    k.r = r;
-    k.p = p;
-    k.grad = static_cast<T*>(grad);
-    k.grad_ld = grad_ld;
-    k.logp = logp;
-    k.stats = stats;
-    k.head = w.head;
-    k.partial = w.partial;
     k.ahead = split.ahead;
     return launch_pipe<T, true>(k, split.C, st);
   }
   // a row too long for a cluster's shared memory: statistics, then gradient
-  cudaError_t e = launch_stats(r, w.row, logp, w.head, st);
+  cudaError_t e = launch_stats(r, w.row, logp, w, st);
   if (e != cudaSuccess) return e;
   policy_tokens_kernel<T><<<1, kTokenThreads, 0, st>>>(r, p, w.row, w.coef, stats);
   e = cudaGetLastError();
@@ -573,7 +617,7 @@ template <typename T>
 cudaError_t preference(const RowsArg& a, const PairIn& p, float* stats, float* logp, void* grad,
                        int64_t grad_ld, const ObjectiveWs& w, cudaStream_t st) {
   const Rows<T> r = rows_of<T>(a);
-  cudaError_t e = launch_stats(r, w.row, logp, w.head, st);
+  cudaError_t e = launch_stats(r, w.row, logp, w, st);
   if (e != cudaSuccess) return e;
   e = launch_behind(pair_kernel<T>, (unsigned)p.pairs, kPairThreads, st, r, p,
                     (const float4*)w.row, w.coef, w.pair, stats, w.head);
@@ -615,8 +659,8 @@ vsf_status vsf_token_logprobs(const void* logits, int32_t dtype, int64_t T, int6
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const ObjectiveWs w(d_workspace, T);
   const cudaError_t e =
-      dtype == VSF_BF16 ? launch_stats(rows_of<uint16_t>(a), nullptr, logp, w.head, st)
-                        : launch_stats(rows_of<float>(a), nullptr, logp, w.head, st);
+      dtype == VSF_BF16 ? launch_stats(rows_of<uint16_t>(a), nullptr, logp, w, st)
+                        : launch_stats(rows_of<float>(a), nullptr, logp, w, st);
   return e == cudaSuccess ? VSF_OK : cuda_error(e, "vsf_token_logprobs");
 }
 

@@ -365,6 +365,23 @@ __device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity,
   return __all_sync(~0u, mbar_wait_cluster(bar, parity, err, stop));
 }
 
+// The loss from the sums of n clusters or CTAs, in their order; one warp.
+template <typename T>
+__device__ __forceinline__ void policy_stats(const PipeArgs<T>& a, int64_t n, int lane) {
+  double v[3] = {0.0, 0.0, 0.0};
+  for (int64_t c = lane; c < n; c += 32)
+    for (int j = 0; j < 3; ++j) v[j] += __ldcg(a.partial + 3 * c + j);
+  for (int j = 0; j < 3; ++j) v[j] = warp_sum(v[j]);
+  if (lane == 0) {
+    const double f = (double)a.p.scale / (a.p.mean && v[2] != 0.0 ? v[2] : 1.0);
+    a.stats[0] = (float)(f * (v[0] + (a.p.beta != 0.f ? (double)a.p.beta * v[1] : 0.0)));
+    a.stats[1] = (float)(f * v[0]);
+    a.stats[2] = (float)(f * v[1]);
+    a.stats[3] = (float)v[2];
+    a.head->ticket = 0;
+  }
+}
+
 // A row whose gradient is still to be written.
 template <uint32_t SLOTS>
 struct Pending {
@@ -665,20 +682,7 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
           last = atomicAdd(&a.head->ticket, 1u) + 1 == (uint32_t)clusters;
           __threadfence();
         }
-        if (__shfl_sync(~0u, last, 0)) {
-          double v[3] = {0.0, 0.0, 0.0};
-          for (int64_t c = lane; c < clusters; c += 32)
-            for (int j = 0; j < 3; ++j) v[j] += __ldcg(a.partial + 3 * c + j);
-          for (int j = 0; j < 3; ++j) v[j] = warp_sum(v[j]);
-          if (lane == 0) {
-            const double f = (double)a.p.scale / (a.p.mean && v[2] != 0.0 ? v[2] : 1.0);
-            a.stats[0] = (float)(f * (v[0] + (a.p.beta != 0.f ? (double)a.p.beta * v[1] : 0.0)));
-            a.stats[1] = (float)(f * v[0]);
-            a.stats[2] = (float)(f * v[1]);
-            a.stats[3] = (float)v[2];
-            a.head->ticket = 0;
-          }
-        }
+        if (__shfl_sync(~0u, last, 0)) policy_stats(a, clusters, lane);
       }
     } else {  // ---------------------------------------------------- consumers
       const PairScale c2 = {f2(r.c.hi, r.c.hi), f2(r.c.lo, r.c.lo)};
