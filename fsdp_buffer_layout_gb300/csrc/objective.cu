@@ -14,7 +14,6 @@
 #include <algorithm>
 #include <cmath>
 #include <mutex>
-#include <utility>
 
 #include "objective.cuh"
 
@@ -197,6 +196,7 @@ template <typename T>
 __global__ void __launch_bounds__(kTokenThreads)
     policy_tokens_kernel(Rows<T> r, PolicyIn p, const float4* row, float* coef, float* stats) {
   __shared__ double part[kTokenThreads / 32];
+  take_turn();
   double n = 0.0;
   for (int64_t t = threadIdx.x; t < r.T_; t += kTokenThreads)
     if (live_target(r, t, nullptr) >= 0) n += r.weight != nullptr ? (double)r.weight[t] : 1.0;
@@ -273,7 +273,9 @@ __global__ void __launch_bounds__(kPairThreads)
                 WsHead* head) {
   __shared__ float2 part[kPairThreads / 32];
   __shared__ bool last;
-  cudaGridDependencySynchronize();
+  // (the gradient's CTAs set up while rows are still summed ended up unevenly
+  // on the SMs: 291 us instead of 262 for 16 pairs of 384 x 32000)
+  take_turn(false);
   const int64_t q = blockIdx.x;
   float ratio[2], length[2];
   int64_t first[2], end[2];
@@ -491,35 +493,9 @@ cudaError_t launch_pipe(PipeArgs<T>& a, int C, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   const int most = pipe_clusters<T, POLICY>(C, &e);
   if (most == 0) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(C * std::max<int64_t>(1, std::min<int64_t>(most, a.r.T_))));
-  cfg.blockDim = dim3(Shape::threads);
-  cfg.dynamicSmemBytes = pipe_smem<kPipeWarps>();
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, row_pipe_kernel<T, kPipeWarps, POLICY>, a);
-}
-
-// A launch that may be set up while the kernel before it on the stream ends.
-template <typename... P, typename... A>
-cudaError_t launch_behind(void (*fn)(P...), unsigned grid, unsigned threads, cudaStream_t st,
-                          A&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, std::forward<A>(args)...);
+  return launch_behind(row_pipe_kernel<T, kPipeWarps, POLICY>,
+                       (unsigned)(C * std::max<int64_t>(1, std::min<int64_t>(most, a.r.T_))),
+                       Shape::threads, pipe_smem<kPipeWarps>(), C, st, a);
 }
 
 // Rows short enough for the registers of 8 warps at 8 vectors a thread.
@@ -540,15 +516,12 @@ cudaError_t launch_regs_as(const PipeArgs<T>& a, const ObjectiveWs& w, cudaStrea
   const double* total = nullptr;
   if (POLICY && a.p.mean && a.r.T_ > 2048) {
     total = w.total;
-    const unsigned n = (unsigned)std::min<int64_t>(64, (a.r.T_ + 2047) / 2048);
-    weight_sum_kernel<<<n, 512, 0, st>>>(a.r.target, a.r.weight, a.r.T_, a.r.V, w.partial, w.total,
-                                         w.head);
-    const cudaError_t e = cudaGetLastError();
+    const unsigned n = (unsigned)std::min<int64_t>(64, (a.r.T_ + 1023) / 1024);
+    const cudaError_t e = launch_behind(weight_sum_kernel, n, 512, 0, 1, st, a.r.target, a.r.weight,
+                                        a.r.T_, a.r.V, w.partial, w.total, w.head);
     if (e != cudaSuccess) return e;
-    return launch_behind(row_regs_kernel<T, G, NV, POLICY>, grid, kRegsThreads, st, a, total);
   }
-  row_regs_kernel<T, G, NV, POLICY><<<grid, kRegsThreads, 0, st>>>(a, total);
-  return cudaGetLastError();
+  return launch_behind(row_regs_kernel<T, G, NV, POLICY>, grid, kRegsThreads, 0, 1, st, a, total);
 }
 
 template <typename T, bool POLICY>
@@ -581,7 +554,7 @@ cudaError_t launch_grad(const Rows<T>& r, const ObjectiveWs& w, void* grad, int6
   const int32_t pieces =
       (int32_t)std::max<int64_t>(1, (r.V / Vec<T>::n + kGradPiece - 1) / kGradPiece);
   return launch_behind(row_grad_kernel<T>, (unsigned)std::min<int64_t>(r.T_ * pieces, 152 * 4),
-                       kGradThreads, st, r, (const float4*)w.row, (const float*)w.coef,
+                       kGradThreads, 0, 1, st, r, (const float4*)w.row, (const float*)w.coef,
                        static_cast<T*>(grad), grad_ld, pieces);
 }
 
@@ -607,8 +580,8 @@ cudaError_t policy(const RowsArg& a, const PolicyIn& p, float* stats, float* log
   // a row too long for a cluster's shared memory: statistics, then gradient
   cudaError_t e = launch_stats(r, w.row, logp, w, st);
   if (e != cudaSuccess) return e;
-  policy_tokens_kernel<T><<<1, kTokenThreads, 0, st>>>(r, p, w.row, w.coef, stats);
-  e = cudaGetLastError();
+  e = launch_behind(policy_tokens_kernel<T>, 1, kTokenThreads, 0, 1, st, r, p, (const float4*)w.row,
+                    w.coef, stats);
   if (e != cudaSuccess) return e;
   return launch_grad(r, w, grad, grad_ld, st);
 }
@@ -619,7 +592,7 @@ cudaError_t preference(const RowsArg& a, const PairIn& p, float* stats, float* l
   const Rows<T> r = rows_of<T>(a);
   cudaError_t e = launch_stats(r, w.row, logp, w, st);
   if (e != cudaSuccess) return e;
-  e = launch_behind(pair_kernel<T>, (unsigned)p.pairs, kPairThreads, st, r, p,
+  e = launch_behind(pair_kernel<T>, (unsigned)p.pairs, kPairThreads, 0, 1, st, r, p,
                     (const float4*)w.row, w.coef, w.pair, stats, w.head);
   if (e != cudaSuccess) return e;
   return launch_grad(r, w, grad, grad_ld, st);

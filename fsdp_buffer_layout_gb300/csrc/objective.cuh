@@ -10,6 +10,7 @@
 #include <cmath>
 #include <cstdint>
 #include <string>
+#include <utility>
 
 #include "vsf_internal.h"
 
@@ -76,6 +77,38 @@ __device__ __forceinline__ float exp_scaled(float d, Log2Scale c) {
 // What a maximum is subtracted as: -inf - (-inf) would be NaN where a run of
 // -inf logits comes first.
 __device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.f : m; }
+
+// At the start of each kernel, before it touches global memory: the kernel
+// behind it on the stream may be set up on the SMs already (early; where it was
+// launched by launch_behind; it waits here in its turn), then wait for the end
+// of the kernels before it.
+__device__ __forceinline__ void take_turn(bool early = true) {
+  if (early) cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
+}
+
+// A launch that may be set up while the kernel before it on the stream runs
+// out, in clusters of C CTAs (C > 1). It pays for calls of a few microseconds:
+// set-up, first loads of parameters and barriers come off each.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*fn)(P...), unsigned grid, unsigned threads, unsigned smem, int C,
+                          cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)C;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, fn, std::forward<A>(args)...);
+}
 
 inline vsf_status cuda_error(cudaError_t e, const char* who) {
   return fail(VSF_ERR_CUDA, std::string(who) + ": " + cudaGetErrorString(e));

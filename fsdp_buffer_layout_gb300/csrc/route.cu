@@ -396,6 +396,7 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(N))
   for (int e = tid; e < N * L; e += kRouteThreads) count[e] = 0;
   if (tid == 0) tokens = 0;
   __syncthreads();
+  take_turn();
   const bool softmax = SCORE < 0 ? p.score == VSF_SCORE_SOFTMAX : SCORE == VSF_SCORE_SOFTMAX;
   const float c = p.c;
   float bias[N];
@@ -528,6 +529,7 @@ __global__ void __launch_bounds__(kRouteThreads)
                         const __grid_constant__ RouteOut o, WsHead* head) {
   __shared__ int last;
   const int e0 = blockIdx.x * kFinishExperts, tid = threadIdx.x;
+  take_turn();
   const float l = route_finish(p, w, o, e0, min(kFinishExperts, p.E - e0), blockIdx.x == 0);
   if (tid == 0) {
     head->part[blockIdx.x] = l;
@@ -560,6 +562,7 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(N))
 #pragma unroll
   for (int j = 0; j < N; ++j) pull[lane + L * j] = 0.f;
   __syncwarp();
+  take_turn();
   const bool softmax = SCORE < 0 ? p.score == VSF_SCORE_SOFTMAX : SCORE == VSF_SCORE_SOFTMAX;
   const float c = p.c;
   const int64_t per = (p.T_ + gridDim.x - 1) / gridDim.x;
@@ -733,22 +736,21 @@ template <typename T, int L, int N, bool FULL, int SCORE>
 cudaError_t route_launch(const void* logits, const RouteIn& p, const RouteOut& o, const RouteWs& w,
                          cudaStream_t st) {
   const bool inside = p.E * p.sequences <= kFinishInside;
-  route_kernel<T, L, N, FULL, SCORE><<<route_grid<L, N>(p.T_), kRouteThreads, 0, st>>>(
-      static_cast<const T*>(logits), p, w.sums, o, w.head, inside);
-  if (!inside)
-    route_finish_kernel<<<(p.E + kFinishExperts - 1) / kFinishExperts, kRouteThreads, 0, st>>>(
-        p, w.sums, o, w.head);
-  return cudaGetLastError();
+  const cudaError_t e = launch_behind(route_kernel<T, L, N, FULL, SCORE>, route_grid<L, N>(p.T_),
+                                      kRouteThreads, 0, 1, st, static_cast<const T*>(logits), p,
+                                      w.sums, o, w.head, (int32_t)inside);
+  if (e != cudaSuccess || inside) return e;
+  return launch_behind(route_finish_kernel, (p.E + kFinishExperts - 1) / kFinishExperts,
+                       kRouteThreads, 0, 1, st, p, w.sums, o, w.head);
 }
 
 template <typename T, int L, int N, bool FULL, int SCORE>
 cudaError_t grad_launch(const void* logits, const RouteIn& p, const int32_t* idx,
                         const float* d_gates, const int32_t* seq_counts, const float* seq_coef,
                         float loss_scale, void* grad, int64_t grad_ld, cudaStream_t st) {
-  route_grad_kernel<T, L, N, FULL, SCORE><<<route_grid<L, N>(p.T_), kRouteThreads, 0, st>>>(
-      static_cast<const T*>(logits), p, idx, d_gates, seq_counts, seq_coef, loss_scale,
-      static_cast<T*>(grad), grad_ld);
-  return cudaGetLastError();
+  return launch_behind(route_grad_kernel<T, L, N, FULL, SCORE>, route_grid<L, N>(p.T_),
+                       kRouteThreads, 0, 1, st, static_cast<const T*>(logits), p, idx, d_gates,
+                       seq_counts, seq_coef, loss_scale, static_cast<T*>(grad), grad_ld);
 }
 
 // F<T, lanes a token, experts a lane, full, score> for the experts of p; wide:

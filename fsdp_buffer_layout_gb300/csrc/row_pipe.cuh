@@ -436,6 +436,7 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
   }
   __syncthreads();
   if (C > 1) cluster_sync();
+  take_turn();
 
   if (warp == W) {  // -------------------------------------------- producer
     Place<slots> at;
@@ -891,7 +892,7 @@ __global__ void __launch_bounds__(kGradThreads, 4)
     row_grad_kernel(const __grid_constant__ Rows<T> r, const float4* row, const float* coef,
                     T* grad, int64_t grad_ld, int32_t pieces) {
   constexpr int VE = Vec<T>::n;
-  cudaGridDependencySynchronize();
+  take_turn();
   const int tid = threadIdx.x;
   const PairScale c2 = {f2(r.c.hi, r.c.hi), f2(r.c.lo, r.c.lo)};
   const int64_t items = r.T_ * pieces;

@@ -16,6 +16,7 @@ __global__ void __launch_bounds__(512)
                       double* partial, double* total, WsHead* head) {
   __shared__ double part[16];
   __shared__ bool last;
+  take_turn();
   float w2[2] = {0.f, 0.f};
   const int64_t step = (int64_t)gridDim.x * 512;
   int64_t t = (int64_t)blockIdx.x * 512 + threadIdx.x;
@@ -55,6 +56,7 @@ __global__ void __launch_bounds__(kRegsThreads, NV <= 4 ? 4 : 3)
   const PairScale c2 = {f2(r.c.hi, r.c.hi), f2(r.c.lo, r.c.lo)};
   const float c1 = (uint32_t)gtid * 2654435769u < r.c.ups ? r.c.up : r.c.hi;
   const F2 cc = f2(c1, c1);
+  take_turn();
   Token next = token_at(r, first);
   float scale = 0.f;
   if (POLICY) {
@@ -70,7 +72,6 @@ __global__ void __launch_bounds__(kRegsThreads, NV <= 4 ? 4 : 3)
       __syncthreads();
       for (int i = 0; i < 8; ++i) n += (double)weights[i];
     } else if (a.p.mean) {
-      cudaGridDependencySynchronize();
       n = __ldcg(total);
     }
     scale = (float)((double)a.p.scale / (a.p.mean && n != 0.0 ? n : 1.0) * r.inv_t);
