@@ -246,56 +246,52 @@ __device__ __forceinline__ int64_t clamp_start(int64_t v, int64_t T_) {
 // first sequence and behind the last one get the coefficient 0. All in fp32 but
 // the sum over pairs: fp64 runs at a 64th of the rate here, and a version in
 // fp64 took 40 us for two pairs.
-constexpr int kPairThreads = 256;
-
-// Sums of two values over the CTA, the same in every thread.
-__device__ __forceinline__ float2 block_sum2(float a, float b, float2* part) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(~0u, a, o);
-    b += __shfl_xor_sync(~0u, b, o);
-  }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(a, b);
-  __syncthreads();
-  a = b = 0.f;
-#pragma unroll
-  for (int w = 0; w < kPairThreads / 32; ++w) {
-    a += part[w].x;
-    b += part[w].y;
-  }
-  return make_float2(a, b);
-}
+constexpr int kPairThreads = 512;  // half of them a sequence
 
 template <typename T>
 __global__ void __launch_bounds__(kPairThreads)
     pair_kernel(Rows<T> r, PairIn p, const float4* row, float* coef, float2* pair, float* stats,
                 WsHead* head) {
+  constexpr int kSide = kPairThreads / 2;
   __shared__ float2 part[kPairThreads / 32];
   __shared__ bool last;
   // (the gradient's CTAs set up while rows are still summed ended up unevenly
   // on the SMs: 291 us instead of 262 for 16 pairs of 384 x 32000)
   take_turn(false);
   const int64_t q = blockIdx.x;
-  float ratio[2], length[2];
-  int64_t first[2], end[2];
-  for (int side = 0; side < 2; ++side) {
-    first[side] = clamp_start(p.starts[side * p.pairs + q], r.T_);
-    end[side] = clamp_start(p.starts[side * p.pairs + q + 1], r.T_);
-    float d = 0.f, n = 0.f;
-    for (int64_t t = first[side] + threadIdx.x; t < end[side]; t += kPairThreads) {
-      const Token k = token_at(r, t);
-      if (live_target(r, k, nullptr) < 0) continue;
-      const float4 ms = row[t];
-      d += k.w * exact_log_ratio(ms.z - ms.x, r.inv_tf, p.ref_logp != nullptr ? p.ref_logp[t] : 0.f,
-                                 log_sum(ms.y));
-      n += k.w;
-    }
-    const float2 sum = block_sum2(d, n, part);
-    length[side] = p.average && sum.y != 0.f ? sum.y : 1.f;
-    ratio[side] = sum.x / length[side];
-    if (threadIdx.x == 0 && p.rewards != nullptr) p.rewards[side * p.pairs + q] = p.beta * ratio[side];
+  const int side = threadIdx.x / kSide, tid = threadIdx.x & (kSide - 1);
+  const int64_t first = clamp_start(p.starts[side * p.pairs + q], r.T_);
+  const int64_t end = clamp_start(p.starts[side * p.pairs + q + 1], r.T_);
+  float d = 0.f, n = 0.f;
+  for (int64_t t = first + tid; t < end; t += kSide) {
+    const Token k = token_at(r, t);
+    const float4 ms = row[t];
+    const float ref = p.ref_logp != nullptr ? p.ref_logp[t] : 0.f;
+    if (live_target(r, k, nullptr) < 0) continue;
+    d += k.w * exact_log_ratio(ms.z - ms.x, r.inv_tf, ref, log_sum(ms.y));
+    n += k.w;
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    d += __shfl_xor_sync(~0u, d, o);
+    n += __shfl_xor_sync(~0u, n, o);
+  }
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(d, n);
+  __syncthreads();
+  float ratio[2], length[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    d = n = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSide / 32; ++w) {
+      d += part[s * (kSide / 32) + w].x;
+      n += part[s * (kSide / 32) + w].y;
+    }
+    length[s] = p.average && n != 0.f ? n : 1.f;
+    ratio[s] = d / length[s];
+  }
+  if (tid == 0 && p.rewards != nullptr)
+    p.rewards[side * p.pairs + q] = p.beta * (side ? ratio[1] : ratio[0]);
   const float h = ratio[0] - ratio[1];
   float loss, slope;
   if (p.kind == VSF_PREF_SIGMOID) {
@@ -317,12 +313,11 @@ __global__ void __launch_bounds__(kPairThreads)
     last = atomicAdd(&head->ticket, 1u) + 1 == gridDim.x;
     __threadfence();
   }
-  for (int side = 0; side < 2; ++side) {
-    const float a = (side ? -1.f : 1.f) * p.scale / (float)p.pairs * slope / length[side] * r.inv_tf;
-    for (int64_t t = first[side] + threadIdx.x; t < end[side]; t += kPairThreads) {
-      const Token k = token_at(r, t);
-      coef[t] = live_target(r, k, nullptr) < 0 ? 0.f : a * k.w;
-    }
+  const float a = (side ? -1.f : 1.f) * p.scale / (float)p.pairs * slope /
+                  (side ? length[1] : length[0]) * r.inv_tf;
+  for (int64_t t = first + tid; t < end; t += kSide) {
+    const Token k = token_at(r, t);
+    coef[t] = live_target(r, k, nullptr) < 0 ? 0.f : a * k.w;
   }
   if (q == 0) {
     const int64_t b = clamp_start(p.starts[0], r.T_);
@@ -553,7 +548,7 @@ cudaError_t launch_grad(const Rows<T>& r, const ObjectiveWs& w, void* grad, int6
   if (r.T_ == 0 || grad == nullptr) return cudaSuccess;
   const int32_t pieces =
       (int32_t)std::max<int64_t>(1, (r.V / Vec<T>::n + kGradPiece - 1) / kGradPiece);
-  return launch_behind(row_grad_kernel<T>, (unsigned)std::min<int64_t>(r.T_ * pieces, 152 * 4),
+  return launch_behind(row_grad_kernel<T>, (unsigned)std::min<int64_t>(r.T_ * pieces, 152 * kGradCtas),
                        kGradThreads, 0, 1, st, r, (const float4*)w.row, (const float*)w.coef,
                        static_cast<T*>(grad), grad_ld, pieces);
 }

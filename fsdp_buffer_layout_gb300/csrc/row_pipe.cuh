@@ -880,83 +880,109 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
 // ------------------------------------------------------------ gradient alone
 // The gradient's rows where a row's coefficient is known only after the sums of
 // all rows (preference loss), or its share of a cluster's shared memory is too
-// long. A thread takes eight vectors of a row at a time. Rows are taken last
+// long. A thread takes six vectors of a row at a time
+// (four and eight are within 2 percent of it). Rows are taken last
 // first: the pass before read them first to last, so that the end of the logits
 // is still in L2.
 constexpr int kGradThreads = 256;
-constexpr int kGradVecs = 8;
+constexpr int kGradVecs = 6;
+constexpr int kGradCtas = 4;  // an SM
 constexpr int kGradPiece = kGradThreads * kGradVecs;  // vectors of a row at a time
 
+// One piece of a gradient row: y < 0 or a = 0: zeros.
 template <typename T>
-__global__ void __launch_bounds__(kGradThreads, 4)
-    row_grad_kernel(const __grid_constant__ Rows<T> r, const float4* row, const float* coef,
-                    T* grad, int64_t grad_ld, int32_t pieces) {
+__device__ __forceinline__ void grad_piece(const Rows<T>& r, int64_t t, int32_t piece,
+                                           int32_t pieces, int32_t y, float a, const float4& st,
+                                           T* grad, int64_t grad_ld) {
   constexpr int VE = Vec<T>::n;
-  take_turn();
   const int tid = threadIdx.x;
   const PairScale c2 = {f2(r.c.hi, r.c.hi), f2(r.c.lo, r.c.lo)};
+  T* g = grad + t * grad_ld;
+  const T* x = r.x + t * r.ld;
+  const Span s = span_of(g, r.V);
+  const int32_t begin = piece * kGradPiece;
+  const int32_t end = piece + 1 == pieces ? s.nvec : min(s.nvec, begin + kGradPiece);
+  const int32_t tail = s.head + s.nvec * VE;
+  // the loose element of this thread, if any
+  int32_t loose = -1;
+  if (piece == 0 && tid < s.head) loose = tid;
+  if (piece + 1 == pieces && tid >= 16 && tail + tid - 16 < r.V) loose = tail + tid - 16;
+  uint4* out = reinterpret_cast<uint4*>(g + s.head) + tid;
+  if (y < 0 || a == 0.f) {
+    for (int32_t v = begin; v + tid < end; v += kGradThreads)
+      __stcs(out + v, make_uint4(0, 0, 0, 0));
+    if (loose >= 0) g[loose] = from_f<T>(0.f);
+    return;
+  }
+  const float z = finite_max(st.x), b = -a / st.y;
+  if (loose >= 0) {
+    const float e = b * exp_scaled(to_f(x[loose]) - z, r.c);
+    g[loose] = from_f<T>(loose == y ? e + a : e);
+  }
+  const int32_t ye = y - s.head, yv = ye / VE;
+  const bool mine = ye >= 0 && yv >= begin && yv < end;  // the target is in this piece
+  if (((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0) {
+    const bool near = sizeof(T) == 2 && fabsf(z) < 1e30f;
+    const F2 nm = f2(-z, -z), b2 = f2(b, b), c0 = f2(r.c.hi, r.c.hi);
+    const F2 kk = f2(-z * r.c.hi, -z * r.c.hi);
+    const uint4* in = reinterpret_cast<const uint4*>(x + s.head) + tid;
+    for (int32_t v = begin; v < end; v += kGradPiece) {
+      uint4 q[kGradVecs];
+#pragma unroll
+      for (int j = 0; j < kGradVecs; ++j)
+        if (v + j * kGradThreads + tid < end) q[j] = __ldcs(in + v + j * kGradThreads);
+#pragma unroll
+      for (int j = 0; j < kGradVecs; ++j) {
+        if (v + j * kGradThreads + tid >= end) break;
+        Pairs<T> e;
+        unpack(q[j], e);
+        float o[VE];
+#pragma unroll
+        for (int k = 0; k < VE / 2; ++k)
+          f2_get(f2_mul(near ? exp2_pair(f2_fma(e.p[k], c0, kk)) : exp_pair(e.p[k], nm, c2), b2),
+                 o[2 * k], o[2 * k + 1]);
+        __stcs(out + v + j * kGradThreads, pack_vec<T>(o));
+      }
+    }
+    if (mine && tid == ((yv - begin) & (kGradThreads - 1)))
+      g[y] = from_f<T>(b * exp_scaled(st.z - z, r.c) + a);
+  } else {
+    const int32_t first = s.head + begin * VE, n = (end - begin) * VE;
+    for (int32_t k = tid; k < n; k += kGradThreads) {
+      const float e = b * exp_scaled(to_f(x[first + k]) - z, r.c);
+      g[first + k] = from_f<T>(first + k == y ? e + a : e);
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kGradThreads, kGradCtas)
+    row_grad_kernel(const __grid_constant__ Rows<T> r, const float4* row, const float* coef,
+                    T* grad, int64_t grad_ld, int32_t pieces) {
+  take_turn();
   const int64_t items = r.T_ * pieces;
+  // what a piece needs of its row, on its way while the piece before is written
+  int64_t t = 0;
+  int32_t piece = 0;
+  Token k = {-1, 0.f};
+  float a = 0.f;
+  float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto fetch = [&](int64_t i) {
+    if (i >= items) return;
+    t = r.T_ - 1 - i / pieces;
+    piece = (int32_t)(i % pieces);
+    k = token_at(r, t);
+    a = coef[t];
+    st = row[t];
+  };
+  fetch(blockIdx.x);
   for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
-    const int64_t t = r.T_ - 1 - i / pieces;
-    const int32_t piece = (int32_t)(i % pieces);
-    const int32_t y = live_target(r, t, nullptr);
-    const float a = coef[t];
-    const float4 st = row[t];
-    T* g = grad + t * grad_ld;
-    const T* x = r.x + t * r.ld;
-    const Span s = span_of(g, r.V);
-    const int32_t begin = piece * kGradPiece;
-    const int32_t end = piece + 1 == pieces ? s.nvec : min(s.nvec, begin + kGradPiece);
-    const int32_t tail = s.head + s.nvec * VE;
-    // the loose element of this thread, if any
-    int32_t loose = -1;
-    if (piece == 0 && tid < s.head) loose = tid;
-    if (piece + 1 == pieces && tid >= 16 && tail + tid - 16 < r.V) loose = tail + tid - 16;
-    uint4* out = reinterpret_cast<uint4*>(g + s.head) + tid;
-    if (y < 0 || a == 0.f) {
-      for (int32_t v = begin; v + tid < end; v += kGradThreads)
-        __stcs(out + v, make_uint4(0, 0, 0, 0));
-      if (loose >= 0) g[loose] = from_f<T>(0.f);
-      continue;
-    }
-    const float z = finite_max(st.x), b = -a / st.y;
-    if (loose >= 0) {
-      const float e = b * exp_scaled(to_f(x[loose]) - z, r.c);
-      g[loose] = from_f<T>(loose == y ? e + a : e);
-    }
-    const int32_t ye = y - s.head, yv = ye / VE;
-    const bool mine = ye >= 0 && yv >= begin && yv < end;  // the target is in this piece
-    if (((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0) {
-      const bool near = sizeof(T) == 2 && fabsf(z) < 1e30f;
-      const F2 nm = f2(-z, -z), b2 = f2(b, b), c0 = f2(r.c.hi, r.c.hi);
-      const F2 kk = f2(-z * r.c.hi, -z * r.c.hi);
-      const uint4* in = reinterpret_cast<const uint4*>(x + s.head) + tid;
-      for (int32_t v = begin; v < end; v += kGradPiece) {
-        uint4 q[kGradVecs];
-#pragma unroll
-        for (int j = 0; j < kGradVecs; ++j)
-          if (v + j * kGradThreads + tid < end) q[j] = __ldcs(in + v + j * kGradThreads);
-#pragma unroll
-        for (int j = 0; j < kGradVecs; ++j) {
-          if (v + j * kGradThreads + tid >= end) break;
-          Pairs<T> e;
-          unpack(q[j], e);
-          float o[VE];
-#pragma unroll
-          for (int k = 0; k < VE / 2; ++k)
-            f2_get(f2_mul(near ? exp2_pair(f2_fma(e.p[k], c0, kk)) : exp_pair(e.p[k], nm, c2), b2),
-                   o[2 * k], o[2 * k + 1]);
-          __stcs(out + v + j * kGradThreads, pack_vec<T>(o));
-        }
-      }
-      if (mine && tid == ((yv - begin) & (kGradThreads - 1)))
-        g[y] = from_f<T>(b * exp_scaled(st.z - z, r.c) + a);
-    } else {
-      const int32_t first = s.head + begin * VE, n = (end - begin) * VE;
-      for (int32_t k = tid; k < n; k += kGradThreads) {
-        const float e = b * exp_scaled(to_f(x[first + k]) - z, r.c);
-        g[first + k] = from_f<T>(first + k == y ? e + a : e);
-      }
-    }
+    const int64_t t0 = t;
+    const int32_t piece0 = piece;
+    const int32_t y = live_target(r, k, nullptr);
+    const float a0 = a;
+    const float4 st0 = st;
+    fetch(i + gridDim.x);
+    grad_piece(r, t0, piece0, pieces, y, a0, st0, grad, grad_ld);
   }
 }
