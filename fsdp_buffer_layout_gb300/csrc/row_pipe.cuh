@@ -489,8 +489,27 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
       if (lane == 0) ok = stream(true);
       return __shfl_sync(~0u, (int)ok, 0) != 0;
     };
-    if (listed)  // the list is there
+    auto fetch = [&](int t) -> RowItem {
+      RowItem it = {t, -1, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (t < 0) return it;
+      const Token k = token_at(r, it.t);
+      it.y = live_target(r, k, nullptr);
+      it.w = k.w;
+      if (it.y < 0) return it;
+      it.xy = to_f(r.x[(int64_t)it.t * r.ld + it.y]);
+      if (POLICY) {
+        it.old = a.p.old_logp[it.t];
+        it.adv = a.p.adv[it.t];
+        if (a.p.beta != 0.f) it.ref = a.p.ref_logp[it.t];
+      }
+      return it;
+    };
+    bool ok = true;
+    if (listed) {  // the first row at once; the others when the list is there
+      const RowItem now = fetch(lane == 0 ? (int)cluster : -1);
+      if (POLICY || __shfl_sync(~0u, now.y, 0) >= 0) ok = hand_on(now, 0);
       asm volatile("bar.sync 1, %0;" ::"r"(Shape::threads) : "memory");
+    }
     // Rows in turn, masked ones spread among the live ones; a lane fetches what
     // the joiner needs of a row, 32 rows at a time and as many ahead.
     const int n_live = listed ? sh->n_live : 0, n_rows = listed ? n_live + sh->n_dead : 0;
@@ -505,27 +524,11 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
       const int after = ((i + 1) * n_live + n_rows - 1) / n_rows;
       return after > before ? sh->rows[before] : sh->rows[kList - 1 - (i - before)];
     };
-    auto fetch = [&](int i) -> RowItem {
-      RowItem it = {row_at(i), -1, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (it.t < 0) return it;
-      const Token k = token_at(r, it.t);
-      it.y = live_target(r, k, nullptr);
-      it.w = k.w;
-      if (it.y < 0) return it;
-      it.xy = to_f(r.x[(int64_t)it.t * r.ld + it.y]);
-      if (POLICY) {
-        it.old = a.p.old_logp[it.t];
-        it.adv = a.p.adv[it.t];
-        if (a.p.beta != 0.f) it.ref = a.p.ref_logp[it.t];
-      }
-      return it;
-    };
-    bool ok = true;
-    RowItem next = fetch(lane);
+    RowItem next = fetch(row_at(lane));
     for (int i0 = 32; ok; i0 += 32) {
       const RowItem now = next;
       const int n = __popc(__ballot_sync(~0u, now.t >= 0));
-      if (n == 32) next = fetch(i0 + lane);
+      if (n == 32) next = fetch(row_at(i0 + lane));
       for (int j = 0; j < n && ok; ++j)
         if (POLICY || __shfl_sync(~0u, now.y, j) >= 0) ok = hand_on(now, j);
       if (n < 32) break;
@@ -561,7 +564,10 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
           const int32_t y = live_target(r, k[j], first ? err : nullptr);
           if (y >= 0) w2[j & 1] += k[j].w;
           else if (first && t < r.T_ && a.logp != nullptr) a.logp[t] = 0.f;
-          const uint32_t l = __ballot_sync(~0u, y >= 0), d = __ballot_sync(~0u, y < 0 && t < r.T_);
+          // (the first row of each cluster is not on its list)
+          const bool late = t >= clusters && t < r.T_;
+          const uint32_t l = __ballot_sync(~0u, y >= 0 && late);
+          const uint32_t d = __ballot_sync(~0u, y < 0 && late);
           if (lane == j) {
             lb = l;
             db = d;
