@@ -24,9 +24,9 @@ struct WsHead {
   uint32_t ticket;  // CTAs of the running launch that have finished
   uint32_t nan;     // a NaN score was seen (router)
   uint32_t pad;
-  float part[12];   // parts of a loss
+  float part[16];   // parts of a loss (router)
 };
-static_assert(sizeof(WsHead) == 64, "the head is four 16-byte words");
+static_assert(sizeof(WsHead) % 16 == 0, "what follows the head is 16-byte aligned");
 
 constexpr uint32_t kErrTarget = 16u;  // error-word bit: a target >= V
 

@@ -209,11 +209,17 @@ struct Raw {
   }
 };
 
-// The K experts of largest key, best first, ties to the lowest; lane k of the
-// group gets the k-th. Keys are lost. Round by round, the group's largest key
-// is found and taken out.
+// A lane's part in a token's choice: expert e takes place `rank` of the K, or
+// none (rank >= K).
+struct Choice {
+  int e, rank;
+};
+
+// The K experts of largest key, ties to the lowest, the k-th in lane k of the
+// group. Keys are lost. Round by round, the group's largest key is found and
+// taken out.
 template <typename H, int N>
-__device__ __forceinline__ int choose_rounds(uint32_t (&key)[N], int K, int lane, uint32_t mask) {
+__device__ __forceinline__ Choice choose_rounds(uint32_t (&key)[N], int K, int lane, uint32_t mask) {
   int mine = -1;
   for (int k = 0; k < K; ++k) {
     uint32_t best = key[0];
@@ -231,20 +237,22 @@ __device__ __forceinline__ int choose_rounds(uint32_t (&key)[N], int K, int lane
       if (H::expert(lane, j) == e) key[j] = 0u;
     if (lane == k) mine = e;
   }
-  return mine;
+  return {mine, lane};
 }
 
-// The same with fewer instructions where a lane holds several keys. A bound
-// from below leaves few candidates, which go to a lane each, and the rounds
-// look at one key a lane. Up to 8 choices, the smallest of the largest keys of
-// 8 groups of 4 lanes bounds them (at least 8 keys reach it; 22 on average, as
-// many as it takes to draw each of 8 kinds); with more choices, or more than 32
-// candidates, the K-th largest of the lanes' largest keys. Where that leaves
-// more than 32 as well (equal keys), the rounds above.
-struct Candidates {
-  uint32_t key[32];
-  int32_t expert[32];
+// The same with fewer and less dependent instructions where a lane holds several
+// keys. A bound from below leaves few candidates, which go to a lane each; a
+// candidate's rank is the number of better ones, counted in shared memory
+// (rounds over the candidates took two dependent warp reductions a choice). Up
+// to 8 choices, the smallest of the largest keys of 8 groups of 4 lanes bounds
+// them (at least 8 keys reach it; 22 on average, as many as it takes to draw
+// each of 8 kinds); with more choices, or more than 32 candidates, the K-th
+// largest of the lanes' largest keys. Where that leaves more than 32 as well
+// (equal keys), the rounds above.
+struct __align__(16) Candidates {
+  uint2 c[32];  // expert (inverted: the lower is the better), key
 };
+__device__ __forceinline__ uint64_t merit(uint2 c) { return (uint64_t)c.y << 32 | c.x; }
 template <typename H, int N>
 __device__ __forceinline__ int gather(const uint32_t (&key)[N], uint32_t bound, int lane,
                                       Candidates& c) {
@@ -255,16 +263,13 @@ __device__ __forceinline__ int gather(const uint32_t (&key)[N], uint32_t bound, 
     const bool in = key[j] >= bound;
     const uint32_t all = __ballot_sync(~0u, in);
     const int at = n + __popc(all & below);
-    if (in && at < 32) {
-      c.key[at] = key[j];
-      c.expert[at] = H::expert(lane, j);
-    }
+    if (in && at < 32) c.c[at] = make_uint2(~(uint32_t)H::expert(lane, j), key[j]);
     n += __popc(all);
   }
   return n;
 }
 template <typename H, int N>
-__device__ __forceinline__ int choose(uint32_t (&key)[N], int K, int lane, Candidates& cand) {
+__device__ __forceinline__ Choice choose(uint32_t (&key)[N], int K, int lane, Candidates& cand) {
   if (N == 1) return choose_rounds<H, N>(key, K, lane, ~0u);
   uint32_t lane_max = key[0];
 #pragma unroll
@@ -287,18 +292,19 @@ __device__ __forceinline__ int choose(uint32_t (&key)[N], int K, int lane, Candi
     n = gather<H, N>(key, max(bound, 1u), lane, cand);
     if (n > 32) return choose_rounds<H, N>(key, K, lane, ~0u);
   }
+  if (lane >= n) cand.c[lane] = make_uint2(0u, 0u);
   __syncwarp();
-  uint32_t mine_key = lane < n ? cand.key[lane] : 0u;
-  const uint32_t mine_e = lane < n ? (uint32_t)cand.expert[lane] : 0xffffffffu;
-  __syncwarp();
-  int mine = -1;
-  for (int k = 0; k < K; ++k) {
-    const uint32_t top = __reduce_max_sync(~0u, mine_key);
-    const uint32_t e = __reduce_min_sync(~0u, mine_key == top ? mine_e : 0xffffffffu);
-    if (mine_e == e) mine_key = 0u;
-    if (lane == k) mine = (int)e;
+  const uint2 own = cand.c[lane];
+  const uint64_t mine = merit(own);
+  int rank = 0;
+  const uint4* two = reinterpret_cast<const uint4*>(cand.c);
+#pragma unroll 4
+  for (int i = 0; 2 * i < n; ++i) {
+    const uint4 v = two[i];
+    rank += (int)(merit(make_uint2(v.x, v.y)) > mine) + (int)(merit(make_uint2(v.z, v.w)) > mine);
   }
-  return mine;
+  __syncwarp();
+  return {(int)~own.x, lane < n ? rank : 32};
 }
 
 // Sums of the calls' workspace, zero between calls.
@@ -464,15 +470,16 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(N))
 #pragma unroll
       for (int j = 0; j < N; ++j)
         if (!H::has(lane, j, p.E)) key[j] = 0u;
-      const int chosen = L == 32 && N > 1 ? choose<H, N>(key, p.K, lane, cand[warp])
-                                          : choose_rounds<H, N>(key, p.K, lane, mask);
+      const Choice mine = L == 32 && N > 1 ? choose<H, N>(key, p.K, lane, cand[warp])
+                                           : choose_rounds<H, N>(key, p.K, lane, mask);
       float score = 0.f;
-      if (on && lane < p.K) score = score_of(to_f(row[chosen]), norm, softmax, c);
+      if (on && mine.rank < p.K) score = score_of(to_f(row[mine.e]), norm, softmax, c);
       const float sum = group_sum<L>(score) + 1e-20f;
-      if (in && lane < p.K) {
-        o.idx[t * p.K + lane] = on ? chosen : -1;
-        o.gates[t * p.K + lane] = on ? p.scale * (p.renorm ? __fdividef(score, sum) : score) : 0.f;
-        if (on && counted) atomicAdd(&count[chosen], 1);
+      if (in && mine.rank < p.K) {
+        o.idx[t * p.K + mine.rank] = on ? mine.e : -1;
+        o.gates[t * p.K + mine.rank] =
+            on ? p.scale * (p.renorm ? __fdividef(score, sum) : score) : 0.f;
+        if (on && counted) atomicAdd(&count[mine.e], 1);
       }
       if (on) {
         const float inv = softmax ? 1.f : rcp(norm.z);
@@ -522,8 +529,9 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(N))
   }
 }
 
-// The finish as a launch of its own, for many sequences: 64 experts a CTA.
-constexpr int kFinishExperts = 64;
+// The finish as a launch of its own, for many sequences: 32 experts a CTA.
+constexpr int kFinishExperts = 32;
+static_assert(kMaxExperts / kFinishExperts <= 16, "parts of the loss in the head");
 __global__ void __launch_bounds__(kRouteThreads)
     route_finish_kernel(const __grid_constant__ RouteIn p, const __grid_constant__ RouteSums w,
                         const __grid_constant__ RouteOut o, WsHead* head) {
@@ -729,8 +737,9 @@ unsigned route_grid(int64_t T_) {
       1, std::min<int64_t>((T_ + least - 1) / least, 152 * route_ctas(N)));
 }
 
-// Up to here the last CTA of the router finishes; beyond, a launch of its own.
-constexpr int64_t kFinishInside = 16384;
+// Up to here the last CTA of the router finishes; beyond, a launch of its own:
+// for 33 sequences of 256 experts the last CTA alone took 12 us.
+constexpr int64_t kFinishInside = 2048;
 
 template <typename T, int L, int N, bool FULL, int SCORE>
 cudaError_t route_launch(const void* logits, const RouteIn& p, const RouteOut& o, const RouteWs& w,
