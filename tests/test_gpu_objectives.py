@@ -353,3 +353,61 @@ def test_python_refusals():
         PreferenceLoss(1, 4, 64)(x, yt, dev([0, 4], torch.int64))
     with pytest.raises(ValueError):
         TokenLogprobs(-1, 64)
+
+
+@pytest.mark.parametrize("vocab,dtype,pad,lengths,lead", [
+    (16500, BF16, 0, (60, 0, 100, 55, 40, 90), 0),
+    (16511, BF16, 3, (400, 300, 1, 0, 500, 299), 7),
+    (70001, FP32, 0, (200, 50, 0, 120, 0, 130, 30, 1), 0),
+    (33000, FP32, 0, (2,) * 300, 3),
+    (32000, BF16, 0, (3, 900), 100),
+])
+@pytest.mark.parametrize("kind,average", [("sigmoid", False), ("squared", True)])
+def test_preference_loss_of_many_long_rows(vocab, dtype, pad, lengths, lead, kind, average):
+    """More rows than SMs, beyond the short ones; sequences of very different
+    lengths; many small pairs."""
+    test_preference_loss(vocab, dtype, pad, lengths, lead, kind, average)
+
+
+def test_preference_long_rows_in_place_and_same_bits():
+    from fsdp_buffer_layout_gb300.objectives import PreferenceLoss
+    rng = np.random.default_rng(8)
+    x = make_logits(rng, 1600, 16500, BF16)
+    y = rng.integers(0, 16500, 1600)
+    y[rng.random(1600) < 0.3] = -1
+    starts = dev([0, 300, 500, 900, 1000, 1300, 1590], torch.int64)
+    ref = dev(rng.normal(size=1600))
+    op = PreferenceLoss(3, 1600, 16500)
+    args = (dev(y, torch.int64), starts, ref)
+    want = [t.clone() for t in op(x, *args)]
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(op(x, *args), want))
+    got = op(x, *args, grad=x)  # over the logits
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert op.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,vocab", [(BF16, 32000), (FP32, 50021), (BF16, 5000)])
+def test_policy_many_rows_masked_in_runs(dtype, vocab):
+    """Several rows a cluster, masked in runs and at random: against the same
+    rows in calls of their own."""
+    from fsdp_buffer_layout_gb300.objectives import PolicyLoss
+    rng = np.random.default_rng(11)
+    n = 1300
+    x = make_logits(rng, n, vocab, dtype)
+    y = rng.integers(0, vocab, n)
+    y[(np.arange(n) % 100 < 30) | (rng.random(n) < 0.2)] = -1
+    old, adv = dev(rng.normal(size=n) - 10), dev(rng.normal(size=n))
+    yt = dev(y, torch.int64)
+    op = PolicyLoss(n, vocab, dtype=dtype, kl_beta=0.1, mean=False)
+    stats, lp, grad = (t.clone() for t in op(x, yt, old, adv, ref_logp=old))
+    assert stats[3].item() == (y >= 0).sum()
+    part = PolicyLoss(n, vocab, dtype=dtype, kl_beta=0.1, mean=False)
+    for i in (0, 31, 299, 1299):
+        s1, l1, g1 = part(x[i:i + 1], yt[i:i + 1], old[i:i + 1], adv[i:i + 1], ref_logp=old[i:i + 1])
+        # (split over more CTAs, so summed in another order)
+        assert abs(l1.item() - lp[i].item()) <= 2 * tol(vocab) + 2.0**-23 * abs(lp[i].item())
+        a, b = host(g1[0]), host(grad[i])
+        assert np.abs(a - b).max() <= 2.0**-7 * np.abs(b).max() if dtype == BF16 else \
+            np.abs(a - b).max() <= 16 * tol(vocab) * np.abs(b).max()
+    assert not grad[torch.from_numpy(y < 0).cuda()].any()
