@@ -347,12 +347,6 @@ __global__ void __launch_bounds__(kPairThreads)
 }
 
 #include "mbarrier.cuh"
-#ifndef VSF_PIPE_W
-#define VSF_PIPE_W 16
-#endif
-#ifndef VSF_PIPE_PER
-#define VSF_PIPE_PER 4
-#endif
 #include "row_pipe.cuh"
 #include "row_regs.cuh"
 
@@ -416,7 +410,7 @@ Rows<T> rows_of(const RowsArg& a) {
   return r;
 }
 
-constexpr int kPipeWarps = VSF_PIPE_W;
+constexpr int kPipeWarps = 16;
 
 // Clusters of C CTAs of a kernel that fit on the current device at a time,
 // looked up once per device and size; 0 with *e set where that fails.
@@ -493,26 +487,26 @@ cudaError_t launch_pipe(PipeArgs<T>& a, int C, cudaStream_t st) {
                        Shape::threads, pipe_smem<kPipeWarps>(), C, st, a);
 }
 
-// Rows short enough for the registers of 8 warps at 8 vectors a thread.
+// Rows short enough for the registers of 8 warps at 8 vectors a thread. Policy
+// loss of 4096 rows, registers against pipeline: 1000 words 16 and 52 us, 8000
+// words 48 and 64, 16000 words 66 and 73 (bf16); 16 vectors a thread would win 4
+// percent at 20000 words and lose 11 at 32000.
 template <typename T>
 bool short_rows(int64_t V) {
-#ifndef VSF_SHORT
-#define VSF_SHORT (8 * kRegsThreads)
-#endif
-  return V / Vec<T>::n <= VSF_SHORT;
+  return V / Vec<T>::n <= 8 * kRegsThreads;
 }
 
 template <typename T, bool POLICY, int G, int NV>
 cudaError_t launch_regs_as(const PipeArgs<T>& a, const ObjectiveWs& w, cudaStream_t st) {
-  const int64_t rows = 8 / G, most = 152 * (NV <= 4 ? 4 : 3);
+  const int64_t rows = 8 / G, most = 152 * regs_ctas(NV);
   const unsigned grid =
       (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, (a.r.T_ + rows - 1) / rows));
   static_assert(152 * 4 <= kMaxPipeClusters, "the workspace holds a sum of every CTA");
   const double* total = nullptr;
   if (POLICY && a.p.mean && a.r.T_ > 2048) {
     total = w.total;
-    const unsigned n = (unsigned)std::min<int64_t>(64, (a.r.T_ + 1023) / 1024);
-    const cudaError_t e = launch_behind(weight_sum_kernel, n, 512, 0, 1, st, a.r.target, a.r.weight,
+    const unsigned n = (unsigned)std::min<int64_t>(64, (a.r.T_ + 8 * kSumThreads - 1) / (8 * kSumThreads));
+    const cudaError_t e = launch_behind(weight_sum_kernel, n, kSumThreads, 0, 1, st, a.r.target, a.r.weight,
                                         a.r.T_, a.r.V, w.partial, w.total, w.head);
     if (e != cudaSuccess) return e;
   }

@@ -25,6 +25,14 @@
 // are read by single threads. A gradient row whose address differs from the
 // logits' modulo 16 bytes is written element by element.
 //
+// Bounds and measurements (GB300, a call among others). Sums alone read at the
+// rate of a plain copy: 4096 x 131072 bf16, 3/4 live, 118 us = 6.8 TB/s. The
+// policy loss is bound by HBM where a CTA's share is long (8192 x 131072 bf16:
+// 715 us, 6.0 TB/s read and written; clusters of 4 leave 8 of the 152 SMs idle)
+// and by a row's fixed cost, about 1.8 us of the consumers' time however short
+// the row, where it is not (4096 x 32000 bf16, 3/4 live: 80 us, 5.7 TB/s).
+// A call costs some 10 us from its first load to its last sum.
+//
 // Every wait is bounded (mbarrier.cuh). After a timeout all waits of the CTA
 // return at once and its warps leave their loops; the cluster then meets at
 // its end as always, and waits a moment for messages still on their way.
@@ -56,20 +64,6 @@ __device__ __forceinline__ F2 f2(float a, float b) {
 __device__ __forceinline__ void f2_get(F2 v, float& a, float& b) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v.v));
 }
-#ifdef VSF_SCALAR
-__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
-  float a0, a1, b0, b1;
-  f2_get(a, a0, a1);
-  f2_get(b, b0, b1);
-  return f2(__fadd_rn(a0, b0), __fadd_rn(a1, b1));
-}
-__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
-  float a0, a1, b0, b1;
-  f2_get(a, a0, a1);
-  f2_get(b, b0, b1);
-  return f2(__fmul_rn(a0, b0), __fmul_rn(a1, b1));
-}
-#else
 __device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
   F2 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
@@ -80,22 +74,11 @@ __device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
-#endif
-#ifdef VSF_SCALAR
-__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
-  float a0, a1, b0, b1, c0, c1;
-  f2_get(a, a0, a1);
-  f2_get(b, b0, b1);
-  f2_get(c, c0, c1);
-  return f2(__fmaf_rn(a0, b0, c0), __fmaf_rn(a1, b1, c1));
-}
-#else
 __device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
   F2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
   return r;
 }
-#endif
 
 // The pairs of one vector.
 template <typename T>
@@ -147,25 +130,12 @@ __device__ __forceinline__ F2 exp2_pair(F2 t) {
 struct PairScale {
   F2 hi, lo;
 };
-#ifdef VSF_SCALAR
-__device__ __forceinline__ F2 exp_pair(F2 x, F2 nm, const PairScale& c) {
-  float x0, x1, m0, m1, h0, h1, l0, l1;
-  f2_get(x, x0, x1);
-  f2_get(nm, m0, m1);
-  f2_get(c.hi, h0, h1);
-  f2_get(c.lo, l0, l1);
-  x0 = __fadd_rn(x0, m0);
-  x1 = __fadd_rn(x1, m0);
-  return f2(ex2(__fmaf_rn(x0, h0, __fmul_rn(x0, l0))), ex2(__fmaf_rn(x1, h0, __fmul_rn(x1, l0))));
-}
-#else
 __device__ __forceinline__ F2 exp_pair(F2 x, F2 nm, const PairScale& c) {
   const F2 d = f2_add(x, nm);
   float a, b;
   f2_get(f2_fma(d, c.hi, f2_mul(d, c.lo)), a, b);
   return f2(ex2(a), ex2(b));
 }
-#endif
 
 __device__ __forceinline__ uint32_t cta_rank() {
   uint32_t r;
@@ -223,11 +193,14 @@ constexpr int kMaxPipeCluster = 16;
 constexpr uint32_t kQueue = 8;  // rows handed on and not yet added up
 constexpr int kList = 2048;     // rows of a cluster that its list holds
 
-// One shape of the kernel: W consumer warps, each thread `per` vectors of a
-// chunk, and a ring of 208 KB for the CTAs of an SM together.
+// W consumer warps, each thread `per` vectors of a chunk; the rings of an SM's
+// CTAs have 208 KB together. W = 16 (one CTA an SM) with 4 vectors measured best:
+// 8192 x 131072 bf16, policy loss: 888 us, against 943 for W = 8 (two CTAs, each
+// with half the ring, so rows in twice as many pieces), 1014 with 2 vectors (a
+// chunk's fixed cost shows) and 1006 with 6 (too few chunks).
 template <int W>
 struct PipeShape {
-  static constexpr int per = VSF_PIPE_PER;
+  static constexpr int per = 4;
   static constexpr int consumers = W * 32;
   static constexpr int threads = consumers + 64;
   static constexpr int chunk_vecs = per * consumers;
@@ -368,9 +341,19 @@ __device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity,
 // The loss from the sums of n clusters or CTAs, in their order; one warp.
 template <typename T>
 __device__ __forceinline__ void policy_stats(const PipeArgs<T>& a, int64_t n, int lane) {
+  constexpr int kAhead = 4;
   double v[3] = {0.0, 0.0, 0.0};
-  for (int64_t c = lane; c < n; c += 32)
-    for (int j = 0; j < 3; ++j) v[j] += __ldcg(a.partial + 3 * c + j);
+  for (int64_t c = lane; c < n; c += 32 * kAhead) {
+    double u[kAhead][3];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+      for (int j = 0; j < 3; ++j) u[k][j] = c + 32 * k < n ? __ldcg(a.partial + 3 * (c + 32 * k) + j) : 0.0;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+      for (int j = 0; j < 3; ++j) v[j] += u[k][j];
+  }
   for (int j = 0; j < 3; ++j) v[j] = warp_sum(v[j]);
   if (lane == 0) {
     const double f = (double)a.p.scale / (a.p.mean && v[2] != 0.0 ? v[2] : 1.0);
@@ -388,6 +371,8 @@ struct Pending {
   int64_t t;
   int32_t y, loose;
   float xl;  // the loose element
+  int32_t head, begin, end;  // the row's first vector; the share's vectors
+  uint32_t skew;             // the logits' address modulo 16
   Place<SLOTS> first;
 };
 
@@ -704,18 +689,16 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
         ++written;
         if (!warp_wait(rbar + 8 * par, phase, err, stop)) return false;
         const float4 res = sh->result[par];
-        const T* x = r.x + p.t * r.ld;
-        const Span s = span_of(x, r.V);
-        const int32_t begin = share(s.nvec, rank, logC), end = share(s.nvec, rank + 1, logC);
+        const int32_t begin = p.begin, end = p.end;
         const float z = finite_max(res.x), b = res.y, coef = res.z;
         T* g = a.grad + p.t * a.grad_ld;
-        const bool same = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
+        const bool same = (reinterpret_cast<uintptr_t>(g) & 15) == p.skew;
         // bf16 keeps 8 bits: there 2^(x c - m c) with rounded c and m c serves,
         // where m c does not overflow
         const bool near = sizeof(T) == 2 && fabsf(z) < 1e30f;
         const F2 nm = f2(-z, -z), b2 = f2(b, b), c0 = f2(r.c.hi, r.c.hi);
         const F2 kk = f2(-z * r.c.hi, -z * r.c.hi);
-        uint4* gv = reinterpret_cast<uint4*>(g + s.head);
+        uint4* gv = reinterpret_cast<uint4*>(g + p.head);
         Place<slots> from = p.first;
         for (int32_t v = begin; v < end; v += Shape::chunk_vecs, from.next()) {
           const unsigned char* chunk = ring + from.slot * Shape::chunk_bytes;
@@ -744,7 +727,7 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
           } else {
             const T* c = reinterpret_cast<const T*>(chunk);
             const int32_t n = min(end - v, (int32_t)Shape::chunk_vecs) * VE;
-            T* out = g + s.head + (int64_t)v * VE;
+            T* out = g + p.head + (int64_t)v * VE;
             for (int32_t i = tid; i < n; i += Shape::consumers)
               out[i] = from_f<T>(b * exp_scaled(to_f(c[i]) - z, r.c));
           }
@@ -761,7 +744,7 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
           g[p.loose] = from_f<T>(p.loose == p.y ? e + coef : e);
         }
         // the target's element again, by the thread that wrote it
-        const int32_t ye = p.y - s.head, yv = ye / VE;
+        const int32_t ye = p.y - p.head, yv = ye / VE;
         if (ye >= 0 && yv >= begin && yv < end &&
             tid == ((same ? yv - begin : ye - begin * VE) & (Shape::consumers - 1)))
           g[p.y] = from_f<T>(b * exp_scaled(res.w - z, r.c) + coef);
@@ -792,6 +775,10 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
         const T* x = r.x + (int64_t)it.t * r.ld;
         const Span s = span_of(x, r.V);
         const int32_t begin = share(s.nvec, rank, logC), end = share(s.nvec, rank + 1, logC);
+        row.head = s.head;
+        row.begin = begin;
+        row.end = end;
+        row.skew = (uint32_t)(reinterpret_cast<uintptr_t>(x) & 15);
         row.loose = -1;
         if (rank == 0 && tid < s.head) row.loose = tid;
         if (rank + 1 == C && tid >= 16 && s.head + s.nvec * VE + tid - 16 < r.V)
@@ -886,10 +873,11 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
 // ------------------------------------------------------------ gradient alone
 // The gradient's rows where a row's coefficient is known only after the sums of
 // all rows (preference loss), or its share of a cluster's shared memory is too
-// long. A thread takes six vectors of a row at a time
-// (four and eight are within 2 percent of it). Rows are taken last
-// first: the pass before read them first to last, so that the end of the logits
-// is still in L2.
+// long. A thread takes six vectors of a row at a time (four and eight are within
+// 2 percent of it). Rows are taken last first: the pass before read them first
+// to last, so that the end of the logits is still in L2 (75 of 221 MB measured).
+// HBM bounds it: for 16 pairs of 384 x 32000 bf16, 3/4 live, the three kernels of
+// the loss take 255 us, of which 175 here (443 MB read, 591 MB written).
 constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 6;
 constexpr int kGradCtas = 4;  // an SM

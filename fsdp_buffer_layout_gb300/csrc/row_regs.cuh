@@ -1,48 +1,62 @@
 // row_regs.cuh — the row operation for short rows (up to 32 KB), whose vectors
 // fit the registers of G warps: one read, one write, no ring. The pipelined
-// kernel hands rows from warp to warp, which takes about 1.5 us a row whatever
-// its length; here many rows are in flight on an SM instead. Included by
-// objective.cu after row_pipe.cuh.
+// kernel hands rows from warp to warp, which takes about 1.8 us a row however
+// short it is; here 3 to 32 rows are in flight on an SM instead. What bounds it
+// is the chain from a row's loads over its sum and its scalars to its stores
+// (policy loss, bf16: 4096 x 16000 66 us, 59 percent of the copy rate; 4096 x
+// 1000 16 us); sums alone reach 5.4 us for 4096 x 1000. Included by objective.cu
+// after row_pipe.cuh.
 //
 // Each group of G warps takes every n-th row. Its threads hold up to NV vectors
 // each. The warps' joins meet in shared memory (G > 1) behind a barrier of the
 // group, and every warp works out the row's scalars for itself.
 constexpr int kRegsThreads = 256;
+constexpr int regs_ctas(int nv) { return nv <= 4 ? 4 : 3; }  // an SM
 
-// Sum of the live weights, for many tokens: several CTAs, the last of which adds
-// up their sums in their order.
-__global__ void __launch_bounds__(512)
+// Sum of the live weights, for many tokens: up to 64 CTAs, the last of which adds
+// up their sums in their order. The kernel behind it may start with its rows
+// meanwhile: it is let go only after the kernels before this one have ended.
+constexpr int kSumThreads = 1024;
+__global__ void __launch_bounds__(kSumThreads)
     weight_sum_kernel(const int64_t* target, const float* weight, int64_t T_, int32_t V,
                       double* partial, double* total, WsHead* head) {
-  __shared__ double part[16];
-  __shared__ bool last;
-  take_turn();
-  float w2[2] = {0.f, 0.f};
-  const int64_t step = (int64_t)gridDim.x * 512;
-  int64_t t = (int64_t)blockIdx.x * 512 + threadIdx.x;
-  for (; t < T_; t += 4 * step)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t u = t + j * step;
-      if (u < T_ && target[u] >= 0 && target[u] < V) w2[j & 1] += weight != nullptr ? weight[u] : 1.f;
-    }
-  const double s = block_sum((double)w2[0] + (double)w2[1], part);
-  if (threadIdx.x == 0) {
+  __shared__ float part[32];
+  const int tid = threadIdx.x;
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
+  float w = 0.f;
+  const int64_t step = (int64_t)gridDim.x * kSumThreads;
+#pragma unroll 4
+  for (int64_t t = (int64_t)blockIdx.x * kSumThreads + tid; t < T_; t += step)
+    if (target[t] >= 0 && target[t] < V) w += weight != nullptr ? weight[t] : 1.f;
+  w = warp_sum(w);
+  if ((tid & 31) == 0) part[tid >> 5] = w;
+  __syncthreads();
+  if (tid >= 32) return;
+  const double s = warp_sum((double)part[tid]);
+  if (gridDim.x == 1) {
+    if (tid == 0) *total = s;
+    return;
+  }
+  uint32_t last = 0;
+  if (tid == 0) {
     partial[blockIdx.x] = s;
     __threadfence();
     last = atomicAdd(&head->ticket, 1u) + 1 == gridDim.x;
     __threadfence();
-    if (last) {
-      double all = 0.0;
-      for (uint32_t i = 0; i < gridDim.x; ++i) all += __ldcg(partial + i);
-      *total = all;
-      head->ticket = 0;
-    }
+  }
+  if (!__shfl_sync(~0u, last, 0)) return;
+  double all = tid < gridDim.x ? __ldcg(partial + tid) : 0.0;
+  if (tid + 32 < gridDim.x) all += __ldcg(partial + tid + 32);
+  all = warp_sum(all);
+  if (tid == 0) {
+    *total = all;
+    head->ticket = 0;
   }
 }
 
 template <typename T, int G, int NV, bool POLICY>
-__global__ void __launch_bounds__(kRegsThreads, NV <= 4 ? 4 : 3)
+__global__ void __launch_bounds__(kRegsThreads, regs_ctas(NV))
     row_regs_kernel(const __grid_constant__ PipeArgs<T> a, const double* total) {
   constexpr int VE = Vec<T>::n, kGroups = 8 / G, kThreads = 32 * G;
   __shared__ float4 part[2][8];  // of each warp: m, s, x_y
@@ -56,7 +70,9 @@ __global__ void __launch_bounds__(kRegsThreads, NV <= 4 ? 4 : 3)
   const PairScale c2 = {f2(r.c.hi, r.c.hi), f2(r.c.lo, r.c.lo)};
   const float c1 = (uint32_t)gtid * 2654435769u < r.c.ups ? r.c.up : r.c.hi;
   const F2 cc = f2(c1, c1);
-  take_turn();
+  // (behind weight_sum_kernel, inputs may be read before its end)
+  if (total == nullptr) cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
   Token next = token_at(r, first);
   float scale = 0.f;
   if (POLICY) {
@@ -72,6 +88,7 @@ __global__ void __launch_bounds__(kRegsThreads, NV <= 4 ? 4 : 3)
       __syncthreads();
       for (int i = 0; i < 8; ++i) n += (double)weights[i];
     } else if (a.p.mean) {
+      cudaGridDependencySynchronize();
       n = __ldcg(total);
     }
     scale = (float)((double)a.p.scale / (a.p.mean && n != 0.0 ? n : 1.0) * r.inv_t);

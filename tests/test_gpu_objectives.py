@@ -411,3 +411,18 @@ def test_policy_many_rows_masked_in_runs(dtype, vocab):
         assert np.abs(a - b).max() <= 2.0**-7 * np.abs(b).max() if dtype == BF16 else \
             np.abs(a - b).max() <= 16 * tol(vocab) * np.abs(b).max()
     assert not grad[torch.from_numpy(y < 0).cuda()].any()
+
+
+def test_rows_longer_than_a_cluster_holds():
+    """800000 words: the policy loss in three passes."""
+    from fsdp_buffer_layout_gb300.objectives import PolicyLoss
+    for vocab, masked in ((800000, False), (790003, True)):
+        x, y, w, old, ref, adv = policy_case(5, vocab, BF16, masked=masked)
+        op = PolicyLoss(5, vocab, clip_low=0.2, clip_high=0.25, kl_beta=0.1, scale=0.5)
+        stats, lp, grad = op(x, dev(y, torch.int64), dev(old), dev(adv), ref_logp=dev(ref),
+                             weights=dev(w))
+        s, l, g, _ = R.policy(host(x), y, old, adv, ref, w, 0.2, 0.25, 0.1, 1.0, 0.5, True)
+        check_logp(lp, l, vocab)
+        big = policy_scale(l, old, adv, ref, w, 0.1, 0.5 / s[3], 1.0)
+        check_grad(grad, g, BF16, vocab, big)
+        assert (np.abs(host(stats) - s) <= big.sum() * 4 * tol(vocab) + 2.0**-22 * np.abs(s)).all()
