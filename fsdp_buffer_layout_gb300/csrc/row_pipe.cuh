@@ -200,7 +200,7 @@ constexpr int kList = 2048;     // rows of a cluster that its list holds
 // chunk's fixed cost shows) and 1006 with 6 (too few chunks).
 template <int W>
 struct PipeShape {
-  static constexpr int per = 4;
+  static constexpr int per = 4;  // (a short chunk's end is written out for it)
   static constexpr int consumers = W * 32;
   static constexpr int threads = consumers + 64;
   static constexpr int chunk_vecs = per * consumers;
@@ -789,7 +789,8 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
         // ---- maximum and sum
         float m = -INFINITY;
         F2 sum0 = f2(0.f, 0.f), sum1 = sum0;
-        auto add_up = [&](const uint4 (&x4)[Shape::per]) {
+        auto add_up = [&](const auto& x4) {
+          constexpr int n = sizeof(x4) / sizeof(uint4);
           const float bm = largest(x4, T());
           if (bm > m) {
             const float f = expf((m - bm) * r.inv_tf);
@@ -800,7 +801,7 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
           const float z = -finite_max(m);
           const F2 nm = f2(z, z);
 #pragma unroll
-          for (int j = 0; j < Shape::per; ++j) {
+          for (int j = 0; j < n; ++j) {
             Pairs<T> p;
             unpack(x4[j], p);
 #pragma unroll
@@ -817,18 +818,20 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
           }
           const uint4* c = reinterpret_cast<const uint4*>(ring + at.slot * Shape::chunk_bytes) + tid;
           const int32_t n = end - v - tid;
-          uint4 x4[Shape::per];
           if (n > (Shape::per - 1) * Shape::consumers) {
+            uint4 x4[Shape::per];
 #pragma unroll
             for (int j = 0; j < Shape::per; ++j) x4[j] = c[j * Shape::consumers];
             add_up(x4);
+          } else if (n > 2 * Shape::consumers) {
+            const uint4 x3[3] = {c[0], c[Shape::consumers], c[2 * Shape::consumers]};
+            add_up(x3);
+          } else if (n > Shape::consumers) {
+            const uint4 x2[2] = {c[0], c[Shape::consumers]};
+            add_up(x2);
           } else if (n > 0) {
-#pragma unroll
-            for (int j = 0; j < Shape::per; ++j) {
-              x4[j] = make_uint4(Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest);
-              if (j == 0 || j * Shape::consumers < n) x4[j] = c[j * Shape::consumers];
-            }
-            add_up(x4);
+            const uint4 x1[1] = {c[0]};
+            add_up(x1);
           }
           if (!POLICY) {
             __syncwarp();
