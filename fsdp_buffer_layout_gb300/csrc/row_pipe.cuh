@@ -707,22 +707,30 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
             const uint4* c = reinterpret_cast<const uint4*>(chunk) + tid;
             uint4* out = gv + v + tid;
             const int32_t n = end - v - tid;
+            if (near) {
 #pragma unroll
-            for (int j = 0; j < Shape::per; ++j) {
-              if (j * Shape::consumers >= n) break;
-              Pairs<T> e;
-              unpack(c[j * Shape::consumers], e);
-              float o[VE];
-              if (near) {
+              for (int j = 0; j < Shape::per; ++j) {
+                if (j * Shape::consumers >= n) break;
+                Pairs<T> e;
+                unpack(c[j * Shape::consumers], e);
+                float o[VE];
 #pragma unroll
                 for (int i = 0; i < VE / 2; ++i)
                   f2_get(f2_mul(exp2_pair(f2_fma(e.p[i], c0, kk)), b2), o[2 * i], o[2 * i + 1]);
-              } else {
+                __stcs(out + j * Shape::consumers, pack_vec<T>(o));
+              }
+            } else {
+#pragma unroll(sizeof(T) == 2 ? 1 : Shape::per)
+              for (int j = 0; j < Shape::per; ++j) {
+                if (j * Shape::consumers >= n) break;
+                Pairs<T> e;
+                unpack(c[j * Shape::consumers], e);
+                float o[VE];
 #pragma unroll
                 for (int i = 0; i < VE / 2; ++i)
                   f2_get(f2_mul(exp_pair(e.p[i], nm, c2), b2), o[2 * i], o[2 * i + 1]);
+                __stcs(out + j * Shape::consumers, pack_vec<T>(o));
               }
-              __stcs(out + j * Shape::consumers, pack_vec<T>(o));
             }
           } else {
             const T* c = reinterpret_cast<const T*>(chunk);
