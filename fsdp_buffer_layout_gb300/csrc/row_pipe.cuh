@@ -304,7 +304,7 @@ __device__ __forceinline__ MaxSum warp_join(MaxSum v, float inv_t) {
 
 // Zeroes the gradient row's share of this CTA.
 template <typename T>
-__device__ __forceinline__ void zero_share(T* g, int32_t V, uint32_t rank, uint32_t log, int tid,
+__device__ __noinline__ void zero_share(T* g, int32_t V, uint32_t rank, uint32_t log, int tid,
                                            int threads) {
   const Span s = span_of(g, V);
   uint4* v = reinterpret_cast<uint4*>(g + s.head);
@@ -736,6 +736,7 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
             const T* c = reinterpret_cast<const T*>(chunk);
             const int32_t n = min(end - v, (int32_t)Shape::chunk_vecs) * VE;
             T* out = g + p.head + (int64_t)v * VE;
+#pragma unroll 1
             for (int32_t i = tid; i < n; i += Shape::consumers)
               out[i] = from_f<T>(b * exp_scaled(to_f(c[i]) - z, r.c));
           }
