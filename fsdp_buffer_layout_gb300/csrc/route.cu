@@ -276,23 +276,23 @@ __device__ __forceinline__ Choice choose(uint32_t (&key)[N], int K, int lane, Ca
   uint32_t lane_max = key[0];
 #pragma unroll
   for (int j = 1; j < N; ++j) lane_max = max(lane_max, key[j]);
-  int n = 33;
-  if (K <= 8) {
-    uint32_t four = max(lane_max, __shfl_xor_sync(~0u, lane_max, 1));
-    four = max(four, __shfl_xor_sync(~0u, four, 2));
-    n = gather<H, N>(key, max(__reduce_min_sync(~0u, four), 1u), lane, cand);
-  }
-  if (n > 32) {
-    uint32_t bound = 0;
-    for (int k = 0; k < K;) {
-      bound = __reduce_max_sync(~0u, lane_max);
-      const bool hit = lane_max == bound;
-      k += __popc(__ballot_sync(~0u, hit));
-      if (hit) lane_max = 0u;
-    }
-    __syncwarp();
+  uint32_t four = max(lane_max, __shfl_xor_sync(~0u, lane_max, 1));
+  four = max(four, __shfl_xor_sync(~0u, four, 2));
+  uint32_t bound = __reduce_min_sync(~0u, four);
+  int n = 0;
+#pragma unroll 1
+  for (bool tight = K > 8;; tight = true) {
+    if (tight)
+      for (int k = 0; k < K;) {
+        bound = __reduce_max_sync(~0u, lane_max);
+        const bool hit = lane_max == bound;
+        k += __popc(__ballot_sync(~0u, hit));
+        if (hit) lane_max = 0u;
+      }
     n = gather<H, N>(key, max(bound, 1u), lane, cand);
-    if (n > 32) return choose_rounds<H, N>(key, K, lane, ~0u);
+    if (n <= 32) break;
+    if (tight) return choose_rounds<H, N>(key, K, lane, ~0u);
+    __syncwarp();
   }
   if (lane >= n) cand.c[lane] = make_uint2(0u, 0u);
   __syncwarp();
