@@ -11,7 +11,7 @@
 //   logits:  d x_e  = s_e (d s_e - sum_j s_j d s_j)              softmax
 //                   = s_e (1 - s_e) d s_e                        sigmoid
 //
-// A group of L lanes (8, 16 or a warp) takes a token and holds its experts in
+// A group of L lanes (8 or a warp) takes a token and holds its experts in
 // registers, N a lane. A CTA takes a run of tokens, one sequence of it after the
 // other, so that the sequence's sums stay in registers. Instructions bound the
 // large sizes (256 experts: 1 KB of logits a token against some hundred
@@ -106,6 +106,7 @@ template <typename T, int L, int N, bool FULL>
 struct Hold {
   static constexpr int V = FULL ? (N * (int)sizeof(T) < 16 ? N : 16 / (int)sizeof(T)) : 1;
   static constexpr bool kWarp = L == 32;
+  static constexpr int kLanes = L;
   static __device__ __forceinline__ int expert(int lane, int j) {
     return FULL ? j / V * (L * V) + lane * V + j % V : lane + L * j;
   }
@@ -221,7 +222,7 @@ struct Choice {
 // group. Keys are lost. Round by round, the group's largest key is found and
 // taken out.
 template <typename H, int N>
-__device__ __forceinline__ Choice choose_rounds(uint32_t (&key)[N], int K, int lane, uint32_t mask) {
+__device__ __forceinline__ Choice choose_rounds(uint32_t (&key)[N], int K, int lane) {
   int mine = -1;
   for (int k = 0; k < K; ++k) {
     uint32_t best = key[0];
@@ -232,8 +233,22 @@ __device__ __forceinline__ Choice choose_rounds(uint32_t (&key)[N], int K, int l
         best = key[j];
         be = H::expert(lane, j);
       }
-    const uint32_t top = __reduce_max_sync(mask, best);
-    const int e = (int)__reduce_min_sync(mask, best == top ? (uint32_t)be : 0xffffffffu);
+    int e;
+    if constexpr (H::kLanes == 32) {
+      const uint32_t top = __reduce_max_sync(~0u, best);
+      e = (int)__reduce_min_sync(~0u, best == top ? (uint32_t)be : 0xffffffffu);
+    } else {
+#pragma unroll
+      for (int o = H::kLanes / 2; o > 0; o >>= 1) {
+        const uint32_t key2 = __shfl_xor_sync(~0u, best, o);
+        const int e2 = __shfl_xor_sync(~0u, be, o);
+        if (key2 > best || (key2 == best && e2 < be)) {
+          best = key2;
+          be = e2;
+        }
+      }
+      e = be;
+    }
 #pragma unroll
     for (int j = 0; j < N; ++j)
       if (H::expert(lane, j) == e) key[j] = 0u;
@@ -272,7 +287,7 @@ __device__ __forceinline__ int gather(const uint32_t (&key)[N], uint32_t bound, 
 }
 template <typename H, int N>
 __device__ __forceinline__ Choice choose(uint32_t (&key)[N], int K, int lane, Candidates& cand) {
-  if (N == 1) return choose_rounds<H, N>(key, K, lane, ~0u);
+  if (N == 1) return choose_rounds<H, N>(key, K, lane);
   uint32_t lane_max = key[0];
 #pragma unroll
   for (int j = 1; j < N; ++j) lane_max = max(lane_max, key[j]);
@@ -291,7 +306,7 @@ __device__ __forceinline__ Choice choose(uint32_t (&key)[N], int K, int lane, Ca
       }
     n = gather<H, N>(key, max(bound, 1u), lane, cand);
     if (n <= 32) break;
-    if (tight) return choose_rounds<H, N>(key, K, lane, ~0u);
+    if (tight) return choose_rounds<H, N>(key, K, lane);
     __syncwarp();
   }
   if (lane >= n) cand.c[lane] = make_uint2(0u, 0u);
@@ -400,7 +415,6 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(N))
   __shared__ Candidates cand[kRouteWarps];
   __shared__ int tokens, last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & (L - 1), group = tid / L;
-  const uint32_t mask = L == 32 ? ~0u : ((1u << (L & 31)) - 1) << ((tid & 31) & ~(L - 1));
   for (int e = tid; e < N * L; e += kRouteThreads) count[e] = 0;
   if (tid == 0) tokens = 0;
   __syncthreads();
@@ -473,7 +487,7 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(N))
       for (int j = 0; j < N; ++j)
         if (!H::has(lane, j, p.E)) key[j] = 0u;
       const Choice mine = L == 32 && N > 1 ? choose<H, N>(key, p.K, lane, cand[warp])
-                                           : choose_rounds<H, N>(key, p.K, lane, mask);
+                                           : choose_rounds<H, N>(key, p.K, lane);
       float score = 0.f;
       if (on && mine.rank < p.K) score = score_of(to_f(row[mine.e]), norm, softmax, c);
       const float sum = group_sum<L>(score) + 1e-20f;
@@ -731,10 +745,10 @@ RouteIn route_in(int64_t T_, int64_t E, int64_t ld, const float* bias, const uin
           hp->route_scale, hp->balance, bias, live, starts, 1.44269504f};
 }
 
-// CTAs: two tokens a group at least, no more than run at a time.
+// CTAs: 16 tokens and one a group at least, no more than run at a time.
 template <int L, int N>
 unsigned route_grid(int64_t T_) {
-  const int64_t least = 2 * kRouteThreads / L;
+  const int64_t least = std::max(16, kRouteThreads / L);
   return (unsigned)std::max<int64_t>(
       1, std::min<int64_t>((T_ + least - 1) / least, 152 * route_ctas(N)));
 }
@@ -765,17 +779,24 @@ cudaError_t grad_launch(const void* logits, const RouteIn& p, const int32_t* idx
 }
 
 // F<T, lanes a token, experts a lane, full, score> for the experts of p; wide:
-// every row of the arrays starts on a 16-byte boundary.
+// every row of the arrays starts on a 16-byte boundary. Up to 64 experts and 8
+// choices four tokens share a warp: a warp a token spends most of its
+// instructions on what does not depend on the number of experts (65536 tokens
+// both ways: 25 us against 49 with 32 experts, 36 against 45 with 64). With 128
+// experts two tokens a warp lose (79 us against 60).
 #define VSF_FULL(F, N, ...)                                                              \
   (p.score == VSF_SCORE_SOFTMAX ? F<T, 32, N, true, VSF_SCORE_SOFTMAX>(__VA_ARGS__)      \
                                 : F<T, 32, N, true, VSF_SCORE_SIGMOID>(__VA_ARGS__))
 #define VSF_BY_EXPERTS(F, wide, ...)                                  \
   do {                                                                \
-    if ((wide) && p.E == 64) return VSF_FULL(F, 2, __VA_ARGS__);      \
+    if (p.K <= 8) {                                                   \
+      if (p.E <= 8) return F<T, 8, 1, false, -1>(__VA_ARGS__);        \
+      if (p.E <= 16) return F<T, 8, 2, false, -1>(__VA_ARGS__);       \
+      if (p.E <= 32) return F<T, 8, 4, false, -1>(__VA_ARGS__);       \
+      if (p.E <= 64) return F<T, 8, 8, false, -1>(__VA_ARGS__);       \
+    }                                                                 \
     if ((wide) && p.E == 128) return VSF_FULL(F, 4, __VA_ARGS__);     \
     if ((wide) && p.E == 256) return VSF_FULL(F, 8, __VA_ARGS__);     \
-    if (p.E <= 8) return F<T, 8, 1, false, -1>(__VA_ARGS__);          \
-    if (p.E <= 16) return F<T, 16, 1, false, -1>(__VA_ARGS__);        \
     if (p.E <= 32) return F<T, 32, 1, false, -1>(__VA_ARGS__);        \
     if (p.E <= 64) return F<T, 32, 2, false, -1>(__VA_ARGS__);        \
     if (p.E <= 128) return F<T, 32, 4, false, -1>(__VA_ARGS__);       \

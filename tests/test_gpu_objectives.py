@@ -426,3 +426,38 @@ def test_rows_longer_than_a_cluster_holds():
         big = policy_scale(l, old, adv, ref, w, 0.1, 0.5 / s[3], 1.0)
         check_grad(grad, g, BF16, vocab, big)
         assert (np.abs(host(stats) - s) <= big.sum() * 4 * tol(vocab) + 2.0**-22 * np.abs(s)).all()
+
+
+def test_no_tokens_of_long_rows():
+    from fsdp_buffer_layout_gb300.objectives import PolicyLoss, PreferenceLoss, TokenLogprobs
+    x, none = torch.empty(0, 40000, dtype=BF16, device="cuda"), torch.empty(0, device="cuda")
+    y = torch.empty(0, dtype=torch.int64, device="cuda")
+    assert TokenLogprobs(4, 40000)(x, y).numel() == 0
+    for mean in (True, False):
+        stats, _, grad = PolicyLoss(4, 40000, mean=mean)(x, y, none, none)
+        assert (stats == 0).all() and grad.shape == (0, 40000)
+    stats, rewards, _, _ = PreferenceLoss(1, 4, 40000)(x, y, dev([0] * 3, torch.int64))
+    assert abs(stats[0].item() - math.log(2)) < 1e-6 and (rewards == 0).all()
+
+
+@pytest.mark.parametrize("vocab", [1000, 16500, 32000])
+def test_calls_on_one_workspace_do_not_disturb_each_other(vocab):
+    """Different sizes in turn on one object, as a ragged batch gives them."""
+    from fsdp_buffer_layout_gb300.objectives import PolicyLoss, PreferenceLoss
+    rng = np.random.default_rng(12)
+    x = make_logits(rng, 2500, vocab, BF16)
+    y = dev(rng.integers(0, vocab, 2500), torch.int64)
+    old, adv = dev(rng.normal(size=2500) - 9), dev(rng.normal(size=2500))
+    op, pop = PolicyLoss(2500, vocab, kl_beta=0.1), PreferenceLoss(2, 2500, vocab)
+    sizes = (2500, 1, 160, 2100, 7, 900)
+    starts = {n: dev([0, n // 4, n // 2, n // 2, n], torch.int64) for n in sizes}
+
+    def calls(n):
+        a = op(x[:n], y[:n], old[:n], adv[:n], ref_logp=old[:n])
+        b = pop(x[:n], y[:n], starts[n], ref_logp=old[:n])
+        return [t.clone() for t in a + b]
+
+    want = {n: calls(n) for n in sizes}
+    torch.cuda.synchronize()
+    for n in sizes[::-1] + sizes:
+        assert all(torch.equal(a, b) for a, b in zip(calls(n), want[n])), n

@@ -202,3 +202,30 @@ def test_python_refusals():
         Router(4, 8, 2, dtype=FP32, sequences=2).forward(x)
     with pytest.raises(ValueError):
         Router(4, 8, 2, score="tanh")
+
+
+@pytest.mark.parametrize("experts,k", [(3, 3), (9, 8), (16, 9), (24, 4), (32, 20), (48, 8), (64, 8), (64, 12)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_few_experts(experts, k, score):
+    """Up to 64 experts: several tokens a warp up to 8 choices, one beyond."""
+    test_route_and_gradient((1037, experts, k, FP32, score, True, True, (0, 5, 5, 700, 1030), True, 0, 0))
+
+
+@pytest.mark.parametrize("sequences", [1, 31, 32, 33, 700])
+def test_many_sequences(sequences):
+    """The walk through the sequences' starts, empty ones among them, and the
+    finish by the last CTA or by a launch of its own."""
+    from fsdp_buffer_layout_gb300.objectives import Router
+    rng = np.random.default_rng(sequences)
+    starts = np.sort(rng.integers(0, 3001, sequences + 1))
+    starts[0] = 0
+    x = make(rng, 3000, 40, FP32, 3, "softmax", None)
+    op = Router(3000, 40, 3, dtype=FP32, balance=0.2, sequences=sequences)
+    more = dict(seq_starts=torch.tensor(starts, device="cuda"))
+    i, g, c, l, grad = R.route(host(x), 3, "softmax", True, 1.0, float(np.float32(0.2)), starts=starts)
+    for _ in range(2):
+        idx, gates, counts, loss = op.forward(x, **more)
+        assert np.array_equal(idx.cpu().numpy(), i) and np.array_equal(counts.cpu().numpy(), c)
+        assert abs(loss.item() - l) <= REL * abs(l) + 40 * sequences * 2.0**-40
+    got = host(op.backward(x, **more))
+    assert np.abs(got - grad).max() <= 8 * REL * max(np.abs(grad).max(), 0.2 * 40 / 3)
