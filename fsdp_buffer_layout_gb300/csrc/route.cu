@@ -779,24 +779,31 @@ cudaError_t grad_launch(const void* logits, const RouteIn& p, const int32_t* idx
 }
 
 // F<T, lanes a token, experts a lane, full, score> for the experts of p; wide:
-// every row of the arrays starts on a 16-byte boundary. Up to 64 experts and 8
-// choices four tokens share a warp: a warp a token spends most of its
-// instructions on what does not depend on the number of experts (65536 tokens
-// both ways: 25 us against 49 with 32 experts, 36 against 45 with 64). With 128
-// experts two tokens a warp lose (79 us against 60).
-#define VSF_FULL(F, N, ...)                                                              \
-  (p.score == VSF_SCORE_SOFTMAX ? F<T, 32, N, true, VSF_SCORE_SOFTMAX>(__VA_ARGS__)      \
-                                : F<T, 32, N, true, VSF_SCORE_SIGMOID>(__VA_ARGS__))
+// every row of the arrays starts on a 16-byte boundary. Both ways, 65536 tokens,
+// fp32, sigmoid, bias, top 8 (in brackets softmax, top 2), in us:
+// - Up to 8 choices four tokens share a warp: a warp a token spends most of its
+//   instructions on what does not depend on the number of experts. With 32
+//   experts 35 (29) against 53 (46), with 64 50 (43) against 58 (55).
+// - Full rows have code of their own: with 32 experts 32 (25) against 35 (29),
+//   with 64 41 (30) against 50 (43), with 256 76 against 100.
+// - With 128 full 8 lanes take 58 (40), a warp 60 (56), not full a warp 68; with
+//   256 two tokens a warp take 103 against 76.
+#define VSF_FULL(F, L, N, ...)                                                           \
+  (p.score == VSF_SCORE_SOFTMAX ? F<T, L, N, true, VSF_SCORE_SOFTMAX>(__VA_ARGS__)       \
+                                : F<T, L, N, true, VSF_SCORE_SIGMOID>(__VA_ARGS__))
 #define VSF_BY_EXPERTS(F, wide, ...)                                  \
   do {                                                                \
     if (p.K <= 8) {                                                   \
+      if ((wide) && p.E == 32) return VSF_FULL(F, 8, 4, __VA_ARGS__); \
+      if ((wide) && p.E == 64) return VSF_FULL(F, 8, 8, __VA_ARGS__); \
+      if ((wide) && p.E == 128) return VSF_FULL(F, 8, 16, __VA_ARGS__); \
       if (p.E <= 8) return F<T, 8, 1, false, -1>(__VA_ARGS__);        \
       if (p.E <= 16) return F<T, 8, 2, false, -1>(__VA_ARGS__);       \
       if (p.E <= 32) return F<T, 8, 4, false, -1>(__VA_ARGS__);       \
       if (p.E <= 64) return F<T, 8, 8, false, -1>(__VA_ARGS__);       \
     }                                                                 \
-    if ((wide) && p.E == 128) return VSF_FULL(F, 4, __VA_ARGS__);     \
-    if ((wide) && p.E == 256) return VSF_FULL(F, 8, __VA_ARGS__);     \
+    if ((wide) && p.E == 128) return VSF_FULL(F, 32, 4, __VA_ARGS__); \
+    if ((wide) && p.E == 256) return VSF_FULL(F, 32, 8, __VA_ARGS__); \
     if (p.E <= 32) return F<T, 32, 1, false, -1>(__VA_ARGS__);        \
     if (p.E <= 64) return F<T, 32, 2, false, -1>(__VA_ARGS__);        \
     if (p.E <= 128) return F<T, 32, 4, false, -1>(__VA_ARGS__);       \

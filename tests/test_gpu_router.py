@@ -125,6 +125,21 @@ def test_ties_infinities_and_nan(dtype):
     assert torch.isfinite(grad).all() and grad[2, 0].item() == 0
 
 
+@pytest.mark.parametrize("experts,k", [(5, 5), (8, 8), (15, 3), (32, 4), (32, 12), (40, 8), (64, 8), (64, 32),
+                                       (100, 6), (128, 8), (128, 30), (200, 8), (256, 8), (256, 32), (400, 10)])
+def test_ties_go_to_the_lowest_expert(experts, k):
+    """Few different logits, so that the K-th place is mostly a tie; all equal
+    in the last rows; some -inf (after every finite logit)."""
+    from fsdp_buffer_layout_gb300.objectives import Router
+    rng = np.random.default_rng(experts + k)
+    x = rng.integers(0, 3, (500, experts)).astype(np.float32)
+    x[100:200][rng.random((100, experts)) < 0.9] = -math.inf
+    x[450:] = 1.0
+    want = np.argsort(-x, axis=1, kind="stable")[:, :k]
+    for dtype in (BF16, FP32):
+        idx = Router(500, experts, k, dtype=dtype).forward(torch.from_numpy(x).to("cuda", dtype))[0]
+        assert np.array_equal(idx.cpu().numpy(), want)
+
 def test_nothing_live_and_no_tokens():
     from fsdp_buffer_layout_gb300.objectives import Router
     op = Router(70, 12, 3, dtype=FP32, balance=0.1)
@@ -204,11 +219,13 @@ def test_python_refusals():
         Router(4, 8, 2, score="tanh")
 
 
-@pytest.mark.parametrize("experts,k", [(3, 3), (9, 8), (16, 9), (24, 4), (32, 20), (48, 8), (64, 8), (64, 12)])
+@pytest.mark.parametrize("experts,k", [(3, 3), (9, 8), (16, 9), (24, 4), (32, 20), (32, 5), (48, 8), (64, 8),
+                                       (64, 12), (128, 3), (128, 8), (128, 11)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
-def test_route_few_experts(experts, k, score):
-    """Up to 64 experts: several tokens a warp up to 8 choices, one beyond."""
-    test_route_and_gradient((1037, experts, k, FP32, score, True, True, (0, 5, 5, 700, 1030), True, 0, 0))
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_route_several_tokens_a_warp(experts, k, score, dtype):
+    """Several tokens a warp up to 8 choices of up to 64, or of 128 experts, else one."""
+    test_route_and_gradient((1037, experts, k, dtype, score, True, True, (0, 5, 5, 700, 1030), True, 0, 0))
 
 
 @pytest.mark.parametrize("sequences", [1, 31, 32, 33, 700])
