@@ -299,8 +299,10 @@ __global__ void __launch_bounds__(kPairThreads)
     const float away = expf(-fabsf(z)), tail = log1pf(away);
     const float up = (z < 0.f ? away : 1.f) / (1.f + away);  // s(z)
     const float down = (z < 0.f ? 1.f : away) / (1.f + away);  // 1 - s(z)
+    // without smoothing a rejected token of probability 0 costs nothing (z = inf)
+    const float swapped = tail + (z < 0.f ? 0.f : z);
     loss = (1.f - p.smoothing) * (tail - (z > 0.f ? 0.f : z)) +
-           p.smoothing * (tail + (z < 0.f ? 0.f : z));
+           (p.smoothing != 0.f ? p.smoothing * swapped : 0.f);
     slope = p.beta * (p.smoothing * up - (1.f - p.smoothing) * down);
   } else {
     const float gap = h - 0.5f / p.beta;

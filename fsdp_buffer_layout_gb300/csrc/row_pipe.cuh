@@ -28,7 +28,7 @@
 // Bounds and measurements (GB300, a call among others). Sums alone read at the
 // rate of a plain copy: 4096 x 131072 bf16, 3/4 live, 118 us = 6.8 TB/s. The
 // policy loss is bound by HBM where a CTA's share is long (8192 x 131072 bf16:
-// 715 us, 6.0 TB/s read and written; clusters of 4 leave 8 of the 152 SMs idle)
+// 691 us, 6.2 TB/s read and written; clusters of 4 leave 8 of the 152 SMs idle)
 // and by a row's fixed cost, about 1.8 us of the consumers' time however short
 // the row, where it is not (4096 x 32000 bf16, 3/4 live: 80 us, 5.7 TB/s).
 // A call costs some 10 us from its first load to its last sum.

@@ -527,6 +527,7 @@ vsf_status vsf_policy_loss(const void* logits, int32_t dtype, int64_t T, int64_t
  *   sum is not 0], h = D_chosen - D_rejected:
  *   VSF_PREF_SIGMOID: z = beta h - margin,
  *                     L = -(1 - smoothing) ln s(z) - smoothing ln s(-z)
+ *                     (no second term where smoothing = 0, z = inf included)
  *   VSF_PREF_SQUARED: L = (h - 1/(2 beta))^2
  *   loss = scale/pairs sum L;  grad = d loss / d logits.
  * ref_logp: fp32[T] or NULL (0: no reference). stats: fp32[2] = loss, mean of

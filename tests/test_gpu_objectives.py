@@ -461,3 +461,35 @@ def test_calls_on_one_workspace_do_not_disturb_each_other(vocab):
     torch.cuda.synchronize()
     for n in sizes[::-1] + sizes:
         assert all(torch.equal(a, b) for a, b in zip(calls(n), want[n])), n
+
+
+@pytest.mark.parametrize("vocab", [257, 20000])
+def test_preference_of_impossible_tokens(vocab):
+    """A target of probability 0 (a -inf logit): the pair's log ratio is
+    infinite, the loss 0 or inf, the gradient what the saturated slope gives."""
+    from fsdp_buffer_layout_gb300.objectives import PreferenceLoss
+    rng = np.random.default_rng(13)
+    x = make_logits(rng, 12, vocab, BF16)
+    y = rng.integers(0, vocab, 12)
+    starts = dev([0, 3, 6, 9, 12], torch.int64)
+    op = PreferenceLoss(2, 12, vocab, beta=0.25)
+    for row, first_loss, reward in ((7, 0.0, 2), (1, math.inf, 0)):
+        z = x.clone()
+        z[row, y[row]] = -math.inf
+        stats, rewards, logp, grad = op(z, dev(y, torch.int64), starts)
+        assert logp[row].item() == -math.inf and rewards[reward].item() == -math.inf
+        assert op.device_error() == 0
+        g = host(grad)
+        assert np.isfinite(g).all()
+        p = np.exp(R.log_softmax(host(z)))
+        a = 0.0 if first_loss == 0.0 else 0.25 / 2
+        for t in (0, 1, 2, 6, 7, 8):  # the first pair: chosen up, rejected down
+            want = (1 if t < 3 else -1) * a * (p[t] - (np.arange(vocab) == y[t]))
+            assert np.abs(g[t] - want).max() <= 2.0**-8 * max(a, 1e-30)
+        pair = op.stats[0].item()
+        if first_loss == 0.0:  # the second pair's alone, over two
+            h = (host(logp)[3:6].sum() - host(logp)[9:12].sum()) * 0.25
+            want = (math.log1p(math.exp(-abs(h))) + max(-h, 0.0)) / 2
+            assert abs(pair - want) <= 1e-5 * max(1.0, abs(want))
+        else:
+            assert pair == math.inf
