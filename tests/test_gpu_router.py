@@ -129,13 +129,15 @@ def test_ties_infinities_and_nan(dtype):
                                        (100, 6), (128, 8), (128, 30), (200, 8), (256, 8), (256, 32), (400, 10)])
 def test_ties_go_to_the_lowest_expert(experts, k):
     """Few different logits, so that the K-th place is mostly a tie; all equal
-    in the last rows; some -inf (after every finite logit)."""
+    in the last rows; some -inf (after every finite logit) and NaN (last)."""
     from fsdp_buffer_layout_gb300.objectives import Router
     rng = np.random.default_rng(experts + k)
     x = rng.integers(0, 3, (500, experts)).astype(np.float32)
     x[100:200][rng.random((100, experts)) < 0.9] = -math.inf
     x[450:] = 1.0
-    want = np.argsort(-x, axis=1, kind="stable")[:, :k]
+    x[150:250][rng.random((100, experts)) < 0.5] = math.nan
+    order = np.where(np.isnan(x), 10.0, np.where(np.isinf(x), 5.0, -x))
+    want = np.argsort(order, axis=1, kind="stable")[:, :k]
     for dtype in (BF16, FP32):
         idx = Router(500, experts, k, dtype=dtype).forward(torch.from_numpy(x).to("cuda", dtype))[0]
         assert np.array_equal(idx.cpu().numpy(), want)
