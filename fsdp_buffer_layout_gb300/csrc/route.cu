@@ -398,8 +398,10 @@ __device__ float route_finish(const RouteIn& p, const RouteSums& w, const RouteO
   return l;
 }
 
-// CTAs an SM: registers for the token ahead as well. At 256 experts 3 run in 93 us
-// (65536 tokens, both ways) where 4, which spill, take 105 and 2 take 106.
+// CTAs an SM: registers for the token ahead as well. At 256 experts 3 run in 76 us
+// (65536 tokens, both ways) where 4, which spill, take 90 and 2 take 88; at 32
+// experts (4 a lane) 4 run in 33 where 3 and 6 take 38; at 512 2 run in 179 where
+// 3 take 325 and 1 takes 182 (rows not full).
 constexpr int route_ctas(int n) { return n <= 4 ? 4 : n <= 8 ? 3 : 2; }
 
 // SCORE: the score's kind, or -1 where it is known at run time only.
@@ -785,7 +787,8 @@ cudaError_t grad_launch(const void* logits, const RouteIn& p, const int32_t* idx
 //   instructions on what does not depend on the number of experts. With 32
 //   experts 35 (29) against 53 (46), with 64 50 (43) against 58 (55).
 // - Full rows have code of their own: with 32 experts 32 (25) against 35 (29),
-//   with 64 41 (30) against 50 (43), with 256 76 against 100.
+//   with 64 41 (30) against 50 (43), with 256 76 against 100, with 512 123
+//   against 179.
 // - With 128 full 8 lanes take 58 (40), a warp 60 (56), not full a warp 68; with
 //   256 two tokens a warp take 103 against 76.
 #define VSF_FULL(F, L, N, ...)                                                           \
@@ -804,6 +807,7 @@ cudaError_t grad_launch(const void* logits, const RouteIn& p, const int32_t* idx
     }                                                                 \
     if ((wide) && p.E == 128) return VSF_FULL(F, 32, 4, __VA_ARGS__); \
     if ((wide) && p.E == 256) return VSF_FULL(F, 32, 8, __VA_ARGS__); \
+    if ((wide) && p.E == 512) return VSF_FULL(F, 32, 16, __VA_ARGS__); \
     if (p.E <= 32) return F<T, 32, 1, false, -1>(__VA_ARGS__);        \
     if (p.E <= 64) return F<T, 32, 2, false, -1>(__VA_ARGS__);        \
     if (p.E <= 128) return F<T, 32, 4, false, -1>(__VA_ARGS__);       \

@@ -126,7 +126,8 @@ def test_ties_infinities_and_nan(dtype):
 
 
 @pytest.mark.parametrize("experts,k", [(5, 5), (8, 8), (15, 3), (32, 4), (32, 12), (40, 8), (64, 8), (64, 32),
-                                       (100, 6), (128, 8), (128, 30), (200, 8), (256, 8), (256, 32), (400, 10)])
+                                       (100, 6), (128, 8), (128, 30), (200, 8), (256, 8), (256, 32), (400, 10),
+                                       (512, 8), (512, 20)])
 def test_ties_go_to_the_lowest_expert(experts, k):
     """Few different logits, so that the K-th place is mostly a tie; all equal
     in the last rows; some -inf (after every finite logit) and NaN (last)."""
@@ -222,11 +223,12 @@ def test_python_refusals():
 
 
 @pytest.mark.parametrize("experts,k", [(3, 3), (9, 8), (16, 9), (24, 4), (32, 20), (32, 5), (48, 8), (64, 8),
-                                       (64, 12), (128, 3), (128, 8), (128, 11)])
+                                       (64, 12), (128, 3), (128, 8), (128, 11), (512, 10)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_route_several_tokens_a_warp(experts, k, score, dtype):
-    """Several tokens a warp up to 8 choices of up to 64, or of 128 experts, else one."""
+    """Several tokens a warp up to 8 choices of up to 64, or of 128 experts, else
+    one; full rows and others."""
     test_route_and_gradient((1037, experts, k, dtype, score, True, True, (0, 5, 5, 700, 1030), True, 0, 0))
 
 
