@@ -137,6 +137,17 @@ __device__ __forceinline__ F2 exp_pair(F2 x, F2 nm, const PairScale& c) {
   return f2(ex2(a), ex2(b));
 }
 
+// Whether a row's gradient may take its terms as 2^(x c - m c), one fused product
+// an element instead of a difference and two products. m c is rounded once, so
+// the exponent is off by half a unit of |m c|'s last place, in every term the
+// same way: 2^-14 below 2^11, less than a 40th of what bf16's rounding takes (2^-9 to
+// 2^-8). Not for fp32, nor for rows farther from 0 or temperatures nearer to it.
+// m: as subtracted (finite_max).
+template <typename T>
+__device__ __forceinline__ bool short_exponent(float m, Log2Scale c) {
+  return sizeof(T) == 2 && fabsf(m * c.hi) < 2048.f;
+}
+
 __device__ __forceinline__ uint32_t cta_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -694,9 +705,7 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
         const float z = finite_max(res.x), b = res.y, coef = res.z;
         T* g = a.grad + p.t * a.grad_ld;
         const bool same = (reinterpret_cast<uintptr_t>(g) & 15) == p.skew;
-        // bf16 keeps 8 bits: there 2^(x c - m c) with rounded c and m c serves,
-        // where m c does not overflow
-        const bool near = sizeof(T) == 2 && fabsf(z) < 1e30f;
+        const bool near = short_exponent<T>(z, r.c);
         const F2 nm = f2(-z, -z), b2 = f2(b, b), c0 = f2(r.c.hi, r.c.hi);
         const F2 kk = f2(-z * r.c.hi, -z * r.c.hi);
         uint4* gv = reinterpret_cast<uint4*>(g + p.head);
@@ -929,7 +938,7 @@ __device__ __forceinline__ void grad_piece(const Rows<T>& r, int64_t t, int32_t 
   const int32_t ye = y - s.head, yv = ye / VE;
   const bool mine = ye >= 0 && yv >= begin && yv < end;  // the target is in this piece
   if (((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0) {
-    const bool near = sizeof(T) == 2 && fabsf(z) < 1e30f;
+    const bool near = short_exponent<T>(z, r.c);
     const F2 nm = f2(-z, -z), b2 = f2(b, b), c0 = f2(r.c.hi, r.c.hi);
     const F2 kk = f2(-z * r.c.hi, -z * r.c.hi);
     const uint4* in = reinterpret_cast<const uint4*>(x + s.head) + tid;

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kRegsThreads, regs_ctas(NV))
       continue;
     }
     const float zm = finite_max(ms.m), b = -coef / ms.s;
-    const bool near = sizeof(T) == 2 && fabsf(zm) < 1e30f;
+    const bool near = short_exponent<T>(zm, r.c);
     const bool same = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
     const F2 nz = f2(-zm, -zm), b2 = f2(b, b), c0 = f2(r.c.hi, r.c.hi);
     const F2 kk = f2(-zm * r.c.hi, -zm * r.c.hi);

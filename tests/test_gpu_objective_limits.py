@@ -1,0 +1,201 @@
+"""The losses where rounding, size and place go wrong: rows far from zero, small
+and large temperatures, long rows and long calls, and the elements of a
+gradient that a loose tolerance would not see.
+
+Tolerances, from the arithmetic. With t = (x - m) log2(e) / temperature, a term
+2^t of a row's sum is within 2^-22 (ex2.approx) and |t| 2^-22 of its value (the
+difference, c and the product are rounded once each: 3 |t| 2^-24); a thread adds
+at most V / 256 + 40 of them in fp32. That bounds the relative error of the sum
+and the absolute one of ln p (tol). Away from the target a gradient element is
+-a p: its error is relative, a's share (coef_error) plus the sum's, the term's
+and the output's rounding (bf16, 8 significant bits: 2^-8). A row of bf16 may
+have the term 2^(x c - m c) with m c rounded once, where |m c| < 2^11: 2^-14 in
+the exponent. At the target a (1 - p) cancels: a's error and p's, absolutely.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import objective_reference as R
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP32 = torch.bfloat16, torch.float32
+LN2 = math.log(2)
+
+
+def host(x):
+    return x.double().cpu().numpy()
+
+
+def dev(a, dtype=torch.float32):
+    return torch.tensor(np.asarray(a), dtype=dtype, device="cuda")
+
+
+def tol(vocab):
+    return 2.0**-22 + (math.log2(vocab) + 1) * 2.0**-22 + (vocab / 256 + 40) * 2.0**-24
+
+
+def logp_error(vocab, logp):
+    return tol(vocab) + 2.0**-23 * np.abs(logp) + 1e-9
+
+
+def nan_rows(tokens, vocab, dtype, pad, shift=0):
+    """A gradient buffer of NaN: (buffer, rows of stride vocab + pad in it)."""
+    ld = vocab + pad
+    buf = torch.full((shift + tokens * ld + 64,), math.nan, dtype=dtype, device="cuda")
+    return buf, buf.as_strided((tokens, vocab), (ld, 1), shift)
+
+
+def check_gradient(got, x, targets, slope, slope_error, inv_t, dtype):
+    """got against slope_t inv_t (1[v = y] - p): slope in 64 bits (None: a masked
+    row, zeros), slope_error its relative error."""
+    vocab = x.shape[1]
+    for t, a in enumerate(slope):
+        row = got[t]
+        if a is None or a == 0:
+            assert not row.any(), t
+            continue
+        z = torch.from_numpy(x[t]).cuda() * inv_t
+        z = z - z.max()
+        p = torch.softmax(z, 0)
+        y = int(targets[t])
+        want = -a * inv_t * p
+        rounding = 2.0**-8 if dtype == BF16 else 2.0**-23
+        term = 2.0**-22 + z.clamp(min=-110.0).abs() / LN2 * 2.0**-22 * LN2
+        if dtype == BF16:
+            term = term + 2.0**-14 * LN2
+        rel = slope_error[t] + 2 * tol(vocab) + term + rounding
+        full = abs(a * inv_t)
+        lim = rel * want.abs() + 2.0**-126 * (1 + full)  # (terms below 2^-126 are flushed)
+        py = float(p[y])
+        want[y] += a * inv_t
+        lim[y] = full * (slope_error[t] + rounding * abs(1 - py) + py * (2 * tol(vocab) + float(term[y])) + 2.0**-22)
+        err = (row.double() - want).abs()
+        assert bool((err <= lim).all()), (t, float((err / lim).max()), int((err / lim).argmax()))
+
+
+def policy_slope_error(lp, old, adv, ref, w, beta, f, slope, vocab):
+    """Relative error of slope = f w (-r A - beta (exp u - 1)): r's and exp(u)'s
+    is ln p's error and a few roundings."""
+    out = []
+    for t, a in enumerate(slope):
+        if not a:
+            out.append(0.0)
+            continue
+        e = logp_error(vocab, lp[t]) + 2.0**-23 * (abs(old[t]) + abs(ref[t])) + 2.0**-20
+        out.append(abs(f * w[t]) * (abs(np.exp(lp[t] - old[t]) * adv[t]) + beta * (1 + np.exp(ref[t] - lp[t]))) * e / abs(a))
+    return out
+
+
+def policy_stats_error(w, adv, f, slope, err):
+    """Of a sum of terms: what ln p's error moves, and each term's own rounding
+    (a clipped one, too, is w times a bound times A)."""
+    return sum(abs(a or 0) * e for a, e in zip(slope, err)) + abs(f) * float(np.abs(w * adv).sum()) * 2.0**-21
+
+
+def policy_inputs(rng, lp, beta):
+    """old, ref, advantages around log probabilities, away from the clipping
+    range's ends."""
+    n = len(lp)
+    ratio = np.exp(0.3 * rng.normal(size=n))
+    for end in (0.8, 1.25):
+        ratio = np.where(np.abs(ratio - end) < 0.02, ratio + 0.05, ratio)
+    old = (lp - np.log(ratio)).astype(np.float32)
+    ref = (lp + 0.3 * rng.normal(size=n)).astype(np.float32)
+    adv = rng.normal(size=n).astype(np.float32)
+    return old, ref, np.where(np.abs(adv) < 0.1, np.float32(0.5), adv)
+
+
+def check_policy(x, y, w, beta=0.1, mean=True, inv_t=1.0, pad=0, shift=0, in_place=False, seed=0):
+    """One call on device logits x against the 64-bit form: stats, logp, every
+    element of the gradient, and nothing written beside its rows."""
+    from fsdp_buffer_layout_gb300.objectives import PolicyLoss
+    tokens, vocab = x.shape
+    dtype, rng = x.dtype, np.random.default_rng(seed)
+    t64 = float(np.float32(inv_t))
+    live, _ = R.live_tokens(y, w, vocab)
+    clean = host(torch.where(dev(live, torch.bool)[:, None], x, torch.zeros_like(x)))
+    lp = R.logprobs(clean, y, t64, w)
+    old, ref, adv = policy_inputs(rng, lp, beta)
+    stats, lp, _, slope = R.policy(clean, y, old, adv, ref, w, 0.2, 0.25, beta, t64, 0.5, mean)
+    op = PolicyLoss(tokens, vocab, dtype=dtype, clip_low=0.2, clip_high=0.25, kl_beta=beta,
+                    inv_temperature=inv_t, scale=0.5, mean=mean)
+    buf, g = (None, x) if in_place else nan_rows(tokens, vocab, dtype, pad, shift)
+    out = op(x, dev(y, torch.int64), dev(old), dev(adv), ref_logp=dev(ref) if beta else None,
+             weights=dev(w), grad=g)
+    assert (np.abs(host(out[1]) - lp) <= logp_error(vocab, lp)).all()
+    f = 0.5 / stats[3] if mean else 0.5
+    err = policy_slope_error(lp, old, adv, ref, w, beta, f, slope, vocab)
+    lim = policy_stats_error(w * live, adv, f, slope, err) + np.abs(stats) * 2.0**-20
+    assert (np.abs(host(out[0]) - stats) <= lim).all()
+    check_gradient(out[2], clean, y, slope, err, t64, dtype)
+    if buf is not None:
+        outside = torch.ones_like(buf, dtype=torch.bool)
+        outside.as_strided((tokens, vocab), g.stride(), shift)[:] = False
+        assert bool(torch.isnan(buf[outside]).all())
+    assert op.device_error() == 0
+
+
+FAR = [-1e9, -1e6, 3e5, -1.3e5, 1.5e7, 1e8, 2.7e9, -1e20, 2000.0, -1400.0, 1500.0]
+
+
+def far_rows(vocab, seed):
+    """bf16 rows whose maximum is far from 0: every third word at the maximum,
+    the others a step or more below it (a row of one value at the end)."""
+    rng = np.random.default_rng(seed)
+    x = np.empty((len(FAR) + 1, vocab), np.float32)
+    for r, m in enumerate(FAR):
+        x[r] = m - abs(m) * 2.0**-6 * rng.integers(0, 3, vocab)
+        x[r, ::3] = m
+    x[-1] = -1e9
+    return torch.from_numpy(x).to("cuda", BF16)
+
+
+# words: rows held by registers of 1 and 8 warps, the pipelined kernel, its ring
+# with one row's share, and the gradient as a pass of its own
+@pytest.mark.parametrize("vocab", [700, 9000, 32000, 420000, 800000])
+def test_policy_gradient_of_rows_far_from_zero(vocab):
+    x = far_rows(vocab, vocab)
+    y = np.random.default_rng(1).integers(0, vocab, len(x))
+    y[0] = 0  # (at the maximum)
+    lp = R.logprobs(host(x), y)
+    y = np.where(lp < -80, 3 * (y // 3), y)  # a probability that fp32 holds
+    check_policy(x, y, np.linspace(0.5, 1.5, len(x)).astype(np.float32), pad=8)
+
+
+@pytest.mark.parametrize("vocab", [700, 9000, 32000, 420000, 800000])
+@pytest.mark.parametrize("inv_t", [1e3, 1e5])
+def test_policy_gradient_at_small_temperatures(vocab, inv_t):
+    """Ordinary logits near temperature 0: the words tied at the maximum (bf16
+    has many) share the probability."""
+    rng = np.random.default_rng(vocab)
+    x = torch.from_numpy((2.5 * rng.normal(size=(6, vocab))).astype(np.float32)).to("cuda", BF16)
+    top = x.float().amax(1)
+    for r, k in enumerate((1, 2, 3, 7, 64, 500)):
+        x[r, torch.from_numpy(rng.choice(vocab, k, replace=False)).cuda()] = top[r].to(BF16)
+    y = x.float().argmax(1).cpu().numpy()
+    check_policy(x, y, np.ones(6, np.float32), inv_t=inv_t, pad=8)
+
+
+@pytest.mark.parametrize("vocab", [700, 32000])
+@pytest.mark.parametrize("inv_t", [1.0, 1e3])
+def test_preference_gradient_of_rows_far_from_zero(vocab, inv_t):
+    from fsdp_buffer_layout_gb300.objectives import PreferenceLoss
+    x = far_rows(vocab, 5)
+    if inv_t != 1.0:
+        x[:] = torch.from_numpy(2.5 * np.random.default_rng(3).normal(size=tuple(x.shape)))
+        x[:, ::3] = x.float().amax(1, keepdim=True).to(BF16)
+    n = len(x)
+    y = 3 * np.random.default_rng(2).integers(0, vocab // 3, n)  # at the maximum
+    starts, t64 = [0, n // 2, n], float(np.float32(inv_t))
+    buf, g = nan_rows(n, vocab, BF16, 8)
+    out = PreferenceLoss(1, n, vocab, beta=0.1, inv_temperature=inv_t)(
+        x, dev(y, torch.int64), dev(starts, torch.int64), grad=g)
+    lp, slope = (R.preference(host(x), y, starts, None, None, "sigmoid", 0.1, 0.0, 0.0, False, t64, 1.0)[i] for i in (2, 4))
+    assert (np.abs(host(out[2]) - lp) <= logp_error(vocab, lp)).all()
+    # s(z) moves by at most beta d h relatively
+    check_gradient(out[3], host(x), y, slope, [2.0**-20 + 0.1 * n * logp_error(vocab, lp).max()] * n,
+                   t64, BF16)
