@@ -136,7 +136,8 @@ class _LogitsLoss(_Objective):
         if self.grad is None:
             return None, None, self.width
         pad = (ld - self.width) % self._step
-        return self._first(self._view(pad), n), self._grad_at, self.width + pad
+        self.grad = self._view(pad)  # (the attribute shows what the call writes)
+        return self._first(self.grad, n), self._grad_at, self.width + pad
 
 
 class PolicyLoss(_LogitsLoss):

@@ -199,3 +199,21 @@ def test_preference_gradient_of_rows_far_from_zero(vocab, inv_t):
     # s(z) moves by at most beta d h relatively
     check_gradient(out[3], host(x), y, slope, [2.0**-20 + 0.1 * n * logp_error(vocab, lp).max()] * n,
                    t64, BF16)
+
+
+@pytest.mark.parametrize("dtype,vocab", [(FP32, 50), (FP32, 1003), (BF16, 1003)])
+def test_grad_attribute_is_the_last_calls_gradient(dtype, vocab):
+    """The object's `grad` shows the rows of the last call whatever the logits'
+    stride was."""
+    from fsdp_buffer_layout_gb300.objectives import PolicyLoss, PreferenceLoss
+    rng = np.random.default_rng(1)
+    y = dev(rng.integers(0, vocab, 6), torch.int64)
+    old, adv = dev(np.full(6, -5.0)), dev(rng.normal(size=6))
+    starts = dev([0, 3, 6], torch.int64)
+    op, pref = PolicyLoss(6, vocab, dtype=dtype), PreferenceLoss(1, 6, vocab, dtype=dtype)
+    for pad in (0, 1, 2, 0, 5):
+        x = torch.from_numpy(rng.normal(size=(6, vocab + pad)).astype(np.float32)).to("cuda", dtype)[:, :vocab]
+        got = op(x, y, old, adv)[2]
+        assert torch.equal(op.grad, got) and op.grad.data_ptr() == got.data_ptr()
+        got = pref(x, y, starts)[3]
+        assert torch.equal(pref.grad, got)
