@@ -8,9 +8,12 @@ Router          top-k choice, gates, per-expert counts, balance loss; gradient
 
 An object owns its workspace and its outputs, sized for the largest call
 (`tokens` rows); a call returns views of the outputs, which the next call of
-the same object overwrites, on the object's stream. As everywhere in the
-library nothing is synchronised: a caller that works on another stream orders
-the two itself. The formulas stand at the C functions in include/vsf.h.
+the same object overwrites, on the object's stream, whose memory they are. As
+everywhere in the library nothing is synchronised: a caller that works on
+another stream orders the two itself, and keeps inputs and outputs (or
+record_stream()s them) until the other stream is done with them. The object's
+device has to be the current one. The formulas stand at the C functions in
+include/vsf.h.
 """
 from __future__ import annotations
 
@@ -39,7 +42,11 @@ class _Objective:
         self._st = self.stream.cuda_stream
 
     def _new(self, *shape, dtype=torch.float32):
-        return torch.empty(*shape, dtype=dtype, device=self.device)
+        # Memory of the object's own stream: a block of the caller's could still
+        # be in use there while it is prepared here, or be handed out again there
+        # while the last call runs.
+        with torch.cuda.stream(self.stream):
+            return torch.empty(*shape, dtype=dtype, device=self.device)
 
     def _workspace(self, nbytes: int):
         if not nbytes:

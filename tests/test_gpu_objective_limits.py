@@ -217,3 +217,26 @@ def test_grad_attribute_is_the_last_calls_gradient(dtype, vocab):
         assert torch.equal(op.grad, got) and op.grad.data_ptr() == got.data_ptr()
         got = pref(x, y, starts)[3]
         assert torch.equal(pref.grad, got)
+
+
+def test_buffers_belong_to_the_objects_stream():
+    """Workspace and outputs come from the memory of the object's own stream, on
+    which they are prepared, written and, at the end, given back: memory of the
+    caller's stream could still be in use there."""
+    from fsdp_buffer_layout_gb300.objectives import PolicyLoss, PreferenceLoss, Router, TokenLogprobs
+    side = torch.cuda.Stream()
+    ops = [TokenLogprobs(5, 100, stream=side), PolicyLoss(5, 100, stream=side),
+           PreferenceLoss(1, 5, 100, stream=side), Router(5, 16, 2, stream=side)]
+    x = torch.randn(5, 16, device="cuda", dtype=BF16)
+    torch.cuda.synchronize()
+    ops[3].forward(x)
+    ops[3].backward(x)
+    side.synchronize()
+    segments = torch.cuda.memory_snapshot()
+    for op in ops:
+        held = [v for v in vars(op).values() if isinstance(v, torch.Tensor)]
+        assert len(held) >= 2
+        for v in held:
+            at = v.untyped_storage().data_ptr()
+            home = [s["stream"] for s in segments if s["address"] <= at < s["address"] + s["total_size"]]
+            assert home == [side.cuda_stream], (type(op).__name__, tuple(v.shape))
