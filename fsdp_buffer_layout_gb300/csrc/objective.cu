@@ -194,7 +194,8 @@ __device__ __forceinline__ double block_sum(double v, double* part) {
 // Policy loss of every token in one CTA, and the gradient's coefficients.
 template <typename T>
 __global__ void __launch_bounds__(kTokenThreads)
-    policy_tokens_kernel(Rows<T> r, PolicyIn p, const float4* row, float* coef, float* stats) {
+    policy_tokens_kernel(Rows<T> r, PolicyIn p, const float4* row, float* coef, float* stats,
+                         WsHead* head) {
   __shared__ double part[kTokenThreads / 32];
   take_turn();
   double n = 0.0;
@@ -225,6 +226,7 @@ __global__ void __launch_bounds__(kTokenThreads)
     stats[1] = (float)pol;
     stats[2] = (float)kl;
     stats[3] = (float)n;
+    head->rows = 1;
   }
 }
 
@@ -345,6 +347,7 @@ __global__ void __launch_bounds__(kPairThreads)
     stats[0] = (float)((double)p.scale * l / (double)p.pairs);
     stats[1] = (float)(m / (double)p.pairs);
     head->ticket = 0;
+    head->rows = 1;
   }
 }
 
@@ -572,7 +575,7 @@ cudaError_t policy(const RowsArg& a, const PolicyIn& p, float* stats, float* log
   cudaError_t e = launch_stats(r, w.row, logp, w, st);
   if (e != cudaSuccess) return e;
   e = launch_behind(policy_tokens_kernel<T>, 1, kTokenThreads, 0, 1, st, r, p, (const float4*)w.row,
-                    w.coef, stats);
+                    w.coef, stats, w.head);
   if (e != cudaSuccess) return e;
   return launch_grad(r, w, grad, grad_ld, st);
 }

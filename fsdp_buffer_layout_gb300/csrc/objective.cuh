@@ -18,17 +18,18 @@ namespace vsf {
 
 // First words of every objective workspace, zeroed by
 // vsf_objective_workspace_init and left zero by each call (but for the error
-// word, which the caller reads).
+// word, which the caller reads, and `rows`).
 struct WsHead {
   uint32_t err;     // device error word: see vsf.h
   uint32_t ticket;  // CTAs of the running launch that have finished
   uint32_t nan;     // a NaN score was seen (router)
-  uint32_t pad;
+  uint32_t rows;    // a loss has left its rows' sums behind the head: not for a router
   float part[16];   // parts of a loss (router)
 };
 static_assert(sizeof(WsHead) % 16 == 0, "what follows the head is 16-byte aligned");
 
 constexpr uint32_t kErrTarget = 16u;  // error-word bit: a target >= V
+constexpr uint32_t kErrShared = 32u;  // error-word bit: a router on a loss's workspace
 
 namespace obj {
 

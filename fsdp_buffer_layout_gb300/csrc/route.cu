@@ -398,6 +398,16 @@ __device__ float route_finish(const RouteIn& p, const RouteSums& w, const RouteO
   return l;
 }
 
+// The call's end, by one thread: the loss, and the head as the next call wants
+// it. Where a loss has used the workspace, its rows lay among the sums.
+__device__ __forceinline__ void route_close(WsHead* head, float* loss, float l) {
+  const bool shared = __ldcg(&head->rows) != 0u;
+  if (shared) atomicOr(&head->err, kErrShared);
+  *loss = shared || __ldcg(&head->nan) ? NAN : l;
+  head->nan = 0u;
+  head->ticket = 0u;
+}
+
 // CTAs an SM: registers for the token ahead as well. At 256 experts 3 run in 76 us
 // (65536 tokens, both ways) where 4, which spill, take 90 and 2 take 88; at 32
 // experts (4 a lane) 4 run in 33 where 3 and 6 take 38; at 512 2 run in 179 where
@@ -540,11 +550,7 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(N))
   }
   const float l = route_finish(p, w, o, 0, p.E, true);
   for (int64_t s = tid; s < p.sequences; s += kRouteThreads) w.tokens[s] = 0;
-  if (tid == 0) {
-    *o.loss = __ldcg(&head->nan) ? NAN : l;
-    head->nan = 0u;
-    head->ticket = 0u;
-  }
+  if (tid == 0) route_close(head, o.loss, l);
 }
 
 // The finish as a launch of its own, for many sequences: 32 experts a CTA.
@@ -569,9 +575,7 @@ __global__ void __launch_bounds__(kRouteThreads)
   if (tid == 0) {
     float sum = 0.f;
     for (uint32_t i = 0; i < gridDim.x; ++i) sum += __ldcg(&head->part[i]);
-    *o.loss = __ldcg(&head->nan) ? NAN : sum;
-    head->nan = 0u;
-    head->ticket = 0u;
+    route_close(head, o.loss, sum);
   }
 }
 

@@ -374,6 +374,7 @@ __device__ __forceinline__ void policy_stats(const PipeArgs<T>& a, int64_t n, in
     a.stats[2] = (float)(f * v[1]);
     a.stats[3] = (float)v[2];
     a.head->ticket = 0;
+    a.head->rows = 1;
   }
 }
 

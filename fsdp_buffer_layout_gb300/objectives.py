@@ -87,7 +87,8 @@ class _Objective:
         return buf if n == self.tokens else buf[:n]
 
     def device_error(self) -> int:
-        """The device error word (0: no wait ran out, every target in range)."""
+        """The device error word (0: no wait ran out, every target in range, the
+        workspace this object's alone)."""
         return int(self.workspace[:4].view(torch.int32).item())
 
 

@@ -470,9 +470,13 @@ vsf_status vsf_group_norm_scale_static(const void* const* grads, const int64_t* 
  *     vsf_objective_workspace_bytes (losses) or vsf_route_workspace_bytes
  *     gives, prepared once by vsf_objective_workspace_init and then left to
  *     the library. Calls that share a workspace must be ordered on the
- *     device. Its first 32-bit word is a device error word: bit 1 (value 2)
- *     a bounded wait ran out (results not to be trusted), bit 4 (value 16) a
- *     target was >= V; such a token is left out like a masked one.
+ *     device; a workspace is for losses or for routers, not for both (a
+ *     router needs zeros where a loss keeps its rows). Its first 32-bit word
+ *     is a device error word: bit 1 (value 2) a bounded wait ran out (results
+ *     not to be trusted), bit 4 (value 16) a target was >= V, such a token is
+ *     left out like a masked one; bit 5 (value 32) a router call on a
+ *     workspace that a loss had used: its loss is NaN, its counts are not to
+ *     be trusted, and the workspace has to be prepared again.
  *   - a live token has 0 <= target < V and a weight that is not 0. The logits
  *     of other tokens are not read (they may be NaN); their log probability
  *     is 0 and their gradient row is zeros. -inf logits have probability 0;

@@ -240,3 +240,49 @@ def test_buffers_belong_to_the_objects_stream():
             at = v.untyped_storage().data_ptr()
             home = [s["stream"] for s in segments if s["address"] <= at < s["address"] + s["total_size"]]
             assert home == [side.cuda_stream], (type(op).__name__, tuple(v.shape))
+
+
+def test_router_refuses_a_workspace_that_a_loss_has_used():
+    """The losses leave their rows' sums where the router counts: a router call
+    there says so in the error word and gives a loss of NaN; a fresh one does not,
+    and losses may follow a router."""
+    from fsdp_buffer_layout_gb300 import vsf as V
+    from fsdp_buffer_layout_gb300.objectives import PolicyLoss, PreferenceLoss, Router
+    rng = np.random.default_rng(3)
+    x = dev(rng.normal(size=(64, 32)))
+    lg = dev(rng.normal(size=(64, 700)))
+    long = torch.full((2, 800000), -1.0, device="cuda", dtype=BF16)  # (the policy loss in three passes)
+    y, zero = dev(rng.integers(0, 700, 64), torch.int64), dev(np.zeros(64))
+    starts = dev([0, 32, 64], torch.int64)
+    losses = [lambda: PolicyLoss(64, 700, dtype=FP32), lambda: PreferenceLoss(1, 64, 700, dtype=FP32),
+              lambda: PolicyLoss(2, 800000)]
+
+    def call(op):
+        if op.tokens == 2:
+            return op(long, y[:2], zero[:2], zero[:2])
+        return op(lg, y, starts) if isinstance(op, PreferenceLoss) else op(lg, y, zero, zero)
+
+    for sequences in (1, 80):  # (finished by the last CTA; by a launch of its own)
+        cuts = dev([0] * sequences + [64], torch.int64)
+
+        def route(r):
+            return [t.clone() for t in r.forward(x, seq_starts=cuts)]
+
+        fresh = Router(64, 32, 4, dtype=FP32, balance=0.1, sequences=sequences)
+        want = route(fresh)
+        assert all(torch.equal(a, b) for a, b in zip(route(fresh), want)) and fresh.device_error() == 0
+        for make in losses:
+            loss, router = make(), Router(64, 32, 4, dtype=FP32, balance=0.1, sequences=sequences)
+            size = max(loss._ws_bytes, router._ws_bytes)
+            both = torch.empty(size, dtype=torch.uint8, device="cuda")
+            V.vsf_objective_workspace_init(both.data_ptr(), size, loss._st)
+            for o in (loss, router):
+                o.workspace, o._ws, o._ws_bytes = both, both.data_ptr(), size
+            first = route(router)
+            assert all(torch.equal(a, b) for a, b in zip(first, want)) and router.device_error() == 0
+            got = [t.clone() for t in call(loss) if t is not None]
+            alone = [t.clone() for t in call(make()) if t is not None]
+            assert all(torch.equal(a, b) for a, b in zip(got, alone)) and loss.device_error() == 0
+            assert math.isnan(route(router)[3].item()) and router.device_error() == 32
+            V.vsf_objective_workspace_init(both.data_ptr(), size, loss._st)
+            assert all(torch.equal(a, b) for a, b in zip(route(router), want)) and router.device_error() == 0
