@@ -31,7 +31,7 @@ class Route(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, router):
         idx, gates, _, balance = router.forward(logits)
-        ctx.router = router
+        ctx.router, ctx.call = router, router.calls
         ctx.save_for_backward(logits)
         ctx.mark_non_differentiable(idx, balance)
         return gates, idx, balance
@@ -39,7 +39,7 @@ class Route(torch.autograd.Function):
     @staticmethod
     def backward(ctx, d_gates, _idx, _balance):
         logits, = ctx.saved_tensors
-        return ctx.router.backward(logits, d_gates.contiguous()), None
+        return ctx.router.backward(logits, d_gates.contiguous(), call=ctx.call), None
 
 
 class TinyMoE:

@@ -222,7 +222,11 @@ class Router(_Objective):
     """A mixture-of-experts router. forward returns (idx [T, top_k] int32,
     gates [T, top_k] fp32, counts [E] int32, balance loss fp32 scalar);
     backward the logits' gradient from the gates' gradient (None: none) and
-    loss_scale times the balance loss, for the last forward call."""
+    loss_scale times the balance loss, for the last forward call, whose choices
+    and counts it reads. `calls` counts the forward calls: a program that may
+    make another one in between (a second micro-batch, activations computed
+    again) keeps the number and gives it to backward as `call`, which refuses
+    if it is not the last one's any more."""
 
     SCORES = {"softmax": V.VSF_SCORE_SOFTMAX, "sigmoid": V.VSF_SCORE_SIGMOID}
 
@@ -245,6 +249,7 @@ class Router(_Objective):
         self._out = [t.data_ptr() for t in (self.idx, self.gates, self.counts, self.loss,
                                             self.seq_counts, self.seq_coef)]
         self.grad = None  # made by the first backward
+        self.calls, self._rows_routed = 0, None
 
     def _args(self, logits, live, seq_starts):
         n, ld = self._rows(logits, "logits")
@@ -258,11 +263,17 @@ class Router(_Objective):
         V.vsf_route(logits.data_ptr(), self._vdt, n, self.width, ld,
                     self._vec(bias, self.width, torch.float32, "bias"), lv, starts,
                     self.sequences, self.hp, *self._out, self._ws, self._ws_bytes, self._st)
+        self.calls += 1
+        self._rows_routed = n
         return self._first(self.idx, n), self._first(self.gates, n), self.counts, self.loss
 
     def backward(self, logits, d_gates=None, live=None, seq_starts=None, loss_scale: float = 1.0,
-                 grad=None):
+                 grad=None, call: int | None = None):
         n, ld, lv, starts = self._args(logits, live, seq_starts)
+        if n != self._rows_routed:
+            raise ValueError(f"backward: {n} tokens, the last forward call had {self._rows_routed}")
+        if call is not None and call != self.calls:
+            raise ValueError(f"backward of forward call {call}: call {self.calls} has followed it")
         if grad is None:
             if self.grad is None:
                 self.grad = self._new(self.tokens, self.width, dtype=self.dtype)

@@ -286,3 +286,30 @@ def test_router_refuses_a_workspace_that_a_loss_has_used():
             assert math.isnan(route(router)[3].item()) and router.device_error() == 32
             V.vsf_objective_workspace_init(both.data_ptr(), size, loss._st)
             assert all(torch.equal(a, b) for a, b in zip(route(router), want)) and router.device_error() == 0
+
+
+def test_router_backward_of_another_call():
+    """The gradient is that of the last forward call: without one, for another
+    number of tokens, or for a call that another has followed, it is refused."""
+    from fsdp_buffer_layout_gb300.objectives import Router
+    rng = np.random.default_rng(4)
+    a, b = dev(rng.normal(size=(9, 12))), dev(rng.normal(size=(9, 12)))
+    dg = dev(rng.normal(size=(9, 2)))
+    op = Router(9, 12, 2, dtype=FP32, balance=0.1)
+    with pytest.raises(ValueError):
+        op.backward(a, dg)
+    op.forward(a)
+    first = op.calls
+    want = op.backward(a, dg, call=first).clone()
+    op.forward(b)
+    assert op.calls != first
+    with pytest.raises(ValueError):
+        op.backward(a, dg, call=first)
+    with pytest.raises(ValueError):
+        op.backward(a[:5], dg[:5])
+    op.backward(b, dg, call=op.calls)
+    op.forward(a)  # computed again
+    assert torch.equal(op.backward(a, dg, call=op.calls), want)
+    with pytest.raises(ValueError):
+        op.forward(a.bfloat16())
+    assert torch.equal(op.backward(a, dg, call=op.calls), want)  # a refused call leaves the last one
