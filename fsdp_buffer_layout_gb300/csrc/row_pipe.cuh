@@ -274,6 +274,7 @@ struct PipeArgs {
 };
 
 // Where a row's vectors lie: `head` elements, then nvec vectors, then a tail.
+// (V may be 2^31 - 1: what is added to the tail's start is compared first.)
 struct Span {
   int32_t head, nvec;
 };
@@ -325,7 +326,7 @@ __device__ __noinline__ void zero_share(T* g, int32_t V, uint32_t rank, uint32_t
     __stcs(v + i, make_uint4(0, 0, 0, 0));
   const int32_t tail = s.head + s.nvec * Vec<T>::n;
   if (rank == 0 && tid < s.head) g[tid] = from_f<T>(0.f);
-  if (rank + 1 == 1u << log && tail + tid < V) g[tail + tid] = from_f<T>(0.f);
+  if (rank + 1 == 1u << log && tid < V - tail) g[tail + tid] = from_f<T>(0.f);
 }
 
 // Whether the phase of the given parity is over; does not wait.
@@ -801,8 +802,8 @@ __global__ void __launch_bounds__(PipeShape<W>::threads, 16 / W)
         row.skew = (uint32_t)(reinterpret_cast<uintptr_t>(x) & 15);
         row.loose = -1;
         if (rank == 0 && tid < s.head) row.loose = tid;
-        if (rank + 1 == C && tid >= 16 && s.head + s.nvec * VE + tid - 16 < r.V)
-          row.loose = s.head + s.nvec * VE + tid - 16;
+        const int32_t tail = s.head + s.nvec * VE;
+        if (rank + 1 == C && tid >= 16 && tid - 16 < r.V - tail) row.loose = tail + (tid - 16);
         row.xl = -INFINITY;
         if (row.loose >= 0) row.xl = to_f(x[row.loose]);
 
@@ -923,7 +924,7 @@ __device__ __forceinline__ void grad_piece(const Rows<T>& r, int64_t t, int32_t 
   // the loose element of this thread, if any
   int32_t loose = -1;
   if (piece == 0 && tid < s.head) loose = tid;
-  if (piece + 1 == pieces && tid >= 16 && tail + tid - 16 < r.V) loose = tail + tid - 16;
+  if (piece + 1 == pieces && tid >= 16 && tid - 16 < r.V - tail) loose = tail + (tid - 16);
   uint4* out = reinterpret_cast<uint4*>(g + s.head) + tid;
   if (y < 0 || a == 0.f) {
     for (int32_t v = begin; v + tid < end; v += kGradThreads)

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kRegsThreads, regs_ctas(NV))
     const int32_t tail = s.head + s.nvec * VE;
     int32_t loose = -1;
     if (gtid < s.head) loose = gtid;
-    if (gtid >= 16 && tail + gtid - 16 < r.V) loose = tail + gtid - 16;
+    if (gtid >= 16 && gtid - 16 < r.V - tail) loose = tail + (gtid - 16);
     float xl = -INFINITY;
     if (loose >= 0) xl = to_f(x[loose]);
     float xy = 0.f, old = 0.f, ref = 0.f, adv = 0.f;

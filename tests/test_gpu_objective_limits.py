@@ -313,3 +313,31 @@ def test_router_backward_of_another_call():
     with pytest.raises(ValueError):
         op.forward(a.bfloat16())
     assert torch.equal(op.backward(a, dg, call=op.calls), want)  # a refused call leaves the last one
+
+
+def test_longest_row():
+    """Rows of 2^31 - 1 words, the most: a few likely words at both ends and in
+    between, the others -inf; a masked row."""
+    from fsdp_buffer_layout_gb300.objectives import PolicyLoss, TokenLogprobs
+    vocab, ld = (1 << 31) - 1, 1 << 31
+    buf = torch.full((3 + 2 * ld,), -math.inf, dtype=BF16, device="cuda")
+    x = buf.as_strided((2, vocab), (ld, 1), 3)
+    words = [0, 1, 4, 5, 1 << 20, (1 << 30) + 7, vocab - 9, vocab - 8, vocab - 2, vocab - 1]
+    at = dev(words, torch.int64)
+    z = np.arange(10) * 0.25
+    x[1, at] = dev(z).to(BF16)
+    p = np.exp(z) / np.exp(z).sum()
+    y = dev([-1, vocab - 1], torch.int64)
+    logp = TokenLogprobs(2, vocab)(x, y)
+    assert logp[0].item() == 0 and abs(logp[1].item() - math.log(p[-1])) <= 2.0**-20
+    out = torch.full((3 + 2 * ld,), math.nan, dtype=BF16, device="cuda")
+    g = out.as_strided((2, vocab), (ld, 1), 3)
+    op = PolicyLoss(2, vocab, with_grad=False)
+    op(x, y, logp, dev([1.0, 1.0]), grad=g)
+    assert op.device_error() == 0
+    want = p.copy()
+    want[-1] -= 1.0  # d loss / d x = p - 1[v = y]
+    assert (np.abs(host(g[1, at]) - want) <= 2.0**-8 * np.abs(want)).all()
+    assert torch.count_nonzero(g[0]).item() == 0
+    assert torch.count_nonzero(g[1]).item() == 10  # (NaN would count)
+    assert torch.isnan(out[:3]).all() and torch.isnan(out[3 + vocab:3 + ld]).all() and torch.isnan(out[3 + ld + vocab:]).all()
