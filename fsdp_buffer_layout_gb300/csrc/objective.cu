@@ -372,8 +372,8 @@ vsf_status check_rows(const char* who, const RowsArg& a, void* ws, size_t ws_byt
   if (a.T_ < 0 || a.T_ > INT32_MAX || a.V < 1 || a.V > INT32_MAX || a.ld < a.V ||
       a.ld > (int64_t(1) << 40))
     return fail(VSF_ERR_ARG, w + ": sizes out of range");
-  if (!(a.inv_t > 0.f) || !std::isfinite(a.inv_t))
-    return fail(VSF_ERR_ARG, w + ": inv_temperature must be positive and finite");
+  if (!(a.inv_t > 0.f && a.inv_t <= kMaxInvTemperature))
+    return fail(VSF_ERR_ARG, w + ": inv_temperature must be positive and at most 2^127");
   if (ws == nullptr || (a.T_ > 0 && (a.logits == nullptr || a.target == nullptr)))
     return fail(VSF_ERR_ARG, w + ": NULL pointer");
   if (ws_bytes < ObjectiveWs::bytes(a.T_, pairs))

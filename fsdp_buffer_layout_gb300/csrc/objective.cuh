@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <limits>
 #include <string>
 #include <utility>
 
@@ -54,20 +55,23 @@ __device__ __forceinline__ float ex2(float t) {
 // The factor c = log2(e) / temperature. One float's rounding error would act
 // like a slightly different temperature, the same way for every token, and add
 // up over a sequence's log ratios. So either as a sum of two floats, hi + lo
-// (both positive: -inf times either is -inf), or, where one product an element
-// has to do, rounded down (hi) in some threads and up in the others, in such a
-// share (ups / 2^32) that the mean is c.
+// (both positive, however small c is: -inf times either is -inf), or, where one
+// product an element has to do, rounded down (hi) in some threads and up in the
+// others, in such a share (ups / 2^32) that the mean is c. c has to fit fp32: 0
+// times an infinite factor would be NaN.
 struct Log2Scale {
   float hi, lo, up;
   uint32_t ups;
 };
+constexpr float kMaxInvTemperature = 1.7014118e38f;  // 2^127
 inline Log2Scale log2_scale(float inv_t) {
   const double c = (double)inv_t * 1.4426950408889634074;
   float hi = (float)c;
   if ((double)hi >= c) hi = std::nextafter(hi, 0.f);
   const float up = std::nextafter(hi, INFINITY);
   const double part = (c - (double)hi) / ((double)up - (double)hi);
-  return {hi, (float)(c - (double)hi), up, (uint32_t)std::min(part * 4294967296.0, 4294967295.0)};
+  const float lo = std::max((float)(c - (double)hi), std::numeric_limits<float>::denorm_min());
+  return {hi, lo, up, (uint32_t)std::min(part * 4294967296.0, 4294967295.0)};
 }
 
 // exp(d / temperature) for d = x - max <= 0.

@@ -481,7 +481,8 @@ vsf_status vsf_group_norm_scale_static(const void* const* grads, const int64_t* 
  *     of other tokens are not read (they may be NaN); their log probability
  *     is 0 and their gradient row is zeros. -inf logits have probability 0;
  *     a live row with a NaN, a +inf or only -inf gives NaN.
- *   - probabilities are softmax(inv_temperature * logits).
+ *   - probabilities are softmax(inv_temperature * logits), with
+ *     0 < inv_temperature <= 2^127.
  *   Errors: VSF_ERR_ARG (NULL, sizes or hyper-parameters out of range, a
  *   workspace too small), VSF_ERR_ALIGN, VSF_ERR_CUDA; all but the last are
  *   found before the first launch. */
@@ -511,7 +512,7 @@ vsf_status vsf_token_logprobs(const void* logits, int32_t dtype, int64_t T, int6
 typedef struct {
   float clip_low, clip_high; /* >= 0; clip_low <= 1 */
   float kl_beta;
-  float inv_temperature;     /* > 0 */
+  float inv_temperature;     /* in (0, 2^127] */
   float scale;
   int32_t mean;
 } vsf_policy_hparams;

@@ -341,3 +341,29 @@ def test_longest_row():
     assert torch.count_nonzero(g[0]).item() == 0
     assert torch.count_nonzero(g[1]).item() == 10  # (NaN would count)
     assert torch.isnan(out[:3]).all() and torch.isnan(out[3 + vocab:3 + ld]).all() and torch.isnan(out[3 + ld + vocab:]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("vocab", [700, 33000, 800000])
+@pytest.mark.parametrize("inv_t", [2.0**127, 1e30, 1e-30, 2.0**-126, 3e-39, 2e-45])
+def test_temperatures_at_the_ends_of_their_range(dtype, vocab, inv_t):
+    """Near temperature 0 the probability lies on the largest logits, at a very
+    large one on all but the -inf words alike."""
+    from fsdp_buffer_layout_gb300.objectives import TokenLogprobs
+    rng = np.random.default_rng(vocab)
+    x = torch.from_numpy(rng.integers(-9, 3, (4, vocab)).astype(np.float32)).to("cuda", dtype)
+    x[:, 1::2] = -math.inf
+    x[:, 0::64] = 4.0
+    y = np.full(4, 64)
+    lp = TokenLogprobs(4, vocab, dtype=dtype, inv_temperature=inv_t)(x, dev(y, torch.int64))
+    want = R.logprobs(host(x), y, float(np.float32(inv_t)))
+    assert (np.abs(host(lp) - want) <= logp_error(vocab, want)).all()
+    # (a gradient of 2^-30 / temperature, so that it fits; far below fp32 it is 0)
+    from fsdp_buffer_layout_gb300.objectives import PolicyLoss
+    op = PolicyLoss(4, vocab, dtype=dtype, inv_temperature=inv_t, scale=2.0**-30 if inv_t > 1 else 1.0, mean=False)
+    g = op(x, dev(y, torch.int64), lp.clone(), dev(np.ones(4)))[2]
+    assert torch.isfinite(g).all() and not g[:, 1::2].any()
+    if inv_t >= 1e-30:
+        t64 = float(np.float32(inv_t))
+        scale = 2.0**-30 if inv_t > 1 else 1.0
+        check_gradient(g, host(x), y, [-scale] * 4, [2.0**-19 + tol(vocab)] * 4, t64, dtype)
