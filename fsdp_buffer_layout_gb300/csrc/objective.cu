@@ -163,7 +163,8 @@ struct PolicyTerm {
 __device__ __forceinline__ PolicyTerm policy_term(const PolicyIn& p, float ahead, float u, float a) {
   PolicyTerm o;
   const float ratio = expf(ahead);
-  const float freed = ratio * a;
+  // (past fp32 above 88: 0 times a ratio that is finite in truth is 0)
+  const float freed = a == 0.f && ahead < INFINITY ? 0.f : ratio * a;
   const float held = fminf(fmaxf(ratio, p.lo), p.hi) * a;
   const bool clipped = freed > held;  // a NaN ratio is not clipped away
   o.policy = -(clipped ? held : freed);

@@ -367,3 +367,19 @@ def test_temperatures_at_the_ends_of_their_range(dtype, vocab, inv_t):
         t64 = float(np.float32(inv_t))
         scale = 2.0**-30 if inv_t > 1 else 1.0
         check_gradient(g, host(x), y, [-scale] * 4, [2.0**-19 + tol(vocab)] * 4, t64, dtype)
+
+
+@pytest.mark.parametrize("vocab", [700, 33000, 800000])
+def test_advantage_zero_where_the_ratio_overflows(vocab):
+    """r A is 0 for A = 0 however far the policy has moved (exp(logp - old) is
+    past fp32 above 88); an advantage above 0 is clipped there."""
+    from fsdp_buffer_layout_gb300.objectives import PolicyLoss
+    rng = np.random.default_rng(vocab)
+    x = torch.from_numpy(rng.normal(size=(3, vocab)).astype(np.float32)).to("cuda", BF16)
+    y = rng.integers(0, vocab, 3)
+    old = np.array([-200, -5, -120], np.float32)
+    adv = np.array([0, 0.5, 2], np.float32)
+    stats, lp, grad = PolicyLoss(3, vocab, mean=False)(x, dev(y, torch.int64), dev(old), dev(adv))
+    s, l, g, _ = R.policy(host(x), y, old, adv, old, None, 0.2, 0.2, 0.0, 1.0, 1.0, False)
+    assert (np.abs(host(stats) - s) <= 1e-4 * np.abs(s)).all()
+    assert not grad[0].any() and not grad[2].any() and torch.isfinite(grad).all()
