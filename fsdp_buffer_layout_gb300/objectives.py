@@ -35,9 +35,10 @@ class _Objective:
         self.tokens, self.width, self.dtype = int(tokens), int(width), dtype
         self._vdt = _DTYPES[dtype]
         device = torch.device("cuda" if device is None else device)
-        self.device = device if device.index is not None \
-            else torch.device(device.type, torch.cuda.current_device())
-        self._index = self.device.index
+        self._index = torch.cuda.current_device()
+        if device.type != "cuda" or device.index not in (None, self._index):
+            raise ValueError(f"device: the current one (cuda:{self._index}), not {device}")
+        self.device = torch.device("cuda", self._index)
         self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
         self._st = self.stream.cuda_stream
 

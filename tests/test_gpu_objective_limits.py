@@ -383,3 +383,15 @@ def test_advantage_zero_where_the_ratio_overflows(vocab):
     s, l, g, _ = R.policy(host(x), y, old, adv, old, None, 0.2, 0.2, 0.0, 1.0, 1.0, False)
     assert (np.abs(host(stats) - s) <= 1e-4 * np.abs(s)).all()
     assert not grad[0].any() and not grad[2].any() and torch.isfinite(grad).all()
+
+
+@pytest.mark.parametrize("device", ["cpu", "cuda:1", torch.device("meta")])
+def test_objects_are_made_on_the_current_device(device):
+    """Their calls launch on it; another one is refused when the object is made,
+    not at its first call."""
+    from fsdp_buffer_layout_gb300.objectives import PolicyLoss, PreferenceLoss, Router, TokenLogprobs
+    for make in (lambda d: TokenLogprobs(4, 64, device=d), lambda d: PolicyLoss(4, 64, device=d),
+                 lambda d: PreferenceLoss(1, 4, 64, device=d), lambda d: Router(4, 8, 2, device=d)):
+        with pytest.raises(ValueError):
+            make(device)
+        assert make("cuda").device == make(torch.device("cuda", 0)).device == torch.device("cuda", 0)
