@@ -395,3 +395,185 @@ def test_objects_are_made_on_the_current_device(device):
         with pytest.raises(ValueError):
             make(device)
         assert make("cuda").device == make(torch.device("cuda", 0)).device == torch.device("cuda", 0)
+
+
+def likely(rng, tokens, vocab, dtype, pad=0, shift=0):
+    """Rows whose ends hold likely words, so that a word left out shows."""
+    ld = vocab + pad
+    buf = torch.empty(shift + tokens * ld + 16, dtype=dtype, device="cuda")
+    buf.copy_(torch.from_numpy((2.5 * rng.normal(size=buf.numel())).astype(np.float32)))
+    x = buf.as_strided((tokens, vocab), (ld, 1), shift)
+    ends = sorted({v % vocab for v in (*range(9), *range(-9, 0), vocab // 2, vocab // 3)})
+    x[:, ends] += 6.0
+    return x
+
+
+STRICT = [  # tokens, vocab, dtype, logits' pad and shift, gradient's pad and shift
+    (3, 2, FP32, 0, 0, 3, 1), (5, 31, BF16, 2, 1, 2, 1), (9, 257, BF16, 0, 0, 3, 5),
+    (6, 1003, FP32, 1, 1, 1, 1), (9, 2048, BF16, 0, 0, 8, 0), (7, 4099, BF16, 0, 3, 5, 2),
+    (5, 9001, FP32, 0, 0, 0, 0), (6, 16384, BF16, 8, 0, 0, 0), (5, 16391, BF16, 1, 7, 1, 7),
+    (170, 20000, BF16, 0, 0, 8, 0), (5, 50021, FP32, 3, 2, 3, 2), (5, 65537, BF16, 0, 0, 7, 0),
+    (4, 131075, FP32, 5, 2, 5, 2), (5, 300001, BF16, 0, 1, 0, 1),
+    # one row's share in the ring: few rows; more rows than clusters; odd places
+    (5, 500000, BF16, 0, 0, 8, 0), (45, 400003, BF16, 5, 3, 5, 3), (5, 200000, FP32, 0, 0, 4, 0),
+    (41, 201089, FP32, 0, 0, 1, 1),
+    # gradient as a pass of its own
+    (5, 800000, BF16, 0, 0, 8, 0), (5, 790003, BF16, 1, 3, 2, 5), (4, 400009, FP32, 3, 1, 3, 1),
+]
+
+
+@pytest.mark.parametrize("tokens,vocab,dtype,pad,shift,gpad,gshift", STRICT)
+@pytest.mark.parametrize("beta,mean", [(0.1, True), (0.0, False)])
+def test_every_element_of_the_policy_gradient(tokens, vocab, dtype, pad, shift, gpad, gshift, beta, mean):
+    rng = np.random.default_rng(vocab)
+    x = likely(rng, tokens, vocab, dtype, pad, shift)
+    y = rng.integers(0, vocab, tokens)
+    w = rng.uniform(0.5, 1.5, tokens).astype(np.float32)
+    y[0], y[1] = 0, vocab - 1
+    if tokens > 3:
+        y[2], w[3] = -1, 0.0
+        x[2:4] = math.nan
+    check_policy(x, y, w, beta, mean, 1.0 if mean else 1.25, gpad, gshift, seed=vocab)
+    check_policy(x, y, w, beta, mean, 1.0, in_place=True, seed=vocab)
+
+
+@pytest.mark.parametrize("tokens", [2049, 8192, 8193, 70000])
+@pytest.mark.parametrize("mean", [True, False])
+def test_policy_loss_of_many_short_rows(tokens, mean):
+    """The sum of the weights by one CTA, by several (the last adds up), by the
+    most there are."""
+    rng = np.random.default_rng(tokens)
+    x = likely(rng, tokens, 40, BF16)
+    y = rng.integers(0, 40, tokens)
+    w = rng.uniform(0.5, 1.5, tokens).astype(np.float32)
+    y[rng.random(tokens) < 0.2], w[rng.random(tokens) < 0.2] = -1, 0.0
+    from fsdp_buffer_layout_gb300.objectives import PolicyLoss
+    lp = R.logprobs(host(x), y, 1.0, w)
+    old, ref, adv = policy_inputs(rng, lp, 0.1)
+    s, _, g, slope = R.policy(host(x), y, old, adv, ref, w, 0.2, 0.25, 0.1, 1.0, 0.5, mean)
+    err = policy_slope_error(lp, old, adv, ref, w, 0.1, 0.5 / (s[3] if mean else 1), slope, 40)
+    op = PolicyLoss(tokens, 40, clip_low=0.2, clip_high=0.25, kl_beta=0.1, scale=0.5, mean=mean)
+    args = (x, dev(y, torch.int64), dev(old), dev(adv), dev(ref), dev(w))
+    for _ in range(2):
+        stats, _, grad = op(*args)
+        lim = policy_stats_error(w * (y >= 0), adv, 0.5 / (s[3] if mean else 1), slope, err)
+        assert (np.abs(host(stats) - s) <= lim + 2.0**-20 * np.abs(s)).all()
+        a = np.array([v or 0.0 for v in slope])
+        p = np.exp(R.log_softmax(host(x)))
+        one = np.arange(40) == y[:, None]
+        lim = np.abs(a[:, None]) * ((np.array(err)[:, None] + 2 * tol(40) + 2.0**-14 + 2.0**-8) * np.where(one, 1 - p, p)
+                                    + one * (np.array(err)[:, None] + 2.0**-14 * p)) + 1e-30
+        assert (np.abs(host(grad) - g) <= lim).all()
+
+
+@pytest.mark.parametrize("keep", [400, 0])
+def test_many_more_long_rows_than_a_list_holds(keep):
+    """157,000 rows of 16,400 words, nearly all of them masked (NaN): clusters
+    take rows as they come."""
+    from fsdp_buffer_layout_gb300.objectives import PolicyLoss, TokenLogprobs
+    tokens, vocab = 157000, 16400
+    rng = np.random.default_rng(6)
+    at = np.sort(rng.choice(tokens, keep, replace=False)) if keep else np.arange(0)
+    x = torch.full((tokens, vocab), math.nan, dtype=BF16, device="cuda")
+    rows = dev(at, torch.int64)
+    part = likely(rng, max(keep, 1), vocab, BF16)[:keep]
+    x[rows] = part
+    y, old, adv = np.full(tokens, -1), np.zeros(tokens, np.float32), np.zeros(tokens, np.float32)
+    yk = rng.integers(0, vocab, keep)
+    y[at] = yk
+    lp = R.logprobs(host(part), yk)
+    ok, _, ak = policy_inputs(rng, lp, 0.0)
+    old[at], adv[at] = ok, ak
+    yt = dev(y, torch.int64)
+    got = TokenLogprobs(tokens, vocab)(x, yt)
+    assert (np.abs(host(got[rows]) - lp) <= logp_error(vocab, lp)).all()
+    assert torch.count_nonzero(got).item() == np.count_nonzero(lp)
+    op = PolicyLoss(tokens, vocab, clip_low=0.2, clip_high=0.25)
+    stats, logp, grad = op(x, yt, dev(old), dev(adv))
+    if not keep:
+        assert not stats.any() and not logp.any() and torch.count_nonzero(grad).item() == 0
+        return
+    s, _, _, slope = R.policy(host(part), yk, ok, ak, ok, None, 0.2, 0.25, 0.0, 1.0, 1.0, True)
+    err = policy_slope_error(lp, ok, ak, ok, np.ones(keep), 0.0, 1 / keep, slope, vocab)
+    lim = policy_stats_error(1.0, ak, 1 / keep, slope, err) + 2.0**-20 * abs(s[0])
+    assert abs(stats[0].item() - s[0]) <= lim
+    assert stats[3].item() == keep
+    check_gradient(grad[rows], host(part), yk, slope, err, 1.0, BF16)
+    grad[rows] = 0
+    assert torch.count_nonzero(grad).item() == 0
+    assert op.device_error() == 0
+
+
+@pytest.mark.parametrize("vocab,dtype,pad,lengths", [
+    (90, BF16, 0, (4100, 3999)), (301, FP32, 1, (1030, 0, 5, 2500)), (16500, BF16, 3, (30, 41, 0, 77)),
+    (70001, FP32, 0, (3, 4)), (200000, BF16, 8, (2, 1)),
+])
+def test_every_element_of_the_preference_gradient(vocab, dtype, pad, lengths):
+    """Sequences of some thousand tokens among them."""
+    from fsdp_buffer_layout_gb300.objectives import PreferenceLoss
+    rng = np.random.default_rng(vocab)
+    starts = np.cumsum([0] + list(lengths)) + 2
+    n = int(starts[-1]) + 3
+    x = likely(rng, n, vocab, dtype, pad)
+    y = rng.integers(0, vocab, n)
+    y[5::7] = -1
+    live = y >= 0
+    lp = R.logprobs(host(x), y)
+    ref = (lp + rng.normal(size=n) * 0.2 / math.sqrt(n)).astype(np.float32)
+    out = R.preference(host(x), y, starts, ref, None, "sigmoid", 0.3, 0.1, 0.2, False, 1.0, 0.5)
+    buf, g = nan_rows(n, vocab, dtype, 5)
+    op = PreferenceLoss(len(lengths) // 2, n, vocab, dtype=dtype, beta=0.3, smoothing=0.1, margin=0.2, scale=0.5)
+    stats, rewards, logp, grad = op(x, dev(y, torch.int64), dev(starts, torch.int64), ref_logp=dev(ref), grad=g)
+    assert (np.abs(host(logp) - lp) <= logp_error(vocab, lp)).all()
+    # a pair's sum: each token's ln p, and fp32 additions of small differences
+    each = np.array([live[a:b].sum() for a, b in zip(starts, starts[1:])]) * (tol(vocab) + 2.0**-20)
+    assert (np.abs(host(rewards) - out[1]) <= 0.3 * each + 2.0**-22 * np.abs(out[1])).all()
+    dh = each[:len(each) // 2] + each[len(each) // 2:]
+    assert (np.abs(host(stats) - out[0]) <= 0.3 * dh.max() + 2.0**-20 * np.abs(out[0])).all()
+    slope = out[4]
+    # d loss / d h moves by at most beta^2 / 4 d h
+    err = [0.0] * n
+    for s in range(len(lengths)):
+        for t in range(starts[s], starts[s + 1]):
+            if slope[t]:
+                err[t] = 2.0**-20 + 0.5 / (len(lengths) // 2) * 0.09 / 4 * dh[s % len(dh)] / abs(slope[t])
+    check_gradient(grad, host(x), y, slope, err, 1.0, dtype)
+    outside = torch.ones_like(buf, dtype=torch.bool)
+    outside.as_strided((n, vocab), g.stride(), 0)[:] = False
+    assert bool(torch.isnan(buf[outside]).all()) and op.device_error() == 0
+
+
+def route_gate_error(x, idx, score, renorm, experts):
+    """Relative error of each gate. A softmax term 2^t, t = (x - m) log2(e), is
+    within 2^-22 (ex2.approx) plus 3 |t| 2^-24 ln 2 (difference, constant and
+    product) of its value, a sigmoid within e / (1 + e) of the same for e =
+    exp(-x), plus 2^-23 each for its sum and its reciprocal (rcp.approx). Sums
+    have at most 21 additions (16 in a lane, 5 by shuffles); one division."""
+    t = (x - x.max(1, keepdims=True) if score == "softmax" else -x) / LN2
+    term = 2.0**-22 + 3 * np.abs(t) * 2.0**-24 * LN2
+    if score == "sigmoid":
+        e = np.exp(np.minimum(-x, 700))
+        term = term * (e / (1 + e)) + 2.0**-22
+    own = np.take_along_axis(term, idx, 1)
+    if renorm:
+        return own + own.max(1, keepdims=True) + 21 * 2.0**-24 + 2.0**-21
+    if score == "sigmoid":
+        return own + 2.0**-23
+    # the sum's error is its terms', weighted: |t| is at most log2 E there
+    return own + 2.0**-22 + 3 * math.log2(2 * experts) * 2.0**-24 + 21 * 2.0**-24 + 2.0**-22
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+@pytest.mark.parametrize("experts,k", [(8, 2), (64, 8), (100, 6), (256, 8), (512, 32)])
+@pytest.mark.parametrize("offset,spread", [(0.0, 12.0), (1e4, 8.0), (-60.0, 4.0)])
+def test_gates_of_spread_and_shifted_logits(experts, k, dtype, score, renorm, offset, spread):
+    """Logits of a wide spread, and all of them far from 0."""
+    from fsdp_buffer_layout_gb300.objectives import Router
+    rng = np.random.default_rng(experts + k)
+    x = dev((offset + spread * rng.normal(size=(200, experts))), dtype)
+    idx, gates, _, _ = Router(200, experts, k, dtype=dtype, score=score, renorm=renorm).forward(x)
+    i, g, *_ = R.route(host(x), k, score, renorm, 1.0, 0.0)
+    assert np.array_equal(idx.cpu().numpy(), i)
+    lim = route_gate_error(host(x), i, score, renorm, experts) * np.abs(g) + 2.0**-125
+    assert (np.abs(host(gates) - g) <= lim).all(), (np.abs(host(gates) - g) / lim).max()
