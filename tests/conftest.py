@@ -27,6 +27,15 @@ def pytest_collection_modifyitems(config, items):
             item.add_marker(skip)
 
 
+@pytest.fixture(scope="session", autouse=True)
+def _library():
+    """libvsf.so as the sources are, so that every test file runs by itself on a
+    clean tree (not under VSF_LIBRARY, which names another build)."""
+    if not os.environ.get("VSF_LIBRARY"):
+        from fsdp_buffer_layout_gb300 import _build
+        _build.build()
+
+
 @pytest.fixture(autouse=True)
 def _bounds_checked_on_close(monkeypatch):
     """Under the bounds-checking build (VSF_LIBRARY set), every ShardStep

@@ -21,3 +21,13 @@ def test_inverse_temperature_out_of_range(bad):
         with pytest.raises(V.VsfError) as e:
             call(**args)
         assert e.value.status == V.VSF_ERR_ARG and "2^127" in str(e.value)
+
+
+def test_structs_match_the_header(tmp_path, monkeypatch):
+    """The hyper-parameters' ctypes structures against the C header."""
+    import test_abi_layout as L
+    monkeypatch.setattr(L, "STRUCTS", [V.vsf_policy_hparams, V.vsf_preference_hparams,
+                                       V.vsf_route_hparams])
+    if L.shutil.which("gcc") is None:
+        pytest.skip("needs gcc")
+    L.test_ctypes_structs_match_the_header(tmp_path)
