@@ -461,8 +461,18 @@ int pipe_clusters(int C, cudaError_t* e) {
 
 // CTAs that share a row (0: none that holds it), and whether two rows' shares
 // fit the ring. `hold`: a share stays in the ring until its gradient is
-// written. With few rows, more CTAs a row as long as they all run at a time and
-// each has 256 vectors to read.
+// written. With few rows, more CTAs a row as long as their number fits the SMs
+// (rows beyond the short ones give each of 8 at least 256 vectors). In us, policy
+// loss with gradient and log probabilities, calls of a graph, with 1, 2, 4 and 8
+// CTAs a row; * is taken:
+//   8 x 32000 bf16     9.4, 9.1, 9.2, 9.2*     5.3, 5.3, 5.1, 5.2*
+//   48 x 32000 bf16    9.5, 9.4*, 11.2, 13.6   5.3, 5.6*, 6.9, 8.6
+//   100 x 32000 bf16   9.8*, 11.9, 13.5, 18.8  5.4*, 7.1, 8.4, 11.8
+//   19 x 131072 bf16   10.1, 10.1, 10.2, 11.5* 8.6, 6.9, 6.0, 7.0*
+//   19 x 50021 fp32    9.5, 9.6, 9.6, 11.3*    6.9, 6.1, 5.7, 6.8*
+// More clusters than run at a time cost a second turn: 76 of 2, 36 of 4 and 15 of
+// 8 CTAs were found to fit (a cluster keeps to one GPC), so for 16 to 19 rows and
+// for 37 and 38 the rule takes one doubling too many, for about 1.5 us.
 struct PipeSplit {
   int C;
   bool ahead;
@@ -478,7 +488,7 @@ PipeSplit pipe_split(int64_t T_, int64_t V, bool hold) {
     if (s.C > 8) s = {chunks(8) <= Shape::slots ? 8 : 0, false};
     if (s.C == 0) return s;
   }
-  while (s.C < 8 && T_ * s.C * 2 <= 152 * (16 / kPipeWarps) && nvec / (2 * s.C) >= 256) s.C *= 2;
+  while (s.C < 8 && T_ * s.C * 2 <= kSms * (16 / kPipeWarps)) s.C *= 2;
   return s;
 }
 
@@ -502,14 +512,20 @@ bool short_rows(int64_t V) {
   return V / Vec<T>::n <= 8 * kRegsThreads;
 }
 
+// Up to this many tokens every CTA adds up the weights for itself; beyond, a
+// launch of its own does it once. In us, own sums against the launch, 1000 words:
+// 1024 tokens 9.4 and 9.9, 2048 13.4 and 11.9, 4096 19.1 and 16.0, 8192 24.6 and
+// 21.1; 16000 words: 1024 tokens 24.0 and 22.8, 4096 59.5 and 58.6.
+constexpr int64_t kSumTokens = 2048;
+
 template <typename T, bool POLICY, int G, int NV>
 cudaError_t launch_regs_as(const PipeArgs<T>& a, const ObjectiveWs& w, cudaStream_t st) {
-  const int64_t rows = 8 / G, most = 152 * regs_ctas(NV);
+  const int64_t rows = 8 / G, most = kSms * regs_ctas(NV);
   const unsigned grid =
       (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, (a.r.T_ + rows - 1) / rows));
-  static_assert(152 * 4 <= kMaxPipeClusters, "the workspace holds a sum of every CTA");
+  static_assert(kSms * 4 <= kMaxPipeClusters, "the workspace holds a sum of every CTA");
   const double* total = nullptr;
-  if (POLICY && a.p.mean && a.r.T_ > 2048) {
+  if (POLICY && a.p.mean && a.r.T_ > kSumTokens) {
     total = w.total;
     const unsigned n = (unsigned)std::min<int64_t>(64, (a.r.T_ + 8 * kSumThreads - 1) / (8 * kSumThreads));
     const cudaError_t e = launch_behind(weight_sum_kernel, n, kSumThreads, 0, 1, st, a.r.target, a.r.weight,
@@ -548,7 +564,7 @@ cudaError_t launch_grad(const Rows<T>& r, const ObjectiveWs& w, void* grad, int6
   if (r.T_ == 0 || grad == nullptr) return cudaSuccess;
   const int32_t pieces =
       (int32_t)std::max<int64_t>(1, (r.V / Vec<T>::n + kGradPiece - 1) / kGradPiece);
-  return launch_behind(row_grad_kernel<T>, (unsigned)std::min<int64_t>(r.T_ * pieces, 152 * kGradCtas),
+  return launch_behind(row_grad_kernel<T>, (unsigned)std::min<int64_t>(r.T_ * pieces, kSms * kGradCtas),
                        kGradThreads, 0, 1, st, r, (const float4*)w.row, (const float*)w.coef,
                        static_cast<T*>(grad), grad_ld, pieces);
 }

@@ -756,7 +756,7 @@ template <int L, int N>
 unsigned route_grid(int64_t T_) {
   const int64_t least = std::max(16, kRouteThreads / L);
   return (unsigned)std::max<int64_t>(
-      1, std::min<int64_t>((T_ + least - 1) / least, 152 * route_ctas(N)));
+      1, std::min<int64_t>((T_ + least - 1) / least, kSms * route_ctas(N)));
 }
 
 // Up to here the last CTA of the router finishes; beyond, a launch of its own:

@@ -205,7 +205,7 @@ constexpr uint32_t kQueue = 8;  // rows handed on and not yet added up
 constexpr int kList = 2048;     // rows of a cluster that its list holds
 
 // W consumer warps, each thread `per` vectors of a chunk; the rings of an SM's
-// CTAs have 208 KB together. W = 16 (one CTA an SM) measured best: 8192 x 131072
+// CTAs have 192 KB together, six chunks each. W = 16 (one CTA an SM) measured best: 8192 x 131072
 // bf16, policy loss: 691 us, against 754 for W = 8 (two CTAs, each with half the
 // ring, so rows in twice as many pieces); 4096 x 32000, 3/4 live: 81 against 85.
 // Before rows were listed in advance 4 vectors took 888 us, 2 took 1014 (a

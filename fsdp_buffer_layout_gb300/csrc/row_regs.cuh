@@ -14,8 +14,9 @@ constexpr int kRegsThreads = 256;
 constexpr int regs_ctas(int nv) { return nv <= 4 ? 4 : 3; }  // an SM
 
 // Sum of the live weights, for many tokens: up to 64 CTAs, the last of which adds
-// up their sums in their order. The kernel behind it may start with its rows
-// meanwhile: it is let go only after the kernels before this one have ended.
+// up their sums in their order. The kernel behind it is set up and fetches its
+// first tokens meanwhile (it is let go only after the kernels before this one
+// have ended) and waits for the sum before its first row.
 constexpr int kSumThreads = 1024;
 __global__ void __launch_bounds__(kSumThreads)
     weight_sum_kernel(const int64_t* target, const float* weight, int64_t T_, int32_t V,

@@ -463,7 +463,8 @@ vsf_status vsf_group_norm_scale_static(const void* const* grads, const int64_t* 
  *     row t starting at element t*ld (ld >= V). Pointers need the alignment
  *     of their element type only, the workspace 16 bytes (VSF_ERR_ALIGN);
  *     rows that start on a 16-byte boundary are read with wide copies. T may
- *     be 0 (scalars are still written); T, V < 2^31; offsets are 64-bit.
+ *     be 0 (scalars are still written); T, V < 2^31 (routers: below); offsets
+ *     are 64-bit.
  *   - sums, maxima and per-token values are fp32 or wider; results do not
  *     depend on scheduling: equal inputs give equal bits.
  *   - d_workspace: caller memory of at least the size that
@@ -572,7 +573,8 @@ vsf_status vsf_preference_loss(const void* logits, int32_t dtype, int64_t T, int
  * Outputs: idx int32[T*top_k], gates fp32[T*top_k], counts int32[E] (over all
  * sequences), loss fp32[1]; seq_counts int32[sequences*E] (n_se) and seq_coef
  * fp32[sequences], which vsf_route_grad reads.
- * 1 <= E <= 512, 1 <= top_k <= min(E, 32), 1 <= sequences <= 2^20. */
+ * T <= 2^23, 1 <= E <= 512, 1 <= top_k <= min(E, 32), 1 <= sequences <=
+ * 2^20 (as for vsf_route_grad). */
 enum { VSF_SCORE_SOFTMAX = 0, VSF_SCORE_SIGMOID = 1 };
 typedef struct {
   int32_t top_k, score, renorm;
