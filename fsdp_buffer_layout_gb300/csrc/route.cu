@@ -25,6 +25,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstddef>
 
 #include "objective.cuh"
 
@@ -401,9 +402,10 @@ __device__ float route_finish(const RouteIn& p, const RouteSums& w, const RouteO
 // The call's end, by one thread: the loss, and the head as the next call wants
 // it. Where a loss has used the workspace, its rows lay among the sums.
 __device__ __forceinline__ void route_close(WsHead* head, float* loss, float l) {
-  const bool shared = __ldcg(&head->rows) != 0u;
-  if (shared) atomicOr(&head->err, kErrShared);
-  *loss = shared || __ldcg(&head->nan) ? NAN : l;
+  static_assert(offsetof(WsHead, nan) == 8 && offsetof(WsHead, rows) == 12, "nan, rows: one load");
+  const uint2 seen = __ldcg(reinterpret_cast<const uint2*>(&head->nan));
+  if (seen.y) atomicOr(&head->err, kErrShared);
+  *loss = seen.x | seen.y ? NAN : l;
   head->nan = 0u;
   head->ticket = 0u;
 }
