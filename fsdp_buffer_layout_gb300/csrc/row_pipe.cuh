@@ -28,7 +28,7 @@
 // Bounds and measurements (GB300, a call among others). Sums alone read at the
 // rate of a plain copy: 4096 x 131072 bf16, 3/4 live, 118 us = 6.8 TB/s. The
 // policy loss is bound by HBM where a CTA's share is long (8192 x 131072 bf16:
-// 691 us, 6.2 TB/s read and written; clusters of 4 leave 8 of the 152 SMs idle)
+// 694 us, 6.2 TB/s read and written; clusters of 4 leave 8 of the 152 SMs idle)
 // and by a row's fixed cost, about 1.8 us of the consumers' time however short
 // the row, where it is not (4096 x 32000 bf16, 3/4 live: 80 us, 5.7 TB/s).
 // A call costs some 10 us from its first load to its last sum.
@@ -206,7 +206,7 @@ constexpr int kList = 2048;     // rows of a cluster that its list holds
 
 // W consumer warps, each thread `per` vectors of a chunk; the rings of an SM's
 // CTAs have 192 KB together, six chunks each. W = 16 (one CTA an SM) measured best: 8192 x 131072
-// bf16, policy loss: 691 us, against 754 for W = 8 (two CTAs, each with half the
+// bf16, policy loss: 694 us, against 754 for W = 8 (two CTAs, each with half the
 // ring, so rows in twice as many pieces); 4096 x 32000, 3/4 live: 81 against 85.
 // Before rows were listed in advance 4 vectors took 888 us, 2 took 1014 (a
 // chunk's fixed cost shows) and 6 took 1006 (too few chunks).
