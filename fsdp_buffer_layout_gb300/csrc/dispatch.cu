@@ -1,0 +1,609 @@
+// dispatch.cu — tokens by expert: the router's choices sorted by expert, rows
+// copied into that order, the experts' outputs combined with their gates, and
+// the gradients of both.
+//
+// Choice c = t top_k + j of token t is the j-th expert it takes. The sort is a
+// stable counting sort: place[c], the row of choice c, counts the choices of
+// lower experts and the earlier ones of its own. With it
+//   gather            rows[place[t, j]] = x[t]
+//   its gradient      dx[t] = sum_j d_rows[place[t, j]]           (combine, gates 1)
+//   combine           out[t] = sum_j g[t, j] y[place[t, j]]
+//   its gradient      dy[place[t, j]] = g[t, j] d_out[t]
+//                     dg[t, j] = sum_h d_out[t, h] y[place[t, j], h]
+// All four go by token, so a token's row is read (or written) once, and sums
+// over j keep their order: equal inputs give equal bits, without an atomic.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <initializer_list>
+#include <string>
+
+#include "objective.cuh"
+
+namespace vsf {
+namespace {
+
+using namespace obj;
+
+constexpr int64_t kMaxTokens = int64_t(1) << 23;
+constexpr int kMaxChoices = 32;   // of a token
+constexpr int kMaxSorted = 512;   // experts
+constexpr int64_t kMaxWidth = int64_t(1) << 24;
+
+// ------------------------------------------------------------------ the sort
+// Each CTA takes a run of consecutive choices, each of its warps a part of the
+// run. The first launch counts the runs' choices by expert, the second adds up
+// the counts of the runs before its own (every CTA for itself: at most 256 runs
+// of 512 counts, from L2) and places its run's choices in their order. Up to
+// kSortOne choices one CTA does both in one launch.
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMaxRuns = 256;
+constexpr int64_t kSortRun = 4096;  // choices a CTA takes at least
+constexpr int64_t kSortOne = 8192;
+
+struct SortIn {
+  const int32_t* idx;
+  int32_t *starts, *source, *place;  // source: may be NULL
+  int32_t* counts;                   // [runs, E]
+  int64_t n, run;                    // choices; of a run
+  int32_t E, runs;
+};
+
+// Choices of this warp: [begin, end) of its CTA's run.
+__device__ __forceinline__ void warp_part(const SortIn& s, int64_t& begin, int64_t& end) {
+  const int64_t first = blockIdx.x * s.run, last = min(s.n, first + s.run);
+  const int64_t per = ((s.run + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
+  begin = min(last, first + (threadIdx.x >> 5) * per);
+  end = min(last, begin + per);
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortIn s) {
+  extern __shared__ int32_t hist[];  // [E]
+  take_turn();
+  for (int e = threadIdx.x; e < s.E; e += kSortThreads) hist[e] = 0;
+  __syncthreads();
+  const int64_t first = blockIdx.x * s.run, last = min(s.n, first + s.run);
+  for (int64_t c = first + threadIdx.x; c < last; c += kSortThreads) {
+    const int32_t e = s.idx[c];
+    if (e >= 0 && e < s.E) atomicAdd(hist + e, 1);  // (whole numbers: any order)
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < s.E; e += kSortThreads) s.counts[(int64_t)blockIdx.x * s.E + e] = hist[e];
+}
+
+template <bool ONE>
+__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortIn s) {
+  // a warp's counts, then the next row of its choices, by expert; behind them
+  // the rows that lower experts and earlier runs take
+  extern __shared__ int32_t next[];  // [kSortWarps, E], [E], [E]
+  __shared__ int32_t sums[kSortWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, E = s.E;
+  int32_t* before = next + kSortWarps * E;
+  int32_t* all = before + E;
+  take_turn();
+  for (int i = tid; i < (kSortWarps + 2) * E; i += kSortThreads) next[i] = 0;
+  __syncthreads();
+  int64_t begin, end;
+  warp_part(s, begin, end);
+  int32_t* mine = next + warp * E;
+  for (int64_t c = begin + lane; c < end; c += 32) {
+    const int32_t e = s.idx[c];
+    if (e >= 0 && e < E) atomicAdd(mine + e, 1);
+  }
+  if (!ONE) {
+    // threads side by side on the experts, slices of the runs
+    const int width = E <= 32 ? 32 : E <= 64 ? 64 : E <= 128 ? 128 : E <= 256 ? 256 : 512;
+    const int slices = kSortThreads / width, slice = tid / width, e = tid & (width - 1);
+    if (e < E) {
+      int32_t pre = 0, sum = 0;
+#pragma unroll 4
+      for (int r = slice; r < s.runs; r += slices) {
+        const int32_t v = __ldcg(s.counts + (int64_t)r * E + e);
+        sum += v;
+        if (r < (int)blockIdx.x) pre += v;
+      }
+      atomicAdd(before + e, pre);
+      atomicAdd(all + e, sum);
+    }
+  }
+  __syncthreads();
+  // the warps' first rows within the run; the run's counts
+  int32_t total = 0;
+  if (tid < E) {
+    int32_t at = 0;
+#pragma unroll 8
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int32_t v = next[w * E + tid];
+      next[w * E + tid] = at;
+      at += v;
+    }
+    total = ONE ? at : all[tid];
+  }
+  // the experts' first rows: a scan over at most 512 of them
+  int32_t scan = total;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t v = __shfl_up_sync(~0u, scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 31) sums[warp] = scan;
+  __syncthreads();
+  int32_t base = 0;
+  for (int w = 0; w < kMaxSorted / 32; ++w)
+    if (w < warp) base += sums[w];
+  const int32_t first = base + scan - total;
+  if (tid < E) {
+    before[tid] += first;
+    if (blockIdx.x == 0) {
+      s.starts[tid] = first;
+      if (tid == E - 1) s.starts[E] = first + total;
+    }
+  }
+  if (tid == E - 1) sums[kSortWarps - 1] = first + total;  // (past the experts' warps, or read)
+  __syncthreads();
+  const int32_t routed = sums[kSortWarps - 1];
+  for (int64_t c0 = begin; c0 < end; c0 += 32) {
+    const int64_t c = c0 + lane;
+    const int32_t e = c < end ? s.idx[c] : -1;
+    const bool ok = e >= 0 && e < E;
+    const uint32_t same = __match_any_sync(~0u, ok ? e : -1);
+    const int rank = __popc(same & ((1u << lane) - 1));
+    int32_t row = -1;
+    if (ok) row = before[e] + mine[e] + rank;
+    __syncwarp();
+    if (ok && rank == 0) mine[e] += __popc(same);
+    __syncwarp();
+    if (c < end) {
+      s.place[c] = row;
+      if (s.source != nullptr && ok) s.source[row] = (int32_t)c;
+    }
+  }
+  if (s.source != nullptr)
+    for (int64_t r = (int64_t)routed + (int64_t)blockIdx.x * kSortThreads + tid; r < s.n;
+         r += (int64_t)gridDim.x * kSortThreads)
+      s.source[r] = -1;
+}
+
+// ------------------------------------------------------------- rows of tokens
+// A row in units: 16 bytes where every row of a call starts on a 16-byte
+// boundary (the elements behind the last whole unit one by one), else elements.
+template <typename T, bool WIDE>
+struct Unit;
+template <typename T>
+struct Unit<T, false> {
+  using raw = T;
+  static constexpr int n = 1;
+  __device__ static __forceinline__ void get(const raw& r, float (&v)[1]) { v[0] = to_f(r); }
+  __device__ static __forceinline__ raw put(const float (&v)[1]) { return from_f<T>(v[0]); }
+};
+template <>
+struct Unit<float, true> {
+  using raw = uint4;
+  static constexpr int n = 4;
+  __device__ static __forceinline__ void get(const raw& r, float (&v)[4]) {
+    v[0] = __uint_as_float(r.x);
+    v[1] = __uint_as_float(r.y);
+    v[2] = __uint_as_float(r.z);
+    v[3] = __uint_as_float(r.w);
+  }
+  __device__ static __forceinline__ raw put(const float (&v)[4]) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3]));
+  }
+};
+template <>
+struct Unit<uint16_t, true> {
+  using raw = uint4;
+  static constexpr int n = 8;
+  __device__ static __forceinline__ void get(const raw& r, float (&v)[8]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ static __forceinline__ raw put(const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+constexpr int kRowThreads = 256;
+constexpr int kRowCtas = 8;  // an SM, at most
+constexpr int kGatherUnits = 4;   // units of a lane in a piece
+constexpr int kCombineUnits = 2;
+
+struct RowIn {
+  int64_t T_, rows, ld, row_ld;  // tokens, rows; strides of the tokens' and of the rows' arrays
+  int32_t K, H;
+  const int32_t* place;
+};
+
+// Row of choice j of token t held by lane j, or -1.
+__device__ __forceinline__ int32_t place_at(const RowIn& p, int64_t t, int lane) {
+  const int32_t r = lane < p.K ? p.place[t * p.K + lane] : -1;
+  return r < p.rows ? r : -1;
+}
+
+// rows[place[t, j]] = x[t]. A warp takes a piece of a token's row, reads it once
+// and writes it to the token's rows.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(kRowThreads)
+    gather_kernel(const RowIn p, const T* __restrict__ x, T* __restrict__ rows, int32_t pieces) {
+  using U = Unit<T, WIDE>;
+  using raw = typename U::raw;
+  constexpr int NU = WIDE ? kGatherUnits : 2 * kGatherUnits;
+  const int lane = threadIdx.x & 31;
+  const int32_t units = p.H / U::n, tail = units * U::n;
+  take_turn();
+  const int64_t step = (int64_t)gridDim.x * (kRowThreads / 32);
+  const int64_t step_t = step / pieces, first = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+  const int32_t step_p = (int32_t)(step - step_t * pieces);
+  int64_t t = first / pieces;
+  int32_t piece = (int32_t)(first - t * pieces);
+  for (; t < p.T_; t += step_t, piece += step_p) {
+    if (piece >= pieces) {
+      piece -= pieces;
+      if (++t >= p.T_) break;
+    }
+    const int32_t row = place_at(p, t, lane);
+    const uint32_t used = __ballot_sync(~0u, row >= 0);
+    if (used == 0) continue;
+    const T* in = x + t * p.ld;
+    const int32_t u0 = piece * (32 * NU) + lane;
+    raw v[NU];
+#pragma unroll
+    for (int k = 0; k < NU; ++k)
+      if (u0 + 32 * k < units) v[k] = reinterpret_cast<const raw*>(in)[u0 + 32 * k];
+    const bool last = piece + 1 == pieces && tail + lane < p.H;
+    T loose = T();
+    if (last) loose = in[tail + lane];
+    for (uint32_t left = used; left != 0; left &= left - 1) {
+      T* out = rows + (int64_t)__shfl_sync(~0u, row, __ffs(left) - 1) * p.row_ld;
+#pragma unroll
+      for (int k = 0; k < NU; ++k)
+        if (u0 + 32 * k < units) reinterpret_cast<raw*>(out)[u0 + 32 * k] = v[k];
+      if (last) out[tail + lane] = loose;
+    }
+  }
+}
+
+// out[t] = sum_j g[t, j] y[place[t, j]] (GATES), or the plain sum; in fp32, one
+// choice after the other, rounded once. A warp takes a piece of a token's row;
+// four choices' loads are on their way at a time.
+template <typename T, bool WIDE, bool GATES>
+__global__ void __launch_bounds__(kRowThreads)
+    combine_kernel(const RowIn p, const T* __restrict__ y, const float* __restrict__ gates,
+                   T* __restrict__ out, int32_t pieces) {
+  using U = Unit<T, WIDE>;
+  using raw = typename U::raw;
+  constexpr int NU = WIDE ? kCombineUnits : 2 * kCombineUnits, JB = 4;
+  const int lane = threadIdx.x & 31;
+  const int32_t units = p.H / U::n, tail = units * U::n;
+  take_turn();
+  const int64_t step = (int64_t)gridDim.x * (kRowThreads / 32);
+  const int64_t step_t = step / pieces, first = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+  const int32_t step_p = (int32_t)(step - step_t * pieces);
+  int64_t t = first / pieces;
+  int32_t piece = (int32_t)(first - t * pieces);
+  for (; t < p.T_; t += step_t, piece += step_p) {
+    if (piece >= pieces) {
+      piece -= pieces;
+      if (++t >= p.T_) break;
+    }
+    const int32_t row = place_at(p, t, lane);
+    const float gate = GATES && lane < p.K ? gates[t * p.K + lane] : 1.f;
+    const int32_t u0 = piece * (32 * NU) + lane;
+    const bool last = piece + 1 == pieces && tail + lane < p.H;
+    float acc[NU][U::n], loose = 0.f;
+#pragma unroll
+    for (int k = 0; k < NU; ++k)
+#pragma unroll
+      for (int q = 0; q < U::n; ++q) acc[k][q] = 0.f;
+    for (int j0 = 0; j0 < p.K; j0 += JB) {
+      raw v[JB][NU];
+      int32_t r[JB];
+      T lv[JB];
+#pragma unroll
+      for (int j = 0; j < JB; ++j) {
+        r[j] = __shfl_sync(~0u, row, (j0 + j) & 31);
+        if (j0 + j >= p.K) r[j] = -1;
+        if (r[j] < 0) continue;
+        const T* in = y + (int64_t)r[j] * p.row_ld;
+#pragma unroll
+        for (int k = 0; k < NU; ++k)
+          if (u0 + 32 * k < units) v[j][k] = reinterpret_cast<const raw*>(in)[u0 + 32 * k];
+        if (last) lv[j] = in[tail + lane];
+      }
+#pragma unroll
+      for (int j = 0; j < JB; ++j) {
+        const float g = __shfl_sync(~0u, gate, (j0 + j) & 31);
+        if (r[j] < 0) continue;
+#pragma unroll
+        for (int k = 0; k < NU; ++k) {
+          float f[U::n];
+          U::get(v[j][k], f);
+#pragma unroll
+          for (int q = 0; q < U::n; ++q) acc[k][q] = GATES ? __fmaf_rn(g, f[q], acc[k][q]) : acc[k][q] + f[q];
+        }
+        if (last) loose = GATES ? __fmaf_rn(g, to_f(lv[j]), loose) : loose + to_f(lv[j]);
+      }
+    }
+    T* to = out + t * p.ld;
+#pragma unroll
+    for (int k = 0; k < NU; ++k)
+      if (u0 + 32 * k < units) reinterpret_cast<raw*>(to)[u0 + 32 * k] = U::put(acc[k]);
+    if (last) to[tail + lane] = from_f<T>(loose);
+  }
+}
+
+// dy[place[t, j]] = g[t, j] d_out[t] and dg[t, j] = <d_out[t], y[place[t, j]]>. A
+// warp takes a choice; the warps of a token read its row at about the same time,
+// all but one of them from L1 or L2. y and d_y may be the same rows.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(kRowThreads)
+    combine_grad_kernel(const RowIn p, const T* __restrict__ d_out, const T* y, int64_t y_ld,
+                        const float* __restrict__ gates, T* d_y, float* __restrict__ d_gates) {
+  using U = Unit<T, WIDE>;
+  using raw = typename U::raw;
+  constexpr int NU = WIDE ? 4 : 8;
+  const int lane = threadIdx.x & 31;
+  const int32_t units = p.H / U::n, tail = units * U::n;
+  take_turn();
+  const int64_t items = p.T_ * p.K, step = (int64_t)gridDim.x * (kRowThreads / 32);
+  for (int64_t c = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); c < items; c += step) {
+    const int32_t row = p.place[c];
+    if (row < 0 || row >= p.rows) {
+      if (lane == 0) d_gates[c] = 0.f;
+      continue;
+    }
+    const float g = gates[c];
+    const T* d = d_out + (int64_t)((uint32_t)c / (uint32_t)p.K) * p.ld;
+    const T* in = y + (int64_t)row * y_ld;
+    T* to = d_y + (int64_t)row * p.row_ld;
+    float dot[NU];
+#pragma unroll
+    for (int k = 0; k < NU; ++k) dot[k] = 0.f;
+    for (int32_t u0 = lane; u0 < units; u0 += 32 * NU) {
+      raw a[NU], b[NU];
+#pragma unroll
+      for (int k = 0; k < NU; ++k)
+        if (u0 + 32 * k < units) {
+          a[k] = reinterpret_cast<const raw*>(d)[u0 + 32 * k];
+          b[k] = reinterpret_cast<const raw*>(in)[u0 + 32 * k];
+        }
+#pragma unroll
+      for (int k = 0; k < NU; ++k)
+        if (u0 + 32 * k < units) {
+          float fa[U::n], fb[U::n];
+          U::get(a[k], fa);
+          U::get(b[k], fb);
+#pragma unroll
+          for (int q = 0; q < U::n; ++q) {
+            dot[k] = __fmaf_rn(fa[q], fb[q], dot[k]);
+            fa[q] *= g;
+          }
+          reinterpret_cast<raw*>(to)[u0 + 32 * k] = U::put(fa);
+        }
+    }
+    if (tail + lane < p.H) {
+      const float a = to_f(d[tail + lane]);
+      dot[0] = __fmaf_rn(a, to_f(in[tail + lane]), dot[0]);
+      to[tail + lane] = from_f<T>(g * a);
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < NU; ++k) sum += dot[k];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    if (lane == 0) d_gates[c] = sum;
+  }
+}
+
+// ------------------------------------------------------------- host side
+int64_t run_of(int64_t n) {
+  const int64_t run = std::max(kSortRun, (n + kMaxRuns - 1) / kMaxRuns);
+  return (run + kSortWarps * 32 - 1) / (kSortWarps * 32) * (kSortWarps * 32);
+}
+
+size_t sort_bytes(int64_t n, int64_t E) {
+  return n <= kSortOne ? 16 : (size_t)(((n + run_of(n) - 1) / run_of(n) * E * 4 + 15) / 16 * 16);
+}
+
+bool sizes_ok(int64_t T_, int64_t K) {
+  return T_ >= 0 && T_ <= kMaxTokens && K >= 1 && K <= kMaxChoices;
+}
+
+struct RowsArg {
+  const char* who;
+  int32_t dtype;
+  int64_t T_, K, H;
+  const int32_t* place;
+};
+// An array of n rows at stride ld.
+struct Strided {
+  const void* p;
+  int64_t n, ld;
+};
+
+vsf_status check_rows(const RowsArg& a, std::initializer_list<Strided> in) {
+  const std::string w(a.who);
+  if (a.dtype != VSF_BF16 && a.dtype != VSF_FP32) return fail(VSF_ERR_ARG, w + ": bad dtype");
+  if (!sizes_ok(a.T_, a.K) || a.H < 1 || a.H > kMaxWidth)
+    return fail(VSF_ERR_ARG, w + ": sizes out of range");
+  for (const Strided& s : in) {
+    if (s.ld < a.H || s.ld > (int64_t(1) << 40)) return fail(VSF_ERR_ARG, w + ": stride out of range");
+    if (a.T_ > 0 && s.p == nullptr) return fail(VSF_ERR_ARG, w + ": NULL pointer");
+    if (!aligned(s.p, a.dtype == VSF_BF16 ? 2 : 4)) return fail(VSF_ERR_ALIGN, w + ": pointer alignment");
+  }
+  if (a.T_ > 0 && a.place == nullptr) return fail(VSF_ERR_ARG, w + ": NULL pointer");
+  if (!aligned(a.place, 4)) return fail(VSF_ERR_ALIGN, w + ": pointer alignment");
+  return VSF_OK;
+}
+
+bool overlap(const RowsArg& a, const Strided& x, const Strided& y) {
+  if (x.n == 0 || y.n == 0) return false;
+  const int64_t size = a.dtype == VSF_BF16 ? 2 : 4;
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x.p), y0 = reinterpret_cast<uintptr_t>(y.p);
+  return x0 < y0 + ((y.n - 1) * y.ld + a.H) * size && y0 < x0 + ((x.n - 1) * x.ld + a.H) * size;
+}
+
+bool wide(const RowsArg& a, std::initializer_list<Strided> in) {
+  const int64_t size = a.dtype == VSF_BF16 ? 2 : 4;
+  for (const Strided& s : in)
+    if (!aligned(s.p, 16) || s.ld * size % 16 != 0) return false;
+  return true;
+}
+
+// Pieces of a row, and CTAs for `items` warps.
+int32_t pieces_of(const RowsArg& a, bool w, int units) {
+  const int64_t n = w ? a.H / (a.dtype == VSF_BF16 ? 8 : 4) : a.H;
+  const int64_t per = 32 * (w ? units : 2 * units);
+  return (int32_t)std::max<int64_t>(1, (n + per - 1) / per);
+}
+unsigned row_grid(int64_t items) {
+  return (unsigned)std::min<int64_t>((items + kRowThreads / 32 - 1) / (kRowThreads / 32),
+                                     kSms * kRowCtas);
+}
+
+template <typename T>
+cudaError_t launch_gather(const RowsArg& a, const RowIn& p, const void* x, void* rows, bool w,
+                          cudaStream_t st) {
+  const int32_t pieces = pieces_of(a, w, kGatherUnits);
+  return launch_behind(w ? gather_kernel<T, true> : gather_kernel<T, false>, row_grid(a.T_ * pieces),
+                       kRowThreads, 0, 1, st, p, static_cast<const T*>(x), static_cast<T*>(rows),
+                       pieces);
+}
+
+template <typename T>
+cudaError_t launch_combine(const RowsArg& a, const RowIn& p, const void* y, const float* gates,
+                           void* out, bool w, cudaStream_t st) {
+  const int32_t pieces = pieces_of(a, w, kCombineUnits);
+  auto fn = gates != nullptr ? (w ? combine_kernel<T, true, true> : combine_kernel<T, false, true>)
+                             : (w ? combine_kernel<T, true, false> : combine_kernel<T, false, false>);
+  return launch_behind(fn, row_grid(a.T_ * pieces), kRowThreads, 0, 1, st, p,
+                       static_cast<const T*>(y), gates, static_cast<T*>(out), pieces);
+}
+
+template <typename T>
+cudaError_t launch_combine_grad(const RowsArg& a, const RowIn& p, const void* d_out, const void* y,
+                                int64_t y_ld, const float* gates, void* d_y, float* d_gates, bool w,
+                                cudaStream_t st) {
+  return launch_behind(w ? combine_grad_kernel<T, true> : combine_grad_kernel<T, false>,
+                       row_grid(a.T_ * a.K), kRowThreads, 0, 1, st, p,
+                       static_cast<const T*>(d_out), static_cast<const T*>(y), y_ld, gates,
+                       static_cast<T*>(d_y), d_gates);
+}
+
+}  // namespace
+}  // namespace vsf
+
+using namespace vsf;
+
+extern "C" {
+
+size_t vsf_expert_sort_workspace_bytes(int64_t tokens, int64_t top_k, int64_t experts) {
+  if (!sizes_ok(tokens, top_k) || experts < 1 || experts > kMaxSorted) return 0;
+  return sort_bytes(tokens * top_k, experts);
+}
+
+vsf_status vsf_expert_sort(const int32_t* idx, int64_t T, int64_t top_k, int64_t E, int32_t* starts,
+                           int32_t* source, int32_t* place, void* d_workspace, size_t ws_bytes,
+                           void* stream) {
+  vsf::Range nvtx_range("vsf_expert_sort");
+  const char* who = "vsf_expert_sort";
+  if (!sizes_ok(T, top_k) || E < 1 || E > kMaxSorted)
+    return fail(VSF_ERR_ARG, "vsf_expert_sort: sizes out of range");
+  if (starts == nullptr || d_workspace == nullptr || (T > 0 && (idx == nullptr || place == nullptr)))
+    return fail(VSF_ERR_ARG, "vsf_expert_sort: NULL pointer");
+  const int64_t n = T * top_k;
+  if (ws_bytes < sort_bytes(n, E)) return fail(VSF_ERR_ARG, "vsf_expert_sort: workspace too small");
+  if (!aligned(idx, 4) || !aligned(starts, 4) || !aligned(source, 4) || !aligned(place, 4) ||
+      !aligned(d_workspace, 16))
+    return fail(VSF_ERR_ALIGN, "vsf_expert_sort: pointer alignment");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool one = n <= kSortOne;
+  const int64_t run = one ? std::max<int64_t>(n, 1) : run_of(n);
+  const int32_t runs = one ? 1 : (int32_t)((n + run - 1) / run);
+  const SortIn s = {idx, starts, source, place, static_cast<int32_t*>(d_workspace),
+                    n,   run,    (int32_t)E, runs};
+  const unsigned smem = (unsigned)((kSortWarps + 2) * E * 4);
+  auto fn = one ? sort_place_kernel<true> : sort_place_kernel<false>;
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024)
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && !one)
+    e = launch_behind(sort_count_kernel, runs, kSortThreads, (unsigned)(E * 4), 1, st, s);
+  if (e == cudaSuccess) e = launch_behind(fn, runs, kSortThreads, smem, 1, st, s);
+  return e == cudaSuccess ? VSF_OK : cuda_error(e, who);
+}
+
+vsf_status vsf_expert_gather(const void* x, int32_t dtype, int64_t T, int64_t H, int64_t ld,
+                             const int32_t* place, int64_t top_k, void* rows, int64_t rows_ld,
+                             void* stream) {
+  vsf::Range nvtx_range("vsf_expert_gather");
+  const RowsArg a = {"vsf_expert_gather", dtype, T, top_k, H, place};
+  const Strided in = {x, T, ld}, out = {rows, T * top_k, rows_ld};
+  const vsf_status s = check_rows(a, {in, out});
+  if (s != VSF_OK) return s;
+  if (overlap(a, in, out)) return fail(VSF_ERR_ARG, "vsf_expert_gather: rows overlap the tokens");
+  if (T == 0) return VSF_OK;
+  const RowIn p = {T, T * top_k, ld, rows_ld, (int32_t)top_k, (int32_t)H, place};
+  const bool w = wide(a, {in, out});
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == VSF_BF16 ? launch_gather<uint16_t>(a, p, x, rows, w, st)
+                                          : launch_gather<float>(a, p, x, rows, w, st);
+  return e == cudaSuccess ? VSF_OK : cuda_error(e, a.who);
+}
+
+vsf_status vsf_expert_combine(const void* y, int32_t dtype, int64_t T, int64_t H, int64_t y_ld,
+                              const int32_t* place, const float* gates, int64_t top_k, void* out,
+                              int64_t out_ld, void* stream) {
+  vsf::Range nvtx_range("vsf_expert_combine");
+  const RowsArg a = {"vsf_expert_combine", dtype, T, top_k, H, place};
+  const Strided in = {y, T * top_k, y_ld}, to = {out, T, out_ld};
+  const vsf_status s = check_rows(a, {in, to});
+  if (s != VSF_OK) return s;
+  if (!aligned(gates, 4)) return fail(VSF_ERR_ALIGN, "vsf_expert_combine: pointer alignment");
+  if (overlap(a, in, to)) return fail(VSF_ERR_ARG, "vsf_expert_combine: rows overlap the tokens");
+  if (T == 0) return VSF_OK;
+  const RowIn p = {T, T * top_k, out_ld, y_ld, (int32_t)top_k, (int32_t)H, place};
+  const bool w = wide(a, {in, to});
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == VSF_BF16 ? launch_combine<uint16_t>(a, p, y, gates, out, w, st)
+                                          : launch_combine<float>(a, p, y, gates, out, w, st);
+  return e == cudaSuccess ? VSF_OK : cuda_error(e, a.who);
+}
+
+vsf_status vsf_expert_combine_grad(const void* d_out, int32_t dtype, int64_t T, int64_t H,
+                                   int64_t d_out_ld, const void* y, int64_t y_ld,
+                                   const int32_t* place, const float* gates, int64_t top_k,
+                                   void* d_y, int64_t d_y_ld, float* d_gates, void* stream) {
+  vsf::Range nvtx_range("vsf_expert_combine_grad");
+  const RowsArg a = {"vsf_expert_combine_grad", dtype, T, top_k, H, place};
+  const Strided d = {d_out, T, d_out_ld}, in = {y, T * top_k, y_ld}, to = {d_y, T * top_k, d_y_ld};
+  const vsf_status s = check_rows(a, {d, in, to});
+  if (s != VSF_OK) return s;
+  if (T > 0 && (gates == nullptr || d_gates == nullptr))
+    return fail(VSF_ERR_ARG, "vsf_expert_combine_grad: NULL pointer");
+  if (!aligned(gates, 4) || !aligned(d_gates, 4))
+    return fail(VSF_ERR_ALIGN, "vsf_expert_combine_grad: pointer alignment");
+  if (overlap(a, d, to) || (overlap(a, in, to) && !(y == d_y && y_ld == d_y_ld)))
+    return fail(VSF_ERR_ARG, "vsf_expert_combine_grad: d_y overlaps an input in part");
+  if (T == 0) return VSF_OK;
+  const RowIn p = {T, T * top_k, d_out_ld, d_y_ld, (int32_t)top_k, (int32_t)H, place};
+  const bool w = wide(a, {d, in, to});
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      dtype == VSF_BF16
+          ? launch_combine_grad<uint16_t>(a, p, d_out, y, y_ld, gates, d_y, d_gates, w, st)
+          : launch_combine_grad<float>(a, p, d_out, y, y_ld, gates, d_y, d_gates, w, st);
+  return e == cudaSuccess ? VSF_OK : cuda_error(e, a.who);
+}
+
+}  // extern "C"

@@ -1,0 +1,418 @@
+// expert_gemm.cuh — the products of rows sorted by expert with their experts'
+// weights, on the fifth-generation tensor cores (tcgen05, sm_103a). Included by
+// experts.cu after tcgen05.cuh.
+//
+// Expert e owns rows [starts[e], starts[e + 1]) of x [R, K] and y [R, N] and the
+// weights W[e] [N, K]. bf16 operands and outputs, fp32 accumulation in tensor
+// memory, one rounding. The three products, as D[i][j] = sum_r A[i][r] B[j][r]:
+//   kForward    y  = x W^T     i: N (A = W, K-major)    j: rows (x, K-major)   r: K
+//   kInput      dx = dy W      i: K (A = W, MN-major)   j: rows (dy, K-major)  r: N
+//   kWeight     dW = dy^T x    i: N (A = dy, MN-major)  j: K (x, MN-major)     r: rows
+// The weights' side is the 256 lanes of a tile, the rows are its columns: a
+// tensor-core product has 128 or 256 lanes but any multiple of 32 columns, and
+// experts have any number of rows. So an expert with few rows costs a narrow tile,
+// and one that streams its weights costs little more than their bytes. Columns
+// behind an expert's last row are computed from what lies there (the next
+// expert's rows, or zeros behind the last row of all) and not stored: columns do
+// not mix. Where rows are what is summed over (kWeight) they would: there the rows
+// of the last stage that are not the expert's, up to the next 16, are zeroed in
+// shared memory before the products read them.
+//
+// Pairs of CTAs compute tiles of 256 lanes with cta_group::2, each CTA half of the
+// lanes, as ns_gemm.cuh does: a ring of six stages of 64 of r, two accumulators.
+//   warp 0      producer: this CTA's halves of both operands' stages;
+//   warp 1      TMEM; one thread of the leader issues the products;
+//   warps 2..5  epilogue, in both CTAs;
+//   warp 6      (kWeight) zeroes, in its CTA, the rows that are not the expert's.
+// Persistent: one pair of CTAs for two SMs, tiles dealt out in turn. The tiles
+// depend on starts, which is device memory: every CTA works out the experts'
+// tiles for itself before it begins. Every wait is bounded (mbarrier.cuh), and a
+// broken pipeline ends as in ns_gemm.cuh.
+
+enum { kForward = 0, kInput = 1, kWeight = 2 };
+
+constexpr int kXStages = 6;
+constexpr int kXDepth = 64;                            // of r a stage
+constexpr int kXLanes = 256;                           // of a tile
+constexpr int kXCols = 256;                            // of a tile, at most
+constexpr int kMaxGroups = 512;                        // experts
+constexpr uint32_t kXHalf = 128 * kXDepth * 2;         // one operand's half of a stage: 16 KB
+constexpr uint32_t kXStage = 2 * kXHalf;
+constexpr uint32_t kXBars = 3 * kXStages + 5;
+struct XTable {
+  int32_t first[kMaxGroups + 1];  // tiles in front of each expert's
+  int32_t start[kMaxGroups + 1];  // its first row
+  uint32_t tmem, stop;
+};
+constexpr uint32_t kXSmem = kXStages * kXStage + 8 * kXBars + (uint32_t)sizeof(XTable) + 1024;
+static_assert(kXSmem <= 227 * 1024, "fits in shared memory");
+
+struct ExpertArgs {
+  const int32_t* starts;
+  int32_t E, rows;    // experts; rows of the arrays
+  int32_t lanes;      // extent of i
+  int32_t cols;       // kWeight: extent of j
+  int32_t depth;      // kForward, kInput: extent of r
+  int32_t lane_tiles, col_tiles;
+  uint16_t* out;
+  int64_t ld, stride; // of out's rows; kWeight: of its experts
+};
+
+struct XTile {
+  int32_t e, lane0;   // expert, first lane (of the pair)
+  int32_t col0;       // first row (kWeight: first column)
+  int32_t width;      // columns computed: a multiple of 32 (kWeight: 128 or 256)
+  int32_t cols;       // columns stored
+  int32_t row0, depth;  // what is summed over
+};
+
+// An expert's rows in tiles of at most 256, as even as can be: one of a width
+// of 256 and a narrow one would cost a whole tile's weights for the narrow one.
+__device__ __forceinline__ int32_t token_tiles(int32_t rows) { return (rows + kXCols - 1) / kXCols; }
+__device__ __forceinline__ int32_t token_width(int32_t rows, int32_t tiles) {
+  return ((rows + tiles - 1) / tiles + 31) / 32 * 32;
+}
+
+// Tile t of the launch; `e` moves on from tile to tile.
+template <int KIND>
+__device__ __forceinline__ XTile tile_at(const ExpertArgs& a, const XTable& x, int32_t t, int32_t& e) {
+  XTile q;
+  if (KIND == kWeight) {
+    const int32_t per = a.lane_tiles * a.col_tiles;
+    q.e = t / per;
+    const int32_t k = t - q.e * per, col = k / a.lane_tiles;
+    q.lane0 = (k - col * a.lane_tiles) * kXLanes;
+    q.col0 = col * kXCols;
+    q.cols = min(kXCols, a.cols - q.col0);
+    q.width = q.cols > 128 ? 256 : 128;
+    q.row0 = x.start[q.e];
+    q.depth = x.start[q.e + 1] - q.row0;
+  } else {
+    while (t >= x.first[e + 1]) ++e;
+    q.e = e;
+    const int32_t k = t - x.first[e], piece = k / a.lane_tiles;
+    const int32_t begin = x.start[e], rows = x.start[e + 1] - begin;
+    q.lane0 = (k - piece * a.lane_tiles) * kXLanes;
+    q.width = token_width(rows, token_tiles(rows));
+    q.col0 = begin + piece * q.width;
+    q.cols = min(q.width, begin + rows - q.col0);
+    q.row0 = 0;
+    q.depth = a.depth;
+  }
+  return q;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int KIND>
+constexpr int kXThreads = KIND == kWeight ? 224 : 192;
+
+// tmA: the lanes' operand. tmB: the columns' operand in boxes of 128 rows (K-major)
+// or 64 x 64 (MN-major); tmB16 in boxes of 16 rows.
+template <int KIND>
+__global__ void __launch_bounds__(kXThreads<KIND>, 1)
+    expert_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmB16, const ExpertArgs g, unsigned* err) {
+  constexpr bool AMN = KIND != kForward, BMN = KIND == kWeight;
+  extern __shared__ __align__(1024) unsigned char raw[];
+  unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  const uint32_t s0 = smem_u32(sm), bar0 = s0 + kXStages * kXStage;
+  XTable& table = *reinterpret_cast<XTable*>(sm + kXStages * kXStage + 8 * kXBars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kXStages + s); };
+  auto tfull_bar = [&](int i) { return bar0 + 8u * (2 * kXStages + i); };
+  auto tempty_bar = [&](int i) { return bar0 + 8u * (2 * kXStages + 2 + i); };
+  const uint32_t done_bar = bar0 + 8u * (2 * kXStages + 4);
+  auto own_bar = [&](int s) { return done_bar + 8u + 8u * s; };
+  volatile uint32_t* stop = &table.stop;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const bool leader = rank == 0;
+  const int cid = blockIdx.x / 2, ncid = gridDim.x / 2;
+  constexpr uint16_t kBoth = 3;
+
+  if (threadIdx.x == 0) {
+    table.stop = 0u;
+    for (int s = 0; s < kXStages; ++s) {
+      mbar_init(full_bar(s), KIND == kWeight ? 2 : 1);  // kWeight: one arrival of each CTA
+      mbar_init(empty_bar(s), 1);
+      mbar_init(own_bar(s), 1);  // kWeight: this CTA's copies of a stage to be mended
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(tfull_bar(i), 1);
+      mbar_init(tempty_bar(i), 8);  // every epilogue warp of both CTAs
+    }
+    mbar_init(done_bar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&table.tmem), 2 * kXCols);
+    tmem_relinquish_pair();
+  }
+  take_turn();
+  // the experts' rows, in order and inside the arrays whatever starts holds
+  for (int e = threadIdx.x; e <= g.E; e += kXThreads<KIND>)
+    table.start[e] = min(max(g.starts[e], 0), g.rows);
+  __syncthreads();
+  if (warp == 2) {
+    // each lane takes a run of experts: their running maximum, their tiles
+    const int per = (g.E + 32) / 32, begin = min(lane * per, g.E + 1), end = min(begin + per, g.E + 1);
+    int32_t top = 0;
+    for (int e = begin; e < end; ++e) table.start[e] = top = max(top, table.start[e]);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t v = __shfl_up_sync(~0u, top, o);
+      if (lane >= o) top = max(top, v);
+    }
+    int32_t low = __shfl_up_sync(~0u, top, 1);
+    if (lane == 0) low = 0;
+    for (int e = begin; e < end; ++e) table.start[e] = max(low, table.start[e]);
+    __syncwarp();
+    int32_t tiles = 0;
+    for (int e = begin; e < min(end, g.E); ++e)
+      tiles += token_tiles(table.start[e + 1] - table.start[e]) * g.lane_tiles;
+    int32_t at = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t v = __shfl_up_sync(~0u, at, o);
+      if (lane >= o) at += v;
+    }
+    at -= tiles;
+    for (int e = begin; e < end; ++e) {
+      table.first[e] = at;
+      if (e < g.E) at += token_tiles(table.start[e + 1] - table.start[e]) * g.lane_tiles;
+    }
+  }
+  tc_fence_before();
+  cluster_barrier();
+  tc_fence_after();
+  const uint32_t tmem = table.tmem;
+  // the leader's products write both CTAs' accumulators at the leader's address
+  if (threadIdx.x == 0 && ld_peer_u32(peer_addr(smem_u32(&table.tmem), (uint32_t)(rank ^ 1))) != tmem) {
+    atomicOr(err, 8u);
+    table.stop = 1u;
+    remote_stop(stop, (uint32_t)(rank ^ 1));
+  }
+  cluster_barrier();
+  const int32_t ntiles =
+      KIND == kWeight ? g.E * g.lane_tiles * g.col_tiles : table.first[g.E];
+  const uint32_t leader_full0 = peer_addr(full_bar(0), 0);
+  const uint32_t leader_tempty0 = peer_addr(tempty_bar(0), 0);
+  auto halt_cluster = [&]() { remote_stop(stop, (uint32_t)(rank ^ 1)); };
+
+  if (warp == 0) {
+    if (lane == 0 && *stop == 0u) {
+      // ---------------- producer (both CTAs)
+      const uint32_t own0 = peer_addr(own_bar(0), (uint32_t)rank);
+      uint32_t it = 0, mended = 0, phases = 0;  // stages mended so far; how often, modulo 2
+      int32_t e = 0;
+      bool halted = false;
+      for (int32_t t = cid; t < ntiles && !halted; t += ncid) {
+        const XTile q = tile_at<KIND>(g, table, t, e);
+        const int32_t half = q.width / 2;
+        const int32_t lane0 = q.lane0 + rank * 128, col0 = q.col0 + rank * half;
+        const uint32_t bytes = kXHalf + (uint32_t)half * (kXDepth * 2);
+        for (int32_t k0 = 0; k0 < q.depth; k0 += kXDepth) {
+          const int s = it % kXStages;
+          const uint32_t ph = (it / kXStages) & 1u;
+          if (!mbar_wait(empty_bar(s), ph ^ 1u, err, stop)) {
+            halted = true;
+            halt_cluster();
+            break;
+          }
+          ++it;
+          uint32_t fb = leader_full0 + 8u * s;
+          if (KIND != kWeight) {
+            if (leader) mbar_expect_tx(full_bar(s), 2 * bytes);
+          } else if (k0 + kXDepth > q.depth && (q.depth & 15) != 0) {
+            fb = own0 + 8u * s;  // warp 6 mends the stage and then arrives
+            mbar_expect_tx(own_bar(s), bytes);
+            mended |= 1u << s;
+            phases ^= 1u << s;
+          } else if (leader) {
+            mbar_expect_tx(full_bar(s), 2 * bytes);
+          } else {
+            mbar_arrive_cluster(fb);
+          }
+          const uint32_t a = s0 + s * kXStage, b = a + kXHalf;
+          if (KIND == kWeight) {
+            const int32_t r = q.row0 + k0;
+            tma3_g2s_pair(a, &tmA, lane0, r, 0, fb);
+            tma3_g2s_pair(a + 8192u, &tmA, lane0 + 64, r, 0, fb);
+            tma3_g2s_pair(b, &tmB, col0, r, 0, fb);
+            if (half > 64) tma3_g2s_pair(b + 8192u, &tmB, col0 + 64, r, 0, fb);
+          } else {
+            if (AMN) {
+              tma3_g2s_pair(a, &tmA, lane0, k0, q.e, fb);
+              tma3_g2s_pair(a + 8192u, &tmA, lane0 + 64, k0, q.e, fb);
+            } else {
+              tma3_g2s_pair(a, &tmA, k0, lane0, q.e, fb);
+            }
+            if (half == 128) {
+              tma3_g2s_pair(b, &tmB, k0, col0, 0, fb);
+            } else {
+              for (int32_t c = 0; c < half; c += 16)
+                tma3_g2s_pair(b + (uint32_t)c * 128u, &tmB16, k0, col0 + c, 0, fb);
+            }
+          }
+        }
+      }
+      // every copy lands before the CTA ends: the leader sees both CTAs' (the
+      // follower's are covered by its wait and the last cluster barrier)
+      const uint64_t deadline = global_ns() + kWaitNs;
+      for (int s = 0; KIND == kWeight && s < kXStages; ++s)
+        if (mended >> s & 1u) mbar_drain(own_bar(s), (phases >> s & 1u) ^ 1u, deadline, err);
+      if (leader) {
+        for (int s = 0; s < kXStages; ++s) {
+          if (it > (uint32_t)s) {
+            const uint32_t last = (it - 1 - s) / kXStages * kXStages + s;
+            mbar_drain(full_bar(s), (last / kXStages) & 1u, deadline, err);
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader && *stop == 0u) {
+      // ---------------- products (leader only)
+      uint32_t it = 0;
+      int32_t e = 0;
+      int lt = 0;
+      bool halted = false;
+      for (int32_t t = cid; t < ntiles && !halted; t += ncid, ++lt) {
+        const XTile q = tile_at<KIND>(g, table, t, e);
+        const uint32_t idesc = umma_idesc_bf16(AMN, BMN, kXLanes, q.width);
+        const int buf = lt & 1;
+        if (!mbar_wait_cluster(tempty_bar(buf), ((uint32_t)(lt >> 1) & 1u) ^ 1u, err, stop)) {
+          halt_cluster();
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(buf * kXCols);
+        for (int32_t k0 = 0; k0 < q.depth; k0 += kXDepth, ++it) {
+          const int s = it % kXStages;
+          if (!mbar_wait_cluster(full_bar(s), (it / kXStages) & 1u, err, stop)) {
+            halted = true;
+            halt_cluster();
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = s0 + s * kXStage, b = a + kXHalf;
+          // (what a stage holds past the depth is zeros, or mended to the next 16)
+          const int steps = min(kXDepth / 16, (q.depth - k0 + 15) / 16);
+#pragma unroll
+          for (int kk = 0; kk < kXDepth / 16; ++kk)
+            if (kk < steps)
+              umma_pair_bf16(d, operand_desc<AMN>(a, kk), operand_desc<BMN>(b, kk), idesc,
+                             (k0 | kk) != 0 ? 1u : 0u);
+          umma_pair_commit(empty_bar(s), kBoth);
+        }
+        if (!halted) umma_pair_commit(tfull_bar(buf), kBoth);
+      }
+      umma_pair_commit(done_bar, 1);  // this CTA only
+      mbar_drain(done_bar, 0u, global_ns() + kWaitNs, err);
+    }
+  } else if (warp < 6) {
+    // ---------------- epilogue (both CTAs): this CTA's 128 lanes
+    const int quarter = warp & 3;
+    int32_t e = 0;
+    int lt = 0;
+    for (int32_t t = cid; t < ntiles; t += ncid, ++lt) {
+      const int buf = lt & 1;
+      const bool ok = __all_sync(~0u, mbar_wait(tfull_bar(buf), (uint32_t)(lt >> 1) & 1u, err, stop));
+      tc_fence_after();
+      if (ok) {
+        const XTile q = tile_at<KIND>(g, table, t, e);
+        const int32_t i = q.lane0 + rank * 128 + 32 * quarter + lane;
+        const uint32_t from = tmem + (uint32_t)(buf * kXCols) + ((uint32_t)(32 * quarter) << 16);
+#pragma unroll 1
+        for (int32_t c = 0; c < q.cols; c += 32) {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld32(from + c, r);
+          if (KIND == kWeight) {
+            if (i >= g.lanes) continue;
+            uint16_t* to = g.out + (int64_t)q.e * g.stride + (int64_t)i * g.ld + q.col0 + c;
+            const int32_t n = q.cols - c;
+            if (q.depth == 0) {  // an expert without a row
+#pragma unroll
+              for (int x = 0; x < 32; ++x) r[x] = 0u;
+            }
+            if (n >= 32) {
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                uint32_t p[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                  p[h] = pack_bf16(__uint_as_float(r[8 * w + 2 * h]), __uint_as_float(r[8 * w + 2 * h + 1]));
+                *reinterpret_cast<uint4*>(to + 8 * w) = make_uint4(p[0], p[1], p[2], p[3]);
+              }
+            } else {
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                if (x < n) to[x] = bf16_rn(__uint_as_float(r[x]));
+            }
+          } else {
+            // Lane pairs trade columns: an even lane keeps column x and gets its
+            // neighbour's, an odd one column x + 1, so that each stores two
+            // adjacent elements of a row.
+            const bool odd = lane & 1;
+            const int32_t n = q.cols - c, i2 = i & ~1;
+            uint16_t* to = g.out + (int64_t)(q.col0 + c + (odd ? 1 : 0)) * g.ld + i2;
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+              const uint32_t give = odd ? r[x] : r[x + 1];
+              const uint32_t got = __shfl_xor_sync(~0u, give, 1);
+              const uint32_t p = odd ? pack_bf16(__uint_as_float(got), __uint_as_float(r[x + 1]))
+                                     : pack_bf16(__uint_as_float(r[x]), __uint_as_float(got));
+              if (x + (odd ? 1 : 0) < n) {
+                if (i2 + 1 < g.lanes)
+                  *reinterpret_cast<uint32_t*>(to + (int64_t)x * g.ld) = p;
+                else if (i2 < g.lanes)
+                  to[(int64_t)x * g.ld] = (uint16_t)p;
+              }
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(leader_tempty0 + 8u * buf);
+    }
+  } else {
+    // ---------------- mending (both CTAs): rows that are not the expert's
+    uint32_t it = 0, phases = 0;
+    int32_t e = 0;
+    for (int32_t t = cid; t < ntiles; t += ncid) {
+      const XTile q = tile_at<KIND>(g, table, t, e);
+      it += (uint32_t)((q.depth + kXDepth - 1) / kXDepth);
+      if ((q.depth & 15) == 0) continue;
+      const int s = (it - 1) % kXStages;
+      if (!__all_sync(~0u, mbar_wait(own_bar(s), phases >> s & 1u, err, stop))) {
+        if (lane == 0) halt_cluster();
+        break;
+      }
+      phases ^= 1u << s;
+      const int32_t from = q.depth & (kXDepth - 1), rows = 16 - (q.depth & 15);
+      const int boxes = 2 + q.width / 128;  // of 64 x 64: two of A, one or two of B
+      unsigned char* a = sm + s * kXStage;
+      for (int k = lane; k < boxes * rows * 8; k += 32) {
+        const int box = k / (rows * 8), w = k - box * (rows * 8);
+        *reinterpret_cast<uint4*>(a + box * 8192 + from * 128 + w * 16) = make_uint4(0, 0, 0, 0);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(leader_full0 + 8u * s);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_barrier();  // no CTA frees TMEM or leaves while the pair's products or copies may touch it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 2 * kXCols);
+  }
+}

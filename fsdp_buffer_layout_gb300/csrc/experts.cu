@@ -1,0 +1,229 @@
+// experts.cu — the products of rows sorted by expert with their experts' weights
+// and both gradients: arguments, tensor maps and launches of expert_gemm.cuh.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+#include <string>
+
+#include "objective.cuh"
+
+namespace vsf {
+namespace {
+
+using namespace obj;
+
+#include "mbarrier.cuh"
+#include "tcgen05.cuh"
+#include "expert_gemm.cuh"
+
+constexpr int64_t kMaxRows = int64_t(1) << 28;
+constexpr int64_t kMaxSide = int64_t(1) << 24;
+
+// An expert launch's arguments as the caller gives them: lhs are the rows' array
+// (kWeight: d_y), rhs the weights (kWeight: x).
+struct Product {
+  const char* who;
+  const int32_t* starts;
+  int64_t rows, E, N, K;
+  const uint16_t *rows_in, *other;
+  int64_t rows_ld, other_ld, other_stride;  // other_stride: of weights
+  uint16_t* out;
+  int64_t out_ld, out_stride;
+  unsigned* err;
+};
+
+bool tma_rows(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
+
+vsf_status check(int kind, const Product& a) {
+  const std::string w(a.who);
+  if (a.rows < 0 || a.rows > kMaxRows || a.E < 1 || a.E > kMaxGroups || a.N < 1 || a.N > kMaxSide ||
+      a.K < 1 || a.K > kMaxSide)
+    return fail(VSF_ERR_ARG, w + ": sizes out of range");
+  const int64_t in = kind == kForward ? a.K : a.N, to = kind == kForward ? a.N : a.K;
+  const int64_t most = int64_t(1) << 40;
+  if (a.rows_ld < in || a.rows_ld > most || a.other_ld < a.K || a.other_ld > most || a.out_ld < to ||
+      a.out_ld > most)
+    return fail(VSF_ERR_ARG, w + ": stride out of range");
+  if (a.starts == nullptr || a.err == nullptr ||
+      (a.rows > 0 && (a.rows_in == nullptr || a.other == nullptr || a.out == nullptr)) ||
+      (kind == kWeight && a.out == nullptr))
+    return fail(VSF_ERR_ARG, w + ": NULL pointer");
+  if (kind == kWeight ? a.E > 1 && (a.out_stride < (a.N - 1) * a.out_ld + a.K || a.out_stride > most)
+                      : a.E > 1 && (a.other_stride < (a.N - 1) * a.other_ld + a.K || a.other_stride > most))
+    return fail(VSF_ERR_ARG, w + ": experts' stride out of range");
+  if (!aligned(a.starts, 4) || !aligned(a.err, 4) || !tma_rows(a.rows_in, a.rows_ld) ||
+      !tma_rows(a.other, a.other_ld) || !tma_rows(a.out, a.out_ld) ||
+      (a.E > 1 && (kind == kWeight ? a.out_stride : a.other_stride) % 8 != 0))
+    return fail(VSF_ERR_ALIGN, w + ": rows have to start on 16-byte boundaries (strides of whole 8 elements)");
+  // what is written overlaps nothing that is read
+  auto end = [](const uint16_t* p, int64_t n, int64_t ld, int64_t width) {
+    return reinterpret_cast<uintptr_t>(p) + (uintptr_t)(n > 0 ? ((n - 1) * ld + width) * 2 : 0);
+  };
+  const uintptr_t o0 = reinterpret_cast<uintptr_t>(a.out);
+  const uintptr_t o1 = kind == kWeight ? end(a.out + (a.E - 1) * a.out_stride, a.N, a.out_ld, a.K)
+                                       : end(a.out, a.rows, a.out_ld, to);
+  const uintptr_t r0 = reinterpret_cast<uintptr_t>(a.rows_in), w0 = reinterpret_cast<uintptr_t>(a.other);
+  const uintptr_t r1 = end(a.rows_in, a.rows, a.rows_ld, in);
+  const uintptr_t w1 = kind == kWeight ? end(a.other, a.rows, a.other_ld, a.K)
+                                       : end(a.other + (a.E - 1) * a.other_stride, a.N, a.other_ld, a.K);
+  if ((o0 < r1 && r0 < o1) || (o0 < w1 && w0 < o1))
+    return fail(VSF_ERR_ARG, w + ": the output overlaps an input");
+  return VSF_OK;
+}
+
+// Tensor map over [batch, rows, width] (row stride ld, batch stride bs, in
+// elements), boxes of 64 elements x box_rows rows, 128-byte swizzle; copies
+// outside read zeros.
+vsf_status operand_map(CUtensorMap* map, const char* who, const uint16_t* p, int64_t width, int64_t rows,
+                       int64_t batch, int64_t ld, int64_t bs, int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = gemm_map_encoder();
+  if (encode == nullptr) return fail(VSF_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)batch};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)std::max(bs, ld) * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(p), dims,
+                            strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(VSF_ERR_CUDA, std::string(who) + ": cuTensorMapEncodeTiled failed (" +
+                                  std::to_string((int)r) + ")");
+  return VSF_OK;
+}
+
+// Pairs of CTAs that run at a time, looked up once a device and kind; 0 with *e
+// set where that fails.
+template <int KIND>
+int expert_pairs(cudaError_t* e) {
+  static std::mutex mu;
+  static int cached[64] = {};
+  int dev = 0;
+  if ((*e = cudaGetDevice(&dev)) != cudaSuccess) return 0;
+  if (dev < 0 || dev >= 64) {
+    *e = cudaErrorInvalidDevice;
+    return 0;
+  }
+  std::lock_guard<std::mutex> lock(mu);
+  if (cached[dev] == 0) {
+    auto fn = expert_gemm_kernel<KIND>;
+    *e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kXSmem);
+    if (*e != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * 64);
+    cfg.blockDim = dim3(kXThreads<KIND>);
+    cfg.dynamicSmemBytes = kXSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int got = 0;
+    *e = cudaOccupancyMaxActiveClusters(&got, fn, &cfg);
+    if (*e != cudaSuccess) return 0;
+    cached[dev] = std::max(1, got);
+  }
+  return cached[dev];
+}
+
+template <int KIND>
+vsf_status product(const Product& a, cudaStream_t st) {
+  const int64_t lanes = KIND == kInput ? a.K : a.N;
+  ExpertArgs g = {};
+  g.starts = a.starts;
+  g.E = (int32_t)a.E;
+  g.rows = (int32_t)a.rows;
+  g.lanes = (int32_t)lanes;
+  g.cols = (int32_t)a.K;
+  g.depth = (int32_t)(KIND == kForward ? a.K : a.N);
+  g.lane_tiles = (int32_t)((lanes + kXLanes - 1) / kXLanes);
+  g.col_tiles = (int32_t)((a.K + kXCols - 1) / kXCols);
+  g.out = a.out;
+  g.ld = a.out_ld;
+  g.stride = a.out_stride;
+  // (an upper bound: the rows' share among the experts is device memory)
+  const int64_t tiles = KIND == kWeight ? a.E * g.lane_tiles * g.col_tiles
+                                        : (a.rows / kXCols + std::min(a.E, a.rows)) * g.lane_tiles;
+  if (tiles > INT32_MAX / 2) return fail(VSF_ERR_ARG, std::string(a.who) + ": too many tiles");
+  CUtensorMap ma, mb, mb16;
+  vsf_status s;
+  if (KIND == kWeight) {
+    s = operand_map(&ma, a.who, a.rows_in, a.N, a.rows, 1, a.rows_ld, 0, 64);
+    if (s == VSF_OK) s = operand_map(&mb, a.who, a.other, a.K, a.rows, 1, a.other_ld, 0, 64);
+    mb16 = mb;
+  } else {
+    s = operand_map(&ma, a.who, a.other, a.K, a.N, a.E, a.other_ld, a.other_stride, KIND == kForward ? 128 : 64);
+    if (s == VSF_OK) s = operand_map(&mb, a.who, a.rows_in, g.depth, a.rows, 1, a.rows_ld, 0, 128);
+    if (s == VSF_OK) s = operand_map(&mb16, a.who, a.rows_in, g.depth, a.rows, 1, a.rows_ld, 0, 16);
+  }
+  if (s != VSF_OK) return s;
+  cudaError_t e = cudaSuccess;
+  const int pairs = expert_pairs<KIND>(&e);
+  if (pairs > 0)
+    e = launch_behind(expert_gemm_kernel<KIND>, (unsigned)(2 * std::min<int64_t>(pairs, tiles)),
+                      kXThreads<KIND>, kXSmem, 2, st, ma, mb, mb16, g, a.err);
+  return e == cudaSuccess ? VSF_OK : cuda_error(e, a.who);
+}
+
+// The weights' gradient where no expert has a row.
+__global__ void __launch_bounds__(256)
+    zero_weights_kernel(uint16_t* out, int64_t rows, int32_t N, int32_t K, int64_t ld, int64_t stride) {
+  take_turn();
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    uint16_t* to = out + r / N * stride + r % N * ld;
+    for (int32_t k = threadIdx.x; k < K; k += 256) to[k] = 0;
+  }
+}
+
+}  // namespace
+}  // namespace vsf
+
+using namespace vsf;
+
+extern "C" {
+
+vsf_status vsf_expert_product(const uint16_t* x, int64_t rows, int64_t K, int64_t x_ld, const uint16_t* w,
+                              int64_t E, int64_t N, int64_t w_ld, int64_t w_stride, const int32_t* starts,
+                              uint16_t* y, int64_t y_ld, unsigned* d_err, void* stream) {
+  vsf::Range nvtx_range("vsf_expert_product");
+  const Product a = {"vsf_expert_product", starts, rows, E, N, K, x, w, x_ld, w_ld, w_stride, y, y_ld, 0, d_err};
+  const vsf_status s = check(kForward, a);
+  if (s != VSF_OK || rows == 0) return s;
+  return product<kForward>(a, static_cast<cudaStream_t>(stream));
+}
+
+vsf_status vsf_expert_product_input_grad(const uint16_t* d_y, int64_t rows, int64_t N, int64_t d_y_ld,
+                                         const uint16_t* w, int64_t E, int64_t K, int64_t w_ld,
+                                         int64_t w_stride, const int32_t* starts, uint16_t* d_x,
+                                         int64_t d_x_ld, unsigned* d_err, void* stream) {
+  vsf::Range nvtx_range("vsf_expert_product_input_grad");
+  const Product a = {"vsf_expert_product_input_grad", starts, rows, E, N, K, d_y, w, d_y_ld, w_ld, w_stride,
+                     d_x, d_x_ld, 0, d_err};
+  const vsf_status s = check(kInput, a);
+  if (s != VSF_OK || rows == 0) return s;
+  return product<kInput>(a, static_cast<cudaStream_t>(stream));
+}
+
+vsf_status vsf_expert_product_weight_grad(const uint16_t* d_y, int64_t rows, int64_t N, int64_t d_y_ld,
+                                          const uint16_t* x, int64_t K, int64_t x_ld, int64_t E,
+                                          const int32_t* starts, uint16_t* d_w, int64_t d_w_ld,
+                                          int64_t d_w_stride, unsigned* d_err, void* stream) {
+  vsf::Range nvtx_range("vsf_expert_product_weight_grad");
+  const Product a = {"vsf_expert_product_weight_grad", starts, rows, E, N, K, d_y, x, d_y_ld, x_ld, 0, d_w,
+                     d_w_ld, d_w_stride, d_err};
+  const vsf_status s = check(kWeight, a);
+  if (s != VSF_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows > 0) return product<kWeight>(a, st);
+  const int64_t n = E * N;
+  const cudaError_t e = launch_behind(zero_weights_kernel, (unsigned)std::min<int64_t>(n, kSms * 8), 256, 0, 1,
+                                      st, d_w, n, (int32_t)N, (int32_t)K, d_w_ld, d_w_stride);
+  return e == cudaSuccess ? VSF_OK : cuda_error(e, a.who);
+}
+
+}  // extern "C"

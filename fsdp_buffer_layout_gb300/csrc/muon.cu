@@ -51,6 +51,7 @@ constexpr int kMaxChunk = 192;                    // matrices in one batched chu
 constexpr int64_t kChunkElems = int64_t(1) << 28;  // bf16 elements of X per chunk (512 MB)
 
 #include "mbarrier.cuh"
+#include "tcgen05.cuh"
 #include "ns_gemm.cuh"
 
 // Packed-buffer offset of every matrix of one chunk (kernel parameter).
@@ -378,21 +379,6 @@ void muon_lanes_free(void* p) {
     if (ml->stream[l]) cudaStreamDestroy(ml->stream[l]);
   }
   delete ml;
-}
-
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no link
-// against libcuda).
-PFN_cuTensorMapEncodeTiled_v12000 gemm_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
-  return fn;
 }
 
 // Tensor map of one GEMM operand over a strided batch of row-major bf16

@@ -190,6 +190,26 @@ def lib():
             L.vsf_route_grad.restype = st
             L.vsf_route_grad.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64,
                                          P(vsf_route_hparams), vp, vp, vp, vp, f32, vp, i64, vp]
+            L.vsf_expert_sort_workspace_bytes.restype = sz
+            L.vsf_expert_sort_workspace_bytes.argtypes = [i64, i64, i64]
+            L.vsf_expert_sort.restype = st
+            L.vsf_expert_sort.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, sz, vp]
+            L.vsf_expert_gather.restype = st
+            L.vsf_expert_gather.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i64, vp]
+            L.vsf_expert_combine.restype = st
+            L.vsf_expert_combine.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, vp, i64, vp]
+            L.vsf_expert_combine_grad.restype = st
+            L.vsf_expert_combine_grad.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, i64, vp,
+                                                  i64, vp, vp]
+            L.vsf_expert_product.restype = st
+            L.vsf_expert_product.argtypes = [vp, i64, i64, i64, vp, i64, i64, i64, i64, vp, vp, i64,
+                                             vp, vp]
+            L.vsf_expert_product_input_grad.restype = st
+            L.vsf_expert_product_input_grad.argtypes = [vp, i64, i64, i64, vp, i64, i64, i64, i64,
+                                                        vp, vp, i64, vp, vp]
+            L.vsf_expert_product_weight_grad.restype = st
+            L.vsf_expert_product_weight_grad.argtypes = [vp, i64, i64, i64, vp, i64, i64, i64, vp,
+                                                         vp, i64, i64, vp, vp]
             L.vsf_status_string.restype = ctypes.c_char_p
             L.vsf_status_string.argtypes = [st]
             L.vsf_last_error.restype = ctypes.c_char_p
@@ -471,6 +491,52 @@ def vsf_route_grad(logits, dtype: int, T: int, E: int, ld: int, live, seq_starts
     _check(lib().vsf_route_grad(logits, dtype, T, E, ld, live, seq_starts, sequences,
                                 ctypes.byref(hp), idx, d_gates, seq_counts, seq_coef, loss_scale,
                                 grad, grad_ld, stream))
+
+
+def vsf_expert_sort_workspace_bytes(tokens: int, top_k: int, experts: int) -> int:
+    return int(lib().vsf_expert_sort_workspace_bytes(tokens, top_k, experts))
+
+
+def vsf_expert_sort(idx, T: int, top_k: int, E: int, starts, source, place, d_workspace,
+                    ws_bytes: int, stream: int) -> None:
+    _check(lib().vsf_expert_sort(idx, T, top_k, E, starts, source, place, d_workspace, ws_bytes,
+                                 stream))
+
+
+def vsf_expert_gather(x, dtype: int, T: int, H: int, ld: int, place, top_k: int, rows,
+                      rows_ld: int, stream: int) -> None:
+    _check(lib().vsf_expert_gather(x, dtype, T, H, ld, place, top_k, rows, rows_ld, stream))
+
+
+def vsf_expert_combine(y, dtype: int, T: int, H: int, y_ld: int, place, gates, top_k: int, out,
+                       out_ld: int, stream: int) -> None:
+    _check(lib().vsf_expert_combine(y, dtype, T, H, y_ld, place, gates, top_k, out, out_ld, stream))
+
+
+def vsf_expert_combine_grad(d_out, dtype: int, T: int, H: int, d_out_ld: int, y, y_ld: int, place,
+                            gates, top_k: int, d_y, d_y_ld: int, d_gates, stream: int) -> None:
+    _check(lib().vsf_expert_combine_grad(d_out, dtype, T, H, d_out_ld, y, y_ld, place, gates, top_k,
+                                         d_y, d_y_ld, d_gates, stream))
+
+
+def vsf_expert_product(x, rows: int, K: int, x_ld: int, w, E: int, N: int, w_ld: int, w_stride: int,
+                       starts, y, y_ld: int, d_err, stream: int) -> None:
+    _check(lib().vsf_expert_product(x, rows, K, x_ld, w, E, N, w_ld, w_stride, starts, y, y_ld,
+                                    d_err, stream))
+
+
+def vsf_expert_product_input_grad(d_y, rows: int, N: int, d_y_ld: int, w, E: int, K: int, w_ld: int,
+                                  w_stride: int, starts, d_x, d_x_ld: int, d_err,
+                                  stream: int) -> None:
+    _check(lib().vsf_expert_product_input_grad(d_y, rows, N, d_y_ld, w, E, K, w_ld, w_stride, starts,
+                                               d_x, d_x_ld, d_err, stream))
+
+
+def vsf_expert_product_weight_grad(d_y, rows: int, N: int, d_y_ld: int, x, K: int, x_ld: int, E: int,
+                                   starts, d_w, d_w_ld: int, d_w_stride: int, d_err,
+                                   stream: int) -> None:
+    _check(lib().vsf_expert_product_weight_grad(d_y, rows, N, d_y_ld, x, K, x_ld, E, starts, d_w,
+                                                d_w_ld, d_w_stride, d_err, stream))
 
 
 def vsf_status_string(status: int) -> str:

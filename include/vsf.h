@@ -599,6 +599,80 @@ vsf_status vsf_route_grad(const void* logits, int32_t dtype, int64_t T, int64_t 
                           const int32_t* seq_counts, const float* seq_coef, float loss_scale,
                           void* grad, int64_t grad_ld, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A mixture-of-experts layer between vsf_route and the losses: tokens sorted by
+ * expert, their rows in that order, the experts' products, and the outputs
+ * combined with the gates; each with its gradient.
+ *
+ * Common to the calls below: choice c = t*top_k + j is the j-th expert of token t
+ * (idx as vsf_route writes it: int32[T*top_k], anything outside [0, E) is no
+ * choice). "Rows" are arrays of T*top_k rows, of which the first starts[E] hold a
+ * choice each; the others are neither read nor written. T <= 2^23, top_k <= 32,
+ * E <= 512. Strides (ld) count elements; offsets are 64-bit. Sums are fp32 in a
+ * fixed order, rounded once to the output's type: equal inputs give equal bits.
+ * Errors: VSF_ERR_ARG (NULL, sizes or strides out of range, a workspace too
+ * small, an output that overlaps an input), VSF_ERR_ALIGN, VSF_ERR_CUDA; all but
+ * the last are found before the first launch. T = 0 (rows = 0) is no error. */
+
+/* Stable sort of the choices by expert. starts: int32[E+1], expert e's rows are
+ * [starts[e], starts[e+1]); place: int32[T*top_k], the row of each choice, -1 for
+ * none; source: int32[T*top_k] or NULL, the choice of each row, -1 behind the
+ * last one. Within an expert the rows are in the choices' order. d_workspace: 16
+ * byte aligned, needs no preparation; calls that share it must be ordered. */
+size_t vsf_expert_sort_workspace_bytes(int64_t tokens, int64_t top_k, int64_t experts);
+vsf_status vsf_expert_sort(const int32_t* idx, int64_t T, int64_t top_k, int64_t E, int32_t* starts,
+                           int32_t* source, int32_t* place, void* d_workspace, size_t ws_bytes,
+                           void* stream);
+
+/* rows[place[t*top_k + j]] = x[t]. x: T rows of H elements (dtype VSF_BF16 or
+ * VSF_FP32). Pointers need the alignment of their type only; where all rows
+ * start on 16-byte boundaries they go in wide pieces (as below). Its gradient is
+ * vsf_expert_combine without gates. H <= 2^24. */
+vsf_status vsf_expert_gather(const void* x, int32_t dtype, int64_t T, int64_t H, int64_t ld,
+                             const int32_t* place, int64_t top_k, void* rows, int64_t rows_ld,
+                             void* stream);
+
+/* out[t] = sum_j gates[t*top_k + j] * y[place[t*top_k + j]]; without a choice 0.
+ * gates: fp32[T*top_k], or NULL for the plain sum. */
+vsf_status vsf_expert_combine(const void* y, int32_t dtype, int64_t T, int64_t H, int64_t y_ld,
+                              const int32_t* place, const float* gates, int64_t top_k, void* out,
+                              int64_t out_ld, void* stream);
+
+/* The gradient of vsf_expert_combine: d_y[place[c]] = gates[c] * d_out[c / top_k],
+ * d_gates[c] = <d_out[c / top_k], y[place[c]]> (0 where c is no choice). d_y may
+ * be y itself (same stride). */
+vsf_status vsf_expert_combine_grad(const void* d_out, int32_t dtype, int64_t T, int64_t H,
+                                   int64_t d_out_ld, const void* y, int64_t y_ld,
+                                   const int32_t* place, const float* gates, int64_t top_k,
+                                   void* d_y, int64_t d_y_ld, float* d_gates, void* stream);
+
+/* The experts' products over sorted rows, bf16 with fp32 accumulation:
+ *   vsf_expert_product:             y[r]  = x[r] W[e]^T
+ *   vsf_expert_product_input_grad:  d_x[r] = d_y[r] W[e]
+ *   vsf_expert_product_weight_grad: d_W[e] = sum_r d_y[r] x[r]^T  (0 without a row)
+ * for r in [starts[e], starts[e+1]), e < E. x, d_x: rows of K elements; y, d_y:
+ * rows of N; W, d_W: E matrices of N rows of K, w_stride elements apart. starts:
+ * device int32[E+1], not decreasing (clamped to the rows and to what precedes).
+ * Rows behind starts[E] are neither read into a result nor written. Every array's
+ * rows start on 16-byte boundaries: pointers aligned to 16 bytes, strides
+ * multiples of 8 elements (VSF_ERR_ALIGN); N and K may be anything up to 2^24.
+ * rows <= 2^28. d_err: a device word in which a bounded wait that runs out sets
+ * bit 1 (value 2; results are then not to be trusted). */
+vsf_status vsf_expert_product(const uint16_t* x, int64_t rows, int64_t K, int64_t x_ld,
+                              const uint16_t* w, int64_t E, int64_t N, int64_t w_ld,
+                              int64_t w_stride, const int32_t* starts, uint16_t* y, int64_t y_ld,
+                              unsigned* d_err, void* stream);
+vsf_status vsf_expert_product_input_grad(const uint16_t* d_y, int64_t rows, int64_t N,
+                                         int64_t d_y_ld, const uint16_t* w, int64_t E, int64_t K,
+                                         int64_t w_ld, int64_t w_stride, const int32_t* starts,
+                                         uint16_t* d_x, int64_t d_x_ld, unsigned* d_err,
+                                         void* stream);
+vsf_status vsf_expert_product_weight_grad(const uint16_t* d_y, int64_t rows, int64_t N,
+                                          int64_t d_y_ld, const uint16_t* x, int64_t K,
+                                          int64_t x_ld, int64_t E, const int32_t* starts,
+                                          uint16_t* d_w, int64_t d_w_ld, int64_t d_w_stride,
+                                          unsigned* d_err, void* stream);
+
 const char* vsf_status_string(vsf_status s);
 const char* vsf_last_error(void);
 

@@ -1,0 +1,386 @@
+"""Tokens by expert and the experts' products on the GPU against the 64-bit reference.
+
+Tolerances. The sort and the rows' copy are exact. A sum of n fp32 products, added
+in any order, is within n 2^-24 of the sum of their absolute values (n 2^-23 for the
+tensor cores, whose additions may cut off instead of rounding); the rounding to
+the output's type adds half a step, 2^-8 of the value for bf16 and 2^-24 for fp32.
+"""
+import numpy as np
+import pytest
+import torch
+
+import expert_reference as R
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP32 = torch.bfloat16, torch.float32
+HALF = {BF16: 2.0**-8, FP32: 2.0**-24}
+
+
+def host(x):
+    return x.double().cpu().numpy()
+
+
+def strided(rows, width, pad, shift, dtype, rng, scale=1.0):
+    """A matrix in rows of width + pad elements, `shift` elements into its memory."""
+    ld = width + pad
+    buf = torch.zeros(shift + max(rows, 1) * ld, dtype=dtype, device="cuda")
+    x = torch.as_strided(buf, (rows, width), (ld, 1), shift)
+    x.copy_(torch.from_numpy((rng.normal(size=(rows, width)) * scale).astype(np.float32)))
+    return x
+
+
+def choices(rng, tokens, experts, k, masked):
+    idx = rng.integers(0, experts, size=(tokens, k)).astype(np.int32)
+    if masked:
+        idx[rng.random((tokens, k)) < 0.2] = -1
+        idx[rng.random(tokens) < 0.2] = -1
+        idx[rng.random((tokens, k)) < 0.02] = experts + 5  # no expert of this layer
+    return torch.from_numpy(idx).cuda()
+
+
+DISPATCH = [  # tokens, experts, k, width, dtype, masked, pad, shift
+    (0, 3, 2, 16, BF16, False, 0, 0),
+    (1, 1, 1, 1, BF16, False, 0, 0),
+    (1, 8, 3, 64, FP32, False, 0, 0),
+    (7, 5, 2, 8, BF16, True, 0, 0),
+    (8, 32, 4, 2880, BF16, False, 0, 0),
+    (33, 6, 5, 257, BF16, True, 0, 0),
+    (33, 6, 6, 257, FP32, True, 2, 1),
+    (40, 4, 2, 1030, BF16, True, 2, 8),    # aligned rows with a tail
+    (100, 512, 8, 130, FP32, True, 2, 4),
+    (65, 3, 32, 96, BF16, True, 0, 3),     # rows off the 16-byte boundaries
+    (300, 7, 7, 40, FP32, True, 1, 0),
+]
+
+
+@pytest.mark.parametrize("case", DISPATCH, ids=str)
+def test_dispatch(case):
+    from fsdp_buffer_layout_gb300.experts import Dispatch
+    tokens, experts, k, width, dtype, masked, pad, shift = case
+    rng = np.random.default_rng(hash(case[:4]) % 1000 + 1)
+    idx = choices(rng, tokens, experts, k, masked)
+    x, d_out = (strided(tokens, width, pad, shift, dtype, rng) for _ in range(2))
+    y, d_rows = (strided(tokens * k, width, pad, shift, dtype, rng) for _ in range(2))
+    gates = torch.from_numpy(rng.normal(size=(tokens, k)).astype(np.float32)).cuda()
+    call = Dispatch(tokens, experts, k, width, dtype=dtype)
+    want_starts, want_source, want_place = R.sort(host(idx).astype(np.int64).reshape(tokens, k), experts)
+    starts, source, place = call.sort(idx)
+    assert np.array_equal(host(starts), want_starts)
+    assert np.array_equal(host(source), want_source)
+    assert np.array_equal(host(place).reshape(tokens, k), want_place)
+    # garbage behind the last row must not matter, nor what no choice took
+    n = int(want_starts[-1])
+    y[n:] = float("nan")
+    d_rows[n:] = float("nan")
+    gates[torch.from_numpy(want_place < 0).cuda()] = float("nan")
+    rows = call.gather(x)
+    assert torch.equal(rows.cpu(), torch.from_numpy(
+        R.gather(host(x), want_place, np.zeros((tokens * k, width)))).to(dtype))
+
+    def check(got, want, size, terms):
+        got = host(got)
+        bound = HALF[dtype] * np.abs(want) + 1.01 * terms * 2.0**-24 * size + 1e-38
+        assert got.shape == want.shape and np.isfinite(got).all()
+        assert (np.abs(got - want) <= bound).all(), np.max(np.abs(got - want) / bound)
+
+    g0, p = np.nan_to_num(host(gates)), want_place
+    y0 = np.nan_to_num(host(y))
+    check(call.combine(y, gates), R.combine(y0, p, g0), R.combine(np.abs(y0), p, np.abs(g0)), k + 1)
+    dr = np.nan_to_num(host(d_rows))
+    one = np.ones((tokens, k))
+    check(call.gather_backward(d_rows), R.combine(dr, p, one), R.combine(np.abs(dr), p, one), k)
+    d_y, d_gates = call.combine_backward(d_out, y, gates)
+    zero = np.zeros((tokens * k, width))
+    want_dy, want_dg = R.combine_grad(host(d_out), y0, p, g0, zero)
+    check(d_y, want_dy, np.abs(want_dy), 2)
+    size = R.combine_grad(np.abs(host(d_out)), np.abs(y0), p, g0, zero)[1]
+    off = np.abs(host(d_gates).reshape(tokens, k) - want_dg)
+    assert (off <= 1.01 * (width / 32 + 48) * 2.0**-24 * size + 1e-38).all()
+    # the same again, and into y itself
+    again = y.clone(memory_format=torch.preserve_format) if pad == 0 and shift == 0 else None
+    if again is not None and tokens:
+        got = call.combine_backward(d_out, again, gates, d_y=again)[0]
+        assert torch.equal(got[:n], d_y[:n]) and torch.isnan(got[n:]).all()
+
+
+@pytest.mark.parametrize("tokens,experts,k,live", [
+    (1025, 8, 8, 1.0), (4096, 3, 2, 0.5), (8193, 1, 1, 1.0), (20000, 512, 8, 0.9), (70001, 33, 3, 0.97),
+    (300000, 256, 5, 1.0)])
+def test_sort_of_many(tokens, experts, k, live):
+    """Against torch's stable sort of whole numbers; more than one run, and more
+    choices a run than the least."""
+    from fsdp_buffer_layout_gb300.experts import Dispatch
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    idx = (torch.rand(tokens, k, device="cuda", generator=g) ** 2 * experts).int().clamp(max=experts - 1)
+    idx[torch.rand(tokens, device="cuda", generator=g) >= live] = -1
+    call = Dispatch(tokens, experts, k, 8, with_grad=False)
+    for _ in range(2):
+        starts, source, place = call.sort(idx)
+        flat = idx.flatten().long()
+        key = torch.where(flat < 0, experts, flat)
+        order = torch.sort(key, stable=True).indices
+        counts = torch.bincount(key, minlength=experts + 1)[:experts]
+        n = int(counts.sum())
+        assert torch.equal(starts[1:].long(), counts.cumsum(0)) and int(starts[0]) == 0
+        assert torch.equal(source[:n].long(), order[:n]) and bool((source[n:] == -1).all())
+        want = torch.full_like(flat, -1)
+        want[order[:n]] = torch.arange(n, device="cuda")
+        assert torch.equal(place.flatten().long(), want)
+        idx = idx.flip(0).contiguous()
+
+
+@pytest.mark.parametrize("dtype,width", [(BF16, 2048), (FP32, 999)])
+def test_many_rows(dtype, width):
+    """More rows than warps run at a time, in both directions."""
+    from fsdp_buffer_layout_gb300.experts import Dispatch
+    g = torch.Generator(device="cuda").manual_seed(5)
+    tokens, experts, k = 4099, 64, 6
+    idx = torch.randint(-1, experts, (tokens, k), device="cuda", generator=g).int()
+    call = Dispatch(tokens, experts, k, width, dtype=dtype)
+    starts, source, place = call.sort(idx)
+    n = int(starts[-1])
+    x, d_out = (torch.randn(tokens, width, device="cuda", generator=g).to(dtype) for _ in range(2))
+    y = torch.randn(tokens * k, width, device="cuda", generator=g).to(dtype)
+    gates = torch.rand(tokens, k, device="cuda", generator=g)
+    rows = call.gather(x)
+    assert torch.equal(rows[:n], x[source[:n].long() // k]) and not rows[n:].any()
+    taken = torch.where((place >= 0)[:, :, None], y[place.long().clamp(min=0)].double(), 0.0)
+    want = (taken * gates.double()[:, :, None]).sum(1)
+    size = (taken.abs() * gates.double()[:, :, None]).sum(1)
+    off = (call.combine(y, gates).double() - want).abs()
+    assert bool((off <= HALF[dtype] * want.abs() + 8 * 2.0**-24 * size).all())
+    d_y, d_gates = call.combine_backward(d_out, y, gates)
+    want = gates.flatten()[source[:n].long()].double()[:, None] * d_out[source[:n].long() // k].double()
+    assert bool(((d_y[:n].double() - want).abs() <= (HALF[dtype] + 2.0**-23) * want.abs()).all())
+    assert not d_y[n:].any()
+    want = (taken * d_out.double()[:, None]).sum(2)
+    size = (taken * d_out.double()[:, None]).abs().sum(2)
+    assert bool(((d_gates.double() - want).abs() <= (width / 32 + 48) * 2.0**-24 * size).all())
+
+
+# ------------------------------------------------------------------ products
+PRODUCTS = [  # rows of each expert, rows behind, out, in, pads
+    ([1], 0, 1, 1, 0),
+    ([3], 0, 8, 16, 0),
+    ([16], 0, 64, 64, 0),
+    ([0, 5, 0], 3, 32, 24, 0),
+    ([17, 1, 0, 40], 2, 130, 70, 8),
+    ([32, 31, 33, 64, 15], 0, 256, 128, 0),
+    ([255, 256, 257], 5, 96, 200, 0),
+    ([1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15, 16], 1, 300, 65, 16),
+    ([700, 0, 129, 513], 100, 521, 333, 0),
+    ([64] * 40 + [0] * 3 + [65], 0, 257, 129, 0),   # many tiles of one stage
+    ([1000], 24, 1000, 520, 0),
+    ([90, 300, 10], 0, 2880, 576, 0),
+]
+
+
+def product_inputs(counts, behind, n, k, pad, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed + 7 * n + k)
+    rows, experts = sum(counts) + behind, len(counts)
+
+    def made(*shape):
+        wide = -(-shape[-1] // 8) * 8 + pad
+        return torch.randn(*shape[:-1], wide, device="cuda", generator=g).bfloat16()[..., :shape[-1]]
+
+    starts = torch.tensor(np.cumsum([0] + counts), dtype=torch.int32, device="cuda")
+    return starts, made(rows, k), made(experts, n, k), made(rows, n)
+
+
+def product_bound(want, size, terms):
+    return HALF[BF16] * want.abs() + 1.01 * terms * 2.0**-23 * size + 1e-38
+
+
+def check_products(call, starts, x, w, d_y):
+    """All three products of every expert against 64 bits; rows behind untouched."""
+    cuts = starts.tolist()
+    y, d_x = call.forward(x, w, starts), call.backward_input(d_y, w, starts)
+    d_w = call.backward_weight(d_y, x, starts)
+    n, k = w.shape[1:]
+    for e, (a, b) in enumerate(zip(cuts, cuts[1:])):
+        xe, we, de = x[a:b].double(), w[e].double(), d_y[a:b].double()
+        for got, p, q, terms in ((y[a:b], xe, we.t(), k), (d_x[a:b], de, we, n),
+                                 (d_w[e], de.t(), xe, b - a)):
+            want, size = p @ q, p.abs() @ q.abs()
+            off = (got.double() - want).abs()
+            assert bool((off <= product_bound(want, size, terms)).all()), (e, float(off.max()))
+    assert not y[cuts[-1]:].any() and not d_x[cuts[-1]:].any()
+    assert call.device_error() == 0
+
+
+@pytest.mark.parametrize("case", PRODUCTS, ids=str)
+def test_products(case):
+    from fsdp_buffer_layout_gb300.experts import ExpertLinear
+    counts, behind, n, k, pad = case
+    starts, x, w, d_y = product_inputs(*case)
+    call = ExpertLinear(x.shape[0], len(counts), n, k)
+    # rows behind the last one, and the weights of experts without a row, are not read
+    x[starts[-1]:] = float("nan")
+    d_y[starts[-1]:] = float("nan")
+    cuts = starts.tolist()
+    call.d_weight.fill_(float("nan"))
+    check_products(call, starts, x, w, d_y)
+    for e, c in enumerate(counts):
+        if c == 0:
+            w[e] = float("nan")
+    y = call.forward(x, w, starts)
+    assert not y[cuts[-1]:].any() and bool(torch.isfinite(y).all())
+
+
+def test_an_experts_rows_stay_its_own():
+    """NaN and infinities in one expert's rows reach no other expert."""
+    from fsdp_buffer_layout_gb300.experts import ExpertLinear
+    counts = [5, 21, 64, 130, 7]
+    starts, x, w, d_y = product_inputs(counts, 0, 200, 136, 0)
+    cuts = starts.tolist()
+    call = ExpertLinear(x.shape[0], 5, 200, 136)
+    for bad in (1, 3):
+        x[cuts[bad]:cuts[bad + 1]] = float("nan")
+        d_y[cuts[bad]:cuts[bad + 1]] = float("inf")
+    y, d_x = call.forward(x, w, starts), call.backward_input(d_y, w, starts)
+    d_w = call.backward_weight(d_y, x, starts)
+    for e in range(5):
+        finite = e not in (1, 3)
+        for part in (y[cuts[e]:cuts[e + 1]], d_x[cuts[e]:cuts[e + 1]], d_w[e]):
+            assert bool(torch.isfinite(part).all()) == finite, e
+    assert call.device_error() == 0
+
+
+def test_products_without_rows():
+    from fsdp_buffer_layout_gb300.experts import ExpertLinear
+    starts = torch.zeros(4, dtype=torch.int32, device="cuda")
+    call = ExpertLinear(50, 3, 40, 24)
+    w = torch.randn(3, 40, 24, device="cuda").bfloat16()
+    for rows in (0, 50):  # none in the arrays, none of any expert
+        x = torch.randn(rows, 24, device="cuda").bfloat16()
+        d_y = torch.randn(rows, 40, device="cuda").bfloat16()
+        call.d_weight.fill_(3.0)
+        assert call.forward(x, w, starts).shape == (rows, 40)
+        assert not call.backward_input(d_y, w, starts).any() and not call.y.any()
+        assert not call.backward_weight(d_y, x, starts).any()
+
+
+def test_starts_out_of_range():
+    """What starts holds is device memory: whatever it is, no access leaves the
+    arrays. Clamped to [0, rows] and to what precedes."""
+    from fsdp_buffer_layout_gb300.experts import ExpertLinear
+    rows, n, k = 70, 48, 40
+    _, x, w, d_y = product_inputs([rows, 0, 0], 0, n, k, 0)
+    call = ExpertLinear(rows, 3, n, k)
+    bad = torch.tensor([-5, 20, 10, 1 << 30], dtype=torch.int32, device="cuda")
+    good = torch.tensor([0, 20, 20, rows], dtype=torch.int32, device="cuda")
+    for run in (lambda s: call.forward(x, w, s), lambda s: call.backward_input(d_y, w, s),
+                lambda s: call.backward_weight(d_y, x, s)):
+        a = run(bad).clone()
+        assert torch.equal(a, run(good))
+    assert call.device_error() == 0
+
+
+def test_products_on_streams_and_in_graphs():
+    """Two objects at once on two streams, and a captured call replayed on new
+    inputs, give the bits of calls one after the other."""
+    from fsdp_buffer_layout_gb300.experts import Dispatch, ExpertLinear
+    tokens, experts, k, h, f = 300, 9, 3, 256, 320
+    g = torch.Generator(device="cuda").manual_seed(11)
+    w = torch.randn(experts, f, h, device="cuda", generator=g).bfloat16()
+
+    def inputs():
+        return (torch.randint(-1, experts, (tokens, k), device="cuda", generator=g).int(),
+                torch.randn(tokens, h, device="cuda", generator=g).bfloat16(),
+                torch.rand(tokens, k, device="cuda", generator=g))
+
+    def made(stream=None):
+        return (Dispatch(tokens, experts, k, h, stream=stream),
+                ExpertLinear(tokens * k, experts, f, h, stream=stream))
+
+    def run(calls, idx, x, gates):
+        to, layer = calls
+        starts, _, _ = to.sort(idx)
+        rows = to.gather(x)
+        y = layer.forward(rows, w, starts)
+        d_rows = layer.backward_input(y, w, starts)
+        d_w = layer.backward_weight(y, rows, starts)
+        return (to.combine(d_rows, gates), *to.combine_backward(x, d_rows, gates), d_w,
+                to.gather_backward(d_rows))
+
+    sets = [inputs() for _ in range(3)]
+    # (an object each: rows behind the last one keep what another call left there)
+    plain = [made() for _ in sets]
+    want = [run(p, *s) for p, s in zip(plain, sets)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    pairs = [made(s) for s in streams]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = [run(p, *s) for p, s in zip(pairs, sets)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            for p, q in zip(a, b):
+                assert torch.equal(p, q)
+    fixed = [t.clone() for t in sets[0]]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    calls = made(stream)
+    with torch.cuda.stream(stream):
+        run(calls, *fixed)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            out = run(calls, *fixed)
+    for s, b in zip(sets, want):
+        for t, v in zip(fixed, s):
+            t.copy_(v)
+        calls[0].d_y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for p, q in zip(out, b):
+            assert torch.equal(p, q)
+    assert all(layer.device_error() == 0 for _, layer in pairs + [calls] + plain)
+
+
+def test_objects_refuse():
+    from fsdp_buffer_layout_gb300.experts import Dispatch, ExpertLinear
+    call = Dispatch(8, 4, 2, 32)
+    x, y = torch.zeros(8, 32, device="cuda", dtype=BF16), torch.zeros(16, 32, device="cuda", dtype=BF16)
+    gates = torch.zeros(8, 2, device="cuda")
+    with pytest.raises(ValueError, match="sort first"):
+        call.gather(x)
+    idx = torch.zeros(8, 2, dtype=torch.int32, device="cuda")
+    for bad in (idx.long(), idx[:, :1], idx.cpu(), torch.zeros(9, 2, dtype=torch.int32, device="cuda"),
+                torch.zeros(2, 8, dtype=torch.int32, device="cuda").t()):
+        with pytest.raises(ValueError, match="idx"):
+            call.sort(bad)
+    call.sort(idx)
+    first = call.calls
+    for bad in (x.float(), x[:4], x[:, :16], x.cpu(), x.t().contiguous().t()):
+        with pytest.raises(ValueError, match="x:"):
+            call.gather(bad)
+    with pytest.raises(ValueError, match="gates"):
+        call.combine(y, gates.double())
+    with pytest.raises(ValueError, match="gates"):
+        call.combine_backward(x, y, None)
+    with pytest.raises(ValueError, match="y:"):
+        call.combine(x, gates)
+    call.sort(idx[:4].contiguous())
+    with pytest.raises(ValueError, match="has followed"):
+        call.gather_backward(y[:8], call=first)
+    bare = Dispatch(8, 4, 2, 32, with_grad=False)
+    bare.sort(idx)
+    with pytest.raises(ValueError, match="with_grad"):
+        bare.gather_backward(y)
+    assert bare.gather_backward(y, out=x) is x
+    for bad in ((-1, 4, 2, 32), (8, 0, 2, 32), (8, 513, 2, 32), (8, 4, 33, 32), (8, 4, 2, 0)):
+        with pytest.raises(ValueError, match="out of range"):
+            Dispatch(*bad)
+    layer = ExpertLinear(16, 4, 24, 32)
+    w = torch.zeros(4, 24, 32, device="cuda", dtype=BF16)
+    starts = torch.zeros(5, dtype=torch.int32, device="cuda")
+    for args, what in (((y, w.float(), starts), "weight"), ((y, w[:3], starts), "weight"),
+                       ((y, w, starts[:4]), "starts"), ((y, w, starts.long()), "starts"),
+                       ((y[:, :16], w, starts), "x"),
+                       ((torch.zeros(17, 32, device="cuda", dtype=BF16), w, starts), "x")):
+        with pytest.raises(ValueError, match=what):
+            layer.forward(*args)
+    odd = torch.zeros(4, 24, 33, device="cuda", dtype=BF16)[:, :, :32]
+    from fsdp_buffer_layout_gb300 import vsf as V
+    with pytest.raises(V.VsfError, match="16-byte"):
+        layer.forward(y, odd, starts)
