@@ -355,6 +355,7 @@ __global__ void __launch_bounds__(kPairThreads)
 #include "mbarrier.cuh"
 #include "row_pipe.cuh"
 #include "row_regs.cuh"
+#include "row_scores.cuh"
 
 // ------------------------------------------------------------- host side
 struct RowsArg {
@@ -609,6 +610,78 @@ cudaError_t preference(const RowsArg& a, const PairIn& p, float* stats, float* l
   return launch_grad(r, w, grad, grad_ld, st);
 }
 
+// How rows of V words are cut for `tokens` of them. Pieces of 16 spans, fewer
+// where the warps would not all get one; groups as few as the second launch holds.
+template <typename T>
+ScoreCut score_cut(int64_t tokens, int64_t V) {
+  ScoreCut c = {};
+  c.spans = (int32_t)std::max<int64_t>(1, (V / Vec<T>::n + 31) / 32);
+  while (((c.spans - 1) >> c.group) + 1 + 2 > kMaxGroupsRow) ++c.group;
+  c.piece = 2;
+  const int64_t warps = kSms * kScoreCtas * (kScoreThreads / 32);
+  while (c.piece < 4 && tokens * c.spans > (warps << (c.piece + 1))) ++c.piece;
+  c.piece = std::max(c.piece, c.group);
+  c.pieces = ((c.spans - 1) >> c.piece) + 1;
+  c.groups = ((c.spans - 1) >> c.group) + 1 + 2;
+  return c;
+}
+
+// Workspace: the head, then per token and piece {m, s, u}, then per token the
+// groups' keys. Sized for the smallest pieces, which fewer tokens would get.
+struct ScoreWs {
+  static size_t bytes(int64_t tokens, int64_t V, int32_t dtype, int64_t K) {
+    const ScoreCut c = dtype == VSF_BF16 ? score_cut<uint16_t>(0, V) : score_cut<float>(0, V);
+    return sizeof(WsHead) + (size_t)tokens * c.pieces * 16 +
+           (K > 0 ? ((size_t)tokens * c.groups * 4 + 15) / 16 * 16 : 0);
+  }
+};
+
+unsigned score_grid(int64_t items) {
+  const int64_t warps = kScoreThreads / 32;
+  return (unsigned)std::min<int64_t>((items + warps - 1) / warps, kSms * kScoreCtas);
+}
+
+template <typename T>
+cudaError_t scores(const RowsArg& a, int32_t K, float* logp, float* entropy, int32_t* top_idx,
+                   float* top_logp, float* norm, void* ws, cudaStream_t st) {
+  ScoreArgs<T> k = {};
+  k.r = rows_of<T>(a);
+  k.cut = score_cut<T>(a.T_, a.V);
+  k.K = K;
+  unsigned char* b = static_cast<unsigned char*>(ws);
+  k.head = reinterpret_cast<WsHead*>(b);
+  k.part = reinterpret_cast<float4*>(b + sizeof(WsHead));
+  k.keys = reinterpret_cast<uint32_t*>(b + sizeof(WsHead) + (size_t)a.T_ * k.cut.pieces * 16);
+  k.logp = logp;
+  k.entropy = entropy;
+  k.top_idx = top_idx;
+  k.top_logp = top_logp;
+  k.norm = reinterpret_cast<float4*>(norm);
+  const cudaError_t e = launch_behind(score_part_kernel<T>, score_grid(a.T_ * k.cut.pieces), kScoreThreads,
+                                      0, 1, st, k);
+  if (e != cudaSuccess) return e;
+  return launch_behind(score_row_kernel<T>, (unsigned)((a.T_ * 32 + kScoreThreads - 1) / kScoreThreads),
+                       kScoreThreads, 0, 1, st, k);
+}
+
+template <typename T>
+cudaError_t scores_grad(const RowsArg& a, int32_t K, const float* norm, const int32_t* top_idx,
+                        const float* d_logp, const float* d_entropy, const float* d_top, void* grad,
+                        int64_t grad_ld, cudaStream_t st) {
+  ScoreGradArgs<T> k = {};
+  k.r = rows_of<T>(a);
+  k.cut = score_cut<T>(a.T_, a.V);
+  k.K = K;
+  k.norm = reinterpret_cast<const float4*>(norm);
+  k.top_idx = top_idx;
+  k.d_logp = d_logp;
+  k.d_entropy = d_entropy;
+  k.d_top = d_top;
+  k.grad = static_cast<T*>(grad);
+  k.grad_ld = grad_ld;
+  return launch_behind(score_grad_kernel<T>, score_grid(a.T_ * k.cut.pieces), kScoreThreads, 0, 1, st, k);
+}
+
 }  // namespace
 }  // namespace vsf
 
@@ -715,6 +788,72 @@ vsf_status vsf_preference_loss(const void* logits, int32_t dtype, int64_t T, int
   const cudaError_t e = dtype == VSF_BF16
                             ? preference<uint16_t>(a, p, stats, logp, grad, grad_ld, w, st)
                             : preference<float>(a, p, stats, logp, grad, grad_ld, w, st);
+  return e == cudaSuccess ? VSF_OK : cuda_error(e, who);
+}
+
+size_t vsf_token_scores_workspace_bytes(int64_t tokens, int64_t V, int32_t dtype, int64_t top_k) {
+  if (tokens < 0 || tokens > INT32_MAX || V < 1 || V > INT32_MAX || top_k < 0 || top_k > kMaxTop ||
+      top_k > V || (dtype != VSF_BF16 && dtype != VSF_FP32))
+    return 0;
+  return ScoreWs::bytes(tokens, V, dtype, top_k);
+}
+
+vsf_status vsf_token_scores(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                            const int64_t* targets, float inv_temperature, int64_t top_k, float* logp,
+                            float* entropy, int32_t* top_idx, float* top_logp, float* norm,
+                            void* d_workspace, size_t ws_bytes, void* stream) {
+  vsf::Range nvtx_range("vsf_token_scores");
+  const char* who = "vsf_token_scores";
+  const RowsArg a = {logits, dtype, T, V, ld, targets, nullptr, inv_temperature};
+  const vsf_status s = check_rows(who, a, d_workspace, SIZE_MAX, 0);
+  if (s != VSF_OK) return s;
+  if (top_k < 0 || top_k > kMaxTop || top_k > V)
+    return fail(VSF_ERR_ARG, "vsf_token_scores: top_k out of range");
+  if (ws_bytes < ScoreWs::bytes(T, V, dtype, top_k))
+    return fail(VSF_ERR_ARG, "vsf_token_scores: workspace too small");
+  if (T > 0 && (logp == nullptr || entropy == nullptr || norm == nullptr ||
+                (top_k > 0 && (top_idx == nullptr || top_logp == nullptr))))
+    return fail(VSF_ERR_ARG, "vsf_token_scores: NULL pointer");
+  if (!aligned(logp, 4) || !aligned(entropy, 4) || !aligned(top_idx, 4) || !aligned(top_logp, 4) ||
+      !aligned(norm, 16))
+    return fail(VSF_ERR_ALIGN, "vsf_token_scores: pointer alignment");
+  if (T == 0) return VSF_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int32_t K = (int32_t)top_k;
+  const cudaError_t e =
+      dtype == VSF_BF16
+          ? scores<uint16_t>(a, K, logp, entropy, top_idx, top_logp, norm, d_workspace, st)
+          : scores<float>(a, K, logp, entropy, top_idx, top_logp, norm, d_workspace, st);
+  return e == cudaSuccess ? VSF_OK : cuda_error(e, who);
+}
+
+vsf_status vsf_token_scores_grad(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                                 const int64_t* targets, float inv_temperature, int64_t top_k,
+                                 const float* norm, const int32_t* top_idx, const float* d_logp,
+                                 const float* d_entropy, const float* d_top, void* grad,
+                                 int64_t grad_ld, void* stream) {
+  vsf::Range nvtx_range("vsf_token_scores_grad");
+  const char* who = "vsf_token_scores_grad";
+  const RowsArg a = {logits, dtype, T, V, ld, targets, nullptr, inv_temperature};
+  alignas(16) static char none[16];
+  vsf_status s = check_rows(who, a, none, SIZE_MAX, 0);  // (needs no workspace)
+  if (s == VSF_OK) s = check_grad(who, a, grad, grad_ld);
+  if (s != VSF_OK) return s;
+  if (top_k < 0 || top_k > kMaxTop || top_k > V)
+    return fail(VSF_ERR_ARG, "vsf_token_scores_grad: top_k out of range");
+  if (T > 0 && (norm == nullptr || grad == nullptr ||
+                (top_k > 0 && d_top != nullptr && top_idx == nullptr)))
+    return fail(VSF_ERR_ARG, "vsf_token_scores_grad: NULL pointer");
+  if (!aligned(norm, 16) || !aligned(top_idx, 4) || !aligned(d_logp, 4) || !aligned(d_entropy, 4) ||
+      !aligned(d_top, 4))
+    return fail(VSF_ERR_ALIGN, "vsf_token_scores_grad: pointer alignment");
+  if (T == 0) return VSF_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int32_t K = (int32_t)top_k;
+  const cudaError_t e =
+      dtype == VSF_BF16
+          ? scores_grad<uint16_t>(a, K, norm, top_idx, d_logp, d_entropy, d_top, grad, grad_ld, st)
+          : scores_grad<float>(a, K, norm, top_idx, d_logp, d_entropy, d_top, grad, grad_ld, st);
   return e == cudaSuccess ? VSF_OK : cuda_error(e, who);
 }
 

@@ -2,6 +2,7 @@
 loss and router calls, as ``step.ShardStep`` is around the shard step.
 
 TokenLogprobs   log probability of each token under its row of logits
+TokenScores     the same with the row's entropy and top alternatives; gradient
 PolicyLoss      clipped policy loss with a KL term, and the logits' gradient
 PreferenceLoss  loss of (chosen, rejected) pairs, and the logits' gradient
 Router          top-k choice, gates, per-expert counts, balance loss; gradient
@@ -119,6 +120,9 @@ class _LogitsLoss(_Objective):
         self.stats = self._new(stats)
         self.logp = self._new(self.tokens)
         self._out = self.stats.data_ptr(), self.logp.data_ptr()
+        self._grad_buffer(with_grad)
+
+    def _grad_buffer(self, with_grad: bool):
         self.grad = None
         # The gradient's rows lie as far apart, modulo 16 bytes, as the logits',
         # so that both go in wide pieces.
@@ -147,6 +151,62 @@ class _LogitsLoss(_Objective):
         pad = (ld - self.width) % self._step
         self.grad = self._view(pad)  # (the attribute shows what the call writes)
         return self._first(self.grad, n), self._grad_at, self.width + pad
+
+
+class TokenScores(_LogitsLoss):
+    """forward(logits, targets) -> (logp [T], entropy [T], top_idx [T, top_k]
+    int32, top_logp [T, top_k]): log probability of each token, entropy of its row
+    and the row's top_k likeliest words (ties to the lowest index). Tokens of a
+    negative target (int64) are masked: zeros, and -1 for the words.
+    backward(logits, targets, d_logp, d_entropy, d_top) -> the logits' gradient
+    (each of the three may be None), for the last forward call, whose rows' sums
+    and words it reads. `calls` counts the forward calls: given to backward as
+    `call`, it refuses if another one has followed. The gradient goes to the
+    object's own buffer or to the tensor given (the logits themselves to write in
+    place); with_grad=False: to the tensor given only."""
+
+    def __init__(self, tokens: int, vocab: int, *, top_k: int = 0, dtype=torch.bfloat16,
+                 inv_temperature: float = 1.0, with_grad: bool = True, device=None, stream=None):
+        super().__init__(tokens, vocab, dtype, device, stream)
+        self.top_k, self.inv_temperature = int(top_k), inv_temperature
+        self._workspace(V.vsf_token_scores_workspace_bytes(self.tokens, self.width, self._vdt,
+                                                           self.top_k))
+        self.logp, self.entropy = self._new(self.tokens), self._new(self.tokens)
+        self.top_idx = self._new(self.tokens, self.top_k, dtype=torch.int32)
+        self.top_logp = self._new(self.tokens, self.top_k)
+        self.norm = self._new(self.tokens, 4)
+        self._out = [t.data_ptr() for t in (self.logp, self.entropy, self.top_idx, self.top_logp,
+                                            self.norm)]
+        self._grad_buffer(with_grad)
+        self.calls, self._rows_scored = 0, None
+
+    def forward(self, logits, targets):
+        n, ld = self._rows(logits, "logits")
+        V.vsf_token_scores(logits.data_ptr(), self._vdt, n, self.width, ld,
+                           self._vec(targets, n, torch.int64, "targets"), self.inv_temperature,
+                           self.top_k, *self._out, self._ws, self._ws_bytes, self._st)
+        self.calls += 1
+        self._rows_scored = n
+        return tuple(self._first(t, n) for t in (self.logp, self.entropy, self.top_idx, self.top_logp))
+
+    def backward(self, logits, targets, d_logp=None, d_entropy=None, d_top=None, grad=None,
+                 call: int | None = None):
+        n, ld = self._rows(logits, "logits")
+        if n != self._rows_scored:
+            raise ValueError(f"backward: {n} tokens, the last forward call had {self._rows_scored}")
+        if call is not None and call != self.calls:
+            raise ValueError(f"backward of forward call {call}: call {self.calls} has followed it")
+        if grad is None and self.grad is None:
+            raise ValueError("grad: none of the object's own (with_grad=False) and none given")
+        grad, g, grad_ld = self._grad(n, ld, grad)
+        f32 = torch.float32
+        V.vsf_token_scores_grad(logits.data_ptr(), self._vdt, n, self.width, ld,
+                                self._vec(targets, n, torch.int64, "targets"), self.inv_temperature,
+                                self.top_k, self._out[4], self._out[2],
+                                self._vec(d_logp, n, f32, "d_logp"),
+                                self._vec(d_entropy, n, f32, "d_entropy"),
+                                self._vec(d_top, n * self.top_k, f32, "d_top"), g, grad_ld, self._st)
+        return grad
 
 
 class PolicyLoss(_LogitsLoss):

@@ -177,6 +177,14 @@ def lib():
             L.vsf_objective_workspace_init.argtypes = [vp, sz, vp]
             L.vsf_token_logprobs.restype = st
             L.vsf_token_logprobs.argtypes = [vp, i32, i64, i64, i64, vp, f32, vp, vp, sz, vp]
+            L.vsf_token_scores_workspace_bytes.restype = sz
+            L.vsf_token_scores_workspace_bytes.argtypes = [i64, i64, i32, i64]
+            L.vsf_token_scores.restype = st
+            L.vsf_token_scores.argtypes = [vp, i32, i64, i64, i64, vp, f32, i64, vp, vp, vp, vp, vp,
+                                           vp, sz, vp]
+            L.vsf_token_scores_grad.restype = st
+            L.vsf_token_scores_grad.argtypes = [vp, i32, i64, i64, i64, vp, f32, i64, vp, vp, vp, vp,
+                                                vp, vp, i64, vp]
             L.vsf_policy_loss.restype = st
             L.vsf_policy_loss.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp,
                                           P(vsf_policy_hparams), vp, vp, vp, i64, vp, sz, vp]
@@ -443,6 +451,24 @@ def vsf_token_logprobs(logits, dtype: int, T: int, V: int, ld: int, targets,
                        stream: int) -> None:
     _check(lib().vsf_token_logprobs(logits, dtype, T, V, ld, targets, inv_temperature, logp,
                                     d_workspace, ws_bytes, stream))
+
+
+def vsf_token_scores_workspace_bytes(tokens: int, V: int, dtype: int, top_k: int) -> int:
+    return int(lib().vsf_token_scores_workspace_bytes(tokens, V, dtype, top_k))
+
+
+def vsf_token_scores(logits, dtype: int, T: int, V: int, ld: int, targets, inv_temperature: float,
+                     top_k: int, logp, entropy, top_idx, top_logp, norm, d_workspace, ws_bytes: int,
+                     stream: int) -> None:
+    _check(lib().vsf_token_scores(logits, dtype, T, V, ld, targets, inv_temperature, top_k, logp,
+                                  entropy, top_idx, top_logp, norm, d_workspace, ws_bytes, stream))
+
+
+def vsf_token_scores_grad(logits, dtype: int, T: int, V: int, ld: int, targets,
+                          inv_temperature: float, top_k: int, norm, top_idx, d_logp, d_entropy,
+                          d_top, grad, grad_ld: int, stream: int) -> None:
+    _check(lib().vsf_token_scores_grad(logits, dtype, T, V, ld, targets, inv_temperature, top_k, norm,
+                                       top_idx, d_logp, d_entropy, d_top, grad, grad_ld, stream))
 
 
 def make_policy_hparams(clip_low=0.2, clip_high=0.2, kl_beta=0.0, inv_temperature=1.0, scale=1.0,

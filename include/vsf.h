@@ -498,6 +498,38 @@ vsf_status vsf_token_logprobs(const void* logits, int32_t dtype, int64_t T, int6
                               const int64_t* targets, float inv_temperature, float* logp,
                               void* d_workspace, size_t ws_bytes, void* stream);
 
+/* Log probability of each token, the row's entropy and its top_k alternatives
+ * (0 <= top_k <= min(V, 32)), and their gradient. With p = softmax as above:
+ *   logp[t]      ln p_t(targets[t])
+ *   entropy[t]   -sum_v p_t(v) ln p_t(v)  (terms of p = 0 are 0)
+ *   top_idx      int32[T*top_k], the words of largest logits, best first, ties to
+ *                the lowest index; top_logp: fp32[T*top_k], their ln p
+ *   norm         fp32[4*T], 16-byte aligned: what the gradient needs of a row
+ * A masked token (target negative; a target >= V sets bit 4) has logp and entropy
+ * 0, top_idx -1 and top_logp 0; a live row with a NaN, a +inf or only -inf gives
+ * NaN and top_idx -1. The workspace is prepared by vsf_objective_workspace_init
+ * and not for routers; its size depends on the rows' too. */
+size_t vsf_token_scores_workspace_bytes(int64_t tokens, int64_t V, int32_t dtype, int64_t top_k);
+vsf_status vsf_token_scores(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                            const int64_t* targets, float inv_temperature, int64_t top_k,
+                            float* logp, float* entropy, int32_t* top_idx, float* top_logp,
+                            float* norm, void* d_workspace, size_t ws_bytes, void* stream);
+
+/* Gradient of sum_t (d_logp[t] logp[t] + d_entropy[t] entropy[t] + sum_j
+ * d_top[t*top_k + j] top_logp[t*top_k + j]) with respect to the logits:
+ *   grad[t][v] = inv_temperature (d_logp[t] 1[v = y] + sum_j d_top_j 1[v = top_j]
+ *                - p(v) (d_logp[t] + sum_j d_top_j + d_entropy[t] (ln p(v) + entropy[t])))
+ * d_logp, d_entropy: fp32[T], d_top: fp32[T*top_k]; NULL: zeros. The forward call's
+ * logits, targets, inv_temperature, top_k, norm and top_idx are passed again (a
+ * top_idx outside [0, V) takes no pull of its own; one that comes twice takes
+ * both). grad as for the losses: the logits' type, T rows at stride grad_ld, the
+ * logits themselves (same ld) or apart from them. Needs no workspace. */
+vsf_status vsf_token_scores_grad(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                                 const int64_t* targets, float inv_temperature, int64_t top_k,
+                                 const float* norm, const int32_t* top_idx, const float* d_logp,
+                                 const float* d_entropy, const float* d_top, void* grad,
+                                 int64_t grad_ld, void* stream);
+
 /* Clipped policy loss with a KL term, loss and gradient:
  *   r = exp(logp - old), u = ref - logp, with N = sum of the live weights
  *   (mean = 1; 1 where that sum is 0) or 1 (mean = 0):
