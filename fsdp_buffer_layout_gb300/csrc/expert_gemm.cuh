@@ -38,13 +38,15 @@ constexpr int kXCols = 256;                            // of a tile, at most
 constexpr int kMaxGroups = 512;                        // experts
 constexpr uint32_t kXHalf = 128 * kXDepth * 2;         // one operand's half of a stage: 16 KB
 constexpr uint32_t kXStage = 2 * kXHalf;
-constexpr uint32_t kXBars = 3 * kXStages + 5;
+constexpr uint32_t kXBars = 4 * kXStages + 5;
 struct XTable {
   int32_t first[kMaxGroups + 1];  // tiles in front of each expert's
   int32_t start[kMaxGroups + 1];  // its first row
   uint32_t tmem, stop;
 };
-constexpr uint32_t kXSmem = kXStages * kXStage + 8 * kXBars + (uint32_t)sizeof(XTable) + 1024;
+constexpr uint32_t kXOut = 4096;  // kWeight: of each epilogue warp, 32 lanes x 64 columns
+constexpr uint32_t kXSmem =
+    kXStages * kXStage + 4 * kXOut + 8 * kXBars + (uint32_t)sizeof(XTable) + 1024;
 static_assert(kXSmem <= 227 * 1024, "fits in shared memory");
 
 struct ExpertArgs {
@@ -111,23 +113,28 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 template <int KIND>
 constexpr int kXThreads = KIND == kWeight ? 224 : 192;
 
-// tmA: the lanes' operand. tmB: the columns' operand in boxes of 128 rows (K-major)
-// or 64 x 64 (MN-major); tmB16 in boxes of 16 rows.
+// Tensor maps: the lanes' operand; the columns' operand, in boxes of 16, 32, 64 and
+// 128 rows (kWeight: of 64 x 64, the first alone); kWeight's output, in boxes of 32
+// rows.
+struct XMaps {
+  CUtensorMap lanes, cols[4], out;
+};
+
 template <int KIND>
 __global__ void __launch_bounds__(kXThreads<KIND>, 1)
-    expert_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                       const __grid_constant__ CUtensorMap tmB16, const ExpertArgs g, unsigned* err) {
+    expert_gemm_kernel(const __grid_constant__ XMaps maps, const ExpertArgs g, unsigned* err) {
   constexpr bool AMN = KIND != kForward, BMN = KIND == kWeight;
   extern __shared__ __align__(1024) unsigned char raw[];
   unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  const uint32_t s0 = smem_u32(sm), bar0 = s0 + kXStages * kXStage;
-  XTable& table = *reinterpret_cast<XTable*>(sm + kXStages * kXStage + 8 * kXBars);
+  const uint32_t s0 = smem_u32(sm), out0 = s0 + kXStages * kXStage, bar0 = out0 + 4 * kXOut;
+  XTable& table = *reinterpret_cast<XTable*>(sm + kXStages * kXStage + 4 * kXOut + 8 * kXBars);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (kXStages + s); };
   auto tfull_bar = [&](int i) { return bar0 + 8u * (2 * kXStages + i); };
   auto tempty_bar = [&](int i) { return bar0 + 8u * (2 * kXStages + 2 + i); };
   const uint32_t done_bar = bar0 + 8u * (2 * kXStages + 4);
   auto own_bar = [&](int s) { return done_bar + 8u + 8u * s; };
+  auto peer_bar = [&](int s) { return own_bar(kXStages + s); };
   volatile uint32_t* stop = &table.stop;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
@@ -138,9 +145,10 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
   if (threadIdx.x == 0) {
     table.stop = 0u;
     for (int s = 0; s < kXStages; ++s) {
-      mbar_init(full_bar(s), KIND == kWeight ? 2 : 1);  // kWeight: one arrival of each CTA
+      mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
-      mbar_init(own_bar(s), 1);  // kWeight: this CTA's copies of a stage to be mended
+      mbar_init(own_bar(s), 1);   // kWeight: this CTA's copies of a stage to be mended
+      mbar_init(peer_bar(s), 1);  // the leader's: the follower's half is mended
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(tfull_bar(i), 1);
@@ -202,6 +210,7 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
       KIND == kWeight ? g.E * g.lane_tiles * g.col_tiles : table.first[g.E];
   const uint32_t leader_full0 = peer_addr(full_bar(0), 0);
   const uint32_t leader_tempty0 = peer_addr(tempty_bar(0), 0);
+  const uint32_t leader_peer0 = peer_addr(peer_bar(0), 0);
   auto halt_cluster = [&]() { remote_stop(stop, (uint32_t)(rank ^ 1)); };
 
   if (warp == 0) {
@@ -215,7 +224,12 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
         const XTile q = tile_at<KIND>(g, table, t, e);
         const int32_t half = q.width / 2;
         const int32_t lane0 = q.lane0 + rank * 128, col0 = q.col0 + rank * half;
-        const uint32_t bytes = kXHalf + (uint32_t)half * (kXDepth * 2);
+        // One copy of the least box that holds the columns' half: rows too many are
+        // read and not used (seven boxes of 16 instead of one of 128 ran 224 columns
+        // at 970 TFLOP/s, 256 columns at 1670).
+        const int32_t box = KIND == kWeight ? half : half <= 16 ? 16 : half <= 32 ? 32 : half <= 64 ? 64 : 128;
+        const CUtensorMap* cols = &maps.cols[box <= 16 ? 0 : box <= 32 ? 1 : box <= 64 ? 2 : 3];
+        const uint32_t bytes = kXHalf + (uint32_t)box * (kXDepth * 2);
         for (int32_t k0 = 0; k0 < q.depth; k0 += kXDepth) {
           const int s = it % kXStages;
           const uint32_t ph = (it / kXStages) & 1u;
@@ -226,38 +240,29 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
           }
           ++it;
           uint32_t fb = leader_full0 + 8u * s;
-          if (KIND != kWeight) {
-            if (leader) mbar_expect_tx(full_bar(s), 2 * bytes);
-          } else if (k0 + kXDepth > q.depth && (q.depth & 15) != 0) {
+          if (KIND == kWeight && k0 + kXDepth > q.depth && (q.depth & 15) != 0) {
             fb = own0 + 8u * s;  // warp 6 mends the stage and then arrives
             mbar_expect_tx(own_bar(s), bytes);
             mended |= 1u << s;
             phases ^= 1u << s;
           } else if (leader) {
             mbar_expect_tx(full_bar(s), 2 * bytes);
-          } else {
-            mbar_arrive_cluster(fb);
           }
           const uint32_t a = s0 + s * kXStage, b = a + kXHalf;
           if (KIND == kWeight) {
             const int32_t r = q.row0 + k0;
-            tma3_g2s_pair(a, &tmA, lane0, r, 0, fb);
-            tma3_g2s_pair(a + 8192u, &tmA, lane0 + 64, r, 0, fb);
-            tma3_g2s_pair(b, &tmB, col0, r, 0, fb);
-            if (half > 64) tma3_g2s_pair(b + 8192u, &tmB, col0 + 64, r, 0, fb);
+            tma3_g2s_pair(a, &maps.lanes, lane0, r, 0, fb);
+            tma3_g2s_pair(a + 8192u, &maps.lanes, lane0 + 64, r, 0, fb);
+            tma3_g2s_pair(b, &maps.cols[0], col0, r, 0, fb);
+            if (half > 64) tma3_g2s_pair(b + 8192u, &maps.cols[0], col0 + 64, r, 0, fb);
           } else {
             if (AMN) {
-              tma3_g2s_pair(a, &tmA, lane0, k0, q.e, fb);
-              tma3_g2s_pair(a + 8192u, &tmA, lane0 + 64, k0, q.e, fb);
+              tma3_g2s_pair(a, &maps.lanes, lane0, k0, q.e, fb);
+              tma3_g2s_pair(a + 8192u, &maps.lanes, lane0 + 64, k0, q.e, fb);
             } else {
-              tma3_g2s_pair(a, &tmA, k0, lane0, q.e, fb);
+              tma3_g2s_pair(a, &maps.lanes, k0, lane0, q.e, fb);
             }
-            if (half == 128) {
-              tma3_g2s_pair(b, &tmB, k0, col0, 0, fb);
-            } else {
-              for (int32_t c = 0; c < half; c += 16)
-                tma3_g2s_pair(b + (uint32_t)c * 128u, &tmB16, k0, col0 + c, 0, fb);
-            }
+            tma3_g2s_pair(b, cols, k0, col0, 0, fb);
           }
         }
       }
@@ -328,34 +333,50 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
         const XTile q = tile_at<KIND>(g, table, t, e);
         const int32_t i = q.lane0 + rank * 128 + 32 * quarter + lane;
         const uint32_t from = tmem + (uint32_t)(buf * kXCols) + ((uint32_t)(32 * quarter) << 16);
+        if (KIND == kWeight) {
+          // A lane holds 64 columns of its row at a time. Through shared memory, in
+          // the swizzle of the tensor copies (16-byte piece p of row l at p ^ (l & 7)),
+          // and out as one copy of 32 rows: 32 lanes' stores to 32 rows took 1640 us
+          // for 32 experts of 1024 rows, 5760 x 2880.
+          const uint32_t to = out0 + (uint32_t)quarter * kXOut;
+          const uint32_t mine = to + (uint32_t)lane * 128u;
 #pragma unroll 1
-        for (int32_t c = 0; c < q.cols; c += 32) {
+          for (int32_t c = 0; c < q.cols; c += 64) {
+            uint32_t p[32];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t r[32];
+              __syncwarp();
+              tmem_ld32(from + c + 32 * h, r);
+#pragma unroll
+              for (int x = 0; x < 16; ++x)
+                p[16 * h + x] = q.depth == 0 ? 0u : pack_bf16(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1]));
+            }
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+#pragma unroll
+            for (int w = 0; w < 8; ++w)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + (uint32_t)((w ^ (lane & 7)) * 16)),
+                           "r"(p[4 * w]), "r"(p[4 * w + 1]), "r"(p[4 * w + 2]), "r"(p[4 * w + 3])
+                           : "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0 && q.lane0 + rank * 128 + 32 * quarter < g.lanes) {
+              asm volatile(
+                  "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                      reinterpret_cast<uint64_t>(&maps.out)),
+                  "r"(q.col0 + c), "r"(q.lane0 + rank * 128 + 32 * quarter), "r"(q.e), "r"(to)
+                  : "memory");
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+          }
+        }
+#pragma unroll 1
+        for (int32_t c = 0; KIND != kWeight && c < q.cols; c += 32) {
           uint32_t r[32];
           __syncwarp();
           tmem_ld32(from + c, r);
-          if (KIND == kWeight) {
-            if (i >= g.lanes) continue;
-            uint16_t* to = g.out + (int64_t)q.e * g.stride + (int64_t)i * g.ld + q.col0 + c;
-            const int32_t n = q.cols - c;
-            if (q.depth == 0) {  // an expert without a row
-#pragma unroll
-              for (int x = 0; x < 32; ++x) r[x] = 0u;
-            }
-            if (n >= 32) {
-#pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                uint32_t p[4];
-#pragma unroll
-                for (int h = 0; h < 4; ++h)
-                  p[h] = pack_bf16(__uint_as_float(r[8 * w + 2 * h]), __uint_as_float(r[8 * w + 2 * h + 1]));
-                *reinterpret_cast<uint4*>(to + 8 * w) = make_uint4(p[0], p[1], p[2], p[3]);
-              }
-            } else {
-#pragma unroll
-              for (int x = 0; x < 32; ++x)
-                if (x < n) to[x] = bf16_rn(__uint_as_float(r[x]));
-            }
-          } else {
+          {
             // Lane pairs trade columns: an even lane keeps column x and gets its
             // neighbour's, an odd one column x + 1, so that each stores two
             // adjacent elements of a row.
@@ -382,6 +403,7 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(leader_tempty0 + 8u * buf);
     }
+    if (KIND == kWeight && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else {
     // ---------------- mending (both CTAs): rows that are not the expert's
     uint32_t it = 0, phases = 0;
@@ -395,7 +417,6 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
         if (lane == 0) halt_cluster();
         break;
       }
-      phases ^= 1u << s;
       const int32_t from = q.depth & (kXDepth - 1), rows = 16 - (q.depth & 15);
       const int boxes = 2 + q.width / 128;  // of 64 x 64: two of A, one or two of B
       unsigned char* a = sm + s * kXStage;
@@ -405,7 +426,16 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(leader_full0 + 8u * s);
+      if (!leader) {
+        if (lane == 0) mbar_arrive_cluster(leader_peer0 + 8u * s);
+      } else {
+        if (!__all_sync(~0u, mbar_wait_cluster(peer_bar(s), phases >> s & 1u, err, stop))) {
+          if (lane == 0) halt_cluster();
+          break;
+        }
+        if (lane == 0) mbar_arrive_cluster(leader_full0 + 8u * s);
+      }
+      phases ^= 1u << s;
     }
   }
   tc_fence_before();

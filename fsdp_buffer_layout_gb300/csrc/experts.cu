@@ -150,23 +150,26 @@ vsf_status product(const Product& a, cudaStream_t st) {
   const int64_t tiles = KIND == kWeight ? a.E * g.lane_tiles * g.col_tiles
                                         : (a.rows / kXCols + std::min(a.E, a.rows)) * g.lane_tiles;
   if (tiles > INT32_MAX / 2) return fail(VSF_ERR_ARG, std::string(a.who) + ": too many tiles");
-  CUtensorMap ma, mb, mb16;
+  XMaps m;
   vsf_status s;
   if (KIND == kWeight) {
-    s = operand_map(&ma, a.who, a.rows_in, a.N, a.rows, 1, a.rows_ld, 0, 64);
-    if (s == VSF_OK) s = operand_map(&mb, a.who, a.other, a.K, a.rows, 1, a.other_ld, 0, 64);
-    mb16 = mb;
+    s = operand_map(&m.lanes, a.who, a.rows_in, a.N, a.rows, 1, a.rows_ld, 0, 64);
+    if (s == VSF_OK) s = operand_map(&m.cols[0], a.who, a.other, a.K, a.rows, 1, a.other_ld, 0, 64);
+    if (s == VSF_OK) s = operand_map(&m.out, a.who, a.out, a.K, a.N, a.E, a.out_ld, a.out_stride, 32);
+    m.cols[1] = m.cols[2] = m.cols[3] = m.cols[0];
   } else {
-    s = operand_map(&ma, a.who, a.other, a.K, a.N, a.E, a.other_ld, a.other_stride, KIND == kForward ? 128 : 64);
-    if (s == VSF_OK) s = operand_map(&mb, a.who, a.rows_in, g.depth, a.rows, 1, a.rows_ld, 0, 128);
-    if (s == VSF_OK) s = operand_map(&mb16, a.who, a.rows_in, g.depth, a.rows, 1, a.rows_ld, 0, 16);
+    s = operand_map(&m.lanes, a.who, a.other, a.K, a.N, a.E, a.other_ld, a.other_stride,
+                    KIND == kForward ? 128 : 64);
+    for (int i = 0; i < 4 && s == VSF_OK; ++i)
+      s = operand_map(&m.cols[i], a.who, a.rows_in, g.depth, a.rows, 1, a.rows_ld, 0, 16 << i);
+    m.out = m.lanes;
   }
   if (s != VSF_OK) return s;
   cudaError_t e = cudaSuccess;
   const int pairs = expert_pairs<KIND>(&e);
   if (pairs > 0)
     e = launch_behind(expert_gemm_kernel<KIND>, (unsigned)(2 * std::min<int64_t>(pairs, tiles)),
-                      kXThreads<KIND>, kXSmem, 2, st, ma, mb, mb16, g, a.err);
+                      kXThreads<KIND>, kXSmem, 2, st, m, g, a.err);
   return e == cudaSuccess ? VSF_OK : cuda_error(e, a.who);
 }
 
