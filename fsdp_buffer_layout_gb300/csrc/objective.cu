@@ -636,9 +636,9 @@ struct ScoreWs {
   }
 };
 
-unsigned score_grid(int64_t items) {
+unsigned score_grid(int64_t items, int ctas) {
   const int64_t warps = kScoreThreads / 32;
-  return (unsigned)std::min<int64_t>((items + warps - 1) / warps, kSms * kScoreCtas);
+  return (unsigned)std::min<int64_t>((items + warps - 1) / warps, kSms * ctas);
 }
 
 template <typename T>
@@ -657,8 +657,8 @@ cudaError_t scores(const RowsArg& a, int32_t K, float* logp, float* entropy, int
   k.top_idx = top_idx;
   k.top_logp = top_logp;
   k.norm = reinterpret_cast<float4*>(norm);
-  const cudaError_t e = launch_behind(score_part_kernel<T>, score_grid(a.T_ * k.cut.pieces), kScoreThreads,
-                                      0, 1, st, k);
+  const cudaError_t e = launch_behind(score_part_kernel<T>, score_grid(a.T_ * k.cut.pieces, kPartCtas),
+                                      kScoreThreads, 0, 1, st, k);
   if (e != cudaSuccess) return e;
   return launch_behind(score_row_kernel<T>, (unsigned)((a.T_ * 32 + kScoreThreads - 1) / kScoreThreads),
                        kScoreThreads, 0, 1, st, k);
@@ -679,7 +679,8 @@ cudaError_t scores_grad(const RowsArg& a, int32_t K, const float* norm, const in
   k.d_top = d_top;
   k.grad = static_cast<T*>(grad);
   k.grad_ld = grad_ld;
-  return launch_behind(score_grad_kernel<T>, score_grid(a.T_ * k.cut.pieces), kScoreThreads, 0, 1, st, k);
+  return launch_behind(score_grad_kernel<T>, score_grid(a.T_ * k.cut.pieces, kScoreCtas), kScoreThreads, 0, 1,
+                       st, k);
 }
 
 }  // namespace

@@ -28,7 +28,8 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 __device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(~0u, v); }
 
 constexpr int kScoreThreads = 256;
-constexpr int kScoreCtas = 4;        // an SM
+constexpr int kScoreCtas = 4;        // an SM (gradient)
+constexpr int kPartCtas = 3;         // an SM (sums)
 constexpr int kScoreBatch = 4;       // vectors of a lane on their way at a time
 constexpr int kMaxGroupsRow = 1024;  // groups of a row, its loose elements among them
 constexpr int kMaxTop = 32;
@@ -66,14 +67,95 @@ __device__ __forceinline__ void score_terms(F2 x, F2 nm, const PairScale& c, F2&
   e = f2(ex2(a), ex2(b));
 }
 
-// {m, s, u} of a piece and its groups' keys; a warp a piece.
+// In the sums the same is reached by raising the logits themselves to a floor 200
+// units of ln 2 below the maximum (or the next smaller logit, where they are that
+// far apart), whose term is 0 as well: one instruction for two bf16 logits. Not
+// where that floor is out of range (`far`: maxima next to the type's lowest value,
+// inverse temperatures below 2^-110) or its z could be (above 64).
+__device__ __forceinline__ bool far_temperature(float inv_t) { return inv_t < 7.7e-34f || inv_t > 64.f; }
+__device__ __forceinline__ uint32_t score_floor(float m, float units, uint16_t) {
+  const uint32_t f = __bfloat16_as_ushort(__float2bfloat16_rd(__fsub_rd(m, units)));
+  return f | f << 16;
+}
+__device__ __forceinline__ uint32_t score_floor(float m, float units, float) {
+  return __float_as_uint(__fsub_rd(m, units));
+}
+__device__ __forceinline__ uint32_t raised(uint32_t w, uint32_t floor, uint16_t) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(floor));
+  return r;
+}
+__device__ __forceinline__ uint32_t raised(uint32_t w, uint32_t floor, float) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(w)), "f"(__uint_as_float(floor)));
+  return __float_as_uint(r);
+}
+
+// What a warp has of a piece: the maximum, the same in all lanes, and each lane's sums.
 template <typename T>
-__global__ void __launch_bounds__(kScoreThreads, kScoreCtas)
+struct ScoreSums {
+  float m = -INFINITY;
+  F2 nm = f2(0.f, 0.f);
+  uint32_t floor;
+  F2 sum0 = f2(0.f, 0.f), sum1 = f2(0.f, 0.f), zum0 = f2(0.f, 0.f), zum1 = f2(0.f, 0.f);
+  __device__ __forceinline__ ScoreSums(float units) : floor(score_floor(0.f, units, T())) {}
+  __device__ __forceinline__ void to(float bm, Log2Scale c, float units) {
+    if (!(bm > m)) return;
+    if (m != -INFINITY) {
+      const float d = fmaxf(__fmaf_rn(m - bm, c.hi, (m - bm) * c.lo), -1e20f), f = ex2(d);
+      const F2 dd = f2(d, d), ff = f2(f, f);
+      zum0 = f2_mul(f2_fma(sum0, dd, zum0), ff);
+      zum1 = f2_mul(f2_fma(sum1, dd, zum1), ff);
+      sum0 = f2_mul(sum0, ff);
+      sum1 = f2_mul(sum1, ff);
+    }
+    m = bm;
+    nm = f2(-m, -m);
+    floor = score_floor(m, units, T());
+  }
+  // c: this thread's factor, rounded down or up (Log2Scale)
+  __device__ __forceinline__ bool out_of_range() const { return floor == Vec<T>::lowest; }
+  template <bool FAR>
+  __device__ __forceinline__ void add(const uint4& v, F2 c) {
+    Pairs<T> q;
+    if (FAR)
+      unpack(v, q);
+    else
+      unpack(make_uint4(raised(v.x, floor, T()), raised(v.y, floor, T()), raised(v.z, floor, T()),
+                        raised(v.w, floor, T())), q);
+#pragma unroll
+    for (int i = 0; i < Vec<T>::n / 2; ++i) {
+      const F2 t = f2_mul(f2_add(q.p[i], nm), c);
+      float a, b;
+      f2_get(t, a, b);
+      if (FAR) {
+        asm("max.NaN.f32 %0, %1, 0fC3480000;" : "=f"(a) : "f"(a));
+        asm("max.NaN.f32 %0, %1, 0fC3480000;" : "=f"(b) : "f"(b));
+      }
+      const F2 z = f2(a, b), e = f2(ex2(a), ex2(b));
+      if (i & 1) {
+        sum1 = f2_add(sum1, e);
+        zum1 = f2_fma(z, e, zum1);
+      } else {
+        sum0 = f2_add(sum0, e);
+        zum0 = f2_fma(z, e, zum0);
+      }
+    }
+  }
+};
+
+// {m, s, u} of a piece and its groups' keys; a warp a piece. Two batches of loads
+// are on their way at a time.
+template <typename T>
+__global__ void __launch_bounds__(kScoreThreads, kPartCtas)
     score_part_kernel(const __grid_constant__ ScoreArgs<T> a) {
   constexpr int VE = Vec<T>::n, B = kScoreBatch;
   const int lane = threadIdx.x & 31;
   const Rows<T>& r = a.r;
-  const PairScale c2 = {f2(r.c.hi, r.c.hi), f2(r.c.lo, r.c.lo)};
+  const float c1 = (uint32_t)threadIdx.x * 2654435769u < r.c.ups ? r.c.up : r.c.hi;
+  const F2 cc = f2(c1, c1);
+  const bool far = far_temperature(r.inv_tf);
+  const float units = 200.f / r.c.hi;
   take_turn();
   const int32_t pieces = a.cut.pieces;
   const int64_t step = (int64_t)gridDim.x * (kScoreThreads / 32);
@@ -92,26 +174,75 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas)
     const uint4* in = reinterpret_cast<const uint4*>(x + s.head) + lane;
     uint32_t* keys = a.K > 0 ? a.keys + t * a.cut.groups : nullptr;
     const int32_t span0 = p << a.cut.piece, span1 = min(span0 + (1 << a.cut.piece), a.cut.spans);
-    float m = -INFINITY;
-    F2 sum0 = f2(0.f, 0.f), sum1 = sum0, zum0 = sum0, zum1 = sum0;
-    auto raise = [&](float bm) {  // a new maximum, the same in all lanes
-      if (!(bm > m)) return;
-      if (m != -INFINITY) {
-        const float d = fmaxf(__fmaf_rn(m - bm, r.c.hi, (m - bm) * r.c.lo), -1e20f), f = ex2(d);
-        const F2 f2d = f2(d, d), ff = f2(f, f);
-        zum0 = f2_mul(f2_fma(sum0, f2d, zum0), ff);
-        zum1 = f2_mul(f2_fma(sum1, f2d, zum1), ff);
-        sum0 = f2_mul(sum0, ff);
-        sum1 = f2_mul(sum1, ff);
+    ScoreSums<T> sums(units);
+    uint32_t group_key = 0;
+    // the maxima of B spans from b on, n of which the row has
+    auto add = [&](const uint4 (&v)[B], int32_t b, int32_t n) {
+      float gm[B], top = -INFINITY, mine = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        const uint4 one[1] = {v[j]};
+        gm[j] = warp_max(largest(one, T()));
+        top = fmaxf(top, gm[j]);
+        if (lane == j) mine = gm[j];
       }
-      m = bm;
+      if (keys != nullptr) {
+        const uint32_t key = lane < n && (b + lane) * 32 < s.nvec ? order_key(mine) : 0;
+        if (a.cut.group == 0) {
+          if (lane < n) keys[1 + b + lane] = key;
+        } else {
+          for (int j = 0; j < n; ++j) {
+            group_key = max(group_key, __shfl_sync(~0u, key, j));
+            const int32_t next = b + j + 1;
+            if ((next & ((1 << a.cut.group) - 1)) == 0 || next == a.cut.spans) {
+              if (lane == 0) keys[1 + (b + j >> a.cut.group)] = group_key;
+              group_key = 0;
+            }
+          }
+        }
+      }
+      sums.to(top, r.c, units);
+      if (far || sums.out_of_range()) {
+#pragma unroll
+        for (int j = 0; j < B; ++j) sums.template add<true>(v[j], cc);
+      } else {
+#pragma unroll
+        for (int j = 0; j < B; ++j) sums.template add<false>(v[j], cc);
+      }
     };
-    // the loose elements, in front of the vectors (first piece) and behind them (last)
-    const int32_t tail = s.head + s.nvec * VE;
-    int32_t loose = -1;
-    if (p == 0 && lane < s.head) loose = lane;
-    if (p + 1 == pieces && lane >= 16 && lane - 16 < r.V - tail) loose = tail + (lane - 16);
+    const int32_t whole = min(span1, s.nvec / 32) - span0;  // spans without a missing vector
+    int32_t b = span0;
+    if (whole >= B) {
+      uint4 v[B];
+#pragma unroll
+      for (int j = 0; j < B; ++j) v[j] = __ldcs(in + (b + j) * 32);
+#pragma unroll 2
+      for (; b + 2 * B <= span0 + whole; b += B) {
+        uint4 w[B];
+#pragma unroll
+        for (int j = 0; j < B; ++j) w[j] = __ldcs(in + (b + B + j) * 32);
+        add(v, b, B);
+#pragma unroll
+        for (int j = 0; j < B; ++j) v[j] = w[j];
+      }
+      add(v, b, B);
+      b += B;
+    }
+    for (; b < span1; b += B) {  // (less than a batch, or the row's end)
+      uint4 v[B];
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        v[j] = make_uint4(Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest);
+        if (b + j < span1 && (b + j) * 32 + lane < s.nvec) v[j] = __ldcs(in + (b + j) * 32);
+      }
+      add(v, b, min(B, span1 - b));
+    }
     if (p == 0 || p + 1 == pieces) {
+      // the loose elements, in front of the vectors and behind them
+      const int32_t tail = s.head + s.nvec * VE;
+      int32_t loose = -1;
+      if (p == 0 && lane < s.head) loose = lane;
+      if (p + 1 == pieces && lane >= 16 && lane - 16 < r.V - tail) loose = tail + (lane - 16);
       const float xl = loose >= 0 ? to_f(x[loose]) : -INFINITY;
       if (keys != nullptr) {
         const uint32_t k = loose >= 0 ? order_key(xl) : 0;
@@ -119,68 +250,23 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas)
         if (lane == 0 && p == 0) keys[0] = front;
         if (lane == 0 && p + 1 == pieces) keys[a.cut.groups - 1] = back;
       }
-      raise(warp_max(xl));
-      F2 z, e;
-      const float nm = -finite_max(m);
-      score_terms(f2(xl, xl), f2(nm, nm), c2, z, e);
-      float z0, z1, e0, e1;
-      f2_get(z, z0, z1);
-      f2_get(e, e0, e1);
+      sums.to(warp_max(xl), r.c, units);
+      const PairScale c2 = {f2(r.c.hi, r.c.hi), f2(r.c.lo, r.c.lo)};
+      const float z = -finite_max(sums.m);
+      F2 zz, ee;
+      score_terms(f2(xl, -INFINITY), f2(z, z), c2, zz, ee);
       if (loose >= 0) {
-        sum0 = f2(e0, 0.f);
-        zum0 = f2(z0 * e0, 0.f);
-      }
-    }
-    uint32_t group_key = 0;
-    for (int32_t b = span0; b < span1; b += B) {
-      uint4 v[B];
-#pragma unroll
-      for (int j = 0; j < B; ++j) {
-        v[j] = make_uint4(Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest);
-        const int32_t at = (b + j) * 32;
-        if (b + j < span1 && at + lane < s.nvec) v[j] = __ldcs(in + at);
-      }
-      float top = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < B; ++j) {
-        const uint4 one[1] = {v[j]};
-        const float gm = warp_max(largest(one, T()));
-        top = fmaxf(top, gm);
-        if (keys != nullptr && b + j < span1) {
-          group_key = max(group_key, (b + j) * 32 < s.nvec ? order_key(gm) : 0u);
-          const int32_t next = b + j + 1;
-          if ((next & ((1 << a.cut.group) - 1)) == 0 || next == a.cut.spans) {
-            if (lane == 0) keys[1 + (b + j >> a.cut.group)] = group_key;
-            group_key = 0;
-          }
-        }
-      }
-      raise(top);
-      const float z = -finite_max(m);
-      const F2 nm = f2(z, z);
-#pragma unroll
-      for (int j = 0; j < B; ++j) {
-        Pairs<T> q;
-        unpack(v[j], q);
-#pragma unroll
-        for (int i = 0; i < VE / 2; i += 2) {
-          F2 z0, e0, z1, e1;
-          score_terms(q.p[i], nm, c2, z0, e0);
-          score_terms(q.p[i + 1], nm, c2, z1, e1);
-          sum0 = f2_add(sum0, e0);
-          sum1 = f2_add(sum1, e1);
-          zum0 = f2_fma(z0, e0, zum0);
-          zum1 = f2_fma(z1, e1, zum1);
-        }
+        sums.sum0 = f2_add(sums.sum0, ee);
+        sums.zum0 = f2_fma(zz, ee, sums.zum0);
       }
     }
     float s0, s1, s2, s3, u0, u1, u2, u3;
-    f2_get(sum0, s0, s1);
-    f2_get(sum1, s2, s3);
-    f2_get(zum0, u0, u1);
-    f2_get(zum1, u2, u3);
+    f2_get(sums.sum0, s0, s1);
+    f2_get(sums.sum1, s2, s3);
+    f2_get(sums.zum0, u0, u1);
+    f2_get(sums.zum1, u2, u3);
     const float sum = warp_sum((s0 + s1) + (s2 + s3)), zum = warp_sum((u0 + u1) + (u2 + u3));
-    if (lane == 0) a.part[t * pieces + p] = make_float4(m, sum, zum, 0.f);
+    if (lane == 0) a.part[t * pieces + p] = make_float4(sums.m, sum, zum, 0.f);
   }
 }
 
@@ -201,16 +287,39 @@ __device__ __forceinline__ void insert(Best& list, uint32_t key, int32_t idx, in
   else if (lane > at) list = {k, i};
 }
 
+// The K best of up to kScoreCandidates entries in shared memory, in any order, into
+// lanes 0 .. K-1: each entry's place is the number of those in front of it. A lane
+// without one gets {0, -1}.
+constexpr int kScoreCandidates = 128;
+__device__ __forceinline__ Best best_of(const Best* list, int n, int K, Best* out, int lane) {
+  out[lane] = {0, -1};
+  __syncwarp();
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const Best own = i0 + lane < n ? list[i0 + lane] : Best{0, INT32_MAX};
+    int at = 0;
+    for (int j = 0; j < n; ++j) {
+      const Best b = list[j];
+      at += in_front(b.key, b.idx, own);
+    }
+    if (i0 + lane < n && at < K) out[at] = own;
+  }
+  __syncwarp();
+  return out[lane];
+}
+
 // Joins a row's pieces and picks its alternatives; a warp a row.
 template <typename T>
 __global__ void __launch_bounds__(kScoreThreads)
     score_row_kernel(const __grid_constant__ ScoreArgs<T> a) {
-  constexpr int VE = Vec<T>::n, NG = kMaxGroupsRow / 32;
-  const int lane = threadIdx.x & 31;
+  constexpr int VE = Vec<T>::n, NG = kMaxGroupsRow / 32, W = kScoreThreads / 32, C = kScoreCandidates;
+  __shared__ Best candidates[W][C];
+  __shared__ Best sorted[W][32];
+  __shared__ int32_t count[W];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Rows<T>& r = a.r;
   take_turn();
   if (blockIdx.x == 0 && threadIdx.x == 0) a.head->rows = 1;
-  const int64_t t = (int64_t)blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);
+  const int64_t t = (int64_t)blockIdx.x * W + warp;
   if (t >= r.T_) return;
   const int32_t y = live_target(r, t, nullptr);
   if (y < 0) {
@@ -227,6 +336,15 @@ __global__ void __launch_bounds__(kScoreThreads)
   }
   const T* x = r.x + t * r.ld;
   const float xy = to_f(x[y]);
+  // ---- the groups' keys, on their way meanwhile
+  const uint32_t* keys = a.K > 0 ? a.keys + t * a.cut.groups : nullptr;
+  uint32_t key[NG];
+#pragma unroll
+  for (int j = 0; j < NG; ++j) {
+    key[j] = 0;
+    if (a.K == 0 || j * 32 >= a.cut.groups) continue;
+    if (j * 32 + lane < a.cut.groups) key[j] = keys[j * 32 + lane];
+  }
   // ---- the pieces
   float m = -INFINITY, sum = 0.f, zum = 0.f;
   const float4* part = a.part + t * a.cut.pieces;
@@ -258,96 +376,157 @@ __global__ void __launch_bounds__(kScoreThreads)
     }
     return;
   }
-  // ---- the K groups of largest maxima; lane i holds the i-th
-  const uint32_t* keys = a.keys + t * a.cut.groups;
-  uint32_t key[NG];
+  // ---- the K groups of largest maxima; lane i holds the i-th. The K-th largest
+  // of the lanes' largest keys is not above the K-th largest key: what is below it
+  // is left out, the others are ranked. Too many of them (equal maxima): one by one.
   uint32_t best = 0;
   int32_t at = 0;
 #pragma unroll
   for (int j = 0; j < NG; ++j) {
-    key[j] = 0;
     if (j * 32 >= a.cut.groups) continue;
-    if (j * 32 + lane < a.cut.groups) key[j] = keys[j * 32 + lane];
     if (key[j] > best) {
       best = key[j];
       at = j;
     }
   }
-  Best group = {0, -1};
-  for (int i = 0; i < a.K; ++i) {
-    const uint32_t top = warp_max(best);
-    if (top == 0) break;  // fewer groups than that
-    const int32_t g = (int32_t)__reduce_min_sync(~0u, best == top ? (uint32_t)(at * 32 + lane) : ~0u);
-    if (lane == i) group = {top, g};
-    if (lane == (g & 31)) {
-      best = 0;
-      const int32_t out = at;
+  uint32_t least = 0;
+  {
+    int before = 0;
 #pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        if (j * 32 >= a.cut.groups) continue;
-        if (j == out) key[j] = 0;
-        if (key[j] > best) {
-          best = key[j];
-          at = j;
+    for (int l = 0; l < 32; ++l) {
+      const uint32_t k = __shfl_sync(~0u, best, l);
+      before += k > best || (k == best && l < lane);
+    }
+    least = __shfl_sync(~0u, best, __ffs(__ballot_sync(~0u, before == a.K - 1)) - 1);
+  }
+  least = max(least, 1u);
+  int n = 0;
+#pragma unroll
+  for (int j = 0; j < NG; ++j) {
+    if (j * 32 >= a.cut.groups) continue;
+    n += key[j] >= least;
+  }
+  int upto = n;  // entries of the lanes up to this one
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(~0u, upto, o);
+    if (lane >= o) upto += v;
+  }
+  const int total = __shfl_sync(~0u, upto, 31);
+  Best group = {0, -1};
+  if (total <= C) {
+    int to = upto - n;
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+      if (j * 32 >= a.cut.groups) continue;
+      if (key[j] >= least) candidates[warp][to++] = {key[j], j * 32 + lane};
+    }
+    __syncwarp();
+    group = best_of(candidates[warp], total, a.K, sorted[warp], lane);
+  } else {
+    for (int i = 0; i < a.K; ++i) {
+      const uint32_t top = warp_max(best);
+      if (top == 0) break;  // fewer groups than that
+      const int32_t g = (int32_t)__reduce_min_sync(~0u, best == top ? (uint32_t)(at * 32 + lane) : ~0u);
+      if (lane == i) group = {top, g};
+      if (lane == (g & 31)) {
+        best = 0;
+        const int32_t out = at;
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+          if (j * 32 >= a.cut.groups) continue;
+          if (j == out) key[j] = 0;
+          if (key[j] > best) {
+            best = key[j];
+            at = j;
+          }
         }
       }
     }
   }
-  // ---- their elements. None below the last group's maximum is among the K.
+  if (lane >= a.K) group = {0, -1};
+  // ---- their elements. None below the last group's maximum is among the K; those
+  // that are not are gathered, whatever their order, and ranked; too many: one by one.
   const Span s = span_of(x, r.V);
   const uint4* in = reinterpret_cast<const uint4*>(x + s.head) + lane;
   const int32_t tail = s.head + s.nvec * VE;
-  Best list = {__shfl_sync(~0u, group.key, a.K - 1), INT32_MAX};
-  for (int i = 0; i < a.K; ++i) {
-    const uint32_t gk = __shfl_sync(~0u, group.key, i);
-    const int32_t g = __shfl_sync(~0u, group.idx, i);
-    // (lanes behind the list's K are never looked at)
-    if (g < 0 || gk < __shfl_sync(~0u, list.key, a.K - 1)) break;
-    const bool loose = g == 0 || g + 1 == a.cut.groups;
-    const int32_t v0 = loose ? 0 : (g - 1 << a.cut.group) * 32;
-    const int32_t v1 = loose ? 32 : min(v0 + (32 << a.cut.group), s.nvec);
-    for (int32_t v = v0; v < v1; v += 32) {
-      float f[VE];
-      int32_t base;
-      int n = VE;  // elements of this lane
-      if (loose) {
-        base = (g == 0 ? 0 : tail) + lane;
-        n = lane < (g == 0 ? s.head : r.V - tail) ? 1 : 0;
+  const uint32_t last_key = __shfl_sync(~0u, group.key, a.K - 1);
+  const float low = last_key == 0 ? -INFINITY : key_value(last_key);
+  if (lane == 0) count[warp] = 0;
+  __syncwarp();
+  auto gathered = [&](float v, int32_t idx) {
+    if (v >= low) {
+      const int to = atomicAdd(&count[warp], 1);
+      if (to < C) candidates[warp][to] = {order_key(v), idx};
+    }
+  };
+  constexpr int GB = 4;  // groups on their way at a time
+  for (int i0 = 0; i0 < a.K; i0 += GB) {
+    const int32_t spans = 1 << a.cut.group;
+    for (int32_t q = 0; q < spans; ++q) {
+      uint4 v[GB];
+      int32_t base[GB];
 #pragma unroll
-        for (int e = 0; e < VE; ++e) f[e] = 0.f;
-        if (n) f[0] = to_f(x[base]);
-      } else {
-        base = s.head + (v + lane) * VE;
-        n = v + lane < v1 ? VE : 0;
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (n) q = in[v];
-        Pairs<T> pr;
-        unpack(q, pr);
-#pragma unroll
-        for (int e = 0; e < VE / 2; ++e) f2_get(pr.p[e], f[2 * e], f[2 * e + 1]);
+      for (int i = 0; i < GB; ++i) {
+        const int32_t g = i0 + i < a.K ? __shfl_sync(~0u, group.idx, (i0 + i) & 31) : -1;
+        base[i] = -1;
+        if (g < 0) continue;
+        if (g == 0 || g + 1 == a.cut.groups) {  // loose elements
+          const int32_t e = g == 0 ? 0 : tail;
+          if (q == 0 && lane < (g == 0 ? s.head : r.V - tail)) gathered(to_f(x[e + lane]), e + lane);
+          continue;
+        }
+        const int32_t at_v = ((g - 1 << a.cut.group) + q) * 32;
+        if (at_v + lane >= s.nvec) continue;
+        base[i] = s.head + (at_v + lane) * VE;
+        v[i] = in[at_v];
       }
-      uint32_t k[VE];
 #pragma unroll
-      for (int e = 0; e < VE; ++e) k[e] = e < n ? order_key(f[e]) : 0;
-      while (true) {
-        uint32_t mine = 0;
-        int32_t which = 0;
+      for (int i = 0; i < GB; ++i) {
+        if (base[i] < 0) continue;
+        const uint4 one[1] = {v[i]};
+        if (!(largest(one, T()) >= low)) continue;
+        Pairs<T> pr;
+        unpack(v[i], pr);
 #pragma unroll
-        for (int e = 0; e < VE; ++e)
-          if (k[e] > mine) {
-            mine = k[e];
-            which = e;
+        for (int e = 0; e < VE / 2; ++e) {
+          float f0, f1;
+          f2_get(pr.p[e], f0, f1);
+          gathered(f0, base[i] + 2 * e);
+          gathered(f1, base[i] + 2 * e + 1);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  const int found = count[warp];
+  Best list;
+  if (found <= C) {
+    list = best_of(candidates[warp], found, a.K, sorted[warp], lane);
+  } else {
+    list = {last_key, INT32_MAX};
+    for (int i = 0; i < a.K; ++i) {
+      const uint32_t gk = __shfl_sync(~0u, group.key, i);
+      const int32_t g = __shfl_sync(~0u, group.idx, i);
+      // (lanes behind the list's K are never looked at)
+      if (g < 0 || gk < __shfl_sync(~0u, list.key, a.K - 1)) break;
+      const bool loose = g == 0 || g + 1 == a.cut.groups;
+      const int32_t v0 = loose ? 0 : (g - 1 << a.cut.group) * 32;
+      const int32_t v1 = loose ? 32 : min(v0 + (32 << a.cut.group), s.nvec);
+      for (int32_t v = v0; v < v1; v += 32) {
+        const int32_t base = loose ? (g == 0 ? 0 : tail) + lane : s.head + (v + lane) * VE;
+        const int32_t mine = loose ? (lane < (g == 0 ? s.head : r.V - tail)) : v + lane < v1 ? VE : 0;
+        for (int32_t e = 0; e < VE; ++e) {  // (a lane's elements in their order)
+          uint32_t k = e < mine ? order_key(to_f(x[base + e])) : 0;
+          while (true) {
+            const Best last = {__shfl_sync(~0u, list.key, a.K - 1), __shfl_sync(~0u, list.idx, a.K - 1)};
+            const bool good = k != 0 && in_front(k, base + e, last);
+            const uint32_t top = warp_max(good ? k : 0u);
+            if (top == 0) break;
+            const int from = __ffs(__ballot_sync(~0u, good && k == top)) - 1;
+            insert(list, top, __shfl_sync(~0u, base + e, from), lane);
+            if (lane == from) k = 0;
           }
-        const Best last = {__shfl_sync(~0u, list.key, a.K - 1), __shfl_sync(~0u, list.idx, a.K - 1)};
-        const bool good = mine != 0 && in_front(mine, base + which, last);
-        const uint32_t top = warp_max(good ? mine : 0u);
-        if (top == 0) break;
-        const int from = __ffs(__ballot_sync(~0u, good && mine == top)) - 1;
-        insert(list, top, __shfl_sync(~0u, base + which, from), lane);
-        if (lane == from) {
-#pragma unroll
-          for (int e = 0; e < VE; ++e)
-            if (e == which) k[e] = 0;
         }
       }
     }

@@ -188,6 +188,24 @@ def test_masked_words(dtype, vocab):
     check_grad(x, y, 1.0, idx, [p.astype(np.float64) for p in pulls], out, dtype)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("inv_t", [1.0, 100.0])
+@pytest.mark.parametrize("vocab", [60, 9000])
+def test_logits_at_the_ends_of_their_range(vocab, inv_t, dtype):
+    """The lowest value beside -inf and nothing else; neighbours of a large value;
+    both ends of the range in one row; ones next to a far smaller maximum."""
+    from fsdp_buffer_layout_gb300.objectives import TokenScores
+    top, rng = torch.finfo(dtype).max, np.random.default_rng(vocab)
+    half = np.arange(vocab) % 2 == 0
+    v = np.stack([np.where(half, -top, -np.inf), np.where(half, 2.0**30, 2.0**30 * (1 - 2.0**-8)),
+                  np.where(half, top, -top), np.where(np.arange(vocab) < vocab - 1, -np.inf, -top),
+                  rng.normal(size=vocab) - 2.0**100, np.where(half, -200.0, -330.0)])
+    x = strided(v, dtype)
+    y = np.array([0, 2, 2, vocab - 1, 4, 6])
+    got = TokenScores(6, vocab, top_k=3, dtype=dtype, inv_temperature=inv_t).forward(x, dev(y, torch.int64))
+    check(x, y, inv_t, 3, got)
+
+
 @pytest.mark.parametrize("vocab", [30, 6001])
 def test_rows_that_give_nan(vocab):
     from fsdp_buffer_layout_gb300.objectives import TokenScores
