@@ -610,29 +610,32 @@ cudaError_t preference(const RowsArg& a, const PairIn& p, float* stats, float* l
   return launch_grad(r, w, grad, grad_ld, st);
 }
 
-// How rows of V words are cut for `tokens` of them. Pieces of 16 spans, fewer
-// where the warps would not all get one; groups as few as the second launch holds.
+// How rows of V words are cut for `tokens` of them. Pieces of 16 spans, of 4 or 8
+// where the warps would not all get one, longer where a row would have over 32 (128).
+constexpr int64_t kScoreWarps = kSms * kPartCtas * (kScoreThreads / 32);
 template <typename T>
 ScoreCut score_cut(int64_t tokens, int64_t V) {
   ScoreCut c = {};
   c.spans = (int32_t)std::max<int64_t>(1, (V / Vec<T>::n + 31) / 32);
-  while (((c.spans - 1) >> c.group) + 1 + 2 > kMaxGroupsRow) ++c.group;
   c.piece = 2;
-  const int64_t warps = kSms * kScoreCtas * (kScoreThreads / 32);
-  while (c.piece < 4 && tokens * c.spans > (warps << (c.piece + 1))) ++c.piece;
-  c.piece = std::max(c.piece, c.group);
+  while (c.piece < 4 && tokens * c.spans > (kScoreWarps << (c.piece + 1))) ++c.piece;
+  while (((c.spans - 1) >> c.piece) + 1 > (c.piece < 4 ? 128 : 32)) ++c.piece;
   c.pieces = ((c.spans - 1) >> c.piece) + 1;
-  c.groups = ((c.spans - 1) >> c.group) + 1 + 2;
   return c;
 }
 
-// Workspace: the head, then per token and piece {m, s, u}, then per token the
-// groups' keys. Sized for the smallest pieces, which fewer tokens would get.
+// Workspace: the head, then per token and piece {m, s, u}, then the lanes' keys. Sized
+// for every call of up to so many tokens: fewer of them get smaller pieces.
 struct ScoreWs {
   static size_t bytes(int64_t tokens, int64_t V, int32_t dtype, int64_t K) {
-    const ScoreCut c = dtype == VSF_BF16 ? score_cut<uint16_t>(0, V) : score_cut<float>(0, V);
-    return sizeof(WsHead) + (size_t)tokens * c.pieces * 16 +
-           (K > 0 ? ((size_t)tokens * c.groups * 4 + 15) / 16 * 16 : 0);
+    auto cut = [&](int64_t t) {
+      return dtype == VSF_BF16 ? score_cut<uint16_t>(t, V) : score_cut<float>(t, V);
+    };
+    const int64_t spans = cut(0).spans;
+    int64_t most = 0;
+    for (const int64_t t : {std::min(tokens, kScoreWarps * 8 / spans), std::min(tokens, kScoreWarps * 16 / spans), tokens})
+      most = std::max(most, t * cut(t).pieces);
+    return sizeof(WsHead) + (size_t)most * (16 + (K > 0 ? 128 : 0));
   }
 };
 

@@ -9,13 +9,16 @@
 //   (a 1[v = y] + sum_j b_j 1[v = top_j] - p_v (a + sum_j b_j + h (z_v - u / s))) / temperature.
 //
 // A row is cut into pieces, a warp takes a piece: {m, s, u} of its elements, and
-// the largest element of each of its groups of consecutive elements (a group is
-// what one load instruction of the warp covers, 512 bytes, more only in rows that
-// have over 1000 of them). A second launch, a warp a row, joins the pieces and
-// picks the alternatives: the k largest elements (ties to the lowest index) lie in
-// the k groups of largest maxima (ties to the lowest group). For were one of them
-// in another group, each of those k groups would hold an element in front of it.
-// So it reads 512 k bytes of the row again, whatever the logits are.
+// each lane's largest element. What a lane has of a piece is a group: there are at
+// most 1024 of them in most rows, and the k largest elements lie in those groups
+// whose maxima are not below the k-th largest of all groups' maxima. A second launch,
+// a warp a row, joins the pieces and ranks the elements of those groups (32 times 512
+// bytes at most, unless maxima are equal); where equal ones are too many, it goes
+// through the whole row.
+//
+// m is a reference for the exponents, not the maximum: the largest of a lane's first
+// vectors, moved only where an element lies 16 units of ln 2 above it. A sum's terms
+// then reach 2^23 at most, and no lane waits for another.
 
 // Order of floats as whole numbers: -0 as 0; 0 is left for "no element".
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -31,15 +34,13 @@ constexpr int kScoreThreads = 256;
 constexpr int kScoreCtas = 4;        // an SM (gradient)
 constexpr int kPartCtas = 3;         // an SM (sums)
 constexpr int kScoreBatch = 4;       // vectors of a lane on their way at a time
-constexpr int kMaxGroupsRow = 1024;  // groups of a row, its loose elements among them
 constexpr int kMaxTop = 32;
 
-// How rows are cut: `spans` of 32 vectors, pieces of 2^piece spans, groups of
-// 2^group. Group 0 are the elements in front of the first vector, the last one
-// those behind the last vector.
+// How rows are cut: `spans` of 32 vectors, pieces of 2^piece spans. The elements in
+// front of a row's first 16-byte boundary belong to the first piece, those behind
+// the last vector to the last.
 struct ScoreCut {
-  int32_t spans, piece, group;
-  int32_t pieces, groups;
+  int32_t spans, piece, pieces;
 };
 
 template <typename T>
@@ -48,7 +49,7 @@ struct ScoreArgs {
   ScoreCut cut;
   int32_t K;
   float4* part;    // [T, pieces] m, s, u (in units of ln 2), -
-  uint32_t* keys;  // [T, groups], written where K > 0
+  uint32_t* keys;  // [T, pieces, 32] of the lanes' maxima, written where K > 0
   float *logp, *entropy, *top_logp;
   float4* norm;    // [T] m, s, u / s, -
   int32_t* top_idx;
@@ -91,16 +92,17 @@ __device__ __forceinline__ uint32_t raised(uint32_t w, uint32_t floor, float) {
   return __float_as_uint(r);
 }
 
-// What a warp has of a piece: the maximum, the same in all lanes, and each lane's sums.
+// What a lane has of a piece.
 template <typename T>
 struct ScoreSums {
-  float m = -INFINITY;
+  float m = -INFINITY, most = -INFINITY;  // the reference; where it is moved
   F2 nm = f2(0.f, 0.f);
   uint32_t floor;
   F2 sum0 = f2(0.f, 0.f), sum1 = f2(0.f, 0.f), zum0 = f2(0.f, 0.f), zum1 = f2(0.f, 0.f);
   __device__ __forceinline__ ScoreSums(float units) : floor(score_floor(0.f, units, T())) {}
+  // bm: the largest of the elements to be added; units: 200 units of ln 2
   __device__ __forceinline__ void to(float bm, Log2Scale c, float units) {
-    if (!(bm > m)) return;
+    if (!(bm > most)) return;
     if (m != -INFINITY) {
       const float d = fmaxf(__fmaf_rn(m - bm, c.hi, (m - bm) * c.lo), -1e20f), f = ex2(d);
       const F2 dd = f2(d, d), ff = f2(f, f);
@@ -110,11 +112,12 @@ struct ScoreSums {
       sum1 = f2_mul(sum1, ff);
     }
     m = bm;
+    most = __fmaf_rn(units, 0.08f, m);
     nm = f2(-m, -m);
     floor = score_floor(m, units, T());
   }
-  // c: this thread's factor, rounded down or up (Log2Scale)
   __device__ __forceinline__ bool out_of_range() const { return floor == Vec<T>::lowest; }
+  // c: this thread's factor, rounded down or up (Log2Scale)
   template <bool FAR>
   __device__ __forceinline__ void add(const uint4& v, F2 c) {
     Pairs<T> q;
@@ -144,8 +147,10 @@ struct ScoreSums {
   }
 };
 
-// {m, s, u} of a piece and its groups' keys; a warp a piece. Two batches of loads
-// are on their way at a time.
+// {m, s, u} of a piece and its lanes' keys; a warp a piece. Two batches of loads
+// are on their way at a time. (A ring of bulk copies for each warp, across pieces, took
+// 14 instructions an element instead of 9 and 227 us instead of 188 for 4096 x 131072
+// bf16, 3/4 live, with 20 alternatives.)
 template <typename T>
 __global__ void __launch_bounds__(kScoreThreads, kPartCtas)
     score_part_kernel(const __grid_constant__ ScoreArgs<T> a) {
@@ -172,101 +177,76 @@ __global__ void __launch_bounds__(kScoreThreads, kPartCtas)
     const T* x = r.x + t * r.ld;
     const Span s = span_of(x, r.V);
     const uint4* in = reinterpret_cast<const uint4*>(x + s.head) + lane;
-    uint32_t* keys = a.K > 0 ? a.keys + t * a.cut.groups : nullptr;
-    const int32_t span0 = p << a.cut.piece, span1 = min(span0 + (1 << a.cut.piece), a.cut.spans);
+    const int32_t v0 = (p << a.cut.piece) * 32, v1 = min(v0 + (32 << a.cut.piece), s.nvec);
     ScoreSums<T> sums(units);
-    uint32_t group_key = 0;
-    // the maxima of B spans from b on, n of which the row has
-    auto add = [&](const uint4 (&v)[B], int32_t b, int32_t n) {
-      float gm[B], top = -INFINITY, mine = -INFINITY;
+    float top = -INFINITY;
+    int32_t v = v0;
+    if (!far && v + 32 * B <= v1) {
+      // whole batches, by turns in two sets of registers
+      uint4 q0[B], q1[B];
+      auto load = [&](uint4 (&q)[B], int32_t at) {
 #pragma unroll
-      for (int j = 0; j < B; ++j) {
-        const uint4 one[1] = {v[j]};
-        gm[j] = warp_max(largest(one, T()));
-        top = fmaxf(top, gm[j]);
-        if (lane == j) mine = gm[j];
+        for (int j = 0; j < B; ++j) q[j] = __ldcs(in + at + 32 * j);
+      };
+      auto add = [&](const uint4 (&q)[B]) -> bool {
+        const float bm = largest(q, T());
+        top = fmaxf(top, bm);
+        sums.to(bm, r.c, units);
+        if (__any_sync(~0u, sums.out_of_range())) return false;
+#pragma unroll
+        for (int j = 0; j < B; ++j) sums.template add<false>(q[j], cc);
+        v += 32 * B;
+        return true;
+      };
+      load(q0, v);
+      while (true) {
+        const bool more1 = v + 64 * B <= v1;
+        if (more1) load(q1, v + 32 * B);
+        if (!add(q0) || !more1) break;
+        const bool more0 = v + 64 * B <= v1;
+        if (more0) load(q0, v + 32 * B);
+        if (!add(q1) || !more0) break;
       }
-      if (keys != nullptr) {
-        const uint32_t key = lane < n && (b + lane) * 32 < s.nvec ? order_key(mine) : 0;
-        if (a.cut.group == 0) {
-          if (lane < n) keys[1 + b + lane] = key;
-        } else {
-          for (int j = 0; j < n; ++j) {
-            group_key = max(group_key, __shfl_sync(~0u, key, j));
-            const int32_t next = b + j + 1;
-            if ((next & ((1 << a.cut.group) - 1)) == 0 || next == a.cut.spans) {
-              if (lane == 0) keys[1 + (b + j >> a.cut.group)] = group_key;
-              group_key = 0;
-            }
-          }
-        }
-      }
-      sums.to(top, r.c, units);
-      if (far || sums.out_of_range()) {
-#pragma unroll
-        for (int j = 0; j < B; ++j) sums.template add<true>(v[j], cc);
-      } else {
-#pragma unroll
-        for (int j = 0; j < B; ++j) sums.template add<false>(v[j], cc);
-      }
-    };
-    const int32_t whole = min(span1, s.nvec / 32) - span0;  // spans without a missing vector
-    int32_t b = span0;
-    if (whole >= B) {
-      uint4 v[B];
-#pragma unroll
-      for (int j = 0; j < B; ++j) v[j] = __ldcs(in + (b + j) * 32);
-#pragma unroll 2
-      for (; b + 2 * B <= span0 + whole; b += B) {
-        uint4 w[B];
-#pragma unroll
-        for (int j = 0; j < B; ++j) w[j] = __ldcs(in + (b + B + j) * 32);
-        add(v, b, B);
-#pragma unroll
-        for (int j = 0; j < B; ++j) v[j] = w[j];
-      }
-      add(v, b, B);
-      b += B;
     }
-    for (; b < span1; b += B) {  // (less than a batch, or the row's end)
-      uint4 v[B];
-#pragma unroll
-      for (int j = 0; j < B; ++j) {
-        v[j] = make_uint4(Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest);
-        if (b + j < span1 && (b + j) * 32 + lane < s.nvec) v[j] = __ldcs(in + (b + j) * 32);
-      }
-      add(v, b, min(B, span1 - b));
+#pragma unroll 1
+    for (; v < v1; v += 32) {  // less than a batch, or what is out of range
+      uint4 q[1] = {make_uint4(Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest)};
+      if (v + lane < v1) q[0] = __ldcs(in + v);
+      const float bm = largest(q, T());
+      top = fmaxf(top, bm);
+      sums.to(bm, r.c, units);
+      sums.template add<true>(q[0], cc);
     }
+    if (a.K > 0) a.keys[(t * pieces + p) * 32 + lane] = v0 + lane < v1 ? order_key(top) : 0;
     if (p == 0 || p + 1 == pieces) {
       // the loose elements, in front of the vectors and behind them
       const int32_t tail = s.head + s.nvec * VE;
       int32_t loose = -1;
       if (p == 0 && lane < s.head) loose = lane;
       if (p + 1 == pieces && lane >= 16 && lane - 16 < r.V - tail) loose = tail + (lane - 16);
-      const float xl = loose >= 0 ? to_f(x[loose]) : -INFINITY;
-      if (keys != nullptr) {
-        const uint32_t k = loose >= 0 ? order_key(xl) : 0;
-        const uint32_t front = warp_max(lane < 16 ? k : 0), back = warp_max(lane < 16 ? 0 : k);
-        if (lane == 0 && p == 0) keys[0] = front;
-        if (lane == 0 && p + 1 == pieces) keys[a.cut.groups - 1] = back;
-      }
-      sums.to(warp_max(xl), r.c, units);
-      const PairScale c2 = {f2(r.c.hi, r.c.hi), f2(r.c.lo, r.c.lo)};
-      const float z = -finite_max(sums.m);
-      F2 zz, ee;
-      score_terms(f2(xl, -INFINITY), f2(z, z), c2, zz, ee);
       if (loose >= 0) {
+        const float xl = to_f(x[loose]);
+        sums.to(xl, r.c, units);
+        const PairScale c2 = {f2(r.c.hi, r.c.hi), f2(r.c.lo, r.c.lo)};
+        const float z = -finite_max(sums.m);
+        F2 zz, ee;
+        score_terms(f2(xl, -INFINITY), f2(z, z), c2, zz, ee);
         sums.sum0 = f2_add(sums.sum0, ee);
         sums.zum0 = f2_fma(zz, ee, sums.zum0);
       }
     }
+    // the lanes' join, by expf (see the join of the losses' sums)
     float s0, s1, s2, s3, u0, u1, u2, u3;
     f2_get(sums.sum0, s0, s1);
     f2_get(sums.sum1, s2, s3);
     f2_get(sums.zum0, u0, u1);
     f2_get(sums.zum1, u2, u3);
-    const float sum = warp_sum((s0 + s1) + (s2 + s3)), zum = warp_sum((u0 + u1) + (u2 + u3));
-    if (lane == 0) a.part[t * pieces + p] = make_float4(sums.m, sum, zum, 0.f);
+    const float m = warp_max(sums.m), d = sums.m - finite_max(m), f = expf(d * r.inv_tf);
+    const float own = (s0 + s1) + (s2 + s3);
+    const float shift = fmaxf(__fmaf_rn(d, r.c.hi, d * r.c.lo), -1e20f);
+    const float sum = warp_sum(own == 0.f ? 0.f : f * own);
+    const float zum = warp_sum(own == 0.f ? 0.f : f * __fmaf_rn(own, shift, (u0 + u1) + (u2 + u3)));
+    if (lane == 0) a.part[t * pieces + p] = make_float4(m, sum, zum, 0.f);
   }
 }
 
@@ -287,16 +267,15 @@ __device__ __forceinline__ void insert(Best& list, uint32_t key, int32_t idx, in
   else if (lane > at) list = {k, i};
 }
 
-// The K best of up to kScoreCandidates entries in shared memory, in any order, into
-// lanes 0 .. K-1: each entry's place is the number of those in front of it. A lane
-// without one gets {0, -1}.
-constexpr int kScoreCandidates = 128;
+// The K best of n entries in shared memory, in any order, into lanes 0 .. K-1: each
+// entry's place is the number of those in front of it. A lane without one gets {0, -1}.
 __device__ __forceinline__ Best best_of(const Best* list, int n, int K, Best* out, int lane) {
   out[lane] = {0, -1};
   __syncwarp();
   for (int i0 = 0; i0 < n; i0 += 32) {
     const Best own = i0 + lane < n ? list[i0 + lane] : Best{0, INT32_MAX};
     int at = 0;
+#pragma unroll 4
     for (int j = 0; j < n; ++j) {
       const Best b = list[j];
       at += in_front(b.key, b.idx, own);
@@ -307,14 +286,84 @@ __device__ __forceinline__ Best best_of(const Best* list, int n, int K, Best* ou
   return out[lane];
 }
 
+// The K best of a whole row, in its order: where equal elements are too many to be
+// gathered. Once the list has K elements, a later one belongs to it only if it is
+// larger than the K-th, so most vectors cost their load and their maximum.
+template <typename T>
+__device__ __noinline__ Best best_of_row(const T* x, int32_t V, int K, int lane) {
+  constexpr int VE = Vec<T>::n, B = 4;
+  Best list = {0, INT32_MAX};
+  // the elements k[] of the lanes, a lane's from index `base` on; 0: none
+  auto take = [&](uint32_t (&k)[VE], int32_t base) {
+    while (true) {
+      uint32_t mine = 0;
+      int32_t which = 0;
+#pragma unroll
+      for (int e = 0; e < VE; ++e)
+        if (k[e] > mine) {
+          mine = k[e];
+          which = e;
+        }
+      const uint32_t last = __shfl_sync(~0u, list.key, K - 1);
+      const uint32_t top = warp_max(mine > last ? mine : 0u);
+      if (top == 0) break;
+      const int from = __ffs(__ballot_sync(~0u, mine == top)) - 1;
+      insert(list, top, __shfl_sync(~0u, base + which, from), lane);
+#pragma unroll
+      for (int e = 0; e < VE; ++e)
+        if (lane == from && e == which) k[e] = 0;
+    }
+  };
+  const Span s = span_of(x, V);
+  const int32_t tail = s.head + s.nvec * VE;
+  uint32_t k[VE];
+#pragma unroll
+  for (int e = 0; e < VE; ++e) k[e] = 0;
+  if (lane < s.head) k[0] = order_key(to_f(x[lane]));
+  take(k, lane);
+  const uint4* in = reinterpret_cast<const uint4*>(x + s.head);
+  for (int32_t v = 0; v < s.nvec; v += 32 * B) {
+    uint4 q[B];
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      q[j] = make_uint4(Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest);
+      if (v + 32 * j + lane < s.nvec) q[j] = in[v + 32 * j + lane];
+    }
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      const int32_t at = v + 32 * j + lane;
+      const uint4 one[1] = {q[j]};
+      const uint32_t last = __shfl_sync(~0u, list.key, K - 1);
+      if (!__any_sync(~0u, at < s.nvec && order_key(largest(one, T())) > last)) continue;
+      Pairs<T> pr;
+      unpack(q[j], pr);
+#pragma unroll
+      for (int e = 0; e < VE / 2; ++e) {
+        float f0, f1;
+        f2_get(pr.p[e], f0, f1);
+        k[2 * e] = at < s.nvec ? order_key(f0) : 0;
+        k[2 * e + 1] = at < s.nvec ? order_key(f1) : 0;
+      }
+      take(k, s.head + at * VE);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < VE; ++e) k[e] = 0;
+  if (lane < V - tail) k[0] = order_key(to_f(x[tail + lane]));
+  take(k, tail + lane);
+  return list;
+}
+
 // Joins a row's pieces and picks its alternatives; a warp a row.
+constexpr int kScoreCandidates = 128;
 template <typename T>
 __global__ void __launch_bounds__(kScoreThreads)
     score_row_kernel(const __grid_constant__ ScoreArgs<T> a) {
-  constexpr int VE = Vec<T>::n, NG = kMaxGroupsRow / 32, W = kScoreThreads / 32, C = kScoreCandidates;
-  __shared__ Best candidates[W][C];
+  constexpr int VE = Vec<T>::n, W = kScoreThreads / 32, C = kScoreCandidates;
+  __shared__ Best groups[W][C];
+  __shared__ Best elements[W][C];
   __shared__ Best sorted[W][32];
-  __shared__ int32_t count[W];
+  __shared__ int32_t counts[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Rows<T>& r = a.r;
   take_turn();
@@ -336,14 +385,13 @@ __global__ void __launch_bounds__(kScoreThreads)
   }
   const T* x = r.x + t * r.ld;
   const float xy = to_f(x[y]);
-  // ---- the groups' keys, on their way meanwhile
-  const uint32_t* keys = a.K > 0 ? a.keys + t * a.cut.groups : nullptr;
-  uint32_t key[NG];
-#pragma unroll
-  for (int j = 0; j < NG; ++j) {
-    key[j] = 0;
-    if (a.K == 0 || j * 32 >= a.cut.groups) continue;
-    if (j * 32 + lane < a.cut.groups) key[j] = keys[j * 32 + lane];
+  // ---- each lane's largest key of the groups lane, lane + 32, ...
+  const int32_t n_keys = a.cut.pieces * 32;
+  const uint32_t* keys = a.keys + t * n_keys + lane;
+  uint32_t best = 0;
+  if (a.K > 0) {
+#pragma unroll 8
+    for (int32_t g = 0; g < n_keys; g += 32) best = max(best, keys[g]);
   }
   // ---- the pieces
   float m = -INFINITY, sum = 0.f, zum = 0.f;
@@ -376,161 +424,85 @@ __global__ void __launch_bounds__(kScoreThreads)
     }
     return;
   }
-  // ---- the K groups of largest maxima; lane i holds the i-th. The K-th largest
-  // of the lanes' largest keys is not above the K-th largest key: what is below it
-  // is left out, the others are ranked. Too many of them (equal maxima): one by one.
-  uint32_t best = 0;
-  int32_t at = 0;
+  // ---- the groups that count. The K-th largest of the lanes' largest keys is not
+  // above the K-th largest key: groups below it are left out, the others ranked.
+  int before = 0;
 #pragma unroll
-  for (int j = 0; j < NG; ++j) {
-    if (j * 32 >= a.cut.groups) continue;
-    if (key[j] > best) {
-      best = key[j];
-      at = j;
-    }
+  for (int l = 0; l < 32; ++l) {
+    const uint32_t k = __shfl_sync(~0u, best, l);
+    before += k > best || (k == best && l < lane);
   }
-  uint32_t least = 0;
-  {
-    int before = 0;
-#pragma unroll
-    for (int l = 0; l < 32; ++l) {
-      const uint32_t k = __shfl_sync(~0u, best, l);
-      before += k > best || (k == best && l < lane);
-    }
-    least = __shfl_sync(~0u, best, __ffs(__ballot_sync(~0u, before == a.K - 1)) - 1);
+  const uint32_t least =
+      max(1u, __shfl_sync(~0u, best, __ffs(__ballot_sync(~0u, before == a.K - 1)) - 1));
+  int n_groups = 0;
+  for (int32_t g = 0; g < n_keys; g += 32) {
+    const uint32_t k = keys[g];
+    const uint32_t in = __ballot_sync(~0u, k >= least);
+    const int to = n_groups + __popc(in & ((1u << lane) - 1));
+    if (k >= least && to < C) groups[warp][to] = {k, g + lane};
+    n_groups += __popc(in);
   }
-  least = max(least, 1u);
-  int n = 0;
-#pragma unroll
-  for (int j = 0; j < NG; ++j) {
-    if (j * 32 >= a.cut.groups) continue;
-    n += key[j] >= least;
-  }
-  int upto = n;  // entries of the lanes up to this one
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(~0u, upto, o);
-    if (lane >= o) upto += v;
-  }
-  const int total = __shfl_sync(~0u, upto, 31);
-  Best group = {0, -1};
-  if (total <= C) {
-    int to = upto - n;
-#pragma unroll
-    for (int j = 0; j < NG; ++j) {
-      if (j * 32 >= a.cut.groups) continue;
-      if (key[j] >= least) candidates[warp][to++] = {key[j], j * 32 + lane};
-    }
-    __syncwarp();
-    group = best_of(candidates[warp], total, a.K, sorted[warp], lane);
-  } else {
-    for (int i = 0; i < a.K; ++i) {
-      const uint32_t top = warp_max(best);
-      if (top == 0) break;  // fewer groups than that
-      const int32_t g = (int32_t)__reduce_min_sync(~0u, best == top ? (uint32_t)(at * 32 + lane) : ~0u);
-      if (lane == i) group = {top, g};
-      if (lane == (g & 31)) {
-        best = 0;
-        const int32_t out = at;
-#pragma unroll
-        for (int j = 0; j < NG; ++j) {
-          if (j * 32 >= a.cut.groups) continue;
-          if (j == out) key[j] = 0;
-          if (key[j] > best) {
-            best = key[j];
-            at = j;
-          }
-        }
-      }
-    }
-  }
-  if (lane >= a.K) group = {0, -1};
-  // ---- their elements. None below the last group's maximum is among the K; those
-  // that are not are gathered, whatever their order, and ranked; too many: one by one.
-  const Span s = span_of(x, r.V);
-  const uint4* in = reinterpret_cast<const uint4*>(x + s.head) + lane;
-  const int32_t tail = s.head + s.nvec * VE;
-  const uint32_t last_key = __shfl_sync(~0u, group.key, a.K - 1);
-  const float low = last_key == 0 ? -INFINITY : key_value(last_key);
-  if (lane == 0) count[warp] = 0;
   __syncwarp();
-  auto gathered = [&](float v, int32_t idx) {
-    if (v >= low) {
-      const int to = atomicAdd(&count[warp], 1);
-      if (to < C) candidates[warp][to] = {order_key(v), idx};
-    }
-  };
-  constexpr int GB = 4;  // groups on their way at a time
-  for (int i0 = 0; i0 < a.K; i0 += GB) {
-    const int32_t spans = 1 << a.cut.group;
-    for (int32_t q = 0; q < spans; ++q) {
-      uint4 v[GB];
-      int32_t base[GB];
+  Best list = {0, -1};
+  bool whole = n_groups > C;
+  if (!whole) {
+    const uint32_t last = __shfl_sync(~0u, best_of(groups[warp], n_groups, a.K, sorted[warp], lane).key, a.K - 1);
+    const float low = last == 0 ? -INFINITY : key_value(last);
+    // ---- their elements that are not below the K-th group's maximum, and the loose ones
+    const Span s = span_of(x, r.V);
+    const int32_t tail = s.head + s.nvec * VE;
+    if (lane == 0) counts[warp] = 0;
+    __syncwarp();
+    auto gather = [&](float v, int32_t idx) {
+      if (v >= low) {
+        const int to = atomicAdd(&counts[warp], 1);
+        if (to < C) elements[warp][to] = {order_key(v), idx};
+      }
+    };
+    if (lane < s.head) gather(to_f(x[lane]), lane);
+    if (lane < r.V - tail) gather(to_f(x[tail + lane]), tail + lane);
+    const uint4* in = reinterpret_cast<const uint4*>(x + s.head);
+    const int log = a.cut.piece;  // a group has 2^log vectors
+    const int64_t n_vecs = (int64_t)n_groups << log;
+    constexpr int B = 4;
+    for (int64_t i0 = lane; i0 < n_vecs; i0 += 32 * B) {
+      uint4 q[B];
+      int32_t at[B];
 #pragma unroll
-      for (int i = 0; i < GB; ++i) {
-        const int32_t g = i0 + i < a.K ? __shfl_sync(~0u, group.idx, (i0 + i) & 31) : -1;
-        base[i] = -1;
-        if (g < 0) continue;
-        if (g == 0 || g + 1 == a.cut.groups) {  // loose elements
-          const int32_t e = g == 0 ? 0 : tail;
-          if (q == 0 && lane < (g == 0 ? s.head : r.V - tail)) gathered(to_f(x[e + lane]), e + lane);
-          continue;
-        }
-        const int32_t at_v = ((g - 1 << a.cut.group) + q) * 32;
-        if (at_v + lane >= s.nvec) continue;
-        base[i] = s.head + (at_v + lane) * VE;
-        v[i] = in[at_v];
+      for (int j = 0; j < B; ++j) {
+        const int64_t i = i0 + 32 * j;
+        at[j] = -1;
+        if (i >= n_vecs) continue;
+        const Best g = groups[warp][i >> log];
+        if (g.key < last) continue;
+        const int32_t v = ((((g.idx >> 5) << log) + (int32_t)(i & ((1 << log) - 1))) << 5) + (g.idx & 31);
+        if (v >= s.nvec) continue;
+        at[j] = v;
+        q[j] = in[v];
       }
 #pragma unroll
-      for (int i = 0; i < GB; ++i) {
-        if (base[i] < 0) continue;
-        const uint4 one[1] = {v[i]};
+      for (int j = 0; j < B; ++j) {
+        if (at[j] < 0) continue;
+        const uint4 one[1] = {q[j]};
         if (!(largest(one, T()) >= low)) continue;
         Pairs<T> pr;
-        unpack(v[i], pr);
+        unpack(q[j], pr);
+        const int32_t base = s.head + at[j] * VE;
 #pragma unroll
         for (int e = 0; e < VE / 2; ++e) {
           float f0, f1;
           f2_get(pr.p[e], f0, f1);
-          gathered(f0, base[i] + 2 * e);
-          gathered(f1, base[i] + 2 * e + 1);
+          gather(f0, base + 2 * e);
+          gather(f1, base + 2 * e + 1);
         }
       }
     }
+    __syncwarp();
+    const int found = counts[warp];
+    whole = found > C;
+    if (!whole) list = best_of(elements[warp], found, a.K, sorted[warp], lane);
   }
-  __syncwarp();
-  const int found = count[warp];
-  Best list;
-  if (found <= C) {
-    list = best_of(candidates[warp], found, a.K, sorted[warp], lane);
-  } else {
-    list = {last_key, INT32_MAX};
-    for (int i = 0; i < a.K; ++i) {
-      const uint32_t gk = __shfl_sync(~0u, group.key, i);
-      const int32_t g = __shfl_sync(~0u, group.idx, i);
-      // (lanes behind the list's K are never looked at)
-      if (g < 0 || gk < __shfl_sync(~0u, list.key, a.K - 1)) break;
-      const bool loose = g == 0 || g + 1 == a.cut.groups;
-      const int32_t v0 = loose ? 0 : (g - 1 << a.cut.group) * 32;
-      const int32_t v1 = loose ? 32 : min(v0 + (32 << a.cut.group), s.nvec);
-      for (int32_t v = v0; v < v1; v += 32) {
-        const int32_t base = loose ? (g == 0 ? 0 : tail) + lane : s.head + (v + lane) * VE;
-        const int32_t mine = loose ? (lane < (g == 0 ? s.head : r.V - tail)) : v + lane < v1 ? VE : 0;
-        for (int32_t e = 0; e < VE; ++e) {  // (a lane's elements in their order)
-          uint32_t k = e < mine ? order_key(to_f(x[base + e])) : 0;
-          while (true) {
-            const Best last = {__shfl_sync(~0u, list.key, a.K - 1), __shfl_sync(~0u, list.idx, a.K - 1)};
-            const bool good = k != 0 && in_front(k, base + e, last);
-            const uint32_t top = warp_max(good ? k : 0u);
-            if (top == 0) break;
-            const int from = __ffs(__ballot_sync(~0u, good && k == top)) - 1;
-            insert(list, top, __shfl_sync(~0u, base + e, from), lane);
-            if (lane == from) k = 0;
-          }
-        }
-      }
-    }
-  }
+  if (whole) list = best_of_row(x, r.V, a.K, lane);
   if (lane < a.K) {
     a.top_idx[t * a.K + lane] = list.idx;
     a.top_logp[t * a.K + lane] = log_ratio(key_value(list.key) - m, r.inv_tf, 0.f, ls);

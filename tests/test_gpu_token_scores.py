@@ -152,7 +152,9 @@ def test_ties(dtype, vocab):
     v = np.stack([np.zeros(vocab), np.where(np.arange(vocab) % 2, 0.0, -0.0), rng.integers(0, 3, vocab),
                   np.arange(vocab)[::-1] // 9, -np.arange(vocab) // 300 * 1.0,
                   np.where(np.arange(vocab) < vocab - 3, 1.0, 1.0), rng.integers(-2, 2, vocab) * 1e-38])
-    x = strided(v, dtype)
+    v[1, ::7] = 1.0
+    v = np.concatenate([v, np.arange(vocab)[None] % 250 * 0.5, np.arange(vocab)[None] // 300 * 0.25])
+    x = strided(v, dtype, pad=1, shift=3)
     y = np.zeros(len(v), np.int64)
     for k in (1, 5, 32):
         check(x, y, 1.0, k, TokenScores(len(v), vocab, top_k=k, dtype=dtype).forward(x, dev(y, torch.int64)))
