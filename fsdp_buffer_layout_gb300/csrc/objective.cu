@@ -663,8 +663,8 @@ cudaError_t scores(const RowsArg& a, int32_t K, float* logp, float* entropy, int
   const cudaError_t e = launch_behind(score_part_kernel<T>, score_grid(a.T_ * k.cut.pieces, kPartCtas),
                                       kScoreThreads, 0, 1, st, k);
   if (e != cudaSuccess) return e;
-  return launch_behind(score_row_kernel<T>, (unsigned)((a.T_ * 32 + kScoreThreads - 1) / kScoreThreads),
-                       kScoreThreads, 0, 1, st, k);
+  return launch_behind(k.cut.pieces <= 32 ? score_row_kernel<T, 8> : score_row_kernel<T, 32>, (unsigned)a.T_,
+                       kRowScoreThreads, 0, 1, st, k);
 }
 
 template <typename T>

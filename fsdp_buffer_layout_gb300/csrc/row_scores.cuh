@@ -11,9 +11,9 @@
 // A row is cut into pieces, a warp takes a piece: {m, s, u} of its elements, and
 // each lane's largest element. What a lane has of a piece is a group: there are at
 // most 1024 of them in most rows, and the k largest elements lie in those groups
-// whose maxima are not below the k-th largest of all groups' maxima. A second launch,
-// a warp a row, joins the pieces and ranks the elements of those groups (32 times 512
-// bytes at most, unless maxima are equal); where equal ones are too many, it goes
+// whose maxima are not below the k-th largest of all groups' maxima. A second launch, a
+// CTA a row, joins the pieces and ranks the elements of those groups (k times 512 bytes
+// or little more, unless maxima are equal); where equal ones are too many, it goes
 // through the whole row.
 //
 // m is a reference for the exponents, not the maximum: the largest of a lane's first
@@ -147,47 +147,75 @@ struct ScoreSums {
   }
 };
 
-// {m, s, u} of a piece and its lanes' keys; a warp a piece. Two batches of loads
-// are on their way at a time. (A ring of bulk copies for each warp, across pieces, took
-// 14 instructions an element instead of 9 and 227 us instead of 188 for 4096 x 131072
-// bf16, 3/4 live, with 20 alternatives.)
+// {m, s, u} of a piece and its lanes' keys; a warp a piece. Two batches of loads are
+// on their way at a time, the first of the next piece while this one is finished. (A
+// ring of bulk copies for each warp, across pieces, took 14 instructions an element
+// instead of 9 and 227 us instead of 188 for 4096 x 131072 bf16, 3/4 live, with 20
+// alternatives.)
 template <typename T>
 __global__ void __launch_bounds__(kScoreThreads, kPartCtas)
     score_part_kernel(const __grid_constant__ ScoreArgs<T> a) {
   constexpr int VE = Vec<T>::n, B = kScoreBatch;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Rows<T>& r = a.r;
   const float c1 = (uint32_t)threadIdx.x * 2654435769u < r.c.ups ? r.c.up : r.c.hi;
   const F2 cc = f2(c1, c1);
   const bool far = far_temperature(r.inv_tf);
   const float units = 200.f / r.c.hi;
   take_turn();
-  const int32_t pieces = a.cut.pieces;
-  const int64_t step = (int64_t)gridDim.x * (kScoreThreads / 32);
-  const int64_t step_t = step / pieces, first = (int64_t)blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);
-  const int32_t step_p = (int32_t)(step - step_t * pieces);
-  int64_t t = first / pieces;
-  int32_t p = (int32_t)(first - t * pieces);
-  for (; t < r.T_; t += step_t, p += step_p) {
-    if (p >= pieces) {
-      p -= pieces;
-      if (++t >= r.T_) break;
+  const int32_t pieces = a.cut.pieces, step = (int32_t)gridDim.x * (kScoreThreads / 32);
+  const int32_t step_t = step / pieces, step_p = step % pieces;
+  // the piece ahead and its row's target
+  const int32_t first = (int32_t)blockIdx.x * (kScoreThreads / 32) + warp;
+  int64_t t_next = first / pieces;
+  int32_t p_next = first % pieces;
+  int64_t y_next = t_next < r.T_ ? r.target[t_next] : -1;
+  int64_t t = -1;
+  int32_t p = 0;
+  // to the next piece of a live row; those of masked rows are left out
+  auto find = [&]() {
+    while (t_next < r.T_) {
+      t = t_next;
+      p = p_next;
+      const int64_t y = y_next;
+      t_next += step_t;
+      p_next += step_p;
+      if (p_next >= pieces) {
+        p_next -= pieces;
+        ++t_next;
+      }
+      y_next = t_next < r.T_ ? r.target[t_next] : -1;
+      if (y >= 0 && y < r.V) return;
+      if (y >= 0 && p == 0 && lane == 0) atomicOr(&a.head->err, kErrTarget);
     }
-    if (live_target(r, t, p == 0 ? &a.head->err : nullptr) < 0) continue;
+    t = -1;
+  };
+  uint4 q0[B], q1[B];
+  const uint4* in = nullptr;
+  int32_t v = 0, v1 = 0, head = 0;
+  auto load = [&](uint4 (&q)[B], int32_t at) {
+#pragma unroll
+    for (int j = 0; j < B; ++j) q[j] = __ldcs(in + at + 32 * j);
+  };
+  auto open = [&]() {  // the piece's vectors, the first of them on their way
+    if (t < 0) return;
     const T* x = r.x + t * r.ld;
     const Span s = span_of(x, r.V);
-    const uint4* in = reinterpret_cast<const uint4*>(x + s.head) + lane;
-    const int32_t v0 = (p << a.cut.piece) * 32, v1 = min(v0 + (32 << a.cut.piece), s.nvec);
+    in = reinterpret_cast<const uint4*>(x + s.head) + lane;
+    head = s.head;
+    v = (p << a.cut.piece) * 32;
+    v1 = min(v + (32 << a.cut.piece), s.nvec);
+    if (!far && v + 32 * B <= v1) load(q0, v);
+  };
+  find();
+  open();
+  while (t >= 0) {
+    const int64_t t0 = t;
+    const int32_t p0 = p, v0 = v;
     ScoreSums<T> sums(units);
     float top = -INFINITY;
-    int32_t v = v0;
     if (!far && v + 32 * B <= v1) {
       // whole batches, by turns in two sets of registers
-      uint4 q0[B], q1[B];
-      auto load = [&](uint4 (&q)[B], int32_t at) {
-#pragma unroll
-        for (int j = 0; j < B; ++j) q[j] = __ldcs(in + at + 32 * j);
-      };
       auto add = [&](const uint4 (&q)[B]) -> bool {
         const float bm = largest(q, T());
         top = fmaxf(top, bm);
@@ -198,7 +226,6 @@ __global__ void __launch_bounds__(kScoreThreads, kPartCtas)
         v += 32 * B;
         return true;
       };
-      load(q0, v);
       while (true) {
         const bool more1 = v + 64 * B <= v1;
         if (more1) load(q1, v + 32 * B);
@@ -217,13 +244,17 @@ __global__ void __launch_bounds__(kScoreThreads, kPartCtas)
       sums.to(bm, r.c, units);
       sums.template add<true>(q[0], cc);
     }
-    if (a.K > 0) a.keys[(t * pieces + p) * 32 + lane] = v0 + lane < v1 ? order_key(top) : 0;
-    if (p == 0 || p + 1 == pieces) {
+    if (a.K > 0) a.keys[(t0 * pieces + p0) * 32 + lane] = v0 + lane < v1 ? order_key(top) : 0;
+    const int32_t head0 = head;
+    find();
+    open();
+    if (p0 == 0 || p0 + 1 == pieces) {
       // the loose elements, in front of the vectors and behind them
-      const int32_t tail = s.head + s.nvec * VE;
+      const T* x = r.x + t0 * r.ld;
+      const int32_t tail = head0 + (r.V - head0) / VE * VE;
       int32_t loose = -1;
-      if (p == 0 && lane < s.head) loose = lane;
-      if (p + 1 == pieces && lane >= 16 && lane - 16 < r.V - tail) loose = tail + (lane - 16);
+      if (p0 == 0 && lane < head0) loose = lane;
+      if (p0 + 1 == pieces && lane >= 16 && lane - 16 < r.V - tail) loose = tail + (lane - 16);
       if (loose >= 0) {
         const float xl = to_f(x[loose]);
         sums.to(xl, r.c, units);
@@ -246,7 +277,7 @@ __global__ void __launch_bounds__(kScoreThreads, kPartCtas)
     const float shift = fmaxf(__fmaf_rn(d, r.c.hi, d * r.c.lo), -1e20f);
     const float sum = warp_sum(own == 0.f ? 0.f : f * own);
     const float zum = warp_sum(own == 0.f ? 0.f : f * __fmaf_rn(own, shift, (u0 + u1) + (u2 + u3)));
-    if (lane == 0) a.part[t * pieces + p] = make_float4(m, sum, zum, 0.f);
+    if (lane == 0) a.part[t0 * pieces + p0] = make_float4(m, sum, zum, 0.f);
   }
 }
 
@@ -267,30 +298,12 @@ __device__ __forceinline__ void insert(Best& list, uint32_t key, int32_t idx, in
   else if (lane > at) list = {k, i};
 }
 
-// The K best of n entries in shared memory, in any order, into lanes 0 .. K-1: each
-// entry's place is the number of those in front of it. A lane without one gets {0, -1}.
-__device__ __forceinline__ Best best_of(const Best* list, int n, int K, Best* out, int lane) {
-  out[lane] = {0, -1};
-  __syncwarp();
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const Best own = i0 + lane < n ? list[i0 + lane] : Best{0, INT32_MAX};
-    int at = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-      const Best b = list[j];
-      at += in_front(b.key, b.idx, own);
-    }
-    if (i0 + lane < n && at < K) out[at] = own;
-  }
-  __syncwarp();
-  return out[lane];
-}
-
-// The K best of a whole row, in its order: where equal elements are too many to be
-// gathered. Once the list has K elements, a later one belongs to it only if it is
-// larger than the K-th, so most vectors cost their load and their maximum.
+// The K best of part `part` of `parts` of a whole row, in its order: where equal
+// elements are too many to be gathered. Once the list has K elements, a later one
+// belongs to it only if it is larger than the K-th, so most vectors cost their load
+// and their maximum. One warp; lane i holds the i-th best.
 template <typename T>
-__device__ __noinline__ Best best_of_row(const T* x, int32_t V, int K, int lane) {
+__device__ __noinline__ Best best_of_part(const T* x, int32_t V, int K, int part, int parts, int lane) {
   constexpr int VE = Vec<T>::n, B = 4;
   Best list = {0, INT32_MAX};
   // the elements k[] of the lanes, a lane's from index `base` on; 0: none
@@ -319,161 +332,190 @@ __device__ __noinline__ Best best_of_row(const T* x, int32_t V, int K, int lane)
   uint32_t k[VE];
 #pragma unroll
   for (int e = 0; e < VE; ++e) k[e] = 0;
-  if (lane < s.head) k[0] = order_key(to_f(x[lane]));
+  if (part == 0 && lane < s.head) k[0] = order_key(to_f(x[lane]));
   take(k, lane);
   const uint4* in = reinterpret_cast<const uint4*>(x + s.head);
-  for (int32_t v = 0; v < s.nvec; v += 32 * B) {
+  const int32_t end = (int32_t)((int64_t)s.nvec * (part + 1) / parts);
+  for (int32_t v = (int32_t)((int64_t)s.nvec * part / parts); v < end; v += 32 * B) {
     uint4 q[B];
 #pragma unroll
     for (int j = 0; j < B; ++j) {
       q[j] = make_uint4(Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest);
-      if (v + 32 * j + lane < s.nvec) q[j] = in[v + 32 * j + lane];
+      if (v + 32 * j + lane < end) q[j] = in[v + 32 * j + lane];
     }
 #pragma unroll
     for (int j = 0; j < B; ++j) {
       const int32_t at = v + 32 * j + lane;
       const uint4 one[1] = {q[j]};
       const uint32_t last = __shfl_sync(~0u, list.key, K - 1);
-      if (!__any_sync(~0u, at < s.nvec && order_key(largest(one, T())) > last)) continue;
+      if (!__any_sync(~0u, at < end && order_key(largest(one, T())) > last)) continue;
       Pairs<T> pr;
       unpack(q[j], pr);
 #pragma unroll
       for (int e = 0; e < VE / 2; ++e) {
         float f0, f1;
         f2_get(pr.p[e], f0, f1);
-        k[2 * e] = at < s.nvec ? order_key(f0) : 0;
-        k[2 * e + 1] = at < s.nvec ? order_key(f1) : 0;
+        k[2 * e] = at < end ? order_key(f0) : 0;
+        k[2 * e + 1] = at < end ? order_key(f1) : 0;
       }
       take(k, s.head + at * VE);
     }
   }
 #pragma unroll
   for (int e = 0; e < VE; ++e) k[e] = 0;
-  if (lane < V - tail) k[0] = order_key(to_f(x[tail + lane]));
+  if (part + 1 == parts && lane < V - tail) k[0] = order_key(to_f(x[tail + lane]));
   take(k, tail + lane);
   return list;
 }
 
-// Joins a row's pieces and picks its alternatives; a warp a row.
-constexpr int kScoreCandidates = 128;
-template <typename T>
-__global__ void __launch_bounds__(kScoreThreads)
+// Joins a row's pieces and picks its alternatives; a CTA a row. (A warp a row took 27
+// us for 4096 rows of 131072, 20 alternatives, and 14 for 64 of them: a chain of some
+// ten loads.) N: keys of a thread.
+constexpr int kRowScoreThreads = 128;
+constexpr int kScoreCandidates = 128;  // groups, and elements, that are ranked
+template <typename T, int N>
+__global__ void __launch_bounds__(kRowScoreThreads)
     score_row_kernel(const __grid_constant__ ScoreArgs<T> a) {
-  constexpr int VE = Vec<T>::n, W = kScoreThreads / 32, C = kScoreCandidates;
-  __shared__ Best groups[W][C];
-  __shared__ Best elements[W][C];
-  __shared__ Best sorted[W][32];
-  __shared__ int32_t counts[W];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int VE = Vec<T>::n, C = kScoreCandidates, W = kRowScoreThreads / 32;
+  static_assert(C == kRowScoreThreads, "a thread ranks an entry");
+  __shared__ Best groups[C], elements[C];
+  __shared__ uint32_t least_of[W], last_of;
+  __shared__ int32_t n_groups, n_elements;
+  __shared__ float row_m, row_sum;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Rows<T>& r = a.r;
   take_turn();
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.head->rows = 1;
-  const int64_t t = (int64_t)blockIdx.x * W + warp;
-  if (t >= r.T_) return;
+  if (blockIdx.x == 0 && tid == 0) a.head->rows = 1;
+  const int64_t t = blockIdx.x;
   const int32_t y = live_target(r, t, nullptr);
   if (y < 0) {
-    if (lane == 0) {
+    if (tid == 0) {
       a.logp[t] = 0.f;
       a.entropy[t] = 0.f;
       a.norm[t] = make_float4(0.f, 1.f, 0.f, 0.f);
     }
-    if (lane < a.K) {
-      a.top_idx[t * a.K + lane] = -1;
-      a.top_logp[t * a.K + lane] = 0.f;
+    if (tid < a.K) {
+      a.top_idx[t * a.K + tid] = -1;
+      a.top_logp[t * a.K + tid] = 0.f;
     }
     return;
   }
   const T* x = r.x + t * r.ld;
-  const float xy = to_f(x[y]);
-  // ---- each lane's largest key of the groups lane, lane + 32, ...
-  const int32_t n_keys = a.cut.pieces * 32;
-  const uint32_t* keys = a.keys + t * n_keys + lane;
-  uint32_t best = 0;
-  if (a.K > 0) {
-#pragma unroll 8
-    for (int32_t g = 0; g < n_keys; g += 32) best = max(best, keys[g]);
-  }
-  // ---- the pieces
-  float m = -INFINITY, sum = 0.f, zum = 0.f;
-  const float4* part = a.part + t * a.cut.pieces;
-  for (int32_t p = lane; p < a.cut.pieces; p += 32) m = fmaxf(m, part[p].x);
-  m = warp_max(m);
-  for (int32_t p = lane; p < a.cut.pieces; p += 32) {
-    const float4 q = part[p];
-    if (q.y == 0.f) continue;  // (nothing but -inf; a NaN goes on)
-    const float d0 = q.x - finite_max(m);
-    const float d = fmaxf(__fmaf_rn(d0, r.c.hi, d0 * r.c.lo), -1e20f);
-    const float f = expf(d0 * r.inv_tf);
-    sum += f * q.y;
-    zum += f * __fmaf_rn(q.y, d, q.z);
-  }
-  sum = warp_sum(sum);
-  zum = warp_sum(zum);
-  const LogSum ls = log_sum(sum);
-  const float mean = zum / sum * 0.693147181f;  // of z, by p
-  if (lane == 0) {
-    a.logp[t] = log_ratio(xy - m, r.inv_tf, 0.f, ls);
-    a.entropy[t] = __fmaf_rn(ls.k, 0.693359375f, __fmaf_rn(ls.k, -2.12194440e-4f, ls.f) - mean);
-    a.norm[t] = make_float4(m, sum, mean, 0.f);
+  // ---- the groups' keys
+  const int32_t n_keys = a.K > 0 ? a.cut.pieces * 32 : 0;
+  const uint32_t* keys = a.keys + t * n_keys;
+  uint32_t key[N], best = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) key[j] = j * kRowScoreThreads + tid < n_keys ? keys[j * kRowScoreThreads + tid] : 0;
+  if (tid == 0) n_groups = n_elements = 0;
+  // ---- the pieces, by the first warp
+  if (warp == 0) {
+    const float xy = lane == 0 ? to_f(x[y]) : 0.f;
+    float4 q[4];  // (at most 128 pieces)
+    float m = -INFINITY, sum = 0.f, zum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      q[j] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      if (32 * j + lane < a.cut.pieces) q[j] = a.part[t * a.cut.pieces + 32 * j + lane];
+      m = fmaxf(m, q[j].x);
+    }
+    m = warp_max(m);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (q[j].y == 0.f) continue;  // (nothing but -inf; a NaN goes on)
+      const float d0 = q[j].x - finite_max(m);
+      const float d = fmaxf(__fmaf_rn(d0, r.c.hi, d0 * r.c.lo), -1e20f);
+      const float f = expf(d0 * r.inv_tf);
+      sum += f * q[j].y;
+      zum += f * __fmaf_rn(q[j].y, d, q[j].z);
+    }
+    sum = warp_sum(sum);
+    zum = warp_sum(zum);
+    if (lane == 0) {
+      const LogSum ls = log_sum(sum);
+      const float mean = zum / sum * 0.693147181f;  // of z, by p
+      a.logp[t] = log_ratio(xy - m, r.inv_tf, 0.f, ls);
+      a.entropy[t] = __fmaf_rn(ls.k, 0.693359375f, __fmaf_rn(ls.k, -2.12194440e-4f, ls.f) - mean);
+      a.norm[t] = make_float4(m, sum, mean, 0.f);
+      row_m = m;
+      row_sum = sum;
+    }
   }
   if (a.K == 0) return;
+  // ---- the groups that count. Each warp's n-th largest of its threads' largest keys,
+  // n = K / W rounded up: there are K keys not below the least of them.
+#pragma unroll
+  for (int j = 0; j < N; ++j) best = max(best, key[j]);
+  uint32_t least = 0;
+  for (int i = 0; i < (a.K + W - 1) / W; ++i) {
+    least = warp_max(best);
+    if (lane == __ffs(__ballot_sync(~0u, best == least)) - 1) best = 0;
+  }
+  if (lane == 0) least_of[warp] = least;
+  __syncthreads();
+  const float m = row_m, sum = row_sum;
   if (!(sum > 0.f && sum < INFINITY)) {  // a NaN, a +inf or only -inf
-    if (lane < a.K) {
-      a.top_idx[t * a.K + lane] = -1;
-      a.top_logp[t * a.K + lane] = NAN;
+    if (tid < a.K) {
+      a.top_idx[t * a.K + tid] = -1;
+      a.top_logp[t * a.K + tid] = NAN;
     }
     return;
   }
-  // ---- the groups that count. The K-th largest of the lanes' largest keys is not
-  // above the K-th largest key: groups below it are left out, the others ranked.
-  int before = 0;
+  for (int w = 0; w < W; ++w) least = min(least, least_of[w]);
+  least = max(least, 1u);
 #pragma unroll
-  for (int l = 0; l < 32; ++l) {
-    const uint32_t k = __shfl_sync(~0u, best, l);
-    before += k > best || (k == best && l < lane);
+  for (int j = 0; j < N; ++j) {
+    if (key[j] < least) continue;
+    const int to = atomicAdd(&n_groups, 1);
+    if (to < C) groups[to] = {key[j], j * kRowScoreThreads + tid};
   }
-  const uint32_t least =
-      max(1u, __shfl_sync(~0u, best, __ffs(__ballot_sync(~0u, before == a.K - 1)) - 1));
-  int n_groups = 0;
-  for (int32_t g = 0; g < n_keys; g += 32) {
-    const uint32_t k = keys[g];
-    const uint32_t in = __ballot_sync(~0u, k >= least);
-    const int to = n_groups + __popc(in & ((1u << lane) - 1));
-    if (k >= least && to < C) groups[warp][to] = {k, g + lane};
-    n_groups += __popc(in);
-  }
-  __syncwarp();
-  Best list = {0, -1};
-  bool whole = n_groups > C;
-  if (!whole) {
-    const uint32_t last = __shfl_sync(~0u, best_of(groups[warp], n_groups, a.K, sorted[warp], lane).key, a.K - 1);
-    const float low = last == 0 ? -INFINITY : key_value(last);
+  __syncthreads();
+  // An entry's place is the number of entries in front of it, whatever their order.
+  auto place = [&](const Best* list, int n, const Best& own) {
+    int at = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const Best b = list[j];
+      at += in_front(b.key, b.idx, own);
+    }
+    return at;
+  };
+  auto put = [&](int at, const Best& own) {
+    if (at >= a.K) return;
+    a.top_idx[t * a.K + at] = own.idx;
+    a.top_logp[t * a.K + at] = log_ratio(key_value(own.key) - m, r.inv_tf, 0.f, log_sum(sum));
+  };
+  const int ng = n_groups;
+  if (ng <= C) {
+    if (tid == 0 && ng < a.K) last_of = 0;
+    if (tid < ng && place(groups, ng, groups[tid]) == a.K - 1) last_of = groups[tid].key;
+    __syncthreads();
     // ---- their elements that are not below the K-th group's maximum, and the loose ones
+    const uint32_t last = last_of;
+    const float low = last == 0 ? -INFINITY : key_value(last);
     const Span s = span_of(x, r.V);
     const int32_t tail = s.head + s.nvec * VE;
-    if (lane == 0) counts[warp] = 0;
-    __syncwarp();
     auto gather = [&](float v, int32_t idx) {
       if (v >= low) {
-        const int to = atomicAdd(&counts[warp], 1);
-        if (to < C) elements[warp][to] = {order_key(v), idx};
+        const int to = atomicAdd(&n_elements, 1);
+        if (to < C) elements[to] = {order_key(v), idx};
       }
     };
-    if (lane < s.head) gather(to_f(x[lane]), lane);
-    if (lane < r.V - tail) gather(to_f(x[tail + lane]), tail + lane);
+    if (tid < s.head) gather(to_f(x[tid]), tid);
+    if (tid < r.V - tail) gather(to_f(x[tail + tid]), tail + tid);
     const uint4* in = reinterpret_cast<const uint4*>(x + s.head);
     const int log = a.cut.piece;  // a group has 2^log vectors
-    const int64_t n_vecs = (int64_t)n_groups << log;
+    const int64_t n_vecs = (int64_t)ng << log;
     constexpr int B = 4;
-    for (int64_t i0 = lane; i0 < n_vecs; i0 += 32 * B) {
+    for (int64_t i0 = tid; i0 < n_vecs; i0 += kRowScoreThreads * B) {
       uint4 q[B];
       int32_t at[B];
 #pragma unroll
       for (int j = 0; j < B; ++j) {
-        const int64_t i = i0 + 32 * j;
+        const int64_t i = i0 + kRowScoreThreads * j;
         at[j] = -1;
         if (i >= n_vecs) continue;
-        const Best g = groups[warp][i >> log];
+        const Best g = groups[i >> log];
         if (g.key < last) continue;
         const int32_t v = ((((g.idx >> 5) << log) + (int32_t)(i & ((1 << log) - 1))) << 5) + (g.idx & 31);
         if (v >= s.nvec) continue;
@@ -497,16 +539,21 @@ __global__ void __launch_bounds__(kScoreThreads)
         }
       }
     }
-    __syncwarp();
-    const int found = counts[warp];
-    whole = found > C;
-    if (!whole) list = best_of(elements[warp], found, a.K, sorted[warp], lane);
+    __syncthreads();
+    const int n = n_elements;
+    if (n <= C) {
+      if (tid < n) put(place(elements, n, elements[tid]), elements[tid]);
+      return;
+    }
+    __syncthreads();  // (n_elements and the lists have been read)
   }
-  if (whole) list = best_of_row(x, r.V, a.K, lane);
-  if (lane < a.K) {
-    a.top_idx[t * a.K + lane] = list.idx;
-    a.top_logp[t * a.K + lane] = log_ratio(key_value(list.key) - m, r.inv_tf, 0.f, ls);
-  }
+  // ---- too many equal ones: the whole row, a part a warp
+  __shared__ Best lists[W * kMaxTop];
+  const Best mine = best_of_part(x, r.V, a.K, warp, W, lane);
+  if (lane < a.K) lists[warp * a.K + lane] = mine;
+  __syncthreads();
+  for (int i = tid; i < W * a.K; i += kRowScoreThreads)
+    if (lists[i].key != 0) put(place(lists, W * a.K, lists[i]), lists[i]);
 }
 
 // ------------------------------------------------------------- the gradient
