@@ -374,7 +374,7 @@ __device__ __noinline__ Best best_of_part(const T* x, int32_t V, int K, int part
 constexpr int kRowScoreThreads = 128;
 constexpr int kScoreCandidates = 128;  // groups, and elements, that are ranked
 template <typename T, int N>
-__global__ void __launch_bounds__(kRowScoreThreads)
+__global__ void __launch_bounds__(kRowScoreThreads, N == 8 ? 12 : 4)
     score_row_kernel(const __grid_constant__ ScoreArgs<T> a) {
   constexpr int VE = Vec<T>::n, C = kScoreCandidates, W = kRowScoreThreads / 32;
   static_assert(C == kRowScoreThreads, "a thread ranks an entry");
@@ -387,6 +387,14 @@ __global__ void __launch_bounds__(kRowScoreThreads)
   take_turn();
   if (blockIdx.x == 0 && tid == 0) a.head->rows = 1;
   const int64_t t = blockIdx.x;
+  // ---- the groups' keys and the pieces, on their way before the row is known to be live
+  const int32_t n_keys = a.K > 0 ? a.cut.pieces * 32 : 0;
+  const uint32_t* keys = a.keys + t * n_keys;
+  uint32_t key[N], best = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) key[j] = j * kRowScoreThreads + tid < n_keys ? keys[j * kRowScoreThreads + tid] : 0;
+  float4 part = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+  if (warp == 0 && lane < a.cut.pieces) part = a.part[t * a.cut.pieces + lane];
   const int32_t y = live_target(r, t, nullptr);
   if (y < 0) {
     if (tid == 0) {
@@ -401,27 +409,22 @@ __global__ void __launch_bounds__(kRowScoreThreads)
     return;
   }
   const T* x = r.x + t * r.ld;
-  // ---- the groups' keys
-  const int32_t n_keys = a.K > 0 ? a.cut.pieces * 32 : 0;
-  const uint32_t* keys = a.keys + t * n_keys;
-  uint32_t key[N], best = 0;
-#pragma unroll
-  for (int j = 0; j < N; ++j) key[j] = j * kRowScoreThreads + tid < n_keys ? keys[j * kRowScoreThreads + tid] : 0;
   if (tid == 0) n_groups = n_elements = 0;
   // ---- the pieces, by the first warp
   if (warp == 0) {
     const float xy = lane == 0 ? to_f(x[y]) : 0.f;
-    float4 q[4];  // (at most 128 pieces)
+    constexpr int NP = N / 8;  // of a lane
+    float4 q[NP];
     float m = -INFINITY, sum = 0.f, zum = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      q[j] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-      if (32 * j + lane < a.cut.pieces) q[j] = a.part[t * a.cut.pieces + 32 * j + lane];
+    for (int j = 0; j < NP; ++j) {
+      q[j] = j == 0 ? part : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      if (j > 0 && 32 * j + lane < a.cut.pieces) q[j] = a.part[t * a.cut.pieces + 32 * j + lane];
       m = fmaxf(m, q[j].x);
     }
     m = warp_max(m);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < NP; ++j) {
       if (q[j].y == 0.f) continue;  // (nothing but -inf; a NaN goes on)
       const float d0 = q[j].x - finite_max(m);
       const float d = fmaxf(__fmaf_rn(d0, r.c.hi, d0 * r.c.lo), -1e20f);
@@ -463,11 +466,23 @@ __global__ void __launch_bounds__(kRowScoreThreads)
   }
   for (int w = 0; w < W; ++w) least = min(least, least_of[w]);
   least = max(least, 1u);
+  int mine = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) mine += key[j] >= least;
+  int to = mine;  // entries of the warp up to this lane's
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(~0u, to, o);
+    if (lane >= o) to += v;
+  }
+  int first = 0;
+  if (lane == 31) first = atomicAdd(&n_groups, to);
+  to += __shfl_sync(~0u, first, 31) - mine;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     if (key[j] < least) continue;
-    const int to = atomicAdd(&n_groups, 1);
     if (to < C) groups[to] = {key[j], j * kRowScoreThreads + tid};
+    ++to;
   }
   __syncthreads();
   // An entry's place is the number of entries in front of it, whatever their order.
@@ -549,8 +564,8 @@ __global__ void __launch_bounds__(kRowScoreThreads)
   }
   // ---- too many equal ones: the whole row, a part a warp
   __shared__ Best lists[W * kMaxTop];
-  const Best mine = best_of_part(x, r.V, a.K, warp, W, lane);
-  if (lane < a.K) lists[warp * a.K + lane] = mine;
+  const Best own = best_of_part(x, r.V, a.K, warp, W, lane);
+  if (lane < a.K) lists[warp * a.K + lane] = own;
   __syncthreads();
   for (int i = tid; i < W * a.K; i += kRowScoreThreads)
     if (lists[i].key != 0) put(place(lists, W * a.K, lists[i]), lists[i]);
