@@ -368,6 +368,10 @@ __device__ __noinline__ Best best_of_part(const T* x, int32_t V, int K, int part
   return list;
 }
 
+__device__ __forceinline__ uint64_t entry(uint32_t key, int32_t idx) {
+  return (uint64_t)key << 32 | (uint32_t)~idx;
+}
+
 // Joins a row's pieces and picks its alternatives; a CTA a row. (A warp a row took 27
 // us for 4096 rows of 131072, 20 alternatives, and 14 for 64 of them: a chain of some
 // ten loads.) N: keys of a thread.
@@ -378,7 +382,8 @@ __global__ void __launch_bounds__(kRowScoreThreads, N == 8 ? 12 : 4)
     score_row_kernel(const __grid_constant__ ScoreArgs<T> a) {
   constexpr int VE = Vec<T>::n, C = kScoreCandidates, W = kRowScoreThreads / 32;
   static_assert(C == kRowScoreThreads, "a thread ranks an entry");
-  __shared__ Best groups[C], elements[C];
+  // key and, inverted, index: the larger number is in front
+  __shared__ uint64_t groups[C], sorted[C], elements[C];
   __shared__ uint32_t least_of[W], last_of;
   __shared__ int32_t n_groups, n_elements;
   __shared__ float row_m, row_sum;
@@ -481,46 +486,47 @@ __global__ void __launch_bounds__(kRowScoreThreads, N == 8 ? 12 : 4)
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     if (key[j] < least) continue;
-    if (to < C) groups[to] = {key[j], j * kRowScoreThreads + tid};
+    if (to < C) groups[to] = entry(key[j], j * kRowScoreThreads + tid);
     ++to;
   }
   __syncthreads();
   // An entry's place is the number of entries in front of it, whatever their order.
-  auto place = [&](const Best* list, int n, const Best& own) {
+  auto place = [&](const uint64_t* list, int n, uint64_t own) {
     int at = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-      const Best b = list[j];
-      at += in_front(b.key, b.idx, own);
-    }
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) at += list[j] > own;
     return at;
   };
-  auto put = [&](int at, const Best& own) {
+  auto put = [&](int at, uint64_t own) {
     if (at >= a.K) return;
-    a.top_idx[t * a.K + at] = own.idx;
-    a.top_logp[t * a.K + at] = log_ratio(key_value(own.key) - m, r.inv_tf, 0.f, log_sum(sum));
+    a.top_idx[t * a.K + at] = (int32_t)~(uint32_t)own;
+    a.top_logp[t * a.K + at] = log_ratio(key_value((uint32_t)(own >> 32)) - m, r.inv_tf, 0.f, log_sum(sum));
   };
   const int ng = n_groups;
   if (ng <= C) {
     if (tid == 0 && ng < a.K) last_of = 0;
-    if (tid < ng && place(groups, ng, groups[tid]) == a.K - 1) last_of = groups[tid].key;
+    if (tid < ng) {
+      const uint64_t own = groups[tid];
+      const int at = place(groups, ng, own);
+      sorted[at] = own;
+      if (at == a.K - 1) last_of = (uint32_t)(own >> 32);
+    }
     __syncthreads();
     // ---- their elements that are not below the K-th group's maximum, and the loose ones
     const uint32_t last = last_of;
+    const int kept = __syncthreads_count(tid < ng && (uint32_t)(sorted[tid] >> 32) >= last);
     const float low = last == 0 ? -INFINITY : key_value(last);
     const Span s = span_of(x, r.V);
     const int32_t tail = s.head + s.nvec * VE;
     auto gather = [&](float v, int32_t idx) {
-      if (v >= low) {
-        const int to = atomicAdd(&n_elements, 1);
-        if (to < C) elements[to] = {order_key(v), idx};
-      }
+      const int to = atomicAdd(&n_elements, 1);
+      if (to < C) elements[to] = entry(order_key(v), idx);
     };
-    if (tid < s.head) gather(to_f(x[tid]), tid);
-    if (tid < r.V - tail) gather(to_f(x[tail + tid]), tail + tid);
+    if (tid < s.head && to_f(x[tid]) >= low) gather(to_f(x[tid]), tid);
+    if (tid < r.V - tail && to_f(x[tail + tid]) >= low) gather(to_f(x[tail + tid]), tail + tid);
     const uint4* in = reinterpret_cast<const uint4*>(x + s.head);
     const int log = a.cut.piece;  // a group has 2^log vectors
-    const int64_t n_vecs = (int64_t)ng << log;
+    const int64_t n_vecs = (int64_t)kept << log;
     constexpr int B = 4;
     for (int64_t i0 = tid; i0 < n_vecs; i0 += kRowScoreThreads * B) {
       uint4 q[B];
@@ -530,9 +536,8 @@ __global__ void __launch_bounds__(kRowScoreThreads, N == 8 ? 12 : 4)
         const int64_t i = i0 + kRowScoreThreads * j;
         at[j] = -1;
         if (i >= n_vecs) continue;
-        const Best g = groups[i >> log];
-        if (g.key < last) continue;
-        const int32_t v = ((((g.idx >> 5) << log) + (int32_t)(i & ((1 << log) - 1))) << 5) + (g.idx & 31);
+        const int32_t g = (int32_t)~(uint32_t)sorted[i >> log];
+        const int32_t v = ((((g >> 5) << log) + (int32_t)(i & ((1 << log) - 1))) << 5) + (g & 31);
         if (v >= s.nvec) continue;
         at[j] = v;
         q[j] = in[v];
@@ -540,17 +545,19 @@ __global__ void __launch_bounds__(kRowScoreThreads, N == 8 ? 12 : 4)
 #pragma unroll
       for (int j = 0; j < B; ++j) {
         if (at[j] < 0) continue;
-        const uint4 one[1] = {q[j]};
-        if (!(largest(one, T()) >= low)) continue;
         Pairs<T> pr;
         unpack(q[j], pr);
-        const int32_t base = s.head + at[j] * VE;
+        uint32_t hits = 0;
 #pragma unroll
         for (int e = 0; e < VE / 2; ++e) {
           float f0, f1;
           f2_get(pr.p[e], f0, f1);
-          gather(f0, base + 2 * e);
-          gather(f1, base + 2 * e + 1);
+          if (f0 >= low) hits |= 1u << (2 * e);
+          if (f1 >= low) hits |= 2u << (2 * e);
+        }
+        for (; hits != 0; hits &= hits - 1) {
+          const int32_t idx = s.head + at[j] * VE + __ffs(hits) - 1;
+          gather(to_f(x[idx]), idx);
         }
       }
     }
@@ -563,12 +570,11 @@ __global__ void __launch_bounds__(kRowScoreThreads, N == 8 ? 12 : 4)
     __syncthreads();  // (n_elements and the lists have been read)
   }
   // ---- too many equal ones: the whole row, a part a warp
-  __shared__ Best lists[W * kMaxTop];
+  static_assert(W * kMaxTop <= C, "the warps' lists are ranked together");
   const Best own = best_of_part(x, r.V, a.K, warp, W, lane);
-  if (lane < a.K) lists[warp * a.K + lane] = own;
+  if (lane < a.K) elements[warp * a.K + lane] = entry(own.key, own.idx);
   __syncthreads();
-  for (int i = tid; i < W * a.K; i += kRowScoreThreads)
-    if (lists[i].key != 0) put(place(lists, W * a.K, lists[i]), lists[i]);
+  if (tid < W * a.K && elements[tid] >> 32 != 0) put(place(elements, W * a.K, elements[tid]), elements[tid]);
 }
 
 // ------------------------------------------------------------- the gradient
