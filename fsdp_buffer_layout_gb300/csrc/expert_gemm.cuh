@@ -36,6 +36,7 @@ constexpr int kXDepth = 64;                            // of r a stage
 constexpr int kXLanes = 256;                           // of a tile
 constexpr int kXCols = 256;                            // of a tile, at most
 constexpr int kMaxGroups = 512;                        // experts
+constexpr int kXBlock = 8;                             // pieces of rows side by side
 constexpr uint32_t kXHalf = 128 * kXDepth * 2;         // one operand's half of a stage: 16 KB
 constexpr uint32_t kXStage = 2 * kXHalf;
 constexpr uint32_t kXBars = 4 * kXStages + 5;
@@ -44,7 +45,7 @@ struct XTable {
   int32_t start[kMaxGroups + 1];  // its first row
   uint32_t tmem, stop;
 };
-constexpr uint32_t kXOut = 4096;  // kWeight: of each epilogue warp, 32 lanes x 64 columns
+constexpr uint32_t kXOut = 4096;  // of each epilogue warp: 32 lanes x 64 columns, or two of 32 x 32
 constexpr uint32_t kXSmem =
     kXStages * kXStage + 4 * kXOut + 8 * kXBars + (uint32_t)sizeof(XTable) + 1024;
 static_assert(kXSmem <= 227 * 1024, "fits in shared memory");
@@ -92,10 +93,16 @@ __device__ __forceinline__ XTile tile_at(const ExpertArgs& a, const XTable& x, i
   } else {
     while (t >= x.first[e + 1]) ++e;
     q.e = e;
-    const int32_t k = t - x.first[e], piece = k / a.lane_tiles;
-    const int32_t begin = x.start[e], rows = x.start[e + 1] - begin;
-    q.lane0 = (k - piece * a.lane_tiles) * kXLanes;
-    q.width = token_width(rows, token_tiles(rows));
+    // eight pieces of rows at a time take a lane tile one after the other: its
+    // weights come from memory once, and are asked for by fewer pairs at a time (2 to 4
+    // percent for 32 experts of 1024 rows, against all lane tiles of a piece in turn)
+    const int32_t begin = x.start[e], rows = x.start[e + 1] - begin, pieces = token_tiles(rows);
+    int32_t k = t - x.first[e];
+    const int32_t block = k / (kXBlock * a.lane_tiles) * kXBlock, n = min(kXBlock, pieces - block);
+    k -= block * a.lane_tiles;
+    const int32_t lane_tile = k / n, piece = block + k - lane_tile * n;
+    q.lane0 = lane_tile * kXLanes;
+    q.width = token_width(rows, pieces);
     q.col0 = begin + piece * q.width;
     q.cols = min(q.width, begin + rows - q.col0);
     q.row0 = 0;
@@ -114,8 +121,8 @@ template <int KIND>
 constexpr int kXThreads = KIND == kWeight ? 224 : 192;
 
 // Tensor maps: the lanes' operand; the columns' operand, in boxes of 16, 32, 64 and
-// 128 rows (kWeight: of 64 x 64, the first alone); kWeight's output, in boxes of 32
-// rows.
+// 128 rows (kWeight: of 64 x 64, the first alone); the output, in boxes of 32 rows of
+// 32 elements (kWeight: of 64).
 struct XMaps {
   CUtensorMap lanes, cols[4], out;
 };
@@ -224,12 +231,10 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
         const XTile q = tile_at<KIND>(g, table, t, e);
         const int32_t half = q.width / 2;
         const int32_t lane0 = q.lane0 + rank * 128, col0 = q.col0 + rank * half;
-        // One copy of the least box that holds the columns' half: rows too many are
-        // read and not used (seven boxes of 16 instead of one of 128 ran 224 columns
-        // at 970 TFLOP/s, 256 columns at 1670).
-        const int32_t box = KIND == kWeight ? half : half <= 16 ? 16 : half <= 32 ? 32 : half <= 64 ? 64 : 128;
-        const CUtensorMap* cols = &maps.cols[box <= 16 ? 0 : box <= 32 ? 1 : box <= 64 ? 2 : 3];
-        const uint32_t bytes = kXHalf + (uint32_t)box * (kXDepth * 2);
+        const int largest = 27 - __clz(half);  // box of 16 << largest rows
+        const int32_t box = 16 << largest;
+        const CUtensorMap* cols = &maps.cols[KIND == kWeight ? 0 : largest];
+        const uint32_t bytes = kXHalf + (uint32_t)half * (kXDepth * 2);
         for (int32_t k0 = 0; k0 < q.depth; k0 += kXDepth) {
           const int s = it % kXStages;
           const uint32_t ph = (it / kXStages) & 1u;
@@ -262,7 +267,15 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
             } else {
               tma3_g2s_pair(a, &maps.lanes, k0, lane0, q.e, fb);
             }
+            // the columns' half in boxes of 128, 64, 32 and 16 rows, each once at most
+            // (seven of 16 for 112 rows ran at 970 TFLOP/s instead of 1470)
             tma3_g2s_pair(b, cols, k0, col0, 0, fb);
+            for (int32_t rest = half - box, c = box; rest != 0;) {
+              const int i = 27 - __clz(rest);
+              tma3_g2s_pair(b + (uint32_t)c * 128u, &maps.cols[i], k0, col0 + c, 0, fb);
+              c += 16 << i;
+              rest -= 16 << i;
+            }
           }
         }
       }
@@ -325,6 +338,7 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
     const int quarter = warp & 3;
     int32_t e = 0;
     int lt = 0;
+    uint32_t turn = 0;
     for (int32_t t = cid; t < ntiles; t += ncid, ++lt) {
       const int buf = lt & 1;
       const bool ok = __all_sync(~0u, mbar_wait(tfull_bar(buf), (uint32_t)(lt >> 1) & 1u, err, stop));
@@ -378,22 +392,48 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
           tmem_ld32(from + c, r);
           {
             // Lane pairs trade columns: an even lane keeps column x and gets its
-            // neighbour's, an odd one column x + 1, so that each stores two
-            // adjacent elements of a row.
+            // neighbour's, an odd one column x + 1, so that each has two adjacent
+            // elements of a row. 32 whole rows go out through shared memory as one
+            // copy, the last rows of an expert by the lanes themselves.
             const bool odd = lane & 1;
             const int32_t n = q.cols - c, i2 = i & ~1;
-            uint16_t* to = g.out + (int64_t)(q.col0 + c + (odd ? 1 : 0)) * g.ld + i2;
+            uint32_t p[16];
 #pragma unroll
             for (int x = 0; x < 32; x += 2) {
               const uint32_t give = odd ? r[x] : r[x + 1];
               const uint32_t got = __shfl_xor_sync(~0u, give, 1);
-              const uint32_t p = odd ? pack_bf16(__uint_as_float(got), __uint_as_float(r[x + 1]))
-                                     : pack_bf16(__uint_as_float(r[x]), __uint_as_float(got));
-              if (x + (odd ? 1 : 0) < n) {
-                if (i2 + 1 < g.lanes)
-                  *reinterpret_cast<uint32_t*>(to + (int64_t)x * g.ld) = p;
-                else if (i2 < g.lanes)
-                  to[(int64_t)x * g.ld] = (uint16_t)p;
+              p[x / 2] = odd ? pack_bf16(__uint_as_float(got), __uint_as_float(r[x + 1]))
+                             : pack_bf16(__uint_as_float(r[x]), __uint_as_float(got));
+            }
+            if (n >= 32) {
+              const uint32_t to = out0 + (uint32_t)quarter * kXOut + (turn++ & 1u) * (kXOut / 2);
+              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+              __syncwarp();
+              const uint32_t mine = to + (odd ? 64u : 0u) + (uint32_t)(lane >> 1) * 4u;
+#pragma unroll
+              for (int x = 0; x < 16; ++x)
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(mine + (uint32_t)x * 128u), "r"(p[x]) : "memory");
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
+              if (lane == 0) {
+                if (i < g.lanes)
+                  asm volatile(
+                      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                          reinterpret_cast<uint64_t>(&maps.out)),
+                      "r"(i), "r"(q.col0 + c), "r"(0), "r"(to)
+                      : "memory");
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+              }
+            } else {
+              uint16_t* to = g.out + (int64_t)(q.col0 + c + (odd ? 1 : 0)) * g.ld + i2;
+#pragma unroll
+              for (int x = 0; x < 32; x += 2) {
+                if (x + (odd ? 1 : 0) < n) {
+                  if (i2 + 1 < g.lanes)
+                    *reinterpret_cast<uint32_t*>(to + (int64_t)x * g.ld) = p[x / 2];
+                  else if (i2 < g.lanes)
+                    to[(int64_t)x * g.ld] = (uint16_t)p[x / 2];
+                }
               }
             }
           }
@@ -403,7 +443,7 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(leader_tempty0 + 8u * buf);
     }
-    if (KIND == kWeight && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else {
     // ---------------- mending (both CTAs): rows that are not the expert's
     uint32_t it = 0, phases = 0;

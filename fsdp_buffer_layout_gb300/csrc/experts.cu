@@ -76,18 +76,19 @@ vsf_status check(int kind, const Product& a) {
 }
 
 // Tensor map over [batch, rows, width] (row stride ld, batch stride bs, in
-// elements), boxes of 64 elements x box_rows rows, 128-byte swizzle; copies
-// outside read zeros.
+// elements), boxes of 64 elements x box_rows rows, 128-byte swizzle (or of 32
+// elements, not swizzled); copies outside read zeros and write nothing.
 vsf_status operand_map(CUtensorMap* map, const char* who, const uint16_t* p, int64_t width, int64_t rows,
-                       int64_t batch, int64_t ld, int64_t bs, int box_rows) {
+                       int64_t batch, int64_t ld, int64_t bs, int box_rows, int box_width = 64) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = gemm_map_encoder();
   if (encode == nullptr) return fail(VSF_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)batch};
   const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)std::max(bs, ld) * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)box_width, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
   const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(p), dims,
                             strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            box_width == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(VSF_ERR_CUDA, std::string(who) + ": cuTensorMapEncodeTiled failed (" +
@@ -162,7 +163,7 @@ vsf_status product(const Product& a, cudaStream_t st) {
                     KIND == kForward ? 128 : 64);
     for (int i = 0; i < 4 && s == VSF_OK; ++i)
       s = operand_map(&m.cols[i], a.who, a.rows_in, g.depth, a.rows, 1, a.rows_ld, 0, 16 << i);
-    m.out = m.lanes;
+    if (s == VSF_OK) s = operand_map(&m.out, a.who, a.out, lanes, a.rows, 1, a.out_ld, 0, 32, 32);
   }
   if (s != VSF_OK) return s;
   cudaError_t e = cudaSuccess;

@@ -25,10 +25,11 @@ from .objectives import _Objective
 class _Rows(_Objective):
     def _check(self, x, rows: int, width: int, what: str) -> int:
         """Checks a matrix of exactly `rows` rows; its row stride."""
-        if x.dtype is not self.dtype or x.dim() != 2 or tuple(x.shape) != (rows, width) \
+        shape = x.shape
+        if x.dtype is not self.dtype or len(shape) != 2 or shape[0] != rows or shape[1] != width \
                 or x.get_device() != self._index:
             raise ValueError(f"{what}: expected {self.dtype} [{rows}, {width}] on {self.device}, got "
-                             f"{x.dtype} {tuple(x.shape)} on {x.device}")
+                             f"{x.dtype} {tuple(shape)} on {x.device}")
         ld, unit = x.stride()
         if unit != 1 and width > 1:
             raise ValueError(f"{what}: the elements of a row must be adjacent (stride {unit})")
@@ -48,6 +49,19 @@ class _Rows(_Objective):
             make = torch.zeros if zero else torch.empty
             return make(*shape[:-1], self._padded(shape[-1]), dtype=self.dtype,
                         device=self.device)[..., :shape[-1]]
+
+    def _output(self, given, own, rows: int, width: int, what: str):
+        """The first rows of an output of the object's own, or of the one given;
+        its address and row stride."""
+        if given is not None:
+            ld = self._check(given, rows, width, what)
+            return given, given.data_ptr(), ld
+        if own is None:
+            raise ValueError(f"{what}: none of the object's own (with_grad=False) and none given")
+        ld = self._padded(width)
+        if rows != own.shape[0]:
+            own = own[:rows]
+        return own, own.data_ptr(), ld
 
 
 class Dispatch(_Rows):
@@ -93,42 +107,34 @@ class Dispatch(_Rows):
             raise ValueError(f"of sort {call}: sort {self.calls} has followed it")
         return self._n
 
-    def _output(self, given, own, rows: int, what: str):
-        if given is None:
-            if own is None:
-                raise ValueError(f"{what}: none of the object's own (with_grad=False) and none given")
-            given = own[:rows]
-        return given, self._check(given, rows, self.width, what)
-
     def sort(self, idx):
-        n = idx.shape[0]
-        if idx.dim() != 2 or n > self.tokens or idx.shape[1] != self.top_k:
-            raise ValueError(f"idx: expected [<= {self.tokens}, {self.top_k}], got {tuple(idx.shape)}")
+        shape = idx.shape
+        if len(shape) != 2 or shape[0] > self.tokens or shape[1] != self.top_k:
+            raise ValueError(f"idx: expected [<= {self.tokens}, {self.top_k}], got {tuple(shape)}")
+        n = shape[0]
         at = self._vec(idx, n * self.top_k, torch.int32, "idx")
         V.vsf_expert_sort(at, n, self.top_k, self.experts, *self._at, self._bytes, self._st)
         self.calls += 1
         self._n = n
-        return self.starts, self._first_of(self.source, n * self.top_k), self._first(self.place, n)
-
-    @staticmethod
-    def _first_of(buf, n: int):
-        return buf if n == buf.shape[0] else buf[:n]
+        if n == self.tokens:
+            return self.starts, self.source, self.place
+        return self.starts, self.source[:n * self.top_k], self.place[:n]
 
     def gather(self, x, out=None, call: int | None = None):
         n = self._sorted(call)
         ld = self._check(x, n, self.width, "x")
-        out, out_ld = self._output(out, self.rows, n * self.top_k, "out")
-        V.vsf_expert_gather(x.data_ptr(), self._vdt, n, self.width, ld, self._at[2], self.top_k,
-                            out.data_ptr(), out_ld, self._st)
+        out, at, out_ld = self._output(out, self.rows, n * self.top_k, self.width, "out")
+        V.vsf_expert_gather(x.data_ptr(), self._vdt, n, self.width, ld, self._at[2], self.top_k, at,
+                            out_ld, self._st)
         return out
 
     def _combine(self, y, gates, out, own, call, what):
         n = self._sorted(call)
         ld = self._check(y, n * self.top_k, self.width, what)
-        out, out_ld = self._output(out, own, n, "out")
+        out, at, out_ld = self._output(out, own, n, self.width, "out")
         g = self._vec(gates, n * self.top_k, torch.float32, "gates")
         V.vsf_expert_combine(y.data_ptr(), self._vdt, n, self.width, ld, self._at[2], g, self.top_k,
-                             out.data_ptr(), out_ld, self._st)
+                             at, out_ld, self._st)
         return out
 
     def combine(self, y, gates, out=None, call: int | None = None):
@@ -142,7 +148,7 @@ class Dispatch(_Rows):
         k = self.top_k
         ld = self._check(d_out, n, self.width, "d_out")
         y_ld = self._check(y, n * k, self.width, "y")
-        d_y, d_ld = self._output(d_y, self.d_y, n * k, "d_y")
+        d_y, at, d_ld = self._output(d_y, self.d_y, n * k, self.width, "d_y")
         if gates is None:
             raise ValueError("gates: needed")
         if d_gates is None:
@@ -151,7 +157,7 @@ class Dispatch(_Rows):
             d_gates = self._first(self.d_gates, n)
         V.vsf_expert_combine_grad(d_out.data_ptr(), self._vdt, n, self.width, ld, y.data_ptr(), y_ld,
                                   self._at[2], self._vec(gates, n * k, torch.float32, "gates"), k,
-                                  d_y.data_ptr(), d_ld,
+                                  at, d_ld,
                                   self._vec(d_gates, n * k, torch.float32, "d_gates"), self._st)
         return d_y, d_gates
 
@@ -205,33 +211,25 @@ class ExpertLinear(_Rows):
             raise ValueError(f"{what}: expected [<= {self.tokens}, {width}], got {tuple(x.shape)}")
         return x.shape[0], self._check(x, x.shape[0], width, what)
 
-    def _output(self, given, own, rows: int, width: int, what: str):
-        if given is None:
-            if own is None:
-                raise ValueError(f"{what}: none of the object's own (with_grad=False) and none given")
-            given = self._first(own, rows)
-        return given, self._check(given, rows, width, what)
-
     def _starts(self, starts):
         return self._vec(starts, self.experts + 1, torch.int32, "starts")
 
     def forward(self, x, weight, starts, out=None):
         n, ld = self._rows_of(x, self.in_features, "x")
         w_ld, w_stride = self._weight(weight, "weight")
-        out, out_ld = self._output(out, self.y, n, self.out_features, "out")
+        out, at, out_ld = self._output(out, self.y, n, self.out_features, "out")
         V.vsf_expert_product(x.data_ptr(), n, self.in_features, ld, weight.data_ptr(), self.experts,
-                             self.out_features, w_ld, w_stride, self._starts(starts), out.data_ptr(),
-                             out_ld, self._ws, self._st)
+                             self.out_features, w_ld, w_stride, self._starts(starts), at, out_ld,
+                             self._ws, self._st)
         return out
 
     def backward_input(self, d_y, weight, starts, out=None):
         n, ld = self._rows_of(d_y, self.out_features, "d_y")
         w_ld, w_stride = self._weight(weight, "weight")
-        out, out_ld = self._output(out, self.d_x, n, self.in_features, "out")
+        out, at, out_ld = self._output(out, self.d_x, n, self.in_features, "out")
         V.vsf_expert_product_input_grad(d_y.data_ptr(), n, self.out_features, ld, weight.data_ptr(),
                                         self.experts, self.in_features, w_ld, w_stride,
-                                        self._starts(starts), out.data_ptr(), out_ld, self._ws,
-                                        self._st)
+                                        self._starts(starts), at, out_ld, self._ws, self._st)
         return out
 
     def backward_weight(self, d_y, x, starts, out=None):
