@@ -29,6 +29,21 @@
 // tiles for itself before it begins. Every wait is bounded (mbarrier.cuh), and a
 // broken pipeline ends as in ns_gemm.cuh.
 
+// One lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
+// The waits of a whole warp: all of its lanes go on, or none does.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned* err, volatile uint32_t* stop) {
+  return __all_sync(~0u, mbar_wait(bar, parity, err, stop));
+}
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, unsigned* err,
+                                                  volatile uint32_t* stop) {
+  return __all_sync(~0u, mbar_wait_cluster(bar, parity, err, stop));
+}
+
 enum { kForward = 0, kInput = 1, kWeight = 2 };
 
 constexpr int kXStages = 6;
@@ -221,10 +236,13 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
   auto halt_cluster = [&]() { remote_stop(stop, (uint32_t)(rank ^ 1)); };
 
   if (warp == 0) {
-    if (lane == 0 && *stop == 0u) {
-      // ---------------- producer (both CTAs)
+    if (__all_sync(~0u, *stop == 0u)) {
+      // ---------------- producer (both CTAs), one lane of a whole warp as for the products
+      const bool one = elect_one();
       const uint32_t own0 = peer_addr(own_bar(0), (uint32_t)rank);
       uint32_t it = 0, mended = 0, phases = 0;  // stages mended so far; how often, modulo 2
+      int s = 0;
+      uint32_t phase = 1;
       int32_t e = 0;
       bool halted = false;
       for (int32_t t = cid; t < ntiles && !halted; t += ncid) {
@@ -236,25 +254,24 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
         const CUtensorMap* cols = &maps.cols[KIND == kWeight ? 0 : largest];
         const uint32_t bytes = kXHalf + (uint32_t)half * (kXDepth * 2);
         for (int32_t k0 = 0; k0 < q.depth; k0 += kXDepth) {
-          const int s = it % kXStages;
-          const uint32_t ph = (it / kXStages) & 1u;
-          if (!mbar_wait(empty_bar(s), ph ^ 1u, err, stop)) {
+          if (!warp_wait(empty_bar(s), phase, err, stop)) {
             halted = true;
-            halt_cluster();
+            if (one) halt_cluster();
             break;
           }
           ++it;
           uint32_t fb = leader_full0 + 8u * s;
           if (KIND == kWeight && k0 + kXDepth > q.depth && (q.depth & 15) != 0) {
             fb = own0 + 8u * s;  // warp 6 mends the stage and then arrives
-            mbar_expect_tx(own_bar(s), bytes);
+            if (one) mbar_expect_tx(own_bar(s), bytes);
             mended |= 1u << s;
             phases ^= 1u << s;
-          } else if (leader) {
+          } else if (leader && one) {
             mbar_expect_tx(full_bar(s), 2 * bytes);
           }
           const uint32_t a = s0 + s * kXStage, b = a + kXHalf;
-          if (KIND == kWeight) {
+          if (!one) {
+          } else if (KIND == kWeight) {
             const int32_t r = q.row0 + k0;
             tma3_g2s_pair(a, &maps.lanes, lane0, r, 0, fb);
             tma3_g2s_pair(a + 8192u, &maps.lanes, lane0 + 64, r, 0, fb);
@@ -277,26 +294,45 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
               rest -= 16 << i;
             }
           }
+          __syncwarp();
+          if (++s == kXStages) {
+            s = 0;
+            phase ^= 1u;
+          }
         }
       }
       // every copy lands before the CTA ends: the leader sees both CTAs' (the
       // follower's are covered by its wait and the last cluster barrier)
-      const uint64_t deadline = global_ns() + kWaitNs;
-      for (int s = 0; KIND == kWeight && s < kXStages; ++s)
-        if (mended >> s & 1u) mbar_drain(own_bar(s), (phases >> s & 1u) ^ 1u, deadline, err);
-      if (leader) {
-        for (int s = 0; s < kXStages; ++s) {
-          if (it > (uint32_t)s) {
-            const uint32_t last = (it - 1 - s) / kXStages * kXStages + s;
-            mbar_drain(full_bar(s), (last / kXStages) & 1u, deadline, err);
+      if (one) {
+        const uint64_t deadline = global_ns() + kWaitNs;
+        for (int s = 0; KIND == kWeight && s < kXStages; ++s)
+          if (mended >> s & 1u) mbar_drain(own_bar(s), (phases >> s & 1u) ^ 1u, deadline, err);
+        if (leader) {
+          for (int s = 0; s < kXStages; ++s) {
+            if (it > (uint32_t)s) {
+              const uint32_t last = (it - 1 - s) / kXStages * kXStages + s;
+              mbar_drain(full_bar(s), (last / kXStages) & 1u, deadline, err);
+            }
           }
         }
       }
+      __syncwarp();
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader && *stop == 0u) {
-      // ---------------- products (leader only)
-      uint32_t it = 0;
+    if (leader && __all_sync(~0u, *stop == 0u)) {
+      // ---------------- products (leader only). What is done for a stage has to fit the
+      // tensor cores' time for it, 512 cycles of 256 columns. So the descriptors' low
+      // words are counted on (their high words do not change), and the whole warp goes
+      // through the loop, whose values are then the warp's and not a lane's; one lane
+      // issues. (Of 44 stages a tile took, in us, of 32, 128 and 256 columns: one lane
+      // and descriptors made anew 14.4, 14.6, 15.8; one lane 11.2, 11.4, 14.0; so 7.8,
+      // 9.0, 13.9 = 2010 TFLOP/s.)
+      const bool one = elect_one();
+      constexpr uint64_t kDescA = operand_desc<AMN>(0u, 0), kDescB = operand_desc<BMN>(0u, 0);
+      constexpr uint32_t kStepA = AMN ? 2048u >> 4 : 32u >> 4, kStepB = BMN ? 2048u >> 4 : 32u >> 4;
+      const uint32_t a0 = (uint32_t)kDescA + (s0 >> 4), b0 = (uint32_t)kDescB + ((s0 + kXHalf) >> 4);
+      int s = 0;
+      uint32_t phase = 0;
       int32_t e = 0;
       int lt = 0;
       bool halted = false;
@@ -304,34 +340,53 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
         const XTile q = tile_at<KIND>(g, table, t, e);
         const uint32_t idesc = umma_idesc_bf16(AMN, BMN, kXLanes, q.width);
         const int buf = lt & 1;
-        if (!mbar_wait_cluster(tempty_bar(buf), ((uint32_t)(lt >> 1) & 1u) ^ 1u, err, stop)) {
-          halt_cluster();
+        if (!warp_wait_cluster(tempty_bar(buf), ((uint32_t)(lt >> 1) & 1u) ^ 1u, err, stop)) {
+          if (one) halt_cluster();
           break;
         }
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(buf * kXCols);
-        for (int32_t k0 = 0; k0 < q.depth; k0 += kXDepth, ++it) {
-          const int s = it % kXStages;
-          if (!mbar_wait_cluster(full_bar(s), (it / kXStages) & 1u, err, stop)) {
+        uint32_t more = 0;
+        for (int32_t left = q.depth; left > 0; left -= kXDepth) {
+          if (!warp_wait_cluster(full_bar(s), phase, err, stop)) {
             halted = true;
-            halt_cluster();
+            if (one) halt_cluster();
             break;
           }
           tc_fence_after();
-          const uint32_t a = s0 + s * kXStage, b = a + kXHalf;
+          const uint32_t a = a0 + (uint32_t)s * (kXStage >> 4), b = b0 + (uint32_t)s * (kXStage >> 4);
+          auto step = [&](int kk, uint32_t accumulate) {
+            umma_pair_words(d, a + kk * kStepA, (uint32_t)(kDescA >> 32), b + kk * kStepB,
+                            (uint32_t)(kDescB >> 32), idesc, accumulate);
+          };
           // (what a stage holds past the depth is zeros, or mended to the next 16)
-          const int steps = min(kXDepth / 16, (q.depth - k0 + 15) / 16);
-#pragma unroll
-          for (int kk = 0; kk < kXDepth / 16; ++kk)
-            if (kk < steps)
-              umma_pair_bf16(d, operand_desc<AMN>(a, kk), operand_desc<BMN>(b, kk), idesc,
-                             (k0 | kk) != 0 ? 1u : 0u);
-          umma_pair_commit(empty_bar(s), kBoth);
+          if (one) {
+            step(0, more);
+            if (left > 48) {
+              step(1, 1);
+              step(2, 1);
+              step(3, 1);
+            } else {
+              if (left > 16) step(1, 1);
+              if (left > 32) step(2, 1);
+            }
+            umma_pair_commit(empty_bar(s), kBoth);
+          }
+          __syncwarp();
+          more = 1;
+          if (++s == kXStages) {
+            s = 0;
+            phase ^= 1u;
+          }
         }
-        if (!halted) umma_pair_commit(tfull_bar(buf), kBoth);
+        if (!halted && one) umma_pair_commit(tfull_bar(buf), kBoth);
+        __syncwarp();
       }
-      umma_pair_commit(done_bar, 1);  // this CTA only
-      mbar_drain(done_bar, 0u, global_ns() + kWaitNs, err);
+      if (one) {
+        umma_pair_commit(done_bar, 1);  // this CTA only
+        mbar_drain(done_bar, 0u, global_ns() + kWaitNs, err);
+      }
+      __syncwarp();
     }
   } else if (warp < 6) {
     // ---------------- epilogue (both CTAs): this CTA's 128 lanes
@@ -341,7 +396,7 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
     uint32_t turn = 0;
     for (int32_t t = cid; t < ntiles; t += ncid, ++lt) {
       const int buf = lt & 1;
-      const bool ok = __all_sync(~0u, mbar_wait(tfull_bar(buf), (uint32_t)(lt >> 1) & 1u, err, stop));
+      const bool ok = warp_wait(tfull_bar(buf), (uint32_t)(lt >> 1) & 1u, err, stop);
       tc_fence_after();
       if (ok) {
         const XTile q = tile_at<KIND>(g, table, t, e);
@@ -453,7 +508,7 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
       it += (uint32_t)((q.depth + kXDepth - 1) / kXDepth);
       if ((q.depth & 15) == 0) continue;
       const int s = (it - 1) % kXStages;
-      if (!__all_sync(~0u, mbar_wait(own_bar(s), phases >> s & 1u, err, stop))) {
+      if (!warp_wait(own_bar(s), phases >> s & 1u, err, stop)) {
         if (lane == 0) halt_cluster();
         break;
       }
@@ -469,7 +524,7 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
       if (!leader) {
         if (lane == 0) mbar_arrive_cluster(leader_peer0 + 8u * s);
       } else {
-        if (!__all_sync(~0u, mbar_wait_cluster(peer_bar(s), phases >> s & 1u, err, stop))) {
+        if (!warp_wait_cluster(peer_bar(s), phases >> s & 1u, err, stop)) {
           if (lane == 0) halt_cluster();
           break;
         }

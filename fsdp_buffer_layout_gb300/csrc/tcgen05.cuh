@@ -39,6 +39,17 @@ __device__ __forceinline__ void umma_pair_bf16(uint32_t d_tmem, uint64_t a_desc,
       : "memory");
 }
 
+// The same with the descriptors' two words.
+__device__ __forceinline__ void umma_pair_words(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                                uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n"
+      " mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // The mbarrier at `bar` in every CTA of cta_mask receives one arrival once
 // every pair MMA this thread issued before has completed.
 __device__ __forceinline__ void umma_pair_commit(uint32_t bar, uint16_t cta_mask) {
@@ -135,7 +146,7 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(bool a_mn, bool b_mn, int
 //     K row k at k * 128 bytes in its box, 8-row groups 1024 bytes apart; K
 //     step kk starts kk * 16 rows = kk * 2048 bytes in.
 template <bool kMN>
-__device__ __forceinline__ uint64_t operand_desc(uint32_t base, int kk) {
+__host__ __device__ __forceinline__ constexpr uint64_t operand_desc(uint32_t base, int kk) {
   return kMN ? umma_smem_desc(base + kk * 2048u, 8192u, 1024u)
              : umma_smem_desc(base + kk * 32u, 16u, 1024u);
 }
