@@ -33,14 +33,16 @@ constexpr int64_t kMaxWidth = int64_t(1) << 24;
 // ------------------------------------------------------------------ the sort
 // Each CTA takes a run of consecutive choices, each of its warps a part of the
 // run. The first launch counts the runs' choices by expert, the second adds up
-// the counts of the runs before its own (every CTA for itself: at most 256 runs
+// the counts of the runs before its own (every CTA for itself: at most 64 runs
 // of 512 counts, from L2) and places its run's choices in their order. Up to
-// kSortOne choices one CTA does both in one launch.
+// kSortOne choices one CTA does both in one launch. In us: 8192 choices of 32 experts
+// by one CTA 10.1, by runs of 1024 6.7; 32768 of 32 by runs of 4096 8.9, of 1024 7.2;
+// 262144 of 256 by runs of 4096 17.6, of 1024 18.5 (a CTA's share of the counts).
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kMaxRuns = 256;
-constexpr int64_t kSortRun = 4096;  // choices a CTA takes at least
-constexpr int64_t kSortOne = 8192;
+constexpr int kMaxRuns = 64;
+constexpr int64_t kSortRun = 1024;  // choices a CTA takes at least
+constexpr int64_t kSortOne = 2048;
 
 struct SortIn {
   const int32_t* idx;
@@ -213,10 +215,16 @@ struct Unit<uint16_t, true> {
   }
 };
 
+// L lanes take an item: a piece of a token's row, or a choice. A warp (L = 32), or, where
+// a row is no longer than what 8 lanes hold and a token has no more than 8 choices, 8
+// of them: 65536 tokens of 64 bf16, 8 choices each, took 23, 51 and 178 us (gather,
+// combine, gradient) with a warp an item.
 constexpr int kRowThreads = 256;
 constexpr int kRowCtas = 8;  // an SM, at most
-constexpr int kGatherUnits = 4;   // units of a lane in a piece
-constexpr int kCombineUnits = 2;
+// Units of a lane in a piece, single elements and wide ones; more of the former pay for
+// the copy and the sum (16384 tokens of 4097 bf16, 2 choices: sum 132 us with 4, 94 with
+// 16), not for the gradient (159 us with 8, 182 with 16).
+constexpr int kGatherUnits[2] = {16, 4}, kCombineUnits[2] = {16, 2}, kGradUnits[2] = {8, 4};
 
 struct RowIn {
   int64_t T_, rows, ld, row_ld;  // tokens, rows; strides of the tokens' and of the rows' arrays
@@ -224,82 +232,92 @@ struct RowIn {
   const int32_t* place;
 };
 
-// Row of choice j of token t held by lane j, or -1.
-__device__ __forceinline__ int32_t place_at(const RowIn& p, int64_t t, int lane) {
-  const int32_t r = lane < p.K ? p.place[t * p.K + lane] : -1;
-  return r < p.rows ? r : -1;
-}
+// The items of a group of lanes: (t, piece), every step-th. All groups of a warp go
+// through as many; `on` is false where there is none.
+template <int L>
+struct Items {
+  int64_t t, step_t;
+  int32_t piece, step_p, pieces, left;
+  __device__ __forceinline__ Items(int64_t T_, int32_t pieces_) : pieces(pieces_) {
+    constexpr int G = 32 / L;
+    const int64_t groups = (int64_t)gridDim.x * (kRowThreads / L), n = T_ * pieces;
+    const int64_t warp0 = ((int64_t)blockIdx.x * kRowThreads + (threadIdx.x & ~31)) / L;
+    const int64_t first = warp0 + (threadIdx.x & 31) / L;
+    left = (int32_t)((n - warp0 + groups - 1) / groups);  // (of the warp's first group)
+    if (warp0 >= n) left = 0;
+    step_t = groups / pieces;
+    step_p = (int32_t)(groups - step_t * pieces);
+    t = first / pieces;
+    piece = (int32_t)(first - t * pieces);
+    static_assert(G >= 1, "");
+  }
+  __device__ __forceinline__ void next() {
+    --left;
+    t += step_t;
+    piece += step_p;
+    if (piece >= pieces) {
+      piece -= pieces;
+      ++t;
+    }
+  }
+};
 
-// rows[place[t, j]] = x[t]. A warp takes a piece of a token's row, reads it once
-// and writes it to the token's rows.
-template <typename T, bool WIDE>
+// rows[place[t, j]] = x[t]: a piece of a token's row, read once and written to the
+// token's rows.
+template <typename T, bool WIDE, int L>
 __global__ void __launch_bounds__(kRowThreads)
     gather_kernel(const RowIn p, const T* __restrict__ x, T* __restrict__ rows, int32_t pieces) {
   using U = Unit<T, WIDE>;
   using raw = typename U::raw;
-  constexpr int NU = WIDE ? kGatherUnits : 2 * kGatherUnits;
-  const int lane = threadIdx.x & 31;
+  constexpr int NU = kGatherUnits[WIDE];
+  const int lane = threadIdx.x & (L - 1);
   const int32_t units = p.H / U::n, tail = units * U::n;
   take_turn();
-  const int64_t step = (int64_t)gridDim.x * (kRowThreads / 32);
-  const int64_t step_t = step / pieces, first = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const int32_t step_p = (int32_t)(step - step_t * pieces);
-  int64_t t = first / pieces;
-  int32_t piece = (int32_t)(first - t * pieces);
-  for (; t < p.T_; t += step_t, piece += step_p) {
-    if (piece >= pieces) {
-      piece -= pieces;
-      if (++t >= p.T_) break;
-    }
-    const int32_t row = place_at(p, t, lane);
-    const uint32_t used = __ballot_sync(~0u, row >= 0);
-    if (used == 0) continue;
-    const T* in = x + t * p.ld;
-    const int32_t u0 = piece * (32 * NU) + lane;
+  for (Items<L> it(p.T_, pieces); it.left > 0; it.next()) {
+    const bool on = it.t < p.T_;
+    int32_t row = on && lane < p.K ? p.place[it.t * p.K + lane] : -1;
+    if (row >= p.rows) row = -1;
+    const T* in = x + (on ? it.t : 0) * p.ld;
+    const int32_t u0 = it.piece * (L * NU) + lane;
+    const bool any = __any_sync(~0u, row >= 0);
     raw v[NU];
 #pragma unroll
     for (int k = 0; k < NU; ++k)
-      if (u0 + 32 * k < units) v[k] = reinterpret_cast<const raw*>(in)[u0 + 32 * k];
-    const bool last = piece + 1 == pieces && tail + lane < p.H;
+      if (any && on && u0 + L * k < units) v[k] = reinterpret_cast<const raw*>(in)[u0 + L * k];
+    const bool last = on && it.piece + 1 == pieces && tail + lane < p.H;
     T loose = T();
     if (last) loose = in[tail + lane];
-    for (uint32_t left = used; left != 0; left &= left - 1) {
-      T* out = rows + (int64_t)__shfl_sync(~0u, row, __ffs(left) - 1) * p.row_ld;
+    for (int j = 0; any && j < p.K; ++j) {
+      const int32_t r = __shfl_sync(~0u, row, j, L);
+      if (r < 0) continue;
+      T* out = rows + (int64_t)r * p.row_ld;
 #pragma unroll
       for (int k = 0; k < NU; ++k)
-        if (u0 + 32 * k < units) reinterpret_cast<raw*>(out)[u0 + 32 * k] = v[k];
+        if (u0 + L * k < units) reinterpret_cast<raw*>(out)[u0 + L * k] = v[k];
       if (last) out[tail + lane] = loose;
     }
   }
 }
 
 // out[t] = sum_j g[t, j] y[place[t, j]] (GATES), or the plain sum; in fp32, one
-// choice after the other, rounded once. A warp takes a piece of a token's row;
-// four choices' loads are on their way at a time.
-template <typename T, bool WIDE, bool GATES>
+// choice after the other, rounded once. Four choices' loads are on their way at a time.
+template <typename T, bool WIDE, bool GATES, int L>
 __global__ void __launch_bounds__(kRowThreads)
     combine_kernel(const RowIn p, const T* __restrict__ y, const float* __restrict__ gates,
                    T* __restrict__ out, int32_t pieces) {
   using U = Unit<T, WIDE>;
   using raw = typename U::raw;
-  constexpr int NU = WIDE ? kCombineUnits : 2 * kCombineUnits, JB = 4;
-  const int lane = threadIdx.x & 31;
+  constexpr int NU = kCombineUnits[WIDE], JB = 4;
+  const int lane = threadIdx.x & (L - 1);
   const int32_t units = p.H / U::n, tail = units * U::n;
   take_turn();
-  const int64_t step = (int64_t)gridDim.x * (kRowThreads / 32);
-  const int64_t step_t = step / pieces, first = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const int32_t step_p = (int32_t)(step - step_t * pieces);
-  int64_t t = first / pieces;
-  int32_t piece = (int32_t)(first - t * pieces);
-  for (; t < p.T_; t += step_t, piece += step_p) {
-    if (piece >= pieces) {
-      piece -= pieces;
-      if (++t >= p.T_) break;
-    }
-    const int32_t row = place_at(p, t, lane);
-    const float gate = GATES && lane < p.K ? gates[t * p.K + lane] : 1.f;
-    const int32_t u0 = piece * (32 * NU) + lane;
-    const bool last = piece + 1 == pieces && tail + lane < p.H;
+  for (Items<L> it(p.T_, pieces); it.left > 0; it.next()) {
+    const bool on = it.t < p.T_;
+    int32_t row = on && lane < p.K ? p.place[it.t * p.K + lane] : -1;
+    if (row >= p.rows) row = -1;
+    const float gate = GATES && row >= 0 ? gates[it.t * p.K + lane] : 1.f;
+    const int32_t u0 = it.piece * (L * NU) + lane;
+    const bool last = on && it.piece + 1 == pieces && tail + lane < p.H;
     float acc[NU][U::n], loose = 0.f;
 #pragma unroll
     for (int k = 0; k < NU; ++k)
@@ -311,18 +329,18 @@ __global__ void __launch_bounds__(kRowThreads)
       T lv[JB];
 #pragma unroll
       for (int j = 0; j < JB; ++j) {
-        r[j] = __shfl_sync(~0u, row, (j0 + j) & 31);
+        r[j] = __shfl_sync(~0u, row, (j0 + j) & (L - 1), L);
         if (j0 + j >= p.K) r[j] = -1;
         if (r[j] < 0) continue;
         const T* in = y + (int64_t)r[j] * p.row_ld;
 #pragma unroll
         for (int k = 0; k < NU; ++k)
-          if (u0 + 32 * k < units) v[j][k] = reinterpret_cast<const raw*>(in)[u0 + 32 * k];
+          if (u0 + L * k < units) v[j][k] = reinterpret_cast<const raw*>(in)[u0 + L * k];
         if (last) lv[j] = in[tail + lane];
       }
 #pragma unroll
       for (int j = 0; j < JB; ++j) {
-        const float g = __shfl_sync(~0u, gate, (j0 + j) & 31);
+        const float g = __shfl_sync(~0u, gate, (j0 + j) & (L - 1), L);
         if (r[j] < 0) continue;
 #pragma unroll
         for (int k = 0; k < NU; ++k) {
@@ -334,74 +352,75 @@ __global__ void __launch_bounds__(kRowThreads)
         if (last) loose = GATES ? __fmaf_rn(g, to_f(lv[j]), loose) : loose + to_f(lv[j]);
       }
     }
-    T* to = out + t * p.ld;
+    if (!on) continue;
+    T* to = out + it.t * p.ld;
 #pragma unroll
     for (int k = 0; k < NU; ++k)
-      if (u0 + 32 * k < units) reinterpret_cast<raw*>(to)[u0 + 32 * k] = U::put(acc[k]);
+      if (u0 + L * k < units) reinterpret_cast<raw*>(to)[u0 + L * k] = U::put(acc[k]);
     if (last) to[tail + lane] = from_f<T>(loose);
   }
 }
 
-// dy[place[t, j]] = g[t, j] d_out[t] and dg[t, j] = <d_out[t], y[place[t, j]]>. A
-// warp takes a choice; the warps of a token read its row at about the same time,
-// all but one of them from L1 or L2. y and d_y may be the same rows.
-template <typename T, bool WIDE>
+// dy[place[t, j]] = g[t, j] d_out[t] and dg[t, j] = <d_out[t], y[place[t, j]]>, a choice
+// at a time; the lanes of a token's choices read its row at about the same time, all
+// but the first from L1 or L2. y and d_y may be the same rows.
+template <typename T, bool WIDE, int L>
 __global__ void __launch_bounds__(kRowThreads)
     combine_grad_kernel(const RowIn p, const T* __restrict__ d_out, const T* y, int64_t y_ld,
                         const float* __restrict__ gates, T* d_y, float* __restrict__ d_gates) {
   using U = Unit<T, WIDE>;
   using raw = typename U::raw;
-  constexpr int NU = WIDE ? 4 : 8;
-  const int lane = threadIdx.x & 31;
+  constexpr int NU = kGradUnits[WIDE];
+  const int lane = threadIdx.x & (L - 1);
   const int32_t units = p.H / U::n, tail = units * U::n;
   take_turn();
-  const int64_t items = p.T_ * p.K, step = (int64_t)gridDim.x * (kRowThreads / 32);
-  for (int64_t c = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); c < items; c += step) {
-    const int32_t row = p.place[c];
-    if (row < 0 || row >= p.rows) {
-      if (lane == 0) d_gates[c] = 0.f;
-      continue;
-    }
-    const float g = gates[c];
-    const T* d = d_out + (int64_t)((uint32_t)c / (uint32_t)p.K) * p.ld;
-    const T* in = y + (int64_t)row * y_ld;
-    T* to = d_y + (int64_t)row * p.row_ld;
+  for (Items<L> it(p.T_, p.K); it.left > 0; it.next()) {
+    const bool on = it.t < p.T_;
+    const int64_t c = it.t * p.K + it.piece;
+    const int32_t row = on ? p.place[c] : -1;
+    const bool used = row >= 0 && row < p.rows;
     float dot[NU];
 #pragma unroll
     for (int k = 0; k < NU; ++k) dot[k] = 0.f;
-    for (int32_t u0 = lane; u0 < units; u0 += 32 * NU) {
-      raw a[NU], b[NU];
+    if (used) {
+      const float g = gates[c];
+      const T* d = d_out + it.t * p.ld;
+      const T* in = y + (int64_t)row * y_ld;
+      T* to = d_y + (int64_t)row * p.row_ld;
+      for (int32_t u0 = lane; u0 < units; u0 += L * NU) {
+        raw a[NU], b[NU];
 #pragma unroll
-      for (int k = 0; k < NU; ++k)
-        if (u0 + 32 * k < units) {
-          a[k] = reinterpret_cast<const raw*>(d)[u0 + 32 * k];
-          b[k] = reinterpret_cast<const raw*>(in)[u0 + 32 * k];
-        }
-#pragma unroll
-      for (int k = 0; k < NU; ++k)
-        if (u0 + 32 * k < units) {
-          float fa[U::n], fb[U::n];
-          U::get(a[k], fa);
-          U::get(b[k], fb);
-#pragma unroll
-          for (int q = 0; q < U::n; ++q) {
-            dot[k] = __fmaf_rn(fa[q], fb[q], dot[k]);
-            fa[q] *= g;
+        for (int k = 0; k < NU; ++k)
+          if (u0 + L * k < units) {
+            a[k] = reinterpret_cast<const raw*>(d)[u0 + L * k];
+            b[k] = reinterpret_cast<const raw*>(in)[u0 + L * k];
           }
-          reinterpret_cast<raw*>(to)[u0 + 32 * k] = U::put(fa);
-        }
-    }
-    if (tail + lane < p.H) {
-      const float a = to_f(d[tail + lane]);
-      dot[0] = __fmaf_rn(a, to_f(in[tail + lane]), dot[0]);
-      to[tail + lane] = from_f<T>(g * a);
+#pragma unroll
+        for (int k = 0; k < NU; ++k)
+          if (u0 + L * k < units) {
+            float fa[U::n], fb[U::n];
+            U::get(a[k], fa);
+            U::get(b[k], fb);
+#pragma unroll
+            for (int q = 0; q < U::n; ++q) {
+              dot[k] = __fmaf_rn(fa[q], fb[q], dot[k]);
+              fa[q] *= g;
+            }
+            reinterpret_cast<raw*>(to)[u0 + L * k] = U::put(fa);
+          }
+      }
+      if (tail + lane < p.H) {
+        const float a = to_f(d[tail + lane]);
+        dot[0] = __fmaf_rn(a, to_f(in[tail + lane]), dot[0]);
+        to[tail + lane] = from_f<T>(g * a);
+      }
     }
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < NU; ++k) sum += dot[k];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    if (lane == 0) d_gates[c] = sum;
+    for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    if (on && lane == 0) d_gates[c] = sum;
   }
 }
 
@@ -453,49 +472,52 @@ bool overlap(const RowsArg& a, const Strided& x, const Strided& y) {
   return x0 < y0 + ((y.n - 1) * y.ld + a.H) * size && y0 < x0 + ((x.n - 1) * x.ld + a.H) * size;
 }
 
-bool wide(const RowsArg& a, std::initializer_list<Strided> in) {
+bool all_wide(const RowsArg& a, std::initializer_list<Strided> in) {
   const int64_t size = a.dtype == VSF_BF16 ? 2 : 4;
   for (const Strided& s : in)
     if (!aligned(s.p, 16) || s.ld * size % 16 != 0) return false;
   return true;
 }
 
-// Pieces of a row, and CTAs for `items` warps.
-int32_t pieces_of(const RowsArg& a, bool w, int units) {
-  const int64_t n = w ? a.H / (a.dtype == VSF_BF16 ? 8 : 4) : a.H;
-  const int64_t per = 32 * (w ? units : 2 * units);
-  return (int32_t)std::max<int64_t>(1, (n + per - 1) / per);
-}
-unsigned row_grid(int64_t items) {
-  return (unsigned)std::min<int64_t>((items + kRowThreads / 32 - 1) / (kRowThreads / 32),
-                                     kSms * kRowCtas);
+// How a call's rows are taken: whether in wide units, by how many lanes, in how many
+// pieces of `units` a lane; and its CTAs.
+struct RowSplit {
+  bool wide;
+  int lanes;
+  int32_t pieces;
+  RowSplit(const RowsArg& a, std::initializer_list<Strided> in, const int (&units)[2]) : wide(all_wide(a, in)) {
+    const int64_t n = wide ? a.H / (a.dtype == VSF_BF16 ? 8 : 4) : a.H;
+    lanes = a.K <= 8 && n <= 8 * units[wide] ? 8 : 32;
+    pieces = (int32_t)std::max<int64_t>(1, (n + lanes * units[wide] - 1) / (lanes * units[wide]));
+  }
+  unsigned grid(int64_t items) const {
+    const int64_t of = kRowThreads / lanes;
+    return (unsigned)std::min<int64_t>((items + of - 1) / of, kSms * kRowCtas);
+  }
+};
+#define VSF_BY_SPLIT(F, T, s, ...)                                             \
+  ((s).wide ? (s).lanes == 8 ? F<T, true, ##__VA_ARGS__, 8> : F<T, true, ##__VA_ARGS__, 32> \
+            : (s).lanes == 8 ? F<T, false, ##__VA_ARGS__, 8> : F<T, false, ##__VA_ARGS__, 32>)
+
+template <typename T>
+cudaError_t launch_gather(const RowIn& p, const void* x, void* rows, const RowSplit& s, cudaStream_t st) {
+  return launch_behind(VSF_BY_SPLIT(gather_kernel, T, s), s.grid(p.T_ * s.pieces), kRowThreads, 0, 1, st, p,
+                       static_cast<const T*>(x), static_cast<T*>(rows), s.pieces);
 }
 
 template <typename T>
-cudaError_t launch_gather(const RowsArg& a, const RowIn& p, const void* x, void* rows, bool w,
-                          cudaStream_t st) {
-  const int32_t pieces = pieces_of(a, w, kGatherUnits);
-  return launch_behind(w ? gather_kernel<T, true> : gather_kernel<T, false>, row_grid(a.T_ * pieces),
-                       kRowThreads, 0, 1, st, p, static_cast<const T*>(x), static_cast<T*>(rows),
-                       pieces);
+cudaError_t launch_combine(const RowIn& p, const void* y, const float* gates, void* out, const RowSplit& s,
+                           cudaStream_t st) {
+  auto fn = gates != nullptr ? VSF_BY_SPLIT(combine_kernel, T, s, true) : VSF_BY_SPLIT(combine_kernel, T, s, false);
+  return launch_behind(fn, s.grid(p.T_ * s.pieces), kRowThreads, 0, 1, st, p, static_cast<const T*>(y), gates,
+                       static_cast<T*>(out), s.pieces);
 }
 
 template <typename T>
-cudaError_t launch_combine(const RowsArg& a, const RowIn& p, const void* y, const float* gates,
-                           void* out, bool w, cudaStream_t st) {
-  const int32_t pieces = pieces_of(a, w, kCombineUnits);
-  auto fn = gates != nullptr ? (w ? combine_kernel<T, true, true> : combine_kernel<T, false, true>)
-                             : (w ? combine_kernel<T, true, false> : combine_kernel<T, false, false>);
-  return launch_behind(fn, row_grid(a.T_ * pieces), kRowThreads, 0, 1, st, p,
-                       static_cast<const T*>(y), gates, static_cast<T*>(out), pieces);
-}
-
-template <typename T>
-cudaError_t launch_combine_grad(const RowsArg& a, const RowIn& p, const void* d_out, const void* y,
-                                int64_t y_ld, const float* gates, void* d_y, float* d_gates, bool w,
+cudaError_t launch_combine_grad(const RowIn& p, const void* d_out, const void* y, int64_t y_ld,
+                                const float* gates, void* d_y, float* d_gates, const RowSplit& s,
                                 cudaStream_t st) {
-  return launch_behind(w ? combine_grad_kernel<T, true> : combine_grad_kernel<T, false>,
-                       row_grid(a.T_ * a.K), kRowThreads, 0, 1, st, p,
+  return launch_behind(VSF_BY_SPLIT(combine_grad_kernel, T, s), s.grid(p.T_ * p.K), kRowThreads, 0, 1, st, p,
                        static_cast<const T*>(d_out), static_cast<const T*>(y), y_ld, gates,
                        static_cast<T*>(d_y), d_gates);
 }
@@ -554,10 +576,10 @@ vsf_status vsf_expert_gather(const void* x, int32_t dtype, int64_t T, int64_t H,
   if (overlap(a, in, out)) return fail(VSF_ERR_ARG, "vsf_expert_gather: rows overlap the tokens");
   if (T == 0) return VSF_OK;
   const RowIn p = {T, T * top_k, ld, rows_ld, (int32_t)top_k, (int32_t)H, place};
-  const bool w = wide(a, {in, out});
+  const RowSplit w(a, {in, out}, kGatherUnits);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == VSF_BF16 ? launch_gather<uint16_t>(a, p, x, rows, w, st)
-                                          : launch_gather<float>(a, p, x, rows, w, st);
+  const cudaError_t e = dtype == VSF_BF16 ? launch_gather<uint16_t>(p, x, rows, w, st)
+                                          : launch_gather<float>(p, x, rows, w, st);
   return e == cudaSuccess ? VSF_OK : cuda_error(e, a.who);
 }
 
@@ -573,10 +595,10 @@ vsf_status vsf_expert_combine(const void* y, int32_t dtype, int64_t T, int64_t H
   if (overlap(a, in, to)) return fail(VSF_ERR_ARG, "vsf_expert_combine: rows overlap the tokens");
   if (T == 0) return VSF_OK;
   const RowIn p = {T, T * top_k, out_ld, y_ld, (int32_t)top_k, (int32_t)H, place};
-  const bool w = wide(a, {in, to});
+  const RowSplit w(a, {in, to}, kCombineUnits);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == VSF_BF16 ? launch_combine<uint16_t>(a, p, y, gates, out, w, st)
-                                          : launch_combine<float>(a, p, y, gates, out, w, st);
+  const cudaError_t e = dtype == VSF_BF16 ? launch_combine<uint16_t>(p, y, gates, out, w, st)
+                                          : launch_combine<float>(p, y, gates, out, w, st);
   return e == cudaSuccess ? VSF_OK : cuda_error(e, a.who);
 }
 
@@ -597,12 +619,12 @@ vsf_status vsf_expert_combine_grad(const void* d_out, int32_t dtype, int64_t T, 
     return fail(VSF_ERR_ARG, "vsf_expert_combine_grad: d_y overlaps an input in part");
   if (T == 0) return VSF_OK;
   const RowIn p = {T, T * top_k, d_out_ld, d_y_ld, (int32_t)top_k, (int32_t)H, place};
-  const bool w = wide(a, {d, in, to});
+  const RowSplit w(a, {d, in, to}, kGradUnits);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
       dtype == VSF_BF16
-          ? launch_combine_grad<uint16_t>(a, p, d_out, y, y_ld, gates, d_y, d_gates, w, st)
-          : launch_combine_grad<float>(a, p, d_out, y, y_ld, gates, d_y, d_gates, w, st);
+          ? launch_combine_grad<uint16_t>(p, d_out, y, y_ld, gates, d_y, d_gates, w, st)
+          : launch_combine_grad<float>(p, d_out, y, y_ld, gates, d_y, d_gates, w, st);
   return e == cudaSuccess ? VSF_OK : cuda_error(e, a.who);
 }
 

@@ -51,6 +51,10 @@ DISPATCH = [  # tokens, experts, k, width, dtype, masked, pad, shift
     (100, 512, 8, 130, FP32, True, 2, 4),
     (65, 3, 32, 96, BF16, True, 0, 3),     # rows off the 16-byte boundaries
     (300, 7, 7, 40, FP32, True, 1, 0),
+    (257, 9, 8, 64, BF16, True, 0, 0),     # eight lanes a token
+    (130, 9, 5, 250, BF16, True, 6, 8),
+    (90, 9, 8, 61, FP32, True, 0, 1),
+    (64, 40, 9, 64, BF16, True, 0, 0),     # as narrow, but nine choices
 ]
 
 
