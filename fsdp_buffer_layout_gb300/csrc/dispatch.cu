@@ -16,6 +16,7 @@
 
 #include <algorithm>
 #include <initializer_list>
+#include <utility>
 #include <string>
 
 #include "objective.cuh"
@@ -548,6 +549,16 @@ vsf_status vsf_expert_sort(const int32_t* idx, int64_t T, int64_t top_k, int64_t
   if (!aligned(idx, 4) || !aligned(starts, 4) || !aligned(source, 4) || !aligned(place, 4) ||
       !aligned(d_workspace, 16))
     return fail(VSF_ERR_ALIGN, "vsf_expert_sort: pointer alignment");
+  // what is written overlaps neither what is read nor each other
+  const std::pair<const void*, int64_t> used[] = {
+      {idx, n * 4}, {starts, (E + 1) * 4}, {source, source != nullptr ? n * 4 : 0}, {place, n * 4},
+      {d_workspace, (int64_t)sort_bytes(n, E)}};
+  for (int i = 0; i < 5; ++i)
+    for (int j = 0; j < i; ++j) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(used[i].first), b = reinterpret_cast<uintptr_t>(used[j].first);
+      if (a < b + used[j].second && b < a + used[i].second)
+        return fail(VSF_ERR_ARG, "vsf_expert_sort: arrays overlap");
+    }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool one = n <= kSortOne;
   const int64_t run = one ? std::max<int64_t>(n, 1) : run_of(n);

@@ -70,7 +70,8 @@ vsf_status check(int kind, const Product& a) {
   const uintptr_t r1 = end(a.rows_in, a.rows, a.rows_ld, in);
   const uintptr_t w1 = kind == kWeight ? end(a.other, a.rows, a.other_ld, a.K)
                                        : end(a.other + (a.E - 1) * a.other_stride, a.N, a.other_ld, a.K);
-  if ((o0 < r1 && r0 < o1) || (o0 < w1 && w0 < o1))
+  const uintptr_t s0 = reinterpret_cast<uintptr_t>(a.starts), s1 = s0 + (uintptr_t)(a.E + 1) * 4;
+  if ((o0 < r1 && r0 < o1) || (o0 < w1 && w0 < o1) || (o0 < s1 && s0 < o1))
     return fail(VSF_ERR_ARG, w + ": the output overlaps an input");
   return VSF_OK;
 }

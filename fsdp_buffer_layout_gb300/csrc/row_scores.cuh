@@ -702,8 +702,8 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas)
         }
       }
     } else {
-      const int32_t e1 = v1 * VE;
-      for (int32_t e = v0 * VE + lane; e < e1; e += 32) g[s.head + e] = from_f<T>(common(to_f(x[s.head + e])));
+      for (int64_t e = (int64_t)v0 * VE + lane; e < (int64_t)v1 * VE; e += 32)
+        g[s.head + e] = from_f<T>(common(to_f(x[s.head + e])));
     }
     if (loose >= 0) g[loose] = from_f<T>(common(xl));
     __syncwarp();

@@ -37,6 +37,7 @@ WEIGHT = dict(d_y=A, rows=16, N=96, d_y_ld=96, x=2 * A, K=64, x_ld=64, E=4, star
     (dict(T=-1), ARG), (dict(T=(1 << 23) + 1), ARG), (dict(top_k=0), ARG), (dict(top_k=33), ARG),
     (dict(E=0), ARG), (dict(E=513), ARG), (dict(ws_bytes=8), ARG),
     (dict(T=8192, ws_bytes=16), ARG),  # 16384 choices need counts of four runs
+    (dict(place=A), ARG), (dict(starts=4 * A + 4), ARG), (dict(source=4 * A + 28), ARG),  # overlaps
     (dict(idx=A + 2), ALIGN), (dict(source=A + 1), ALIGN), (dict(d_workspace=A + 8), ALIGN)])
 def test_sort_refusals(change, want):
     refuse(V.vsf_expert_sort, SORT, change, want)
@@ -75,7 +76,8 @@ def test_row_refusals(call, args, extra):
         (dict(w_ld=56), ARG), (dict(w_stride=95 * 64), ARG), (dict(y=A), ARG), (dict(y=2 * A + 64), ARG),
         (dict(x=A + 8), ALIGN), (dict(w=2 * A + 2), ALIGN), (dict(y=4 * A + 4), ALIGN),
         (dict(x_ld=65), ALIGN), (dict(w_ld=65, w_stride=97 * 65), ALIGN), (dict(y_ld=97), ALIGN),
-        (dict(w_stride=96 * 64 + 4), ALIGN)]),
+        (dict(w_stride=96 * 64 + 4), ALIGN),
+        (dict(starts=4 * A + 16), ARG)]),
     (V.vsf_expert_product_input_grad, INPUT, [
         (dict(d_y=0), ARG), (dict(w=0), ARG), (dict(d_x=0), ARG), (dict(d_y_ld=88), ARG),
         (dict(d_x_ld=56), ARG), (dict(w_stride=95 * 64), ARG), (dict(d_x=A), ARG),

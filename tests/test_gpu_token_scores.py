@@ -357,3 +357,40 @@ def test_object_refuses():
     for bad in (dict(top_k=33), dict(top_k=-1), dict(top_k=101)):
         with pytest.raises(ValueError):
             TokenScores(8, 100 if bad["top_k"] != 101 else 3, **bad)
+
+
+def test_longest_row():
+    """Rows of 2^31 - 1 words, the most: a few finite ones at both ends and in
+    between, the others -inf; a masked row; the gradient with rows that start
+    elsewhere against 16 bytes than the logits'."""
+    from fsdp_buffer_layout_gb300.objectives import TokenScores
+    vocab, ld = (1 << 31) - 1, 1 << 31
+    buf = torch.full((3 + 2 * ld,), -math.inf, dtype=BF16, device="cuda")
+    x = buf.as_strided((2, vocab), (ld, 1), 3)
+    words = [0, 1, 4, 5, 1 << 20, (1 << 30) + 7, vocab - 9, vocab - 8, vocab - 2, vocab - 1]
+    at = dev(words, torch.int64)
+    z = np.arange(10) * 0.25
+    x[1, at] = dev(z).to(BF16)
+    y = dev([-1, vocab - 1], torch.int64)
+    op = TokenScores(2, vocab, top_k=4, with_grad=False)
+    logp, entropy, idx, top_logp = op.forward(x, y)
+    p = np.exp(z) / np.exp(z).sum()
+    assert idx[1].tolist() == words[:5:-1] and idx[0].tolist() == [-1] * 4
+    assert abs(logp[1].item() - math.log(p[-1])) <= 2.0**-20
+    assert abs(entropy[1].item() + (p * np.log(p)).sum()) <= 2.0**-19
+    assert np.abs(host(top_logp[1]) - np.log(p[:5:-1])).max() <= 2.0**-20
+    h, d_top = -(p * np.log(p)).sum(), np.array([0.5, 0, -1.0, 2.0])
+    want = -p * (1.0 + d_top.sum() + 3.0 * (np.log(p) + h))
+    want[-1] += 1.0
+    want[:5:-1] += d_top
+    del logp, entropy, top_logp
+    for shift in (3, 4):
+        out = torch.full((shift + 2 * ld,), math.nan, dtype=BF16, device="cuda")
+        g = out.as_strided((2, vocab), (ld, 1), shift)
+        op.backward(x, y, dev([1.0, 1.0]), dev([3.0, 3.0]), dev(np.stack([d_top, d_top])), grad=g)
+        assert (np.abs(host(g[1, at]) - want) <= 2.0**-8 * np.abs(want) + 2.0**-18).all()
+        assert torch.count_nonzero(g[0]).item() == 0
+        assert torch.count_nonzero(g[1]).item() == 10  # (NaN would count)
+        assert torch.isnan(out[:shift]).all() and torch.isnan(out[shift + vocab:shift + ld]).all()
+        del out, g
+    assert op.device_error() == 0
