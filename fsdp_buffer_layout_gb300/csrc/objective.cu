@@ -682,7 +682,7 @@ cudaError_t scores_grad(const RowsArg& a, int32_t K, const float* norm, const in
   k.d_top = d_top;
   k.grad = static_cast<T*>(grad);
   k.grad_ld = grad_ld;
-  return launch_behind(score_grad_kernel<T>, score_grid(a.T_ * k.cut.pieces, kScoreCtas), kScoreThreads, 0, 1,
+  return launch_behind(score_grad_kernel<T>, score_grid(a.T_ * k.cut.pieces, kPartCtas), kScoreThreads, 0, 1,
                        st, k);
 }
 

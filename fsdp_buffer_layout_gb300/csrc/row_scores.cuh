@@ -31,8 +31,7 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 __device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(~0u, v); }
 
 constexpr int kScoreThreads = 256;
-constexpr int kScoreCtas = 4;        // an SM (gradient)
-constexpr int kPartCtas = 3;         // an SM (sums)
+constexpr int kPartCtas = 3;         // an SM
 constexpr int kScoreBatch = 4;       // vectors of a lane on their way at a time
 constexpr int kMaxTop = 32;
 
@@ -592,7 +591,7 @@ struct ScoreGradArgs {
 
 // A warp a piece of a row, as in the sums.
 template <typename T>
-__global__ void __launch_bounds__(kScoreThreads, kScoreCtas)
+__global__ void __launch_bounds__(kScoreThreads, kPartCtas)
     score_grad_kernel(const __grid_constant__ ScoreGradArgs<T> a) {
   constexpr int VE = Vec<T>::n, B = kScoreBatch;
   const int lane = threadIdx.x & 31;
@@ -610,6 +609,12 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas)
       p -= pieces;
       if (++t >= r.T_) break;
     }
+    // (all of a row's scalars on their way at a time)
+    const float4 nm4 = a.norm[t];
+    const float da = a.d_logp != nullptr ? a.d_logp[t] : 0.f;
+    const float dh = a.d_entropy != nullptr ? a.d_entropy[t] : 0.f;
+    const float db = lane < a.K && a.d_top != nullptr ? a.d_top[t * a.K + lane] : 0.f;
+    const int32_t ti = lane < a.K && a.d_top != nullptr ? a.top_idx[t * a.K + lane] : -1;
     const int32_t y = live_target(r, t, nullptr);
     const T* x = r.x + t * r.ld;
     T* g = a.grad + t * a.grad_ld;
@@ -627,11 +632,16 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas)
       if (loose >= 0) g[loose] = from_f<T>(0.f);
       continue;
     }
-    const float4 nm4 = a.norm[t];
-    const float da = a.d_logp != nullptr ? a.d_logp[t] : 0.f;
-    const float dh = a.d_entropy != nullptr ? a.d_entropy[t] : 0.f;
-    const float db = lane < a.K && a.d_top != nullptr ? a.d_top[t * a.K + lane] : 0.f;
-    const int32_t ti = lane < a.K && a.d_top != nullptr ? a.top_idx[t * a.K + lane] : -1;
+    // the first vectors
+    const bool same = ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0;
+    const uint4* in = reinterpret_cast<const uint4*>(x + s.head) + lane;
+    uint4 q0[B], q1[B];
+    auto load = [&](uint4 (&q)[B], int32_t v) {
+#pragma unroll
+      for (int j = 0; j < B; ++j)
+        if (v + 32 * j + lane < v1) q[j] = __ldcs(in + v + 32 * j);
+    };
+    if (same) load(q0, v0);
     const float pull = da + warp_sum(db);
     const float z0 = finite_max(nm4.x);
     const float scale = -r.inv_tf / nm4.y;
@@ -679,13 +689,9 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas)
     if (loose >= 0) xl = to_f(x[loose]);
     __syncwarp();
     const F2 nz = f2(-z0, -z0), c02 = f2(c0, c0), h22 = f2(h2, h2);
-    if (((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(x)) & 15) == 0) {
-      const uint4* in = reinterpret_cast<const uint4*>(x + s.head) + lane;
-      for (int32_t v = v0; v < v1; v += 32 * B) {
-        uint4 q[B];
-#pragma unroll
-        for (int j = 0; j < B; ++j)
-          if (v + 32 * j + lane < v1) q[j] = __ldcs(in + v + 32 * j);
+    if (same) {
+      // by turns in two sets of registers
+      auto put = [&](const uint4 (&q)[B], int32_t v) {
 #pragma unroll
         for (int j = 0; j < B; ++j) {
           if (v + 32 * j + lane >= v1) break;
@@ -700,6 +706,12 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas)
           }
           __stcs(out + v + 32 * j, pack_vec<T>(o));
         }
+      };
+      for (int32_t v = v0; v < v1; v += 64 * B) {
+        load(q1, v + 32 * B);
+        put(q0, v);
+        load(q0, v + 64 * B);
+        put(q1, v + 32 * B);
       }
     } else {
       for (int64_t e = (int64_t)v0 * VE + lane; e < (int64_t)v1 * VE; e += 32)
