@@ -91,7 +91,7 @@ __device__ __forceinline__ int32_t token_width(int32_t rows, int32_t tiles) {
   return ((rows + tiles - 1) / tiles + 31) / 32 * 32;
 }
 
-// Tile t of the launch; `e` moves on from tile to tile.
+// Tile t of the launch, for a converged warp; `e` moves on from tile to tile.
 template <int KIND>
 __device__ __forceinline__ XTile tile_at(const ExpertArgs& a, const XTable& x, int32_t t, int32_t& e) {
   XTile q;
@@ -106,7 +106,13 @@ __device__ __forceinline__ XTile tile_at(const ExpertArgs& a, const XTable& x, i
     q.row0 = x.start[q.e];
     q.depth = x.start[q.e + 1] - q.row0;
   } else {
-    while (t >= x.first[e + 1]) ++e;
+    // 32 experts at a time (one after the other the walk bound a launch of many small
+    // experts: 512 of 4 rows, 256 x 64, 29 us instead of 16)
+    for (int32_t n = 32; n == 32;) {
+      const int32_t k = e + 1 + (int32_t)(threadIdx.x & 31);
+      n = __popc(__ballot_sync(~0u, k <= a.E && t >= x.first[k]));
+      e += n;
+    }
     q.e = e;
     // eight pieces of rows at a time take a lane tile one after the other: its
     // weights come from memory once, and are asked for by fewer pairs at a time (2 to 4
@@ -398,6 +404,14 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
       const int buf = lt & 1;
       const bool ok = warp_wait(tfull_bar(buf), (uint32_t)(lt >> 1) & 1u, err, stop);
       tc_fence_after();
+      // The accumulator is free once its last columns are in registers: said before
+      // they are stored, as the arrival (a release) waits for the warp's stores.
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(leader_tempty0 + 8u * buf);
+      };
+      if (!ok) release();
       if (ok) {
         const XTile q = tile_at<KIND>(g, table, t, e);
         const int32_t i = q.lane0 + rank * 128 + 32 * quarter + lane;
@@ -417,6 +431,7 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
               uint32_t r[32];
               __syncwarp();
               tmem_ld32(from + c + 32 * h, r);
+              if (h == 1 && c + 64 >= q.cols) release();
 #pragma unroll
               for (int x = 0; x < 16; ++x)
                 p[16 * h + x] = q.depth == 0 ? 0u : pack_bf16(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1]));
@@ -445,6 +460,7 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
           uint32_t r[32];
           __syncwarp();
           tmem_ld32(from + c, r);
+          if (c + 32 >= q.cols) release();
           {
             // Lane pairs trade columns: an even lane keeps column x and gets its
             // neighbour's, an odd one column x + 1, so that each has two adjacent
@@ -494,9 +510,6 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(leader_tempty0 + 8u * buf);
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else {
