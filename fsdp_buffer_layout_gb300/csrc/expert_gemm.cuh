@@ -84,12 +84,10 @@ struct XTile {
   int32_t row0, depth;  // what is summed over
 };
 
-// An expert's rows in tiles of at most 256, as even as can be: one of a width
-// of 256 and a narrow one would cost a whole tile's weights for the narrow one.
+// An expert's rows in tiles of at most 256, as even as can be in units of 32: one of 256
+// and a narrow one would cost more than half a tile for the narrow one, and as many of
+// one width compute up to an eighth too many.
 __device__ __forceinline__ int32_t token_tiles(int32_t rows) { return (rows + kXCols - 1) / kXCols; }
-__device__ __forceinline__ int32_t token_width(int32_t rows, int32_t tiles) {
-  return ((rows + tiles - 1) / tiles + 31) / 32 * 32;
-}
 
 // Tile t of the launch, for a converged warp; `e` moves on from tile to tile.
 template <int KIND>
@@ -123,8 +121,9 @@ __device__ __forceinline__ XTile tile_at(const ExpertArgs& a, const XTable& x, i
     k -= block * a.lane_tiles;
     const int32_t lane_tile = k / n, piece = block + k - lane_tile * n;
     q.lane0 = lane_tile * kXLanes;
-    q.width = token_width(rows, pieces);
-    q.col0 = begin + piece * q.width;
+    const int32_t unit = (rows + 31) / 32, unit0 = (int32_t)((int64_t)unit * piece / pieces);
+    q.width = 32 * ((int32_t)((int64_t)unit * (piece + 1) / pieces) - unit0);
+    q.col0 = begin + 32 * unit0;
     q.cols = min(q.width, begin + rows - q.col0);
     q.row0 = 0;
     q.depth = a.depth;
