@@ -631,6 +631,10 @@ vsf_status vsf_expert_combine_grad(const void* d_out, int32_t dtype, int64_t T, 
     return fail(VSF_ERR_ALIGN, "vsf_expert_combine_grad: pointer alignment");
   if (overlap(a, d, to) || (overlap(a, in, to) && !(y == d_y && y_ld == d_y_ld)))
     return fail(VSF_ERR_ARG, "vsf_expert_combine_grad: d_y overlaps an input in part");
+  const uintptr_t n = (uintptr_t)(T * top_k) * 4, g0 = reinterpret_cast<uintptr_t>(d_gates);
+  for (const void* p : {static_cast<const void*>(gates), static_cast<const void*>(place)})
+    if (g0 < reinterpret_cast<uintptr_t>(p) + n && reinterpret_cast<uintptr_t>(p) < g0 + n)
+      return fail(VSF_ERR_ARG, "vsf_expert_combine_grad: d_gates overlaps an input");
   if (T == 0) return VSF_OK;
   const RowIn p = {T, T * top_k, d_out_ld, d_y_ld, (int32_t)top_k, (int32_t)H, place};
   const RowSplit w(a, {d, in, to}, kGradUnits);

@@ -59,7 +59,7 @@ def test_sort_workspace():
         (dict(out=A), ARG), (dict(gates=A + 2), ALIGN), (dict(y=A + 2), ALIGN)]),
     (V.vsf_expert_combine_grad, GRAD, [
         (dict(d_out=0), ARG), (dict(y=0), ARG), (dict(d_y=0), ARG), (dict(gates=0), ARG),
-        (dict(d_gates=0), ARG), (dict(d_y=A), ARG), (dict(d_y=2 * A + 2), ARG),
+        (dict(d_gates=0), ARG), (dict(d_gates=4 * A), ARG), (dict(d_gates=3 * A + 4), ARG), (dict(d_y=A), ARG), (dict(d_y=2 * A + 2), ARG),
         (dict(d_y=2 * A, d_y_ld=72), ARG), (dict(d_gates=A + 2), ALIGN), (dict(d_y=5 * A + 1), ALIGN)])])
 def test_row_refusals(call, args, extra):
     for change, want in extra + [

@@ -281,6 +281,50 @@ def test_starts_out_of_range():
     assert call.device_error() == 0
 
 
+def test_offsets_past_32_bits():
+    """Rows 2^20 elements apart, 2^31 and more from the first to the last."""
+    from fsdp_buffer_layout_gb300.experts import Dispatch, ExpertLinear
+    tokens, experts, k, width, ld = 1100, 5, 2, 72, 1 << 20
+    g = torch.Generator(device="cuda").manual_seed(2)
+
+    def far(rows):
+        x = torch.empty(rows * ld, dtype=BF16, device="cuda").as_strided((rows, width), (ld, 1))
+        return x.copy_(torch.randn(rows, width, device="cuda", generator=g))
+
+    idx = torch.randint(-1, experts, (tokens, k), device="cuda", generator=g).int()
+    gates = torch.rand(tokens, k, device="cuda", generator=g)
+    x, y = far(tokens), far(tokens * k)
+    near = [t.contiguous() for t in (x, y)]
+    calls = [Dispatch(tokens, experts, k, width) for _ in range(2)]
+    starts = [c.sort(idx)[0] for c in calls][0]
+    rows = far(tokens * k).zero_()
+    assert torch.equal(calls[0].gather(x, out=rows), calls[1].gather(near[0]))
+    assert torch.equal(calls[0].combine(y, gates), calls[1].combine(near[1], gates))
+    assert torch.equal(calls[0].gather_backward(y), calls[1].gather_backward(near[1]))
+    d_y = far(tokens * k).zero_()
+    a = calls[0].combine_backward(x, y, gates, d_y=d_y)
+    b = calls[1].combine_backward(near[0], near[1], gates)
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    del d_y, a, x
+    w = torch.randn(experts, 96, width, device="cuda", generator=g).bfloat16()
+    d = torch.randn(tokens * k, 96, device="cuda", generator=g).bfloat16()
+    layers = [ExpertLinear(tokens * k, experts, 96, width) for _ in range(2)]
+    assert torch.equal(layers[0].forward(y, w, starts), layers[1].forward(near[1], w, starts))
+    assert torch.equal(layers[0].backward_weight(d, y, starts), layers[1].backward_weight(d, near[1], starts))
+    rows.zero_()
+    assert torch.equal(layers[0].backward_input(d, w, starts, out=rows),
+                       layers[1].backward_input(d, w, starts))
+
+
+@pytest.mark.parametrize("experts,rows", [(512, 1), (512, 3), (300, 40)])
+def test_many_experts(experts, rows):
+    """As many as a launch may have, a row or some each, every third without one."""
+    from fsdp_buffer_layout_gb300.experts import ExpertLinear
+    counts = [0 if e % 3 == 1 else rows + e % 2 for e in range(experts)]
+    starts, x, w, d_y = product_inputs(counts, 0, 72, 40, 0)
+    check_products(ExpertLinear(x.shape[0], experts, 72, 40), starts, x, w, d_y)
+
+
 def test_products_on_streams_and_in_graphs():
     """Two objects at once on two streams, and a captured call replayed on new
     inputs, give the bits of calls one after the other."""

@@ -329,6 +329,15 @@ def test_calls_are_independent():
         assert all(torch.equal(p, q) for p, q in zip(out, b))
 
 
+def test_no_tokens():
+    from fsdp_buffer_layout_gb300.objectives import TokenScores
+    x, y = torch.zeros(0, 50, device="cuda", dtype=BF16), torch.zeros(0, dtype=torch.int64, device="cuda")
+    for op in (TokenScores(0, 50, top_k=2), TokenScores(3, 50, top_k=2)):
+        got = op.forward(x, y)
+        assert [tuple(t.shape) for t in got] == [(0,), (0,), (0, 2), (0, 2)]
+        assert op.backward(x, y).shape == (0, 50)
+
+
 def test_object_refuses():
     from fsdp_buffer_layout_gb300.objectives import TokenScores
     op = TokenScores(8, 100, top_k=2)
