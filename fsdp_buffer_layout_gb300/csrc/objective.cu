@@ -639,6 +639,26 @@ struct ScoreWs {
   }
 };
 
+// For a CTA a row, which has room for 32 pieces.
+template <typename T>
+ScoreCut score_cut_one(int64_t V) {
+  ScoreCut c = score_cut<T>(0, V);
+  while (((c.spans - 1) >> c.piece) + 1 > 32) ++c.piece;
+  c.pieces = ((c.spans - 1) >> c.piece) + 1;
+  return c;
+}
+
+// Whether a CTA does a row: up to two of them to an SM. A row's CTA reads some 70 GB/s,
+// so rows that are long beside their number are better shared out: as measured (L2 warm,
+// 5 alternatives, us here and in two launches), 1 row of 200 KB 6.5 / 6.7, 32 of 256 KB
+// 8.7 / 8.2, 64 of 256 KB 8.7 / 9.5, of 512 KB 12.9 / 13.2, 32 of 512 KB 12.9 / 9.5,
+// 300 of 512 KB 30 / 34. Above 1 MB the two are alike.
+template <typename T>
+bool one_score_launch(int64_t tokens, int64_t V) {
+  const int64_t bytes = V * (int64_t)sizeof(T);
+  return tokens <= 2 * kSms && bytes < 8192 * std::max<int64_t>(tokens, 25) && bytes <= int64_t(1) << 20;
+}
+
 unsigned score_grid(int64_t items, int ctas) {
   const int64_t warps = kScoreThreads / 32;
   return (unsigned)std::min<int64_t>((items + warps - 1) / warps, kSms * ctas);
@@ -655,11 +675,15 @@ cudaError_t scores(const RowsArg& a, int32_t K, float* logp, float* entropy, int
   k.head = reinterpret_cast<WsHead*>(b);
   k.part = reinterpret_cast<float4*>(b + sizeof(WsHead));
   k.keys = reinterpret_cast<uint32_t*>(b + sizeof(WsHead) + (size_t)a.T_ * k.cut.pieces * 16);
+  const bool one = one_score_launch<T>(a.T_, a.V);
+  if (one) k.cut = score_cut_one<T>(a.V);
   k.logp = logp;
   k.entropy = entropy;
   k.top_idx = top_idx;
   k.top_logp = top_logp;
   k.norm = reinterpret_cast<float4*>(norm);
+  if (one && a.T_ <= kSms) return launch_behind(score_one_kernel<T, 512>, (unsigned)a.T_, 512, 0, 1, st, k);
+  if (one) return launch_behind(score_one_kernel<T, 256>, (unsigned)a.T_, 256, 0, 1, st, k);
   const cudaError_t e = launch_behind(score_part_kernel<T>, score_grid(a.T_ * k.cut.pieces, kPartCtas),
                                       kScoreThreads, 0, 1, st, k);
   if (e != cudaSuccess) return e;

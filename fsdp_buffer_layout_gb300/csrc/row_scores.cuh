@@ -14,7 +14,7 @@
 // whose maxima are not below the k-th largest of all groups' maxima. A second launch, a
 // CTA a row, joins the pieces and ranks the elements of those groups (k times 512 bytes
 // or little more, unless maxima are equal); where equal ones are too many, it goes
-// through the whole row.
+// through the whole row. Few rows take one launch for both, a CTA a row.
 //
 // m is a reference for the exponents, not the maximum: the largest of a lane's first
 // vectors, moved only where an element lies 16 units of ln 2 above it. A sum's terms
@@ -157,21 +157,131 @@ struct ScoreSums {
   }
 };
 
-// {m, s, u} of a piece and its lanes' keys; a warp a piece. Two batches of loads are
-// on their way at a time, the first of the next piece while this one is finished. (A
-// ring of bulk copies for each warp, across pieces, took 14 instructions an element
-// instead of 9 and 227 us instead of 188 for 4096 x 131072 bf16, 3/4 live, with 20
-// alternatives.)
+// What the sums of a launch's rows have in common.
+struct ScoreLane {
+  F2 cc;  // this thread's factor, rounded down or up (Log2Scale)
+  float units;
+  bool far;
+  __device__ __forceinline__ ScoreLane(const Log2Scale& c, float inv_t)
+      : units(200.f / c.hi), far(far_temperature(inv_t)) {
+    const float c1 = (uint32_t)threadIdx.x * 2654435769u < c.ups ? c.up : c.hi;
+    cc = f2(c1, c1);
+  }
+};
+
+// A piece of a row, and where its vectors lie.
+template <typename T>
+struct Piece {
+  const uint4* in = nullptr;  // the row's first vector, and this lane's offset
+  int64_t t = -1;
+  int32_t p = 0, head = 0, v = 0, v1 = 0;
+  __device__ __forceinline__ bool whole(bool far) const { return !far && v + 32 * kScoreBatch <= v1; }
+  __device__ __forceinline__ void load(uint4 (&q)[kScoreBatch], int32_t at) const {
+#pragma unroll
+    for (int j = 0; j < kScoreBatch; ++j) q[j] = __ldcs(in + at + 32 * j);
+  }
+  // with its first vectors on their way
+  __device__ __forceinline__ void open(const ScoreArgs<T>& a, bool far, uint4 (&q)[kScoreBatch]) {
+    const T* x = a.r.x + t * a.r.ld;
+    const Span s = span_of(x, a.r.V);
+    in = reinterpret_cast<const uint4*>(x + s.head) + (threadIdx.x & 31);
+    head = s.head;
+    v = (p << a.cut.piece) * 32;
+    v1 = min(v + (32 << a.cut.piece), s.nvec);
+    if (whole(far)) load(q, v);
+  }
+};
+
+// {m, s, u} of a piece whose first vectors q0 holds; one warp. Two batches of loads are
+// on their way at a time; ahead(key), with this lane's key, is called when the last
+// of them have been added, and may open the next piece in their place.
+template <typename T, typename Ahead>
+__device__ __forceinline__ float4 piece_sums(const ScoreArgs<T>& a, const ScoreLane& c, Piece<T>& piece,
+                                             uint4 (&q0)[kScoreBatch], Ahead ahead) {
+  constexpr int VE = Vec<T>::n, B = kScoreBatch;
+  const Rows<T>& r = a.r;
+  const int lane = threadIdx.x & 31;
+  const int64_t t0 = piece.t;
+  const int32_t p0 = piece.p, v0 = piece.v;
+  int32_t& v = piece.v;
+  const int32_t& v1 = piece.v1;
+  ScoreSums<T> sums(c.units);
+  float top = -INFINITY;
+  if (piece.whole(c.far)) {
+    // whole batches, by turns in two sets of registers
+    uint4 q1[B];
+    auto add = [&](const uint4 (&q)[B]) -> bool {
+      const float bm = largest(q, T());
+      top = fmaxf(top, bm);
+      sums.to(bm, r.c, c.units);
+      if (__any_sync(~0u, sums.out_of_range())) return false;
+#pragma unroll
+      for (int j = 0; j < B; ++j) sums.template add<false>(q[j], c.cc);
+      v += 32 * B;
+      return true;
+    };
+    while (true) {
+      const bool more1 = v + 64 * B <= v1;
+      if (more1) piece.load(q1, v + 32 * B);
+      if (!add(q0) || !more1) break;
+      const bool more0 = v + 64 * B <= v1;
+      if (more0) piece.load(q0, v + 32 * B);
+      if (!add(q1) || !more0) break;
+    }
+  }
+#pragma unroll 1
+  for (; v < v1; v += 32) {  // less than a batch, or what is out of range
+    uint4 q[1] = {make_uint4(Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest)};
+    if (v + lane < v1) q[0] = __ldcs(piece.in + v);
+    const float bm = largest(q, T());
+    top = fmaxf(top, bm);
+    sums.to(bm, r.c, c.units);
+    sums.template add<true>(q[0], c.cc);
+  }
+  const int32_t head0 = piece.head;
+  ahead(v0 + lane < v1 ? order_key(top) : 0u);
+  if (p0 == 0 || p0 + 1 == a.cut.pieces) {
+    // the loose elements, in front of the vectors and behind them
+    const T* x = r.x + t0 * r.ld;
+    const int32_t tail = head0 + (r.V - head0) / VE * VE;
+    int32_t loose = -1;
+    if (p0 == 0 && lane < head0) loose = lane;
+    if (p0 + 1 == a.cut.pieces && lane >= 16 && lane - 16 < r.V - tail) loose = tail + (lane - 16);
+    if (loose >= 0) {
+      const float xl = to_f(x[loose]);
+      sums.to(xl, r.c, c.units);
+      const PairScale c2 = {f2(r.c.hi, r.c.hi), f2(r.c.lo, r.c.lo)};
+      const float z = -finite_max(sums.m);
+      F2 zz, ee;
+      score_terms(f2(xl, -INFINITY), f2(z, z), c2, zz, ee);
+      sums.sum0 = f2_add(sums.sum0, ee);
+      sums.zum0 = f2_fma(zz, ee, sums.zum0);
+    }
+  }
+  // the lanes' join, by expf (see the join of the losses' sums)
+  float s0, s1, s2, s3, u0, u1, u2, u3;
+  f2_get(sums.sum0, s0, s1);
+  f2_get(sums.sum1, s2, s3);
+  f2_get(sums.zum0, u0, u1);
+  f2_get(sums.zum1, u2, u3);
+  const float m = warp_max(sums.m), d = sums.m - finite_max(m), f = expf(d * r.inv_tf);
+  const float own = (s0 + s1) + (s2 + s3);
+  const float shift = fmaxf(__fmaf_rn(d, r.c.hi, d * r.c.lo), -1e20f);
+  const float sum = warp_sum(own == 0.f ? 0.f : f * own);
+  const float zum = warp_sum(own == 0.f ? 0.f : f * __fmaf_rn(own, shift, (u0 + u1) + (u2 + u3)));
+  return make_float4(m, sum, zum, 0.f);
+}
+
+// The pieces of many rows; a warp a piece, the first vectors of the next one on their
+// way while one is finished. (A ring of bulk copies for each warp, across pieces, took
+// 14 instructions an element instead of 9 and 227 us instead of 188 for 4096 x 131072
+// bf16, 3/4 live, with 20 alternatives.)
 template <typename T>
 __global__ void __launch_bounds__(kScoreThreads, kPartCtas)
     score_part_kernel(const __grid_constant__ ScoreArgs<T> a) {
-  constexpr int VE = Vec<T>::n, B = kScoreBatch;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Rows<T>& r = a.r;
-  const float c1 = (uint32_t)threadIdx.x * 2654435769u < r.c.ups ? r.c.up : r.c.hi;
-  const F2 cc = f2(c1, c1);
-  const bool far = far_temperature(r.inv_tf);
-  const float units = 200.f / r.c.hi;
+  const ScoreLane c(r.c, r.inv_tf);
   take_turn();
   const int32_t pieces = a.cut.pieces, step = (int32_t)gridDim.x * (kScoreThreads / 32);
   const int32_t step_t = step / pieces, step_p = step % pieces;
@@ -180,13 +290,13 @@ __global__ void __launch_bounds__(kScoreThreads, kPartCtas)
   int64_t t_next = first / pieces;
   int32_t p_next = first % pieces;
   int64_t y_next = t_next < r.T_ ? r.target[t_next] : -1;
-  int64_t t = -1;
-  int32_t p = 0;
+  Piece<T> piece;
+  uint4 q0[kScoreBatch];
   // to the next piece of a live row; those of masked rows are left out
   auto find = [&]() {
     while (t_next < r.T_) {
-      t = t_next;
-      p = p_next;
+      piece.t = t_next;
+      piece.p = p_next;
       const int64_t y = y_next;
       t_next += step_t;
       p_next += step_p;
@@ -196,98 +306,21 @@ __global__ void __launch_bounds__(kScoreThreads, kPartCtas)
       }
       y_next = t_next < r.T_ ? r.target[t_next] : -1;
       if (y >= 0 && y < r.V) return;
-      if (y >= 0 && p == 0 && lane == 0) atomicOr(&a.head->err, kErrTarget);
+      if (y >= 0 && piece.p == 0 && lane == 0) atomicOr(&a.head->err, kErrTarget);
     }
-    t = -1;
-  };
-  uint4 q0[B], q1[B];
-  const uint4* in = nullptr;
-  int32_t v = 0, v1 = 0, head = 0;
-  auto load = [&](uint4 (&q)[B], int32_t at) {
-#pragma unroll
-    for (int j = 0; j < B; ++j) q[j] = __ldcs(in + at + 32 * j);
-  };
-  auto open = [&]() {  // the piece's vectors, the first of them on their way
-    if (t < 0) return;
-    const T* x = r.x + t * r.ld;
-    const Span s = span_of(x, r.V);
-    in = reinterpret_cast<const uint4*>(x + s.head) + lane;
-    head = s.head;
-    v = (p << a.cut.piece) * 32;
-    v1 = min(v + (32 << a.cut.piece), s.nvec);
-    if (!far && v + 32 * B <= v1) load(q0, v);
+    piece.t = -1;
   };
   find();
-  open();
-  while (t >= 0) {
-    const int64_t t0 = t;
-    const int32_t p0 = p, v0 = v;
-    ScoreSums<T> sums(units);
-    float top = -INFINITY;
-    if (!far && v + 32 * B <= v1) {
-      // whole batches, by turns in two sets of registers
-      auto add = [&](const uint4 (&q)[B]) -> bool {
-        const float bm = largest(q, T());
-        top = fmaxf(top, bm);
-        sums.to(bm, r.c, units);
-        if (__any_sync(~0u, sums.out_of_range())) return false;
-#pragma unroll
-        for (int j = 0; j < B; ++j) sums.template add<false>(q[j], cc);
-        v += 32 * B;
-        return true;
-      };
-      while (true) {
-        const bool more1 = v + 64 * B <= v1;
-        if (more1) load(q1, v + 32 * B);
-        if (!add(q0) || !more1) break;
-        const bool more0 = v + 64 * B <= v1;
-        if (more0) load(q0, v + 32 * B);
-        if (!add(q1) || !more0) break;
-      }
-    }
-#pragma unroll 1
-    for (; v < v1; v += 32) {  // less than a batch, or what is out of range
-      uint4 q[1] = {make_uint4(Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest, Vec<T>::lowest)};
-      if (v + lane < v1) q[0] = __ldcs(in + v);
-      const float bm = largest(q, T());
-      top = fmaxf(top, bm);
-      sums.to(bm, r.c, units);
-      sums.template add<true>(q[0], cc);
-    }
-    if (a.K > 0) a.keys[(t0 * pieces + p0) * 32 + lane] = v0 + lane < v1 ? order_key(top) : 0;
-    const int32_t head0 = head;
-    find();
-    open();
-    if (p0 == 0 || p0 + 1 == pieces) {
-      // the loose elements, in front of the vectors and behind them
-      const T* x = r.x + t0 * r.ld;
-      const int32_t tail = head0 + (r.V - head0) / VE * VE;
-      int32_t loose = -1;
-      if (p0 == 0 && lane < head0) loose = lane;
-      if (p0 + 1 == pieces && lane >= 16 && lane - 16 < r.V - tail) loose = tail + (lane - 16);
-      if (loose >= 0) {
-        const float xl = to_f(x[loose]);
-        sums.to(xl, r.c, units);
-        const PairScale c2 = {f2(r.c.hi, r.c.hi), f2(r.c.lo, r.c.lo)};
-        const float z = -finite_max(sums.m);
-        F2 zz, ee;
-        score_terms(f2(xl, -INFINITY), f2(z, z), c2, zz, ee);
-        sums.sum0 = f2_add(sums.sum0, ee);
-        sums.zum0 = f2_fma(zz, ee, sums.zum0);
-      }
-    }
-    // the lanes' join, by expf (see the join of the losses' sums)
-    float s0, s1, s2, s3, u0, u1, u2, u3;
-    f2_get(sums.sum0, s0, s1);
-    f2_get(sums.sum1, s2, s3);
-    f2_get(sums.zum0, u0, u1);
-    f2_get(sums.zum1, u2, u3);
-    const float m = warp_max(sums.m), d = sums.m - finite_max(m), f = expf(d * r.inv_tf);
-    const float own = (s0 + s1) + (s2 + s3);
-    const float shift = fmaxf(__fmaf_rn(d, r.c.hi, d * r.c.lo), -1e20f);
-    const float sum = warp_sum(own == 0.f ? 0.f : f * own);
-    const float zum = warp_sum(own == 0.f ? 0.f : f * __fmaf_rn(own, shift, (u0 + u1) + (u2 + u3)));
-    if (lane == 0) a.part[t0 * pieces + p0] = make_float4(m, sum, zum, 0.f);
+  if (piece.t >= 0) piece.open(a, c.far, q0);
+  while (piece.t >= 0) {
+    const int64_t t0 = piece.t;
+    const int32_t p0 = piece.p;
+    const float4 part = piece_sums(a, c, piece, q0, [&](uint32_t key) {
+      if (a.K > 0) a.keys[(t0 * pieces + p0) * 32 + lane] = key;
+      find();
+      if (piece.t >= 0) piece.open(a, c.far, q0);
+    });
+    if (lane == 0) a.part[t0 * pieces + p0] = part;
   }
 }
 
@@ -382,49 +415,43 @@ __device__ __forceinline__ uint64_t entry(uint32_t key, int32_t idx) {
   return (uint64_t)key << 32 | (uint32_t)~idx;
 }
 
-// Joins a row's pieces and picks its alternatives; a CTA a row: what a call of 64 rows
-// of 131072 takes longer with 20 alternatives than without is 3.5 us, with a warp a
-// row it was 18, a chain of some ten loads. N: keys of a thread, 8 for up to 32 pieces.
-constexpr int kRowScoreThreads = 128;
+constexpr int kRowScoreThreads = 128;  // of the row's finish
 constexpr int kScoreCandidates = 128;  // groups, and elements, that are ranked
-template <typename T, int N>
-__global__ void __launch_bounds__(kRowScoreThreads, N == 8 ? 12 : 4)
-    score_row_kernel(const __grid_constant__ ScoreArgs<T> a) {
-  constexpr int VE = Vec<T>::n, C = kScoreCandidates, W = kRowScoreThreads / 32;
-  static_assert(C == kRowScoreThreads, "a thread ranks an entry");
+struct RowShared {
   // key and, inverted, index: the larger number is in front
-  __shared__ uint64_t groups[C], sorted[C], elements[C];
-  __shared__ uint32_t least_of[W], last_of;
-  __shared__ int32_t n_groups, n_elements;
-  __shared__ float row_m, row_sum;
+  uint64_t groups[kScoreCandidates], sorted[kScoreCandidates], elements[kScoreCandidates];
+  uint32_t least_of[32], last_of;
+  int32_t n_groups, n_elements;
+  float m, sum;
+};
+
+template <typename T>
+__device__ __forceinline__ void masked_row(const ScoreArgs<T>& a, int64_t t) {
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    a.logp[t] = 0.f;
+    a.entropy[t] = 0.f;
+    a.norm[t] = make_float4(0.f, 1.f, 0.f, 0.f);
+  }
+  if (tid < a.K) {
+    a.top_idx[t * a.K + tid] = -1;
+    a.top_logp[t * a.K + tid] = 0.f;
+  }
+}
+
+// Joins the pieces of row t, whose target is y, and picks its alternatives; a CTA of
+// kRowScoreThreads. key: N of the row's keys each (key j * kRowScoreThreads + tid), part: the first warp's
+// first pieces, parts: all of them.
+template <int N, typename T>
+__device__ __forceinline__ void finish_row(const ScoreArgs<T>& a, int64_t t, int32_t y, const uint32_t (&key)[N],
+                                           float4 part, const float4* parts, RowShared& sh) {
+  constexpr int VE = Vec<T>::n, C = kScoreCandidates, NT = kRowScoreThreads, W = NT / 32;
+  static_assert(C == NT, "a thread ranks an entry");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Rows<T>& r = a.r;
-  take_turn();
-  if (blockIdx.x == 0 && tid == 0) a.head->rows = 1;
-  const int64_t t = blockIdx.x;
-  // ---- the groups' keys and the pieces, on their way before the row is known to be live
-  const int32_t n_keys = a.K > 0 ? a.cut.pieces * 32 : 0;
-  const uint32_t* keys = a.keys + t * n_keys;
-  uint32_t key[N], best = 0;
-#pragma unroll
-  for (int j = 0; j < N; ++j) key[j] = j * kRowScoreThreads + tid < n_keys ? keys[j * kRowScoreThreads + tid] : 0;
-  float4 part = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-  if (warp == 0 && lane < a.cut.pieces) part = a.part[t * a.cut.pieces + lane];
-  const int32_t y = live_target(r, t, nullptr);
-  if (y < 0) {
-    if (tid == 0) {
-      a.logp[t] = 0.f;
-      a.entropy[t] = 0.f;
-      a.norm[t] = make_float4(0.f, 1.f, 0.f, 0.f);
-    }
-    if (tid < a.K) {
-      a.top_idx[t * a.K + tid] = -1;
-      a.top_logp[t * a.K + tid] = 0.f;
-    }
-    return;
-  }
+  uint32_t best = 0;
   const T* x = r.x + t * r.ld;
-  if (tid == 0) n_groups = n_elements = 0;
+  if (tid == 0) sh.n_groups = sh.n_elements = 0;
   // ---- the pieces, by the first warp
   if (warp == 0) {
     const float xy = lane == 0 ? to_f(x[y]) : 0.f;
@@ -434,7 +461,7 @@ __global__ void __launch_bounds__(kRowScoreThreads, N == 8 ? 12 : 4)
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       q[j] = j == 0 ? part : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-      if (j > 0 && 32 * j + lane < a.cut.pieces) q[j] = a.part[t * a.cut.pieces + 32 * j + lane];
+      if (j > 0 && 32 * j + lane < a.cut.pieces) q[j] = parts[32 * j + lane];
       m = fmaxf(m, q[j].x);
     }
     m = warp_max(m);
@@ -455,8 +482,8 @@ __global__ void __launch_bounds__(kRowScoreThreads, N == 8 ? 12 : 4)
       a.logp[t] = log_ratio(xy - m, r.inv_tf, 0.f, ls);
       a.entropy[t] = __fmaf_rn(ls.k, 0.693359375f, __fmaf_rn(ls.k, -2.12194440e-4f, ls.f) - mean);
       a.norm[t] = make_float4(m, sum, mean, 0.f);
-      row_m = m;
-      row_sum = sum;
+      sh.m = m;
+      sh.sum = sum;
     }
   }
   if (a.K == 0) return;
@@ -469,9 +496,9 @@ __global__ void __launch_bounds__(kRowScoreThreads, N == 8 ? 12 : 4)
     least = warp_max(best);
     if (lane == __ffs(__ballot_sync(~0u, best == least)) - 1) best = 0;
   }
-  if (lane == 0) least_of[warp] = least;
+  if (lane == 0) sh.least_of[warp] = least;
   __syncthreads();
-  const float m = row_m, sum = row_sum;
+  const float m = sh.m, sum = sh.sum;
   if (!(sum > 0.f && sum < INFINITY)) {  // a NaN, a +inf or only -inf
     if (tid < a.K) {
       a.top_idx[t * a.K + tid] = -1;
@@ -479,7 +506,7 @@ __global__ void __launch_bounds__(kRowScoreThreads, N == 8 ? 12 : 4)
     }
     return;
   }
-  for (int w = 0; w < W; ++w) least = min(least, least_of[w]);
+  for (int w = 0; w < W; ++w) least = min(least, sh.least_of[w]);
   least = max(least, 1u);
   int mine = 0;
 #pragma unroll
@@ -491,12 +518,12 @@ __global__ void __launch_bounds__(kRowScoreThreads, N == 8 ? 12 : 4)
     if (lane >= o) to += v;
   }
   int first = 0;
-  if (lane == 31) first = atomicAdd(&n_groups, to);
+  if (lane == 31) first = atomicAdd(&sh.n_groups, to);
   to += __shfl_sync(~0u, first, 31) - mine;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     if (key[j] < least) continue;
-    if (to < C) groups[to] = entry(key[j], j * kRowScoreThreads + tid);
+    if (to < C) sh.groups[to] = entry(key[j], j * NT + tid);
     ++to;
   }
   __syncthreads();
@@ -512,25 +539,25 @@ __global__ void __launch_bounds__(kRowScoreThreads, N == 8 ? 12 : 4)
     a.top_idx[t * a.K + at] = (int32_t)~(uint32_t)own;
     a.top_logp[t * a.K + at] = log_ratio(key_value((uint32_t)(own >> 32)) - m, r.inv_tf, 0.f, log_sum(sum));
   };
-  const int ng = n_groups;
+  const int ng = sh.n_groups;
   if (ng <= C) {
-    if (tid == 0 && ng < a.K) last_of = 0;
+    if (tid == 0 && ng < a.K) sh.last_of = 0;
     if (tid < ng) {
-      const uint64_t own = groups[tid];
-      const int at = place(groups, ng, own);
-      sorted[at] = own;
-      if (at == a.K - 1) last_of = (uint32_t)(own >> 32);
+      const uint64_t own = sh.groups[tid];
+      const int at = place(sh.groups, ng, own);
+      sh.sorted[at] = own;
+      if (at == a.K - 1) sh.last_of = (uint32_t)(own >> 32);
     }
     __syncthreads();
     // ---- their elements that are not below the K-th group's maximum, and the loose ones
-    const uint32_t last = last_of;
-    const int kept = __syncthreads_count(tid < ng && (uint32_t)(sorted[tid] >> 32) >= last);
+    const uint32_t last = sh.last_of;
+    const int kept = __syncthreads_count(tid < ng && (uint32_t)(sh.sorted[tid] >> 32) >= last);
     const float low = last == 0 ? -INFINITY : key_value(last);
     const Span s = span_of(x, r.V);
     const int32_t tail = s.head + s.nvec * VE;
     auto gather = [&](float v, int32_t idx) {
-      const int to = atomicAdd(&n_elements, 1);
-      if (to < C) elements[to] = entry(order_key(v), idx);
+      const int to = atomicAdd(&sh.n_elements, 1);
+      if (to < C) sh.elements[to] = entry(order_key(v), idx);
     };
     if (tid < s.head && to_f(x[tid]) >= low) gather(to_f(x[tid]), tid);
     if (tid < r.V - tail && to_f(x[tail + tid]) >= low) gather(to_f(x[tail + tid]), tail + tid);
@@ -538,15 +565,15 @@ __global__ void __launch_bounds__(kRowScoreThreads, N == 8 ? 12 : 4)
     const int log = a.cut.piece;  // a group has 2^log vectors
     const int64_t n_vecs = (int64_t)kept << log;
     constexpr int B = 4;
-    for (int64_t i0 = tid; i0 < n_vecs; i0 += kRowScoreThreads * B) {
+    for (int64_t i0 = tid; i0 < n_vecs; i0 += NT * B) {
       uint4 q[B];
       int32_t at[B];
 #pragma unroll
       for (int j = 0; j < B; ++j) {
-        const int64_t i = i0 + kRowScoreThreads * j;
+        const int64_t i = i0 + NT * j;
         at[j] = -1;
         if (i >= n_vecs) continue;
-        const int32_t g = (int32_t)~(uint32_t)sorted[i >> log];
+        const int32_t g = (int32_t)~(uint32_t)sh.sorted[i >> log];
         const int32_t v = ((((g >> 5) << log) + (int32_t)(i & ((1 << log) - 1))) << 5) + (g & 31);
         if (v >= s.nvec) continue;
         at[j] = v;
@@ -572,9 +599,9 @@ __global__ void __launch_bounds__(kRowScoreThreads, N == 8 ? 12 : 4)
       }
     }
     __syncthreads();
-    const int n = n_elements;
+    const int n = sh.n_elements;
     if (n <= C) {
-      if (tid < n) put(place(elements, n, elements[tid]), elements[tid]);
+      if (tid < n) put(place(sh.elements, n, sh.elements[tid]), sh.elements[tid]);
       return;
     }
     __syncthreads();  // (n_elements and the lists have been read)
@@ -582,9 +609,78 @@ __global__ void __launch_bounds__(kRowScoreThreads, N == 8 ? 12 : 4)
   // ---- too many equal ones: the whole row, a part a warp
   static_assert(W * kMaxTop <= C, "the warps' lists are ranked together");
   const Best own = best_of_part(x, r.V, a.K, warp, W, lane);
-  if (lane < a.K) elements[warp * a.K + lane] = entry(own.key, own.idx);
+  if (lane < a.K) sh.elements[warp * a.K + lane] = entry(own.key, own.idx);
   __syncthreads();
-  if (tid < W * a.K && elements[tid] >> 32 != 0) put(place(elements, W * a.K, elements[tid]), elements[tid]);
+  if (tid < W * a.K && sh.elements[tid] >> 32 != 0)
+    put(place(sh.elements, W * a.K, sh.elements[tid]), sh.elements[tid]);
+}
+
+// Finishes the rows whose pieces score_part_kernel has left, a CTA a row: what a call of
+// 64 rows of 131072 takes longer with 20 alternatives than without is 3.5 us, with a
+// warp a row it was 18, a chain of some ten loads. N: keys of a thread, 8 for up to 32
+// pieces.
+template <typename T, int N>
+__global__ void __launch_bounds__(kRowScoreThreads, N == 8 ? 12 : 4)
+    score_row_kernel(const __grid_constant__ ScoreArgs<T> a) {
+  __shared__ RowShared sh;
+  const int tid = threadIdx.x;
+  const int64_t t = blockIdx.x;
+  take_turn();
+  if (t == 0 && tid == 0) a.head->rows = 1;
+  // the groups' keys and the pieces are on their way before the row is known to be live
+  const int32_t n_keys = a.K > 0 ? a.cut.pieces * 32 : 0;
+  const uint32_t* keys = a.keys + t * n_keys;
+  const float4* parts = a.part + t * a.cut.pieces;
+  uint32_t key[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) key[j] = j * kRowScoreThreads + tid < n_keys ? keys[j * kRowScoreThreads + tid] : 0;
+  float4 part = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+  if (tid < 32 && tid < a.cut.pieces) part = parts[tid];
+  const int32_t y = live_target(a.r, t, nullptr);
+  if (y < 0)
+    masked_row(a, t);
+  else
+    finish_row<N>(a, t, y, key, part, parts, sh);
+}
+
+// Few rows: a CTA does all of a row, its pieces' sums and keys in shared memory, in one
+// launch instead of two: 5.5 us instead of 6.0 for 8 rows of 32000 bf16 with 5
+// alternatives, 8.9 instead of 14.1 for 152 of 131072. NT: 512 threads for up to a row
+// an SM, 256 for two. (All the SMs' registers, so that rows do not wait: with three or
+// more to an SM the other way is faster, 15.8 us instead of 21 for 777 of 32000.)
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT, 512 / NT) score_one_kernel(const __grid_constant__ ScoreArgs<T> a) {
+  __shared__ RowShared sh;
+  __shared__ float4 parts[32];  // (at most 32 pieces)
+  __shared__ uint32_t keys[1024];
+  constexpr int N = 1024 / kRowScoreThreads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t t = blockIdx.x;
+  const ScoreLane c(a.r.c, a.r.inv_tf);
+  take_turn();
+  if (t == 0 && tid == 0) a.head->rows = 1;
+  const int32_t y = live_target(a.r, t, tid == 0 ? &a.head->err : nullptr);
+  if (y < 0) {
+    masked_row(a, t);
+    return;
+  }
+  for (int32_t p = warp; p < a.cut.pieces; p += NT / 32) {
+    Piece<T> piece;
+    uint4 q0[kScoreBatch];
+    piece.t = t;
+    piece.p = p;
+    piece.open(a, c.far, q0);
+    const float4 part = piece_sums(a, c, piece, q0, [&](uint32_t key) { keys[p * 32 + lane] = key; });
+    if (lane == 0) parts[p] = part;
+  }
+  __syncthreads();
+  if (tid >= kRowScoreThreads) return;  // (a barrier waits for the threads that are left)
+  uint32_t key[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    key[j] = j * kRowScoreThreads + tid < a.cut.pieces * 32 ? keys[j * kRowScoreThreads + tid] : 0;
+  const float4 part = tid < 32 && tid < a.cut.pieces ? parts[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+  finish_row<N>(a, t, y, key, part, parts, sh);
 }
 
 // ------------------------------------------------------------- the gradient

@@ -248,6 +248,39 @@ def test_temperatures_at_the_ends_of_their_range(vocab, inv_t):
         assert (np.abs(host(out) - want) <= (2.0**-7) * np.abs(want) + 2.0**-18 * t32 * pulls[0][0]).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("tokens,vocab", [(120, 70003), (220, 5000), (220, 300), (400, 5000), (400, 70003), (3, 150001)])
+@pytest.mark.parametrize("inv_t,k", [(1.0, 8), (1e30, 3), (1.0, 32)])
+def test_edge_rows_in_calls_of_any_size(tokens, vocab, dtype, inv_t, k):
+    """Ties, masked words and rows that give NaN, some of each left out, however a
+    call's rows are shared out."""
+    from fsdp_buffer_layout_gb300.objectives import TokenScores
+    rng = np.random.default_rng(vocab)
+    low, n = torch.finfo(dtype).min, np.arange(vocab)
+    v = np.stack([np.zeros(vocab), rng.integers(0, 3, vocab), n[::-1] // 99, np.where(n % 250 == 249, 4.0, -np.inf),
+                  np.where(n < 5, 2.0, -np.inf), np.where(n < 5, 2.0, low), np.where(n == vocab - 1, -1.0, -np.inf),
+                  np.full(vocab, low), n % 128 * 0.5, n // 300 % 4 * 0.25, np.full(vocab, -np.inf)])
+    sound = len(v) - 1
+    which = np.arange(tokens) % len(v)
+    x, y = strided(v[which], dtype, pad=1, shift=2), np.where(which == 6, vocab - 1, np.where(which == 3, 249, 2))
+    y[which == 7] = np.where(np.arange(tokens)[which == 7] % 2, -1, 2)
+    op = TokenScores(tokens, vocab, top_k=k, dtype=dtype, inv_temperature=inv_t)
+    got = op.forward(x, dev(y, torch.int64))
+    assert op.device_error() == 0
+    inv_t = float(np.float32(inv_t))
+    for i in {0, tokens // len(v) // 2 * len(v), (tokens - 1) // len(v) * len(v)}:
+        rows = slice(i, min(i + sound, tokens))
+        check(x[rows], y[rows], inv_t, k, [o[rows] for o in got])
+    same = torch.from_numpy(which + len(v) * (y < 0))
+    for w in same.unique():
+        idx = got[2].cpu()[same == w]
+        assert (idx == idx[0]).all()
+    nan = torch.from_numpy(which == sound).cuda()
+    for o in (got[0], got[1], got[3]):
+        assert torch.isnan(o[nan]).all() and not torch.isnan(o[~nan]).any()
+    assert (got[2][nan] == -1).all()
+
+
 def test_targets_and_words_out_of_range():
     """A target >= V is left out and reported; words out of range, and a word
     twice, in what backward is given."""
