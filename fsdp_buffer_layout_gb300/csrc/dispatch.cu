@@ -460,7 +460,7 @@ vsf_status check_rows(const RowsArg& a, std::initializer_list<Strided> in) {
   if (!sizes_ok(a.T_, a.K) || a.H < 1 || a.H > kMaxWidth)
     return fail(VSF_ERR_ARG, w + ": sizes out of range");
   for (const Strided& s : in) {
-    if (s.ld < a.H || s.ld > (int64_t(1) << 40)) return fail(VSF_ERR_ARG, w + ": stride out of range");
+    if (s.ld < a.H || !offsets_ok(s.n, s.ld)) return fail(VSF_ERR_ARG, w + ": stride out of range");
     if (a.T_ > 0 && s.p == nullptr) return fail(VSF_ERR_ARG, w + ": NULL pointer");
     if (!aligned(s.p, a.dtype == VSF_BF16 ? 2 : 4)) return fail(VSF_ERR_ALIGN, w + ": pointer alignment");
   }
@@ -469,11 +469,17 @@ vsf_status check_rows(const RowsArg& a, std::initializer_list<Strided> in) {
   return VSF_OK;
 }
 
-bool overlap(const RowsArg& a, const Strided& x, const Strided& y) {
-  if (x.n == 0 || y.n == 0) return false;
+Area area(const RowsArg& a, const Strided& s) {
   const int64_t size = a.dtype == VSF_BF16 ? 2 : 4;
-  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x.p), y0 = reinterpret_cast<uintptr_t>(y.p);
-  return x0 < y0 + ((y.n - 1) * y.ld + a.H) * size && y0 < x0 + ((x.n - 1) * x.ld + a.H) * size;
+  return {s.p, s.n, s.ld * size, a.H * size};
+}
+// A value a choice.
+Area per_choice(const RowsArg& a, const void* p) {
+  const int64_t bytes = a.T_ * a.K * 4;
+  return {p, p != nullptr, bytes, bytes};
+}
+bool meets_any(const Area& out, std::initializer_list<Area> in) {
+  return std::any_of(in.begin(), in.end(), [&](const Area& x) { return meet(out, x); });
 }
 
 bool all_wide(const RowsArg& a, std::initializer_list<Strided> in) {
@@ -587,7 +593,8 @@ vsf_status vsf_expert_gather(const void* x, int32_t dtype, int64_t T, int64_t H,
   const Strided in = {x, T, ld}, out = {rows, T * top_k, rows_ld};
   const vsf_status s = check_rows(a, {in, out});
   if (s != VSF_OK) return s;
-  if (overlap(a, in, out)) return fail(VSF_ERR_ARG, "vsf_expert_gather: rows overlap the tokens");
+  if (meets_any(area(a, out), {area(a, in), per_choice(a, place)}))
+    return fail(VSF_ERR_ARG, "vsf_expert_gather: the output overlaps an input");
   if (T == 0) return VSF_OK;
   const RowIn p = {T, T * top_k, ld, rows_ld, (int32_t)top_k, (int32_t)H, place};
   const RowSplit w(a, {in, out}, kGatherUnits);
@@ -606,7 +613,8 @@ vsf_status vsf_expert_combine(const void* y, int32_t dtype, int64_t T, int64_t H
   const vsf_status s = check_rows(a, {in, to});
   if (s != VSF_OK) return s;
   if (!aligned(gates, 4)) return fail(VSF_ERR_ALIGN, "vsf_expert_combine: pointer alignment");
-  if (overlap(a, in, to)) return fail(VSF_ERR_ARG, "vsf_expert_combine: rows overlap the tokens");
+  if (meets_any(area(a, to), {area(a, in), per_choice(a, place), per_choice(a, gates)}))
+    return fail(VSF_ERR_ARG, "vsf_expert_combine: the output overlaps an input");
   if (T == 0) return VSF_OK;
   const RowIn p = {T, T * top_k, out_ld, y_ld, (int32_t)top_k, (int32_t)H, place};
   const RowSplit w(a, {in, to}, kCombineUnits);
@@ -629,12 +637,12 @@ vsf_status vsf_expert_combine_grad(const void* d_out, int32_t dtype, int64_t T, 
     return fail(VSF_ERR_ARG, "vsf_expert_combine_grad: NULL pointer");
   if (!aligned(gates, 4) || !aligned(d_gates, 4))
     return fail(VSF_ERR_ALIGN, "vsf_expert_combine_grad: pointer alignment");
-  if (overlap(a, d, to) || (overlap(a, in, to) && !(y == d_y && y_ld == d_y_ld)))
-    return fail(VSF_ERR_ARG, "vsf_expert_combine_grad: d_y overlaps an input in part");
-  const uintptr_t n = (uintptr_t)(T * top_k) * 4, g0 = reinterpret_cast<uintptr_t>(d_gates);
-  for (const void* p : {static_cast<const void*>(gates), static_cast<const void*>(place)})
-    if (g0 < reinterpret_cast<uintptr_t>(p) + n && reinterpret_cast<uintptr_t>(p) < g0 + n)
-      return fail(VSF_ERR_ARG, "vsf_expert_combine_grad: d_gates overlaps an input");
+  const Area from = per_choice(a, place), by = per_choice(a, gates), dg = per_choice(a, d_gates);
+  if (meets_any(area(a, to), {area(a, d), from, by, dg}) ||
+      (meet(area(a, to), area(a, in)) && !(y == d_y && y_ld == d_y_ld)))
+    return fail(VSF_ERR_ARG, "vsf_expert_combine_grad: d_y overlaps another array (y in part)");
+  if (meets_any(dg, {area(a, d), area(a, in), from, by}))
+    return fail(VSF_ERR_ARG, "vsf_expert_combine_grad: d_gates overlaps an input");
   if (T == 0) return VSF_OK;
   const RowIn p = {T, T * top_k, d_out_ld, d_y_ld, (int32_t)top_k, (int32_t)H, place};
   const RowSplit w(a, {d, in, to}, kGradUnits);

@@ -44,35 +44,38 @@ vsf_status check(int kind, const Product& a) {
       a.K < 1 || a.K > kMaxSide)
     return fail(VSF_ERR_ARG, w + ": sizes out of range");
   const int64_t in = kind == kForward ? a.K : a.N, to = kind == kForward ? a.N : a.K;
-  const int64_t most = int64_t(1) << 40;
-  if (a.rows_ld < in || a.rows_ld > most || a.other_ld < a.K || a.other_ld > most || a.out_ld < to ||
-      a.out_ld > most)
+  auto stride_ok = [](int64_t n, int64_t ld, int64_t width) { return ld >= width && offsets_ok(n, ld); };
+  const bool grad = kind == kWeight;
+  if (!stride_ok(a.rows, a.rows_ld, in) || !stride_ok(grad ? a.rows : a.N, a.other_ld, a.K) ||
+      !stride_ok(grad ? a.N : a.rows, a.out_ld, to))
     return fail(VSF_ERR_ARG, w + ": stride out of range");
   if (a.starts == nullptr || a.err == nullptr ||
       (a.rows > 0 && (a.rows_in == nullptr || a.other == nullptr || a.out == nullptr)) ||
       (kind == kWeight && a.out == nullptr))
     return fail(VSF_ERR_ARG, w + ": NULL pointer");
-  if (kind == kWeight ? a.E > 1 && (a.out_stride < (a.N - 1) * a.out_ld + a.K || a.out_stride > most)
-                      : a.E > 1 && (a.other_stride < (a.N - 1) * a.other_ld + a.K || a.other_stride > most))
+  // the experts' matrices
+  const int64_t stride = a.E == 1 ? 0 : grad ? a.out_stride : a.other_stride;
+  const int64_t whole = (a.N - 1) * (grad ? a.out_ld : a.other_ld) + a.K;
+  if (a.E > 1 && !stride_ok(a.E, stride, whole))
     return fail(VSF_ERR_ARG, w + ": experts' stride out of range");
   if (!aligned(a.starts, 4) || !aligned(a.err, 4) || !tma_rows(a.rows_in, a.rows_ld) ||
       !tma_rows(a.other, a.other_ld) || !tma_rows(a.out, a.out_ld) ||
-      (a.E > 1 && (kind == kWeight ? a.out_stride : a.other_stride) % 8 != 0))
+      stride % 8 != 0)
     return fail(VSF_ERR_ALIGN, w + ": rows have to start on 16-byte boundaries (strides of whole 8 elements)");
   // what is written overlaps nothing that is read
-  auto end = [](const uint16_t* p, int64_t n, int64_t ld, int64_t width) {
-    return reinterpret_cast<uintptr_t>(p) + (uintptr_t)(n > 0 ? ((n - 1) * ld + width) * 2 : 0);
+  auto rows_of = [](const uint16_t* p, int64_t n, int64_t ld, int64_t width) -> Area {
+    return {p, n, 2 * ld, 2 * width};
   };
-  const uintptr_t o0 = reinterpret_cast<uintptr_t>(a.out);
-  const uintptr_t o1 = kind == kWeight ? end(a.out + (a.E - 1) * a.out_stride, a.N, a.out_ld, a.K)
-                                       : end(a.out, a.rows, a.out_ld, to);
-  const uintptr_t r0 = reinterpret_cast<uintptr_t>(a.rows_in), w0 = reinterpret_cast<uintptr_t>(a.other);
-  const uintptr_t r1 = end(a.rows_in, a.rows, a.rows_ld, in);
-  const uintptr_t w1 = kind == kWeight ? end(a.other, a.rows, a.other_ld, a.K)
-                                       : end(a.other + (a.E - 1) * a.other_stride, a.N, a.other_ld, a.K);
-  const uintptr_t s0 = reinterpret_cast<uintptr_t>(a.starts), s1 = s0 + (uintptr_t)(a.E + 1) * 4;
-  if ((o0 < r1 && r0 < o1) || (o0 < w1 && w0 < o1) || (o0 < s1 && s0 < o1))
-    return fail(VSF_ERR_ARG, w + ": the output overlaps an input");
+  auto matrices = [&](const uint16_t* p) -> Area {
+    const int64_t bytes = 2 * ((a.E - 1) * stride + whole);
+    return {p, 1, bytes, bytes};
+  };
+  const Area out = grad ? matrices(a.out) : rows_of(a.out, a.rows, a.out_ld, to);
+  const int64_t starts_bytes = (a.E + 1) * 4;
+  for (const Area& read : {rows_of(a.rows_in, a.rows, a.rows_ld, in),
+                           grad ? rows_of(a.other, a.rows, a.other_ld, a.K) : matrices(a.other),
+                           Area{a.starts, 1, starts_bytes, starts_bytes}})
+    if (meet(out, read)) return fail(VSF_ERR_ARG, w + ": the output overlaps an input");
   return VSF_OK;
 }
 
@@ -84,7 +87,7 @@ vsf_status operand_map(CUtensorMap* map, const char* who, const uint16_t* p, int
   PFN_cuTensorMapEncodeTiled_v12000 encode = gemm_map_encoder();
   if (encode == nullptr) return fail(VSF_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)batch};
-  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)std::max(bs, ld) * 2};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(batch > 1 ? bs : ld) * 2};
   const cuuint32_t box[3] = {(cuuint32_t)box_width, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
   const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(p), dims,
                             strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -33,10 +33,10 @@ class _Rows(_Objective):
         ld, unit = x.stride()
         if unit != 1 and width > 1:
             raise ValueError(f"{what}: the elements of a row must be adjacent (stride {unit})")
+        if rows <= 1:  # (no stride to speak of)
+            return self._padded(width)
         if ld < width:
-            if rows > 1:
-                raise ValueError(f"{what}: rows overlap (stride {ld}, {width} elements)")
-            ld = self._padded(width)
+            raise ValueError(f"{what}: rows overlap (stride {ld}, {width} elements)")
         return ld
 
     def _padded(self, width: int) -> int:
@@ -202,7 +202,7 @@ class ExpertLinear(_Rows):
         stride, ld, unit = w.stride()
         if unit != 1 and shape[2] > 1:
             raise ValueError(f"{what}: the elements of a row must be adjacent (stride {unit})")
-        if ld < shape[2] and shape[1] == 1:
+        if shape[1] == 1:
             ld = self._padded(shape[2])
         return ld, stride
 

@@ -94,6 +94,29 @@ def test_product_refusals(call, args, extra):
         refuse(call, args, change, want)
 
 
+@pytest.mark.parametrize("call,args,changes", [
+    (V.vsf_expert_gather, GATHER, [
+        dict(rows=2 * A), dict(rows=2 * A + 16), dict(ld=1 << 39), dict(ld=1 << 57),
+        dict(rows_ld=96, ld=96, rows=A + 62), dict(rows_ld=96, ld=96, rows=A + 66)]),
+    (V.vsf_expert_combine, COMBINE, [
+        dict(out=2 * A), dict(out=3 * A + 28), dict(y_ld=1 << 39), dict(T=1 << 23, out_ld=1 << 38),
+        dict(y_ld=130, out_ld=130, out=A + 4 * 63), dict(y_ld=130, out_ld=130, out=A + 4 * 67)]),
+    (V.vsf_expert_combine_grad, GRAD, [
+        dict(d_gates=A), dict(d_gates=2 * A + 1020), dict(d_gates=5 * A), dict(d_y=3 * A), dict(d_y=4 * A + 28),
+        dict(d_y=6 * A), dict(d_out_ld=1 << 39), dict(y_ld=128, d_y_ld=128, d_y=2 * A + 126)]),
+    (V.vsf_expert_product, FORWARD, [
+        dict(x_ld=1 << 39), dict(rows=1 << 28, y_ld=1 << 32), dict(w_stride=1 << 39),
+        dict(x_ld=160, y_ld=160, y=A + 112), dict(x_ld=152, y_ld=152, y=A + 128)]),
+    (V.vsf_expert_product_input_grad, INPUT, [
+        dict(d_x=3 * A), dict(d_y_ld=160, d_x_ld=160, d_x=A + 176)]),
+    (V.vsf_expert_product_weight_grad, WEIGHT, [
+        dict(d_w=3 * A), dict(d_w=A + 64), dict(d_w_ld=1 << 39), dict(d_w_stride=1 << 39)])])
+def test_overlaps_and_long_strides(call, args, changes):
+    """An output among an input's rows, by one column too many; offsets past 2^58."""
+    for change in changes:
+        refuse(call, args, change, ARG)
+
+
 def test_no_rows_is_no_error():
     V.vsf_expert_product(**{**FORWARD, "rows": 0})
     V.vsf_expert_product_input_grad(**{**INPUT, "rows": 0})

@@ -385,6 +385,67 @@ def test_products_on_streams_and_in_graphs():
     assert all(layer.device_error() == 0 for _, layer in pairs + [calls] + plain)
 
 
+@pytest.mark.parametrize("dtype,width,gap", [(BF16, 128, 0), (FP32, 77, 3), (BF16, 200, 8)])
+def test_columns_of_shared_rows(dtype, width, gap):
+    """Inputs and outputs side by side in the rows of one array."""
+    from fsdp_buffer_layout_gb300.experts import Dispatch
+    rng = np.random.default_rng(width)
+    tokens, experts, k, at = 50, 5, 3, width + gap
+    buf = strided(tokens * k, 2 * at, 0, 0, dtype, rng)
+    before = host(buf)
+    left, right = buf[:, :width], buf[:, at:at + width]
+    idx = choices(rng, tokens, experts, k, True)
+    gates = torch.from_numpy(rng.normal(size=(tokens, k)).astype(np.float32)).cuda()
+    op = Dispatch(tokens, experts, k, width, dtype=dtype)
+    starts, _, place = op.sort(idx)
+    place, n = host(place).astype(int), int(starts[-1])
+    op.gather(left[:tokens], out=right)
+    want = before.copy()
+    want[:, at:at + width] = R.gather(before[:tokens, :width], place, before[:, at:at + width])
+    assert np.array_equal(host(buf), want) and n > 0
+    d_out = strided(tokens, width, 0, 0, dtype, rng)
+    d_y, d_gates = op.combine_backward(d_out, right, gates, d_y=left)
+    want_y, want_gates = R.combine_grad(host(d_out), want[:, at:at + width], place, host(gates), want[:, :width])
+    assert d_y is left
+    assert (np.abs(host(left) - want_y) <= (HALF[dtype] + 2.0**-24) * np.abs(want_y) * 1.01).all()
+    assert np.array_equal(host(right), want[:, at:at + width])
+    size = R.combine_grad(np.abs(host(d_out)), np.abs(want[:, at:at + width]), place, host(gates),
+                          want[:, :width])[1]
+    assert (np.abs(host(d_gates) - want_gates) <= (width + 1) * 2.0**-24 * size * 1.01).all()
+
+
+def test_products_beside_their_rows():
+    """Rows and products in the rows of one array; one expert whose matrix has an
+    odd stride; a single row of any stride."""
+    from fsdp_buffer_layout_gb300.experts import ExpertLinear
+    rng = np.random.default_rng(5)
+    rows, experts, n_out, n_in = 70, 3, 40, 64
+    buf = strided(rows, n_in + n_out, 0, 0, BF16, rng)
+    x, y = buf[:, :n_in], buf[:, n_in:]
+    w = strided(experts * n_out, n_in, 0, 0, BF16, rng).view(experts, n_out, n_in)
+    starts = torch.tensor([0, 20, 20, 61], dtype=torch.int32, device="cuda")
+    before = host(buf)
+    op = ExpertLinear(rows, experts, n_out, n_in)
+    op.forward(x, w, starts, out=y)
+    got = host(buf)
+    want = R.product(before[:, :n_in], host(w), host(starts).astype(int))
+    size = R.product(np.abs(before[:, :n_in]), np.abs(host(w)), host(starts).astype(int))
+    lim = HALF[BF16] * np.abs(want[:61]) + n_in * 2.0**-23 * size[:61]
+    assert np.array_equal(got[:, :n_in], before[:, :n_in]) and np.array_equal(got[61:], before[61:])
+    assert (np.abs(got[:61, n_in:] - want[:61]) <= lim * 1.01).all()
+    one = ExpertLinear(1, 1, n_out, n_in)
+    w1, starts = w[1].as_strided((1, n_out, n_in), (n_out * n_in - 3, n_in, 1)), starts[:2].clamp(max=1)
+    x1 = x[3:4].clone().as_strided((1, n_in), (n_in + 1, 1))
+    got = host(one.forward(x1, w1, starts))
+    want, size = host(x1) @ host(w1)[0].T, np.abs(host(x1)) @ np.abs(host(w1)[0]).T
+    assert (np.abs(got - want) <= (HALF[BF16] * np.abs(want) + n_in * 2.0**-23 * size) * 1.01).all()
+    d_w = torch.empty_like(w1[0]).as_strided((1, n_out, n_in), (n_out * n_in + 5, n_in, 1))
+    d_y = strided(1, n_out, 0, 0, BF16, rng).as_strided((1, n_out), (n_out + 3, 1))
+    assert one.backward_weight(d_y, x1, starts, out=d_w) is d_w
+    want = host(d_y).T @ host(x1)
+    assert (np.abs(host(d_w)[0] - want) <= HALF[BF16] * np.abs(want) * 1.01).all()
+
+
 def test_objects_refuse():
     from fsdp_buffer_layout_gb300.experts import Dispatch, ExpertLinear
     call = Dispatch(8, 4, 2, 32)
