@@ -648,15 +648,29 @@ ScoreCut score_cut_one(int64_t V) {
   return c;
 }
 
-// Whether a CTA does a row: up to two of them to an SM. A row's CTA reads some 70 GB/s,
-// so rows that are long beside their number are better shared out: as measured (L2 warm,
-// 5 alternatives, us here and in two launches), 1 row of 200 KB 6.5 / 6.7, 32 of 256 KB
-// 8.7 / 8.2, 64 of 256 KB 8.7 / 9.5, of 512 KB 12.9 / 13.2, 32 of 512 KB 12.9 / 9.5,
-// 300 of 512 KB 30 / 34. Above 1 MB the two are alike.
+// How many rows an SM is to have, a CTA each: 1, 2, 3 or 6; 0: the pieces are shared
+// out and the rows finished by a second launch. As measured (L2 warm, 5 alternatives,
+// us here and in two launches):
+//  - a row's CTA reads some 70 GB/s, so rows that are long beside their number are
+//    shared out: 1 row of 200 KB 6.5 / 6.7, 32 of 256 KB 8.7 / 8.2, 64 of 256 KB 8.7 / 9.5,
+//    of 512 KB 12.9 / 13.2, 32 of 512 KB 12.9 / 9.5. Above 1 MB the two are alike.
+//  - 300 rows of 64 KB 7.6 / 10.8 (in CTAs for three to an SM 9.5), of 512 KB 30 / 34; 400
+//    of 64 KB 9.6 / 11.9, of 512 KB 34.5 / 39.6.
+//    Without alternatives 200 of 200 KB 10.5 / 8.6.
+//  - four and more rows an SM leave 128 threads for each: 600 of 2 KB 5.3 / 8.1, of
+//    32 KB 8.9 / 10.4, of 64 KB 15.9 / 14.7. From 7 on rows wait for others: 2048 rows of
+//    16 KB 17.7 / 16.8.
 template <typename T>
-bool one_score_launch(int64_t tokens, int64_t V) {
-  const int64_t bytes = V * (int64_t)sizeof(T);
-  return tokens <= 2 * kSms && bytes < 8192 * std::max<int64_t>(tokens, 25) && bytes <= int64_t(1) << 20;
+int one_score_launch(int64_t tokens, int64_t V, int32_t K) {
+  const int64_t bytes = V * (int64_t)sizeof(T), of = (tokens + kSms - 1) / kSms;
+  if (bytes >= 8192 * std::max<int64_t>(tokens, 25) || bytes > int64_t(1) << 20) return 0;
+  if (K == 0 && of > 1 && bytes > int64_t(1) << 17) return 0;
+  return of <= 3 ? (int)of : of <= 6 && bytes <= 32768 ? 6 : 0;
+}
+
+template <typename T, int NT, int CTAS>
+cudaError_t scores_one(const ScoreArgs<T>& k, cudaStream_t st) {
+  return launch_behind(score_one_kernel<T, NT, CTAS>, (unsigned)k.r.T_, NT, 0, 1, st, k);
 }
 
 unsigned score_grid(int64_t items, int ctas) {
@@ -675,15 +689,17 @@ cudaError_t scores(const RowsArg& a, int32_t K, float* logp, float* entropy, int
   k.head = reinterpret_cast<WsHead*>(b);
   k.part = reinterpret_cast<float4*>(b + sizeof(WsHead));
   k.keys = reinterpret_cast<uint32_t*>(b + sizeof(WsHead) + (size_t)a.T_ * k.cut.pieces * 16);
-  const bool one = one_score_launch<T>(a.T_, a.V);
-  if (one) k.cut = score_cut_one<T>(a.V);
+  const int one = one_score_launch<T>(a.T_, a.V, K);
+  if (one > 0) k.cut = score_cut_one<T>(a.V);
   k.logp = logp;
   k.entropy = entropy;
   k.top_idx = top_idx;
   k.top_logp = top_logp;
   k.norm = reinterpret_cast<float4*>(norm);
-  if (one && a.T_ <= kSms) return launch_behind(score_one_kernel<T, 512>, (unsigned)a.T_, 512, 0, 1, st, k);
-  if (one) return launch_behind(score_one_kernel<T, 256>, (unsigned)a.T_, 256, 0, 1, st, k);
+  if (one == 1) return scores_one<T, 512, 1>(k, st);
+  if (one == 2) return scores_one<T, 256, 2>(k, st);
+  if (one == 3) return scores_one<T, 256, 3>(k, st);
+  if (one == 6) return scores_one<T, 128, 6>(k, st);
   const cudaError_t e = launch_behind(score_part_kernel<T>, score_grid(a.T_ * k.cut.pieces, kPartCtas),
                                       kScoreThreads, 0, 1, st, k);
   if (e != cudaSuccess) return e;

@@ -645,11 +645,10 @@ __global__ void __launch_bounds__(kRowScoreThreads, N == 8 ? 12 : 4)
 
 // Few rows: a CTA does all of a row, its pieces' sums and keys in shared memory, in one
 // launch instead of two: 5.5 us instead of 6.0 for 8 rows of 32000 bf16 with 5
-// alternatives, 8.9 instead of 14.1 for 152 of 131072. NT: 512 threads for up to a row
-// an SM, 256 for two. (All the SMs' registers, so that rows do not wait: with three or
-// more to an SM the other way is faster, 15.8 us instead of 21 for 777 of 32000.)
-template <typename T, int NT>
-__global__ void __launch_bounds__(NT, 512 / NT) score_one_kernel(const __grid_constant__ ScoreArgs<T> a) {
+// alternatives, 8.9 instead of 14.1 for 152 of 131072. CTAS of NT threads an SM, so that
+// all rows are in work at a time.
+template <typename T, int NT, int CTAS>
+__global__ void __launch_bounds__(NT, CTAS) score_one_kernel(const __grid_constant__ ScoreArgs<T> a) {
   __shared__ RowShared sh;
   __shared__ float4 parts[32];  // (at most 32 pieces)
   __shared__ uint32_t keys[1024];

@@ -249,7 +249,8 @@ def test_temperatures_at_the_ends_of_their_range(vocab, inv_t):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
-@pytest.mark.parametrize("tokens,vocab", [(120, 70003), (220, 5000), (220, 300), (400, 5000), (400, 70003), (3, 150001)])
+@pytest.mark.parametrize("tokens,vocab", [(120, 70003), (220, 5000), (220, 300), (400, 5000), (400, 70003), (600, 5000),
+                                          (500, 30001), (1000, 900), (3, 150001)])
 @pytest.mark.parametrize("inv_t,k", [(1.0, 8), (1e30, 3), (1.0, 32)])
 def test_edge_rows_in_calls_of_any_size(tokens, vocab, dtype, inv_t, k):
     """Ties, masked words and rows that give NaN, some of each left out, however a
