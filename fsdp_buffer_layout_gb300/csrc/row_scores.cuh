@@ -440,8 +440,8 @@ __device__ __forceinline__ void masked_row(const ScoreArgs<T>& a, int64_t t) {
 }
 
 // Joins the pieces of row t, whose target is y, and picks its alternatives; a CTA of
-// kRowScoreThreads. key: N of the row's keys each (key j * kRowScoreThreads + tid), part: the first warp's
-// first pieces, parts: all of them.
+// kRowScoreThreads. key: N of the row's keys each, key j * kRowScoreThreads + tid of
+// them; part: the first warp's first pieces; parts: all of them.
 template <int N, typename T>
 __device__ __forceinline__ void finish_row(const ScoreArgs<T>& a, int64_t t, int32_t y, const uint32_t (&key)[N],
                                            float4 part, const float4* parts, RowShared& sh) {
