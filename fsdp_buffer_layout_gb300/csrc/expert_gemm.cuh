@@ -74,6 +74,7 @@ struct XTable {
   int32_t first[kMaxGroups + 1];  // tiles in front of each expert's
   int32_t start[kMaxGroups + 1];  // its first row
   uint32_t tmem, stop;
+  int32_t most;                   // rows of a tile at most, 2^most (kForward, kInput)
 };
 constexpr uint32_t kXOut = 4096;  // of each epilogue warp: 32 lanes x 64 columns, or two of 32 x 32
 constexpr uint32_t kXSmem =
@@ -99,10 +100,14 @@ struct XTile {
   int32_t row0, depth;  // what is summed over
 };
 
-// An expert's rows in tiles of at most 256, as even as can be in units of 32: one of 256
-// and a narrow one would cost more than half a tile for the narrow one, and as many of
-// one width compute up to an eighth too many.
-__device__ __forceinline__ int32_t token_tiles(int32_t rows) { return (rows + kXCols - 1) / kXCols; }
+// An expert's rows in tiles of at most `most`, as even as can be in units of 32: one of
+// 256 and a narrow one would cost more than half a tile for the narrow one, and as many
+// of one width compute up to an eighth too many. `most` is 256, or 128 where the tiles
+// of that are no more than the pairs of CTAs: 4 experts of 256 rows, 1024 x 4096, 19.8 us
+// instead of 25.3, 4 of 1190 rows, 64 x 4352, 21.7 instead of 26.3. (With 64 as well 19.7
+// and 20.5, but 8 of 128 rows, 1024 x 4096, 20.5 instead of 20.0, weights read more often.)
+constexpr int kXMost = 8, kXLeast = 7;  // 2^8, 2^7
+__device__ __forceinline__ int32_t token_tiles(int32_t rows, int32_t most) { return (rows + (1 << most) - 1) >> most; }
 
 // Tile t of the launch, for a converged warp; `e` moves on from tile to tile.
 template <int KIND>
@@ -130,7 +135,7 @@ __device__ __forceinline__ XTile tile_at(const ExpertArgs& a, const XTable& x, i
     // eight pieces of rows at a time take a lane tile one after the other: its
     // weights come from memory once, and are asked for by fewer pairs at a time (2 to 4
     // percent for 32 experts of 1024 rows, against all lane tiles of a piece in turn)
-    const int32_t begin = x.start[e], rows = x.start[e + 1] - begin, pieces = token_tiles(rows);
+    const int32_t begin = x.start[e], rows = x.start[e + 1] - begin, pieces = token_tiles(rows, x.most);
     int32_t k = t - x.first[e];
     const int32_t block = k / (kXBlock * a.lane_tiles) * kXBlock, n = min(kXBlock, pieces - block);
     k -= block * a.lane_tiles;
@@ -222,9 +227,18 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
     if (lane == 0) low = 0;
     for (int e = begin; e < end; ++e) table.start[e] = max(low, table.start[e]);
     __syncwarp();
-    int32_t tiles = 0;
-    for (int e = begin; e < min(end, g.E); ++e)
-      tiles += token_tiles(table.start[e + 1] - table.start[e]) * g.lane_tiles;
+    int32_t tiles = 0, narrow = 0;
+    for (int e = begin; e < min(end, g.E); ++e) {
+      const int32_t rows = table.start[e + 1] - table.start[e];
+      tiles += token_tiles(rows, kXMost) * g.lane_tiles;
+      narrow += token_tiles(rows, kXLeast) * g.lane_tiles;
+    }
+    int32_t most = kXMost;
+    if (KIND != kWeight && __reduce_add_sync(~0u, narrow) <= ncid) {
+      most = kXLeast;
+      tiles = narrow;
+    }
+    if (lane == 0) table.most = most;
     int32_t at = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -234,7 +248,7 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
     at -= tiles;
     for (int e = begin; e < end; ++e) {
       table.first[e] = at;
-      if (e < g.E) at += token_tiles(table.start[e + 1] - table.start[e]) * g.lane_tiles;
+      if (e < g.E) at += token_tiles(table.start[e + 1] - table.start[e], most) * g.lane_tiles;
     }
   }
   tc_fence_before();

@@ -154,7 +154,8 @@ vsf_status product(const Product& a, cudaStream_t st) {
   // (an upper bound: the rows' share among the experts is device memory)
   const int64_t tiles = KIND == kWeight ? a.E * g.lane_tiles * g.col_tiles
                                         : (a.rows / kXCols + std::min(a.E, a.rows)) * g.lane_tiles;
-  if (tiles > INT32_MAX / 2) return fail(VSF_ERR_ARG, std::string(a.who) + ": too many tiles");
+  const int64_t narrow = KIND == kWeight ? tiles : ((a.rows >> kXLeast) + std::min(a.E, a.rows)) * g.lane_tiles;
+  if (tiles > INT32_MAX / 4) return fail(VSF_ERR_ARG, std::string(a.who) + ": too many tiles");
   XMaps m;
   vsf_status s;
   if (KIND == kWeight) {
@@ -173,7 +174,7 @@ vsf_status product(const Product& a, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   const int pairs = expert_pairs<KIND>(&e);
   if (pairs > 0)
-    e = launch_behind(expert_gemm_kernel<KIND>, (unsigned)(2 * std::min<int64_t>(pairs, tiles)),
+    e = launch_behind(expert_gemm_kernel<KIND>, (unsigned)(2 * std::min<int64_t>(pairs, narrow)),
                       kXThreads<KIND>, kXSmem, 2, st, m, g, a.err);
   return e == cudaSuccess ? VSF_OK : cuda_error(e, a.who);
 }

@@ -177,6 +177,10 @@ PRODUCTS = [  # rows of each expert, rows behind, out, in, pads
     ([64] * 40 + [0] * 3 + [65], 0, 257, 129, 0),   # many tiles of one stage
     ([1000], 24, 1000, 520, 0),
     ([90, 300, 10], 0, 2880, 576, 0),
+    ([300, 7, 220, 31, 0, 513], 3, 9000, 70, 0),    # more wide tiles than pairs of CTAs
+    ([200, 130, 257], 0, 70, 9000, 0),
+    ([150, 400], 9, 1030, 1100, 0),                 # tiles of half the width
+    ([1200, 1100, 900], 0, 64, 1500, 0),            # of a quarter
 ]
 
 
