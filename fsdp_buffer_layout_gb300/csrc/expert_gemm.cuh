@@ -34,7 +34,8 @@
 // runs); 32 of 1024 rows, 5632 x 2816: 550 to 575 us forward, 600 to 620 input
 // gradient, 620 to 655 weight gradient; the tensor pipe is busy in 91 percent of the
 // cycles, and calls in a row for longer than some 0.1 s are slower by the card's
-// power limit. 32 experts of 16 rows, 5760 x 2880: 163 us, 6.6 TB/s of weights; their
+// power limit (32 of 1024 rows, 5760 x 2880, for 2 s: 1603, 1538 and 1520 TFLOP/s, torch's
+// batched products 1618, 1487 and 1423, its one product of 8192^3 1693). 32 experts of 16 rows, 5760 x 2880: 163 us, 6.6 TB/s of weights; their
 // weight gradient 255 us, 4.2 TB/s written (torch's fill of as much: 4.0). Bound by a
 // call's fixed 5 us, a tile's first loads and its epilogue (2 us) where there are few
 // tiles of little depth.
