@@ -556,11 +556,10 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
       }
       const int32_t from = q.depth & (kXDepth - 1), rows = 16 - (q.depth & 15);
       const int boxes = 2 + q.width / 128;  // of 64 x 64: two of A, one or two of B
-      unsigned char* a = sm + s * kXStage;
-      for (int k = lane; k < boxes * rows * 8; k += 32) {
-        const int box = k / (rows * 8), w = k - box * (rows * 8);
-        *reinterpret_cast<uint4*>(a + box * 8192 + from * 128 + w * 16) = make_uint4(0, 0, 0, 0);
-      }
+      // eight lanes a box, a row at a time
+      unsigned char* a = sm + s * kXStage + (lane >> 3) * 8192 + from * 128 + (lane & 7) * 16;
+      for (int i = 0; i < rows && (lane >> 3) < boxes; ++i)
+        *reinterpret_cast<uint4*>(a + i * 128) = make_uint4(0, 0, 0, 0);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (!leader) {
