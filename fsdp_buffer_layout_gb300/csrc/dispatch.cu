@@ -434,8 +434,11 @@ int64_t run_of(int64_t n) {
   return (run + kSortWarps * 32 - 1) / (kSortWarps * 32) * (kSortWarps * 32);
 }
 
+// Counts of as many runs as any call of up to n choices takes. Their number falls
+// where a run grows: 65536 choices are 64 runs, 65537 are 33.
 size_t sort_bytes(int64_t n, int64_t E) {
-  return n <= kSortOne ? 16 : (size_t)(((n + run_of(n) - 1) / run_of(n) * E * 4 + 15) / 16 * 16);
+  const int64_t runs = std::min<int64_t>(kMaxRuns, (n + kSortRun - 1) / kSortRun);
+  return n <= kSortOne ? 16 : (size_t)((runs * E * 4 + 15) / 16 * 16);
 }
 
 bool sizes_ok(int64_t T_, int64_t K) {

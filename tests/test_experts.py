@@ -50,6 +50,20 @@ def test_sort_workspace():
         assert V.vsf_expert_sort_workspace_bytes(*bad) == 0
 
 
+@pytest.mark.parametrize("top_k,experts", [(1, 1), (1, 32), (4, 32), (5, 3), (8, 256), (32, 512)])
+def test_sort_workspace_holds_every_smaller_call(top_k, experts):
+    """The size asked for the most tokens is enough for fewer: it never falls, and a
+    call is refused for less than what is asked for its own number only."""
+    edges = [m * n // top_k + d for n in (1024, 2048, 65536) for m in range(1, 9) for d in range(-2, 3)]
+    sizes = [V.vsf_expert_sort_workspace_bytes(t, top_k, experts)
+             for t in sorted({0, 1, 1 << 23, *range(0, 400_000 // top_k, 331), *edges})]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+    args = dict(SORT, top_k=top_k, E=experts, idx=1 << 40, starts=2 << 40, source=3 << 40, place=4 << 40)
+    for t in (3000, 65536 // top_k, 65536 // top_k + 1):
+        least = V.vsf_expert_sort_workspace_bytes(t, top_k, experts)
+        refuse(V.vsf_expert_sort, args, dict(T=t, ws_bytes=least - 1), ARG)
+
+
 @pytest.mark.parametrize("call,args,extra", [
     (V.vsf_expert_gather, GATHER, [
         (dict(x=0), ARG), (dict(rows=0), ARG), (dict(ld=63), ARG), (dict(rows_ld=63), ARG),

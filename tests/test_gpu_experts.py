@@ -134,6 +134,26 @@ def test_sort_of_many(tokens, experts, k, live):
         idx = idx.flip(0).contiguous()
 
 
+@pytest.mark.parametrize("tokens,experts,k,calls", [
+    (20000, 32, 4, (20000, 16384, 15000, 3000, 10241, 400, 0, 20000)),
+    (10000, 256, 8, (8192, 10000, 8193, 1)), (131073, 5, 1, (65536, 65537, 131072, 131073, 70000))])
+def test_sorts_of_fewer_tokens(tokens, experts, k, calls):
+    """One object, calls of fewer tokens than it holds, one after the other; and rows
+    of as many tokens to their places and back."""
+    from fsdp_buffer_layout_gb300.experts import Dispatch
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    call = Dispatch(tokens, experts, k, 8, with_grad=False)
+    for n in calls:
+        idx = torch.randint(-1, experts, (n, k), device="cuda", generator=g).int()
+        starts, source, place = call.sort(idx)
+        want_starts, want_source, want_place = R.sort(host(idx).astype(np.int64).reshape(n, k), experts)
+        assert np.array_equal(host(starts), want_starts) and np.array_equal(host(source), want_source)
+        assert np.array_equal(host(place).reshape(n, k), want_place)
+        x = torch.randn(n, 8, device="cuda", generator=g).bfloat16()
+        rows, here = call.gather(x), source >= 0
+        assert torch.equal(rows[here], x[source[here].long() // k])
+
+
 @pytest.mark.parametrize("dtype,width", [(BF16, 2048), (FP32, 999)])
 def test_many_rows(dtype, width):
     """More rows than warps run at a time, in both directions."""
