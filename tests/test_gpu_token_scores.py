@@ -248,6 +248,47 @@ def test_temperatures_at_the_ends_of_their_range(vocab, inv_t):
         assert (np.abs(host(out) - want) <= (2.0**-7) * np.abs(want) + 2.0**-18 * t32 * pulls[0][0]).all()
 
 
+@pytest.mark.parametrize("vocab", [40000, 131076])
+def test_reference_of_the_exponents(vocab):
+    """The exponents' reference lies at most 16 units of ln 2 below the row's maximum,
+    also where 16 units are no number of the logits' type: next to 2^27, whose neighbours
+    are 16 apart, 30 units at this temperature. Every lane begins at the lower one."""
+    from fsdp_buffer_layout_gb300.objectives import TokenScores
+    inv_t, n = 1.3, np.arange(vocab)
+    v = np.where(n // 128 % 16 < 4, 2.0**27, 2.0**27 + 16)[None].repeat(3, 0)
+    v[1, -1] = 2.0**27 - 8
+    v[2, n // 128 % 16 == 5] = 2.0**27 + 32
+    x, y = strided(v, FP32), np.array([5, vocab - 1, vocab // 2])
+    op = TokenScores(3, vocab, top_k=2, dtype=FP32, inv_temperature=inv_t)
+    check(x, y, float(np.float32(inv_t)), 2, op.forward(x, dev(y, torch.int64)))
+    norm = host(op.norm)
+    above = (v.max(1) - norm[:, 0]) * inv_t / math.log(2)
+    # (0.08 and 200 / c are within 2^-23 of what they stand for)
+    assert (above >= 0).all() and (above <= 16 * (1 + 2.0**-20)).all(), above
+    assert (norm[:, 1] <= vocab * 2.0**16 * (1 + 2.0**-10)).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("vocab", [9000, 40000, 131075])
+def test_far_logits_at_a_high_temperature(vocab, dtype):
+    """Logits whose difference is out of range, low ones first in every lane, at a
+    temperature that leaves them 60 apart."""
+    from fsdp_buffer_layout_gb300.objectives import TokenScores
+    n = np.arange(vocab)
+    span = 32 * 16 // dtype.itemsize
+    v = np.where(n // span % 16 < 4, -3e38, 3e38)[None].repeat(2, 0)
+    v[1] *= -1
+    x = strided(v, dtype)
+    y = np.array([5 * span, 1])
+    for inv_t in (1e-37, 3e-37):
+        op = TokenScores(2, vocab, top_k=3, dtype=dtype, inv_temperature=inv_t)
+        got = op.forward(x, dev(y, torch.int64))
+        check(x, y, float(np.float32(inv_t)), 3, got)
+        pulls = [np.ones(s, np.float32) for s in (2, 2, (2, 3))]
+        out = op.backward(x, dev(y, torch.int64), *[dev(p) for p in pulls])
+        assert torch.isfinite(out).all()
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("tokens,vocab", [(120, 70003), (220, 5000), (220, 300), (400, 5000), (400, 70003), (600, 5000),
                                           (500, 30001), (1000, 900), (3, 150001)])
