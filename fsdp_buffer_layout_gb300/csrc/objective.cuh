@@ -130,16 +130,17 @@ struct Area {
   const void* p;
   int64_t n, ld, width;
 };
-// Whether two areas share a byte. Columns of the same rows are told apart; else their
-// ends decide.
+// Whether two areas share a byte. Columns of the same rows are told apart (a single row
+// goes by the other area's stride); else their ends decide.
 inline bool meet(const Area& x, const Area& y) {
   if (x.n <= 0 || y.n <= 0) return false;
   const uintptr_t x0 = reinterpret_cast<uintptr_t>(x.p), y0 = reinterpret_cast<uintptr_t>(y.p);
   if (x0 >= y0 + (uintptr_t)((y.n - 1) * y.ld + y.width) || y0 >= x0 + (uintptr_t)((x.n - 1) * x.ld + x.width))
     return false;
-  if (x.ld != y.ld || x.ld < x.width) return true;
-  const int64_t d = ((int64_t)(y0 - x0) % x.ld + x.ld) % x.ld;
-  return d < x.width || d + y.width > x.ld;
+  const int64_t ld = x.n > 1 ? x.ld : y.ld;
+  if ((y.n > 1 && y.ld != ld) || ld < x.width) return true;
+  const int64_t d = ((int64_t)(y0 - x0) % ld + ld) % ld;
+  return d < x.width || d + y.width > ld;
 }
 // Whether n rows at stride ld, in elements, have offsets that count.
 inline bool offsets_ok(int64_t n, int64_t ld) {

@@ -438,6 +438,34 @@ def test_columns_of_shared_rows(dtype, width, gap):
     assert (np.abs(host(d_gates) - want_gates) <= (width + 1) * 2.0**-24 * size * 1.01).all()
 
 
+def test_a_single_row_among_others():
+    """One token's row in a column block of the array whose other columns are
+    written: a single row has no stride, and shares no byte with them."""
+    from fsdp_buffer_layout_gb300.experts import Dispatch, ExpertLinear
+    rng = np.random.default_rng(8)
+    buf = strided(8, 128, 0, 0, BF16, rng)
+    left, right = buf[:, :64], buf[:, 64:]
+    want = host(left[3])
+    idx = torch.arange(8, dtype=torch.int32, device="cuda")[None]
+    op = Dispatch(1, 8, 8, 64)
+    op.sort(idx)
+    op.gather(left[3:4], out=right)
+    assert (host(right) == want).all()
+    out = op.combine(right, torch.ones(1, 8, device="cuda"), out=left[5:6])
+    assert (host(out) == 8 * want).all() and (host(left[3]) == want).all()
+    w = strided(64, 64, 0, 0, BF16, rng)[None]
+    starts = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    before, y = host(buf), ExpertLinear(1, 1, 64, 64).forward(left[2:3], w, starts, out=right[2:3])
+    want, size = before[2:3, :64] @ host(w[0]).T, np.abs(before[2:3, :64]) @ np.abs(host(w[0])).T
+    assert (np.abs(host(y) - want) <= (HALF[BF16] * np.abs(want) + 64 * 2.0**-23 * size) * 1.01).all()
+    before[2, 64:] = host(y)
+    assert np.array_equal(host(buf), before)
+    from fsdp_buffer_layout_gb300 import vsf as V
+    for bad in (buf[:, 63:127], buf[:, 1:65]):  # one column of the row itself
+        with pytest.raises(V.VsfError, match="overlaps"):
+            op.gather(left[3:4], out=bad)
+
+
 def test_products_beside_their_rows():
     """Rows and products in the rows of one array; one expert whose matrix has an
     odd stride; a single row of any stride."""
