@@ -52,12 +52,13 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 // The waits of a whole warp: all of its lanes go on, or none does.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned* err, volatile uint32_t* stop) {
-  return __all_sync(~0u, mbar_wait(bar, parity, err, stop));
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned* err, volatile uint32_t* stop,
+                                          uint64_t limit_ns) {
+  return __all_sync(~0u, mbar_wait(bar, parity, err, stop, limit_ns));
 }
 __device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, unsigned* err,
-                                                  volatile uint32_t* stop) {
-  return __all_sync(~0u, mbar_wait_cluster(bar, parity, err, stop));
+                                                  volatile uint32_t* stop, uint64_t limit_ns) {
+  return __all_sync(~0u, mbar_wait_cluster(bar, parity, err, stop, limit_ns));
 }
 
 enum { kForward = 0, kInput = 1, kWeight = 2 };
@@ -76,6 +77,7 @@ struct XTable {
   int32_t start[kMaxGroups + 1];  // its first row
   uint32_t tmem, stop;
   int32_t most;                   // rows of a tile at most, 2^most (kForward, kInput)
+  uint32_t loaded[2];             // stages that each CTA of the pair has loaded (pair_end)
 };
 constexpr uint32_t kXOut = 4096;  // of each epilogue warp: 32 lanes x 64 columns, or two of 32 x 32
 constexpr uint32_t kXSmem =
@@ -91,6 +93,7 @@ struct ExpertArgs {
   int32_t lane_tiles, col_tiles;
   uint16_t* out;
   int64_t ld, stride; // of out's rows; kWeight: of its experts
+  PairLimits limits;
 };
 
 struct XTile {
@@ -100,6 +103,13 @@ struct XTile {
   int32_t cols;       // columns stored
   int32_t row0, depth;  // what is summed over
 };
+
+// Of one CTA's copies into a stage; whether the stage of r from k0 on is mended (below).
+__device__ __forceinline__ uint32_t stage_bytes(const XTile& q) { return kXHalf + (uint32_t)(q.width / 2) * (kXDepth * 2); }
+template <int KIND>
+__device__ __forceinline__ bool mended_stage(const XTile& q, int32_t k0) {
+  return KIND == kWeight && k0 + kXDepth > q.depth && (q.depth & 15) != 0;
+}
 
 // An expert's rows in tiles of at most `most`, as even as can be in units of 32: one of
 // 256 and a narrow one would cost more than half a tile for the narrow one, and as many
@@ -190,7 +200,7 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
   constexpr uint16_t kBoth = 3;
 
   if (threadIdx.x == 0) {
-    table.stop = 0u;
+    table.stop = table.loaded[0] = table.loaded[1] = 0u;
     for (int s = 0; s < kXStages; ++s) {
       // kWeight: both CTAs' warps 6 arrive for a mended stage, the leader's producer twice
       // for others (by one of its warps 6 after the other: a row more or less an expert
@@ -276,27 +286,28 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
       const bool one = elect_one();
       const uint32_t own0 = peer_addr(own_bar(0), (uint32_t)rank);
       uint32_t it = 0, mended = 0, phases = 0;  // stages mended so far; how often, modulo 2
+      const int32_t end = last_tile(g.limits, leader, ntiles, cid, ncid);
       int s = 0;
       uint32_t phase = 1;
       int32_t e = 0;
       bool halted = false;
-      for (int32_t t = cid; t < ntiles && !halted; t += ncid) {
+      for (int32_t t = cid; t < end && !halted; t += ncid) {
         const XTile q = tile_at<KIND>(g, table, t, e);
         const int32_t half = q.width / 2;
         const int32_t lane0 = q.lane0 + rank * 128, col0 = q.col0 + rank * half;
         const int largest = 27 - __clz(half);  // box of 16 << largest rows
         const int32_t box = 16 << largest;
         const CUtensorMap* cols = &maps.cols[KIND == kWeight ? 0 : largest];
-        const uint32_t bytes = kXHalf + (uint32_t)half * (kXDepth * 2);
+        const uint32_t bytes = stage_bytes(q);
         for (int32_t k0 = 0; k0 < q.depth; k0 += kXDepth) {
-          if (!warp_wait(empty_bar(s), phase, err, stop)) {
+          if (!warp_wait(empty_bar(s), phase, err, stop, g.limits.wait_ns)) {
             halted = true;
             if (one) halt_cluster();
             break;
           }
           ++it;
           uint32_t fb = leader_full0 + 8u * s;
-          if (KIND == kWeight && k0 + kXDepth > q.depth && (q.depth & 15) != 0) {
+          if (mended_stage<KIND>(q, k0)) {
             fb = own0 + 8u * s;  // warp 6 mends the stage and then arrives
             if (one) mbar_expect_tx(own_bar(s), bytes);
             mended |= 1u << s;
@@ -338,8 +349,9 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
         }
       }
       // every copy lands before the CTA ends: the leader sees both CTAs' (the
-      // follower's are covered by its wait and the last cluster barrier)
+      // follower's are covered by its wait and pair_end)
       if (one) {
+        pair_tell(table.loaded, (uint32_t)rank, it);
         const uint64_t deadline = global_ns() + kWaitNs;
         for (int s = 0; KIND == kWeight && s < kXStages; ++s)
           if (mended >> s & 1u) mbar_drain(own_bar(s), (phases >> s & 1u) ^ 1u, deadline, err);
@@ -376,7 +388,7 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
         const XTile q = tile_at<KIND>(g, table, t, e);
         const uint32_t idesc = umma_idesc_bf16(AMN, BMN, kXLanes, q.width);
         const int buf = lt & 1;
-        if (!warp_wait_cluster(tempty_bar(buf), ((uint32_t)(lt >> 1) & 1u) ^ 1u, err, stop)) {
+        if (!warp_wait_cluster(tempty_bar(buf), ((uint32_t)(lt >> 1) & 1u) ^ 1u, err, stop, g.limits.wait_ns)) {
           if (one) halt_cluster();
           break;
         }
@@ -384,7 +396,7 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
         const uint32_t d = tmem + (uint32_t)(buf * kXCols);
         uint32_t more = 0;
         for (int32_t left = q.depth; left > 0; left -= kXDepth) {
-          if (!warp_wait_cluster(full_bar(s), phase, err, stop)) {
+          if (!warp_wait_cluster(full_bar(s), phase, err, stop, g.limits.wait_ns)) {
             halted = true;
             if (one) halt_cluster();
             break;
@@ -432,7 +444,10 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
     uint32_t turn = 0;
     for (int32_t t = cid; t < ntiles; t += ncid, ++lt) {
       const int buf = lt & 1;
-      const bool ok = warp_wait(tfull_bar(buf), (uint32_t)(lt >> 1) & 1u, err, stop);
+      if (!warp_wait(tfull_bar(buf), (uint32_t)(lt >> 1) & 1u, err, stop, g.limits.wait_ns)) {
+        if (lane == 0) halt_cluster();
+        break;
+      }
       tc_fence_after();
       // The accumulator is free once its last columns are in registers: said before
       // they are stored, as the arrival (a release) waits for the warp's stores.
@@ -441,100 +456,97 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(leader_tempty0 + 8u * buf);
       };
-      if (!ok) release();
-      if (ok) {
-        const XTile q = tile_at<KIND>(g, table, t, e);
-        const int32_t i = q.lane0 + rank * 128 + 32 * quarter + lane;
-        const uint32_t from = tmem + (uint32_t)(buf * kXCols) + ((uint32_t)(32 * quarter) << 16);
-        if (KIND == kWeight) {
-          // A lane holds 64 columns of its row at a time. Through shared memory, in
-          // the swizzle of the tensor copies (16-byte piece p of row l at p ^ (l & 7)),
-          // and out as one copy of 32 rows: 32 lanes' stores to 32 rows took 1640 us
-          // for 32 experts of 1024 rows, 5760 x 2880.
-          const uint32_t to = out0 + (uint32_t)quarter * kXOut;
-          const uint32_t mine = to + (uint32_t)lane * 128u;
+      const XTile q = tile_at<KIND>(g, table, t, e);
+      const int32_t i = q.lane0 + rank * 128 + 32 * quarter + lane;
+      const uint32_t from = tmem + (uint32_t)(buf * kXCols) + ((uint32_t)(32 * quarter) << 16);
+      if (KIND == kWeight) {
+        // A lane holds 64 columns of its row at a time. Through shared memory, in
+        // the swizzle of the tensor copies (16-byte piece p of row l at p ^ (l & 7)),
+        // and out as one copy of 32 rows: 32 lanes' stores to 32 rows took 1640 us
+        // for 32 experts of 1024 rows, 5760 x 2880.
+        const uint32_t to = out0 + (uint32_t)quarter * kXOut;
+        const uint32_t mine = to + (uint32_t)lane * 128u;
 #pragma unroll 1
-          for (int32_t c = 0; c < q.cols; c += 64) {
-            uint32_t p[32];
+        for (int32_t c = 0; c < q.cols; c += 64) {
+          uint32_t p[32];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t r[32];
-              __syncwarp();
-              tmem_ld32(from + c + 32 * h, r);
-              if (h == 1 && c + 64 >= q.cols) release();
-#pragma unroll
-              for (int x = 0; x < 16; ++x)
-                p[16 * h + x] = q.depth == 0 ? 0u : pack_bf16(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1]));
-            }
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[32];
             __syncwarp();
+            tmem_ld32(from + c + 32 * h, r);
+            if (h == 1 && c + 64 >= q.cols) release();
 #pragma unroll
-            for (int w = 0; w < 8; ++w)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + (uint32_t)((w ^ (lane & 7)) * 16)),
-                           "r"(p[4 * w]), "r"(p[4 * w + 1]), "r"(p[4 * w + 2]), "r"(p[4 * w + 3])
-                           : "memory");
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0 && q.lane0 + rank * 128 + 32 * quarter < g.lanes) {
-              asm volatile(
-                  "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                      reinterpret_cast<uint64_t>(&maps.out)),
-                  "r"(q.col0 + c), "r"(q.lane0 + rank * 128 + 32 * quarter), "r"(q.e), "r"(to)
-                  : "memory");
-              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            }
+            for (int x = 0; x < 16; ++x)
+              p[16 * h + x] = q.depth == 0 ? 0u : pack_bf16(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1]));
+          }
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+#pragma unroll
+          for (int w = 0; w < 8; ++w)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + (uint32_t)((w ^ (lane & 7)) * 16)),
+                         "r"(p[4 * w]), "r"(p[4 * w + 1]), "r"(p[4 * w + 2]), "r"(p[4 * w + 3])
+                         : "memory");
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0 && q.lane0 + rank * 128 + 32 * quarter < g.lanes) {
+            asm volatile(
+                "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                    reinterpret_cast<uint64_t>(&maps.out)),
+                "r"(q.col0 + c), "r"(q.lane0 + rank * 128 + 32 * quarter), "r"(q.e), "r"(to)
+                : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
         }
+      }
 #pragma unroll 1
-        for (int32_t c = 0; KIND != kWeight && c < q.cols; c += 32) {
-          uint32_t r[32];
-          __syncwarp();
-          tmem_ld32(from + c, r);
-          if (c + 32 >= q.cols) release();
-          {
-            // Lane pairs trade columns: an even lane keeps column x and gets its
-            // neighbour's, an odd one column x + 1, so that each has two adjacent
-            // elements of a row. 32 whole rows go out through shared memory as one
-            // copy, the last rows of an expert by the lanes themselves.
-            const bool odd = lane & 1;
-            const int32_t n = q.cols - c, i2 = i & ~1;
-            uint32_t p[16];
+      for (int32_t c = 0; KIND != kWeight && c < q.cols; c += 32) {
+        uint32_t r[32];
+        __syncwarp();
+        tmem_ld32(from + c, r);
+        if (c + 32 >= q.cols) release();
+        {
+          // Lane pairs trade columns: an even lane keeps column x and gets its
+          // neighbour's, an odd one column x + 1, so that each has two adjacent
+          // elements of a row. 32 whole rows go out through shared memory as one
+          // copy, the last rows of an expert by the lanes themselves.
+          const bool odd = lane & 1;
+          const int32_t n = q.cols - c, i2 = i & ~1;
+          uint32_t p[16];
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            const uint32_t give = odd ? r[x] : r[x + 1];
+            const uint32_t got = __shfl_xor_sync(~0u, give, 1);
+            p[x / 2] = odd ? pack_bf16(__uint_as_float(got), __uint_as_float(r[x + 1]))
+                           : pack_bf16(__uint_as_float(r[x]), __uint_as_float(got));
+          }
+          if (n >= 32) {
+            const uint32_t to = out0 + (uint32_t)quarter * kXOut + (turn++ & 1u) * (kXOut / 2);
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            __syncwarp();
+            const uint32_t mine = to + (odd ? 64u : 0u) + (uint32_t)(lane >> 1) * 4u;
+#pragma unroll
+            for (int x = 0; x < 16; ++x)
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(mine + (uint32_t)x * 128u), "r"(p[x]) : "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              if (i < g.lanes)
+                asm volatile(
+                    "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                        reinterpret_cast<uint64_t>(&maps.out)),
+                    "r"(i), "r"(q.col0 + c), "r"(0), "r"(to)
+                    : "memory");
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+          } else {
+            uint16_t* to = g.out + (int64_t)(q.col0 + c + (odd ? 1 : 0)) * g.ld + i2;
 #pragma unroll
             for (int x = 0; x < 32; x += 2) {
-              const uint32_t give = odd ? r[x] : r[x + 1];
-              const uint32_t got = __shfl_xor_sync(~0u, give, 1);
-              p[x / 2] = odd ? pack_bf16(__uint_as_float(got), __uint_as_float(r[x + 1]))
-                             : pack_bf16(__uint_as_float(r[x]), __uint_as_float(got));
-            }
-            if (n >= 32) {
-              const uint32_t to = out0 + (uint32_t)quarter * kXOut + (turn++ & 1u) * (kXOut / 2);
-              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-              __syncwarp();
-              const uint32_t mine = to + (odd ? 64u : 0u) + (uint32_t)(lane >> 1) * 4u;
-#pragma unroll
-              for (int x = 0; x < 16; ++x)
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(mine + (uint32_t)x * 128u), "r"(p[x]) : "memory");
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              __syncwarp();
-              if (lane == 0) {
-                if (i < g.lanes)
-                  asm volatile(
-                      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                          reinterpret_cast<uint64_t>(&maps.out)),
-                      "r"(i), "r"(q.col0 + c), "r"(0), "r"(to)
-                      : "memory");
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-              }
-            } else {
-              uint16_t* to = g.out + (int64_t)(q.col0 + c + (odd ? 1 : 0)) * g.ld + i2;
-#pragma unroll
-              for (int x = 0; x < 32; x += 2) {
-                if (x + (odd ? 1 : 0) < n) {
-                  if (i2 + 1 < g.lanes)
-                    *reinterpret_cast<uint32_t*>(to + (int64_t)x * g.ld) = p[x / 2];
-                  else if (i2 < g.lanes)
-                    to[(int64_t)x * g.ld] = (uint16_t)p[x / 2];
-                }
+              if (x + (odd ? 1 : 0) < n) {
+                if (i2 + 1 < g.lanes)
+                  *reinterpret_cast<uint32_t*>(to + (int64_t)x * g.ld) = p[x / 2];
+                else if (i2 < g.lanes)
+                  to[(int64_t)x * g.ld] = (uint16_t)p[x / 2];
               }
             }
           }
@@ -551,7 +563,7 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
       it += (uint32_t)((q.depth + kXDepth - 1) / kXDepth);
       if ((q.depth & 15) == 0) continue;
       const int s = (it - 1) % kXStages;
-      if (!warp_wait(own_bar(s), phases >> s & 1u, err, stop)) {
+      if (!warp_wait(own_bar(s), phases >> s & 1u, err, stop, g.limits.wait_ns)) {
         if (lane == 0) halt_cluster();
         break;
       }
@@ -568,8 +580,23 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
     }
   }
   tc_fence_before();
-  __syncthreads();
-  cluster_barrier();  // no CTA frees TMEM or leaves while the pair's products or copies may touch it
+  // no CTA frees TMEM or leaves while the pair's products or copies may touch it
+  pair_end(table.loaded, (uint32_t)rank, [&](uint32_t lead, uint32_t other) {
+    uint32_t k = 0;  // stage
+    int32_t e = 0;
+    for (int32_t t = cid; t < ntiles && k < other; t += ncid) {
+      const XTile q = tile_at<KIND>(g, table, t, e);
+      for (int32_t k0 = 0; k0 < q.depth && k < other; k0 += kXDepth, ++k) {
+        // (a mended stage's copies come to the other CTA's own barrier)
+        if (k < lead || mended_stage<KIND>(q, k0) || lane != 0) continue;
+        const uint32_t s = k % kXStages;
+        mbar_expect_tx(full_bar(s), stage_bytes(q));
+        if (KIND == kWeight) mbar_arrive(full_bar(s));
+        mbar_drain(full_bar(s), (k / kXStages) & 1u, global_ns() + kWaitNs, err);
+      }
+      __syncwarp();
+    }
+  });
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 2 * kXCols);

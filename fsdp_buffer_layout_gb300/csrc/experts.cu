@@ -151,6 +151,7 @@ vsf_status product(const Product& a, cudaStream_t st) {
   g.out = a.out;
   g.ld = a.out_ld;
   g.stride = a.out_stride;
+  g.limits = pair_limits();
   // (an upper bound: the rows' share among the experts is device memory)
   const int64_t tiles = KIND == kWeight ? a.E * g.lane_tiles * g.col_tiles
                                         : (a.rows / kXCols + std::min(a.E, a.rows)) * g.lane_tiles;
@@ -194,7 +195,25 @@ __global__ void __launch_bounds__(256)
 
 using namespace vsf;
 
+namespace {
+std::mutex pair_limits_mu;
+PairLimits pair_limits_now = {kWaitNs, {INT32_MAX, INT32_MAX}};
+}  // namespace
+
+PairLimits vsf::pair_limits() {
+  std::lock_guard<std::mutex> lock(pair_limits_mu);
+  return pair_limits_now;
+}
+
 extern "C" {
+
+vsf_status vsf_selftest_pair_waits(uint64_t limit_ns, int32_t lead_tiles, int32_t other_tiles) {
+  if (limit_ns > 1000000000ull) return fail(VSF_ERR_ARG, "vsf_selftest_pair_waits: limit above 1 s");
+  std::lock_guard<std::mutex> lock(pair_limits_mu);
+  pair_limits_now = {limit_ns > 0 ? limit_ns : kWaitNs,
+                     {lead_tiles < 0 ? INT32_MAX : lead_tiles, other_tiles < 0 ? INT32_MAX : other_tiles}};
+  return VSF_OK;
+}
 
 vsf_status vsf_expert_product(const uint16_t* x, int64_t rows, int64_t K, int64_t x_ld, const uint16_t* w,
                               int64_t E, int64_t N, int64_t w_ld, int64_t w_stride, const int32_t* starts,

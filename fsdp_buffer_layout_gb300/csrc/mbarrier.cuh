@@ -74,12 +74,12 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigne
 
 // The same at cluster scope (acquire), for barriers that peers arrive on.
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, unsigned* err,
-                                                  volatile uint32_t* stop) {
+                                                  volatile uint32_t* stop, uint64_t limit_ns = kWaitNs) {
   if (mbar_try_cluster(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   while (*stop == 0u) {
     if (mbar_try_cluster(bar, parity)) return true;
-    if (global_ns() - t0 > kWaitNs) {
+    if (global_ns() - t0 > limit_ns) {
       *stop = 1u;
       atomicOr(err, 2u);
       return false;

@@ -502,6 +502,7 @@ vsf_status ns_gemm(bool a_mn, bool b_mn, bool sym, int64_t M, int64_t N, int64_t
   g.D = D;
   g.ldd = ldd;
   g.sd = sd;
+  g.limits = pair_limits();
   const int nblocks = (int)((N + kGemmBN - 1) / kGemmBN);
   {
     // work items of the tensor-core kernel: 256 x 256 output tiles (one per

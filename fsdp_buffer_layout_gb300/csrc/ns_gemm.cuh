@@ -49,8 +49,8 @@
 //               the MMAs of the next.
 // Every wait is bounded (mbarrier.cuh): a broken pipeline sets bit 1 of the
 // device error word and stops both CTAs of the pair; the leader waits for
-// the pair's copies and its MMAs before exit, and the pair synchronises
-// before TMEM is freed. A pair whose two TMEM allocations differ in address
+// the pair's copies (pair_end) and its MMAs before exit, and the pair
+// synchronises before TMEM is freed. A pair whose two TMEM allocations differ in address
 // (the leader's MMAs write both at the leader's) sets bit 3 and computes
 // nothing.
 
@@ -78,6 +78,7 @@ struct NsGemmArgs {
   int64_t ldd, sd;
   int tiles_per_matrix;  // 256 x 256 output tiles per matrix
   int mgroups;           // 256-row groups per matrix
+  PairLimits limits;
 };
 
 __device__ __forceinline__ int imin(int a, int b) { return a < b ? a : b; }
@@ -123,6 +124,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const uint32_t done_bar = bar0 + 8u * (2 * kGemmStages + 4);
   __shared__ uint32_t tmem_slot;
   __shared__ uint32_t stop_flag;
+  __shared__ uint32_t loaded[2];  // stages that each CTA of the pair has loaded (pair_end)
   volatile uint32_t* stop = &stop_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
@@ -131,7 +133,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   constexpr uint16_t kBoth = 3;
 
   if (threadIdx.x == 0) {
-    stop_flag = 0u;
+    stop_flag = loaded[0] = loaded[1] = 0u;
     for (int s = 0; s < kGemmStages; ++s) {
       mbar_init(full_bar(s), 1);   // the leader's producer posts both CTAs' bytes
       mbar_init(empty_bar(s), 1);  // the leader's MMA commit
@@ -168,15 +170,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (lane == 0 && *stop == 0u) {
       // ---------------- producer (both CTAs): this CTA's opA and opB rows
       uint32_t it = 0;
+      const int end = last_tile(g.limits, leader, ntiles, cid, ncid);
       bool halted = false;
-      for (int t = cid; t < ntiles && !halted; t += ncid) {
+      for (int t = cid; t < end && !halted; t += ncid) {
         int b, m0, n0;
         gemm_tile(g, SYM, t, rank, b, m0, n0);
         const int nb0 = n0 + rank * (kGemmBN / 2);  // this CTA's opB rows
         for (int kb = 0; kb < KB; ++kb) {
           const int s = it % kGemmStages;
           const uint32_t ph = (it / kGemmStages) & 1u;
-          if (!mbar_wait(empty_bar(s), ph ^ 1u, err, stop)) {
+          if (!mbar_wait(empty_bar(s), ph ^ 1u, err, stop, g.limits.wait_ns)) {
             halted = true;
             halt_cluster();
             break;
@@ -201,7 +204,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
       }
       // the leader sees every copy of both CTAs land; the follower's copies
-      // are covered by the leader's wait and the final cluster barrier
+      // are covered by the leader's wait and pair_end
+      pair_tell(loaded, (uint32_t)rank, it);
       if (leader) {
         const uint64_t deadline = global_ns() + kWaitNs;
         for (int s = 0; s < kGemmStages; ++s) {
@@ -222,7 +226,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       for (int t = cid; t < ntiles && !halted; t += ncid, ++lt) {
         const int buf = lt & 1;
         const uint32_t tph = ((uint32_t)(lt >> 1) & 1u) ^ 1u;
-        if (!mbar_wait_cluster(tempty_bar(buf), tph, err, stop)) {
+        if (!mbar_wait_cluster(tempty_bar(buf), tph, err, stop, g.limits.wait_ns)) {
           halt_cluster();
           break;
         }
@@ -230,7 +234,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const uint32_t d = tmem + (uint32_t)(buf * kGemmBN);
         for (int kb = 0; kb < KB; ++kb, ++it) {
           const int s = it % kGemmStages;
-          if (!mbar_wait(full_bar(s), (it / kGemmStages) & 1u, err, stop)) {
+          if (!mbar_wait(full_bar(s), (it / kGemmStages) & 1u, err, stop, g.limits.wait_ns)) {
             halted = true;
             halt_cluster();
             break;
@@ -255,7 +259,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     for (int t = cid; t < ntiles; t += ncid, ++lt) {
       const int buf = lt & 1;
       const uint32_t fph = (uint32_t)(lt >> 1) & 1u;
-      const bool ok = __all_sync(0xffffffffu, mbar_wait(tfull_bar(buf), fph, err, stop));
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(tfull_bar(buf), fph, err, stop, g.limits.wait_ns));
       tc_fence_after();
       if (ok) {
         int b, m0, n0;
@@ -328,8 +332,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
   }
   tc_fence_before();
-  __syncthreads();
-  cluster_barrier();  // no CTA frees TMEM or leaves while the pair's MMAs or copies may touch it
+  // no CTA frees TMEM or leaves while the pair's MMAs or copies may touch it
+  pair_end(loaded, (uint32_t)rank, [&](uint32_t lead, uint32_t other) {
+    for (uint32_t k = lead; lane == 0 && k < other; ++k) {
+      const int s = k % kGemmStages;
+      mbar_expect_tx(full_bar(s), kGemmStageBytes);
+      mbar_drain(full_bar(s), (k / kGemmStages) & 1u, global_ns() + kWaitNs, err);
+    }
+  });
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kGemmTmemCols);

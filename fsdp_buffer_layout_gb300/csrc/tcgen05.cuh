@@ -107,17 +107,46 @@ __device__ __forceinline__ uint32_t ld_peer_u32(uint32_t cluster_addr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
   return v;
 }
+__device__ __forceinline__ void st_peer_u32(uint32_t cluster_addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
 // Sets the stop flag at the same shared-memory offset in cluster rank `rank`.
 __device__ __forceinline__ void remote_stop(volatile uint32_t* stop, uint32_t rank) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
-                   peer_addr(smem_u32(const_cast<uint32_t*>(stop)), rank)),
-               "r"(1u)
-               : "memory");
+  st_peer_u32(peer_addr(smem_u32(const_cast<uint32_t*>(stop)), rank), 1u);
 }
 // Arrival on an mbarrier of the cluster (release at cluster scope).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
+}
+
+// How a pair ends whose waits have run out. Both CTAs' copies of a stage come to the
+// leader's barrier, and the leader waits for the stages that it has asked for. The other
+// CTA may have loaded up to a ring of stages more by the time it sees the stop flag: it
+// must not leave while those are in flight. So each CTA's producer tells both CTAs how
+// many stages it has loaded (`loaded`, two words, 0 at first), and behind the cluster
+// barrier that follows, the leader asks for what is missing and waits for it (bounded):
+// ask(lead, other), by its first warp, for the stages from `lead` on. Called by all
+// threads of both CTAs.
+__device__ __forceinline__ void pair_tell(uint32_t* loaded, uint32_t rank, uint32_t stages) {
+  loaded[rank] = stages;
+  st_peer_u32(peer_addr(smem_u32(loaded + rank), rank ^ 1u), stages);
+}
+// The end of the tiles that a CTA's producer loads: all, but for a self-test.
+__device__ __forceinline__ int32_t last_tile(const PairLimits& l, bool leader, int32_t tiles, int32_t first,
+                                             int32_t step) {
+  const int32_t n = leader ? l.tiles[0] : l.tiles[1];
+  return n >= (tiles - first) / step + 1 ? tiles : first + n * step;
+}
+template <typename Ask>
+__device__ __forceinline__ void pair_end(const uint32_t* loaded, uint32_t rank, Ask ask) {
+  __syncthreads();
+  cluster_barrier();
+  const uint32_t lead = loaded[0], other = loaded[1];
+  if (other <= lead) return;
+  if (rank == 0 && threadIdx.x < 32) ask(lead, other);
+  __syncwarp();
+  cluster_barrier();
 }
 
 // Shared-memory matrix descriptor of tcgen05 (128-byte swizzle): start

@@ -39,6 +39,15 @@ constexpr int kTmaNarrowWarps = 4;
 constexpr int64_t kTmaNarrowMaxUnit = 48 * 1024;
 constexpr int tma_chunk_elems(int warps) { return warps * 32 * 8 * kTmaGroups; }
 
+// Limits of the kernels that run on pairs of CTAs (ns_gemm.cuh, expert_gemm.cuh): of
+// one wait, and of the tiles that the leading and the other CTA of a pair load. The
+// waits' own limit and all tiles, unless vsf_selftest_pair_waits has set others.
+struct PairLimits {
+  uint64_t wait_ns;
+  int32_t tiles[2];
+};
+PairLimits pair_limits();
+
 // One quantisation block as the kernels see it: a row-major region.
 struct QBlock {
   int64_t base;    // buffer element of the first element

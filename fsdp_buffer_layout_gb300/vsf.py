@@ -125,6 +125,8 @@ def lib():
             L.vsf_pack.argtypes = [vp, P(vp), i32, vp, vp]
             L.vsf_selftest_wait_timeout.restype = st
             L.vsf_selftest_wait_timeout.argtypes = [vp, ctypes.c_uint64, vp]
+            L.vsf_selftest_pair_waits.restype = st
+            L.vsf_selftest_pair_waits.argtypes = [ctypes.c_uint64, ctypes.c_int32, ctypes.c_int32]
             L.vsf_device_copy.restype = st
             L.vsf_device_copy.argtypes = [vp, vp, ctypes.c_size_t, vp]
             L.vsf_ns_gemm.restype = st
@@ -281,6 +283,10 @@ def vsf_plan_deserialize(data: bytes) -> int:
 
 def vsf_selftest_wait_timeout(d_err: int, limit_ns: int, stream: int) -> None:
     _check(lib().vsf_selftest_wait_timeout(d_err, limit_ns, stream))
+
+
+def vsf_selftest_pair_waits(limit_ns: int = 0, lead_tiles: int = -1, other_tiles: int = -1) -> None:
+    _check(lib().vsf_selftest_pair_waits(limit_ns, lead_tiles, other_tiles))
 
 
 def vsf_ns_gemm(a_mn: bool, b_mn: bool, sym: bool, M: int, N: int, K: int, batch: int,

@@ -422,6 +422,15 @@ vsf_status vsf_ns_gemm(int32_t a_mn, int32_t b_mn, int32_t sym, int64_t M, int64
  * 1 s), VSF_ERR_CUDA. */
 vsf_status vsf_selftest_wait_timeout(unsigned* d_err, uint64_t limit_ns, void* stream);
 
+/* Self-test of the waits of the kernels that run on pairs of CTAs
+ * (vsf_ns_gemm, the experts' products): for the calls that this process makes
+ * from now on, the limit of one wait (at most 1 s; 0: the normal 2 s), and how many
+ * of its tiles the leading and the other CTA of each pair load (negative: all), so
+ * that the waits for others run out. Such a call sets bit 1 of its error word and
+ * ends, with no result, within a few limits (and 2 s, where the leading CTA's copies
+ * wait for the other's). (0, -1, -1) puts everything back. Errors: VSF_ERR_ARG. */
+vsf_status vsf_selftest_pair_waits(uint64_t limit_ns, int32_t lead_tiles, int32_t other_tiles);
+
 /* Group norm and scale WITHOUT any device allocation or workspace. The pages
  * have no counterpart: this entry point exists for callers that cannot
  * allocate device memory where they need the gradient norm, such as a hook

@@ -131,6 +131,13 @@ def test_overlaps_and_long_strides(call, args, changes):
         refuse(call, args, change, ARG)
 
 
+def test_wait_selftest_refuses_a_limit_above_one_second():
+    with pytest.raises(V.VsfError) as e:
+        V.vsf_selftest_pair_waits(1_000_000_001)
+    assert e.value.status == ARG
+    V.vsf_selftest_pair_waits()
+
+
 def test_no_rows_is_no_error():
     V.vsf_expert_product(**{**FORWARD, "rows": 0})
     V.vsf_expert_product_input_grad(**{**INPUT, "rows": 0})
