@@ -72,6 +72,29 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigne
   return false;
 }
 
+// The same for a wait that many steps of the CTA's producer may pass by: the limit
+// counts from the last change of `moved`, a shared word, that was seen.
+__device__ __forceinline__ bool mbar_wait_moving(uint32_t bar, uint32_t parity, unsigned* err,
+                                                 volatile uint32_t* stop, uint64_t limit_ns,
+                                                 const volatile uint32_t* moved) {
+  if (mbar_try(bar, parity)) return true;
+  uint64_t t0 = global_ns();
+  uint32_t seen = *moved;
+  while (*stop == 0u) {
+    if (mbar_try(bar, parity)) return true;
+    const uint32_t now = *moved;
+    if (now != seen) {
+      seen = now;
+      t0 = global_ns();
+    } else if (global_ns() - t0 > limit_ns) {
+      *stop = 1u;
+      atomicOr(err, 2u);
+      return false;
+    }
+  }
+  return false;
+}
+
 // The same at cluster scope (acquire), for barriers that peers arrive on.
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, unsigned* err,
                                                   volatile uint32_t* stop, uint64_t limit_ns = kWaitNs) {

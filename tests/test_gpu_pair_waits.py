@@ -81,3 +81,49 @@ def test_newton_schulz_products_that_stand_still(limits, lead, other):
     want = product(0)
     stalled(limits, lead, other, lambda: product(1))
     assert torch.equal(product(0), want) and err.tolist() == [0, 2]
+
+
+def signs(rows, width, seed):
+    """-1, 0 and 1: their products' sums are exact in fp32 up to 2^24 of them."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(-1, 2, (rows, width), device="cuda", generator=g).bfloat16()
+
+
+@pytest.mark.parametrize("counts,n,k,limit", [
+    ([(1 << 21) + 5], 64, 64, 2 * MS),               # a tile of 32769 stages, the last one mended
+    ([1 << 18, 37, 0, 21], 2048, 2048, MS // 2),     # long tiles in front of the mended ones
+    ([(1 << 20) + 16], 130, 70, MS)])
+def test_long_tiles_are_not_given_up(limits, counts, n, k, limit):
+    """A wait for a whole tile, or for the next mended stage, is longer than the limit
+    while stages go by: the limit counts from the last of them."""
+    from fsdp_buffer_layout_gb300.experts import ExpertLinear
+    rows, experts = sum(counts), len(counts)
+    starts = torch.tensor([sum(counts[:i]) for i in range(experts + 1)], dtype=torch.int32, device="cuda")
+    # rows start on 16-byte boundaries
+    x, d_y = (signs(rows, -(-w // 8) * 8, w + i)[:, :w] for i, w in enumerate((k, n)))
+    op = ExpertLinear(rows, experts, n, k)
+    op.backward_weight(d_y, x, starts)
+    limits(limit)
+    d_w = op.backward_weight(d_y, x, starts)
+    assert op.device_error() == 0
+    cuts = starts.tolist()
+    for e, (a, b) in enumerate(zip(cuts, cuts[1:])):
+        want = d_y[a:b].float().t() @ x[a:b].float()
+        assert torch.equal(d_w[e], want.bfloat16()), e
+
+
+def test_a_long_depth_is_not_given_up(limits):
+    """The same for the other products: 2^15 stages a tile."""
+    from fsdp_buffer_layout_gb300.experts import ExpertLinear
+    rows, depth = 40, 1 << 21
+    starts = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    x, w = signs(rows, depth, 1), signs(64, depth, 2)[None]
+    op = ExpertLinear(rows, 1, 64, depth, with_grad=False)
+    limits(2 * MS)
+    y = op.forward(x, w, starts)
+    assert op.device_error() == 0
+    assert torch.equal(y, (x.float() @ w[0].float().t()).bfloat16())
+    flip = ExpertLinear(rows, 1, depth, 64, with_grad=False)
+    out = torch.empty(rows, 64, dtype=torch.bfloat16, device="cuda")
+    d_x = flip.backward_input(x, w[0].t().contiguous()[None], starts, out=out)
+    assert flip.device_error() == 0 and torch.equal(d_x, y)
