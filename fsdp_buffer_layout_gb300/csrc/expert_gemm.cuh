@@ -100,7 +100,7 @@ struct ExpertArgs {
   int32_t depth;      // kForward, kInput: extent of r
   int32_t lane_tiles, col_tiles;
   uint16_t* out;
-  int64_t ld, stride; // of out's rows; kWeight: of its experts
+  int64_t ld;         // of out's rows
   PairLimits limits;
 };
 

@@ -150,7 +150,6 @@ vsf_status product(const Product& a, cudaStream_t st) {
   g.col_tiles = (int32_t)((a.K + kXCols - 1) / kXCols);
   g.out = a.out;
   g.ld = a.out_ld;
-  g.stride = a.out_stride;
   g.limits = pair_limits();
   // (an upper bound: the rows' share among the experts is device memory)
   const int64_t tiles = KIND == kWeight ? a.E * g.lane_tiles * g.col_tiles

@@ -614,13 +614,17 @@ cudaError_t preference(const RowsArg& a, const PairIn& p, float* stats, float* l
 // where the warps would not all get one, longer where a row would have over 32 (128).
 constexpr int64_t kScoreWarps = kSms * kPartCtas * (kScoreThreads / 32);
 template <typename T>
+int32_t score_spans(int64_t V) {
+  return (int32_t)std::max<int64_t>(1, (V / Vec<T>::n + 31) / 32);
+}
+template <typename T>
 ScoreCut score_cut(int64_t tokens, int64_t V) {
+  const int32_t spans = score_spans<T>(V);
   ScoreCut c = {};
-  c.spans = (int32_t)std::max<int64_t>(1, (V / Vec<T>::n + 31) / 32);
   c.piece = 2;
-  while (c.piece < 4 && tokens * c.spans > (kScoreWarps << (c.piece + 1))) ++c.piece;
-  while (((c.spans - 1) >> c.piece) + 1 > (c.piece < 4 ? 128 : 32)) ++c.piece;
-  c.pieces = ((c.spans - 1) >> c.piece) + 1;
+  while (c.piece < 4 && tokens * spans > (kScoreWarps << (c.piece + 1))) ++c.piece;
+  while (((spans - 1) >> c.piece) + 1 > (c.piece < 4 ? 128 : 32)) ++c.piece;
+  c.pieces = ((spans - 1) >> c.piece) + 1;
   return c;
 }
 
@@ -631,7 +635,7 @@ struct ScoreWs {
     auto cut = [&](int64_t t) {
       return dtype == VSF_BF16 ? score_cut<uint16_t>(t, V) : score_cut<float>(t, V);
     };
-    const int64_t spans = cut(0).spans;
+    const int64_t spans = dtype == VSF_BF16 ? score_spans<uint16_t>(V) : score_spans<float>(V);
     int64_t most = 0;
     for (const int64_t t : {std::min(tokens, kScoreWarps * 8 / spans), std::min(tokens, kScoreWarps * 16 / spans), tokens})
       most = std::max(most, t * cut(t).pieces);
@@ -642,9 +646,10 @@ struct ScoreWs {
 // For a CTA a row, which has room for 32 pieces.
 template <typename T>
 ScoreCut score_cut_one(int64_t V) {
+  const int32_t spans = score_spans<T>(V);
   ScoreCut c = score_cut<T>(0, V);
-  while (((c.spans - 1) >> c.piece) + 1 > 32) ++c.piece;
-  c.pieces = ((c.spans - 1) >> c.piece) + 1;
+  while (((spans - 1) >> c.piece) + 1 > 32) ++c.piece;
+  c.pieces = ((spans - 1) >> c.piece) + 1;
   return c;
 }
 

@@ -34,7 +34,8 @@ constexpr uint32_t kErrShared = 32u;  // error-word bit: a router on a loss's wo
 
 namespace obj {
 
-constexpr int kSms = 152;  // of a GB300: no grid here has more CTAs than run at a time
+constexpr int kSms = 152;  // of a GB300: no grid here has more CTAs than run at a time, but
+                           // for the kernels that take a row of scores a CTA
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }

@@ -47,11 +47,11 @@ constexpr int kPartCtas = 3;         // an SM
 constexpr int kScoreBatch = 4;       // vectors of a lane on their way at a time
 constexpr int kMaxTop = 32;
 
-// How rows are cut: `spans` of 32 vectors, pieces of 2^piece spans. The elements in
+// How rows are cut: spans of 32 vectors, `pieces` of 2^piece spans. The elements in
 // front of a row's first 16-byte boundary belong to the first piece, those behind
 // the last vector to the last.
 struct ScoreCut {
-  int32_t spans, piece, pieces;
+  int32_t piece, pieces;
 };
 
 template <typename T>
