@@ -51,21 +51,36 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
   return r != 0;
 }
+// What is left of a wait whose first try failed, out of line: a call of a few tiles waits
+// for its code as well (13 experts of some 200 rows, 1001 x 523, the three products: 41.4
+// us, with a copy at each wait 42.1).
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, unsigned* err, volatile uint32_t* stop,
+                                     uint64_t limit_ns) {
+  return mbar_wait_rest(bar, parity, err, stop, limit_ns);
+}
+__device__ __noinline__ bool wait_on_cluster(uint32_t bar, uint32_t parity, unsigned* err,
+                                             volatile uint32_t* stop, uint64_t limit_ns) {
+  return mbar_wait_rest_cluster(bar, parity, err, stop, limit_ns);
+}
+__device__ __noinline__ bool wait_on_moving(uint32_t bar, uint32_t parity, unsigned* err,
+                                            volatile uint32_t* stop, uint64_t limit_ns,
+                                            const volatile uint32_t* moved) {
+  return mbar_wait_rest_moving(bar, parity, err, stop, limit_ns, moved);
+}
 // The waits of a whole warp: all of its lanes go on, or none does.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned* err, volatile uint32_t* stop,
                                           uint64_t limit_ns) {
-  return __all_sync(~0u, mbar_wait(bar, parity, err, stop, limit_ns));
+  return __all_sync(~0u, mbar_try(bar, parity) || wait_on(bar, parity, err, stop, limit_ns));
 }
 __device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, unsigned* err,
                                                   volatile uint32_t* stop, uint64_t limit_ns) {
-  return __all_sync(~0u, mbar_wait_cluster(bar, parity, err, stop, limit_ns));
+  return __all_sync(~0u, mbar_try_cluster(bar, parity) || wait_on_cluster(bar, parity, err, stop, limit_ns));
 }
-
 // For a tile's end or the next mended stage: as long as the producer's stages go by.
 __device__ __forceinline__ bool warp_wait_moving(uint32_t bar, uint32_t parity, unsigned* err,
                                                  volatile uint32_t* stop, uint64_t limit_ns,
                                                  const volatile uint32_t* moved) {
-  return __all_sync(~0u, mbar_wait_moving(bar, parity, err, stop, limit_ns, moved));
+  return __all_sync(~0u, mbar_try(bar, parity) || wait_on_moving(bar, parity, err, stop, limit_ns, moved));
 }
 
 enum { kForward = 0, kInput = 1, kWeight = 2 };
@@ -85,7 +100,7 @@ struct XTable {
   int32_t start[kMaxGroups + 1];  // its first row
   uint32_t tmem, stop, moved;     // (moved: this CTA's producer, stages)
   int32_t most;                   // rows of a tile at most, 2^most (kForward, kInput)
-  uint32_t loaded[2];             // stages that each CTA of the pair has loaded (pair_end)
+  PairEnd end;
 };
 constexpr uint32_t kXOut = 4096;  // of each epilogue warp: 32 lanes x 64 columns, or two of 32 x 32
 constexpr uint32_t kXSmem =
@@ -210,7 +225,7 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
   constexpr uint16_t kBoth = 3;
 
   if (threadIdx.x == 0) {
-    table.stop = table.moved = table.loaded[0] = table.loaded[1] = 0u;
+    table.stop = table.moved = table.end.loaded = table.end.early = 0u;
     for (int s = 0; s < kXStages; ++s) {
       // kWeight: both CTAs' warps 6 arrive for a mended stage, the leader's producer twice
       // for others (by one of its warps 6 after the other: a row more or less an expert
@@ -367,7 +382,7 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
       // every copy lands before the CTA ends: the leader sees both CTAs' (the
       // follower's are covered by its wait and pair_end)
       if (one) {
-        pair_tell(table.loaded, (uint32_t)rank, it);
+        pair_loaded(table.end, it, leader && (halted || end < ntiles));
         const uint64_t deadline = global_ns() + kWaitNs;
         for (int s = 0; KIND == kWeight && s < kXStages; ++s)
           if (mended >> s & 1u) mbar_drain(own_bar(s), (phases >> s & 1u) ^ 1u, deadline, err);
@@ -597,7 +612,7 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
   }
   tc_fence_before();
   // no CTA frees TMEM or leaves while the pair's products or copies may touch it
-  pair_end(table.loaded, (uint32_t)rank, [&](uint32_t lead, uint32_t other) {
+  pair_end(table.end, leader, [&](uint32_t lead, uint32_t other) {
     uint32_t k = 0;  // stage
     int32_t e = 0;
     for (int32_t t = cid; t < ntiles && k < other; t += ncid) {

@@ -56,10 +56,9 @@ __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) 
 // Bounded wait for the phase of the given parity. Returns false at once if
 // the CTA's stop flag is set, or after limit_ns (kWaitNs unless given) of
 // wall-clock time (global timer), having then set the stop flag and bit 1 of
-// the error word.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigned* err,
-                                          volatile uint32_t* stop, uint64_t limit_ns = kWaitNs) {
-  if (mbar_try(bar, parity)) return true;
+// the error word. ..._rest: what is left of a wait whose first test has failed.
+__device__ __forceinline__ bool mbar_wait_rest(uint32_t bar, uint32_t parity, unsigned* err,
+                                               volatile uint32_t* stop, uint64_t limit_ns) {
   const uint64_t t0 = global_ns();
   while (*stop == 0u) {
     if (mbar_try(bar, parity)) return true;
@@ -72,12 +71,16 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigne
   return false;
 }
 
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigned* err,
+                                          volatile uint32_t* stop, uint64_t limit_ns = kWaitNs) {
+  return mbar_try(bar, parity) || mbar_wait_rest(bar, parity, err, stop, limit_ns);
+}
+
 // The same for a wait that many steps of the CTA's producer may pass by: the limit
 // counts from the last change of `moved`, a shared word, that was seen.
-__device__ __forceinline__ bool mbar_wait_moving(uint32_t bar, uint32_t parity, unsigned* err,
-                                                 volatile uint32_t* stop, uint64_t limit_ns,
-                                                 const volatile uint32_t* moved) {
-  if (mbar_try(bar, parity)) return true;
+__device__ __forceinline__ bool mbar_wait_rest_moving(uint32_t bar, uint32_t parity, unsigned* err,
+                                                      volatile uint32_t* stop, uint64_t limit_ns,
+                                                      const volatile uint32_t* moved) {
   uint64_t t0 = global_ns();
   uint32_t seen = *moved;
   while (*stop == 0u) {
@@ -96,9 +99,8 @@ __device__ __forceinline__ bool mbar_wait_moving(uint32_t bar, uint32_t parity, 
 }
 
 // The same at cluster scope (acquire), for barriers that peers arrive on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, unsigned* err,
-                                                  volatile uint32_t* stop, uint64_t limit_ns = kWaitNs) {
-  if (mbar_try_cluster(bar, parity)) return true;
+__device__ __forceinline__ bool mbar_wait_rest_cluster(uint32_t bar, uint32_t parity, unsigned* err,
+                                                       volatile uint32_t* stop, uint64_t limit_ns) {
   const uint64_t t0 = global_ns();
   while (*stop == 0u) {
     if (mbar_try_cluster(bar, parity)) return true;
@@ -109,6 +111,11 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
     }
   }
   return false;
+}
+
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, unsigned* err,
+                                                  volatile uint32_t* stop, uint64_t limit_ns = kWaitNs) {
+  return mbar_try_cluster(bar, parity) || mbar_wait_rest_cluster(bar, parity, err, stop, limit_ns);
 }
 
 // Wait for an issued copy to land, ignoring the stop flag, until the global

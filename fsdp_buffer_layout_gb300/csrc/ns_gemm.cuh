@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const uint32_t done_bar = bar0 + 8u * (2 * kGemmStages + 4);
   __shared__ uint32_t tmem_slot;
   __shared__ uint32_t stop_flag;
-  __shared__ uint32_t loaded[2];  // stages that each CTA of the pair has loaded (pair_end)
+  __shared__ PairEnd pair;
   volatile uint32_t* stop = &stop_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   constexpr uint16_t kBoth = 3;
 
   if (threadIdx.x == 0) {
-    stop_flag = loaded[0] = loaded[1] = 0u;
+    stop_flag = pair.loaded = pair.early = 0u;
     for (int s = 0; s < kGemmStages; ++s) {
       mbar_init(full_bar(s), 1);   // the leader's producer posts both CTAs' bytes
       mbar_init(empty_bar(s), 1);  // the leader's MMA commit
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
       // the leader sees every copy of both CTAs land; the follower's copies
       // are covered by the leader's wait and pair_end
-      pair_tell(loaded, (uint32_t)rank, it);
+      pair_loaded(pair, it, leader && (halted || end < ntiles));
       if (leader) {
         const uint64_t deadline = global_ns() + kWaitNs;
         for (int s = 0; s < kGemmStages; ++s) {
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
   tc_fence_before();
   // no CTA frees TMEM or leaves while the pair's MMAs or copies may touch it
-  pair_end(loaded, (uint32_t)rank, [&](uint32_t lead, uint32_t other) {
+  pair_end(pair, leader, [&](uint32_t lead, uint32_t other) {
     for (uint32_t k = lead; lane == 0 && k < other; ++k) {
       const int s = k % kGemmStages;
       mbar_expect_tx(full_bar(s), kGemmStageBytes);

@@ -123,14 +123,19 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
 // How a pair ends whose waits have run out. Both CTAs' copies of a stage come to the
 // leader's barrier, and the leader waits for the stages that it has asked for. The other
 // CTA may have loaded up to a ring of stages more by the time it sees the stop flag: it
-// must not leave while those are in flight. So each CTA's producer tells both CTAs how
-// many stages it has loaded (`loaded`, two words, 0 at first), and behind the cluster
-// barrier that follows, the leader asks for what is missing and waits for it (bounded):
-// ask(lead, other), by its first warp, for the stages from `lead` on. Called by all
-// threads of both CTAs.
-__device__ __forceinline__ void pair_tell(uint32_t* loaded, uint32_t rank, uint32_t stages) {
-  loaded[rank] = stages;
-  st_peer_u32(peer_addr(smem_u32(loaded + rank), rank ^ 1u), stages);
+// must not leave while those are in flight. So a leader whose producer ends early says so
+// to both CTAs, and behind the cluster barrier that follows it asks for what the other
+// one has loaded more and waits for it (bounded), before either leaves.
+struct PairEnd {
+  uint32_t loaded;  // stages that this CTA's producer has loaded
+  uint32_t early;   // the leader's has not loaded all of its tiles
+};
+__device__ __forceinline__ void pair_loaded(PairEnd& end, uint32_t stages, bool early) {
+  end.loaded = stages;
+  if (early) {
+    end.early = 1u;
+    st_peer_u32(peer_addr(smem_u32(&end.early), 1u), 1u);
+  }
 }
 // The end of the tiles that a CTA's producer loads: all, but for a self-test.
 __device__ __forceinline__ int32_t last_tile(const PairLimits& l, bool leader, int32_t tiles, int32_t first,
@@ -138,13 +143,14 @@ __device__ __forceinline__ int32_t last_tile(const PairLimits& l, bool leader, i
   const int32_t n = leader ? l.tiles[0] : l.tiles[1];
   return n >= (tiles - first) / step + 1 ? tiles : first + n * step;
 }
+// Called by all threads of both CTAs; ask(lead, other), by the leader's first warp: for
+// the stages from `lead` on.
 template <typename Ask>
-__device__ __forceinline__ void pair_end(const uint32_t* loaded, uint32_t rank, Ask ask) {
+__device__ __forceinline__ void pair_end(const PairEnd& end, bool leader, Ask ask) {
   __syncthreads();
   cluster_barrier();
-  const uint32_t lead = loaded[0], other = loaded[1];
-  if (other <= lead) return;
-  if (rank == 0 && threadIdx.x < 32) ask(lead, other);
+  if (*const_cast<const volatile uint32_t*>(&end.early) == 0u) return;
+  if (leader && threadIdx.x < 32) ask(end.loaded, ld_peer_u32(peer_addr(smem_u32(&end.loaded), 1u)));
   __syncwarp();
   cluster_barrier();
 }
