@@ -9,10 +9,17 @@ ExpertLinear  the products of sorted rows with their experts' weights; the
 As for the objects of ``objectives``: an object owns its outputs, sized for the
 largest call; a call returns views of them, which the next call of the same
 object overwrites, on the object's stream, whose memory they are. Nothing is
-synchronised. Rows behind the last one that holds a choice are left as they
-were: zeros in a new object's outputs. Every output may also be given by the
-caller (`out` and its like), so that several micro-batches keep theirs. The
-formulas stand at the C functions in include/vsf.h.
+synchronised. Every output may also be given by the caller (`out` and its
+like), so that several micro-batches keep theirs. The formulas stand at the C
+functions in include/vsf.h.
+
+Rows behind the last one that holds a choice (rows from starts[-1] on) are left
+as they were, in the object's outputs and in given ones. The object's hold
+zeros there at first, and after that what earlier calls with more choices left:
+a call's result is the first starts[-1] rows alone. The calls here go by that.
+What a program computes over whole arrays in between (a bias' gradient
+d_y.sum(0), a largest absolute value) has to leave the others out, for instance
+by torch.where(source[:, None] >= 0, d_y, 0), which waits for nothing.
 """
 from __future__ import annotations
 

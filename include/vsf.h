@@ -648,7 +648,8 @@ vsf_status vsf_route_grad(const void* logits, int32_t dtype, int64_t T, int64_t 
  * Common to the calls below: choice c = t*top_k + j is the j-th expert of token t
  * (idx as vsf_route writes it: int32[T*top_k], anything outside [0, E) is no
  * choice). "Rows" are arrays of T*top_k rows, of which the first starts[E] hold a
- * choice each; the others are neither read nor written. T <= 2^23, top_k <= 32,
+ * choice each; the others are neither read nor written: an array used again still
+ * has rows of earlier calls there. T <= 2^23, top_k <= 32,
  * E <= 512. Strides (ld) count elements, up to 2^39 (rows times stride: 2^58).
  * Arrays may be columns of one another's rows (the same stride). Sums are fp32 in a
  * fixed order, rounded once to the output's type: equal inputs give equal bits.

@@ -438,6 +438,39 @@ def test_columns_of_shared_rows(dtype, width, gap):
     assert (np.abs(host(d_gates) - want_gates) <= (width + 1) * 2.0**-24 * size * 1.01).all()
 
 
+def test_rows_of_earlier_calls():
+    """A call with fewer choices leaves the rows behind its last one as they were, in
+    the object's outputs and in given ones; what `source` marks is the result."""
+    from fsdp_buffer_layout_gb300.experts import Dispatch, ExpertLinear
+    rng = np.random.default_rng(21)
+    tokens, experts, k, width = 90, 5, 3, 72
+    x, d_out = (strided(tokens, width, 0, 0, BF16, rng) for _ in range(2))
+    y, given = (strided(tokens * k, width, 0, 0, BF16, rng) for _ in range(2))
+    w = strided(experts * width, width, 0, 0, BF16, rng).view(experts, width, width)
+    gates = torch.from_numpy(rng.random(size=(tokens, k)).astype(np.float32)).cuda()
+    idx = [choices(rng, tokens, experts, k, masked) for masked in (False, True)]
+
+    def run(to, layer, idx):
+        starts, source, _ = to.sort(idx)
+        rows = to.gather(x)
+        out = (rows, to.combine_backward(d_out, y, gates)[0], layer.forward(rows, w, starts),
+               layer.backward_input(y, w, starts), to.gather(x, out=given))
+        return int(starts[-1]), source, out
+
+    made = [(Dispatch(tokens, experts, k, width), ExpertLinear(tokens * k, experts, width, width))
+            for _ in range(2)]
+    full, _, out = run(*made[0], idx[0])
+    before = [t.clone() for t in out]
+    n, source, out = run(*made[0], idx[1])
+    _, _, want = run(*made[1], idx[1])
+    assert full == tokens * k > n
+    for got, old, new in zip(out, before, want):
+        assert torch.equal(got[n:], old[n:]) and got[n:].any()
+        kept = torch.where(source[:, None] >= 0, got, 0)
+        assert torch.equal(kept[:n], new[:n]) and not kept[n:].any()
+        assert torch.equal(kept.float().sum(0), torch.where(source[:, None] >= 0, new, 0).float().sum(0))
+
+
 def test_a_single_row_among_others():
     """One token's row in a column block of the array whose other columns are
     written: a single row has no stride, and shares no byte with them."""
