@@ -39,6 +39,13 @@
 // weight gradient 255 us, 4.2 TB/s written (torch's fill of as much: 4.0). Bound by a
 // call's fixed 5 us, a tile's first loads and its epilogue (2 us) where there are few
 // tiles of little depth.
+// A tile sums its whole depth on one pair of SMs, 0.2 to 0.3 us for 64 of r, whatever
+// number of pairs is idle, and has 256 lanes, however few the weights' side has. So few
+// tiles of a long depth take several times their bytes' time: the weight gradients of 4
+// experts of 8192 rows, 256 x 256, 41 us (5 us of bytes), of 2 of 65536 rows, 64 x 64, 179
+// (5); forward of 4 of 64 rows, 8192 deep to 256 lanes, 28 (3). And a narrow side pays for
+// 256 lanes: 8 experts of 4096 rows, forward 64 deep to 4096 lanes 103 us, its input
+// gradient with 64 lanes and 4096 deep 56 (41 us of bytes each).
 // Measured and not kept: eight epilogue warps (2700 rows of 13 experts, 1001 x 523, 10.1
 // us instead of 10.8, but 626 instead of 614 for 32768 rows, 5760 x 2880); the
 // accumulator's next columns read while the ones before are stored, which needs the

@@ -699,7 +699,9 @@ vsf_status vsf_expert_combine_grad(const void* d_out, int32_t dtype, int64_t T, 
  * Rows behind starts[E] are neither read into a result nor written. Every array's
  * rows start on 16-byte boundaries: pointers aligned to 16 bytes, strides
  * multiples of 8 elements (VSF_ERR_ALIGN); N and K may be anything up to 2^24.
- * rows <= 2^28. d_err: a device word in which a bounded wait that runs out sets
+ * rows <= 2^28. bf16 only: d_W is rounded to it and written over what is there (add
+ * the gradients of several calls with vsf_group_add, into fp32 if need be).
+ * d_err: a device word in which a bounded wait that runs out sets
  * bit 1 (value 2; results are then not to be trusted). */
 vsf_status vsf_expert_product(const uint16_t* x, int64_t rows, int64_t K, int64_t x_ld,
                               const uint16_t* w, int64_t E, int64_t N, int64_t w_ld,
