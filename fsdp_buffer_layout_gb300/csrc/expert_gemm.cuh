@@ -122,7 +122,7 @@ struct ExpertArgs {
   int32_t depth;      // kForward, kInput: extent of r
   int32_t lane_tiles, col_tiles;
   uint16_t* out;
-  int64_t ld;         // of out's rows
+  int64_t ld, stride; // of out's rows; kWeight: of its experts
   PairLimits limits;
 };
 
@@ -206,6 +206,10 @@ constexpr int kXThreads = KIND == kWeight ? 224 : 192;
 // Tensor maps: the lanes' operand; the columns' operand, in boxes of 16, 32, 64 and
 // 128 rows (kWeight: of 64 x 64, the first alone); the output, in boxes of 32 rows of
 // 32 elements (kWeight: of 64).
+// A copy to memory leaves out what lies behind a map's width in whole pieces of 16 bytes
+// only: of the last piece it writes all. So the output's map ends at its last whole
+// piece, whole_pieces(width), and the up to seven elements behind it are stored by the lanes.
+__host__ __device__ constexpr int32_t whole_pieces(int32_t width) { return width & ~7; }
 struct XMaps {
   CUtensorMap lanes, cols[4], out;
 };
@@ -526,13 +530,24 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
                          : "memory");
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if (lane == 0 && q.lane0 + rank * 128 + 32 * quarter < g.lanes) {
+          const int32_t whole = whole_pieces(g.cols), at = whole - (q.col0 + c);  // (see whole_pieces)
+          if (lane == 0 && at > 0 && q.lane0 + rank * 128 + 32 * quarter < g.lanes) {
             asm volatile(
                 "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
                     reinterpret_cast<uint64_t>(&maps.out)),
                 "r"(q.col0 + c), "r"(q.lane0 + rank * 128 + 32 * quarter), "r"(q.e), "r"(to)
                 : "memory");
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+          if (whole != g.cols && at < 64 && i < g.lanes) {
+            uint16_t* rest = g.out + q.e * g.stride + i * g.ld + whole;
+            for (int32_t x = 0; x < g.cols - whole; ++x) {
+              uint16_t v;
+              asm volatile("ld.shared.u16 %0, [%1];"
+                           : "=h"(v)
+                           : "r"(mine + (uint32_t)((at / 8 ^ (lane & 7)) * 16 + 2 * x)));
+              rest[x] = v;
+            }
           }
         }
       }
@@ -546,9 +561,10 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
           // Lane pairs trade columns: an even lane keeps column x and gets its
           // neighbour's, an odd one column x + 1, so that each has two adjacent
           // elements of a row. 32 whole rows go out through shared memory as one
-          // copy, the last rows of an expert by the lanes themselves.
+          // copy, the last rows of an expert by the lanes themselves, and what is
+          // left behind the last 8 lanes of all.
           const bool odd = lane & 1;
-          const int32_t n = q.cols - c, i2 = i & ~1;
+          const int32_t n = q.cols - c, i2 = i & ~1, whole = whole_pieces(g.lanes);  // (see whole_pieces)
           uint32_t p[16];
 #pragma unroll
           for (int x = 0; x < 32; x += 2) {
@@ -568,7 +584,7 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
-              if (i < g.lanes)
+              if (i < whole)
                 asm volatile(
                     "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
                         reinterpret_cast<uint64_t>(&maps.out)),
@@ -576,14 +592,15 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
                     : "memory");
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
-          } else {
+          }
+          if ((n < 32 || i2 >= whole) && i2 < g.lanes) {
             uint16_t* to = g.out + (int64_t)(q.col0 + c + (odd ? 1 : 0)) * g.ld + i2;
 #pragma unroll
             for (int x = 0; x < 32; x += 2) {
               if (x + (odd ? 1 : 0) < n) {
                 if (i2 + 1 < g.lanes)
                   *reinterpret_cast<uint32_t*>(to + (int64_t)x * g.ld) = p[x / 2];
-                else if (i2 < g.lanes)
+                else
                   to[(int64_t)x * g.ld] = (uint16_t)p[x / 2];
               }
             }

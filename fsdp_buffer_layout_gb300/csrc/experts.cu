@@ -81,7 +81,8 @@ vsf_status check(int kind, const Product& a) {
 
 // Tensor map over [batch, rows, width] (row stride ld, batch stride bs, in
 // elements), boxes of 64 elements x box_rows rows, 128-byte swizzle (or of 32
-// elements, not swizzled); copies outside read zeros and write nothing.
+// elements, not swizzled); copies outside read zeros and write nothing, but for what is
+// left of the 16 bytes that hold a row's last element.
 vsf_status operand_map(CUtensorMap* map, const char* who, const uint16_t* p, int64_t width, int64_t rows,
                        int64_t batch, int64_t ld, int64_t bs, int box_rows, int box_width = 64) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = gemm_map_encoder();
@@ -150,6 +151,7 @@ vsf_status product(const Product& a, cudaStream_t st) {
   g.col_tiles = (int32_t)((a.K + kXCols - 1) / kXCols);
   g.out = a.out;
   g.ld = a.out_ld;
+  g.stride = a.out_stride;
   g.limits = pair_limits();
   // (an upper bound: the rows' share among the experts is device memory)
   const int64_t tiles = KIND == kWeight ? a.E * g.lane_tiles * g.col_tiles
@@ -158,17 +160,19 @@ vsf_status product(const Product& a, cudaStream_t st) {
   if (tiles > INT32_MAX / 4) return fail(VSF_ERR_ARG, std::string(a.who) + ": too many tiles");
   XMaps m;
   vsf_status s;
+  // (a map has to have a width; where the output has no whole piece none is copied)
+  const int64_t out_width = std::max<int64_t>(8, whole_pieces((int32_t)(KIND == kWeight ? a.K : lanes)));
   if (KIND == kWeight) {
     s = operand_map(&m.lanes, a.who, a.rows_in, a.N, a.rows, 1, a.rows_ld, 0, 64);
     if (s == VSF_OK) s = operand_map(&m.cols[0], a.who, a.other, a.K, a.rows, 1, a.other_ld, 0, 64);
-    if (s == VSF_OK) s = operand_map(&m.out, a.who, a.out, a.K, a.N, a.E, a.out_ld, a.out_stride, 32);
+    if (s == VSF_OK) s = operand_map(&m.out, a.who, a.out, out_width, a.N, a.E, a.out_ld, a.out_stride, 32);
     m.cols[1] = m.cols[2] = m.cols[3] = m.cols[0];
   } else {
     s = operand_map(&m.lanes, a.who, a.other, a.K, a.N, a.E, a.other_ld, a.other_stride,
                     KIND == kForward ? 128 : 64);
     for (int i = 0; i < 4 && s == VSF_OK; ++i)
       s = operand_map(&m.cols[i], a.who, a.rows_in, g.depth, a.rows, 1, a.rows_ld, 0, 16 << i);
-    if (s == VSF_OK) s = operand_map(&m.out, a.who, a.out, lanes, a.rows, 1, a.out_ld, 0, 32, 32);
+    if (s == VSF_OK) s = operand_map(&m.out, a.who, a.out, out_width, a.rows, 1, a.out_ld, 0, 32, 32);
   }
   if (s != VSF_OK) return s;
   cudaError_t e = cudaSuccess;

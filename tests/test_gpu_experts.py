@@ -438,6 +438,54 @@ def test_columns_of_shared_rows(dtype, width, gap):
     assert (np.abs(host(d_gates) - want_gates) <= (width + 1) * 2.0**-24 * size * 1.01).all()
 
 
+@pytest.mark.parametrize("counts,n,k", [
+    ([40, 0, 33, 70], 3, 5), ([64, 32, 96], 94, 523), ([100, 32], 1001, 257), ([70, 64], 7, 9),
+    ([33, 64, 31], 130, 70), ([300, 257], 263, 1030), ([64], 1, 1), ([32, 64], 8, 16), ([128], 511, 383)])
+def test_products_stay_inside_their_rows(counts, n, k):
+    """What lies beside and behind the outputs' rows keeps its values, whatever the
+    widths are; NaN beside and behind the inputs' rows does not matter."""
+    from fsdp_buffer_layout_gb300.experts import ExpertLinear
+    g = torch.Generator(device="cuda").manual_seed(n)
+    rows, experts = sum(counts) + 4, len(counts)
+    starts = torch.tensor(np.cumsum([0] + counts), dtype=torch.int32, device="cuda")
+
+    def among(rows, width, fill):
+        """An array of `width` in rows 16 to 23 elements longer, 8 elements into a buffer."""
+        ld = -(-width // 8) * 8 + 16
+        buf = fill(8 + rows * ld + 24)
+        return buf, buf.as_strided((rows, width), (ld, 1), 8)
+
+    def noise(size):
+        return torch.randn(size, device="cuda", generator=g).bfloat16()
+
+    def nan(size):
+        return torch.full((size,), float("nan"), dtype=BF16, device="cuda")
+
+    x, d_y, w = (among(r, c, nan)[1] for r, c in ((rows, k), (rows, n), (experts * (n + 1), k)))
+    for t in (x[:-4], d_y[:-4], w):
+        t.copy_(torch.randn(t.shape, device="cuda", generator=g))
+    w = w.as_strided((experts, n, k), ((n + 1) * w.stride(0), w.stride(0), 1), w.storage_offset())
+    op = ExpertLinear(rows, experts, n, k)
+    want = [t.clone() for t in (op.forward(x, w, starts), op.backward_input(d_y, w, starts),
+                                op.backward_weight(d_y, x, starts))]
+    assert all(torch.isfinite(t).all() for t in want)
+    used = sum(counts)
+    for call, args, new, height, width in ((op.forward, (x, w, starts), want[0], rows, n),
+                                           (op.backward_input, (d_y, w, starts), want[1], rows, k)):
+        buf, out = among(height, width, noise)
+        before = buf.clone()
+        assert call(*args, out=out) is out
+        before.as_strided(out.shape, out.stride(), out.storage_offset())[:used] = new[:used]
+        assert torch.equal(buf, before)
+    buf, flat = among(experts * (n + 1), k, noise)
+    shape, stride = (experts, n, k), ((n + 1) * flat.stride(0), flat.stride(0), 1)
+    before, out = buf.clone(), buf.as_strided(shape, stride, 8)
+    op.backward_weight(d_y, x, starts, out=out)
+    before.as_strided(shape, stride, 8).copy_(want[2])
+    assert torch.equal(buf, before)
+    assert op.device_error() == 0
+
+
 def test_rows_of_earlier_calls():
     """A call with fewer choices leaves the rows behind its last one as they were, in
     the object's outputs and in given ones; what `source` marks is the result."""
