@@ -208,8 +208,27 @@ constexpr int kXThreads = KIND == kWeight ? 224 : 192;
 // 32 elements (kWeight: of 64).
 // A copy to memory leaves out what lies behind a map's width in whole pieces of 16 bytes
 // only: of the last piece it writes all. So the output's map ends at its last whole
-// piece, whole_pieces(width), and the up to seven elements behind it are stored by the lanes.
+// piece, whole_pieces(width), and the up to seven elements behind it are stored by the
+// lanes, a row each (13 experts of some 200 rows, 1001 x 523, the three products: 42.4 us;
+// by two lanes of 16 rows, or an element at a time, 47.0).
 __host__ __device__ constexpr int32_t whole_pieces(int32_t width) { return width & ~7; }
+// n elements, 1 to 7, of a piece in shared memory.
+__device__ __forceinline__ void store_rest(uint16_t* to, uint32_t from, int32_t n) {
+  uint32_t a, b, c, d;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(from));
+  if (n & 4) {
+    *reinterpret_cast<uint2*>(to) = make_uint2(a, b);
+    to += 4;
+    a = c;
+    b = d;
+  }
+  if (n & 2) {
+    *reinterpret_cast<uint32_t*>(to) = a;
+    to += 2;
+    a = b;
+  }
+  if (n & 1) *to = (uint16_t)a;
+}
 struct XMaps {
   CUtensorMap lanes, cols[4], out;
 };
@@ -539,16 +558,9 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
                 : "memory");
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
-          if (whole != g.cols && at < 64 && i < g.lanes) {
-            uint16_t* rest = g.out + q.e * g.stride + i * g.ld + whole;
-            for (int32_t x = 0; x < g.cols - whole; ++x) {
-              uint16_t v;
-              asm volatile("ld.shared.u16 %0, [%1];"
-                           : "=h"(v)
-                           : "r"(mine + (uint32_t)((at / 8 ^ (lane & 7)) * 16 + 2 * x)));
-              rest[x] = v;
-            }
-          }
+          if (whole != g.cols && at < 64 && i < g.lanes)
+            store_rest(g.out + q.e * g.stride + i * g.ld + whole,
+                       mine + (uint32_t)((at / 8 ^ (lane & 7)) * 16), g.cols - whole);
         }
       }
 #pragma unroll 1
@@ -561,8 +573,7 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
           // Lane pairs trade columns: an even lane keeps column x and gets its
           // neighbour's, an odd one column x + 1, so that each has two adjacent
           // elements of a row. 32 whole rows go out through shared memory as one
-          // copy, the last rows of an expert by the lanes themselves, and what is
-          // left behind the last 8 lanes of all.
+          // copy, the last rows of an expert by the lanes themselves.
           const bool odd = lane & 1;
           const int32_t n = q.cols - c, i2 = i & ~1, whole = whole_pieces(g.lanes);  // (see whole_pieces)
           uint32_t p[16];
@@ -583,6 +594,10 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
               asm volatile("st.shared.b32 [%0], %1;" ::"r"(mine + (uint32_t)x * 128u), "r"(p[x]) : "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
+            const int32_t at = whole - (i - lane);
+            if (whole != g.lanes && at >= 0 && at < 32)  // a lane a row
+              store_rest(g.out + (int64_t)(q.col0 + c + lane) * g.ld + whole,
+                         to + (uint32_t)(lane * 64 + at * 2), g.lanes - whole);
             if (lane == 0) {
               if (i < whole)
                 asm volatile(
@@ -592,15 +607,14 @@ __global__ void __launch_bounds__(kXThreads<KIND>, 1)
                     : "memory");
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
-          }
-          if ((n < 32 || i2 >= whole) && i2 < g.lanes) {
+          } else {
             uint16_t* to = g.out + (int64_t)(q.col0 + c + (odd ? 1 : 0)) * g.ld + i2;
 #pragma unroll
             for (int x = 0; x < 32; x += 2) {
               if (x + (odd ? 1 : 0) < n) {
                 if (i2 + 1 < g.lanes)
                   *reinterpret_cast<uint32_t*>(to + (int64_t)x * g.ld) = p[x / 2];
-                else
+                else if (i2 < g.lanes)
                   to[(int64_t)x * g.ld] = (uint16_t)p[x / 2];
               }
             }
