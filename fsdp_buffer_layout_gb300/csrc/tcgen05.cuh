@@ -1,8 +1,9 @@
 // tcgen05.cuh — what the kernels on the fifth-generation tensor cores share
 // (ns_gemm.cuh: Newton-Schulz products; expert_gemm.cuh: the experts'
 // products): TMEM, pair MMAs, tensor copies and cluster barriers as inline PTX
-// for sm_103a, the operands' descriptors, and the tensor maps' encoder. Included
-// inside a namespace by each translation unit that uses it, after mbarrier.cuh.
+// for sm_103a, how a pair ends that was stopped, the operands' descriptors, and the
+// tensor maps' encoder. Included inside a namespace by each translation unit that uses
+// it, after mbarrier.cuh.
 #pragma once
 
 // ---------------------------------------------------------------- PTX wrappers
